@@ -13,6 +13,9 @@ backward (dq, dk, dv, dg, dbeta, dS0 from dO and dS_T).
 
 High-level helpers: ``forward`` / ``backward`` allocate outputs and workspace with
 torch; ``chunk_gated_delta_rule`` is the autograd entry point.
+
+The operators that stand around it in a model (short causal convolution, selective
+scan, block norms, single-token step) are in ``block`` and re-exported here.
 """
 from __future__ import annotations
 
@@ -22,6 +25,12 @@ import os
 from typing import Optional
 
 import torch
+
+from . import block as _block
+from .block import (  # noqa: F401 - the operators around the gated delta rule
+    BLOCK_EXPORTS, block_norm, causal_conv, conv_backward, conv_forward, conv_step, gdr_conv_problem,
+    gdr_norm_problem, gdr_ssm_problem, norm_backward, norm_forward, selective_scan, ssm_backward, ssm_forward,
+    ssm_step, step)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdr.so")
@@ -59,7 +68,8 @@ _STAGE_ARR = None
 EXPORTS = ["gdr_max_chunks", "gdr_saved_states_bytes", "gdr_fwd_workspace_bytes", "gdr_bwd_workspace_bytes",
            "gdr_fwd", "gdr_bwd", "gdr_workspace_status", "gdr_status_string", "gdr_path",
            "gdr_debug_set_stage_events", "gdr_debug_stage_count", "gdr_debug_stage_name",
-           "gdr_debug_launch_count", "gdr_debug_last_cuda_error", "gdr_debug_cuda_error_string", "gdr_fwd_noalloc", "gdr_noalloc_status", "gdr_debug_tc_gemm", "gdr_debug_timeout_selftest", "gdr_debug_cp_segment", "gdr_debug_cp_segments"]
+           "gdr_debug_launch_count", "gdr_debug_last_cuda_error", "gdr_debug_cuda_error_string", "gdr_fwd_noalloc", "gdr_noalloc_status", "gdr_debug_tc_gemm", "gdr_debug_timeout_selftest", "gdr_debug_cp_segment", "gdr_debug_cp_segments",
+           *BLOCK_EXPORTS]
 
 
 def _open(path: str):
@@ -105,6 +115,7 @@ def _open(path: str):
     lib.gdr_debug_cp_segment.restype = i
     lib.gdr_debug_cp_segments.argtypes = [P, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]
     lib.gdr_debug_cp_segments.restype = i
+    _block.declare(lib, gdr_problem)
     return lib
 
 

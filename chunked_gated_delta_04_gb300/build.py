@@ -41,7 +41,7 @@ def _sources():
 
 def _deps():
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))) + [
-        os.path.join(INCLUDE, "gdr.h")]
+        os.path.join(INCLUDE, "gdr.h"), os.path.join(INCLUDE, "gdr_block.h")]
 
 
 def _target(delay: bool):

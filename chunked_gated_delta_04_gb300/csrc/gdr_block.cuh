@@ -1,0 +1,137 @@
+// gdr_block.cuh -- what the operators of include/gdr_block.h share: vector access, activations,
+// the sequence check of packed batches, the column reduction of parameter gradients.
+#pragma once
+
+#include "../../include/gdr_block.h"
+#include "gdr_device.cuh"
+#include "gdr_internal.h"
+
+namespace gdr {
+
+constexpr int kSmCount = 152;  // SMs of a GB300: grids are sized against it
+
+// V elements of one row in fp32: 16-byte accesses for V = 8 (one of bf16, two of fp32), scalar
+// for V = 1.  p is 16-byte aligned for V = 8.
+template <int V>
+__device__ __forceinline__ void load_v(const float* p, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = p[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p + i);
+      v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void load_v(const __nv_bfloat16* p, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = __bfloat162float(p[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 8) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p + i);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // a bf16 is the upper half of the float of the same value
+        v[i + 2 * j] = __uint_as_float(w[j] << 16);
+        v[i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_v(float* p, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    p[0] = v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_v(__nv_bfloat16* p, const float (&v)[V]) {
+  if constexpr (V == 1) {
+    p[0] = __float2bfloat16_rn(v[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      *reinterpret_cast<uint4*>(p + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcpf(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 1 / (1 + e^-x).  e^-x overflows to infinity below -88, where the reciprocal gives 0, the limit.
+__device__ __forceinline__ float sigmoid_f(float x) { return rcpf(1.f + ex2f(-kLog2e * x)); }
+
+// softplus(x) = max(x, 0) + log(1 + u), u = e^-|x| in (0, 1], to fp32 accuracy also where it is
+// tiny: log(1 + u) = 2 artanh(s), s = u / (2 + u) <= 1/3, by artanh's series (s^2 <= 1/9, so the
+// first term left out, s^17 / 17, is below 2^-26 of the sum).  *sig receives sigmoid(x).
+__device__ __forceinline__ float softplus_f(float x, float* sig) {
+  const float u = ex2f(-kLog2e * fabsf(x));
+  const float s = u * rcpf(2.f + u), q = s * s;
+  float p = 1.f / 15.f;
+  p = fmaf(p, q, 1.f / 13.f);
+  p = fmaf(p, q, 1.f / 11.f);
+  p = fmaf(p, q, 1.f / 9.f);
+  p = fmaf(p, q, 1.f / 7.f);
+  p = fmaf(p, q, 1.f / 5.f);
+  p = fmaf(p, q, 1.f / 3.f);
+  p = fmaf(p, q, 1.f);
+  const float r = rcpf(1.f + u);
+  if (sig) *sig = x >= 0.f ? r : u * r;
+  return fmaxf(x, 0.f) + 2.f * s * p;
+}
+
+// The sequence of packed token t (cu valid, t < cu[num_seqs]): the last n with cu[n] <= t.
+__device__ __forceinline__ int seq_of(const int32_t* cu, int num_seqs, long long t) {
+  int lo = 0, hi = num_seqs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+inline size_t block_align(size_t x) { return (x + 255) & ~(size_t)255; }
+inline bool vec_ok(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+inline bool elem_ok(const void* p, size_t el) { return ((uintptr_t)p & (el - 1)) == 0; }
+inline bool dtype_ok(gdr_dtype t) { return t == GDR_DTYPE_F32 || t == GDR_DTYPE_BF16; }
+inline size_t dtype_bytes(gdr_dtype t) { return t == GDR_DTYPE_BF16 ? 2 : 4; }
+
+// Checks cu_seqlens (0 .. T, non-decreasing) and writes status word 0: 0, or the bad bit, on which
+// the kernels that follow return at once.
+cudaError_t launch_seq_check(const int32_t* cu, int num_seqs, int T, uint32_t* status, cudaStream_t s);
+
+// Sums over the rows of partial[rows][parts][width], in a fixed order: parts k < mat_parts go to
+// mat[c * mat_parts + k], the others to vec[k - mat_parts][c] (skipped where null).
+struct ColumnSums {
+  float* mat;
+  int mat_parts;
+  float* vec[3];
+  int parts, width;
+  const uint32_t* status;  // nullable: nothing is written where the sequence check's word is set
+};
+cudaError_t launch_column_sums(const float* partial, long long rows, const ColumnSums& out, cudaStream_t s,
+                               const char* stage);
+
+}  // namespace gdr

@@ -1,0 +1,158 @@
+// gdr_norm.cu -- norms before and after a block with its gate and residual scale, forward
+// (include/gdr_block.h):
+//
+//   u = x [rstd(x) w_post] [silu(z)] [scale],   r = [residual +] u,   y = r rstd(r) w_pre
+//
+// in one pass: a row stays in registers from its load to the store of r and y, so the bytes are
+// those of the tensors once each.  Bound by memory (about 10 operations per element).  The norm
+// before the block is taken of r as stored (rounded to its type): the backward, which gets r and
+// not the unrounded sum, then differentiates exactly what ran.
+#include "gdr_norm.cuh"
+
+namespace gdr {
+namespace {
+
+template <typename IT, typename RT, int TPR, int K>
+__global__ void __launch_bounds__(TPR > 32 ? TPR : 256)
+    norm_fwd_kernel(NormDims d, const IT* __restrict__ x, const float* __restrict__ w_post,
+                    const IT* __restrict__ gate, const float* __restrict__ scale, const RT* __restrict__ residual,
+                    const float* __restrict__ w_pre, void* __restrict__ r_out, IT* __restrict__ y) {
+  constexpr int kRowsPerBlock = TPR > 32 ? 1 : 256 / TPR;
+  __shared__ float red[TPR > 32 ? 2 * TPR / 32 : 1];
+  int flip = 0;
+  const int i0 = threadIdx.x % TPR;
+  const long long step = (long long)gridDim.x * kRowsPerBlock;
+  const float inv = 1.f / (float)d.D;
+  // rows of a block run together (barriers): the loop's trip count is the block's
+  for (long long base = (long long)blockIdx.x * kRowsPerBlock; base < d.rows; base += step) {
+    const long long row = base + threadIdx.x / TPR;
+    const bool live = row < d.rows;
+    const long long tok = row / d.heads;
+    const int hd = (int)(row - tok * d.heads);
+    const int D = live ? d.D : 0;  // a dead row loads and stores nothing
+    float u[K][8], t[8];
+    const IT* xr = x + tok * d.ld_x + (long long)hd * d.D;
+#pragma unroll
+    for (int k = 0; k < K; ++k) load8(xr, 8 * (k * TPR + i0), D, d.vec, u[k]);
+    if (w_post) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[0] = fmaf(u[k][i], u[k][i], s[0]);
+      row_sums<TPR, 1>(s, red, flip);
+      const float rs = rsqrtf(s[0] * inv + d.eps);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        load8(w_post, 8 * (k * TPR + i0), D, d.vec, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[k][i] *= rs * t[i];
+      }
+    }
+    if (gate) {
+      const IT* zr = gate + tok * d.ld_gate + (long long)hd * d.D;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        load8(zr, 8 * (k * TPR + i0), D, d.vec, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[k][i] *= t[i] * sigmoid_f(t[i]);
+      }
+    }
+    if (scale) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        load8(scale, 8 * (k * TPR + i0), D, d.vec, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[k][i] *= t[i];
+      }
+    }
+    if (residual) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        load8(residual + row * d.D, 8 * (k * TPR + i0), D, d.vec, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[k][i] = to_f32(from_f32<RT>(u[k][i] + t[i]));
+        store8((RT*)r_out + row * d.D, 8 * (k * TPR + i0), D, d.vec, u[k]);
+      }
+    } else if (!w_pre) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) store8((IT*)r_out + row * d.D, 8 * (k * TPR + i0), D, d.vec, u[k]);
+    }
+    if (w_pre) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[0] = fmaf(u[k][i], u[k][i], s[0]);
+      row_sums<TPR, 1>(s, red, flip);
+      const float rs = rsqrtf(s[0] * inv + d.eps);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        load8(w_pre, 8 * (k * TPR + i0), D, d.vec, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] *= u[k][i] * rs;
+        store8(y + row * d.D, 8 * (k * TPR + i0), D, d.vec, t);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+gdr_status resolve_norm(const gdr_norm_problem* p, NormDims* d) {
+  if (p == nullptr || p->tokens < 0 || p->heads <= 0 || p->D <= 0) return GDR_ERR_INVALID_ARG;
+  if (!dtype_ok(p->dtype) || !dtype_ok(p->res_dtype)) return GDR_ERR_INVALID_ARG;
+  if (p->dtype == GDR_DTYPE_F32 && p->res_dtype != GDR_DTYPE_F32) return GDR_ERR_INVALID_ARG;
+  if (!(p->eps > 0.f)) return GDR_ERR_INVALID_ARG;
+  const long long w = (long long)p->heads * p->D;
+  if ((p->ld_x != 0 && p->ld_x < w) || (p->ld_gate != 0 && p->ld_gate < w)) return GDR_ERR_INVALID_ARG;
+  if (p->D > kNormMaxD || p->tokens > (1ll << 60) / w) return GDR_ERR_UNSUPPORTED;
+  d->rows = p->tokens * p->heads;
+  d->heads = p->heads;
+  d->D = p->D;
+  d->ld_x = p->ld_x ? p->ld_x : w;
+  d->ld_gate = p->ld_gate ? p->ld_gate : w;
+  d->eps = p->eps;
+  d->vec = 0;
+  return GDR_OK;
+}
+
+}  // namespace gdr
+
+using namespace gdr;
+
+extern "C" gdr_status gdr_norm_fwd(const gdr_norm_problem* p, const void* x, const float* w_post, const void* gate,
+                                   const float* scale, const void* residual, const float* w_pre, void* r, void* y,
+                                   gdr_stream_t stream) {
+  NormDims d;
+  const gdr_status st = resolve_norm(p, &d);
+  if (st != GDR_OK) return st;
+  if (!w_post && !gate && !scale && !residual && !w_pre) return GDR_ERR_INVALID_ARG;
+  if (w_pre && !residual && (w_post || gate || scale)) return GDR_ERR_INVALID_ARG;
+  if (d.rows > 0 && (!x || (w_pre && !y) || ((residual || !w_pre) && !r))) return GDR_ERR_INVALID_ARG;
+  const size_t el = dtype_bytes(p->dtype), rel = residual ? dtype_bytes(p->res_dtype) : el;
+  if (!elem_ok(x, el) || !elem_ok(gate, el) || !elem_ok(y, el) || !elem_ok(residual, rel) || !elem_ok(r, rel) ||
+      !elem_ok(w_post, 4) || !elem_ok(scale, 4) || !elem_ok(w_pre, 4))
+    return GDR_ERR_ALIGNMENT;
+  if (d.rows == 0) return GDR_OK;
+  d.vec = d.D % 8 == 0 && d.ld_x % 8 == 0 && d.ld_gate % 8 == 0 && vec_ok(x) && vec_ok(w_post) && vec_ok(gate) &&
+          vec_ok(scale) && vec_ok(residual) && vec_ok(w_pre) && vec_ok(r) && vec_ok(y);
+  cudaStream_t s = (cudaStream_t)stream;
+  stage_begin(s);
+  auto go = [&](auto it, auto rt) {
+    using IT = decltype(it);
+    using RT = decltype(rt);
+    return norm_shape(d.D, [&](auto tpr, auto k) {
+      constexpr int TPR = decltype(tpr)::value, K = decltype(k)::value;
+      constexpr int kBlock = TPR > 32 ? TPR : 256, kRows = TPR > 32 ? 1 : 256 / TPR;
+      const long long want = (d.rows + kRows - 1) / kRows;
+      const unsigned grid = (unsigned)(want < (1ll << 20) ? want : (1ll << 20));
+      norm_fwd_kernel<IT, RT, TPR, K><<<grid, kBlock, 0, s>>>(d, (const IT*)x, w_post, (const IT*)gate, scale,
+                                                             (const RT*)residual, w_pre, r, (IT*)y);
+      stage_mark(s, "norm_fwd");
+      return cudaGetLastError();
+    });
+  };
+  if (p->dtype == GDR_DTYPE_F32) return status_of(go(float{}, float{}));
+  return status_of(p->res_dtype == GDR_DTYPE_F32 ? go(__nv_bfloat16{}, float{}) : go(__nv_bfloat16{}, __nv_bfloat16{}));
+}
