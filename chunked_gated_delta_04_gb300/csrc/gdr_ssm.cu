@@ -305,10 +305,10 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmDims d, int B, int num
     const IT* bp = Bm + b * d.ld_b + g * N + 4 * ln;
     const IT* cp = Cm + b * d.ld_c + g * N + 4 * ln;
     const float u = dl * xv, d2 = dl * kLog2e;
-    h.x = fmaf(ex2f(d2 * a.x), h.x, u * to_f32(bp[0]));
-    h.y = fmaf(ex2f(d2 * a.y), h.y, u * to_f32(bp[1]));
-    h.z = fmaf(ex2f(d2 * a.z), h.z, u * to_f32(bp[2]));
-    h.w = fmaf(ex2f(d2 * a.w), h.w, u * to_f32(bp[3]));
+    h.x = fmaf(ex2f(d2 * fmaxf(a.x, -kBig)), h.x, u * to_f32(bp[0]));
+    h.y = fmaf(ex2f(d2 * fmaxf(a.y, -kBig)), h.y, u * to_f32(bp[1]));
+    h.z = fmaf(ex2f(d2 * fmaxf(a.z, -kBig)), h.z, u * to_f32(bp[2]));
+    h.w = fmaf(ex2f(d2 * fmaxf(a.w, -kBig)), h.w, u * to_f32(bp[3]));
     __stcs(hp, h);
     p = fmaf(h.x, to_f32(cp[0]), fmaf(h.y, to_f32(cp[1]), fmaf(h.z, to_f32(cp[2]), h.w * to_f32(cp[3]))));
   }
