@@ -14,8 +14,8 @@ stream, and the caller orders the inputs before it.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import sys
 
 import torch
 
@@ -69,35 +69,33 @@ def declare(lib, gdr_problem) -> None:
     lib.gdr_step.restype = _I
 
 
-def _main():
-    import chunked_gated_delta_04_gb300 as gdr
-
-    return gdr
+_gdr = sys.modules[__package__]  # the package itself, which imports this module
 
 
 def _lib():
-    return _main()._lib_handle()
+    return _gdr._LIB or _gdr._lib_handle()
 
 
 def _raise(status, where):
-    raise _main().GDRError(status, where)
+    raise _gdr.GDRError(status, where)
 
 
 _CODE = {torch.float32: 0, torch.bfloat16: 1}
-_NO_STREAM = contextlib.nullcontext()
+_F32 = torch.float32
+_empty = torch.empty
 
 
 def _on(stream):
-    """The context in which a call allocates and launches."""
-    if stream is None:
-        return _NO_STREAM
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    return torch.cuda.stream(stream)
+    """The context in which a call on a stream of its own allocates and launches."""
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
-def _now():
-    return torch.cuda.current_stream().cuda_stream
+# The current stream's handle.  torch.cuda.current_stream() builds an object for it (2.9 us on the
+# GPU's host, against 2.7 us for a whole launch through the library); the raw query takes 0.1 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def _p(t):
@@ -109,6 +107,11 @@ def _need(cond, what):
         raise ValueError(what)
 
 
+def _is(t, shape, dtype=_F32):
+    """Whether t is a contiguous CUDA tensor of a shape and type (None passes)."""
+    return t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda)
+
+
 def _act(name, t, shape, dtype):
     """An activation of the call: on the GPU, of the call's type and shape."""
     if t.shape != shape or t.dtype != dtype or not t.is_cuda:
@@ -118,7 +121,7 @@ def _act(name, t, shape, dtype):
 
 def _full(name, t, shape, dtype=torch.float32):
     """A contiguous tensor of a given shape and type, or None."""
-    if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous()):
+    if not _is(t, shape, dtype):
         raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
 
@@ -146,6 +149,10 @@ def _ld(name, t, inner):
 def _seqs(cu_seqlens, B):
     if cu_seqlens is None:
         return B
+    if B == 1 and cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous():
+        n = cu_seqlens.numel()
+        if n >= 2 and cu_seqlens.is_cuda:
+            return n - 1
     _need(cu_seqlens.dtype == torch.int32 and cu_seqlens.is_cuda and cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2
           and cu_seqlens.is_contiguous(), "cu_seqlens: expected a contiguous CUDA int32 vector of at least 2 entries")
     _need(B == 1, "cu_seqlens needs a batch of 1 (the packed tokens)")
@@ -160,23 +167,35 @@ def _slots(slots, B):
 
 def _workspace(nbytes, device):
     # torch's allocator returns 512-byte aligned blocks, which covers the 256-byte requirement
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    return _empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def _type(x):
     code = _CODE.get(x.dtype)
-    _need(code is not None, f"dtype {x.dtype}: float32 or bfloat16")
+    if code is None:
+        raise ValueError(f"dtype {x.dtype}: float32 or bfloat16")
     return code
 
 
+def _step_state(state, slots, B):
+    _slots(slots, B)
+    if slots is None and state.shape[0] < B:
+        raise ValueError(f"state: {state.shape[0]} states for {B} rows")
+
+
 # ---------------------------------------------------------------------------------- convolution
+_SILU = {"silu": 1, "none": 0, None: 0}
+
+
 def _silu(activation):
-    _need(activation in ("silu", "none", None), f"activation {activation!r}: 'silu' or 'none'")
-    return int(activation == "silu")
+    if activation not in _SILU:
+        raise ValueError(f"activation {activation!r}: 'silu' or 'none'")
+    return _SILU[activation]
 
 
 def _conv_problem(x, weight, bias, cu_seqlens, activation, state, name, dy=None):
-    _need(x.dim() == 3, "x: expected [B, T, C]")
+    if x.dim() != 3:
+        raise ValueError(f"x: expected [B, T, C], got {tuple(x.shape)}")
     B, T, C = x.shape
     W = weight.shape[-1]
     _act("x", x, (B, T, C), x.dtype)
@@ -196,14 +215,16 @@ def conv_forward(x, weight, bias=None, initial_state=None, cu_seqlens=None, acti
     """Short causal depthwise convolution: x [B, T, C] (may be a slice of a wider tensor), weight
     [C, W] and bias [C] fp32, initial_state [num_seqs, W - 1, C] (oldest row first).  Returns
     (y, final state or None)."""
+    if stream is not None:
+        with _on(stream):
+            return conv_forward(x, weight, bias, initial_state, cu_seqlens, activation, output_final_state)
     p = _conv_problem(x, weight, bias, cu_seqlens, activation, initial_state, "initial_state")
     lib = _lib()
-    with _on(stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        last = (torch.empty(p.num_seqs, p.W - 1, p.C, dtype=x.dtype, device=x.device) if output_final_state else None)
-        ws = _workspace(256 if cu_seqlens is not None else 0, x.device)
-        st = lib.gdr_conv_fwd(_c.byref(p), _p(x), _p(weight), _p(bias), _p(initial_state), _p(y), _p(last), _p(ws),
-                              256 if ws is not None else 0, _now())
+    y = _empty(x.shape, dtype=x.dtype, device=x.device)
+    last = (_empty(p.num_seqs, p.W - 1, p.C, dtype=x.dtype, device=x.device) if output_final_state else None)
+    ws = _workspace(256 if cu_seqlens is not None else 0, x.device)
+    st = lib.gdr_conv_fwd(_c.byref(p), _p(x), _p(weight), _p(bias), _p(initial_state), _p(y), _p(last), _p(ws),
+                          256 if ws is not None else 0, _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_conv_fwd")
     return y, last
@@ -212,18 +233,20 @@ def conv_forward(x, weight, bias=None, initial_state=None, cu_seqlens=None, acti
 def conv_backward(x, weight, bias, dy, initial_state=None, dfinal_state=None, cu_seqlens=None, activation="silu",
                   stream=None):
     """Gradients of conv_forward: (dx, dweight, dbias or None, dinitial_state or None)."""
+    if stream is not None:
+        with _on(stream):
+            return conv_backward(x, weight, bias, dy, initial_state, dfinal_state, cu_seqlens, activation)
     p = _conv_problem(x, weight, bias, cu_seqlens, activation, initial_state, "initial_state", dy)
     _full("dfinal_state", dfinal_state, (p.num_seqs, p.W - 1, p.C), x.dtype)
     lib = _lib()
-    with _on(stream):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty_like(weight)
-        db = torch.empty_like(bias) if bias is not None else None
-        dstate = torch.empty_like(initial_state) if initial_state is not None else None
-        n = lib.gdr_conv_bwd_workspace_bytes(_c.byref(p))
-        ws = _workspace(n, x.device)
-        st = lib.gdr_conv_bwd(_c.byref(p), _p(x), _p(weight), _p(bias), _p(initial_state), _p(dy), _p(dfinal_state), _p(dx),
-                              _p(dw), _p(db), _p(dstate), _p(ws), n, _now())
+    dx = _empty(x.shape, dtype=x.dtype, device=x.device)
+    dw = torch.empty_like(weight)
+    db = torch.empty_like(bias) if bias is not None else None
+    dstate = torch.empty_like(initial_state) if initial_state is not None else None
+    n = lib.gdr_conv_bwd_workspace_bytes(_c.byref(p))
+    ws = _workspace(n, x.device)
+    st = lib.gdr_conv_bwd(_c.byref(p), _p(x), _p(weight), _p(bias), _p(initial_state), _p(dy), _p(dfinal_state), _p(dx),
+                          _p(dw), _p(db), _p(dstate), _p(ws), n, _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_conv_bwd")
     return dx, dw, db, dstate
@@ -233,18 +256,19 @@ def conv_step(x, state, weight, bias=None, slots=None, activation="silu", stream
     """One token per row: x [B, C]; state, a pool [num_slots, W - 1, C], is updated in place at each
     row's slot (int32 [B]; None: row i at slot i).  Returns y [B, C]; a row whose slot is outside the
     pool is skipped and returns zeros."""
+    if stream is not None:
+        with _on(stream):
+            return conv_step(x, state, weight, bias, slots, activation)
     B, C = x.shape
     W = weight.shape[-1]
     _act("x", x, (B, C), x.dtype)
     _full("weight", weight, (C, W))
     _full("bias", bias, (C,))
     _full("state", state, (state.shape[0], W - 1, C), x.dtype)
-    _slots(slots, B)
-    _need(slots is not None or state.shape[0] >= B, "state: fewer states than rows")
+    _step_state(state, slots, B)
     p = gdr_conv_problem(B, 1, C, W, B, None, _type(x), _silu(activation), _ld("x", x, 1), 0, state.shape[0])
-    with _on(stream):
-        y = torch.empty((B, C), dtype=x.dtype, device=x.device)
-        st = _lib().gdr_conv_step(_c.byref(p), _p(x), _p(weight), _p(bias), _p(state), _p(slots), _p(y), _now())
+    y = _empty((B, C), dtype=x.dtype, device=x.device)
+    st = _lib().gdr_conv_step(_c.byref(p), _p(x), _p(weight), _p(bias), _p(state), _p(slots), _p(y), _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_conv_step")
     return y
@@ -285,7 +309,8 @@ def causal_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, activ
 
 # ------------------------------------------------------------------------------- selective scan
 def _ssm_problem(x, dt, A, Bm, Cm, Dskip, dt_bias, cu_seqlens, dt_softplus, dy=None):
-    _need(x.dim() == 3 and Bm.dim() == 4, "x: expected [B, T, D]; Bm, Cm: [B, T, G, N]")
+    if x.dim() != 3 or Bm.dim() != 4:
+        raise ValueError(f"expected x [B, T, D] and Bm, Cm [B, T, G, N], got {tuple(x.shape)} and {tuple(Bm.shape)}")
     B, T, D = x.shape
     G, N = Bm.shape[2], Bm.shape[3]
     _act("x", x, (B, T, D), x.dtype)
@@ -308,19 +333,21 @@ def ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, cu_seqlens=None
     """Selective state space scan: x, dt [B, T, D], A [D, N] fp32, Bm, Cm [B, T, G, N], D and dt_bias
     [D] fp32, S0 [num_seqs, D, N] fp32.  Returns (y, S_T or None, h_saved or None); save keeps the
     states that ssm_backward needs."""
+    if stream is not None:
+        with _on(stream):
+            return ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus, output_final_state, save)
     p = _ssm_problem(x, dt, A, Bm, Cm, D, dt_bias, cu_seqlens, dt_softplus)
     _full("S0", S0, (p.num_seqs, p.D, p.N))
     lib = _lib()
-    with _on(stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        S_T = torch.empty((p.num_seqs, p.D, p.N), dtype=torch.float32, device=x.device) if output_final_state else None
-        saved = None
-        if save:
-            saved = torch.empty(lib.gdr_ssm_saved_bytes(_c.byref(p)) // 4, dtype=torch.float32, device=x.device)
-        n = lib.gdr_ssm_fwd_workspace_bytes(_c.byref(p))
-        ws = _workspace(n, x.device)
-        st = lib.gdr_ssm_fwd(_c.byref(p), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(S0), _p(y), _p(S_T),
-                             _p(saved), _p(ws), n, _now())
+    y = _empty(x.shape, dtype=x.dtype, device=x.device)
+    S_T = _empty((p.num_seqs, p.D, p.N), dtype=torch.float32, device=x.device) if output_final_state else None
+    saved = None
+    if save:
+        saved = _empty(lib.gdr_ssm_saved_bytes(_c.byref(p)) // 4, dtype=torch.float32, device=x.device)
+    n = lib.gdr_ssm_fwd_workspace_bytes(_c.byref(p))
+    ws = _workspace(n, x.device)
+    st = lib.gdr_ssm_fwd(_c.byref(p), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(S0), _p(y), _p(S_T),
+                         _p(saved), _p(ws), n, _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_ssm_fwd")
     return y, S_T, saved
@@ -329,25 +356,27 @@ def ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, cu_seqlens=None
 def ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D=None, dt_bias=None, dS_T=None, cu_seqlens=None, dt_softplus=True,
                  want_dS0=True, stream=None):
     """Gradients of ssm_forward: (dx, ddt, dA, dBm, dCm, dD or None, ddt_bias or None, dS0 or None)."""
+    if stream is not None:
+        with _on(stream):
+            return ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D, dt_bias, dS_T, cu_seqlens, dt_softplus, want_dS0)
     p = _ssm_problem(x, dt, A, Bm, Cm, D, dt_bias, cu_seqlens, dt_softplus, dy)
     _full("dS_T", dS_T, (p.num_seqs, p.D, p.N))
     lib = _lib()
     need = lib.gdr_ssm_saved_bytes(_c.byref(p)) // 4
-    _need(h_saved is not None and h_saved.dtype == torch.float32 and h_saved.is_contiguous() and h_saved.numel() >= need,
-          f"h_saved: expected the {need} floats that ssm_forward kept (save=True)")
+    if h_saved is None or h_saved.dtype != _F32 or not h_saved.is_contiguous() or h_saved.numel() < need:
+        raise ValueError(f"h_saved: expected the {need} floats that ssm_forward kept (save=True)")
     f32 = torch.float32
-    with _on(stream):
-        dx, ddt = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
-        dB, dC = (torch.empty(Bm.shape, dtype=x.dtype, device=x.device) for _ in range(2))
-        dA = torch.empty_like(A)
-        dD = torch.empty_like(D) if D is not None else None
-        dbias = torch.empty_like(dt_bias) if dt_bias is not None else None
-        dS0 = torch.empty((p.num_seqs, p.D, p.N), dtype=f32, device=x.device) if want_dS0 else None
-        n = lib.gdr_ssm_bwd_workspace_bytes(_c.byref(p))
-        ws = _workspace(n, x.device)
-        st = lib.gdr_ssm_bwd(_c.byref(p), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(h_saved), _p(dy),
-                             _p(dS_T), _p(dx), _p(ddt), _p(dA), _p(dB), _p(dC), _p(dD), _p(dbias), _p(dS0), _p(ws), n,
-                             _now())
+    dx, ddt = (_empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
+    dB, dC = (_empty(Bm.shape, dtype=x.dtype, device=x.device) for _ in range(2))
+    dA = torch.empty_like(A)
+    dD = torch.empty_like(D) if D is not None else None
+    dbias = torch.empty_like(dt_bias) if dt_bias is not None else None
+    dS0 = _empty((p.num_seqs, p.D, p.N), dtype=f32, device=x.device) if want_dS0 else None
+    n = lib.gdr_ssm_bwd_workspace_bytes(_c.byref(p))
+    ws = _workspace(n, x.device)
+    st = lib.gdr_ssm_bwd(_c.byref(p), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(h_saved), _p(dy),
+                         _p(dS_T), _p(dx), _p(ddt), _p(dA), _p(dB), _p(dC), _p(dD), _p(dbias), _p(dS0), _p(ws), n,
+                         _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_ssm_bwd")
     return dx, ddt, dA, dB, dC, dD, dbias, dS0
@@ -356,6 +385,9 @@ def ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D=None, dt_bias=None, dS_T=None,
 def ssm_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, slots=None, dt_softplus=True, stream=None):
     """One token per row: x, dt [B, D], Bm, Cm [B, G, N]; state, a pool [num_slots, D, N] fp32, is
     updated in place at each row's slot (see conv_step).  Returns y [B, D]."""
+    if stream is not None:
+        with _on(stream):
+            return ssm_step(x, dt, A, Bm, Cm, state, D, dt_bias, slots, dt_softplus)
     B, d = x.shape
     G, N = Bm.shape[1], Bm.shape[2]
     _act("x", x, (B, d), x.dtype)
@@ -366,14 +398,12 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, slots=None, dt_softp
     _full("D", D, (d,))
     _full("dt_bias", dt_bias, (d,))
     _full("state", state, (state.shape[0], d, N))
-    _slots(slots, B)
-    _need(slots is not None or state.shape[0] >= B, "state: fewer states than rows")
+    _step_state(state, slots, B)
     p = gdr_ssm_problem(B, 1, d, N, G, B, None, _type(x), int(bool(dt_softplus)), _ld("x", x, 1), _ld("dt", dt, 1),
                         _ld("Bm", Bm, 2), _ld("Cm", Cm, 2), 0, state.shape[0])
-    with _on(stream):
-        y = torch.empty((B, d), dtype=x.dtype, device=x.device)
-        st = _lib().gdr_ssm_step(_c.byref(p), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(state), _p(slots),
-                                 _p(y), _now())
+    y = _empty((B, d), dtype=x.dtype, device=x.device)
+    st = _lib().gdr_ssm_step(_c.byref(p), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(state), _p(slots),
+                             _p(y), _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_ssm_step")
     return y
@@ -433,7 +463,8 @@ def _norm_problem(x, post_weight, gate, scale, pre_weight, stream_dtype, eps):
     _full("scale", scale, (D,))
     _full("pre_weight", pre_weight, (D,))
     tokens, heads, ld_x, ld_gate = _norm_rows(x, gate)
-    _need(stream_dtype in _CODE, f"residual dtype {stream_dtype}: float32 or bfloat16")
+    if stream_dtype not in _CODE:
+        raise ValueError(f"residual dtype {stream_dtype}: float32 or bfloat16")
     return gdr_norm_problem(tokens, heads, D, _type(x), _CODE[stream_dtype], eps, ld_x, ld_gate)
 
 
@@ -442,14 +473,16 @@ def norm_forward(x, post_weight=None, gate=None, scale=None, residual=None, pre_
     Rows are the last dimension.  Returns (r, y): r in the residual's dtype (fp32 or x's), or in x's
     without one; r is None for a plain norm in front of a block (pre_weight alone), y is None without
     pre_weight."""
+    if stream is not None:
+        with _on(stream):
+            return norm_forward(x, post_weight, gate, scale, residual, pre_weight, eps)
     res_dtype = x.dtype if residual is None else residual.dtype
     p = _norm_problem(x, post_weight, gate, scale, pre_weight, res_dtype, eps)
     _full("residual", residual, x.shape, res_dtype)
-    with _on(stream):
-        r = torch.empty(x.shape, dtype=res_dtype, device=x.device) if residual is not None or pre_weight is None else None
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if pre_weight is not None else None
-        st = _lib().gdr_norm_fwd(_c.byref(p), _p(x), _p(post_weight), _p(gate), _p(scale), _p(residual), _p(pre_weight), _p(r),
-                                 _p(y), _now())
+    r = _empty(x.shape, dtype=res_dtype, device=x.device) if residual is not None or pre_weight is None else None
+    y = _empty(x.shape, dtype=x.dtype, device=x.device) if pre_weight is not None else None
+    st = _lib().gdr_norm_fwd(_c.byref(p), _p(x), _p(post_weight), _p(gate), _p(scale), _p(residual), _p(pre_weight), _p(r),
+                             _p(y), _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_norm_fwd")
     return r, y
@@ -460,6 +493,9 @@ def norm_backward(x, post_weight=None, gate=None, scale=None, r=None, pre_weight
     """Gradients of norm_forward from dr and dy (either may be None): (dx, dgate, dresidual, dpost_weight,
     dscale, dpre_weight), None where the forward had no such tensor.  r: the forward's r where it had a
     residual, else None."""
+    if stream is not None:
+        with _on(stream):
+            return norm_backward(x, post_weight, gate, scale, r, pre_weight, dr, dy, eps)
     has_residual = r is not None
     res_dtype = r.dtype if has_residual else x.dtype
     p = _norm_problem(x, post_weight, gate, scale, pre_weight, res_dtype, eps)
@@ -469,19 +505,19 @@ def norm_backward(x, post_weight=None, gate=None, scale=None, r=None, pre_weight
     if not has_residual and pre_weight is not None:
         _need(x.is_contiguous(), "x: a plain norm's backward needs a contiguous x")
     lib = _lib()
-    with _on(stream):
-        def new(like, dtype=None):
-            return None if like is None else torch.empty(like.shape, dtype=dtype or like.dtype, device=x.device)
 
-        dx, dgate = new(x), new(gate)
-        dres = new(x, res_dtype) if has_residual else None
-        dpost, dscale, dpre = new(post_weight), new(scale), new(pre_weight)
-        n = lib.gdr_norm_bwd_workspace_bytes(_c.byref(p))
-        ws = _workspace(n, x.device)
-        rr = r if has_residual else (x if pre_weight is not None else None)
-        st = lib.gdr_norm_bwd(_c.byref(p), _p(x), _p(post_weight), _p(gate), _p(scale), _p(rr), _p(pre_weight),
-                              int(has_residual), _p(dr), _p(dy), _p(dx), _p(dgate), _p(dres), _p(dpost), _p(dscale), _p(dpre),
-                              _p(ws), n, _now())
+    def new(like, dtype=None):
+        return None if like is None else _empty(like.shape, dtype=dtype or like.dtype, device=x.device)
+
+    dx, dgate = new(x), new(gate)
+    dres = new(x, res_dtype) if has_residual else None
+    dpost, dscale, dpre = new(post_weight), new(scale), new(pre_weight)
+    n = lib.gdr_norm_bwd_workspace_bytes(_c.byref(p))
+    ws = _workspace(n, x.device)
+    rr = r if has_residual else (x if pre_weight is not None else None)
+    st = lib.gdr_norm_bwd(_c.byref(p), _p(x), _p(post_weight), _p(gate), _p(scale), _p(rr), _p(pre_weight),
+                          int(has_residual), _p(dr), _p(dy), _p(dx), _p(dgate), _p(dres), _p(dpost), _p(dscale), _p(dpre),
+                          _p(ws), n, _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_norm_bwd")
     return dx, dgate, dres, dpost, dscale, dpre
@@ -524,24 +560,25 @@ def step(q, k, v, g, beta, state, layout="KV", scale=None, slots=None, prologue=
     beta [B, Hv]; state, a pool [num_slots, Hv, DK, DV] ("KV") or [num_slots, Hv, DV, DK] ("VK") fp32,
     is updated in place at each row's slot (see conv_step).  prologue: GDR_PROLOGUE_* bits, as in
     forward (the mapped q, k and beta stay in fp32 here).  Returns o [B, Hv, DV]."""
+    if stream is not None:
+        with _on(stream):
+            return step(q, k, v, g, beta, state, layout, scale, slots, prologue)
     B, Hk, DK = q.shape
     Hv, DV = v.shape[1], v.shape[2]
-    _need(layout in ("KV", "VK"), f"layout {layout!r}: 'KV' or 'VK'")
+    if layout not in ("KV", "VK"):
+        raise ValueError(f"layout {layout!r}: 'KV' or 'VK'")
     _full("q", q, (B, Hk, DK), q.dtype)
     _full("k", k, (B, Hk, DK), q.dtype)
     _full("v", v, (B, Hv, DV), q.dtype)
     _full("g", g, (B, Hv))
     _full("beta", beta, (B, Hv), q.dtype)
     _full("state", state, (state.shape[0], Hv, DK, DV) if layout == "KV" else (state.shape[0], Hv, DV, DK))
-    _slots(slots, B)
-    _need(slots is not None or state.shape[0] >= B, "state: fewer states than rows")
-    gdr = _main()
-    p = gdr.gdr_problem(B, 1, Hk, Hv, DK, DV, B, None, _type(q), 0 if layout == "KV" else 1,
+    _step_state(state, slots, B)
+    p = _gdr.gdr_problem(B, 1, Hk, Hv, DK, DV, B, None, _type(q), 0 if layout == "KV" else 1,
                         0.0 if scale is None else float(scale), 0, int(prologue), 0, 1, 1)
-    with _on(stream):
-        o = torch.empty((B, Hv, DV), dtype=q.dtype, device=q.device)
-        st = gdr._lib_handle().gdr_step(_c.byref(p), _p(q), _p(k), _p(v), _p(g), _p(beta), _p(state), state.shape[0],
-                                        _p(slots), _p(o), _now())
+    o = _empty((B, Hv, DV), dtype=q.dtype, device=q.device)
+    st = _lib().gdr_step(_c.byref(p), _p(q), _p(k), _p(v), _p(g), _p(beta), _p(state), state.shape[0],
+                         _p(slots), _p(o), _raw_stream(q.get_device()))
     if st:
         _raise(st, "gdr_step")
     return o
