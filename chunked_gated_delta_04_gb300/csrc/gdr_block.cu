@@ -15,37 +15,36 @@ __global__ void __launch_bounds__(256) seq_check_kernel(const int32_t* __restric
   if (threadIdx.x == 0) status[0] = bad ? kDevErrBadCuSeqlens : 0u;
 }
 
-// 32 columns x 8 row groups per block; each thread sums every 8th row in order, then the eight
-// sums are added in order: the same result on every run.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ partial, long long rows,
-                                                          ColumnSums out) {
-  __shared__ float part[8][33];
+// 32 columns x 32 row groups per block; a thread sums every 32nd row in order, then the sums are
+// added in order: the same result on every run.
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restrict__ partial, long long rows,
+                                                           ColumnSums out) {
+  __shared__ float part[32][33];
   if (out.status && *out.status) return;
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const long long cols = (long long)out.parts * out.width, col = (long long)blockIdx.x * 32 + x;
+  const int k = (int)(col / out.width), c = (int)(col - (long long)k * out.width);
+  float* to = col >= cols ? nullptr : k < out.mat_parts ? out.mat + (long long)c * out.mat_parts + k
+                                    : out.vec[k - out.mat_parts] ? out.vec[k - out.mat_parts] + c : nullptr;
   float a = 0.f;
-  if (col < cols) {
+  if (to) {
     long long r = y;
-    for (; r + 24 < rows; r += 32) {
-      const float v0 = partial[r * cols + col], v1 = partial[(r + 8) * cols + col];
-      const float v2 = partial[(r + 16) * cols + col], v3 = partial[(r + 24) * cols + col];
+    for (; r + 96 < rows; r += 128) {
+      const float v0 = partial[r * cols + col], v1 = partial[(r + 32) * cols + col];
+      const float v2 = partial[(r + 64) * cols + col], v3 = partial[(r + 96) * cols + col];
       a += v0;
       a += v1;
       a += v2;
       a += v3;
     }
-    for (; r < rows; r += 8) a += partial[r * cols + col];
+    for (; r < rows; r += 32) a += partial[r * cols + col];
   }
   part[y][x] = a;
   __syncthreads();
-  if (y == 0 && col < cols) {
+  if (y == 0 && to) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) a += part[i][x];
-    const int k = (int)(col / out.width), c = (int)(col - (long long)k * out.width);
-    if (k < out.mat_parts)
-      out.mat[(long long)c * out.mat_parts + k] = a;
-    else if (out.vec[k - out.mat_parts])
-      out.vec[k - out.mat_parts][c] = a;
+    for (int i = 1; i < 32; ++i) a += part[i][x];
+    *to = a;
   }
 }
 
@@ -61,7 +60,7 @@ cudaError_t launch_column_sums(const float* partial, long long rows, const Colum
                                const char* stage) {
   const long long cols = (long long)out.parts * out.width;
   if (cols == 0) return cudaSuccess;
-  column_sums_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, s>>>(partial, rows, out);
+  column_sums_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(partial, rows, out);
   stage_mark(s, stage);
   return cudaGetLastError();
 }

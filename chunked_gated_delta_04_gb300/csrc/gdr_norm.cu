@@ -12,29 +12,53 @@
 namespace gdr {
 namespace {
 
-template <typename IT, typename RT, int TPR, int K>
-__global__ void __launch_bounds__(TPR > 32 ? TPR : 256)
-    norm_fwd_kernel(NormDims d, const IT* __restrict__ x, const float* __restrict__ w_post,
-                    const IT* __restrict__ gate, const float* __restrict__ scale, const RT* __restrict__ residual,
-                    const float* __restrict__ w_pre, void* __restrict__ r_out, IT* __restrict__ y) {
-  constexpr int kRowsPerBlock = TPR > 32 ? 1 : 256 / TPR;
+struct FwdPtrs {
+  const void *x, *gate, *residual;
+  const float *w_post, *scale, *w_pre;
+  void *r, *y;
+};
+
+// A block walks rows and has the next ones' loads in flight while it works on the present ones.
+template <typename IT, typename RT, int TPR, int K, int PARTS>
+__global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(NormDims d, FwdPtrs a) {
+  constexpr int kRows = norm_rows(TPR);
   __shared__ float red[TPR > 32 ? 2 * TPR / 32 : 1];
   int flip = 0;
+  const bool post = PARTS >= 0 ? (PARTS & kNormPost) != 0 : a.w_post != nullptr;
+  const bool gate = PARTS >= 0 ? (PARTS & kNormGate) != 0 : a.gate != nullptr;
+  const bool scale = PARTS >= 0 ? (PARTS & kNormScale) != 0 : a.scale != nullptr;
+  const bool pre = PARTS >= 0 ? (PARTS & kNormPre) != 0 : a.w_pre != nullptr;
+  const bool res = PARTS >= 0 ? (PARTS & kNormRes) != 0 : a.residual != nullptr;
   const int i0 = threadIdx.x % TPR;
-  const long long step = (long long)gridDim.x * kRowsPerBlock;
   const float inv = 1.f / (float)d.D;
-  // rows of a block run together (barriers): the loop's trip count is the block's
-  for (long long base = (long long)blockIdx.x * kRowsPerBlock; base < d.rows; base += step) {
-    const long long row = base + threadIdx.x / TPR;
-    const bool live = row < d.rows;
-    const long long tok = row / d.heads;
-    const int hd = (int)(row - tok * d.heads);
-    const int D = live ? d.D : 0;  // a dead row loads and stores nothing
-    float u[K][8], t[8];
-    const IT* xr = x + tok * d.ld_x + (long long)hd * d.D;
+  struct Row {
+    Raw8<IT> x[K], z[K];
+    Raw8<RT> res[K];
+  };
+  auto load = [&](long long row, Row& o) {
+    const int D = row < d.rows ? d.D : 0;  // a missing row is zeros and is not stored
+    const long long tok = row / d.heads, at = (row - tok * d.heads) * d.D;
 #pragma unroll
-    for (int k = 0; k < K; ++k) load8(xr, 8 * (k * TPR + i0), D, d.vec, u[k]);
-    if (w_post) {
+    for (int k = 0; k < K; ++k) {
+      const int c = 8 * (k * TPR + i0);
+      o.x[k] = load_raw8((const IT*)a.x + tok * d.ld_x + at, c, D, d.vec);
+      if (gate) o.z[k] = load_raw8((const IT*)a.gate + tok * d.ld_gate + at, c, D, d.vec);
+      if (res) o.res[k] = load_raw8((const RT*)a.residual + row * d.D, c, D, d.vec);
+    }
+  };
+  // rows of a block run together (barriers): the loop's trip count is the block's
+  const long long step = (long long)gridDim.x * kRows;
+  long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
+  Row cur;
+  load(row, cur);
+  for (long long base = (long long)blockIdx.x * kRows; base < d.rows; base += step, row += step) {
+    Row next;
+    if (base + step < d.rows) load(row + step, next);
+    const int D = row < d.rows ? d.D : 0;
+    float u[K][8], t[8];
+#pragma unroll
+    for (int k = 0; k < K; ++k) cur.x[k].get(u[k]);
+    if (post) {
       float s[1] = {0.f};
 #pragma unroll
       for (int k = 0; k < K; ++k)
@@ -44,16 +68,15 @@ __global__ void __launch_bounds__(TPR > 32 ? TPR : 256)
       const float rs = rsqrtf(s[0] * inv + d.eps);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        load8(w_post, 8 * (k * TPR + i0), D, d.vec, t);
+        load_raw8(a.w_post, 8 * (k * TPR + i0), D, d.vec).get(t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[k][i] *= rs * t[i];
       }
     }
     if (gate) {
-      const IT* zr = gate + tok * d.ld_gate + (long long)hd * d.D;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        load8(zr, 8 * (k * TPR + i0), D, d.vec, t);
+        cur.z[k].get(t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[k][i] *= t[i] * sigmoid_f(t[i]);
       }
@@ -61,24 +84,24 @@ __global__ void __launch_bounds__(TPR > 32 ? TPR : 256)
     if (scale) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        load8(scale, 8 * (k * TPR + i0), D, d.vec, t);
+        load_raw8(a.scale, 8 * (k * TPR + i0), D, d.vec).get(t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[k][i] *= t[i];
       }
     }
-    if (residual) {
+    if (res) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        load8(residual + row * d.D, 8 * (k * TPR + i0), D, d.vec, t);
+        cur.res[k].get(t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[k][i] = to_f32(from_f32<RT>(u[k][i] + t[i]));
-        store8((RT*)r_out + row * d.D, 8 * (k * TPR + i0), D, d.vec, u[k]);
+        store8((RT*)a.r + row * d.D, 8 * (k * TPR + i0), D, d.vec, u[k]);
       }
-    } else if (!w_pre) {
+    } else if (!pre) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) store8((IT*)r_out + row * d.D, 8 * (k * TPR + i0), D, d.vec, u[k]);
+      for (int k = 0; k < K; ++k) store8((IT*)a.r + row * d.D, 8 * (k * TPR + i0), D, d.vec, u[k]);
     }
-    if (w_pre) {
+    if (pre) {
       float s[1] = {0.f};
 #pragma unroll
       for (int k = 0; k < K; ++k)
@@ -88,12 +111,13 @@ __global__ void __launch_bounds__(TPR > 32 ? TPR : 256)
       const float rs = rsqrtf(s[0] * inv + d.eps);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        load8(w_pre, 8 * (k * TPR + i0), D, d.vec, t);
+        load_raw8(a.w_pre, 8 * (k * TPR + i0), D, d.vec).get(t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) t[i] *= u[k][i] * rs;
-        store8(y + row * d.D, 8 * (k * TPR + i0), D, d.vec, t);
+        store8((IT*)a.y + row * d.D, 8 * (k * TPR + i0), D, d.vec, t);
       }
     }
+    cur = next;
   }
 }
 
@@ -139,18 +163,22 @@ extern "C" gdr_status gdr_norm_fwd(const gdr_norm_problem* p, const void* x, con
           vec_ok(scale) && vec_ok(residual) && vec_ok(w_pre) && vec_ok(r) && vec_ok(y);
   cudaStream_t s = (cudaStream_t)stream;
   stage_begin(s);
+  const FwdPtrs a{x, gate, residual, w_post, scale, w_pre, r, y};
+  const int parts = (w_post ? kNormPost : 0) | (gate ? kNormGate : 0) | (scale ? kNormScale : 0) | (w_pre ? kNormPre : 0) |
+                    (residual ? kNormRes : 0);
   auto go = [&](auto it, auto rt) {
     using IT = decltype(it);
     using RT = decltype(rt);
     return norm_shape(d.D, [&](auto tpr, auto k) {
       constexpr int TPR = decltype(tpr)::value, K = decltype(k)::value;
-      constexpr int kBlock = TPR > 32 ? TPR : 256, kRows = TPR > 32 ? 1 : 256 / TPR;
-      const long long want = (d.rows + kRows - 1) / kRows;
-      const unsigned grid = (unsigned)(want < (1ll << 20) ? want : (1ll << 20));
-      norm_fwd_kernel<IT, RT, TPR, K><<<grid, kBlock, 0, s>>>(d, (const IT*)x, w_post, (const IT*)gate, scale,
-                                                             (const RT*)residual, w_pre, r, (IT*)y);
-      stage_mark(s, "norm_fwd");
-      return cudaGetLastError();
+      return norm_parts(parts, [&](auto pt) {
+        constexpr auto kernel = norm_fwd_kernel<IT, RT, TPR, K, decltype(pt)::value>;
+        static const long long most = (long long)kSmCount * resident_blocks(kernel, norm_block(TPR));
+        const long long want = (d.rows + norm_rows(TPR) - 1) / norm_rows(TPR);
+        kernel<<<(unsigned)(want < most ? want : most), norm_block(TPR), 0, s>>>(d, a);
+        stage_mark(s, "norm_fwd");
+        return cudaGetLastError();
+      });
     });
   };
   if (p->dtype == GDR_DTYPE_F32) return status_of(go(float{}, float{}));

@@ -1,4 +1,4 @@
-// gdr_norm.cuh -- row layout of the block norms' kernels (gdr_norm.cu, gdr_norm_bwd.cu).
+// gdr_norm.cuh -- row layout of the block norms' kernels (gdr_norm.cu, gdr_norm_bwd*.cu).
 //
 // TPR threads hold a row of D channels in registers, K chunks of 8 channels each (chunk k of
 // thread i: channels 8 (k TPR + i) ..).  Up to 32 threads share a warp and reduce by shuffles;
@@ -17,19 +17,64 @@ struct NormDims {
   int vec;  // every pointer and stride 16-byte aligned and D a multiple of 8
 };
 
+// Which tensors a call has.  The kernels are built for the combinations that models use, where
+// what is absent costs no registers, and once for any other (kNormAny: asked at run time).
+enum NormParts { kNormPost = 1, kNormGate = 2, kNormScale = 4, kNormPre = 8, kNormRes = 16, kNormAny = -1 };
+
+// Eight neighbouring channels as they come from memory, converted where they are used, so that a
+// load is not waited for before that.
 template <typename IT>
-__device__ __forceinline__ void load8(const IT* p, int c, int D, int vec, float (&v)[8]) {
-  if (vec) {
-    if (c < D) {
-      load_v<8>(p + c, v);
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < D ? to_f32(p[c + i]) : 0.f;
+struct Raw8;
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 w;
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+};
+// Channels c .. c + 7 of a row of D (zeros past its end).
+template <typename IT>
+__device__ __forceinline__ Raw8<IT> load_raw8(const IT* p, int c, int D, int vec) {
+  Raw8<IT> r;
+  if constexpr (sizeof(IT) == 4) {
+    r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (vec) {
+      if (c < D) {
+        r.a = *reinterpret_cast<const float4*>(p + c);
+        r.b = *reinterpret_cast<const float4*>(p + c + 4);
+      }
+    } else {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c + i < D ? p[c + i] : 0.f;
+      r.a = make_float4(v[0], v[1], v[2], v[3]);
+      r.b = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  } else {
+    r.w = make_uint4(0, 0, 0, 0);
+    if (vec) {
+      if (c < D) r.w = *reinterpret_cast<const uint4*>(p + c);
+    } else {
+      const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c + i < D ? q[c + i] : 0;
+      r.w = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+  }
+  return r;
 }
 template <typename IT>
 __device__ __forceinline__ void store8(IT* p, int c, int D, int vec, const float (&v)[8]) {
@@ -88,7 +133,31 @@ cudaError_t norm_shape(int D, F f) {
   return cudaErrorInvalidValue;
 }
 constexpr int kNormMaxD = 16384;
+constexpr int norm_block(int TPR) { return TPR > 32 ? TPR : 256; }
+constexpr int norm_rows(int TPR) { return norm_block(TPR) / TPR; }  // rows of a block at a time
+
+// f(parts): the built combination of a call's.
+template <typename F>
+cudaError_t norm_parts(int parts, F f) {
+  constexpr int kGated = kNormPost | kNormGate, kAdd = kNormPre | kNormRes;
+  constexpr int kFull = kNormPost | kNormGate | kNormScale | kNormPre | kNormRes;
+  if (parts == kGated) return f(std::integral_constant<int, kGated>{});
+  if (parts == kAdd) return f(std::integral_constant<int, kAdd>{});
+  if (parts == kFull) return f(std::integral_constant<int, kFull>{});
+  return f(std::integral_constant<int, kNormAny>{});
+}
 
 gdr_status resolve_norm(const gdr_norm_problem* p, NormDims* d);
+
+struct NormBwdPtrs {
+  const void *x, *gate, *r, *dr, *dy;
+  const float *w_post, *scale, *w_pre;
+  void *dx, *dgate, *dres;
+  float* partial;  // [grid][3][D]: dw_post, dscale, dw_pre
+};
+// The backward's kernel for one pair of types (gdr_norm_bwd_*.cu).  *grid: blocks, lowered to what
+// fits the GPU at once.
+template <typename IT, typename RT>
+cudaError_t norm_bwd_launch(const NormDims& d, const NormBwdPtrs& a, int parts, long long* grid, cudaStream_t s);
 
 }  // namespace gdr

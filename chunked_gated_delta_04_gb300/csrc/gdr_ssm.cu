@@ -5,8 +5,8 @@
 // Every (channel, state) pair decays at a rate of its own, so there is no matrix product whose
 // factors stay in range: the recurrence runs token by token in fp32 registers.  NL = N / 4 lanes
 // share a channel, four states each; the sum over n runs over those lanes for four tokens at a
-// time.  A block holds CB channels; it stages 16 tokens of D_t, D_t x_t, B_t and C_t in shared memory (formed once
-// per token and channel) while the loads of the next 16 are in flight.  Bound by arithmetic from
+// time.  A block holds CB channels; D_t, D_t x_t, B_t and C_t of 16 tokens are formed once per token
+// and channel and staged in shared memory.  Bound by arithmetic from
 // N = 16 on: per (token, channel, state) one exponential and four multiply-adds, against
 // 6 / N bytes in bf16.
 //
@@ -18,13 +18,18 @@
 namespace gdr {
 namespace {
 
-constexpr int fwd_threads(int NL) { return NL <= 4 ? 128 : 32 * NL; }
+constexpr int fwd_threads(int NL) { return NL == 1 ? 64 : NL <= 4 ? 128 : 32 * NL; }
 
 enum SsmMode { kFull, kEndState, kStartGrad };
 
 // kFull: y (and states, S_T).  kEndState: R[u] = end state of unit u from zero, and sum of D_t.
 // kStartGrad (in reverse): R[u] = gradient of the state in front of unit u from a zero gradient
 // behind it; x is dy, and C plays B's part.
+//
+// One barrier per tile: while tile k is computed from one buffer, tile k + 1 is formed in the other
+// from registers that tile k + 2's loads then refill, and tile k - 1's y leaves.  A thread forms and
+// finishes the same four channels of a token.  (D, D, D x, D x) are kept as register pairs for the
+// packed fp32 instructions, two states at a time.
 template <typename IT, int NL, int MODE>
 __global__ void __launch_bounds__(fwd_threads(NL))
     ssm_scan_kernel(SsmDims d, const IT* __restrict__ x, long long ld_x, const IT* __restrict__ dt,
@@ -33,128 +38,214 @@ __global__ void __launch_bounds__(fwd_threads(NL))
                     const float* __restrict__ start, int start_per_unit, IT* __restrict__ y, float* __restrict__ S_T,
                     float* __restrict__ h_saved, float* __restrict__ R, float* __restrict__ sum_delta) {
   constexpr int NT = fwd_threads(NL), CB = NT / NL, N = 4 * NL;
-  constexpr int PER = kTile * CB / NT, PB = (kTile * N + NT - 1) / NT;
-  __shared__ float sd[kTile][CB], su[kTile][CB], sx[MODE == kFull ? kTile : 1][CB];
-  __shared__ __align__(16) float sB[kTile][N], sC[MODE == kFull ? kTile : 1][N];
+  constexpr int Q = CB / 4, QP = NL >= 4 ? 1 : 4 / NL;  // quads of channels; quads of a tile per thread
+  constexpr int YS = CB + 8;                            // padded rows: 4 tokens x 8 channels hit 32 banks
+  constexpr bool kY = MODE == kFull;
+  __shared__ Pair2 sdu[2][kTile][CB];  // {D, D}, {D x, D x}, at slot(channel)
+  __shared__ __align__(16) float sB[2][kTile][N], sC[kY ? 2 : 1][kTile][N];
+  __shared__ __align__(16) float sy[kY ? 2 : 1][kY ? kTile : 1][YS];
   if (ssm_bad(d)) return;
+  // 16-byte slots: a quad's four stores and a warp's loads of eight channels each hit all banks
+  auto slot = [](int c) { return c ^ ((c >> 3) & 3); };
   const int tid = threadIdx.x, ln = tid % NL, ch = tid / NL;
   const int blocks = (d.Dg + CB - 1) / CB, grp = blockIdx.x / blocks, c0 = (blockIdx.x - grp * blocks) * CB;
-  const int nch = min(CB, d.Dg - c0);           // live channels of this block
+  const int nch = min(CB, d.Dg - c0);                // live channels of this block
   const long long dc0 = (long long)grp * d.Dg + c0;  // its first channel
   const bool live = ch < nch;
   const long long dch = dc0 + ch;
-  float A2[4] = {};
+  f32x2 A2[2] = {0, 0};
   if (live) {
     const float4 a = *reinterpret_cast<const float4*>(A + dch * N + 4 * ln);
     // finite, so that D = 0 past the end gives exp(0) = 1 also for A = -infinity
-    A2[0] = fmaxf(a.x * kLog2e, -kBig); A2[1] = fmaxf(a.y * kLog2e, -kBig);
-    A2[2] = fmaxf(a.z * kLog2e, -kBig); A2[3] = fmaxf(a.w * kLog2e, -kBig);
+    A2[0] = pack2(fmaxf(a.x * kLog2e, -kBig), fmaxf(a.y * kLog2e, -kBig));
+    A2[1] = pack2(fmaxf(a.z * kLog2e, -kBig), fmaxf(a.w * kLog2e, -kBig));
   }
-  const float skip = MODE == kFull && Dskip && live ? Dskip[dch] : 0.f;
+  // staging: quad of channels qc of token qt (+ 4 NL tokens per further quad)
+  const int qc = 4 * (tid % Q), qt = tid / Q, qn = qt < kTile ? nch - qc : 0;
+  float bias[4] = {}, skip[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (dt_bias && i < qn) bias[i] = dt_bias[dc0 + qc + i];
+    if (kY && Dskip && i < qn) skip[i] = Dskip[dc0 + qc + i];
+  }
+  const bool vec = d.vec & 1, vec_bc = d.vec & 2;
+  const bool is_c = tid >= 4 * N, has_bc = tid < (kY ? 8 : 4) * N;  // one quad of B or C per thread
+  const int bt = (tid % (4 * N)) / NL, bn = 4 * (tid % NL);
+  const IT* bc_src = is_c ? Cm : Bm;
+  const long long ld_bc = is_c ? d.ld_c : ld_b;
 
   const long long units = ssm_unit_count(d);
   for (long long un = blockIdx.y; un < units; un += gridDim.y) {
     const SsmUnit q = ssm_unit(d, un);
-    float h[4] = {};
-    if (MODE == kFull && start && live) {
+    f32x2 h[2] = {0, 0};
+    if (kY && start && live) {
       const long long at = start_per_unit ? un : q.seq;
       const float4 v = *reinterpret_cast<const float4*>(start + (at * d.D + dch) * N + 4 * ln);
-      h[0] = v.x; h[1] = v.y; h[2] = v.z; h[3] = v.w;
+      h[0] = pack2(v.x, v.y);
+      h[1] = pack2(v.z, v.w);
     }
     float dsum = 0.f;
     const int tiles = (q.len + kTile - 1) / kTile;
-    IT px[PER], pd[PER], pB[PB], pC[PB];
-    auto fetch = [&](int tile) {
-      const int base = (MODE == kStartGrad ? tiles - 1 - tile : tile) * kTile;
+    auto base_of = [&](int k) { return (MODE == kStartGrad ? tiles - 1 - k : k) * kTile; };
+    // a tile whose 16 tokens and CB channels all exist, aligned: no bounds in its loads and stores
+    auto whole = [&](int k) { return vec && nch == CB && base_of(k) + kTile <= q.len; };
+    Raw4<IT> rx[QP], rd[QP], rb, x0[QP], x1[QP];  // loads under way; x of the two tiles before
+    const IT* xq = x + (long long)q.t0 * ld_x + dc0 + qc;
+    const IT* dq = dt + (long long)q.t0 * d.ld_dt + dc0 + qc;
+    const IT* bq = bc_src + (long long)q.t0 * ld_bc + (long long)grp * N + bn;
+    IT* yq = kY ? y + (long long)q.t0 * d.D + dc0 + qc : nullptr;
+    auto fetch = [&](int k) {
+      const int base = base_of(k);
+      const long long t0 = base + qt;
+      if (whole(k)) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = i * NT + tid, t = base + e / CB, c = e % CB;
-        const bool in = t < q.len && c < nch;
-        px[i] = in ? x[(long long)(q.t0 + t) * ld_x + dc0 + c] : from_f32<IT>(0.f);
-        pd[i] = in ? dt[(long long)(q.t0 + t) * d.ld_dt + dc0 + c] : from_f32<IT>(0.f);
-      }
+        for (int i = 0; i < QP; ++i)
+          if (qt < kTile) {
+            rx[i] = load_raw4(xq + (t0 + i * (NT / Q)) * ld_x, 4, true);
+            rd[i] = load_raw4(dq + (t0 + i * (NT / Q)) * d.ld_dt, 4, true);
+          }
+      } else {
 #pragma unroll
-      for (int i = 0; i < PB; ++i) {
-        const int e = i * NT + tid, t = base + e / N, n = e % N;
-        const bool in = e < kTile * N && t < q.len;
-        pB[i] = in ? Bm[(long long)(q.t0 + t) * ld_b + grp * N + n] : from_f32<IT>(0.f);
-        if (MODE == kFull) pC[i] = in ? Cm[(long long)(q.t0 + t) * d.ld_c + grp * N + n] : from_f32<IT>(0.f);
-      }
-    };
-    if (tiles > 0) fetch(0);
-    for (int tile = 0; tile < tiles; ++tile) {
-      const int base = (MODE == kStartGrad ? tiles - 1 - tile : tile) * kTile;
-      __syncthreads();  // the previous tile's readers are done
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = i * NT + tid, t = e / CB, c = e % CB;
-        const bool in = base + t < q.len && c < nch;
-        const float xv = to_f32(px[i]);
-        float raw = to_f32(pd[i]);
-        if (in && dt_bias) raw += dt_bias[dc0 + c];
-        float dl = 0.f;  // past the end: D = 0 leaves the state as it is
-        if (in) dl = d.softplus ? softplus_f(raw, nullptr) : raw;
-        sd[t][c] = dl;
-        su[t][c] = MODE == kStartGrad ? xv : dl * xv;
-        if (MODE == kFull) sx[t][c] = xv;
-      }
-#pragma unroll
-      for (int i = 0; i < PB; ++i) {
-        const int e = i * NT + tid;
-        if (e < kTile * N) {
-          sB[e / N][e % N] = to_f32(pB[i]);
-          if (MODE == kFull) sC[e / N][e % N] = to_f32(pC[i]);
+        for (int i = 0; i < QP; ++i) {
+          const long long t = t0 + i * (NT / Q);
+          const int n = t < q.len ? qn : 0;
+          rx[i] = load_raw4(xq + t * ld_x, n, vec);
+          rd[i] = load_raw4(dq + t * d.ld_dt, n, vec);
         }
       }
-      __syncthreads();
-      if (tile + 1 < tiles) fetch(tile + 1);
-      if (MODE == kFull && h_saved && live)
-        *reinterpret_cast<float4*>(h_saved + ((q.tile0 + tile) * d.D + dch) * N + 4 * ln) =
-            make_float4(h[0], h[1], h[2], h[3]);
+      if (has_bc) rb = load_raw4(bq + (base + bt) * ld_bc, base + bt < q.len ? 4 : 0, vec_bc);
+    };
+    auto form = [&](int k) {  // tile k from the registers
+      const int base = base_of(k), buf = k & 1;
+      const bool full = whole(k);
 #pragma unroll
-      for (int t4 = 0; t4 < kTile; t4 += 4) {
+      for (int i = 0; i < QP; ++i) {
+        const int tt = qt + i * (NT / Q);
+        float xv[4], dv[4];
+        rx[i].get(xv);
+        rd[i].get(dv);
+        if (kY) {
+          x0[i] = x1[i];
+          x1[i] = rx[i];
+        }
+        if (qt < kTile) {
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            f32x2 dl = add2(pack2(dv[c], dv[c + 1]), pack2(bias[c], bias[c + 1]));
+            if (d.softplus) dl = softplus2(lo2(dl), hi2(dl), nullptr, nullptr);
+            if (!full) {  // past the end the state stays as it is
+              const int n = base + tt < q.len ? qn : 0;
+              dl = pack2(c < n ? lo2(dl) : 0.f, c + 1 < n ? hi2(dl) : 0.f);
+            }
+            f32x2 u = pack2(xv[c], xv[c + 1]);
+            if (MODE != kStartGrad) u = mul2(dl, u);
+            sdu[buf][tt][slot(qc + c)] = Pair2{pack2(lo2(dl), lo2(dl)), pack2(lo2(u), lo2(u))};
+            sdu[buf][tt][slot(qc + c + 1)] = Pair2{pack2(hi2(dl), hi2(dl)), pack2(hi2(u), hi2(u))};
+          }
+        }
+      }
+      if (has_bc) {
+        float v[4];
+        rb.get(v);
+        *reinterpret_cast<float4*>(is_c ? &sC[kY ? buf : 0][bt][bn] : &sB[buf][bt][bn]) = make_float4(v[0], v[1], v[2], v[3]);
+      }
+    };
+    // y of tile k; xs: its x
+    auto finish = [&](int k, const Raw4<IT>(&xs)[QP]) {
+      if constexpr (kY) {
+        const bool full = whole(k);
+#pragma unroll
+        for (int i = 0; i < QP; ++i) {
+          const int tt = qt + i * (NT / Q);
+          const long long t = k * kTile + tt;
+          if (qt < kTile) {
+            float xv[4], v[4];
+            xs[i].get(xv);
+            const float4 p = *reinterpret_cast<const float4*>(&sy[k & 1][tt][qc]);
+            v[0] = fmaf(skip[0], xv[0], p.x); v[1] = fmaf(skip[1], xv[1], p.y);
+            v[2] = fmaf(skip[2], xv[2], p.z); v[3] = fmaf(skip[3], xv[3], p.w);
+            if (full)
+              store4(yq + t * d.D, 4, true, v);
+            else
+              store4(yq + t * d.D, t < q.len ? qn : 0, vec, v);
+          }
+        }
+      }
+    };
+    if (tiles > 0) {
+      fetch(0);
+      form(0);
+      if (tiles > 1) fetch(1);
+    }
+    const int sl = slot(ch);
+    for (int k = 0; k < tiles; ++k) {
+      const int buf = k & 1;
+      __syncthreads();
+      // Groups of four tokens: a group's loads and exponentials (which nothing in the recurrence
+      // waits for) are issued a group ahead of its recurrence.
+      f32x2 e[2][4][2], ub[2][4][2];
+      Pair2 cc[2][4];
+      auto ahead = [&](int g) {
+        const int w = g & 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = MODE == kStartGrad ? kTile - 1 - (4 * g + i) : 4 * g + i;
+          const Pair2 du = sdu[buf][t][sl];
+          const Pair2 b = *reinterpret_cast<const Pair2*>(&sB[buf][t][4 * ln]);
+          if (kY) cc[w][i] = *reinterpret_cast<const Pair2*>(&sC[kY ? buf : 0][t][4 * ln]);
+          e[w][i][0] = ex2_2(mul2(du.a, A2[0]));
+          e[w][i][1] = ex2_2(mul2(du.a, A2[1]));
+          ub[w][i][0] = mul2(du.b, b.a);
+          ub[w][i][1] = mul2(du.b, b.b);
+          if (!kY) dsum += lo2(du.a);
+        }
+      };
+      ahead(0);
+      if (k > 0) finish(k - 1, x0);
+      if (k + 1 < tiles) {
+        form(k + 1);  // x0 becomes tile k's x, x1 tile k + 1's
+      } else if (kY) {
+#pragma unroll
+        for (int i = 0; i < QP; ++i) x0[i] = x1[i];
+      }
+      if (k + 2 < tiles) fetch(k + 2);
+      if (kY && h_saved && live)
+        *reinterpret_cast<float4*>(h_saved + ((q.tile0 + k) * d.D + dch) * N + 4 * ln) =
+            make_float4(lo2(h[0]), hi2(h[0]), lo2(h[1]), hi2(h[1]));
+#pragma unroll
+      for (int g = 0; g < kTile / 4; ++g) {
+        if (g + 1 < kTile / 4) ahead(g + 1);
+        const int w = g & 1;
         float p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int t = MODE == kStartGrad ? kTile - 1 - (t4 + i) : t4 + i;
-          const float dl = sd[t][ch], uu = su[t][ch];
-          const float4 b = *reinterpret_cast<const float4*>(&sB[t][4 * ln]);
-          const float bb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float a = ex2f(dl * A2[j]);
-            h[j] = MODE == kStartGrad ? a * fmaf(uu, bb[j], h[j]) : fmaf(a, h[j], uu * bb[j]);
-          }
-          if (MODE == kFull) {
-            const float4 c = *reinterpret_cast<const float4*>(&sC[t][4 * ln]);
-            p[i] = fmaf(h[0], c.x, fmaf(h[1], c.y, fmaf(h[2], c.z, h[3] * c.w)));
+          if (MODE == kStartGrad) {
+            h[0] = mul2(e[w][i][0], add2(ub[w][i][0], h[0]));
+            h[1] = mul2(e[w][i][1], add2(ub[w][i][1], h[1]));
           } else {
-            dsum += dl;
+            h[0] = fma2(e[w][i][0], h[0], ub[w][i][0]);
+            h[1] = fma2(e[w][i][1], h[1], ub[w][i][1]);
+          }
+          if (kY) {
+            const f32x2 s = fma2(h[0], cc[w][i].a, mul2(h[1], cc[w][i].b));
+            p[i] = lo2(s) + hi2(s);
           }
         }
-        if (MODE == kFull) {
-          LaneSum<NL>::run(p, ln);
-          if (LaneSum<NL>::holds(ln)) {
+        if (kY) {
+          using Sum = LaneSums<4, NL, 1>;
+          Sum::run(p, ln);
+          if (Sum::holds(ln)) {
 #pragma unroll
-            for (int k = 0; k < LaneSum<NL>::kKeep; ++k) {
-              const int t = t4 + LaneSum<NL>::tok(ln) + k;
-              su[t][ch] = fmaf(skip, sx[t][ch], p[k]);  // D_t x_t of these tokens has been used
-            }
+            for (int i = 0; i < Sum::KEEP; ++i) sy[kY ? buf : 0][kY ? 4 * g + Sum::index(ln) + i : 0][ch] = p[i];
           }
-        }
-      }
-      if (MODE == kFull) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int e = i * NT + tid, t = e / CB, c = e % CB;
-          if (base + t < q.len && c < nch) y[(long long)(q.t0 + base + t) * d.D + dc0 + c] = from_f32<IT>(su[t][c]);
         }
       }
     }
+    __syncthreads();
+    if (tiles > 0) finish(tiles - 1, x0);
     if (live) {
-      const float4 v = make_float4(h[0], h[1], h[2], h[3]);
-      if (MODE == kFull) {
+      const float4 v = make_float4(lo2(h[0]), hi2(h[0]), lo2(h[1]), hi2(h[1]));
+      if (kY) {
         if (S_T && q.last) *reinterpret_cast<float4*>(S_T + ((long long)q.seq * d.D + dch) * N + 4 * ln) = v;
       } else {
         *reinterpret_cast<float4*>(R + (un * d.D + dch) * N + 4 * ln) = v;
@@ -331,6 +422,13 @@ unsigned unit_rows(const SsmDims& d) { return (unsigned)(d.max_units < 32768 ? d
 
 }  // namespace
 
+int ssm_vec(const SsmDims& d, size_t el, std::initializer_list<const void*> rows, std::initializer_list<const void*> bc) {
+  bool v = d.Dg % 4 == 0 && d.ld_x % 4 == 0 && d.ld_dt % 4 == 0 && d.ld_dy % 4 == 0, b = d.ld_b % 4 == 0 && d.ld_c % 4 == 0;
+  for (const void* p : rows) v = v && elem_ok(p, 4 * el);
+  for (const void* p : bc) b = b && elem_ok(p, 4 * el);
+  return (v ? 1 : 0) | (b ? 2 : 0);
+}
+
 bool ssm_split(const SsmDims& d) { return d.Lseg < d.T; }
 
 gdr_status resolve_ssm(const gdr_ssm_problem* p, bool step, SsmDims* d) {
@@ -368,7 +466,7 @@ gdr_status resolve_ssm(const gdr_ssm_problem* p, bool step, SsmDims* d) {
   // of at least 64 tokens, enough of them for four blocks per SM.
   const long long blocks = fwd_blocks(*d), whole = (d->T + kTile - 1) / kTile * (long long)kTile;
   d->Lseg = (int)(whole < kTile ? kTile : whole);
-  if (!step && blocks * d->num_seqs < 2 * kSmCount) {
+  if (!step && blocks * d->num_seqs < kSmCount) {
     const long long want = (4ll * kSmCount + blocks - 1) / blocks;  // segments over all sequences
     long long L = (d->total / want + kTile - 1) / kTile * kTile;
     if (L < 64) L = 64;
@@ -477,6 +575,7 @@ gdr_status gdr_ssm_fwd(const gdr_ssm_problem* p, const void* x, const void* dt, 
   const SsmWorkspace w = ssm_workspace(d, (char*)workspace, false);
   if (!workspace || workspace_bytes < w.bytes) return GDR_ERR_WORKSPACE;
   if (d.num_seqs == 0) return GDR_OK;
+  d.vec = ssm_vec(d, el, {x, dt, y}, {Bm, Cm});
   cudaStream_t s = (cudaStream_t)stream;
   stage_begin(s);
   cudaError_t e = ssm_launch_index(&d, w, s);

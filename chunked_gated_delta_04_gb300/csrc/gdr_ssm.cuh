@@ -6,6 +6,8 @@
 // every 16 tokens of a sequence (a tile).
 #pragma once
 
+#include <initializer_list>
+
 #include "gdr_block.cuh"
 
 namespace gdr {
@@ -16,6 +18,7 @@ constexpr float kBig = 3.4e38f;
 struct SsmDims {
   int D, N, G, Dg, T, num_seqs, softplus;
   long long total, ld_x, ld_dt, ld_b, ld_c, ld_dy;
+  int vec;  // rows of x, dt, dy and outputs (bit 0), of B and C (bit 1) aligned to four elements
   int Lseg;
   int seq_units, seq_tiles;  // fixed length: units and tiles of a sequence
   long long max_units, max_tiles;
@@ -73,6 +76,8 @@ struct SsmWorkspace {
   size_t bytes;
 };
 
+// SsmDims::vec for a call's pointers (rows: of D channels; bc: of G N states).
+int ssm_vec(const SsmDims& d, size_t el, std::initializer_list<const void*> rows, std::initializer_list<const void*> bc);
 bool ssm_split(const SsmDims& d);
 gdr_status resolve_ssm(const gdr_ssm_problem* p, bool step, SsmDims* d);
 SsmWorkspace ssm_workspace(const SsmDims& d, char* base, bool backward);
@@ -103,33 +108,127 @@ cudaError_t ssm_lanes(int N, F f) {
   }
 }
 
-// Four values (of tokens 4 i .. 4 i + 3) summed over the NL lanes of a channel.  Afterwards lane ln
-// holds kKeep of the sums, v[0 .. kKeep), of tokens tok(ln) + 0 .. kKeep - 1; holds(ln) says whether
-// it is the one to use them.
-template <int NL>
-struct LaneSum {
-  static constexpr int kKeep = NL >= 4 ? 1 : NL == 2 ? 2 : 4;
-  __device__ static __forceinline__ int tok(int ln) { return NL >= 4 ? ln & 3 : NL == 2 ? 2 * (ln & 1) : 0; }
-  __device__ static __forceinline__ bool holds(int ln) { return NL <= 4 || ln < 4; }
-  __device__ static __forceinline__ void run(float (&v)[4], int ln) {
-    if constexpr (NL >= 4) {
-      const bool hi = ln & 2;
+// Two fp32 values in a register pair, for the packed fp32 instructions.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float lo2(f32x2 v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(f32x2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 ex2_2(f32x2 v) { return pack2(ex2f(lo2(v)), ex2f(hi2(v))); }
+
+// softplus_f of two values (and, with sig, their sigmoids).
+__device__ __forceinline__ f32x2 softplus2(float x, float y, float* sigx, float* sigy) {
+  const float u = ex2f(-kLog2e * fabsf(x)), v = ex2f(-kLog2e * fabsf(y));
+  const f32x2 uv = pack2(u, v);
+  const f32x2 den = add2(uv, pack2(2.f, 2.f));
+  const f32x2 s = mul2(uv, pack2(rcpf(lo2(den)), rcpf(hi2(den)))), q = mul2(s, s);
+  f32x2 p = pack2(artanh_c(4), artanh_c(4));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float send = hi ? v[i] : v[i + 2], keep = hi ? v[i + 2] : v[i];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2);
-      }
-      const bool h1 = ln & 1;
-      const float send = h1 ? v[0] : v[1], keep = h1 ? v[1] : v[0];
-      v[0] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
+  for (int i = 3; i >= 0; --i) p = fma2(p, q, pack2(artanh_c(i), artanh_c(i)));
+  if (sigx) {
+    const float r = rcpf(1.f + u), t = rcpf(1.f + v);
+    *sigx = x >= 0.f ? r : u * r;
+    *sigy = y >= 0.f ? t : v * t;
+  }
+  return fma2(add2(s, s), p, pack2(fmaxf(x, 0.f), fmaxf(y, 0.f)));
+}
+
+struct alignas(16) Pair2 {
+  f32x2 a, b;
+};
+
+// Four neighbouring elements of a row as they come from memory, converted where they are used, so
+// that the load is not waited for before that.
+template <typename IT>
+struct Raw4;
+template <>
+struct Raw4<float> {
+  float4 v;
+  __device__ __forceinline__ void get(float (&o)[4]) const { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void get(float (&o)[4]) const {
+    o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xffff0000u);
+    o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+};
+// n of the four exist (n <= 0: none); vec: they are aligned to the four elements' size.
+template <typename IT>
+__device__ __forceinline__ Raw4<IT> load_raw4(const IT* p, int n, bool vec) {
+  Raw4<IT> r;
+  if (vec && n >= 4) {
+    r.v = *reinterpret_cast<const decltype(r.v)*>(p);
+  } else if constexpr (sizeof(IT) == 4) {
+    r.v = make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
+  } else {
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+    const uint32_t a = n > 0 ? q[0] : 0, b = n > 1 ? q[1] : 0, c = n > 2 ? q[2] : 0, e = n > 3 ? q[3] : 0;
+    r.v = make_uint2(a | b << 16, c | e << 16);
+  }
+  return r;
+}
+template <typename IT>
+__device__ __forceinline__ void store4(IT* p, int n, bool vec, const float (&v)[4]) {
+  if (vec && n >= 4) {
+    if constexpr (sizeof(IT) == 4) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+      *reinterpret_cast<uint2*>(p) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+  } else {
 #pragma unroll
-      for (int o = 4; o < NL; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-    } else if constexpr (NL == 2) {
-      const bool hi = ln & 1;
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = from_f32<IT>(v[i]);
+  }
+}
+
+// NV values in every lane, summed over LANES = 2^k lanes that are OFF apart: each exchange halves
+// the values a lane keeps, so it takes about NV exchanges in place of NV log2(LANES).  Lane l (of
+// the LANES) ends with the sums of values index(l) .. index(l) + KEEP - 1 in v[0 .. KEEP).
+template <int NV, int LANES, int OFF>
+struct LaneSums {
+  static constexpr int KEEP = NV >= LANES ? NV / LANES : 1;
+  __device__ static __forceinline__ int index(int l) {
+    int at = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float send = hi ? v[i] : v[i + 2], keep = hi ? v[i + 2] : v[i];
-        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
+    for (int m = NV / 2, b = 1; m >= 1 && b < LANES; m >>= 1, b <<= 1) at += l & b ? m : 0;
+    return at;
+  }
+  __device__ static __forceinline__ bool holds(int l) { return l < NV; }  // once per value
+  __device__ static __forceinline__ void run(float* v, int l) {
+#pragma unroll
+    for (int m = NV / 2, b = 1; b < LANES; m >>= 1, b <<= 1) {
+      if (m >= 1) {
+        const bool hi = l & b;
+#pragma unroll
+        for (int i = 0; i < m; ++i) {
+          const float send = hi ? v[i] : v[i + m], keep = hi ? v[i + m] : v[i];
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, b * OFF);
+        }
+      } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], b * OFF);
       }
     }
   }

@@ -5,17 +5,19 @@
 //   dB_t = sum_d dh_t D_t x_t,   dC_t = sum_d dy_t h_t,   ddt = dD_t softplus'(dt + dt_bias),   dS0 = a_0 dh_0.
 //
 // A block walks its units' tiles of 16 tokens from the last to the first.  The forward left the
-// state at the start of every tile, so the tile's 16 states are formed again in registers (16 x 4
-// per thread) and then used in reverse; the decays are formed again too (an exponential costs less
-// than 64 more registers).  Sums: over n across the lanes of a channel, over the channels of a warp
-// by exchanges that halve the values a lane keeps, over warps in shared memory, over blocks by a
-// second kernel from per-block partial rows in order, so results do not depend on timing.
+// state at the start of every tile, so the tile's 16 states and decays are formed again in registers
+// (a thread: two channels by two states) and then used in reverse.  Two channels share a register
+// pair for the packed fp32 instructions.  Sums: over n across the N / 2 lanes of a channel pair and over the
+// channels of a warp, by exchanges that halve the values a lane keeps; over warps in shared memory;
+// over blocks by a second kernel from per-block partial rows, in order: results do not depend on timing.
+// Bound by instruction issue: about 20 per (token, channel, state) and thread, a third of them the
+// exchanges.
 #include "gdr_ssm.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int bwd_threads(int NL) { return NL == 1 ? 64 : NL == 2 ? 128 : 256; }
+constexpr int bwd_threads(int N) { return N == 4 ? 128 : 256; }
 
 struct SsmBwdArgs {
   const void *x, *dt, *Bm, *Cm, *dy;
@@ -25,205 +27,291 @@ struct SsmBwdArgs {
   float *dS0, *grads, *bc;
 };
 
-template <typename IT, int NL>
-__global__ void __launch_bounds__(bwd_threads(NL), 1) ssm_bwd_kernel(SsmDims d, SsmBwdArgs a) {
-  constexpr int NT = bwd_threads(NL), CB = NT / NL, N = 4 * NL, WARPS = NT / 32, CL = 32 / NL;
-  constexpr int PER = kTile * CB / NT, PB = (kTile * N + NT - 1) / NT;
-  extern __shared__ __align__(16) float smem[];
-  float(*sd)[CB] = reinterpret_cast<float(*)[CB]>(smem);                // D_t
-  float(*sx)[CB] = sd + kTile;                                          // x_t, then ddt
-  float(*sy)[CB] = sx + kTile;                                          // dy_t, then dx
-  float(*sg)[CB] = sy + kTile;                                          // softplus' (0 past the end)
-  float(*sB)[N] = reinterpret_cast<float(*)[N]>(sg + kTile);
-  float(*sC)[N] = sB + kTile;
-  float* red = reinterpret_cast<float*>(sC + kTile);                    // [WARPS][16][2 N]
+// Shared memory of a block, two tiles of everything: the one being computed and the one that is
+// formed (or finished) beside it.
+template <int N>
+struct BwdSmem {
+  static constexpr int NT = bwd_threads(N), ML = N / 2, CB = 2 * NT / ML, WARPS = NT / 32;
+  Pair2 du[2][kTile][CB / 2];                      // {D, D'}, {D x, D' x'} of a channel pair
+  f32x2 dy[2][kTile][CB / 2];
+  alignas(16) float x[2][kTile][CB], sig[2][kTile][CB];
+  // sum_n dh B and sum_n l A; padded so that the eight values (two of each, of two tokens and two
+  // channels) that the lanes of a pair hold, for the four pairs of a warp, hit 32 banks
+  static constexpr int SR = CB + 8, SN = kTile * SR + 16;
+  alignas(16) float s[2][2][SN];
+  alignas(16) f32x2 B[2][kTile][N], C[2][kTile][N];      // each value twice
+  float red[2][WARPS][kTile][2 * N];                     // dB, dC of a warp's channels
+};
+
+template <typename IT, int N>
+__global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, SsmBwdArgs a) {
+  using Smem = BwdSmem<N>;
+  constexpr int NT = Smem::NT, ML = Smem::ML, CB = Smem::CB, WARPS = Smem::WARPS, CL = 32 / ML;
+  constexpr int Q = CB / 4, QP = 4 * CB > NT ? 4 * CB / NT : 1;  // quads of channels; of a tile per thread
+  constexpr int BQ = (8 * N + NT - 1) / NT;                      // quads of B and C per thread
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   if (ssm_bad(d)) return;
-  const int tid = threadIdx.x, ln = tid % NL, ch = tid / NL, lane = tid & 31, warp = tid >> 5, cl = lane / NL;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nl = tid % ML, cl = lane / ML, pr = tid / ML;  // states 2 nl, 2 nl + 1 of channel pair pr
   const int blocks = (d.Dg + CB - 1) / CB, grp = blockIdx.x / blocks, blk = blockIdx.x - grp * blocks, c0 = blk * CB;
   const int nch = min(CB, d.Dg - c0);
   const long long dc0 = (long long)grp * d.Dg + c0;
-  const bool live = ch < nch;
-  const long long dch = dc0 + ch;
-  float A1[4] = {}, A2[4] = {};
-  if (live) {
-    const float4 v = *reinterpret_cast<const float4*>(a.A + dch * N + 4 * ln);
-    A1[0] = v.x; A1[1] = v.y; A1[2] = v.z; A1[3] = v.w;
+  const bool live0 = 2 * pr < nch, live1 = 2 * pr + 1 < nch;
+  const long long dch = dc0 + 2 * pr;
+  // pairs over the two channels, of state j; a missing channel has A = 0 and loads zeros
+  auto load_pair = [&](const float* p, f32x2 (&v)[2]) {  // p: [D][N]
+    const float2 u = live0 ? *reinterpret_cast<const float2*>(p + dch * N + 2 * nl) : make_float2(0.f, 0.f);
+    const float2 w = live1 ? *reinterpret_cast<const float2*>(p + (dch + 1) * N + 2 * nl) : make_float2(0.f, 0.f);
+    v[0] = pack2(u.x, w.x);
+    v[1] = pack2(u.y, w.y);
+  };
+  f32x2 A1[2], A2[2];
+  load_pair(a.A, A1);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) A2[j] = fmaxf(A1[j] * kLog2e, -kBig);
+  for (int j = 0; j < 2; ++j) A2[j] = pack2(fmaxf(lo2(A1[j]) * kLog2e, -kBig), fmaxf(hi2(A1[j]) * kLog2e, -kBig));
+  f32x2 dA[2] = {0, 0};
+  float dDs[4] = {}, dbias[4] = {};
+  const int qc = 4 * (tid % Q), qt = tid / Q, qn = qt < kTile ? nch - qc : 0;
+  float bias[4] = {}, skip[4] = {};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (a.dt_bias && i < qn) bias[i] = a.dt_bias[dc0 + qc + i];
+    if (a.Dskip && i < qn) skip[i] = a.Dskip[dc0 + qc + i];
   }
-  const float skip = a.Dskip && live ? a.Dskip[dch] : 0.f;
-  float dA[4] = {}, dDs = 0.f, dbias = 0.f;
-  const IT *x = (const IT*)a.x, *dt = (const IT*)a.dt, *Bm = (const IT*)a.Bm, *Cm = (const IT*)a.Cm, *dy = (const IT*)a.dy;
+  const bool vec = d.vec & 1, vec_bc = d.vec & 2;
 
   const long long units = ssm_unit_count(d);
   for (long long un = blockIdx.y; un < units; un += gridDim.y) {
     const SsmUnit q = ssm_unit(d, un);
-    float dh[4] = {};
-    if (a.edge && live) {
-      const float4 v = *reinterpret_cast<const float4*>(a.edge + ((a.edge_per_unit ? un : q.seq) * d.D + dch) * N + 4 * ln);
-      dh[0] = v.x; dh[1] = v.y; dh[2] = v.z; dh[3] = v.w;
-    }
+    f32x2 dh[2] = {0, 0};
+    if (a.edge) load_pair(a.edge + (a.edge_per_unit ? un : q.seq) * (long long)d.D * N, dh);
     const int tiles = (q.len + kTile - 1) / kTile;
-    IT px[PER], pd[PER], py[PER], pB[PB], pC[PB];
-    float4 ph = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto fetch = [&](int tile) {
-      const int base = tile * kTile;
+    const IT* xq = (const IT*)a.x + (long long)q.t0 * d.ld_x + dc0 + qc;
+    const IT* dq = (const IT*)a.dt + (long long)q.t0 * d.ld_dt + dc0 + qc;
+    const IT* yq = (const IT*)a.dy + (long long)q.t0 * d.ld_dy + dc0 + qc;
+    Raw4<IT> rx[QP], rd[QP], ry[QP], rb[BQ];
+    f32x2 ph[2] = {0, 0};
+    // step k works on tile tiles - 1 - k; whole: its 16 tokens and CB channels all exist, aligned
+    auto whole = [&](int k) { return vec && nch == CB && (tiles - k) * kTile <= q.len; };
+    auto fetch = [&](int k) {
+      const int base = (tiles - 1 - k) * kTile;
+      if (whole(k)) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = i * NT + tid, t = base + e / CB, c = e % CB;
-        const bool in = t < q.len && c < nch;
-        const long long tok = q.t0 + t;
-        px[i] = in ? x[tok * d.ld_x + dc0 + c] : from_f32<IT>(0.f);
-        pd[i] = in ? dt[tok * d.ld_dt + dc0 + c] : from_f32<IT>(0.f);
-        py[i] = in ? dy[tok * d.ld_dy + dc0 + c] : from_f32<IT>(0.f);
+        for (int i = 0; i < QP; ++i) {
+          const long long t = base + qt + i * (NT / Q);
+          if (qt < kTile) {
+            rx[i] = load_raw4(xq + t * d.ld_x, 4, true);
+            rd[i] = load_raw4(dq + t * d.ld_dt, 4, true);
+            ry[i] = load_raw4(yq + t * d.ld_dy, 4, true);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < QP; ++i) {
+          const long long t = base + qt + i * (NT / Q);
+          const int n = t < q.len ? qn : 0;
+          rx[i] = load_raw4(xq + t * d.ld_x, n, vec);
+          rd[i] = load_raw4(dq + t * d.ld_dt, n, vec);
+          ry[i] = load_raw4(yq + t * d.ld_dy, n, vec);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < PB; ++i) {
-        const int e = i * NT + tid, t = base + e / N, n = e % N;
-        const bool in = e < kTile * N && t < q.len;
-        pB[i] = in ? Bm[(long long)(q.t0 + t) * d.ld_b + grp * N + n] : from_f32<IT>(0.f);
-        pC[i] = in ? Cm[(long long)(q.t0 + t) * d.ld_c + grp * N + n] : from_f32<IT>(0.f);
+      for (int i = 0; i < BQ; ++i) {
+        const int e = i * NT + tid, w = e % (4 * N), t = base + w / (N / 4), n = 4 * (w % (N / 4));
+        if (e < 8 * N) {
+          const IT* p = e < 4 * N ? (const IT*)a.Bm + (q.t0 + (long long)t) * d.ld_b : (const IT*)a.Cm + (q.t0 + (long long)t) * d.ld_c;
+          rb[i] = load_raw4(p + (long long)grp * N + n, t < q.len ? 4 : 0, vec_bc);
+        }
       }
-      if (live) ph = *reinterpret_cast<const float4*>(a.h_saved + ((q.tile0 + tile) * d.D + dch) * N + 4 * ln);
     };
-    if (tiles > 0) fetch(tiles - 1);
-    for (int tile = tiles - 1; tile >= 0; --tile) {
-      const int base = tile * kTile;
-      __syncthreads();  // the previous tile's readers are done
+    auto form = [&](int k) {
+      const int base = (tiles - 1 - k) * kTile, buf = k & 1;
+      const bool full = whole(k);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = i * NT + tid, t = e / CB, c = e % CB;
-        const bool in = base + t < q.len && c < nch;
-        float raw = to_f32(pd[i]), dl = 0.f, sig = 0.f;
-        if (in) {
-          if (a.dt_bias) raw += a.dt_bias[dc0 + c];
-          dl = raw;
-          sig = 1.f;
-          if (d.softplus) dl = softplus_f(raw, &sig);
+      for (int i = 0; i < QP; ++i) {
+        const int tt = qt + i * (NT / Q);
+        if (qt < kTile) {
+          float xv[4], dv[4], yv[4], sg[4] = {1.f, 1.f, 1.f, 1.f};
+          rx[i].get(xv);
+          rd[i].get(dv);
+          ry[i].get(yv);
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            f32x2 dl = add2(pack2(dv[c], dv[c + 1]), pack2(bias[c], bias[c + 1]));
+            if (d.softplus) dl = softplus2(lo2(dl), hi2(dl), &sg[c], &sg[c + 1]);
+            if (!full) {  // past the end nothing moves
+              const int n = base + tt < q.len ? qn : 0;
+              dl = pack2(c < n ? lo2(dl) : 0.f, c + 1 < n ? hi2(dl) : 0.f);
+              if (c >= n) sg[c] = 0.f;
+              if (c + 1 >= n) sg[c + 1] = 0.f;
+            }
+            sm.du[buf][tt][(qc + c) / 2] = Pair2{dl, mul2(dl, pack2(xv[c], xv[c + 1]))};
+          }
+          *reinterpret_cast<float4*>(&sm.dy[buf][tt][qc / 2]) = make_float4(yv[0], yv[1], yv[2], yv[3]);
+          *reinterpret_cast<float4*>(&sm.x[buf][tt][qc]) = make_float4(xv[0], xv[1], xv[2], xv[3]);
+          *reinterpret_cast<float4*>(&sm.sig[buf][tt][qc]) = make_float4(sg[0], sg[1], sg[2], sg[3]);
         }
-        sd[t][c] = dl;
-        sg[t][c] = sig;
-        sx[t][c] = to_f32(px[i]);
-        sy[t][c] = to_f32(py[i]);
       }
 #pragma unroll
-      for (int i = 0; i < PB; ++i) {
-        const int e = i * NT + tid;
-        if (e < kTile * N) {
-          sB[e / N][e % N] = to_f32(pB[i]);
-          sC[e / N][e % N] = to_f32(pC[i]);
+      for (int i = 0; i < BQ; ++i) {
+        const int e = i * NT + tid, w = e % (4 * N), t = w / (N / 4), n = 4 * (w % (N / 4));
+        if (e < 8 * N) {
+          float v[4];
+          rb[i].get(v);
+          f32x2* o = e < 4 * N ? &sm.B[buf][t][n] : &sm.C[buf][t][n];
+          reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[0], v[1], v[1]);
+          reinterpret_cast<float4*>(o)[1] = make_float4(v[2], v[2], v[3], v[3]);
         }
       }
-      float h[kTile + 1][4];  // h[t]: the state in front of token t
-      h[0][0] = ph.x; h[0][1] = ph.y; h[0][2] = ph.z; h[0][3] = ph.w;
+    };
+    // what leaves from step k: dx, ddt of this thread's quads, dB and dC of the block
+    auto finish = [&](int k) {
+      const int base = (tiles - 1 - k) * kTile, buf = k & 1;
+#pragma unroll
+      for (int i = 0; i < QP; ++i) {
+        const int tt = qt + i * (NT / Q), t = base + tt;
+        if (qt < kTile && t < q.len) {
+          const float4 s1 = *reinterpret_cast<const float4*>(&sm.s[buf][0][tt * Smem::SR + qc]);
+          const float4 s2 = *reinterpret_cast<const float4*>(&sm.s[buf][1][tt * Smem::SR + qc]);
+          const float4 x4 = *reinterpret_cast<const float4*>(&sm.x[buf][tt][qc]);
+          const float4 g4 = *reinterpret_cast<const float4*>(&sm.sig[buf][tt][qc]);
+          const float4 y4 = *reinterpret_cast<const float4*>(&sm.dy[buf][tt][qc / 2]);
+          const f32x2 d0 = sm.du[buf][tt][qc / 2].a, d1 = sm.du[buf][tt][qc / 2 + 1].a;
+          const float s1v[4] = {s1.x, s1.y, s1.z, s1.w}, s2v[4] = {s2.x, s2.y, s2.z, s2.w};
+          const float xv[4] = {x4.x, x4.y, x4.z, x4.w}, gv[4] = {g4.x, g4.y, g4.z, g4.w}, yv[4] = {y4.x, y4.y, y4.z, y4.w};
+          const float dl[4] = {lo2(d0), hi2(d0), lo2(d1), hi2(d1)};
+          float ox[4], og[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            ox[c] = fmaf(s1v[c], dl[c], skip[c] * yv[c]);
+            og[c] = fmaf(s1v[c], xv[c], s2v[c]) * gv[c];
+            dDs[c] = fmaf(yv[c], xv[c], dDs[c]);
+            dbias[c] += og[c];
+          }
+          const long long at = (long long)(q.t0 + t) * d.D + dc0 + qc;
+          store4((IT*)a.dx + at, qn, vec, ox);
+          store4((IT*)a.ddt + at, qn, vec, og);
+        }
+      }
+#pragma unroll 2
+      for (int e = tid; e < kTile * N / 2; e += NT) {  // four sums each
+        const int t = e / (N / 2), v = 4 * (e % (N / 2));
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float4 r = *reinterpret_cast<const float4*>(&sm.red[buf][w][t][v]);
+          s.x += r.x; s.y += r.y; s.z += r.z; s.w += r.w;
+        }
+        if (base + t < q.len)
+          *reinterpret_cast<float4*>(a.bc + (((long long)blk * d.total + q.t0 + base + t) * d.G + grp) * 2 * N + v) = s;
+      }
+    };
+    if (tiles > 0) {
+      load_pair(a.h_saved + (q.tile0 + tiles - 1) * d.D * N, ph);
+      fetch(0);
+      form(0);
+      if (tiles > 1) fetch(1);
+    }
+    for (int k = 0; k < tiles; ++k) {
+      const int buf = k & 1;
       __syncthreads();
-      if (tile > 0) fetch(tile - 1);
+      if (k > 0) finish(k - 1);  // before form overwrites this thread's own entries of that tile
+      if (k + 1 < tiles) form(k + 1);
+      if (k + 2 < tiles) fetch(k + 2);
+      f32x2 h[kTile + 1][2], e[kTile][2];  // h[t]: in front of token t
+      h[0][0] = ph[0];
+      h[0][1] = ph[1];
+      if (k + 1 < tiles) load_pair(a.h_saved + (q.tile0 + tiles - 2 - k) * d.D * N, ph);
 #pragma unroll
       for (int t = 0; t < kTile; ++t) {
-        const float dl = sd[t][ch], u = dl * sx[t][ch];
-        const float4 b = *reinterpret_cast<const float4*>(&sB[t][4 * ln]);
-        const float bb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[t + 1][j] = fmaf(ex2f(dl * A2[j]), h[t][j], u * bb[j]);
+        const Pair2 du = sm.du[buf][t][pr];
+        const Pair2 b = *reinterpret_cast<const Pair2*>(&sm.B[buf][t][2 * nl]);
+        e[t][0] = ex2_2(mul2(du.a, A2[0]));
+        e[t][1] = ex2_2(mul2(du.a, A2[1]));
+        h[t + 1][0] = fma2(e[t][0], h[t][0], mul2(du.b, b.a));
+        h[t + 1][1] = fma2(e[t][1], h[t][1], mul2(du.b, b.b));
       }
+      f32x2 dAt[2] = {0, 0};  // a tile's part first: the long sum then has 1/16 of the terms
 #pragma unroll
-      for (int t4 = kTile - 4; t4 >= 0; t4 -= 4) {
-        float s1[4], s2[4];  // sum_n dh B and sum_n l A of the four tokens
+      for (int t2 = kTile - 2; t2 >= 0; t2 -= 2) {
+        float s[8];  // {s1, s1', s2, s2'} of tokens t2, t2 + 1
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {
-          const int t = t4 + i;
-          const float dl = sd[t][ch], u = dl * sx[t][ch], dyv = sy[t][ch];
-          const float4 b = *reinterpret_cast<const float4*>(&sB[t][4 * ln]);
-          const float4 c = *reinterpret_cast<const float4*>(&sC[t][4 * ln]);
-          const float bb[4] = {b.x, b.y, b.z, b.w}, cc[4] = {c.x, c.y, c.z, c.w};
-          float w[8];  // this channel's part of dB_t and dC_t
-          s1[i] = s2[i] = 0.f;
+        for (int i = 1; i >= 0; --i) {
+          const int t = t2 + i;
+          const Pair2 du = sm.du[buf][t][pr];
+          const f32x2 dyv = sm.dy[buf][t][pr];
+          const Pair2 b = *reinterpret_cast<const Pair2*>(&sm.B[buf][t][2 * nl]);
+          const Pair2 c = *reinterpret_cast<const Pair2*>(&sm.C[buf][t][2 * nl]);
+          dh[0] = fma2(dyv, c.a, dh[0]);
+          dh[1] = fma2(dyv, c.b, dh[1]);
+          const f32x2 b0 = mul2(dh[0], du.b), b1 = mul2(dh[1], du.b);
+          const f32x2 c0v = mul2(dyv, h[t + 1][0]), c1v = mul2(dyv, h[t + 1][1]);
+          float w[4] = {lo2(b0) + hi2(b0), lo2(b1) + hi2(b1), lo2(c0v) + hi2(c0v), lo2(c1v) + hi2(c1v)};
+          using Chan = LaneSums<4, CL, ML>;  // over the warp's channel pairs
+          Chan::run(w, cl);
+          if (Chan::holds(cl)) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            dh[j] = fmaf(dyv, cc[j], dh[j]);
-            w[j] = dh[j] * u;
-            w[4 + j] = dyv * h[t + 1][j];
-            s1[i] = fmaf(dh[j], bb[j], s1[i]);
-            dh[j] *= ex2f(dl * A2[j]);
-            const float l = dh[j] * h[t][j];
-            s2[i] = fmaf(l, A1[j], s2[i]);
-            dA[j] = fmaf(l, dl, dA[j]);
-          }
-          // over the warp's channels: value index bits 2, 1, 0 go to channel bits 0, 1, 2
-#pragma unroll
-          for (int bit = 0; (1 << bit) < CL; ++bit) {
-            const int off = NL << bit, m = bit == 0 ? 4 : bit == 1 ? 2 : bit == 2 ? 1 : 0;
-            if (m > 0) {
-              const bool hi = cl & (1 << bit);
-#pragma unroll
-              for (int v = 0; v < m; ++v) {
-                const float send = hi ? w[v] : w[v + m], keep = hi ? w[v + m] : w[v];
-                w[v] = keep + __shfl_xor_sync(0xffffffffu, send, off);
-              }
-            } else {
-              w[0] += __shfl_xor_sync(0xffffffffu, w[0], off);
+            for (int v = 0; v < Chan::KEEP; ++v) {
+              const int vi = Chan::index(cl) + v;  // 0, 1: dB of states 2 nl, 2 nl + 1; 2, 3: dC
+              sm.red[buf][warp][t][(vi >> 1) * N + 2 * nl + (vi & 1)] = w[v];
             }
           }
-          constexpr int KEEP = CL >= 8 ? 1 : 8 / CL;
-          const int first = CL >= 8 ? (cl & 1) * 4 + ((cl >> 1) & 1) * 2 + ((cl >> 2) & 1)
-                                    : CL == 4 ? (cl & 1) * 4 + ((cl >> 1) & 1) * 2 : CL == 2 ? (cl & 1) * 4 : 0;
-          if (cl < 8)
-#pragma unroll
-            for (int v = 0; v < KEEP; ++v) {
-              const int vi = first + v;  // dB of state 4 ln + vi, or dC of state 4 ln + vi - 4
-              red[(warp * kTile + t) * 2 * N + (vi < 4 ? 0 : N) + 4 * ln + (vi & 3)] = w[v];
-            }
+          const f32x2 s1 = fma2(dh[0], b.a, mul2(dh[1], b.b));
+          dh[0] = mul2(dh[0], e[t][0]);
+          dh[1] = mul2(dh[1], e[t][1]);
+          const f32x2 l0 = mul2(dh[0], h[t][0]), l1 = mul2(dh[1], h[t][1]);
+          const f32x2 s2 = fma2(l0, A1[0], mul2(l1, A1[1]));
+          dAt[0] = fma2(l0, du.a, dAt[0]);
+          dAt[1] = fma2(l1, du.a, dAt[1]);
+          s[4 * i] = lo2(s1);
+          s[4 * i + 1] = hi2(s1);
+          s[4 * i + 2] = lo2(s2);
+          s[4 * i + 3] = hi2(s2);
         }
-        LaneSum<NL>::run(s1, ln);
-        LaneSum<NL>::run(s2, ln);
-        if (LaneSum<NL>::holds(ln)) {
+        using Chan = LaneSums<8, ML, 1>;  // over the states
+        Chan::run(s, nl);
+        if (Chan::holds(nl)) {
 #pragma unroll
-          for (int k = 0; k < LaneSum<NL>::kKeep; ++k) {
-            const int t = t4 + LaneSum<NL>::tok(ln) + k;
-            const float xv = sx[t][ch], dyv = sy[t][ch], g = fmaf(s1[k], xv, s2[k]) * sg[t][ch];
-            dDs = fmaf(dyv, xv, dDs);
-            dbias += g;
-            sy[t][ch] = fmaf(s1[k], sd[t][ch], skip * dyv);
-            sx[t][ch] = g;
+          for (int v = 0; v < Chan::KEEP; ++v) {
+            const int vi = Chan::index(nl) + v;
+            sm.s[buf][(vi >> 1) & 1][(t2 + (vi >> 2)) * Smem::SR + 2 * pr + (vi & 1)] = s[v];
           }
         }
       }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int e = i * NT + tid, t = e / CB, c = e % CB;
-        if (base + t < q.len && c < nch) {
-          const long long at = (long long)(q.t0 + base + t) * d.D + dc0 + c;
-          ((IT*)a.dx)[at] = from_f32<IT>(sy[t][c]);
-          ((IT*)a.ddt)[at] = from_f32<IT>(sx[t][c]);
-        }
-      }
-      for (int e = tid; e < kTile * 2 * N; e += NT) {
-        const int t = e / (2 * N), v = e % (2 * N);
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w) s += red[w * kTile * 2 * N + e];
-        if (base + t < q.len)
-          a.bc[(((long long)blk * d.total + q.t0 + base + t) * d.G + grp) * 2 * N + v] = s;
-      }
+      dA[0] = add2(dA[0], dAt[0]);
+      dA[1] = add2(dA[1], dAt[1]);
     }
-    if (a.dS0 && q.first && live)
-      *reinterpret_cast<float4*>(a.dS0 + ((long long)q.seq * d.D + dch) * N + 4 * ln) = make_float4(dh[0], dh[1], dh[2], dh[3]);
+    __syncthreads();
+    if (tiles > 0) finish(tiles - 1);
+    if (a.dS0 && q.first) {
+      float* o = a.dS0 + ((long long)q.seq * d.D + dch) * N + 2 * nl;
+      if (live0) *reinterpret_cast<float2*>(o) = make_float2(lo2(dh[0]), lo2(dh[1]));
+      if (live1) *reinterpret_cast<float2*>(o + N) = make_float2(hi2(dh[0]), hi2(dh[1]));
+    }
+    __syncthreads();  // the next unit's first tile overwrites what finish read
   }
   // this row's sums over tokens: [N][D] of dA, [D] of dDskip, [D] of ddt_bias
   float* out = a.grads + (long long)blockIdx.y * (N + 2) * d.D;
 #pragma unroll
-  for (int o = 1; o < NL; o <<= 1) {
-    dDs += __shfl_xor_sync(0xffffffffu, dDs, o);
-    dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
+  for (int j = 0; j < 2; ++j) {
+    if (live0) out[(long long)(2 * nl + j) * d.D + dch] = lo2(dA[j]);
+    if (live1) out[(long long)(2 * nl + j) * d.D + dch + 1] = hi2(dA[j]);
   }
-  if (live) {
+  // dDskip, ddt_bias: over the threads that held the same channels
+  __syncthreads();
+  float* cols = reinterpret_cast<float*>(smem_raw);  // [NT][8]
 #pragma unroll
-    for (int j = 0; j < 4; ++j) out[(long long)(4 * ln + j) * d.D + dch] = dA[j];
-    if (ln == 0) {
-      out[(long long)N * d.D + dch] = dDs;
-      out[(long long)(N + 1) * d.D + dch] = dbias;
-    }
+  for (int i = 0; i < 4; ++i) {
+    cols[tid * 8 + i] = dDs[i];
+    cols[tid * 8 + 4 + i] = dbias[i];
+  }
+  __syncthreads();
+  for (int c = tid; c < 2 * CB; c += NT) {
+    const int m = c / CB, cc = c - m * CB;
+    float s = 0.f;
+    for (int r = 0; r < NT / Q; ++r) s += cols[(r * Q + cc / 4) * 8 + 4 * m + (cc & 3)];
+    if (cc < nch) out[(long long)(N + m) * d.D + dc0 + cc] = s;
   }
 }
 
@@ -246,14 +334,15 @@ __global__ void __launch_bounds__(256) ssm_bc_kernel(SsmDims d, const float* __r
     dC[tg * d.N + v - d.N] = from_f32<IT>(s);
 }
 
-size_t bwd_smem(int NL) {
-  const int NT = bwd_threads(NL), CB = NT / NL, N = 4 * NL;
-  return sizeof(float) * (size_t)(4 * kTile * CB + 2 * kTile * N + NT / 32 * kTile * 2 * N);
+// Calls f(N).
+template <typename F>
+cudaError_t ssm_states(int N, F f) {
+  return ssm_lanes(N, [&](auto nl) { return f(std::integral_constant<int, 4 * decltype(nl)::value>{}); });
 }
 
 }  // namespace
 
-int ssm_bwd_channels(int N) { return bwd_threads(N / 4) / (N / 4); }
+int ssm_bwd_channels(int N) { return 2 * bwd_threads(N) / (N / 2); }
 
 int ssm_bwd_rows(const SsmDims& d) {
   const int cb = ssm_bwd_channels(d.N);
@@ -293,6 +382,7 @@ gdr_status gdr_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt, 
     return GDR_ERR_ALIGNMENT;
   const SsmWorkspace w = ssm_workspace(d, (char*)workspace, true);
   if (!workspace || workspace_bytes < w.bytes) return GDR_ERR_WORKSPACE;
+  d.vec = ssm_vec(d, el, {x, dt, dy, dx, ddt}, {Bm, Cm});
   cudaStream_t s = (cudaStream_t)stream;
   stage_begin(s);
   cudaError_t e = ssm_launch_index(&d, w, s);
@@ -308,12 +398,12 @@ gdr_status gdr_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt, 
                      dx, ddt, dS0, w.grads, w.bc};
   auto run = [&](auto it) {
     using IT = decltype(it);
-    cudaError_t r = ssm_lanes(d.N, [&](auto nl) {
-      constexpr int NL = decltype(nl)::value;
-      const size_t smem = bwd_smem(NL);
-      const cudaError_t se = set_smem_once((const void*)ssm_bwd_kernel<IT, NL>, smem);
+    cudaError_t r = ssm_states(d.N, [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      const size_t smem = sizeof(BwdSmem<N>);
+      const cudaError_t se = set_smem_once((const void*)ssm_bwd_kernel<IT, N>, smem);
       if (se != cudaSuccess) return se;
-      ssm_bwd_kernel<IT, NL><<<dim3((unsigned)(d.G * blocks), (unsigned)rows), bwd_threads(NL), smem, s>>>(d, a);
+      ssm_bwd_kernel<IT, N><<<dim3((unsigned)(d.G * blocks), (unsigned)rows), bwd_threads(N), smem, s>>>(d, a);
       stage_mark(s, "ssm_bwd");
       return cudaGetLastError();
     });
