@@ -10,8 +10,8 @@ namespace gdr {
 
 constexpr int kSmCount = 152;  // SMs of a GB300: grids are sized against it
 
-// V elements of one row in fp32: 16-byte accesses for V = 8 (one of bf16, two of fp32), scalar
-// for V = 1.  p is 16-byte aligned for V = 8.
+// V elements of one row in fp32: vector accesses for V = 4 and 8, scalar for V = 1.  p is aligned to
+// the access (at most 16 bytes).
 template <int V>
 __device__ __forceinline__ void load_v(const float* p, float (&v)[V]) {
   if constexpr (V == 1) {
@@ -28,6 +28,10 @@ template <int V>
 __device__ __forceinline__ void load_v(const __nv_bfloat16* p, float (&v)[V]) {
   if constexpr (V == 1) {
     v[0] = __bfloat162float(p[0]);
+  } else if constexpr (V == 4) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
+    v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
   } else {
 #pragma unroll
     for (int i = 0; i < V; i += 8) {
@@ -54,6 +58,9 @@ template <int V>
 __device__ __forceinline__ void store_v(__nv_bfloat16* p, const float (&v)[V]) {
   if constexpr (V == 1) {
     p[0] = __float2bfloat16_rn(v[0]);
+  } else if constexpr (V == 4) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   } else {
 #pragma unroll
     for (int i = 0; i < V; i += 8) {
@@ -102,6 +109,38 @@ __device__ __forceinline__ float softplus_f(float x, float* sig) {
     *sig = x >= 0.f ? r : u * r;
   }
   return fmaf(2.f * s, p, fmaxf(x, 0.f));
+}
+
+// Two fp32 values in a register pair, for the packed fp32 instructions.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float lo2(f32x2 v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(f32x2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 ex2_2(f32x2 v) { return pack2(ex2f(lo2(v)), ex2f(hi2(v))); }
+
+// Sigmoids of a pair.
+__device__ __forceinline__ f32x2 sigmoid2(f32x2 v) {
+  const f32x2 d = add2(ex2_2(mul2(v, pack2(-kLog2e, -kLog2e))), pack2(1.f, 1.f));
+  return pack2(rcpf(lo2(d)), rcpf(hi2(d)));
 }
 
 // The sequence of packed token t (cu valid, t < cu[num_seqs]): the last n with cu[n] <= t.

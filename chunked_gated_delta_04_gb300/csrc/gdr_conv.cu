@@ -8,7 +8,7 @@
 //   dw[j] = sum_t dpre[t] X[t - (W - 1) + j],   dbias = sum_t dpre[t].
 //
 // Both are bound by memory: 2 W multiply-adds per element against 4 (forward) or 6 (backward)
-// bytes in bf16.  A thread owns V channels (16 bytes) and walks a run of tokens with the last
+// bytes in bf16.  A thread owns V channels and walks a run of tokens with the last
 // W - 1 inputs (and, backward, the last W - 1 dpre) in registers, so each element is read once but
 // for the W - 1 rows in front of (backward: also behind) a run, which its neighbour's reads have
 // brought into the L2.
@@ -18,6 +18,9 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBwdVec = 4;
+constexpr int kFwdVec = 4;  // channels per thread of the vector paths
+constexpr int kFwdBlocks = 3;  // blocks per SM of the forward
 
 struct ConvDims {
   int T, C, num_seqs, silu;
@@ -55,56 +58,132 @@ struct SeqWalk {
   }
 };
 
+// V channels of a row as P register pairs (V = 1: the upper half of the pair is idle).
+template <int V>
+constexpr int kPairs = (V + 1) / 2;
+
 template <int V, int W>
-__device__ __forceinline__ void load_taps(const float* w, const float* bias, long long c, float (&wt)[W][V],
-                                          float (&b)[V]) {
+__device__ __forceinline__ void load_taps(const float* w, const float* bias, long long c, f32x2 (&wt)[W][kPairs<V>],
+                                          f32x2 (&b)[kPairs<V>]) {
+  float t[W][kPairs<V> * 2] = {}, bs[kPairs<V> * 2] = {};
   if constexpr (V > 1 && W == 4) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const float4 x = *reinterpret_cast<const float4*>(w + (c + i) * 4);
-      wt[0][i] = x.x; wt[1][i] = x.y; wt[2][i] = x.z; wt[3][i] = x.w;
+      t[0][i] = x.x; t[1][i] = x.y; t[2][i] = x.z; t[3][i] = x.w;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int j = 0; j < W; ++j) wt[j][i] = w[(c + i) * W + j];
+      for (int j = 0; j < W; ++j) t[j][i] = w[(c + i) * W + j];
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) b[i] = bias ? bias[c + i] : 0.f;
+  for (int i = 0; i < V; ++i) bs[i] = bias ? bias[c + i] : 0.f;
+#pragma unroll
+  for (int i = 0; i < kPairs<V>; ++i) {
+    b[i] = pack2(bs[2 * i], bs[2 * i + 1]);
+#pragma unroll
+    for (int j = 0; j < W; ++j) wt[j][i] = pack2(t[j][2 * i], t[j][2 * i + 1]);
+  }
+}
+
+// V neighbouring elements as they come from memory, converted where they are used, so that a load is
+// not waited for before that.
+template <typename IT, int V>
+struct Raw {
+  uint32_t w[V * sizeof(IT) / 4];
+  __device__ __forceinline__ void load(const IT* p) {
+    if constexpr (sizeof(w) == 8) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x; w[1] = x.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < (int)(sizeof(w) / 4); i += 4) {
+        const uint4 x = reinterpret_cast<const uint4*>(p)[i / 4];
+        w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void get(f32x2 (&v)[kPairs<V>]) const {
+#pragma unroll
+    for (int i = 0; i < kPairs<V>; ++i) {
+      if constexpr (sizeof(IT) == 4)
+        v[i] = pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+      else
+        v[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+  }
+};
+template <typename IT>
+struct Raw<IT, 1> {
+  IT w;
+  __device__ __forceinline__ void load(const IT* p) { w = *p; }
+  __device__ __forceinline__ void get(f32x2 (&v)[1]) const { v[0] = pack2(to_f32(w), 0.f); }
+};
+template <int V, typename IT>
+__device__ __forceinline__ void store_row(IT* p, const f32x2 (&v)[kPairs<V>]) {
+  float f[kPairs<V> * 2];
+#pragma unroll
+  for (int i = 0; i < kPairs<V>; ++i) {
+    f[2 * i] = lo2(v[i]);
+    f[2 * i + 1] = hi2(v[i]);
+  }
+  store_v<V>(p, *reinterpret_cast<const float(*)[V]>(&f));
 }
 
 // Row p (p < s1) of X: a token, or, before s0, a row of the state.
 template <typename IT, int V, int W>
 __device__ __forceinline__ void load_row(const ConvDims& d, const SeqWalk& q, const IT* x, const IT* state,
-                                         long long p, long long c, float (&v)[V]) {
+                                         long long p, long long c, f32x2 (&v)[kPairs<V>]) {
+  Raw<IT, V> r;
   if (p >= q.s0) {
-    load_v<V>(x + p * d.ld_x + c, v);
+    r.load(x + p * d.ld_x + c);
+    r.get(v);
   } else if (state) {
-    load_v<V>(state + ((long long)q.n * (W - 1) + (p - q.s0 + W - 1)) * d.C + c, v);
+    r.load(state + ((long long)q.n * (W - 1) + (p - q.s0 + W - 1)) * d.C + c);
+    r.get(v);
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 0.f;
+    for (int i = 0; i < kPairs<V>; ++i) v[i] = 0;
   }
 }
 
 template <int V, int W>
-__device__ __forceinline__ void taps(const float (&win)[W][V], const float (&wt)[W][V], const float (&b)[V],
-                                     float (&pre)[V]) {
+__device__ __forceinline__ void taps(const f32x2 (&win)[W][kPairs<V>], const f32x2 (&wt)[W][kPairs<V>],
+                                     const f32x2 (&b)[kPairs<V>], f32x2 (&pre)[kPairs<V>]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) pre[i] = b[i];
+  for (int i = 0; i < kPairs<V>; ++i) pre[i] = b[i];
 #pragma unroll
   for (int j = 0; j < W; ++j)
 #pragma unroll
-    for (int i = 0; i < V; ++i) pre[i] = fmaf(wt[j][i], win[j][i], pre[i]);
+    for (int i = 0; i < kPairs<V>; ++i) pre[i] = fma2(wt[j][i], win[j][i], pre[i]);
+}
+template <int V>
+__device__ __forceinline__ void silu_row(f32x2 (&v)[kPairs<V>]) {
+#pragma unroll
+  for (int i = 0; i < kPairs<V>; ++i) v[i] = mul2(v[i], sigmoid2(v[i]));
+}
+// The window moves on by one row.
+template <int V, int W>
+__device__ __forceinline__ void push(f32x2 (&ring)[W][kPairs<V>], const f32x2 (&v)[kPairs<V>]) {
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+    for (int i = 0; i < kPairs<V>; ++i) ring[j][i] = ring[j + 1][i];
+#pragma unroll
+  for (int i = 0; i < kPairs<V>; ++i) ring[W - 1][i] = v[i];
 }
 
+// B = 2, T = 4096, C = 6144, bf16, W = 4, from a cold L2: 46 us, 201 MB, 4.4 TB/s.  8 channels a
+// thread with two blocks per SM: 48 us; runs of 32 tokens (2.5 waves) instead of one wave's: 52 us.
 template <typename IT, int V, int W>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvDims d, const IT* __restrict__ x,
-                                                            const float* __restrict__ w,
-                                                            const float* __restrict__ bias,
-                                                            const IT* __restrict__ state, IT* __restrict__ y,
-                                                            IT* __restrict__ last, int L) {
+__global__ void __launch_bounds__(kThreads, kFwdBlocks) conv_fwd_kernel(ConvDims d, const IT* __restrict__ x,
+                                                               const float* __restrict__ w,
+                                                               const float* __restrict__ bias,
+                                                               const IT* __restrict__ state, IT* __restrict__ y,
+                                                               IT* __restrict__ last, int L) {
+  constexpr int P = kPairs<V>, kDeep = 4;
   if (d.status && *d.status) return;
   const int ncg = d.C / V;
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
@@ -114,153 +193,169 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(ConvDims d, const IT
   if (run >= runs) {  // the state after the last token: one thread per sequence and V channels
     if (last == nullptr || run - runs >= d.num_seqs) return;
     q.of(d, (int)(run - runs));
-    float v[V];
+    f32x2 v[P];
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
       load_row<IT, V, W>(d, q, x, state, q.s1 - (W - 1) + j, c, v);
-      store_v<V>(last + ((long long)q.n * (W - 1) + j) * d.C + c, v);
+      store_row<V>(last + ((long long)q.n * (W - 1) + j) * d.C + c, v);
     }
     return;
   }
   const long long t0 = run * L, t1 = min(t0 + L, d.total);
-  float wt[W][V], b[V], win[W][V], pre[V];
+  f32x2 wt[W][P], b[P], win[W][P];
   load_taps<V, W>(w, bias, c, wt, b);
   q.find(d, t0);
-  for (long long t = t0; t < t1;) {
-    const long long end = min(t1, q.s1);
+  for (long long a = t0; a < t1;) {
+    const int n = (int)(min(t1, q.s1) - a);  // this run's tokens of the sequence
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) load_row<IT, V, W>(d, q, x, state, t - (W - 1) + j, c, win[j + 1]);
-    auto one = [&](long long p, const float (&in)[V]) {
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) win[j][i] = win[j + 1][i];
-#pragma unroll
-      for (int i = 0; i < V; ++i) win[W - 1][i] = in[i];
+    for (int j = 0; j < W - 1; ++j) load_row<IT, V, W>(d, q, x, state, a - (W - 1) + j, c, win[j + 1]);
+    const IT* xp = x + a * d.ld_x + c;
+    IT* yp = y + a * d.C + c;
+    auto one = [&](const f32x2(&in)[P]) {
+      f32x2 pre[P];
+      push<V, W>(win, in);
       taps<V, W>(win, wt, b, pre);
-      if (d.silu) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) pre[i] *= sigmoid_f(pre[i]);
-      }
-      store_v<V>(y + p * d.C + c, pre);
+      if (d.silu) silu_row<V>(pre);
+      store_row<V>(yp, pre);
+      yp += d.C;
     };
-    for (; t + 4 <= end; t += 4) {  // four rows in flight
-      float in[4][V];
+    // kDeep rows in flight: once a row has been converted its registers take the load of the row kDeep
+    // further on.  Whole groups run without conditions on the windows, whose moves then are renamings.
+    Raw<IT, V> r[kDeep];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) load_v<V>(x + (t + u) * d.ld_x + c, in[u]);
+    for (int u = 0; u < kDeep; ++u) {
+      if (u < n) r[u].load(xp);
+      xp += d.ld_x;
+    }
+    int t = 0;
+    for (; t + kDeep <= n; t += kDeep) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) one(t + u, in[u]);
+      for (int u = 0; u < kDeep; ++u) {
+        f32x2 in[P];
+        r[u].get(in);
+        if (t + u + kDeep < n) r[u].load(xp);
+        xp += d.ld_x;
+        one(in);
+      }
     }
-    for (; t < end; ++t) {
-      float in[V];
-      load_v<V>(x + t * d.ld_x + c, in);
-      one(t, in);
+#pragma unroll
+    for (int u = 0; u < kDeep - 1; ++u) {
+      if (t + u < n) {
+        f32x2 in[P];
+        r[u].get(in);
+        one(in);
+      }
     }
-    if (t < t1) q.next(d);
+    a += n;
+    if (a < t1) q.next(d);
   }
 }
 
-// dpre of token t from its window and dy.
+// dpre of a row from its window and dy: dy silu'(pre), silu'(p) = s + p s (1 - s).
 template <int V, int W>
-__device__ __forceinline__ void grad_pre(const float (&win)[W][V], const float (&wt)[W][V], const float (&b)[V],
-                                         int silu, float (&g)[V]) {
+__device__ __forceinline__ void grad_pre(const f32x2 (&win)[W][kPairs<V>], const f32x2 (&wt)[W][kPairs<V>],
+                                         const f32x2 (&b)[kPairs<V>], int silu, f32x2 (&g)[kPairs<V>]) {
   if (silu) {
-    float pre[V];
+    f32x2 pre[kPairs<V>];
     taps<V, W>(win, wt, b, pre);
+    const f32x2 one = pack2(1.f, 1.f), minus = pack2(-1.f, -1.f);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float s = sigmoid_f(pre[i]);
-      g[i] *= s * fmaf(pre[i], 1.f - s, 1.f);
+    for (int i = 0; i < kPairs<V>; ++i) {
+      const f32x2 s = sigmoid2(pre[i]);
+      g[i] = mul2(mul2(g[i], s), fma2(pre[i], fma2(s, minus, one), one));
     }
   }
 }
 
+// B = 2, T = 4096, C = 6144, bf16, W = 4, from a cold L2: 86 us, 302 MB, 3.5 TB/s (16 warps per SM; 30
+// instructions per element).  With a condition on every row's window moves, so that they are real
+// moves: 120 us.
+//
 // Blocks of kThreads / cpb runs of L tokens by cpb groups of V channels; a block's sums of dw and
 // dbias go to partial[blockIdx.x][W + 1][C].  blockIdx.x >= tiles: dstate, one sequence per run.
 template <typename IT, int V, int W>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvDims d, const IT* __restrict__ x,
-                                                            const float* __restrict__ w,
-                                                            const float* __restrict__ bias,
-                                                            const IT* __restrict__ state,
-                                                            const IT* __restrict__ dy,
-                                                            const IT* __restrict__ dlast, IT* __restrict__ dx,
-                                                            IT* __restrict__ dstate, float* __restrict__ partial,
-                                                            int L, int cpb, int tiles) {
+__global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvDims d, const IT* __restrict__ x,
+                                                               const float* __restrict__ w,
+                                                               const float* __restrict__ bias,
+                                                               const IT* __restrict__ state,
+                                                               const IT* __restrict__ dy,
+                                                               const IT* __restrict__ dlast, IT* __restrict__ dx,
+                                                               IT* __restrict__ dstate, float* __restrict__ partial,
+                                                               int L, int cpb, int tiles) {
+  constexpr int P = kPairs<V>;
   __shared__ float red[kThreads * V];
   if (d.status && *d.status) return;
   const int subs = kThreads / cpb, sub = threadIdx.x / cpb, cg = threadIdx.x - sub * cpb;
   const long long c = ((long long)blockIdx.y * cpb + cg) * V;
   const bool live = c < d.C;
   SeqWalk q;
-  float wt[W][V], b[V], win[W][V], dwin[W][V], g[V];
-  float acc[W + 1][V];
+  f32x2 wt[W][P], b[P], win[W][P], dwin[W][P];  // win: the last W inputs; dwin: the last W dpre
+  f32x2 acc[W + 1][P];
 #pragma unroll
   for (int j = 0; j <= W; ++j)
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
+    for (int i = 0; i < P; ++i) acc[j][i] = 0;
   if (live) load_taps<V, W>(w, bias, c, wt, b);
+  const f32x2 zero[P] = {};
 
-  // dX of row p of sequence q from the dpre of rows p .. p + W - 1 (dwin[j] = dpre[p + j])
-  auto row_grad = [&](long long p, float (&out)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) out[i] = fmaf(wt[W - 1 - j][i], dwin[j][i], out[i]);
-    const long long k = p - (q.s1 - (W - 1));
-    if (dlast && k >= 0) {
-      float v[V];
-      load_v<V>(dlast + ((long long)q.n * (W - 1) + k) * d.C + c, v);
-#pragma unroll
-      for (int i = 0; i < V; ++i) out[i] += v[i];
-    }
-  };
-  auto push = [&](float (&ring)[W][V], const float (&v)[V]) {
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) ring[j][i] = ring[j + 1][i];
-#pragma unroll
-    for (int i = 0; i < V; ++i) ring[W - 1][i] = v[i];
-  };
-  // dpre of row u of sequence q, both windows moved on to it
-  auto advance = [&](long long u, const float (&in)[V], float (&dyv)[V]) {
-    push(win, in);
-#pragma unroll
-    for (int i = 0; i < V; ++i) g[i] = dyv[i];
-    grad_pre<V, W>(win, wt, b, d.silu, g);
-    push(dwin, g);
-  };
-  auto open = [&](long long u) {  // windows in front of row u; dpre before it counts as zero
+  // windows in front of row u; dpre before it counts as zero
+  auto open = [&](long long u) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) load_row<IT, V, W>(d, q, x, state, u - (W - 1) + j, c, win[j + 1]);
 #pragma unroll
     for (int j = 0; j < W; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) dwin[j][i] = 0.f;
+      for (int i = 0; i < P; ++i) dwin[j][i] = 0;
   };
-  const float zero[V] = {};
+  // dX of row p from the dpre of rows p .. p + W - 1 (dwin[j] = dpre[p + j])
+  auto row_grad = [&](long long p, f32x2 (&out)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) out[i] = mul2(wt[W - 1][i], dwin[0][i]);
+#pragma unroll
+    for (int j = 1; j < W; ++j)
+#pragma unroll
+      for (int i = 0; i < P; ++i) out[i] = fma2(wt[W - 1 - j][i], dwin[j][i], out[i]);
+    if (dlast) {
+      const long long k = p - (q.s1 - (W - 1));
+      if (k >= 0) {
+        f32x2 v[P];
+        Raw<IT, V> r;
+        r.load(dlast + ((long long)q.n * (W - 1) + k) * d.C + c);
+        r.get(v);
+#pragma unroll
+        for (int i = 0; i < P; ++i) out[i] = add2(out[i], v[i]);
+      }
+    }
+  };
+  // both windows move on to a row (g: its dy); its dpre is left in dwin[W - 1]
+  auto advance = [&](const f32x2(&in)[P], f32x2(&g)[P]) {
+    push<V, W>(win, in);
+    grad_pre<V, W>(win, wt, b, d.silu, g);
+    push<V, W>(dwin, g);
+  };
 
   if ((int)blockIdx.x >= tiles) {
     const long long n = (long long)(blockIdx.x - tiles) * subs + sub;
     if (!live || n >= d.num_seqs) return;
     q.of(d, (int)n);
     open(q.s0);
-    for (int k = 0; k < W - 1; ++k) {  // row u = s0 + k completes the window of row u - (W - 1)
+    for (int k = 0; k < W - 1; ++k) {  // row s0 + k completes the window of row s0 + k - (W - 1)
       const long long u = q.s0 + k;
       if (u < q.s1) {
-        float in[V], dyv[V];
-        load_v<V>(x + u * d.ld_x + c, in);
-        load_v<V>(dy + u * d.ld_dy + c, dyv);
-        advance(u, in, dyv);
+        Raw<IT, V> rx, rd;
+        f32x2 in[P], g[P];
+        rx.load(x + u * d.ld_x + c);
+        rd.load(dy + u * d.ld_dy + c);
+        rx.get(in);
+        rd.get(g);
+        advance(in, g);
       } else {
-        push(dwin, zero);
+        push<V, W>(dwin, zero);
       }
       // state row k is X row s0 - (W - 1) + k: dpre of rows s0 .. s0 + k reach it
-      float out[V];
+      f32x2 out[P];
       row_grad(u - (W - 1), out);
-      store_v<V>(dstate + (n * (W - 1) + k) * d.C + c, out);
+      store_row<V>(dstate + (n * (W - 1) + k) * d.C + c, out);
     }
     return;
   }
@@ -269,51 +364,72 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvDims d, const IT
   if (live && t0 < t1) {
     q.find(d, t0);
     for (long long a = t0; a < t1;) {
-      const long long end = min(t1, q.s1);          // rows [a, end) are this run's
-      const long long stop = min(q.s1, end + W - 1);  // dpre is needed up to here
+      const int n = (int)(min(t1, q.s1) - a);                    // this run's rows of the sequence
+      const int stop = (int)min((long long)n + W - 1, q.s1 - a);  // dpre is needed up to here
       open(a);
-      auto emit = [&](long long u) {  // row u's dpre is in: row u - (W - 1) is complete
-        const long long p = u - (W - 1);
-        if (p >= a && p < end) {
-          float out[V];
-          row_grad(p, out);
-          store_v<V>(dx + p * d.C + c, out);
+      const IT* xp = x + a * d.ld_x + c;
+      const IT* dp = dy + a * d.ld_dy + c;
+      IT* op = dx + a * d.C + c;
+      auto emit = [&](int u) {  // row u's dpre is in: row u - (W - 1) is complete
+        if (u >= W - 1) {
+          f32x2 out[P];
+          row_grad(a + u - (W - 1), out);
+          store_row<V>(op, out);
+          op += d.C;
         }
       };
-      auto one = [&](long long u, const float (&in)[V], float (&dyv)[V]) {
-        advance(u, in, dyv);
-        if (u < end) {
+      auto one = [&](int u, const f32x2(&in)[P], f32x2(&g)[P]) {
+        advance(in, g);
+        if (u < n) {
 #pragma unroll
           for (int j = 0; j < W; ++j)
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[j][i] = fmaf(g[i], win[j][i], acc[j][i]);
+            for (int i = 0; i < P; ++i) acc[j][i] = fma2(dwin[W - 1][i], win[j][i], acc[j][i]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) acc[W][i] += g[i];
+          for (int i = 0; i < P; ++i) acc[W][i] = add2(acc[W][i], dwin[W - 1][i]);
         }
         emit(u);
       };
-      long long u = a;
+      Raw<IT, V> rx[4], rd[4];  // four rows in flight, as in the forward
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k < stop) {
+          rx[k].load(xp);
+          rd[k].load(dp);
+        }
+        xp += d.ld_x;
+        dp += d.ld_dy;
+      }
+      int u = 0;
       for (; u + 4 <= stop; u += 4) {
-        float in[4][V], dyv[4][V];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          load_v<V>(x + (u + k) * d.ld_x + c, in[k]);
-          load_v<V>(dy + (u + k) * d.ld_dy + c, dyv[k]);
+          f32x2 in[P], g[P];
+          rx[k].get(in);
+          rd[k].get(g);
+          if (u + k + 4 < stop) {
+            rx[k].load(xp);
+            rd[k].load(dp);
+          }
+          xp += d.ld_x;
+          dp += d.ld_dy;
+          one(u + k, in, g);
         }
+      }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) one(u + k, in[k], dyv[k]);
+      for (int k = 0; k < 3; ++k) {
+        if (u + k < stop) {
+          f32x2 in[P], g[P];
+          rx[k].get(in);
+          rd[k].get(g);
+          one(u + k, in, g);
+        }
       }
-      for (; u < stop; ++u) {
-        float in[V], dyv[V];
-        load_v<V>(x + u * d.ld_x + c, in);
-        load_v<V>(dy + u * d.ld_dy + c, dyv);
-        one(u, in, dyv);
-      }
-      for (; u < end + W - 1; ++u) {  // past the sequence's end: no dpre
-        push(dwin, zero);
+      for (int u = stop; u < n + W - 1; ++u) {  // past the sequence's end: no dpre
+        push<V, W>(dwin, zero);
         emit(u);
       }
-      a = end;
+      a += n;
       if (a < t1) q.next(d);
     }
   }
@@ -321,14 +437,14 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(ConvDims d, const IT
   for (int j = 0; j <= W; ++j) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < V; ++i) red[(sub * V + i) * cpb + cg] = acc[j][i];
+    for (int i = 0; i < V; ++i) red[(sub * V + i) * cpb + cg] = i & 1 ? hi2(acc[j][i / 2]) : lo2(acc[j][i / 2]);
     __syncthreads();
     for (int k = threadIdx.x; k < cpb * V; k += kThreads) {
       const int i = k / cpb, kg = k - i * cpb;
-      float a = 0.f;
-      for (int r = 0; r < subs; ++r) a += red[(r * V + i) * cpb + kg];
+      float sum = 0.f;
+      for (int r = 0; r < subs; ++r) sum += red[(r * V + i) * cpb + kg];
       const long long cc = ((long long)blockIdx.y * cpb + kg) * V + i;
-      if (cc < d.C) partial[((long long)blockIdx.x * (W + 1) + j) * d.C + cc] = a;
+      if (cc < d.C) partial[((long long)blockIdx.x * (W + 1) + j) * d.C + cc] = sum;
     }
   }
 }
@@ -344,27 +460,26 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(int B, int C, long 
   if (b >= B) return;
   const long long c = (id - b * ncg) * V;
   const long long slot = slots ? slots[b] : b;
-  float pre[V];
+  constexpr int P = kPairs<V>;
+  f32x2 pre[P] = {};
   if (slot < 0 || slot >= num_slots) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) pre[i] = 0.f;
-    store_v<V>(y + b * C + c, pre);
+    store_row<V>(y + b * C + c, pre);
     return;
   }
   IT* st = pool + slot * (W - 1) * C + c;
-  float win[W][V], wt[W][V], bs[V];
+  Raw<IT, V> r[W];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) load_v<V>(st + (long long)j * C, win[j]);
-  load_v<V>(x + b * ld_x + c, win[W - 1]);
+  for (int j = 0; j < W - 1; ++j) r[j].load(st + (long long)j * C);
+  r[W - 1].load(x + b * ld_x + c);
+  f32x2 win[W][P], wt[W][P], bs[P];
   load_taps<V, W>(w, bias, c, wt, bs);
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) store_v<V>(st + (long long)j * C, win[j + 1]);
-  taps<V, W>(win, wt, bs, pre);
-  if (silu) {
+  for (int j = 0; j < W; ++j) r[j].get(win[j]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) pre[i] *= sigmoid_f(pre[i]);
-  }
-  store_v<V>(y + b * C + c, pre);
+  for (int j = 0; j < W - 1; ++j) store_row<V>(st + (long long)j * C, win[j + 1]);
+  taps<V, W>(win, wt, bs, pre);
+  if (silu) silu_row<V>(pre);
+  store_row<V>(y + b * C + c, pre);
 }
 
 gdr_status resolve_conv(const gdr_conv_problem* p, bool step, ConvDims* d) {
@@ -397,12 +512,16 @@ struct BwdShape {
 };
 BwdShape bwd_shape(const ConvDims& d) {
   BwdShape b;
-  const int ncg = (d.C + 7) / 8;
+  const int ncg = (d.C + kBwdVec - 1) / kBwdVec;
   b.cpb = ncg >= 32 ? 32 : ncg >= 16 ? 16 : 8;
-  const int subs = kThreads / b.cpb;
-  b.L = 32;
-  while (b.L > 4 && (d.total + b.L * subs - 1) / (b.L * subs) * ((ncg + b.cpb - 1) / b.cpb) < 2 * kSmCount) b.L /= 2;
-  b.tiles = (d.total + (long long)b.L * subs - 1) / ((long long)b.L * subs);
+  // whole waves of two blocks per SM, as in the forward; runs of 4 to 256 tokens (long runs also keep
+  // the partial rows few)
+  const long long subs = kThreads / b.cpb, gy = (ncg + b.cpb - 1) / b.cpb;
+  const long long per_wave = 2 * kSmCount > gy ? 2 * kSmCount / gy : 1;
+  const long long waves = (d.total + per_wave * subs * 256 - 1) / (per_wave * subs * 256), tiles = per_wave * waves;
+  const long long L = tiles > 0 ? (d.total + tiles * subs - 1) / (tiles * subs) : 4;
+  b.L = (int)(L < 4 ? 4 : L);
+  b.tiles = (d.total + b.L * subs - 1) / (b.L * subs);
   return b;
 }
 
@@ -410,16 +529,16 @@ size_t conv_bwd_bytes(const ConvDims& d, int W) {
   return 256 + block_align(sizeof(float) * (size_t)bwd_shape(d).tiles * (W + 1) * d.C);
 }
 
-template <typename F>
+template <int VEC, typename F>
 cudaError_t by_type(gdr_dtype dt, bool vec, int W, F f) {
   auto width = [&](auto it, auto v) {
     return W == 2 ? f(it, v, std::integral_constant<int, 2>{})
                   : W == 3 ? f(it, v, std::integral_constant<int, 3>{}) : f(it, v, std::integral_constant<int, 4>{});
   };
-  using V8 = std::integral_constant<int, 8>;
+  using VN = std::integral_constant<int, VEC>;
   using V1 = std::integral_constant<int, 1>;
-  if (dt == GDR_DTYPE_BF16) return vec ? width(__nv_bfloat16{}, V8{}) : width(__nv_bfloat16{}, V1{});
-  return vec ? width(float{}, V8{}) : width(float{}, V1{});
+  if (dt == GDR_DTYPE_BF16) return vec ? width(__nv_bfloat16{}, VN{}) : width(__nv_bfloat16{}, V1{});
+  return vec ? width(float{}, VN{}) : width(float{}, V1{});
 }
 
 }  // namespace
@@ -459,16 +578,18 @@ gdr_status gdr_conv_fwd(const gdr_conv_problem* p, const void* x, const float* w
     if (e != cudaSuccess) return status_of(e);
   }
   const bool vec = d.C % 8 == 0 && d.ld_x % 8 == 0 && vec_ok(x) && vec_ok(y) && vec_ok(state) && vec_ok(last) && vec_ok(w);
-  const long long ncg = vec ? d.C / 8 : d.C;
-  // runs of 32 tokens read 3 rows twice (from the L2); short batches take shorter runs so that
-  // there are threads enough to keep the memory busy
-  int L = 32;
-  while (L > 4 && (d.total + L - 1) / L * ncg < (long long)kSmCount * 1024) L /= 2;
+  const long long ncg = vec ? d.C / kFwdVec : d.C;
+  // Runs of equal length in whole waves of blocks: as many tokens as one wave needs, at
+  // most 128 (a run reads W - 1 rows of its neighbour's again), at least 4.
+  const long long wave = (long long)kFwdBlocks * kSmCount * kThreads, per = (d.total * ncg + wave - 1) / wave, waves = (per + 127) / 128;
+  long long run = waves > 0 ? (per + waves - 1) / waves : 4;
+  run = (run + 3) / 4 * 4;
+  const int L = (int)(run < 4 ? 4 : run);
   const long long threads = ((d.total + L - 1) / L + (last ? d.num_seqs : 0)) * ncg;
   if (threads == 0) return GDR_OK;
   const long long grid = (threads + kThreads - 1) / kThreads;
   if (grid >= (1ll << 31)) return GDR_ERR_UNSUPPORTED;
-  return status_of(by_type(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
+  return status_of(by_type<kFwdVec>(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
     using IT = decltype(it);
     conv_fwd_kernel<IT, decltype(v)::value, decltype(wd)::value><<<(unsigned)grid, kThreads, 0, s>>>(
         d, (const IT*)x, w, bias, (const IT*)state, (IT*)y, (IT*)last, L);
@@ -503,11 +624,11 @@ gdr_status gdr_conv_bwd(const gdr_conv_problem* p, const void* x, const float* w
   const BwdShape b = bwd_shape(d);
   const int subs = kThreads / b.cpb;
   const long long gx = b.tiles + (dstate ? ((long long)d.num_seqs + subs - 1) / subs : 0);
-  const int ncg = vec ? d.C / 8 : d.C;
+  const int ncg = vec ? d.C / kBwdVec : d.C;
   const int gy = (ncg + b.cpb - 1) / b.cpb;
   if (gx >= (1ll << 31) || gy > 65535) return GDR_ERR_UNSUPPORTED;
   if (gx > 0) {
-    const cudaError_t e = by_type(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
+    const cudaError_t e = by_type<kBwdVec>(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
       using IT = decltype(it);
       conv_bwd_kernel<IT, decltype(v)::value, decltype(wd)::value><<<dim3((unsigned)gx, gy), kThreads, 0, s>>>(
           d, (const IT*)x, w, bias, (const IT*)state, (const IT*)dy, (const IT*)dlast, (IT*)dx, (IT*)dstate, partial,
@@ -541,9 +662,9 @@ gdr_status gdr_conv_step(const gdr_conv_problem* p, const void* x, const float* 
   cudaStream_t s = (cudaStream_t)stream;
   stage_begin(s);
   const bool vec = d.C % 8 == 0 && d.ld_x % 8 == 0 && vec_ok(x) && vec_ok(y) && vec_ok(pool) && vec_ok(w);
-  const long long grid = (d.total * (vec ? d.C / 8 : d.C) + kThreads - 1) / kThreads;
+  const long long grid = (d.total * (vec ? d.C / kFwdVec : d.C) + kThreads - 1) / kThreads;
   if (grid >= (1ll << 31)) return GDR_ERR_UNSUPPORTED;
-  return status_of(by_type(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
+  return status_of(by_type<kFwdVec>(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
     using IT = decltype(it);
     conv_step_kernel<IT, decltype(v)::value, decltype(wd)::value><<<(unsigned)grid, kThreads, 0, s>>>(
         p->B, d.C, d.ld_x, d.silu, p->num_slots, (const IT*)x, w, bias, (IT*)pool, slots, (IT*)y);
