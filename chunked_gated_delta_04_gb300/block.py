@@ -177,6 +177,16 @@ def _type(x):
     return code
 
 
+_LAYOUT = {"KV": 0, "VK": 1}
+_I32 = torch.int32
+
+
+def _slots_ok(slots, n, B):
+    if slots is None:
+        return n >= B
+    return slots.dtype is _I32 and slots.shape == (B,) and slots.is_contiguous() and slots.is_cuda
+
+
 def _step_state(state, slots, B):
     _slots(slots, B)
     if slots is None and state.shape[0] < B:
@@ -223,7 +233,7 @@ def conv_forward(x, weight, bias=None, initial_state=None, cu_seqlens=None, acti
     y = _empty(x.shape, dtype=x.dtype, device=x.device)
     last = (_empty(p.num_seqs, p.W - 1, p.C, dtype=x.dtype, device=x.device) if output_final_state else None)
     ws = _workspace(256 if cu_seqlens is not None else 0, x.device)
-    st = lib.gdr_conv_fwd(_c.byref(p), _p(x), _p(weight), _p(bias), _p(initial_state), _p(y), _p(last), _p(ws),
+    st = lib.gdr_conv_fwd(p, _p(x), _p(weight), _p(bias), _p(initial_state), _p(y), _p(last), _p(ws),
                           256 if ws is not None else 0, _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_conv_fwd")
@@ -243,9 +253,9 @@ def conv_backward(x, weight, bias, dy, initial_state=None, dfinal_state=None, cu
     dw = torch.empty_like(weight)
     db = torch.empty_like(bias) if bias is not None else None
     dstate = torch.empty_like(initial_state) if initial_state is not None else None
-    n = lib.gdr_conv_bwd_workspace_bytes(_c.byref(p))
+    n = lib.gdr_conv_bwd_workspace_bytes(p)
     ws = _workspace(n, x.device)
-    st = lib.gdr_conv_bwd(_c.byref(p), _p(x), _p(weight), _p(bias), _p(initial_state), _p(dy), _p(dfinal_state), _p(dx),
+    st = lib.gdr_conv_bwd(p, _p(x), _p(weight), _p(bias), _p(initial_state), _p(dy), _p(dfinal_state), _p(dx),
                           _p(dw), _p(db), _p(dstate), _p(ws), n, _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_conv_bwd")
@@ -259,16 +269,27 @@ def conv_step(x, state, weight, bias=None, slots=None, activation="silu", stream
     if stream is not None:
         with _on(stream):
             return conv_step(x, state, weight, bias, slots, activation)
+    dtype = x.dtype
     B, C = x.shape
-    W = weight.shape[-1]
-    _act("x", x, (B, C), x.dtype)
-    _full("weight", weight, (C, W))
-    _full("bias", bias, (C,))
-    _full("state", state, (state.shape[0], W - 1, C), x.dtype)
-    _step_state(state, slots, B)
-    p = gdr_conv_problem(B, 1, C, W, B, None, _type(x), _silu(activation), _ld("x", x, 1), 0, state.shape[0])
-    y = _empty((B, C), dtype=x.dtype, device=x.device)
-    st = _lib().gdr_conv_step(_c.byref(p), _p(x), _p(weight), _p(bias), _p(state), _p(slots), _p(y), _raw_stream(x.get_device()))
+    n, W, c = state.shape
+    W += 1
+    ld = 0
+    # the usual call passes here; anything else is named by the checks
+    if not (c == C and state.dtype is dtype and weight.dtype is _F32 and weight.shape == (C, W) and x.is_contiguous()
+            and state.is_contiguous() and weight.is_contiguous() and x.is_cuda and state.is_cuda and weight.is_cuda
+            and dtype in _CODE and (bias is None or _is(bias, (C,))) and _slots_ok(slots, n, B) and activation in _SILU):
+        _act("x", x, (B, C), dtype)
+        _full("weight", weight, (C, W))
+        _full("bias", bias, (C,))
+        _full("state", state, (n, W - 1, C), dtype)
+        _step_state(state, slots, B)
+        _type(x)
+        _silu(activation)
+        ld = _ld("x", x, 1)
+    p = gdr_conv_problem(B, 1, C, W, B, None, _CODE[dtype], _SILU[activation], ld, 0, n)
+    y = _empty((B, C), dtype=dtype, device=x.device) if ld else torch.empty_like(x)
+    st = _lib().gdr_conv_step(p, x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(), _p(slots), y.data_ptr(),
+                              _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_conv_step")
     return y
@@ -343,10 +364,10 @@ def ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, cu_seqlens=None
     S_T = _empty((p.num_seqs, p.D, p.N), dtype=torch.float32, device=x.device) if output_final_state else None
     saved = None
     if save:
-        saved = _empty(lib.gdr_ssm_saved_bytes(_c.byref(p)) // 4, dtype=torch.float32, device=x.device)
-    n = lib.gdr_ssm_fwd_workspace_bytes(_c.byref(p))
+        saved = _empty(lib.gdr_ssm_saved_bytes(p) // 4, dtype=torch.float32, device=x.device)
+    n = lib.gdr_ssm_fwd_workspace_bytes(p)
     ws = _workspace(n, x.device)
-    st = lib.gdr_ssm_fwd(_c.byref(p), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(S0), _p(y), _p(S_T),
+    st = lib.gdr_ssm_fwd(p, _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(S0), _p(y), _p(S_T),
                          _p(saved), _p(ws), n, _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_ssm_fwd")
@@ -362,7 +383,7 @@ def ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D=None, dt_bias=None, dS_T=None,
     p = _ssm_problem(x, dt, A, Bm, Cm, D, dt_bias, cu_seqlens, dt_softplus, dy)
     _full("dS_T", dS_T, (p.num_seqs, p.D, p.N))
     lib = _lib()
-    need = lib.gdr_ssm_saved_bytes(_c.byref(p)) // 4
+    need = lib.gdr_ssm_saved_bytes(p) // 4
     if h_saved is None or h_saved.dtype != _F32 or not h_saved.is_contiguous() or h_saved.numel() < need:
         raise ValueError(f"h_saved: expected the {need} floats that ssm_forward kept (save=True)")
     f32 = torch.float32
@@ -372,9 +393,9 @@ def ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D=None, dt_bias=None, dS_T=None,
     dD = torch.empty_like(D) if D is not None else None
     dbias = torch.empty_like(dt_bias) if dt_bias is not None else None
     dS0 = _empty((p.num_seqs, p.D, p.N), dtype=f32, device=x.device) if want_dS0 else None
-    n = lib.gdr_ssm_bwd_workspace_bytes(_c.byref(p))
+    n = lib.gdr_ssm_bwd_workspace_bytes(p)
     ws = _workspace(n, x.device)
-    st = lib.gdr_ssm_bwd(_c.byref(p), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(h_saved), _p(dy),
+    st = lib.gdr_ssm_bwd(p, _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(h_saved), _p(dy),
                          _p(dS_T), _p(dx), _p(ddt), _p(dA), _p(dB), _p(dC), _p(dD), _p(dbias), _p(dS0), _p(ws), n,
                          _raw_stream(x.get_device()))
     if st:
@@ -388,22 +409,31 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, slots=None, dt_softp
     if stream is not None:
         with _on(stream):
             return ssm_step(x, dt, A, Bm, Cm, state, D, dt_bias, slots, dt_softplus)
+    dtype = x.dtype
     B, d = x.shape
-    G, N = Bm.shape[1], Bm.shape[2]
-    _act("x", x, (B, d), x.dtype)
-    _act("dt", dt, (B, d), x.dtype)
-    _act("Bm", Bm, (B, G, N), x.dtype)
-    _act("Cm", Cm, (B, G, N), x.dtype)
-    _full("A", A, (d, N))
-    _full("D", D, (d,))
-    _full("dt_bias", dt_bias, (d,))
-    _full("state", state, (state.shape[0], d, N))
-    _step_state(state, slots, B)
-    p = gdr_ssm_problem(B, 1, d, N, G, B, None, _type(x), int(bool(dt_softplus)), _ld("x", x, 1), _ld("dt", dt, 1),
-                        _ld("Bm", Bm, 2), _ld("Cm", Cm, 2), 0, state.shape[0])
-    y = _empty((B, d), dtype=x.dtype, device=x.device)
-    st = _lib().gdr_ssm_step(_c.byref(p), _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(state), _p(slots),
-                             _p(y), _raw_stream(x.get_device()))
+    _, G, N = Bm.shape
+    n = state.shape[0]
+    lds = (0, 0, 0, 0)
+    if not (dt.dtype is dtype and Bm.dtype is dtype and Cm.dtype is dtype and dt.shape == (B, d) and Bm.shape == (B, G, N)
+            and Cm.shape == (B, G, N) and x.is_contiguous() and dt.is_contiguous() and Bm.is_contiguous()
+            and Cm.is_contiguous() and x.is_cuda and dt.is_cuda and Bm.is_cuda and Cm.is_cuda and dtype in _CODE
+            and _is(A, (d, N)) and _is(state, (n, d, N)) and (D is None or _is(D, (d,)))
+            and (dt_bias is None or _is(dt_bias, (d,))) and _slots_ok(slots, n, B)):
+        _act("x", x, (B, d), dtype)
+        _act("dt", dt, (B, d), dtype)
+        _act("Bm", Bm, (B, G, N), dtype)
+        _act("Cm", Cm, (B, G, N), dtype)
+        _full("A", A, (d, N))
+        _full("D", D, (d,))
+        _full("dt_bias", dt_bias, (d,))
+        _full("state", state, (n, d, N))
+        _step_state(state, slots, B)
+        _type(x)
+        lds = (_ld("x", x, 1), _ld("dt", dt, 1), _ld("Bm", Bm, 2), _ld("Cm", Cm, 2))
+    p = gdr_ssm_problem(B, 1, d, N, G, B, None, _CODE[dtype], 1 if dt_softplus else 0, *lds, 0, n)
+    y = _empty((B, d), dtype=dtype, device=x.device)
+    st = _lib().gdr_ssm_step(p, x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _p(D), _p(dt_bias),
+                             state.data_ptr(), _p(slots), y.data_ptr(), _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_ssm_step")
     return y
@@ -476,13 +506,26 @@ def norm_forward(x, post_weight=None, gate=None, scale=None, residual=None, pre_
     if stream is not None:
         with _on(stream):
             return norm_forward(x, post_weight, gate, scale, residual, pre_weight, eps)
-    res_dtype = x.dtype if residual is None else residual.dtype
-    p = _norm_problem(x, post_weight, gate, scale, pre_weight, res_dtype, eps)
-    _full("residual", residual, x.shape, res_dtype)
-    r = _empty(x.shape, dtype=res_dtype, device=x.device) if residual is not None or pre_weight is None else None
-    y = _empty(x.shape, dtype=x.dtype, device=x.device) if pre_weight is not None else None
-    st = _lib().gdr_norm_fwd(_c.byref(p), _p(x), _p(post_weight), _p(gate), _p(scale), _p(residual), _p(pre_weight), _p(r),
-                             _p(y), _raw_stream(x.get_device()))
+    dtype, shape = x.dtype, x.shape
+    res_dtype = dtype if residual is None else residual.dtype
+    D = shape[-1]
+    if (x.is_contiguous() and x.is_cuda and dtype in _CODE and res_dtype in _CODE and D > 0
+            and (gate is None or _is(gate, shape, dtype)) and (residual is None or _is(residual, shape, res_dtype))
+            and (post_weight is None or _is(post_weight, (D,))) and (scale is None or _is(scale, (D,)))
+            and (pre_weight is None or _is(pre_weight, (D,)))):
+        p = gdr_norm_problem(x.numel() // D, 1, D, _CODE[dtype], _CODE[res_dtype], eps, 0, 0)
+    else:
+        p = _norm_problem(x, post_weight, gate, scale, pre_weight, res_dtype, eps)
+        _full("residual", residual, shape, res_dtype)
+    r = y = None
+    if residual is not None:
+        r = torch.empty_like(residual)
+    elif pre_weight is None:
+        r = _empty(shape, dtype=dtype, device=x.device)
+    if pre_weight is not None:
+        y = _empty(shape, dtype=dtype, device=x.device)
+    st = _lib().gdr_norm_fwd(p, x.data_ptr(), _p(post_weight), _p(gate), _p(scale), _p(residual), _p(pre_weight), _p(r), _p(y),
+                             _raw_stream(x.get_device()))
     if st:
         _raise(st, "gdr_norm_fwd")
     return r, y
@@ -512,10 +555,10 @@ def norm_backward(x, post_weight=None, gate=None, scale=None, r=None, pre_weight
     dx, dgate = new(x), new(gate)
     dres = new(x, res_dtype) if has_residual else None
     dpost, dscale, dpre = new(post_weight), new(scale), new(pre_weight)
-    n = lib.gdr_norm_bwd_workspace_bytes(_c.byref(p))
+    n = lib.gdr_norm_bwd_workspace_bytes(p)
     ws = _workspace(n, x.device)
     rr = r if has_residual else (x if pre_weight is not None else None)
-    st = lib.gdr_norm_bwd(_c.byref(p), _p(x), _p(post_weight), _p(gate), _p(scale), _p(rr), _p(pre_weight),
+    st = lib.gdr_norm_bwd(p, _p(x), _p(post_weight), _p(gate), _p(scale), _p(rr), _p(pre_weight),
                           int(has_residual), _p(dr), _p(dy), _p(dx), _p(dgate), _p(dres), _p(dpost), _p(dscale), _p(dpre),
                           _p(ws), n, _raw_stream(x.get_device()))
     if st:
@@ -563,22 +606,28 @@ def step(q, k, v, g, beta, state, layout="KV", scale=None, slots=None, prologue=
     if stream is not None:
         with _on(stream):
             return step(q, k, v, g, beta, state, layout, scale, slots, prologue)
+    dtype = q.dtype
     B, Hk, DK = q.shape
-    Hv, DV = v.shape[1], v.shape[2]
-    if layout not in ("KV", "VK"):
-        raise ValueError(f"layout {layout!r}: 'KV' or 'VK'")
-    _full("q", q, (B, Hk, DK), q.dtype)
-    _full("k", k, (B, Hk, DK), q.dtype)
-    _full("v", v, (B, Hv, DV), q.dtype)
-    _full("g", g, (B, Hv))
-    _full("beta", beta, (B, Hv), q.dtype)
-    _full("state", state, (state.shape[0], Hv, DK, DV) if layout == "KV" else (state.shape[0], Hv, DV, DK))
-    _step_state(state, slots, B)
-    p = _gdr.gdr_problem(B, 1, Hk, Hv, DK, DV, B, None, _type(q), 0 if layout == "KV" else 1,
-                        0.0 if scale is None else float(scale), 0, int(prologue), 0, 1, 1)
-    o = _empty((B, Hv, DV), dtype=q.dtype, device=q.device)
-    st = _lib().gdr_step(_c.byref(p), _p(q), _p(k), _p(v), _p(g), _p(beta), _p(state), state.shape[0],
-                         _p(slots), _p(o), _raw_stream(q.get_device()))
+    Hv, DV = v.shape[1:]
+    n = state.shape[0]
+    if not (_is(q, (B, Hk, DK), dtype) and _is(k, (B, Hk, DK), dtype) and _is(v, (B, Hv, DV), dtype) and _is(g, (B, Hv))
+            and _is(beta, (B, Hv), dtype) and layout in _LAYOUT and dtype in _CODE and _slots_ok(slots, n, B)
+            and _is(state, (n, Hv, DK, DV) if layout == "KV" else (n, Hv, DV, DK))):
+        if layout not in _LAYOUT:
+            raise ValueError(f"layout {layout!r}: 'KV' or 'VK'")
+        _type(q)
+        _full("q", q, (B, Hk, DK), dtype)
+        _full("k", k, (B, Hk, DK), dtype)
+        _full("v", v, (B, Hv, DV), dtype)
+        _full("g", g, (B, Hv))
+        _full("beta", beta, (B, Hv), dtype)
+        _full("state", state, (n, Hv, DK, DV) if layout == "KV" else (n, Hv, DV, DK))
+        _step_state(state, slots, B)
+    p = _gdr.gdr_problem(B, 1, Hk, Hv, DK, DV, B, None, _CODE[dtype], _LAYOUT[layout], 0.0 if scale is None else scale, 0,
+                         prologue, 0, 1, 1)
+    o = torch.empty_like(v)
+    st = _lib().gdr_step(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), n,
+                         _p(slots), o.data_ptr(), _raw_stream(q.get_device()))
     if st:
         _raise(st, "gdr_step")
     return o
