@@ -5,7 +5,7 @@
 // Every (channel, state) pair decays at a rate of its own, so there is no matrix product whose
 // factors stay in range: the recurrence runs token by token in fp32 registers.  NL = N / 4 lanes
 // share a channel, four states each; the sum over n runs over those lanes for four tokens at a
-// time.  A block holds CB channels; D_t, D_t x_t, B_t and C_t of 16 tokens are formed once per token
+// time.  A block holds 64 channels; D_t, D_t x_t, B_t and C_t of 16 tokens are formed once per token
 // and channel and staged in shared memory.  Bound by arithmetic from
 // N = 16 on: per (token, channel, state) one exponential and four multiply-adds, against
 // 6 / N bytes in bf16.
@@ -18,7 +18,9 @@
 namespace gdr {
 namespace {
 
-constexpr int fwd_threads(int NL) { return NL == 1 ? 64 : NL <= 4 ? 128 : 32 * NL; }
+// Threads of a block: 32 pairs of channels by the NL lanes of each.
+constexpr int fwd_threads(int NL) { return 32 * NL; }
+constexpr int kFwdChannels = 64;
 
 enum SsmMode { kFull, kEndState, kStartGrad };
 
@@ -26,10 +28,14 @@ enum SsmMode { kFull, kEndState, kStartGrad };
 // kStartGrad (in reverse): R[u] = gradient of the state in front of unit u from a zero gradient
 // behind it; x is dy, and C plays B's part.
 //
+// A thread holds two channels by four states.  What a token needs comes from shared memory in three
+// 16-byte loads (the two channels' D and D x, four B, four C) for eight states: with one channel
+// (and D, D x stored twice for the packed instructions) the loads' return path, 128 bytes a clock
+// and SM, was the bound: 213 us at B = 1, T = 32768, D = 1024, N = 16.
+//
 // One barrier per tile: while tile k is computed from one buffer, tile k + 1 is formed in the other
 // from registers that tile k + 2's loads then refill, and tile k - 1's y leaves.  A thread forms and
-// finishes the same four channels of a token.  (D, D, D x, D x) are kept as register pairs for the
-// packed fp32 instructions, two states at a time.
+// finishes the same four channels of a token.
 template <typename IT, int NL, int MODE>
 __global__ void __launch_bounds__(fwd_threads(NL))
     ssm_scan_kernel(SsmDims d, const IT* __restrict__ x, long long ld_x, const IT* __restrict__ dt,
@@ -37,30 +43,43 @@ __global__ void __launch_bounds__(fwd_threads(NL))
                     const IT* __restrict__ Cm, const float* __restrict__ Dskip, const float* __restrict__ dt_bias,
                     const float* __restrict__ start, int start_per_unit, IT* __restrict__ y, float* __restrict__ S_T,
                     float* __restrict__ h_saved, float* __restrict__ R, float* __restrict__ sum_delta) {
-  constexpr int NT = fwd_threads(NL), CB = NT / NL, N = 4 * NL;
-  constexpr int Q = CB / 4, QP = NL >= 4 ? 1 : 4 / NL;  // quads of channels; quads of a tile per thread
-  constexpr int YS = CB + 8;                            // padded rows: 4 tokens x 8 channels hit 32 banks
+  constexpr int NT = fwd_threads(NL), CB = kFwdChannels, PB = CB / 2, N = 4 * NL;
+  constexpr int Q = CB / 4, QP = kTile * Q > NT ? kTile * Q / NT : 1;  // quads of channels; of a tile per thread
+  constexpr int YS = CB + 16;
   constexpr bool kY = MODE == kFull;
-  __shared__ Pair2 sdu[2][kTile][CB];  // {D, D}, {D x, D x}, at slot(channel)
+  __shared__ Pair2 sdu[2][kTile][PB];  // {D, D'}, {D x, D' x'} of a channel pair, at slot(pair)
   __shared__ __align__(16) float sB[2][kTile][N], sC[kY ? 2 : 1][kTile][N];
   __shared__ __align__(16) float sy[kY ? 2 : 1][kY ? kTile : 1][YS];
   if (ssm_bad(d)) return;
-  // 16-byte slots: a quad's four stores and a warp's loads of eight channels each hit all banks
-  auto slot = [](int c) { return c ^ ((c >> 3) & 3); };
-  const int tid = threadIdx.x, ln = tid % NL, ch = tid / NL;
+  auto slot = [](int p) { return p ^ ((p >> 3) & 1); };  // a quad's two stores hit all banks
+  const int tid = threadIdx.x, ln = tid % NL, pr = tid / NL;
   const int blocks = (d.Dg + CB - 1) / CB, grp = blockIdx.x / blocks, c0 = (blockIdx.x - grp * blocks) * CB;
   const int nch = min(CB, d.Dg - c0);                // live channels of this block
   const long long dc0 = (long long)grp * d.Dg + c0;  // its first channel
-  const bool live = ch < nch;
-  const long long dch = dc0 + ch;
-  f32x2 A2[2] = {0, 0};
-  if (live) {
-    const float4 a = *reinterpret_cast<const float4*>(A + dch * N + 4 * ln);
-    // finite, so that D = 0 past the end gives exp(0) = 1 also for A = -infinity
-    A2[0] = pack2(fmaxf(a.x * kLog2e, -kBig), fmaxf(a.y * kLog2e, -kBig));
-    A2[1] = pack2(fmaxf(a.z * kLog2e, -kBig), fmaxf(a.w * kLog2e, -kBig));
-  }
-  // staging: quad of channels qc of token qt (+ 4 NL tokens per further quad)
+  const bool live[2] = {2 * pr < nch, 2 * pr + 1 < nch};
+  const long long dch = dc0 + 2 * pr;
+  auto load_state = [&](const float* p, f32x2 (&v)[2][2]) {  // p: [D][N]; a missing channel is zeros
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const float4 f = live[c] ? *reinterpret_cast<const float4*>(p + (dch + c) * N + 4 * ln) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[c][0] = pack2(f.x, f.y);
+      v[c][1] = pack2(f.z, f.w);
+    }
+  };
+  auto store_state = [&](float* p, const f32x2 (&v)[2][2]) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (live[c])
+        *reinterpret_cast<float4*>(p + (dch + c) * N + 4 * ln) = make_float4(lo2(v[c][0]), hi2(v[c][0]), lo2(v[c][1]), hi2(v[c][1]));
+  };
+  f32x2 A2[2][2];
+  load_state(A, A2);
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)  // finite, so that D = 0 past the end gives exp(0) = 1 also for A = -infinity
+      A2[c][j] = pack2(fmaxf(lo2(A2[c][j]) * kLog2e, -kBig), fmaxf(hi2(A2[c][j]) * kLog2e, -kBig));
+  // staging: quad of channels qc of token qt (+ NT / Q tokens per further quad)
   const int qc = 4 * (tid % Q), qt = tid / Q, qn = qt < kTile ? nch - qc : 0;
   float bias[4] = {}, skip[4] = {};
 #pragma unroll
@@ -77,14 +96,9 @@ __global__ void __launch_bounds__(fwd_threads(NL))
   const long long units = ssm_unit_count(d);
   for (long long un = blockIdx.y; un < units; un += gridDim.y) {
     const SsmUnit q = ssm_unit(d, un);
-    f32x2 h[2] = {0, 0};
-    if (kY && start && live) {
-      const long long at = start_per_unit ? un : q.seq;
-      const float4 v = *reinterpret_cast<const float4*>(start + (at * d.D + dch) * N + 4 * ln);
-      h[0] = pack2(v.x, v.y);
-      h[1] = pack2(v.z, v.w);
-    }
-    float dsum = 0.f;
+    f32x2 h[2][2] = {};
+    if (kY && start) load_state(start + (start_per_unit ? un : q.seq) * (long long)d.D * N, h);
+    f32x2 dsum = 0;
     const int tiles = (q.len + kTile - 1) / kTile;
     auto base_of = [&](int k) { return (MODE == kStartGrad ? tiles - 1 - k : k) * kTile; };
     // a tile whose 16 tokens and CB channels all exist, aligned: no bounds in its loads and stores
@@ -137,10 +151,8 @@ __global__ void __launch_bounds__(fwd_threads(NL))
               const int n = base + tt < q.len ? qn : 0;
               dl = pack2(c < n ? lo2(dl) : 0.f, c + 1 < n ? hi2(dl) : 0.f);
             }
-            f32x2 u = pack2(xv[c], xv[c + 1]);
-            if (MODE != kStartGrad) u = mul2(dl, u);
-            sdu[buf][tt][slot(qc + c)] = Pair2{pack2(lo2(dl), lo2(dl)), pack2(lo2(u), lo2(u))};
-            sdu[buf][tt][slot(qc + c + 1)] = Pair2{pack2(hi2(dl), hi2(dl)), pack2(hi2(u), hi2(u))};
+            const f32x2 xp = pack2(xv[c], xv[c + 1]);
+            sdu[buf][tt][slot((qc + c) / 2)] = Pair2{dl, MODE == kStartGrad ? xp : mul2(dl, xp)};
           }
         }
       }
@@ -177,27 +189,32 @@ __global__ void __launch_bounds__(fwd_threads(NL))
       form(0);
       if (tiles > 1) fetch(1);
     }
-    const int sl = slot(ch);
+    const int sl = slot(pr);
     for (int k = 0; k < tiles; ++k) {
       const int buf = k & 1;
       __syncthreads();
-      // Groups of four tokens: a group's loads and exponentials (which nothing in the recurrence
-      // waits for) are issued a group ahead of its recurrence.
-      f32x2 e[2][4][2], ub[2][4][2];
-      Pair2 cc[2][4];
+      // Two tokens at a time: a pair's loads and exponentials (which nothing in the recurrence waits
+      // for) are issued a pair ahead of its recurrence.
+      f32x2 e[2][2][2][2], ub[2][2][2][2];  // [turn][token][channel][two states]
+      Pair2 cc[2][2];
       auto ahead = [&](int g) {
         const int w = g & 1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = MODE == kStartGrad ? kTile - 1 - (4 * g + i) : 4 * g + i;
+        for (int i = 0; i < 2; ++i) {
+          const int t = MODE == kStartGrad ? kTile - 1 - (2 * g + i) : 2 * g + i;
           const Pair2 du = sdu[buf][t][sl];
           const Pair2 b = *reinterpret_cast<const Pair2*>(&sB[buf][t][4 * ln]);
           if (kY) cc[w][i] = *reinterpret_cast<const Pair2*>(&sC[kY ? buf : 0][t][4 * ln]);
-          e[w][i][0] = ex2_2(mul2(du.a, A2[0]));
-          e[w][i][1] = ex2_2(mul2(du.a, A2[1]));
-          ub[w][i][0] = mul2(du.b, b.a);
-          ub[w][i][1] = mul2(du.b, b.b);
-          if (!kY) dsum += lo2(du.a);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float dl = c ? hi2(du.a) : lo2(du.a), u = c ? hi2(du.b) : lo2(du.b);
+            const f32x2 dd = pack2(dl, dl), uu = pack2(u, u);
+            e[w][i][c][0] = ex2_2(mul2(dd, A2[c][0]));
+            e[w][i][c][1] = ex2_2(mul2(dd, A2[c][1]));
+            ub[w][i][c][0] = mul2(uu, b.a);
+            ub[w][i][c][1] = mul2(uu, b.b);
+          }
+          if (!kY) dsum = add2(dsum, du.a);
         }
       };
       ahead(0);
@@ -209,47 +226,47 @@ __global__ void __launch_bounds__(fwd_threads(NL))
         for (int i = 0; i < QP; ++i) x0[i] = x1[i];
       }
       if (k + 2 < tiles) fetch(k + 2);
-      if (kY && h_saved && live)
-        *reinterpret_cast<float4*>(h_saved + ((q.tile0 + k) * d.D + dch) * N + 4 * ln) =
-            make_float4(lo2(h[0]), hi2(h[0]), lo2(h[1]), hi2(h[1]));
+      if (kY && h_saved) store_state(h_saved + (q.tile0 + k) * (long long)d.D * N, h);
+      float p[8];  // [token of four][channel]
 #pragma unroll
-      for (int g = 0; g < kTile / 4; ++g) {
-        if (g + 1 < kTile / 4) ahead(g + 1);
+      for (int g = 0; g < kTile / 2; ++g) {
+        if (g + 1 < kTile / 2) ahead(g + 1);
         const int w = g & 1;
-        float p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (MODE == kStartGrad) {
-            h[0] = mul2(e[w][i][0], add2(ub[w][i][0], h[0]));
-            h[1] = mul2(e[w][i][1], add2(ub[w][i][1], h[1]));
-          } else {
-            h[0] = fma2(e[w][i][0], h[0], ub[w][i][0]);
-            h[1] = fma2(e[w][i][1], h[1], ub[w][i][1]);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              h[c][j] = MODE == kStartGrad ? mul2(e[w][i][c][j], add2(ub[w][i][c][j], h[c][j]))
+                                           : fma2(e[w][i][c][j], h[c][j], ub[w][i][c][j]);
+            if (kY) {
+              const f32x2 s = fma2(h[c][0], cc[w][i].a, mul2(h[c][1], cc[w][i].b));
+              p[4 * w + 2 * i + c] = lo2(s) + hi2(s);
+            }
           }
-          if (kY) {
-            const f32x2 s = fma2(h[0], cc[w][i].a, mul2(h[1], cc[w][i].b));
-            p[i] = lo2(s) + hi2(s);
-          }
-        }
-        if (kY) {
-          using Sum = LaneSums<4, NL, 1>;
+        if (kY && w == 1) {
+          using Sum = LaneSums<8, NL, 1>;
           Sum::run(p, ln);
           if (Sum::holds(ln)) {
 #pragma unroll
-            for (int i = 0; i < Sum::KEEP; ++i) sy[kY ? buf : 0][kY ? 4 * g + Sum::index(ln) + i : 0][ch] = p[i];
+            for (int i = 0; i < Sum::KEEP; ++i) {
+              const int at = Sum::index(ln) + i;
+              sy[kY ? buf : 0][kY ? 2 * (g - 1) + (at >> 1) : 0][2 * pr + (at & 1)] = p[i];
+            }
           }
         }
       }
     }
     __syncthreads();
     if (tiles > 0) finish(tiles - 1, x0);
-    if (live) {
-      const float4 v = make_float4(lo2(h[0]), hi2(h[0]), lo2(h[1]), hi2(h[1]));
-      if (kY) {
-        if (S_T && q.last) *reinterpret_cast<float4*>(S_T + ((long long)q.seq * d.D + dch) * N + 4 * ln) = v;
-      } else {
-        *reinterpret_cast<float4*>(R + (un * d.D + dch) * N + 4 * ln) = v;
-        if (ln == 0) sum_delta[un * d.D + dch] = dsum;
+    if (kY) {
+      if (S_T && q.last) store_state(S_T + (long long)q.seq * d.D * N, h);
+    } else {
+      store_state(R + un * (long long)d.D * N, h);
+      if (ln == 0) {
+        if (live[0]) sum_delta[un * d.D + dch] = lo2(dsum);
+        if (live[1]) sum_delta[un * d.D + dch + 1] = hi2(dsum);
       }
     }
   }
@@ -409,8 +426,7 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmDims d, int B, int num
 }
 
 int fwd_blocks(const SsmDims& d) {
-  const int NL = d.N / 4, CB = fwd_threads(NL) / NL;
-  return d.G * ((d.Dg + CB - 1) / CB);
+  return d.G * ((d.Dg + kFwdChannels - 1) / kFwdChannels);
 }
 
 template <typename F>
@@ -462,12 +478,15 @@ gdr_status resolve_ssm(const gdr_ssm_problem* p, bool step, SsmDims* d) {
   d->ld_b = p->ld_b ? p->ld_b : gn;
   d->ld_c = p->ld_c ? p->ld_c : gn;
   d->cu = p->cu_seqlens;
-  // One segment per sequence where the channels alone give every SM about two blocks; else segments
-  // of at least 64 tokens, enough of them for four blocks per SM.
+  // A block takes about 80 ns a token however few there are, and an SM is full at 2.2 of them; cutting
+  // sequences into segments costs the first pass (0.7 of the full one).  So segments pay below about
+  // one block per SM (B = 2, T = 4096, D = 4096, N = 16, 128 blocks: 285 us against 328), and where a
+  // packed batch's longest sequence, which the host does not know, may be twice the average, below
+  // two.  They are made of at least 64 tokens, enough for six blocks per SM.
   const long long blocks = fwd_blocks(*d), whole = (d->T + kTile - 1) / kTile * (long long)kTile;
   d->Lseg = (int)(whole < kTile ? kTile : whole);
-  if (!step && blocks * d->num_seqs < kSmCount) {
-    const long long want = (4ll * kSmCount + blocks - 1) / blocks;  // segments over all sequences
+  if (!step && blocks * d->num_seqs < (d->cu ? 2 : 1) * kSmCount) {
+    const long long want = (6ll * kSmCount + blocks - 1) / blocks;  // segments over all sequences
     long long L = (d->total / want + kTile - 1) / kTile * kTile;
     if (L < 64) L = 64;
     if (L < d->Lseg) d->Lseg = (int)L;

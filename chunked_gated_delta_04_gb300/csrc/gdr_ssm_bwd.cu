@@ -27,11 +27,23 @@ struct SsmBwdArgs {
   float *dS0, *grads, *bc;
 };
 
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// Copies `bytes` (4, 8 or 16; the rest of a Bytes-wide destination is zeros) without passing registers.
+template <int Bytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src), "n"(Bytes), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Shared memory of a block, two tiles of everything: the one being computed and the one that is
 // formed (or finished) beside it.
-template <int N>
+template <typename IT, int N>
 struct BwdSmem {
   static constexpr int NT = bwd_threads(N), ML = N / 2, CB = 2 * NT / ML, WARPS = NT / 32;
+  static constexpr int QP = 4 * CB > NT ? 4 * CB / NT : 1;  // quads of channels of a tile per thread
+  // what a thread's own copies bring: its quads of x, dt, dy of the next tile, its states of the next two
+  Raw4<IT> raw[2][3][QP][NT];
+  float2 h[3][2][NT];
   Pair2 du[2][kTile][CB / 2];                      // {D, D'}, {D x, D' x'} of a channel pair
   f32x2 dy[2][kTile][CB / 2];
   alignas(16) float x[2][kTile][CB], sig[2][kTile][CB];
@@ -45,9 +57,9 @@ struct BwdSmem {
 
 template <typename IT, int N>
 __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, SsmBwdArgs a) {
-  using Smem = BwdSmem<N>;
+  using Smem = BwdSmem<IT, N>;
   constexpr int NT = Smem::NT, ML = Smem::ML, CB = Smem::CB, WARPS = Smem::WARPS, CL = 32 / ML;
-  constexpr int Q = CB / 4, QP = 4 * CB > NT ? 4 * CB / NT : 1;  // quads of channels; of a tile per thread
+  constexpr int Q = CB / 4, QP = Smem::QP;  // quads of channels; of a tile per thread
   constexpr int BQ = (8 * N + NT - 1) / NT;                      // quads of B and C per thread
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
@@ -90,20 +102,25 @@ __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, S
     const IT* xq = (const IT*)a.x + (long long)q.t0 * d.ld_x + dc0 + qc;
     const IT* dq = (const IT*)a.dt + (long long)q.t0 * d.ld_dt + dc0 + qc;
     const IT* yq = (const IT*)a.dy + (long long)q.t0 * d.ld_dy + dc0 + qc;
-    Raw4<IT> rx[QP], rd[QP], ry[QP], rb[BQ];
-    f32x2 ph[2] = {0, 0};
-    // step k works on tile tiles - 1 - k; whole: its 16 tokens and CB channels all exist, aligned
+    Raw4<IT> rb[BQ];
+    // Step k works on tile tiles - 1 - k; whole: its 16 tokens and CB channels all exist, aligned.
+    // The copies go straight to shared memory: as register loads they were put off to the end of the
+    // computation they were to overlap with, there being no registers to hold them.
     auto whole = [&](int k) { return vec && nch == CB && (tiles - k) * kTile <= q.len; };
     auto fetch = [&](int k) {
       const int base = (tiles - 1 - k) * kTile;
+      const float* hs = a.h_saved + ((q.tile0 + tiles - 1 - k) * d.D + dch) * N + 2 * nl;
+      copy_async<8>(&sm.h[k % 3][0][tid], live0 ? hs : a.h_saved, live0 ? 8 : 0);
+      copy_async<8>(&sm.h[k % 3][1][tid], live1 ? hs + N : a.h_saved, live1 ? 8 : 0);
+      Raw4<IT>(*raw)[QP][NT] = sm.raw[k & 1];
       if (whole(k)) {
 #pragma unroll
         for (int i = 0; i < QP; ++i) {
           const long long t = base + qt + i * (NT / Q);
           if (qt < kTile) {
-            rx[i] = load_raw4(xq + t * d.ld_x, 4, true);
-            rd[i] = load_raw4(dq + t * d.ld_dt, 4, true);
-            ry[i] = load_raw4(yq + t * d.ld_dy, 4, true);
+            copy_async<sizeof(Raw4<IT>)>(&raw[0][i][tid], xq + t * d.ld_x, sizeof(Raw4<IT>));
+            copy_async<sizeof(Raw4<IT>)>(&raw[1][i][tid], dq + t * d.ld_dt, sizeof(Raw4<IT>));
+            copy_async<sizeof(Raw4<IT>)>(&raw[2][i][tid], yq + t * d.ld_dy, sizeof(Raw4<IT>));
           }
         }
       } else {
@@ -111,9 +128,9 @@ __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, S
         for (int i = 0; i < QP; ++i) {
           const long long t = base + qt + i * (NT / Q);
           const int n = t < q.len ? qn : 0;
-          rx[i] = load_raw4(xq + t * d.ld_x, n, vec);
-          rd[i] = load_raw4(dq + t * d.ld_dt, n, vec);
-          ry[i] = load_raw4(yq + t * d.ld_dy, n, vec);
+          raw[0][i][tid] = load_raw4(xq + t * d.ld_x, n, vec);
+          raw[1][i][tid] = load_raw4(dq + t * d.ld_dt, n, vec);
+          raw[2][i][tid] = load_raw4(yq + t * d.ld_dy, n, vec);
         }
       }
 #pragma unroll
@@ -133,9 +150,9 @@ __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, S
         const int tt = qt + i * (NT / Q);
         if (qt < kTile) {
           float xv[4], dv[4], yv[4], sg[4] = {1.f, 1.f, 1.f, 1.f};
-          rx[i].get(xv);
-          rd[i].get(dv);
-          ry[i].get(yv);
+          sm.raw[buf][0][i][tid].get(xv);
+          sm.raw[buf][1][i][tid].get(dv);
+          sm.raw[buf][2][i][tid].get(yv);
 #pragma unroll
           for (int c = 0; c < 4; c += 2) {
             f32x2 dl = add2(pack2(dv[c], dv[c + 1]), pack2(bias[c], bias[c + 1]));
@@ -208,30 +225,40 @@ __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, S
       }
     };
     if (tiles > 0) {
-      load_pair(a.h_saved + (q.tile0 + tiles - 1) * d.D * N, ph);
       fetch(0);
+      copy_async_wait();
       form(0);
       if (tiles > 1) fetch(1);
     }
     for (int k = 0; k < tiles; ++k) {
       const int buf = k & 1;
+      copy_async_wait();  // the copies of tile k + 1, a whole tile's work ago
       __syncthreads();
       if (k > 0) finish(k - 1);  // before form overwrites this thread's own entries of that tile
       if (k + 1 < tiles) form(k + 1);
       if (k + 2 < tiles) fetch(k + 2);
       f32x2 h[kTile + 1][2], e[kTile][2];  // h[t]: in front of token t
-      h[0][0] = ph[0];
-      h[0][1] = ph[1];
-      if (k + 1 < tiles) load_pair(a.h_saved + (q.tile0 + tiles - 2 - k) * d.D * N, ph);
+      {
+        const float2 u = sm.h[k % 3][0][tid], w = sm.h[k % 3][1][tid];
+        h[0][0] = pack2(u.x, w.x);
+        h[0][1] = pack2(u.y, w.y);
+      }
+      // a token's operands are loaded a token ahead
+      Pair2 du = sm.du[buf][0][pr], b = *reinterpret_cast<const Pair2*>(&sm.B[buf][0][2 * nl]);
 #pragma unroll
       for (int t = 0; t < kTile; ++t) {
-        const Pair2 du = sm.du[buf][t][pr];
-        const Pair2 b = *reinterpret_cast<const Pair2*>(&sm.B[buf][t][2 * nl]);
-        e[t][0] = ex2_2(mul2(du.a, A2[0]));
-        e[t][1] = ex2_2(mul2(du.a, A2[1]));
-        h[t + 1][0] = fma2(e[t][0], h[t][0], mul2(du.b, b.a));
-        h[t + 1][1] = fma2(e[t][1], h[t][1], mul2(du.b, b.b));
+        const Pair2 du_t = du, b_t = b;
+        if (t + 1 < kTile) {
+          du = sm.du[buf][t + 1][pr];
+          b = *reinterpret_cast<const Pair2*>(&sm.B[buf][t + 1][2 * nl]);
+        }
+        e[t][0] = ex2_2(mul2(du_t.a, A2[0]));
+        e[t][1] = ex2_2(mul2(du_t.a, A2[1]));
+        h[t + 1][0] = fma2(e[t][0], h[t][0], mul2(du_t.b, b_t.a));
+        h[t + 1][1] = fma2(e[t][1], h[t][1], mul2(du_t.b, b_t.b));
       }
+      f32x2 dyv = sm.dy[buf][kTile - 1][pr];
+      Pair2 c = *reinterpret_cast<const Pair2*>(&sm.C[buf][kTile - 1][2 * nl]);
       f32x2 dAt[2] = {0, 0};  // a tile's part first: the long sum then has 1/16 of the terms
 #pragma unroll
       for (int t2 = kTile - 2; t2 >= 0; t2 -= 2) {
@@ -239,14 +266,18 @@ __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, S
 #pragma unroll
         for (int i = 1; i >= 0; --i) {
           const int t = t2 + i;
-          const Pair2 du = sm.du[buf][t][pr];
-          const f32x2 dyv = sm.dy[buf][t][pr];
-          const Pair2 b = *reinterpret_cast<const Pair2*>(&sm.B[buf][t][2 * nl]);
-          const Pair2 c = *reinterpret_cast<const Pair2*>(&sm.C[buf][t][2 * nl]);
-          dh[0] = fma2(dyv, c.a, dh[0]);
-          dh[1] = fma2(dyv, c.b, dh[1]);
-          const f32x2 b0 = mul2(dh[0], du.b), b1 = mul2(dh[1], du.b);
-          const f32x2 c0v = mul2(dyv, h[t + 1][0]), c1v = mul2(dyv, h[t + 1][1]);
+          const Pair2 du_t = du, b_t = b, c_t = c;
+          const f32x2 dy_t = dyv;
+          if (t > 0) {
+            du = sm.du[buf][t - 1][pr];
+            b = *reinterpret_cast<const Pair2*>(&sm.B[buf][t - 1][2 * nl]);
+            c = *reinterpret_cast<const Pair2*>(&sm.C[buf][t - 1][2 * nl]);
+            dyv = sm.dy[buf][t - 1][pr];
+          }
+          dh[0] = fma2(dy_t, c_t.a, dh[0]);
+          dh[1] = fma2(dy_t, c_t.b, dh[1]);
+          const f32x2 b0 = mul2(dh[0], du_t.b), b1 = mul2(dh[1], du_t.b);
+          const f32x2 c0v = mul2(dy_t, h[t + 1][0]), c1v = mul2(dy_t, h[t + 1][1]);
           float w[4] = {lo2(b0) + hi2(b0), lo2(b1) + hi2(b1), lo2(c0v) + hi2(c0v), lo2(c1v) + hi2(c1v)};
           using Chan = LaneSums<4, CL, ML>;  // over the warp's channel pairs
           Chan::run(w, cl);
@@ -257,13 +288,13 @@ __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, S
               sm.red[buf][warp][t][(vi >> 1) * N + 2 * nl + (vi & 1)] = w[v];
             }
           }
-          const f32x2 s1 = fma2(dh[0], b.a, mul2(dh[1], b.b));
+          const f32x2 s1 = fma2(dh[0], b_t.a, mul2(dh[1], b_t.b));
           dh[0] = mul2(dh[0], e[t][0]);
           dh[1] = mul2(dh[1], e[t][1]);
           const f32x2 l0 = mul2(dh[0], h[t][0]), l1 = mul2(dh[1], h[t][1]);
           const f32x2 s2 = fma2(l0, A1[0], mul2(l1, A1[1]));
-          dAt[0] = fma2(l0, du.a, dAt[0]);
-          dAt[1] = fma2(l1, du.a, dAt[1]);
+          dAt[0] = fma2(l0, du_t.a, dAt[0]);
+          dAt[1] = fma2(l1, du_t.a, dAt[1]);
           s[4 * i] = lo2(s1);
           s[4 * i + 1] = hi2(s1);
           s[4 * i + 2] = lo2(s2);
@@ -400,7 +431,8 @@ gdr_status gdr_ssm_bwd(const gdr_ssm_problem* p, const void* x, const void* dt, 
     using IT = decltype(it);
     cudaError_t r = ssm_states(d.N, [&](auto n) {
       constexpr int N = decltype(n)::value;
-      const size_t smem = sizeof(BwdSmem<N>);
+      constexpr size_t smem = sizeof(BwdSmem<IT, N>);
+      static_assert(smem <= 227 * 1024, "shared memory of a block");
       const cudaError_t se = set_smem_once((const void*)ssm_bwd_kernel<IT, N>, smem);
       if (se != cudaSuccess) return se;
       ssm_bwd_kernel<IT, N><<<dim3((unsigned)(d.G * blocks), (unsigned)rows), bwd_threads(N), smem, s>>>(d, a);
