@@ -1,11 +1,10 @@
 """The operators around the gated delta rule (C ABI in ``include/gdr_block.h``): the short causal
 convolution, the selective state space scan, the block norms and the single-token step.
 
-As in the package's main module the functions with a C name marshal arguments and return the
-status; the others check shapes, types and strides, allocate outputs and workspace and raise
-(``ValueError`` for what they find themselves, ``GDRError`` for a status).  Everything runs on the
-current stream, or on ``stream`` if one is given: outputs and workspace are then allocated on that
-stream, and the caller orders the inputs before it.
+The functions here check shapes, types and strides, allocate outputs and workspace and make the call
+(in ``csrc/gdr_binding.cpp``), and raise: ``ValueError`` for what they find themselves, ``GDRError`` for
+a status.  Everything runs on the current stream, or on ``stream`` if one is given: outputs and
+workspace are then allocated on that stream, and the caller orders the inputs before it.
 
     conv_forward, conv_backward, conv_step, causal_conv        (autograd)
     ssm_forward, ssm_backward, ssm_step, selective_scan        (autograd)
@@ -15,6 +14,9 @@ stream, and the caller orders the inputs before it.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 import sys
 
 import torch
@@ -70,19 +72,32 @@ def declare(lib, gdr_problem) -> None:
 
 
 _gdr = sys.modules[__package__]  # the package itself, which imports this module
+BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "gdr_binding.so")
+_module = _bound = None
 
 
-def _lib():
-    return _gdr._LIB or _gdr._lib_handle()
+def _binding():
+    """The torch binding, bound to the library that the package has open."""
+    global _module, _bound
+    lib = _gdr._LIB or _gdr._lib_handle()
+    if _bound is not lib:
+        if _module is None:
+            if not os.path.exists(BINDING_PATH):
+                raise ImportError(f"gdr_binding.so not built ({BINDING_PATH}); run `python -m {__package__}.build`")
+            loader = importlib.machinery.ExtensionFileLoader("gdr_binding", BINDING_PATH)
+            spec = importlib.util.spec_from_loader("gdr_binding", loader)
+            _module = importlib.util.module_from_spec(spec)
+            loader.exec_module(_module)
+        _module.bind({n: _c.cast(getattr(lib, n), _c.c_void_p).value for n in BLOCK_EXPORTS})
+        _bound = lib
+    return _module
 
 
-def _raise(status, where):
-    raise _gdr.GDRError(status, where)
-
-
-_CODE = {torch.float32: 0, torch.bfloat16: 1}
-_F32 = torch.float32
-_empty = torch.empty
+def _done(result, where):
+    """A call's outputs, or GDRError for the status in their place."""
+    if type(result) is int:
+        raise _gdr.GDRError(result, where)
+    return result
 
 
 def _on(stream):
@@ -90,107 +105,14 @@ def _on(stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
-# The current stream's handle.  torch.cuda.current_stream() builds an object for it (2.9 us on the
-# GPU's host, against 2.7 us for a whole launch through the library); the raw query takes 0.1 us.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-if _raw_stream is None:
-    def _raw_stream(device):
-        return torch.cuda.current_stream(device).cuda_stream
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
-
-
-def _need(cond, what):
-    if not cond:
-        raise ValueError(what)
-
-
-def _is(t, shape, dtype=_F32):
-    """Whether t is a contiguous CUDA tensor of a shape and type (None passes)."""
-    return t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda)
-
-
-def _act(name, t, shape, dtype):
-    """An activation of the call: on the GPU, of the call's type and shape."""
-    if t.shape != shape or t.dtype != dtype or not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-
-
-def _full(name, t, shape, dtype=torch.float32):
-    """A contiguous tensor of a given shape and type, or None."""
-    if not _is(t, shape, dtype):
-        raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)}, strides {t.stride()}, on {t.device}")
-
-
 def _ld(name, t, inner):
     """Token stride of a [B, T, ...inner] activation (0: contiguous); its rows must be contiguous and
     evenly spaced over the batch."""
-    if t.is_contiguous():
-        return 0
-    shape, st = t.shape, t.stride()
-    width = 1
-    for k in range(len(shape) - 1, len(shape) - 1 - inner, -1):
-        _need(shape[k] == 1 or st[k] == width, f"{name}: rows must be contiguous (strides {st})")
-        width *= shape[k]
-    lead = [k for k in range(len(shape) - inner) if shape[k] != 1]
-    if not lead:
-        return 0
-    ld = st[lead[-1]]
-    for a, b in zip(lead, lead[1:]):
-        _need(st[a] == st[b] * shape[b], f"{name}: the batch must be evenly strided (strides {st})")
-    _need(ld >= width, f"{name}: token stride {ld} below the row width {width}")
+    ld = _binding().stride(t, inner)
+    if ld < 0:
+        raise ValueError(f"{name}: rows must be contiguous and evenly spaced over the batch (shape {tuple(t.shape)}, "
+                         f"strides {t.stride()})")
     return ld
-
-
-def _seqs(cu_seqlens, B):
-    if cu_seqlens is None:
-        return B
-    if B == 1 and cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1 and cu_seqlens.is_contiguous():
-        n = cu_seqlens.numel()
-        if n >= 2 and cu_seqlens.is_cuda:
-            return n - 1
-    _need(cu_seqlens.dtype == torch.int32 and cu_seqlens.is_cuda and cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2
-          and cu_seqlens.is_contiguous(), "cu_seqlens: expected a contiguous CUDA int32 vector of at least 2 entries")
-    _need(B == 1, "cu_seqlens needs a batch of 1 (the packed tokens)")
-    return cu_seqlens.numel() - 1
-
-
-def _slots(slots, B):
-    if slots is not None and (slots.dtype != torch.int32 or slots.shape != (B,) or not slots.is_cuda
-                              or not slots.is_contiguous()):
-        raise ValueError(f"slots: expected a contiguous CUDA int32 vector of {B} entries")
-
-
-def _workspace(nbytes, device):
-    # torch's allocator returns 512-byte aligned blocks, which covers the 256-byte requirement
-    return _empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-
-
-def _type(x):
-    code = _CODE.get(x.dtype)
-    if code is None:
-        raise ValueError(f"dtype {x.dtype}: float32 or bfloat16")
-    return code
-
-
-_LAYOUT = {"KV": 0, "VK": 1}
-_I32 = torch.int32
-
-
-def _slots_ok(slots, n, B):
-    if slots is None:
-        return n >= B
-    return slots.dtype is _I32 and slots.shape == (B,) and slots.is_contiguous() and slots.is_cuda
-
-
-def _step_state(state, slots, B):
-    _slots(slots, B)
-    if slots is None and state.shape[0] < B:
-        raise ValueError(f"state: {state.shape[0]} states for {B} rows")
 
 
 # ---------------------------------------------------------------------------------- convolution
@@ -203,23 +125,6 @@ def _silu(activation):
     return _SILU[activation]
 
 
-def _conv_problem(x, weight, bias, cu_seqlens, activation, state, name, dy=None):
-    if x.dim() != 3:
-        raise ValueError(f"x: expected [B, T, C], got {tuple(x.shape)}")
-    B, T, C = x.shape
-    W = weight.shape[-1]
-    _act("x", x, (B, T, C), x.dtype)
-    _full("weight", weight, (C, W))
-    _full("bias", bias, (C,))
-    N = _seqs(cu_seqlens, B)
-    _full(name, state, (N, W - 1, C), x.dtype)
-    ld_dy = 0
-    if dy is not None:
-        _act("dy", dy, (B, T, C), x.dtype)
-        ld_dy = _ld("dy", dy, 1)
-    return gdr_conv_problem(B, T, C, W, N, _p(cu_seqlens), _type(x), _silu(activation), _ld("x", x, 1), ld_dy, 0)
-
-
 def conv_forward(x, weight, bias=None, initial_state=None, cu_seqlens=None, activation="silu", output_final_state=False,
                  stream=None):
     """Short causal depthwise convolution: x [B, T, C] (may be a slice of a wider tensor), weight
@@ -228,16 +133,8 @@ def conv_forward(x, weight, bias=None, initial_state=None, cu_seqlens=None, acti
     if stream is not None:
         with _on(stream):
             return conv_forward(x, weight, bias, initial_state, cu_seqlens, activation, output_final_state)
-    p = _conv_problem(x, weight, bias, cu_seqlens, activation, initial_state, "initial_state")
-    lib = _lib()
-    y = _empty(x.shape, dtype=x.dtype, device=x.device)
-    last = (_empty(p.num_seqs, p.W - 1, p.C, dtype=x.dtype, device=x.device) if output_final_state else None)
-    ws = _workspace(256 if cu_seqlens is not None else 0, x.device)
-    st = lib.gdr_conv_fwd(p, _p(x), _p(weight), _p(bias), _p(initial_state), _p(y), _p(last), _p(ws),
-                          256 if ws is not None else 0, _raw_stream(x.get_device()))
-    if st:
-        _raise(st, "gdr_conv_fwd")
-    return y, last
+    return _done(_binding().conv_forward(x, weight, bias, initial_state, cu_seqlens, _silu(activation), output_final_state),
+                 "gdr_conv_fwd")
 
 
 def conv_backward(x, weight, bias, dy, initial_state=None, dfinal_state=None, cu_seqlens=None, activation="silu",
@@ -246,20 +143,8 @@ def conv_backward(x, weight, bias, dy, initial_state=None, dfinal_state=None, cu
     if stream is not None:
         with _on(stream):
             return conv_backward(x, weight, bias, dy, initial_state, dfinal_state, cu_seqlens, activation)
-    p = _conv_problem(x, weight, bias, cu_seqlens, activation, initial_state, "initial_state", dy)
-    _full("dfinal_state", dfinal_state, (p.num_seqs, p.W - 1, p.C), x.dtype)
-    lib = _lib()
-    dx = _empty(x.shape, dtype=x.dtype, device=x.device)
-    dw = torch.empty_like(weight)
-    db = torch.empty_like(bias) if bias is not None else None
-    dstate = torch.empty_like(initial_state) if initial_state is not None else None
-    n = lib.gdr_conv_bwd_workspace_bytes(p)
-    ws = _workspace(n, x.device)
-    st = lib.gdr_conv_bwd(p, _p(x), _p(weight), _p(bias), _p(initial_state), _p(dy), _p(dfinal_state), _p(dx),
-                          _p(dw), _p(db), _p(dstate), _p(ws), n, _raw_stream(x.get_device()))
-    if st:
-        _raise(st, "gdr_conv_bwd")
-    return dx, dw, db, dstate
+    return _done(_binding().conv_backward(x, weight, bias, dy, initial_state, dfinal_state, cu_seqlens, _silu(activation)),
+                 "gdr_conv_bwd")
 
 
 def conv_step(x, state, weight, bias=None, slots=None, activation="silu", stream=None):
@@ -269,30 +154,7 @@ def conv_step(x, state, weight, bias=None, slots=None, activation="silu", stream
     if stream is not None:
         with _on(stream):
             return conv_step(x, state, weight, bias, slots, activation)
-    dtype = x.dtype
-    B, C = x.shape
-    n, W, c = state.shape
-    W += 1
-    ld = 0
-    # the usual call passes here; anything else is named by the checks
-    if not (c == C and state.dtype is dtype and weight.dtype is _F32 and weight.shape == (C, W) and x.is_contiguous()
-            and state.is_contiguous() and weight.is_contiguous() and x.is_cuda and state.is_cuda and weight.is_cuda
-            and dtype in _CODE and (bias is None or _is(bias, (C,))) and _slots_ok(slots, n, B) and activation in _SILU):
-        _act("x", x, (B, C), dtype)
-        _full("weight", weight, (C, W))
-        _full("bias", bias, (C,))
-        _full("state", state, (n, W - 1, C), dtype)
-        _step_state(state, slots, B)
-        _type(x)
-        _silu(activation)
-        ld = _ld("x", x, 1)
-    p = gdr_conv_problem(B, 1, C, W, B, None, _CODE[dtype], _SILU[activation], ld, 0, n)
-    y = _empty((B, C), dtype=dtype, device=x.device) if ld else torch.empty_like(x)
-    st = _lib().gdr_conv_step(p, x.data_ptr(), weight.data_ptr(), _p(bias), state.data_ptr(), _p(slots), y.data_ptr(),
-                              _raw_stream(x.get_device()))
-    if st:
-        _raise(st, "gdr_conv_step")
-    return y
+    return _done(_binding().conv_step(x, state, weight, bias, slots, _silu(activation)), "gdr_conv_step")
 
 
 class _ConvFunction(torch.autograd.Function):
@@ -314,11 +176,7 @@ class _ConvFunction(torch.autograd.Function):
 
 def _rows_ok(t, inner):
     """t if a call can take its strides, else a contiguous copy."""
-    try:
-        _ld("", t, inner)
-        return t
-    except ValueError:
-        return t.contiguous()
+    return t if _binding().stride(t, inner) >= 0 else t.contiguous()
 
 
 def causal_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, activation="silu"):
@@ -329,26 +187,6 @@ def causal_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, activ
 
 
 # ------------------------------------------------------------------------------- selective scan
-def _ssm_problem(x, dt, A, Bm, Cm, Dskip, dt_bias, cu_seqlens, dt_softplus, dy=None):
-    if x.dim() != 3 or Bm.dim() != 4:
-        raise ValueError(f"expected x [B, T, D] and Bm, Cm [B, T, G, N], got {tuple(x.shape)} and {tuple(Bm.shape)}")
-    B, T, D = x.shape
-    G, N = Bm.shape[2], Bm.shape[3]
-    _act("x", x, (B, T, D), x.dtype)
-    _act("dt", dt, (B, T, D), x.dtype)
-    _act("Bm", Bm, (B, T, G, N), x.dtype)
-    _act("Cm", Cm, (B, T, G, N), x.dtype)
-    _full("A", A, (D, N))
-    _full("D", Dskip, (D,))
-    _full("dt_bias", dt_bias, (D,))
-    ld_dy = 0
-    if dy is not None:
-        _act("dy", dy, (B, T, D), x.dtype)
-        ld_dy = _ld("dy", dy, 1)
-    return gdr_ssm_problem(B, T, D, N, G, _seqs(cu_seqlens, B), _p(cu_seqlens), _type(x), int(bool(dt_softplus)),
-                           _ld("x", x, 1), _ld("dt", dt, 1), _ld("Bm", Bm, 2), _ld("Cm", Cm, 2), ld_dy, 0)
-
-
 def ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, cu_seqlens=None, dt_softplus=True,
                 output_final_state=True, save=True, stream=None):
     """Selective state space scan: x, dt [B, T, D], A [D, N] fp32, Bm, Cm [B, T, G, N], D and dt_bias
@@ -357,21 +195,8 @@ def ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, cu_seqlens=None
     if stream is not None:
         with _on(stream):
             return ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus, output_final_state, save)
-    p = _ssm_problem(x, dt, A, Bm, Cm, D, dt_bias, cu_seqlens, dt_softplus)
-    _full("S0", S0, (p.num_seqs, p.D, p.N))
-    lib = _lib()
-    y = _empty(x.shape, dtype=x.dtype, device=x.device)
-    S_T = _empty((p.num_seqs, p.D, p.N), dtype=torch.float32, device=x.device) if output_final_state else None
-    saved = None
-    if save:
-        saved = _empty(lib.gdr_ssm_saved_bytes(p) // 4, dtype=torch.float32, device=x.device)
-    n = lib.gdr_ssm_fwd_workspace_bytes(p)
-    ws = _workspace(n, x.device)
-    st = lib.gdr_ssm_fwd(p, _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(S0), _p(y), _p(S_T),
-                         _p(saved), _p(ws), n, _raw_stream(x.get_device()))
-    if st:
-        _raise(st, "gdr_ssm_fwd")
-    return y, S_T, saved
+    return _done(_binding().ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, bool(dt_softplus), output_final_state,
+                                        save), "gdr_ssm_fwd")
 
 
 def ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D=None, dt_bias=None, dS_T=None, cu_seqlens=None, dt_softplus=True,
@@ -380,27 +205,8 @@ def ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D=None, dt_bias=None, dS_T=None,
     if stream is not None:
         with _on(stream):
             return ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D, dt_bias, dS_T, cu_seqlens, dt_softplus, want_dS0)
-    p = _ssm_problem(x, dt, A, Bm, Cm, D, dt_bias, cu_seqlens, dt_softplus, dy)
-    _full("dS_T", dS_T, (p.num_seqs, p.D, p.N))
-    lib = _lib()
-    need = lib.gdr_ssm_saved_bytes(p) // 4
-    if h_saved is None or h_saved.dtype != _F32 or not h_saved.is_contiguous() or h_saved.numel() < need:
-        raise ValueError(f"h_saved: expected the {need} floats that ssm_forward kept (save=True)")
-    f32 = torch.float32
-    dx, ddt = (_empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
-    dB, dC = (_empty(Bm.shape, dtype=x.dtype, device=x.device) for _ in range(2))
-    dA = torch.empty_like(A)
-    dD = torch.empty_like(D) if D is not None else None
-    dbias = torch.empty_like(dt_bias) if dt_bias is not None else None
-    dS0 = _empty((p.num_seqs, p.D, p.N), dtype=f32, device=x.device) if want_dS0 else None
-    n = lib.gdr_ssm_bwd_workspace_bytes(p)
-    ws = _workspace(n, x.device)
-    st = lib.gdr_ssm_bwd(p, _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(dt_bias), _p(h_saved), _p(dy),
-                         _p(dS_T), _p(dx), _p(ddt), _p(dA), _p(dB), _p(dC), _p(dD), _p(dbias), _p(dS0), _p(ws), n,
-                         _raw_stream(x.get_device()))
-    if st:
-        _raise(st, "gdr_ssm_bwd")
-    return dx, ddt, dA, dB, dC, dD, dbias, dS0
+    return _done(_binding().ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D, dt_bias, dS_T, cu_seqlens, bool(dt_softplus),
+                                         want_dS0), "gdr_ssm_bwd")
 
 
 def ssm_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, slots=None, dt_softplus=True, stream=None):
@@ -409,34 +215,7 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, slots=None, dt_softp
     if stream is not None:
         with _on(stream):
             return ssm_step(x, dt, A, Bm, Cm, state, D, dt_bias, slots, dt_softplus)
-    dtype = x.dtype
-    B, d = x.shape
-    _, G, N = Bm.shape
-    n = state.shape[0]
-    lds = (0, 0, 0, 0)
-    if not (dt.dtype is dtype and Bm.dtype is dtype and Cm.dtype is dtype and dt.shape == (B, d) and Bm.shape == (B, G, N)
-            and Cm.shape == (B, G, N) and x.is_contiguous() and dt.is_contiguous() and Bm.is_contiguous()
-            and Cm.is_contiguous() and x.is_cuda and dt.is_cuda and Bm.is_cuda and Cm.is_cuda and dtype in _CODE
-            and _is(A, (d, N)) and _is(state, (n, d, N)) and (D is None or _is(D, (d,)))
-            and (dt_bias is None or _is(dt_bias, (d,))) and _slots_ok(slots, n, B)):
-        _act("x", x, (B, d), dtype)
-        _act("dt", dt, (B, d), dtype)
-        _act("Bm", Bm, (B, G, N), dtype)
-        _act("Cm", Cm, (B, G, N), dtype)
-        _full("A", A, (d, N))
-        _full("D", D, (d,))
-        _full("dt_bias", dt_bias, (d,))
-        _full("state", state, (n, d, N))
-        _step_state(state, slots, B)
-        _type(x)
-        lds = (_ld("x", x, 1), _ld("dt", dt, 1), _ld("Bm", Bm, 2), _ld("Cm", Cm, 2))
-    p = gdr_ssm_problem(B, 1, d, N, G, B, None, _CODE[dtype], 1 if dt_softplus else 0, *lds, 0, n)
-    y = _empty((B, d), dtype=dtype, device=x.device)
-    st = _lib().gdr_ssm_step(p, x.data_ptr(), dt.data_ptr(), A.data_ptr(), Bm.data_ptr(), Cm.data_ptr(), _p(D), _p(dt_bias),
-                             state.data_ptr(), _p(slots), y.data_ptr(), _raw_stream(x.get_device()))
-    if st:
-        _raise(st, "gdr_ssm_step")
-    return y
+    return _done(_binding().ssm_step(x, dt, A, Bm, Cm, state, D, dt_bias, slots, bool(dt_softplus)), "gdr_ssm_step")
 
 
 class _SSMFunction(torch.autograd.Function):
@@ -467,37 +246,6 @@ def selective_scan(x, dt, A, Bm, Cm, D=None, dt_bias=None, initial_state=None, c
 
 
 # ---------------------------------------------------------------------------------- block norms
-def _norm_rows(x, gate):
-    """(tokens, heads, ld_x, ld_gate): rows are the last dimension; a tensor of heads may be a slice
-    of a wider one (its tokens strided, its heads side by side)."""
-    D = x.shape[-1]
-    if (x.is_contiguous()) and (gate is None or gate.is_contiguous()):
-        return x.numel() // D if D else 0, 1, 0, 0
-    err = None
-    for inner in (1, 2) if x.dim() > 2 else (1,):
-        heads = 1 if inner == 1 else x.shape[-2]
-        try:
-            ld = [0 if t is None else _ld(n, t, inner) for n, t in (("x", x), ("gate", gate))]
-            return x.numel() // (D * heads), heads, ld[0], ld[1]
-        except ValueError as e:
-            err = e
-    raise err
-
-
-def _norm_problem(x, post_weight, gate, scale, pre_weight, stream_dtype, eps):
-    D = x.shape[-1]
-    _act("x", x, x.shape, x.dtype)
-    if gate is not None:
-        _act("gate", gate, x.shape, x.dtype)
-    _full("post_weight", post_weight, (D,))
-    _full("scale", scale, (D,))
-    _full("pre_weight", pre_weight, (D,))
-    tokens, heads, ld_x, ld_gate = _norm_rows(x, gate)
-    if stream_dtype not in _CODE:
-        raise ValueError(f"residual dtype {stream_dtype}: float32 or bfloat16")
-    return gdr_norm_problem(tokens, heads, D, _type(x), _CODE[stream_dtype], eps, ld_x, ld_gate)
-
-
 def norm_forward(x, post_weight=None, gate=None, scale=None, residual=None, pre_weight=None, eps=1e-6, stream=None):
     """u = x [rstd(x) post_weight] [silu(gate)] [scale]; r = [residual +] u; y = r rstd(r) pre_weight.
     Rows are the last dimension.  Returns (r, y): r in the residual's dtype (fp32 or x's), or in x's
@@ -506,29 +254,7 @@ def norm_forward(x, post_weight=None, gate=None, scale=None, residual=None, pre_
     if stream is not None:
         with _on(stream):
             return norm_forward(x, post_weight, gate, scale, residual, pre_weight, eps)
-    dtype, shape = x.dtype, x.shape
-    res_dtype = dtype if residual is None else residual.dtype
-    D = shape[-1]
-    if (x.is_contiguous() and x.is_cuda and dtype in _CODE and res_dtype in _CODE and D > 0
-            and (gate is None or _is(gate, shape, dtype)) and (residual is None or _is(residual, shape, res_dtype))
-            and (post_weight is None or _is(post_weight, (D,))) and (scale is None or _is(scale, (D,)))
-            and (pre_weight is None or _is(pre_weight, (D,)))):
-        p = gdr_norm_problem(x.numel() // D, 1, D, _CODE[dtype], _CODE[res_dtype], eps, 0, 0)
-    else:
-        p = _norm_problem(x, post_weight, gate, scale, pre_weight, res_dtype, eps)
-        _full("residual", residual, shape, res_dtype)
-    r = y = None
-    if residual is not None:
-        r = torch.empty_like(residual)
-    elif pre_weight is None:
-        r = _empty(shape, dtype=dtype, device=x.device)
-    if pre_weight is not None:
-        y = _empty(shape, dtype=dtype, device=x.device)
-    st = _lib().gdr_norm_fwd(p, x.data_ptr(), _p(post_weight), _p(gate), _p(scale), _p(residual), _p(pre_weight), _p(r), _p(y),
-                             _raw_stream(x.get_device()))
-    if st:
-        _raise(st, "gdr_norm_fwd")
-    return r, y
+    return _done(_binding().norm_forward(x, post_weight, gate, scale, residual, pre_weight, eps), "gdr_norm_fwd")
 
 
 def norm_backward(x, post_weight=None, gate=None, scale=None, r=None, pre_weight=None, dr=None, dy=None, eps=1e-6,
@@ -539,31 +265,7 @@ def norm_backward(x, post_weight=None, gate=None, scale=None, r=None, pre_weight
     if stream is not None:
         with _on(stream):
             return norm_backward(x, post_weight, gate, scale, r, pre_weight, dr, dy, eps)
-    has_residual = r is not None
-    res_dtype = r.dtype if has_residual else x.dtype
-    p = _norm_problem(x, post_weight, gate, scale, pre_weight, res_dtype, eps)
-    _full("r", r, x.shape, res_dtype)
-    _full("dr", dr, x.shape, res_dtype)
-    _full("dy", dy, x.shape, x.dtype)
-    if not has_residual and pre_weight is not None:
-        _need(x.is_contiguous(), "x: a plain norm's backward needs a contiguous x")
-    lib = _lib()
-
-    def new(like, dtype=None):
-        return None if like is None else _empty(like.shape, dtype=dtype or like.dtype, device=x.device)
-
-    dx, dgate = new(x), new(gate)
-    dres = new(x, res_dtype) if has_residual else None
-    dpost, dscale, dpre = new(post_weight), new(scale), new(pre_weight)
-    n = lib.gdr_norm_bwd_workspace_bytes(p)
-    ws = _workspace(n, x.device)
-    rr = r if has_residual else (x if pre_weight is not None else None)
-    st = lib.gdr_norm_bwd(p, _p(x), _p(post_weight), _p(gate), _p(scale), _p(rr), _p(pre_weight),
-                          int(has_residual), _p(dr), _p(dy), _p(dx), _p(dgate), _p(dres), _p(dpost), _p(dscale), _p(dpre),
-                          _p(ws), n, _raw_stream(x.get_device()))
-    if st:
-        _raise(st, "gdr_norm_bwd")
-    return dx, dgate, dres, dpost, dscale, dpre
+    return _done(_binding().norm_backward(x, post_weight, gate, scale, r, pre_weight, dr, dy, eps), "gdr_norm_bwd")
 
 
 class _NormFunction(torch.autograd.Function):
@@ -598,6 +300,9 @@ def block_norm(x, post_weight=None, gate=None, scale=None, residual=None, pre_we
 
 
 # ----------------------------------------------------------------- the delta rule, one token each
+_LAYOUT = {"KV": 0, "VK": 1}
+
+
 def step(q, k, v, g, beta, state, layout="KV", scale=None, slots=None, prologue=0, stream=None):
     """The gated delta rule for one token per row: q, k [B, Hk, DK], v [B, Hv, DV], g [B, Hv] fp32,
     beta [B, Hv]; state, a pool [num_slots, Hv, DK, DV] ("KV") or [num_slots, Hv, DV, DK] ("VK") fp32,
@@ -606,28 +311,7 @@ def step(q, k, v, g, beta, state, layout="KV", scale=None, slots=None, prologue=
     if stream is not None:
         with _on(stream):
             return step(q, k, v, g, beta, state, layout, scale, slots, prologue)
-    dtype = q.dtype
-    B, Hk, DK = q.shape
-    Hv, DV = v.shape[1:]
-    n = state.shape[0]
-    if not (_is(q, (B, Hk, DK), dtype) and _is(k, (B, Hk, DK), dtype) and _is(v, (B, Hv, DV), dtype) and _is(g, (B, Hv))
-            and _is(beta, (B, Hv), dtype) and layout in _LAYOUT and dtype in _CODE and _slots_ok(slots, n, B)
-            and _is(state, (n, Hv, DK, DV) if layout == "KV" else (n, Hv, DV, DK))):
-        if layout not in _LAYOUT:
-            raise ValueError(f"layout {layout!r}: 'KV' or 'VK'")
-        _type(q)
-        _full("q", q, (B, Hk, DK), dtype)
-        _full("k", k, (B, Hk, DK), dtype)
-        _full("v", v, (B, Hv, DV), dtype)
-        _full("g", g, (B, Hv))
-        _full("beta", beta, (B, Hv), dtype)
-        _full("state", state, (n, Hv, DK, DV) if layout == "KV" else (n, Hv, DV, DK))
-        _step_state(state, slots, B)
-    p = _gdr.gdr_problem(B, 1, Hk, Hv, DK, DV, B, None, _CODE[dtype], _LAYOUT[layout], 0.0 if scale is None else scale, 0,
-                         prologue, 0, 1, 1)
-    o = torch.empty_like(v)
-    st = _lib().gdr_step(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), n,
-                         _p(slots), o.data_ptr(), _raw_stream(q.get_device()))
-    if st:
-        _raise(st, "gdr_step")
-    return o
+    if layout not in _LAYOUT:
+        raise ValueError(f"layout {layout!r}: 'KV' or 'VK'")
+    return _done(_binding().step(q, k, v, g, beta, state, _LAYOUT[layout], 0.0 if scale is None else scale, slots, prologue),
+                 "gdr_step")

@@ -1,4 +1,5 @@
-"""Build libgdr.so in-tree: every csrc/*.cu compiled for sm_103a only, in parallel, then linked.
+"""Build libgdr.so in-tree: every csrc/*.cu compiled for sm_103a only, in parallel, then linked; and
+gdr_binding.so, the torch binding of the block operators (csrc/gdr_binding.cpp, g++).
 
     python -m chunked_gated_delta_04_gb300.build [--force] [--delay]
 
@@ -24,6 +25,8 @@ LIB = os.path.join(PKG, "libgdr.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 DELAY_LIB = os.path.join(PKG, "libgdr_delay.so")
 DELAY_BUILD_DIR = os.path.join(PKG, "_build_delay")
+BINDING = os.path.join(PKG, "gdr_binding.so")
+BINDING_SRC = os.path.join(CSRC, "gdr_binding.cpp")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -69,10 +72,49 @@ def up_to_date(delay: bool = False) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _binding_flags() -> list:
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return (["-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+            + [f for i in inc for f in ("-isystem", i)]
+            + ["-L" + os.path.join(root, "lib"), "-Wl,-rpath," + os.path.join(root, "lib")])
+
+
+def build_binding(force: bool = False) -> str:
+    """Builds gdr_binding.so for the torch that is installed unless it is up to date; returns its path."""
+    import torch
+
+    flags = _binding_flags()
+    stamp, stamp_path = " ".join([torch.__version__] + flags), BINDING + ".flags"
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "gdr.h"), os.path.join(INCLUDE, "gdr_block.h")]
+    if not force and os.path.exists(BINDING) and os.path.exists(stamp_path):
+        with open(stamp_path) as f:
+            if f.read() == stamp and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+                return BINDING
+    tmp = BINDING + f".tmp{os.getpid()}"
+    r = subprocess.run(["g++"] + flags + [BINDING_SRC, "-o", tmp, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    with open(stamp_path, "w") as f:
+        f.write(stamp)
+    return BINDING
+
+
 def build(force: bool = False, delay: bool = False, verbose: bool = False) -> str:
-    """Builds libgdr.so (or, with delay, libgdr_delay.so) unless it is up to date; returns its path."""
+    """Builds libgdr.so and gdr_binding.so (or, with delay, libgdr_delay.so) unless they are up to date;
+    returns the library's path."""
     lib, build_dir, stamp_path = _target(delay)
     if not force and up_to_date(delay):
+        if not delay:
+            build_binding()
         return lib
     nvcc = nvcc_path()
     os.makedirs(build_dir, exist_ok=True)
@@ -90,7 +132,10 @@ def build(force: bool = False, delay: bool = False, verbose: bool = False) -> st
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = None if delay else ex.submit(build_binding, force)
         results = list(ex.map(compile_one, _sources()))
+        if binding is not None:
+            binding.result()
     if verbose:
         for _, err in results:
             print(err)

@@ -377,7 +377,7 @@ int ssm_bwd_channels(int N) { return 2 * bwd_threads(N) / (N / 2); }
 
 int ssm_bwd_rows(const SsmDims& d) {
   const int cb = ssm_bwd_channels(d.N);
-  const long long blocks = (long long)d.G * ((d.Dg + cb - 1) / cb), most = (4 * kSmCount + blocks - 1) / blocks;
+  const long long blocks = (long long)d.G * ((d.Dg + cb - 1) / cb), most = (8 * kSmCount + blocks - 1) / blocks;
   const long long rows = d.max_units < most ? d.max_units : most;
   return (int)(rows < 1 ? 1 : rows);
 }
