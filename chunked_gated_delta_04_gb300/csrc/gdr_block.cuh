@@ -153,6 +153,14 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int num_seqs, long long
   return lo;
 }
 
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// Copies `bytes` (4, 8 or 16; the rest of a Bytes-wide destination is zeros) without passing registers.
+template <int Bytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src), "n"(Bytes), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 inline size_t block_align(size_t x) { return (x + 255) & ~(size_t)255; }
 inline bool vec_ok(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 inline bool elem_ok(const void* p, size_t el) { return ((uintptr_t)p & (el - 1)) == 0; }

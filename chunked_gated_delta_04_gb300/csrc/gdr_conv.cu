@@ -449,37 +449,46 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvDims d, const
   }
 }
 
-template <typename IT, int V, int W>
+// V channels of R rows per thread: the taps are read once for them.
+template <typename IT, int V, int W, int R>
 __global__ void __launch_bounds__(kThreads) conv_step_kernel(int B, int C, long long ld_x, int silu, int num_slots,
                                                              const IT* __restrict__ x, const float* __restrict__ w,
                                                              const float* __restrict__ bias, IT* __restrict__ pool,
                                                              const int32_t* __restrict__ slots,
                                                              IT* __restrict__ y) {
-  const int ncg = C / V;
-  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x, b = id / ncg;
-  if (b >= B) return;
-  const long long c = (id - b * ncg) * V;
-  const long long slot = slots ? slots[b] : b;
   constexpr int P = kPairs<V>;
-  f32x2 pre[P] = {};
-  if (slot < 0 || slot >= num_slots) {
-    store_row<V>(y + b * C + c, pre);
-    return;
-  }
-  IT* st = pool + slot * (W - 1) * C + c;
-  Raw<IT, V> r[W];
+  const long long c = ((long long)blockIdx.x * kThreads + threadIdx.x) * V;
+  if (c >= C) return;
+  const int b0 = blockIdx.y * R;
+  Raw<IT, V> r[R][W];
+  IT* st[R];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) r[j].load(st + (long long)j * C);
-  r[W - 1].load(x + b * ld_x + c);
-  f32x2 win[W][P], wt[W][P], bs[P];
+  for (int i = 0; i < R; ++i) {
+    const int b = b0 + i, slot = b < B ? (slots ? slots[b] : b) : -1;
+    st[i] = slot >= 0 && slot < num_slots ? pool + (long long)slot * (W - 1) * C + c : nullptr;
+    if (st[i]) {
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) r[i][j].load(st[i] + (long long)j * C);
+      r[i][W - 1].load(x + b * ld_x + c);
+    }
+  }
+  f32x2 wt[W][P], bs[P];
   load_taps<V, W>(w, bias, c, wt, bs);
 #pragma unroll
-  for (int j = 0; j < W; ++j) r[j].get(win[j]);
+  for (int i = 0; i < R; ++i) {
+    if (b0 + i >= B) return;
+    f32x2 pre[P] = {};
+    if (st[i]) {
+      f32x2 win[W][P];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) store_row<V>(st + (long long)j * C, win[j + 1]);
-  taps<V, W>(win, wt, bs, pre);
-  if (silu) silu_row<V>(pre);
-  store_row<V>(y + b * C + c, pre);
+      for (int j = 0; j < W; ++j) r[i][j].get(win[j]);
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) store_row<V>(st[i] + (long long)j * C, win[j + 1]);
+      taps<V, W>(win, wt, bs, pre);
+      if (silu) silu_row<V>(pre);
+    }
+    store_row<V>(y + (long long)(b0 + i) * C + c, pre);
+  }
 }
 
 gdr_status resolve_conv(const gdr_conv_problem* p, bool step, ConvDims* d) {
@@ -662,12 +671,16 @@ gdr_status gdr_conv_step(const gdr_conv_problem* p, const void* x, const float* 
   cudaStream_t s = (cudaStream_t)stream;
   stage_begin(s);
   const bool vec = d.C % 8 == 0 && d.ld_x % 8 == 0 && vec_ok(x) && vec_ok(y) && vec_ok(pool) && vec_ok(w);
-  const long long grid = (d.total * (vec ? d.C / kFwdVec : d.C) + kThreads - 1) / kThreads;
-  if (grid >= (1ll << 31)) return GDR_ERR_UNSUPPORTED;
+  const int ncg = vec ? d.C / kFwdVec : d.C, gx = (ncg + kThreads - 1) / kThreads;
+  const bool four = (long long)gx * ((p->B + 3) / 4) >= 2 * kSmCount;  // rows enough to keep every SM busy
+  const int rows = four ? 4 : 1;
+  if ((p->B + rows - 1) / rows > 65535) return GDR_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)gx, (unsigned)((p->B + rows - 1) / rows));
   return status_of(by_type<kFwdVec>(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
     using IT = decltype(it);
-    conv_step_kernel<IT, decltype(v)::value, decltype(wd)::value><<<(unsigned)grid, kThreads, 0, s>>>(
-        p->B, d.C, d.ld_x, d.silu, p->num_slots, (const IT*)x, w, bias, (IT*)pool, slots, (IT*)y);
+    constexpr int V = decltype(v)::value, W = decltype(wd)::value;
+    const auto kernel = four ? conv_step_kernel<IT, V, W, 4> : conv_step_kernel<IT, V, W, 1>;
+    kernel<<<grid, kThreads, 0, s>>>(p->B, d.C, d.ld_x, d.silu, p->num_slots, (const IT*)x, w, bias, (IT*)pool, slots, (IT*)y);
     stage_mark(s, "conv_step");
     return cudaGetLastError();
   }));

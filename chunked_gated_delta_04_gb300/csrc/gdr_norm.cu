@@ -19,7 +19,7 @@ struct FwdPtrs {
 };
 
 // A block walks rows and has the next ones' loads in flight while it works on the present ones.
-template <typename IT, typename RT, int TPR, int K, int PARTS>
+template <typename IT, typename RT, int TPR, int K, int PARTS, bool SIDE>
 __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(NormDims d, FwdPtrs a) {
   constexpr int kRows = norm_rows(TPR);
   __shared__ float red[TPR > 32 ? 2 * TPR / 32 : 1];
@@ -40,10 +40,9 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(NormDims d, F
     const long long tok = row / d.heads, at = (row - tok * d.heads) * d.D;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = 8 * (k * TPR + i0);
-      o.x[k] = load_raw8((const IT*)a.x + tok * d.ld_x + at, c, D, d.vec);
-      if (gate) o.z[k] = load_raw8((const IT*)a.gate + tok * d.ld_gate + at, c, D, d.vec);
-      if (res) o.res[k] = load_raw8((const RT*)a.residual + row * d.D, c, D, d.vec);
+      o.x[k] = load_raw8<TPR, SIDE>((const IT*)a.x + tok * d.ld_x + at, k, i0, D, d.vec);
+      if (gate) o.z[k] = load_raw8<TPR, SIDE>((const IT*)a.gate + tok * d.ld_gate + at, k, i0, D, d.vec);
+      if (res) o.res[k] = load_raw8<TPR, SIDE>((const RT*)a.residual + row * d.D, k, i0, D, d.vec);
     }
   };
   // rows of a block run together (barriers): the loop's trip count is the block's
@@ -68,7 +67,7 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(NormDims d, F
       const float rs = rsqrtf(s[0] * inv + d.eps);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        load_raw8(a.w_post, 8 * (k * TPR + i0), D, d.vec).get(t);
+        load_raw8<TPR, SIDE>(a.w_post, k, i0, D, d.vec).get(t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[k][i] *= rs * t[i];
       }
@@ -84,7 +83,7 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(NormDims d, F
     if (scale) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        load_raw8(a.scale, 8 * (k * TPR + i0), D, d.vec).get(t);
+        load_raw8<TPR, SIDE>(a.scale, k, i0, D, d.vec).get(t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[k][i] *= t[i];
       }
@@ -95,11 +94,11 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(NormDims d, F
         cur.res[k].get(t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) u[k][i] = to_f32(from_f32<RT>(u[k][i] + t[i]));
-        store8((RT*)a.r + row * d.D, 8 * (k * TPR + i0), D, d.vec, u[k]);
+        store8<TPR, SIDE>((RT*)a.r + row * d.D, k, i0, D, d.vec, u[k]);
       }
     } else if (!pre) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) store8((IT*)a.r + row * d.D, 8 * (k * TPR + i0), D, d.vec, u[k]);
+      for (int k = 0; k < K; ++k) store8<TPR, SIDE>((IT*)a.r + row * d.D, k, i0, D, d.vec, u[k]);
     }
     if (pre) {
       float s[1] = {0.f};
@@ -111,10 +110,10 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(NormDims d, F
       const float rs = rsqrtf(s[0] * inv + d.eps);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        load_raw8(a.w_pre, 8 * (k * TPR + i0), D, d.vec).get(t);
+        load_raw8<TPR, SIDE>(a.w_pre, k, i0, D, d.vec).get(t);
 #pragma unroll
         for (int i = 0; i < 8; ++i) t[i] *= u[k][i] * rs;
-        store8((IT*)a.y + row * d.D, 8 * (k * TPR + i0), D, d.vec, t);
+        store8<TPR, SIDE>((IT*)a.y + row * d.D, k, i0, D, d.vec, t);
       }
     }
     cur = next;
@@ -172,12 +171,14 @@ extern "C" gdr_status gdr_norm_fwd(const gdr_norm_problem* p, const void* x, con
     return norm_shape(d.D, [&](auto tpr, auto k) {
       constexpr int TPR = decltype(tpr)::value, K = decltype(k)::value;
       return norm_parts(parts, [&](auto pt) {
-        constexpr auto kernel = norm_fwd_kernel<IT, RT, TPR, K, decltype(pt)::value>;
-        static const long long most = (long long)kSmCount * resident_blocks(kernel, norm_block(TPR));
-        const long long want = (d.rows + norm_rows(TPR) - 1) / norm_rows(TPR);
-        kernel<<<(unsigned)(want < most ? want : most), norm_block(TPR), 0, s>>>(d, a);
-        stage_mark(s, "norm_fwd");
-        return cudaGetLastError();
+        return norm_side<TPR>(d.vec, [&](auto side) {
+          constexpr auto kernel = norm_fwd_kernel<IT, RT, TPR, K, decltype(pt)::value, decltype(side)::value>;
+          static const long long most = (long long)kSmCount * resident_blocks(kernel, norm_block(TPR));
+          const long long want = (d.rows + norm_rows(TPR) - 1) / norm_rows(TPR);
+          kernel<<<(unsigned)(want < most ? want : most), norm_block(TPR), 0, s>>>(d, a);
+          stage_mark(s, "norm_fwd");
+          return cudaGetLastError();
+        });
       });
     });
   };

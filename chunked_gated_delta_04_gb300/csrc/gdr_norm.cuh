@@ -1,7 +1,8 @@
 // gdr_norm.cuh -- row layout of the block norms' kernels (gdr_norm.cu, gdr_norm_bwd*.cu).
 //
-// TPR threads hold a row of D channels in registers, K chunks of 8 channels each (chunk k of
-// thread i: channels 8 (k TPR + i) ..).  Up to 32 threads share a warp and reduce by shuffles;
+// TPR threads hold a row of D channels in registers, K chunks of 8 channels each: chunk k of thread i
+// is channels 8 (k TPR + i) .., or, in the kernels for rows that do not take 16-byte accesses and fill
+// a block (SIDE), channels (8 k + j) TPR + i for j < 8, so that a warp's single loads lie side by side.  Up to 32 threads share a warp and reduce by shuffles;
 // more are a block of their own.
 #pragma once
 
@@ -44,46 +45,51 @@ struct Raw8<__nv_bfloat16> {
     }
   }
 };
-// Channels c .. c + 7 of a row of D (zeros past its end).
-template <typename IT>
-__device__ __forceinline__ Raw8<IT> load_raw8(const IT* p, int c, int D, int vec) {
+// Channel of element j of chunk k.
+template <int TPR, bool SIDE>
+__device__ __forceinline__ int channel(int k, int i0, int j) {
+  return SIDE ? (8 * k + j) * TPR + i0 : 8 * (k * TPR + i0) + j;
+}
+// Chunk k of a row of D channels (zeros past its end); vec: in 16-byte accesses.
+template <int TPR, bool SIDE, typename IT>
+__device__ __forceinline__ Raw8<IT> load_raw8(const IT* p, int k, int i0, int D, int vec) {
   Raw8<IT> r;
-  if constexpr (sizeof(IT) == 4) {
-    r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (vec) {
+  if (!SIDE && vec) {
+    const int c = channel<TPR, SIDE>(k, i0, 0);
+    if constexpr (sizeof(IT) == 4) {
+      r.a = r.b = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c < D) {
         r.a = *reinterpret_cast<const float4*>(p + c);
         r.b = *reinterpret_cast<const float4*>(p + c + 4);
       }
     } else {
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c + i < D ? p[c + i] : 0.f;
-      r.a = make_float4(v[0], v[1], v[2], v[3]);
-      r.b = make_float4(v[4], v[5], v[6], v[7]);
-    }
-  } else {
-    r.w = make_uint4(0, 0, 0, 0);
-    if (vec) {
+      r.w = make_uint4(0, 0, 0, 0);
       if (c < D) r.w = *reinterpret_cast<const uint4*>(p + c);
-    } else {
-      const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
-      uint32_t v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c + i < D ? q[c + i] : 0;
-      r.w = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
+  } else if constexpr (sizeof(IT) == 4) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = channel<TPR, SIDE>(k, i0, j) < D ? p[channel<TPR, SIDE>(k, i0, j)] : 0.f;
+    r.a = make_float4(v[0], v[1], v[2], v[3]);
+    r.b = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = channel<TPR, SIDE>(k, i0, j) < D ? q[channel<TPR, SIDE>(k, i0, j)] : 0;
+    r.w = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
   }
   return r;
 }
-template <typename IT>
-__device__ __forceinline__ void store8(IT* p, int c, int D, int vec, const float (&v)[8]) {
-  if (vec) {
+template <int TPR, bool SIDE, typename IT>
+__device__ __forceinline__ void store8(IT* p, int k, int i0, int D, int vec, const float (&v)[8]) {
+  if (!SIDE && vec) {
+    const int c = channel<TPR, SIDE>(k, i0, 0);
     if (c < D) store_v<8>(p + c, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < D) p[c + i] = from_f32<IT>(v[i]);
+    for (int j = 0; j < 8; ++j)
+      if (channel<TPR, SIDE>(k, i0, j) < D) p[channel<TPR, SIDE>(k, i0, j)] = from_f32<IT>(v[j]);
   }
 }
 
@@ -145,6 +151,18 @@ cudaError_t norm_parts(int parts, F f) {
   if (parts == kAdd) return f(std::integral_constant<int, kAdd>{});
   if (parts == kFull) return f(std::integral_constant<int, kFull>{});
   return f(std::integral_constant<int, kNormAny>{});
+}
+
+// f(SIDE): rows of blocks have a kernel of their own for rows that do not take 16-byte accesses (8192 x
+// 2047, full backward: 204 us in chunks of 8, 142 us side by side).  The kernel for those that do still asks for
+// `vec` at run time: without the question its loads and arithmetic become one block of code, in which
+// the compiler orders the next row's loads late (8192 x 4096, full backward: 184 us against 142).
+template <int TPR, typename F>
+cudaError_t norm_side(int vec, F f) {
+  if constexpr (TPR <= 32)
+    return f(std::false_type{});
+  else
+    return vec ? f(std::false_type{}) : f(std::true_type{});
 }
 
 gdr_status resolve_norm(const gdr_norm_problem* p, NormDims* d);

@@ -8,7 +8,7 @@ namespace gdr {
 // Rows of more than a warp: the weights stay in shared memory (3 x D floats), since a row's work is
 // a chain of two block sums and each read of a weight from the L2 would lengthen it (8192 x 4096
 // with everything, fp32 stream: 193 us with global reads, 136 us with these).
-template <typename IT, typename RT, int TPR, int K, int PARTS>
+template <typename IT, typename RT, int TPR, int K, int PARTS, bool SIDE>
 __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, NormBwdPtrs a) {
   constexpr int kBlock = norm_block(TPR), kRows = norm_rows(TPR);
   constexpr bool kAhead = K == 1;  // two rows in registers; wider ones would spill
@@ -33,11 +33,11 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
     }
     __syncthreads();
   }
-  auto weight = [&](const float* p, int part, int c, int D, float (&v)[8]) {
+  auto weight = [&](const float* p, int part, int k, int D, float (&v)[8]) {
     if constexpr (TPR > 32)
-      load_raw8(weights + part * Dp, c, Dp, 1).get(v);
+      load_raw8<TPR, SIDE>(weights + part * Dp, k, i0, SIDE ? d.D : Dp, 1).get(v);
     else
-      load_raw8(p, c, D, d.vec).get(v);
+      load_raw8<TPR, SIDE>(p, k, i0, D, d.vec).get(v);
   };
   constexpr int kAcc = PARTS >= 0 ? ((PARTS & kNormPost) != 0) + ((PARTS & kNormScale) != 0) + ((PARTS & kNormPre) != 0) : 3;
   constexpr int kScaleAt = PARTS >= 0 ? ((PARTS & kNormPost) != 0) : 1;
@@ -58,14 +58,13 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
     const long long tok = row / d.heads, at = (row - tok * d.heads) * d.D;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = 8 * (k * TPR + i0);
-      if (need_x) o.x[k] = load_raw8((const IT*)a.x + tok * d.ld_x + at, c, D, d.vec);
+      if (need_x) o.x[k] = load_raw8<TPR, SIDE>((const IT*)a.x + tok * d.ld_x + at, k, i0, D, d.vec);
       if (pre) {
-        o.r[k] = load_raw8((const RT*)a.r + row * d.D, c, D, d.vec);
-        o.dy[k] = load_raw8((const IT*)a.dy + row * d.D, c, D, d.vec);
+        o.r[k] = load_raw8<TPR, SIDE>((const RT*)a.r + row * d.D, k, i0, D, d.vec);
+        o.dy[k] = load_raw8<TPR, SIDE>((const IT*)a.dy + row * d.D, k, i0, D, d.vec);
       }
-      if (has_dr) o.dr[k] = load_raw8((const RT*)a.dr + row * d.D, c, D, d.vec);
-      if (gate) o.z[k] = load_raw8((const IT*)a.gate + tok * d.ld_gate + at, c, D, d.vec);
+      if (has_dr) o.dr[k] = load_raw8<TPR, SIDE>((const RT*)a.dr + row * d.D, k, i0, D, d.vec);
+      if (gate) o.z[k] = load_raw8<TPR, SIDE>((const IT*)a.gate + tok * d.ld_gate + at, k, i0, D, d.vec);
     }
   };
   const long long step = (long long)gridDim.x * kRows;
@@ -81,7 +80,6 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
     float s[3] = {0.f, 0.f, 0.f};  // sum x^2, sum r^2, sum dy w_pre r
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = 8 * (k * TPR + i0);
       if (post) {
         cur.x[k].get(v);
 #pragma unroll
@@ -90,7 +88,7 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
       if (pre) {
         cur.r[k].get(v);
         cur.dy[k].get(t);
-        weight(a.w_pre, 2, c, D, w);
+        weight(a.w_pre, 2, k, D, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           s[1] = fmaf(v[i], v[i], s[1]);
@@ -104,7 +102,6 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
     float q[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = 8 * (k * TPR + i0);
       if (has_dr) {
         cur.dr[k].get(du[k]);
       } else {
@@ -114,7 +111,7 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
       if (pre) {
         cur.r[k].get(v);
         cur.dy[k].get(t);
-        weight(a.w_pre, 2, c, D, w);
+        weight(a.w_pre, 2, k, D, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float rh = v[i] * rr;
@@ -122,12 +119,12 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
           du[k][i] = fmaf(rr, t[i] * w[i] - rh * m1, du[k][i]);
         }
       }
-      if (a.dres) store8((RT*)a.dres + row * d.D, c, D, d.vec, du[k]);
+      if (a.dres) store8<TPR, SIDE>((RT*)a.dres + row * d.D, k, i0, D, d.vec, du[k]);
       if (need_x) {
         float sc[8], z[8];
         cur.x[k].get(v);
-        if (post) weight(a.w_post, 0, c, D, w);
-        if (scale) weight(a.scale, 1, c, D, sc);
+        if (post) weight(a.w_post, 0, k, D, w);
+        if (scale) weight(a.scale, 1, k, D, sc);
         if (gate) cur.z[k].get(z);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -151,7 +148,7 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
           }
           du[k][i] = e;
         }
-        if (gate) store8((IT*)a.dgate + row * d.D, c, D, d.vec, t);
+        if (gate) store8<TPR, SIDE>((IT*)a.dgate + row * d.D, k, i0, D, d.vec, t);
       }
     }
     if (post) {
@@ -165,7 +162,7 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
       }
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) store8((IT*)a.dx + row * d.D, 8 * (k * TPR + i0), D, d.vec, du[k]);
+    for (int k = 0; k < K; ++k) store8<TPR, SIDE>((IT*)a.dx + row * d.D, k, i0, D, d.vec, du[k]);
     if (kAhead) cur = next;
   }
 #pragma unroll
@@ -174,7 +171,7 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
     float* out = a.partial + ((long long)blockIdx.x * 3 + slot) * d.D;
     if constexpr (kRows == 1) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) store8(out, 8 * (k * TPR + i0), d.D, d.vec, acc[m][k]);
+      for (int k = 0; k < K; ++k) store8<TPR, SIDE>(out, k, i0, d.D, d.vec, acc[m][k]);
     } else {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -198,18 +195,20 @@ cudaError_t norm_bwd_launch(const NormDims& d, const NormBwdPtrs& a, int parts, 
   return norm_shape(d.D, [&](auto tpr, auto k) {
     constexpr int TPR = decltype(tpr)::value, K = decltype(k)::value;
     return norm_parts(parts, [&](auto pt) {
-      constexpr auto kernel = norm_bwd_kernel<IT, RT, TPR, K, decltype(pt)::value>;
-      const size_t smem = TPR > 32 ? 3 * sizeof(float) * (size_t)((d.D + 7) & ~7) : 0;
-      if (smem > 0) {
-        const cudaError_t e = set_smem_once((const void*)kernel, smem);
-        if (e != cudaSuccess) return e;
-      }
-      // for the widest row of this shape
-      static const long long most = (long long)kSmCount * resident_blocks(kernel, norm_block(TPR), TPR > 32 ? 96 * TPR * K : 0);
-      if (*grid > most) *grid = most;
-      kernel<<<(unsigned)*grid, norm_block(TPR), smem, s>>>(d, a);
-      stage_mark(s, "norm_bwd");
-      return cudaGetLastError();
+      return norm_side<TPR>(d.vec, [&](auto side) {
+        constexpr auto kernel = norm_bwd_kernel<IT, RT, TPR, K, decltype(pt)::value, decltype(side)::value>;
+        constexpr size_t widest = TPR > 32 ? 3 * sizeof(float) * 8 * TPR * K : 0;  // for the shape's widest row
+        const size_t smem = TPR > 32 ? 3 * sizeof(float) * (size_t)((d.D + 7) & ~7) : 0;
+        if (smem > 0) {
+          const cudaError_t e = set_smem_once((const void*)kernel, widest);
+          if (e != cudaSuccess) return e;
+        }
+        static const long long most = (long long)kSmCount * resident_blocks(kernel, norm_block(TPR), widest);
+        if (*grid > most) *grid = most;
+        kernel<<<(unsigned)*grid, norm_block(TPR), smem, s>>>(d, a);
+        stage_mark(s, "norm_bwd");
+        return cudaGetLastError();
+      });
     });
   });
 }

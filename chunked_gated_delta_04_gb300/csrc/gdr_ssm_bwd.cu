@@ -27,14 +27,6 @@ struct SsmBwdArgs {
   float *dS0, *grads, *bc;
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-// Copies `bytes` (4, 8 or 16; the rest of a Bytes-wide destination is zeros) without passing registers.
-template <int Bytes>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src), "n"(Bytes), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 // Shared memory of a block, two tiles of everything: the one being computed and the one that is
 // formed (or finished) beside it.
 template <typename IT, int N>

@@ -19,7 +19,9 @@ namespace gdr {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kSlice = 32;  // value features per block
+// Value features of a block whose keys fit DKP (64 or 128) features: 16 KB of state either way, eight
+// 16-byte loads in flight per thread.
+constexpr int slice_of(int DKP) { return 32 * 128 / DKP; }
 
 struct StepDims {
   int Hk, Hv, DK, DV, G, num_slots, prologue;
@@ -34,12 +36,16 @@ __device__ __forceinline__ float block_sum(float v, float* red) {  // red: 4 flo
   return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-template <typename IT, bool KV>
+template <typename IT, bool KV, int DKP>
 __global__ void __launch_bounds__(kThreads) step_kernel(StepDims d, const IT* __restrict__ q, const IT* __restrict__ k,
                                                         const IT* __restrict__ v, const float* __restrict__ g,
                                                         const IT* __restrict__ beta, float* __restrict__ pool,
                                                         const int32_t* __restrict__ slots, IT* __restrict__ o) {
-  __shared__ float sk[128], sq[128], red[4];
+  constexpr int kSlice = slice_of(DKP);
+  constexpr int CQ = kSlice / 4;                // KV: float4 columns of the slice; row groups of 128 / CQ rows
+  constexpr int LR = DKP / 4, RP = 32 / LR;     // VK: lanes of a row, rows of a warp at a time
+  __shared__ __align__(16) float sk[128], sq[128];
+  __shared__ float red[4];
   __shared__ float part[2][4][kSlice];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.y, h = blockIdx.x % d.Hv, v0 = (blockIdx.x / d.Hv) * kSlice;
@@ -54,20 +60,20 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepDims d, const IT* __
   float* S = pool + ((long long)slot * d.Hv + h) * d.DK * d.DV;
   // this thread's part of the slice: 8 float4
   float4 st[8];
-  if constexpr (KV) {  // rows 16 i + tid / 8 of S^T, value features v0 + 4 (tid % 8) ..
-    const int c = 4 * (tid & 7);
+  if constexpr (KV) {  // rows (128 / CQ) i + tid / CQ of S^T, value features v0 + 4 (tid % CQ) ..
+    const int c = 4 * (tid % CQ);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = 16 * i + (tid >> 3);
+      const int r = (kThreads / CQ) * i + tid / CQ;
       st[i] = r < d.DK && c < nv ? __ldcs(reinterpret_cast<const float4*>(S + (long long)r * d.DV + v0 + c))
                                  : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-  } else {  // rows v0 + 8 warp + i of S, key features 4 lane ..
+  } else {  // rows v0 + RP (8 warp + i) + lane / LR of S, key features 4 (lane % LR) ..
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = 8 * warp + i;
-      st[i] = r < nv && 4 * lane < d.DK ? __ldcs(reinterpret_cast<const float4*>(S + (long long)(v0 + r) * d.DK + 4 * lane))
-                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      const int r = RP * (8 * warp + i) + lane / LR, c = 4 * (lane % LR);
+      st[i] = r < nv && c < d.DK ? __ldcs(reinterpret_cast<const float4*>(S + (long long)(v0 + r) * d.DK + c))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
   // q, k, their product, the gates
@@ -87,11 +93,12 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepDims d, const IT* __
   const float kq = block_sum(kv * qv, red);  // its barriers order sk, sq too
 
   if constexpr (KV) {
-    const int c = 4 * (tid & 7);
+    const int c = 4 * (tid % CQ);
     float p[4] = {}, z[4] = {};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float kr = sk[16 * i + (tid >> 3)], qr = sq[16 * i + (tid >> 3)];
+      const int r = (kThreads / CQ) * i + tid / CQ;
+      const float kr = sk[r], qr = sq[r];
       const float e[4] = {st[i].x, st[i].y, st[i].z, st[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -100,13 +107,13 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepDims d, const IT* __
       }
     }
 #pragma unroll
-    for (int off = 8; off < 32; off <<= 1)
+    for (int off = CQ; off < 32; off <<= 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         p[j] += __shfl_xor_sync(0xffffffffu, p[j], off);
         z[j] += __shfl_xor_sync(0xffffffffu, z[j], off);
       }
-    if (lane < 8)
+    if (lane < CQ)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         part[0][warp][c + j] = p[j];
@@ -121,11 +128,11 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepDims d, const IT* __
       const float zj = (part[1][0][cc] + part[1][1][cc]) + (part[1][2][cc] + part[1][3][cc]);
       const float vv = cc < nv ? to_f32(v[bh * d.DV + v0 + cc]) : 0.f;
       u[j] = bt * fmaf(-eg, pj, vv);
-      if (tid < 8 && cc < nv) oh[cc] = from_f32<IT>(d.scale * fmaf(eg, zj, u[j] * kq));
+      if (tid < CQ && cc < nv) oh[cc] = from_f32<IT>(d.scale * fmaf(eg, zj, u[j] * kq));
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int r = 16 * i + (tid >> 3);
+      const int r = (kThreads / CQ) * i + tid / CQ;
       const float kr = sk[r];
       if (r < d.DK && c < nv)
         __stcs(reinterpret_cast<float4*>(S + (long long)r * d.DV + v0 + c),
@@ -133,33 +140,39 @@ __global__ void __launch_bounds__(kThreads) step_kernel(StepDims d, const IT* __
                            fmaf(eg, st[i].w, u[3] * kr)));
     }
   } else {
-    const float4 k4 = *reinterpret_cast<const float4*>(sk + 4 * lane), q4 = *reinterpret_cast<const float4*>(sq + 4 * lane);
+    const int c = 4 * (lane % LR);
+    const float4 k4 = *reinterpret_cast<const float4*>(sk + c), q4 = *reinterpret_cast<const float4*>(sq + c);
     float w[16];  // p of rows 0..7, then S q
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       w[i] = fmaf(st[i].x, k4.x, fmaf(st[i].y, k4.y, fmaf(st[i].z, k4.z, st[i].w * k4.w)));
       w[8 + i] = fmaf(st[i].x, q4.x, fmaf(st[i].y, q4.y, fmaf(st[i].z, q4.z, st[i].w * q4.w)));
     }
-    // 16 sums over 32 lanes: each exchange halves the values a lane keeps
+    // 16 sums over the LR lanes of a row: each exchange halves the values a lane keeps, so that lane
+    // LR / 16 * i of the row ends with value i (and, of 32 lanes, its neighbour with the other half of it)
 #pragma unroll
     for (int m = 8; m >= 1; m >>= 1) {
+      const int bit = m * LR / 16;
 #pragma unroll
       for (int i = 0; i < m; ++i) {
-        const bool up = lane & (2 * m);
+        const bool up = lane & bit;
         const float send = up ? w[i] : w[i + m], keep = up ? w[i + m] : w[i];
-        w[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * m);
+        w[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
       }
     }
-    const float total = w[0] + __shfl_xor_sync(0xffffffffu, w[0], 1);  // value lane / 2
+    float total = w[0];
+    if constexpr (LR == 32) total += __shfl_xor_sync(0xffffffffu, total, 1);
+    const int row0 = lane / LR * LR;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float pi = __shfl_sync(0xffffffffu, total, 2 * i), zi = __shfl_sync(0xffffffffu, total, 16 + 2 * i);
-      const int r = 8 * warp + i;
+      const float pi = __shfl_sync(0xffffffffu, total, row0 + LR / 16 * i);
+      const float zi = __shfl_sync(0xffffffffu, total, row0 + LR / 16 * (8 + i));
+      const int r = RP * (8 * warp + i) + lane / LR;
       const float vv = r < nv ? to_f32(v[bh * d.DV + v0 + r]) : 0.f;
       const float u = bt * fmaf(-eg, pi, vv);
-      if (lane == 0 && r < nv) oh[r] = from_f32<IT>(d.scale * fmaf(eg, zi, u * kq));
-      if (r < nv && 4 * lane < d.DK)
-        __stcs(reinterpret_cast<float4*>(S + (long long)(v0 + r) * d.DK + 4 * lane),
+      if (lane % LR == 0 && r < nv) oh[r] = from_f32<IT>(d.scale * fmaf(eg, zi, u * kq));
+      if (r < nv && c < d.DK)
+        __stcs(reinterpret_cast<float4*>(S + (long long)(v0 + r) * d.DK + c),
                make_float4(fmaf(eg, st[i].x, u * k4.x), fmaf(eg, st[i].y, u * k4.y), fmaf(eg, st[i].z, u * k4.z),
                            fmaf(eg, st[i].w, u * k4.w)));
     }
@@ -179,7 +192,7 @@ extern "C" gdr_status gdr_step(const gdr_problem* p, const void* q, const void* 
   if (!dtype_ok(p->dtype) || (p->layout != GDR_STATE_KV && p->layout != GDR_STATE_VK)) return GDR_ERR_INVALID_ARG;
   if (p->prologue & ~7u) return GDR_ERR_INVALID_ARG;
   if (p->DK % 16 != 0 || p->DV % 16 != 0 || p->DK > 128 || p->DV > 128) return GDR_ERR_UNSUPPORTED;
-  const int slices = (p->DV + kSlice - 1) / kSlice;
+  const int DKP = p->DK > 64 ? 128 : 64, slice = slice_of(DKP), slices = (p->DV + slice - 1) / slice;
   if (p->B > 65535 || (long long)p->Hv * slices >= (1ll << 31)) return GDR_ERR_UNSUPPORTED;
   if (p->B == 0) return GDR_OK;
   if (!q || !k || !v || !g || !beta || !o || (!pool && num_slots > 0)) return GDR_ERR_INVALID_ARG;
@@ -194,8 +207,9 @@ extern "C" gdr_status gdr_step(const gdr_problem* p, const void* q, const void* 
   const dim3 grid((unsigned)(p->Hv * slices), (unsigned)p->B);
   auto go = [&](auto it, auto kv) {
     using IT = decltype(it);
-    step_kernel<IT, decltype(kv)::value><<<grid, kThreads, 0, s>>>(d, (const IT*)q, (const IT*)k, (const IT*)v, g,
-                                                                  (const IT*)beta, pool, slots, (IT*)o);
+    constexpr bool KV = decltype(kv)::value;
+    const auto kernel = DKP == 128 ? step_kernel<IT, KV, 128> : step_kernel<IT, KV, 64>;
+    kernel<<<grid, kThreads, 0, s>>>(d, (const IT*)q, (const IT*)k, (const IT*)v, g, (const IT*)beta, pool, slots, (IT*)o);
     stage_mark(s, "step");
     return cudaGetLastError();
   };
