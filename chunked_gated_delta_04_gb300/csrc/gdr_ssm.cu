@@ -502,7 +502,7 @@ gdr_status resolve_ssm(const gdr_ssm_problem* p, bool step, SsmDims* d) {
   // two.  They are made of at least 64 tokens, enough for six blocks per SM.
   const long long blocks = fwd_blocks(*d), whole = (d->T + kTile - 1) / kTile * (long long)kTile;
   d->Lseg = (int)(whole < kTile ? kTile : whole);
-  if (!step && blocks * d->num_seqs < (d->cu ? 2 : 1) * kSmCount) {
+  if (!step && d->total > 0 && blocks * d->num_seqs < (d->cu ? 2 : 1) * kSmCount) {
     const long long want = (6ll * kSmCount + blocks - 1) / blocks;  // segments over all sequences
     long long L = (d->total / want + kTile - 1) / kTile * kTile;
     if (L < 64) L = 64;

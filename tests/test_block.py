@@ -486,3 +486,22 @@ def test_autograd_against_differences():
         num = (loss(dict(P, **{k: P[k] + eps * d})) - loss(dict(P, **{k: P[k] - eps * d}))) / (2 * eps)
         ana = (leaf[k].grad.double() * d).sum()
         assert (num - ana).abs() <= 1e-2 * max(1.0, ana.abs().item()), (k, num.item(), ana.item())
+
+
+@pytest.mark.parametrize("B,T", [(0, 5), (0, 4096), (3, 0)])
+def test_nothing_to_do(B, T):
+    """No sequences, or sequences without tokens: empty outputs, zero parameter gradients, states handed on."""
+    C = 24
+    x = torch.zeros(B, T, C, device="cuda", dtype=BF)
+    w, b, st = torch.ones(C, 4, device="cuda"), torch.ones(C, device="cuda"), torch.ones(B, 3, C, device="cuda", dtype=BF)
+    y, last = gdr.conv_forward(x, w, b, st, output_final_state=True)
+    dx, dw, db, ds = gdr.conv_backward(x, w, b, x, st, st)
+    assert y.shape == dx.shape == x.shape and torch.equal(last, st) and torch.equal(ds, st) and not dw.any() and not db.any()
+    A, S0 = -torch.ones(C, 16, device="cuda"), torch.ones(B, C, 16, device="cuda")
+    bc = torch.zeros(B, T, 1, 16, device="cuda", dtype=BF)
+    y, S_T, saved = gdr.ssm_forward(x, x, A, bc, bc, b, b, S0)
+    dx, ddt, dA, dB, dC, dD, dbias, dS0 = gdr.ssm_backward(x, x, A, bc, bc, saved, x, b, b, S0)
+    assert torch.equal(S_T, S0) and torch.equal(dS0, S0) and not dA.any() and not dD.any() and not dbias.any()
+    r, y = gdr.norm_forward(x, b, x, b, x, b)
+    g = gdr.norm_backward(x, b, x, b, r, b, x, x)
+    assert r.shape == y.shape == x.shape and not g[3].any() and not g[4].any() and not g[5].any()
