@@ -150,14 +150,14 @@ extern "C" gdr_status gdr_norm_fwd(const gdr_norm_problem* p, const void* x, con
   NormDims d;
   const gdr_status st = resolve_norm(p, &d);
   if (st != GDR_OK) return st;
+  if (d.rows == 0) return GDR_OK;  // tensors of no rows may have no address
   if (!w_post && !gate && !scale && !residual && !w_pre) return GDR_ERR_INVALID_ARG;
   if (w_pre && !residual && (w_post || gate || scale)) return GDR_ERR_INVALID_ARG;
-  if (d.rows > 0 && (!x || (w_pre && !y) || ((residual || !w_pre) && !r))) return GDR_ERR_INVALID_ARG;
+  if ((!x || (w_pre && !y) || ((residual || !w_pre) && !r))) return GDR_ERR_INVALID_ARG;
   const size_t el = dtype_bytes(p->dtype), rel = residual ? dtype_bytes(p->res_dtype) : el;
   if (!elem_ok(x, el) || !elem_ok(gate, el) || !elem_ok(y, el) || !elem_ok(residual, rel) || !elem_ok(r, rel) ||
       !elem_ok(w_post, 4) || !elem_ok(scale, 4) || !elem_ok(w_pre, 4))
     return GDR_ERR_ALIGNMENT;
-  if (d.rows == 0) return GDR_OK;
   d.vec = d.D % 8 == 0 && d.ld_x % 8 == 0 && d.ld_gate % 8 == 0 && vec_ok(x) && vec_ok(w_post) && vec_ok(gate) &&
           vec_ok(scale) && vec_ok(residual) && vec_ok(w_pre) && vec_ok(r) && vec_ok(y);
   cudaStream_t s = (cudaStream_t)stream;

@@ -49,12 +49,14 @@ gdr_status gdr_norm_bwd(const gdr_norm_problem* p, const void* x, const float* w
   NormDims d;
   const gdr_status st = resolve_norm(p, &d);
   if (st != GDR_OK) return st;
-  if (!w_post && !gate && !scale && !has_residual && !w_pre) return GDR_ERR_INVALID_ARG;
-  if (w_pre && !has_residual && (w_post || gate || scale || dr)) return GDR_ERR_INVALID_ARG;
-  if (!w_pre != !dy || (!dr && !dy)) return GDR_ERR_INVALID_ARG;
-  if (dresidual && !has_residual) return GDR_ERR_INVALID_ARG;
   if ((w_post && !dw_post) || (scale && !dscale) || (w_pre && !dw_pre)) return GDR_ERR_INVALID_ARG;
-  if (d.rows > 0 && (!x || !dx || (w_pre && !r) || (gate && !dgate))) return GDR_ERR_INVALID_ARG;
+  if (d.rows > 0) {  // tensors of no rows may have no address
+    if (!w_post && !gate && !scale && !has_residual && !w_pre) return GDR_ERR_INVALID_ARG;
+    if (w_pre && !has_residual && (w_post || gate || scale || dr)) return GDR_ERR_INVALID_ARG;
+    if (!w_pre != !dy || (!dr && !dy)) return GDR_ERR_INVALID_ARG;
+    if (dresidual && !has_residual) return GDR_ERR_INVALID_ARG;
+    if (!x || !dx || (w_pre && !r) || (gate && !dgate)) return GDR_ERR_INVALID_ARG;
+  }
   const size_t el = dtype_bytes(p->dtype), rel = has_residual ? dtype_bytes(p->res_dtype) : el;
   if (!elem_ok(x, el) || !elem_ok(gate, el) || !elem_ok(dy, el) || !elem_ok(dx, el) || !elem_ok(dgate, el) ||
       !elem_ok(r, rel) || !elem_ok(dr, rel) || !elem_ok(dresidual, rel) || !elem_ok(w_post, 4) || !elem_ok(scale, 4) ||

@@ -96,6 +96,8 @@ __global__ void __launch_bounds__(fwd_threads(NL))
   const long long units = ssm_unit_count(d);
   for (long long un = blockIdx.y; un < units; un += gridDim.y) {
     const SsmUnit q = ssm_unit(d, un);
+    // nothing follows a sequence's last unit (in reverse: its first) that its boundary would be for
+    if (MODE == kEndState ? q.last : MODE == kStartGrad ? q.first : false) continue;
     f32x2 h[2][2] = {};
     if (kY && start) load_state(start + (start_per_unit ? un : q.seq) * (long long)d.D * N, h);
     f32x2 dsum = 0;
@@ -274,7 +276,8 @@ __global__ void __launch_bounds__(fwd_threads(NL))
 
 // Joins the segments of every sequence: cur = edge; in order (backward: reversed) of its units,
 // R[u] <- cur, cur <- exp(A sum D) cur + R[u].  One thread per (sequence, channel, state); the
-// loads of the next four units are in flight while four are joined.
+// loads of the next four units are in flight while four are joined.  The last unit contributes
+// nothing.
 __global__ void __launch_bounds__(256) ssm_join_kernel(SsmDims d, const float* __restrict__ A,
                                                        const float* __restrict__ edge, float* R,
                                                        const float* __restrict__ sum_delta, int backward) {
@@ -292,8 +295,8 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(SsmDims d, const float* _
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const long long u = u0 + (backward ? count - 1 - (k + i) : k + i);
-      r[i] = k + i < count ? R[u * DN + dn] : 0.f;
-      s[i] = k + i < count ? sum_delta[u * d.D + ch] : 0.f;
+      r[i] = k + i + 1 < count ? R[u * DN + dn] : 0.f;
+      s[i] = k + i + 1 < count ? sum_delta[u * d.D + ch] : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
