@@ -159,6 +159,12 @@ template <int Bytes>
 __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_addr(dst)), "l"(src), "n"(Bytes), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most `Left` of the groups committed last are under way.
+template <int Left>
+__device__ __forceinline__ void copy_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(Left) : "memory");
+}
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 inline size_t block_align(size_t x) { return (x + 255) & ~(size_t)255; }

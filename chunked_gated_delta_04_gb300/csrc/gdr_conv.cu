@@ -12,14 +12,15 @@
 // W - 1 inputs (and, backward, the last W - 1 dpre) in registers, so each element is read once but
 // for the W - 1 rows in front of (backward: also behind) a run, which its neighbour's reads have
 // brought into the L2.
+#include <initializer_list>
+
 #include "gdr_block.cuh"
 
 namespace gdr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBwdVec = 4;
-constexpr int kFwdVec = 4;  // channels per thread of the vector paths
+constexpr int kVec = 4;        // channels per thread of the vector paths
 constexpr int kFwdBlocks = 3;  // blocks per SM of the forward
 
 struct ConvDims {
@@ -132,6 +133,75 @@ __device__ __forceinline__ void store_row(IT* p, const f32x2 (&v)[kPairs<V>]) {
   store_v<V>(p, *reinterpret_cast<const float(*)[V]>(&f));
 }
 
+// Calls row(t, in) for the n rows of NS tensors in order, in[s] being the row's V channels of tensor s.
+// Vector rows are copied, DEEP - 1 of them ahead, to slots in shared memory that only this thread uses
+// (slots: its column of [DEEP][NS][kThreads]), so that the rows in flight take no registers; a slot is
+// refilled a step after it was read.  Scalar rows wait in registers, four ahead.  Bytes in flight are
+// what a kernel's nearness to the memory rate depends on: forward, B = 2, T = 4096, C = 6144, bf16, from
+// a cold L2: 46 us with four rows in registers, 43 us with seven in shared memory.
+// Groups of four rows run without conditions on what row() keeps: its windows' moves are renamings.
+template <typename IT, int V, int NS, int DEEP, typename F>
+__device__ __forceinline__ void walk_rows(const IT* const (&src)[NS], const long long (&ld)[NS], int n, Raw<IT, V>* slots,
+                                          F row) {
+  const IT* p[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) p[s] = src[s];
+  if constexpr (V > 1) {
+    auto start = [&](int slot, bool some) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        if (some) copy_async<sizeof(Raw<IT, V>)>(slots + (slot * NS + s) * kThreads, p[s], sizeof(Raw<IT, V>));
+        p[s] += ld[s];
+      }
+      copy_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < DEEP - 1; ++i) start(i, i < n);
+    auto step = [&](int t) {
+      copy_async_wait_group<DEEP - 2>();  // of the t + DEEP - 1 rows started, row t is there
+      f32x2 in[NS][kPairs<V>];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) slots[(t % DEEP * NS + s) * kThreads].get(in[s]);
+      start((t + DEEP - 1) % DEEP, t + DEEP - 1 < n);
+      row(t, in);
+    };
+    int t = 0;
+    for (; t + 4 <= n; t += 4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) step(t + u);
+    }
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+      if (t + u < n) step(t + u);
+  } else {
+    Raw<IT, V> r[4][NS];
+    auto start = [&](int i, bool some) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        if (some) r[i][s].load(p[s]);
+        p[s] += ld[s];
+      }
+    };
+    auto step = [&](int t, int u) {
+      f32x2 in[NS][kPairs<V>];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) r[u][s].get(in[s]);
+      start(u, t + 4 < n);
+      row(t, in);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) start(i, i < n);
+    int t = 0;
+    for (; t + 4 <= n; t += 4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) step(t + u, u);
+    }
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+      if (t + u < n) step(t + u, u);
+  }
+}
+
 // Row p (p < s1) of X: a token, or, before s0, a row of the state.
 template <typename IT, int V, int W>
 __device__ __forceinline__ void load_row(const ConvDims& d, const SeqWalk& q, const IT* x, const IT* state,
@@ -175,15 +245,16 @@ __device__ __forceinline__ void push(f32x2 (&ring)[W][kPairs<V>], const f32x2 (&
   for (int i = 0; i < kPairs<V>; ++i) ring[W - 1][i] = v[i];
 }
 
-// B = 2, T = 4096, C = 6144, bf16, W = 4, from a cold L2: 46 us, 201 MB, 4.4 TB/s.  8 channels a
-// thread with two blocks per SM: 48 us; runs of 32 tokens (2.5 waves) instead of one wave's: 52 us.
+// B = 2, T = 4096, C = 6144, bf16, W = 4, from a cold L2: 43 us, 201 MB, 4.7 TB/s.  Runs of 32 tokens
+// (2.5 waves) instead of one wave's cost 6 us.
 template <typename IT, int V, int W>
 __global__ void __launch_bounds__(kThreads, kFwdBlocks) conv_fwd_kernel(ConvDims d, const IT* __restrict__ x,
                                                                const float* __restrict__ w,
                                                                const float* __restrict__ bias,
                                                                const IT* __restrict__ state, IT* __restrict__ y,
                                                                IT* __restrict__ last, int L) {
-  constexpr int P = kPairs<V>, kDeep = 4;
+  constexpr int P = kPairs<V>, kDeep = 8;
+  __shared__ Raw<IT, V> slots[V > 1 ? kDeep * kThreads : 1];
   if (d.status && *d.status) return;
   const int ncg = d.C / V;
   const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
@@ -209,43 +280,17 @@ __global__ void __launch_bounds__(kThreads, kFwdBlocks) conv_fwd_kernel(ConvDims
     const int n = (int)(min(t1, q.s1) - a);  // this run's tokens of the sequence
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) load_row<IT, V, W>(d, q, x, state, a - (W - 1) + j, c, win[j + 1]);
-    const IT* xp = x + a * d.ld_x + c;
     IT* yp = y + a * d.C + c;
-    auto one = [&](const f32x2(&in)[P]) {
+    const IT* const src[1] = {x + a * d.ld_x + c};
+    const long long ld[1] = {d.ld_x};
+    walk_rows<IT, V, 1, kDeep>(src, ld, n, slots + threadIdx.x * (V > 1), [&](int, const f32x2(&in)[1][P]) {
       f32x2 pre[P];
-      push<V, W>(win, in);
+      push<V, W>(win, in[0]);
       taps<V, W>(win, wt, b, pre);
       if (d.silu) silu_row<V>(pre);
       store_row<V>(yp, pre);
       yp += d.C;
-    };
-    // kDeep rows in flight: once a row has been converted its registers take the load of the row kDeep
-    // further on.  Whole groups run without conditions on the windows, whose moves then are renamings.
-    Raw<IT, V> r[kDeep];
-#pragma unroll
-    for (int u = 0; u < kDeep; ++u) {
-      if (u < n) r[u].load(xp);
-      xp += d.ld_x;
-    }
-    int t = 0;
-    for (; t + kDeep <= n; t += kDeep) {
-#pragma unroll
-      for (int u = 0; u < kDeep; ++u) {
-        f32x2 in[P];
-        r[u].get(in);
-        if (t + u + kDeep < n) r[u].load(xp);
-        xp += d.ld_x;
-        one(in);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kDeep - 1; ++u) {
-      if (t + u < n) {
-        f32x2 in[P];
-        r[u].get(in);
-        one(in);
-      }
-    }
+    });
     a += n;
     if (a < t1) q.next(d);
   }
@@ -267,9 +312,9 @@ __device__ __forceinline__ void grad_pre(const f32x2 (&win)[W][kPairs<V>], const
   }
 }
 
-// B = 2, T = 4096, C = 6144, bf16, W = 4, from a cold L2: 86 us, 302 MB, 3.5 TB/s (16 warps per SM; 30
-// instructions per element).  With a condition on every row's window moves, so that they are real
-// moves: 120 us.
+// B = 2, T = 4096, C = 6144, bf16, W = 4, from a cold L2: 71 us, 302 MB, 4.3 TB/s (16 warps per SM, 26
+// instructions per element).  With four rows in registers 86 us; with a condition on every row's
+// window moves besides, so that they are real moves, 120 us.
 //
 // Blocks of kThreads / cpb runs of L tokens by cpb groups of V channels; a block's sums of dw and
 // dbias go to partial[blockIdx.x][W + 1][C].  blockIdx.x >= tiles: dstate, one sequence per run.
@@ -282,7 +327,8 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvDims d, const
                                                                const IT* __restrict__ dlast, IT* __restrict__ dx,
                                                                IT* __restrict__ dstate, float* __restrict__ partial,
                                                                int L, int cpb, int tiles) {
-  constexpr int P = kPairs<V>;
+  constexpr int P = kPairs<V>, kDeep = sizeof(IT) == 2 ? 8 : 4;
+  __shared__ Raw<IT, V> slots[V > 1 ? 2 * kDeep * kThreads : 1];
   __shared__ float red[kThreads * V];
   if (d.status && *d.status) return;
   const int subs = kThreads / cpb, sub = threadIdx.x / cpb, cg = threadIdx.x - sub * cpb;
@@ -367,8 +413,6 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvDims d, const
       const int n = (int)(min(t1, q.s1) - a);                    // this run's rows of the sequence
       const int stop = (int)min((long long)n + W - 1, q.s1 - a);  // dpre is needed up to here
       open(a);
-      const IT* xp = x + a * d.ld_x + c;
-      const IT* dp = dy + a * d.ld_dy + c;
       IT* op = dx + a * d.C + c;
       auto emit = [&](int u) {  // row u's dpre is in: row u - (W - 1) is complete
         if (u >= W - 1) {
@@ -390,41 +434,11 @@ __global__ void __launch_bounds__(kThreads, 2) conv_bwd_kernel(ConvDims d, const
         }
         emit(u);
       };
-      Raw<IT, V> rx[4], rd[4];  // four rows in flight, as in the forward
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k < stop) {
-          rx[k].load(xp);
-          rd[k].load(dp);
-        }
-        xp += d.ld_x;
-        dp += d.ld_dy;
-      }
-      int u = 0;
-      for (; u + 4 <= stop; u += 4) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f32x2 in[P], g[P];
-          rx[k].get(in);
-          rd[k].get(g);
-          if (u + k + 4 < stop) {
-            rx[k].load(xp);
-            rd[k].load(dp);
-          }
-          xp += d.ld_x;
-          dp += d.ld_dy;
-          one(u + k, in, g);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        if (u + k < stop) {
-          f32x2 in[P], g[P];
-          rx[k].get(in);
-          rd[k].get(g);
-          one(u + k, in, g);
-        }
-      }
+      const IT* const src[2] = {x + a * d.ld_x + c, dy + a * d.ld_dy + c};
+      const long long ld[2] = {d.ld_x, d.ld_dy};
+      walk_rows<IT, V, 2, kDeep>(src, ld, stop, slots + threadIdx.x * (V > 1), [&](int u, f32x2(&in)[2][P]) {
+        one(u, in[0], in[1]);
+      });
       for (int u = stop; u < n + W - 1; ++u) {  // past the sequence's end: no dpre
         push<V, W>(dwin, zero);
         emit(u);
@@ -514,6 +528,13 @@ gdr_status resolve_conv(const gdr_conv_problem* p, bool step, ConvDims* d) {
   return GDR_OK;
 }
 
+// Whether every tensor is aligned to kVec elements.
+bool quads(std::initializer_list<const void*> ps, size_t el) {
+  for (const void* p : ps)
+    if (!elem_ok(p, kVec * el)) return false;
+  return true;
+}
+
 // Launch shape of the backward: channel groups per block and tokens per run.
 struct BwdShape {
   int cpb, L;
@@ -521,7 +542,7 @@ struct BwdShape {
 };
 BwdShape bwd_shape(const ConvDims& d) {
   BwdShape b;
-  const int ncg = (d.C + kBwdVec - 1) / kBwdVec;
+  const int ncg = (d.C + kVec - 1) / kVec;
   b.cpb = ncg >= 32 ? 32 : ncg >= 16 ? 16 : 8;
   // whole waves of two blocks per SM, as in the forward; runs of 4 to 256 tokens (long runs also keep
   // the partial rows few)
@@ -538,13 +559,13 @@ size_t conv_bwd_bytes(const ConvDims& d, int W) {
   return 256 + block_align(sizeof(float) * (size_t)bwd_shape(d).tiles * (W + 1) * d.C);
 }
 
-template <int VEC, typename F>
+template <typename F>
 cudaError_t by_type(gdr_dtype dt, bool vec, int W, F f) {
   auto width = [&](auto it, auto v) {
     return W == 2 ? f(it, v, std::integral_constant<int, 2>{})
                   : W == 3 ? f(it, v, std::integral_constant<int, 3>{}) : f(it, v, std::integral_constant<int, 4>{});
   };
-  using VN = std::integral_constant<int, VEC>;
+  using VN = std::integral_constant<int, kVec>;
   using V1 = std::integral_constant<int, 1>;
   if (dt == GDR_DTYPE_BF16) return vec ? width(__nv_bfloat16{}, VN{}) : width(__nv_bfloat16{}, V1{});
   return vec ? width(float{}, VN{}) : width(float{}, V1{});
@@ -586,8 +607,8 @@ gdr_status gdr_conv_fwd(const gdr_conv_problem* p, const void* x, const float* w
     const cudaError_t e = launch_seq_check(d.cu, d.num_seqs, d.T, (uint32_t*)workspace, s);
     if (e != cudaSuccess) return status_of(e);
   }
-  const bool vec = d.C % 8 == 0 && d.ld_x % 8 == 0 && vec_ok(x) && vec_ok(y) && vec_ok(state) && vec_ok(last) && vec_ok(w);
-  const long long ncg = vec ? d.C / kFwdVec : d.C;
+  const bool vec = d.C % kVec == 0 && d.ld_x % kVec == 0 && quads({x, y, state, last}, el) && vec_ok(w);
+  const long long ncg = vec ? d.C / kVec : d.C;
   // Runs of equal length in whole waves of blocks: as many tokens as one wave needs, at
   // most 128 (a run reads W - 1 rows of its neighbour's again), at least 4.
   const long long wave = (long long)kFwdBlocks * kSmCount * kThreads, per = (d.total * ncg + wave - 1) / wave, waves = (per + 127) / 128;
@@ -598,7 +619,7 @@ gdr_status gdr_conv_fwd(const gdr_conv_problem* p, const void* x, const float* w
   if (threads == 0) return GDR_OK;
   const long long grid = (threads + kThreads - 1) / kThreads;
   if (grid >= (1ll << 31)) return GDR_ERR_UNSUPPORTED;
-  return status_of(by_type<kFwdVec>(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
+  return status_of(by_type(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
     using IT = decltype(it);
     conv_fwd_kernel<IT, decltype(v)::value, decltype(wd)::value><<<(unsigned)grid, kThreads, 0, s>>>(
         d, (const IT*)x, w, bias, (const IT*)state, (IT*)y, (IT*)last, L);
@@ -628,16 +649,16 @@ gdr_status gdr_conv_bwd(const gdr_conv_problem* p, const void* x, const float* w
     if (e != cudaSuccess) return status_of(e);
   }
   float* partial = (float*)((char*)workspace + 256);
-  const bool vec = d.C % 8 == 0 && d.ld_x % 8 == 0 && d.ld_dy % 8 == 0 && vec_ok(x) && vec_ok(dy) && vec_ok(dx) &&
-                   vec_ok(state) && vec_ok(dlast) && vec_ok(dstate) && vec_ok(w);
+  const bool vec = d.C % kVec == 0 && d.ld_x % kVec == 0 && d.ld_dy % kVec == 0 &&
+                   quads({x, dy, dx, state, dlast, dstate}, el) && vec_ok(w);
   const BwdShape b = bwd_shape(d);
   const int subs = kThreads / b.cpb;
   const long long gx = b.tiles + (dstate ? ((long long)d.num_seqs + subs - 1) / subs : 0);
-  const int ncg = vec ? d.C / kBwdVec : d.C;
+  const int ncg = vec ? d.C / kVec : d.C;
   const int gy = (ncg + b.cpb - 1) / b.cpb;
   if (gx >= (1ll << 31) || gy > 65535) return GDR_ERR_UNSUPPORTED;
   if (gx > 0) {
-    const cudaError_t e = by_type<kBwdVec>(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
+    const cudaError_t e = by_type(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
       using IT = decltype(it);
       conv_bwd_kernel<IT, decltype(v)::value, decltype(wd)::value><<<dim3((unsigned)gx, gy), kThreads, 0, s>>>(
           d, (const IT*)x, w, bias, (const IT*)state, (const IT*)dy, (const IT*)dlast, (IT*)dx, (IT*)dstate, partial,
@@ -670,13 +691,13 @@ gdr_status gdr_conv_step(const gdr_conv_problem* p, const void* x, const float* 
   if (d.total == 0) return GDR_OK;
   cudaStream_t s = (cudaStream_t)stream;
   stage_begin(s);
-  const bool vec = d.C % 8 == 0 && d.ld_x % 8 == 0 && vec_ok(x) && vec_ok(y) && vec_ok(pool) && vec_ok(w);
-  const int ncg = vec ? d.C / kFwdVec : d.C, gx = (ncg + kThreads - 1) / kThreads;
+  const bool vec = d.C % kVec == 0 && d.ld_x % kVec == 0 && quads({x, y, pool}, el) && vec_ok(w);
+  const int ncg = vec ? d.C / kVec : d.C, gx = (ncg + kThreads - 1) / kThreads;
   const bool four = (long long)gx * ((p->B + 3) / 4) >= 2 * kSmCount;  // rows enough to keep every SM busy
   const int rows = four ? 4 : 1;
   if ((p->B + rows - 1) / rows > 65535) return GDR_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)gx, (unsigned)((p->B + rows - 1) / rows));
-  return status_of(by_type<kFwdVec>(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
+  return status_of(by_type(p->dtype, vec, p->W, [&](auto it, auto v, auto wd) {
     using IT = decltype(it);
     constexpr int V = decltype(v)::value, W = decltype(wd)::value;
     const auto kernel = four ? conv_step_kernel<IT, V, W, 4> : conv_step_kernel<IT, V, W, 1>;
