@@ -17,7 +17,9 @@
 namespace gdr {
 namespace {
 
-constexpr int bwd_threads(int N) { return N == 4 ? 128 : 256; }
+// Threads of a block: 32 channel pairs (for N = 64: 16) by the N / 4 lanes of each.
+constexpr int kHalf = kTile / 2;
+constexpr int bwd_threads(int N) { return N == 64 ? 256 : 8 * N; }
 
 struct SsmBwdArgs {
   const void *x, *dt, *Bm, *Cm, *dy;
@@ -31,24 +33,23 @@ struct SsmBwdArgs {
 // formed (or finished) beside it.
 template <typename IT, int N>
 struct BwdSmem {
-  static constexpr int NT = bwd_threads(N), ML = N / 2, CB = 2 * NT / ML, WARPS = NT / 32;
+  static constexpr int NT = bwd_threads(N), ML = N / 4, CB = 2 * NT / ML, WARPS = NT / 32;
   static constexpr int QP = 4 * CB > NT ? 4 * CB / NT : 1;  // quads of channels of a tile per thread
   // what a thread's own copies bring: its quads of x, dt, dy of the next tile, its states of the next two
   Raw4<IT> raw[2][3][QP][NT];
-  float2 h[3][2][NT];
+  float4 h[3][2][NT];
   Pair2 du[2][kTile][CB / 2];                      // {D, D'}, {D x, D' x'} of a channel pair
   f32x2 dy[2][kTile][CB / 2];
   alignas(16) float x[2][kTile][CB], sig[2][kTile][CB];
-  // sum_n dh B and sum_n l A; padded so that the eight values (two of each, of two tokens and two
-  // channels) that the lanes of a pair hold, for the four pairs of a warp, hit 32 banks
+  // sum_n dh B and sum_n l A; padded for the stores of a warp's lanes
   static constexpr int SR = CB + 8, SN = kTile * SR + 16;
   alignas(16) float s[2][2][SN];
-  alignas(16) f32x2 B[2][kTile][N], C[2][kTile][N];      // each value twice
+  alignas(16) float B[2][kTile][N], C[2][kTile][N];
   float red[2][WARPS][kTile][2 * N];                     // dB, dC of a warp's channels
 };
 
 template <typename IT, int N>
-__global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, SsmBwdArgs a) {
+__global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_kernel(SsmDims d, SsmBwdArgs a) {
   using Smem = BwdSmem<IT, N>;
   constexpr int NT = Smem::NT, ML = Smem::ML, CB = Smem::CB, WARPS = Smem::WARPS, CL = 32 / ML;
   constexpr int Q = CB / 4, QP = Smem::QP;  // quads of channels; of a tile per thread
@@ -57,24 +58,29 @@ __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, S
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   if (ssm_bad(d)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nl = tid % ML, cl = lane / ML, pr = tid / ML;  // states 2 nl, 2 nl + 1 of channel pair pr
+  const int nl = tid % ML, cl = lane / ML, pr = tid / ML;  // states 4 nl .. 4 nl + 3 of channel pair pr
   const int blocks = (d.Dg + CB - 1) / CB, grp = blockIdx.x / blocks, blk = blockIdx.x - grp * blocks, c0 = blk * CB;
   const int nch = min(CB, d.Dg - c0);
   const long long dc0 = (long long)grp * d.Dg + c0;
-  const bool live0 = 2 * pr < nch, live1 = 2 * pr + 1 < nch;
+  const bool live[2] = {2 * pr < nch, 2 * pr + 1 < nch};
   const long long dch = dc0 + 2 * pr;
-  // pairs over the two channels, of state j; a missing channel has A = 0 and loads zeros
-  auto load_pair = [&](const float* p, f32x2 (&v)[2]) {  // p: [D][N]
-    const float2 u = live0 ? *reinterpret_cast<const float2*>(p + dch * N + 2 * nl) : make_float2(0.f, 0.f);
-    const float2 w = live1 ? *reinterpret_cast<const float2*>(p + (dch + 1) * N + 2 * nl) : make_float2(0.f, 0.f);
-    v[0] = pack2(u.x, w.x);
-    v[1] = pack2(u.y, w.y);
-  };
-  f32x2 A1[2], A2[2];
-  load_pair(a.A, A1);
+  // [channel][pair of states]; a missing channel has A = 0 and loads zeros
+  using States = f32x2[2][2];
+  auto load_states = [&](const float* p, States& v) {  // p: [D][N]
 #pragma unroll
-  for (int j = 0; j < 2; ++j) A2[j] = pack2(fmaxf(lo2(A1[j]) * kLog2e, -kBig), fmaxf(hi2(A1[j]) * kLog2e, -kBig));
-  f32x2 dA[2] = {0, 0};
+    for (int c = 0; c < 2; ++c) {
+      const float4 f = live[c] ? *reinterpret_cast<const float4*>(p + (dch + c) * N + 4 * nl) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[c][0] = pack2(f.x, f.y);
+      v[c][1] = pack2(f.z, f.w);
+    }
+  };
+  States A1, A2, dA = {};
+  load_states(a.A, A1);
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      A2[c][j] = pack2(fmaxf(lo2(A1[c][j]) * kLog2e, -kBig), fmaxf(hi2(A1[c][j]) * kLog2e, -kBig));
   float dDs[4] = {}, dbias[4] = {};
   const int qc = 4 * (tid % Q), qt = tid / Q, qn = qt < kTile ? nch - qc : 0;
   float bias[4] = {}, skip[4] = {};
@@ -88,8 +94,8 @@ __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, S
   const long long units = ssm_unit_count(d);
   for (long long un = blockIdx.y; un < units; un += gridDim.y) {
     const SsmUnit q = ssm_unit(d, un);
-    f32x2 dh[2] = {0, 0};
-    if (a.edge) load_pair(a.edge + (a.edge_per_unit ? un : q.seq) * (long long)d.D * N, dh);
+    States dh = {};
+    if (a.edge) load_states(a.edge + (a.edge_per_unit ? un : q.seq) * (long long)d.D * N, dh);
     const int tiles = (q.len + kTile - 1) / kTile;
     const IT* xq = (const IT*)a.x + (long long)q.t0 * d.ld_x + dc0 + qc;
     const IT* dq = (const IT*)a.dt + (long long)q.t0 * d.ld_dt + dc0 + qc;
@@ -101,9 +107,9 @@ __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, S
     auto whole = [&](int k) { return vec && nch == CB && (tiles - k) * kTile <= q.len; };
     auto fetch = [&](int k) {
       const int base = (tiles - 1 - k) * kTile;
-      const float* hs = a.h_saved + ((q.tile0 + tiles - 1 - k) * d.D + dch) * N + 2 * nl;
-      copy_async<8>(&sm.h[k % 3][0][tid], live0 ? hs : a.h_saved, live0 ? 8 : 0);
-      copy_async<8>(&sm.h[k % 3][1][tid], live1 ? hs + N : a.h_saved, live1 ? 8 : 0);
+      const float* hs = a.h_saved + ((q.tile0 + tiles - 1 - k) * d.D + dch) * N + 4 * nl;
+      copy_async<16>(&sm.h[k % 3][0][tid], live[0] ? hs : a.h_saved, live[0] ? 16 : 0);
+      copy_async<16>(&sm.h[k % 3][1][tid], live[1] ? hs + N : a.h_saved, live[1] ? 16 : 0);
       Raw4<IT>(*raw)[QP][NT] = sm.raw[k & 1];
       if (whole(k)) {
 #pragma unroll
@@ -168,9 +174,7 @@ __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, S
         if (e < 8 * N) {
           float v[4];
           rb[i].get(v);
-          f32x2* o = e < 4 * N ? &sm.B[buf][t][n] : &sm.C[buf][t][n];
-          reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[0], v[1], v[1]);
-          reinterpret_cast<float4*>(o)[1] = make_float4(v[2], v[2], v[3], v[3]);
+          *reinterpret_cast<float4*>(e < 4 * N ? &sm.B[buf][t][n] : &sm.C[buf][t][n]) = make_float4(v[0], v[1], v[2], v[3]);
         }
       }
     };
@@ -229,98 +233,155 @@ __global__ void __launch_bounds__(bwd_threads(N), 1) ssm_bwd_kernel(SsmDims d, S
       if (k > 0) finish(k - 1);  // before form overwrites this thread's own entries of that tile
       if (k + 1 < tiles) form(k + 1);
       if (k + 2 < tiles) fetch(k + 2);
-      f32x2 h[kTile + 1][2], e[kTile][2];  // h[t]: in front of token t
-      {
-        const float2 u = sm.h[k % 3][0][tid], w = sm.h[k % 3][1][tid];
-        h[0][0] = pack2(u.x, w.x);
-        h[0][1] = pack2(u.y, w.y);
-      }
-      // a token's operands are loaded a token ahead
-      Pair2 du = sm.du[buf][0][pr], b = *reinterpret_cast<const Pair2*>(&sm.B[buf][0][2 * nl]);
+      States h0;  // in front of the tile
 #pragma unroll
-      for (int t = 0; t < kTile; ++t) {
-        const Pair2 du_t = du, b_t = b;
-        if (t + 1 < kTile) {
-          du = sm.du[buf][t + 1][pr];
-          b = *reinterpret_cast<const Pair2*>(&sm.B[buf][t + 1][2 * nl]);
+      for (int c = 0; c < 2; ++c) {
+        const float4 f = sm.h[k % 3][c][tid];
+        h0[c][0] = pack2(f.x, f.y);
+        h0[c][1] = pack2(f.z, f.w);
+      }
+      struct Operands {
+        Pair2 du, b, c;
+        f32x2 dy;
+      };
+      auto load_db = [&](int t, Operands& o) {
+        o.du = sm.du[buf][t][pr];
+        o.b = *reinterpret_cast<const Pair2*>(&sm.B[buf][t][4 * nl]);
+      };
+      auto load_cy = [&](int t, Operands& o) {
+        o.c = *reinterpret_cast<const Pair2*>(&sm.C[buf][t][4 * nl]);
+        o.dy = sm.dy[buf][t][pr];
+      };
+      auto both = [](f32x2 v, int c) { return c ? pack2(hi2(v), hi2(v)) : pack2(lo2(v), lo2(v)); };
+      // from the state in front of token t to the one behind it; e: the decays
+      auto advance = [&](const Operands& o, const States& from, States& to, States& e) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const f32x2 dd = both(o.du.a, c), uu = both(o.du.b, c);
+          e[c][0] = ex2_2(mul2(dd, A2[c][0]));
+          e[c][1] = ex2_2(mul2(dd, A2[c][1]));
+          to[c][0] = fma2(e[c][0], from[c][0], mul2(uu, o.b.a));
+          to[c][1] = fma2(e[c][1], from[c][1], mul2(uu, o.b.b));
         }
-        e[t][0] = ex2_2(mul2(du_t.a, A2[0]));
-        e[t][1] = ex2_2(mul2(du_t.a, A2[1]));
-        h[t + 1][0] = fma2(e[t][0], h[t][0], mul2(du_t.b, b_t.a));
-        h[t + 1][1] = fma2(e[t][1], h[t][1], mul2(du_t.b, b_t.b));
-      }
-      f32x2 dyv = sm.dy[buf][kTile - 1][pr];
-      Pair2 c = *reinterpret_cast<const Pair2*>(&sm.C[buf][kTile - 1][2 * nl]);
-      f32x2 dAt[2] = {0, 0};  // a tile's part first: the long sum then has 1/16 of the terms
+      };
+      States dAt = {};  // a tile's part first: the long sum then has 1/16 of the terms
+      // half a tile: its states and decays in order, then its gradients in reverse
+      auto half = [&](int first, const States& from) {
+        States h[kHalf + 1], e[kHalf];
 #pragma unroll
-      for (int t2 = kTile - 2; t2 >= 0; t2 -= 2) {
-        float s[8];  // {s1, s1', s2, s2'} of tokens t2, t2 + 1
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int i = 1; i >= 0; --i) {
-          const int t = t2 + i;
-          const Pair2 du_t = du, b_t = b, c_t = c;
-          const f32x2 dy_t = dyv;
-          if (t > 0) {
-            du = sm.du[buf][t - 1][pr];
-            b = *reinterpret_cast<const Pair2*>(&sm.B[buf][t - 1][2 * nl]);
-            c = *reinterpret_cast<const Pair2*>(&sm.C[buf][t - 1][2 * nl]);
-            dyv = sm.dy[buf][t - 1][pr];
-          }
-          dh[0] = fma2(dy_t, c_t.a, dh[0]);
-          dh[1] = fma2(dy_t, c_t.b, dh[1]);
-          const f32x2 b0 = mul2(dh[0], du_t.b), b1 = mul2(dh[1], du_t.b);
-          const f32x2 c0v = mul2(dy_t, h[t + 1][0]), c1v = mul2(dy_t, h[t + 1][1]);
-          float w[4] = {lo2(b0) + hi2(b0), lo2(b1) + hi2(b1), lo2(c0v) + hi2(c0v), lo2(c1v) + hi2(c1v)};
-          using Chan = LaneSums<4, CL, ML>;  // over the warp's channel pairs
-          Chan::run(w, cl);
-          if (Chan::holds(cl)) {
+          for (int j = 0; j < 2; ++j) h[0][c][j] = from[c][j];
+        Operands nx;  // a token's operands are loaded a token ahead
+        load_db(first, nx);
 #pragma unroll
-            for (int v = 0; v < Chan::KEEP; ++v) {
-              const int vi = Chan::index(cl) + v;  // 0, 1: dB of states 2 nl, 2 nl + 1; 2, 3: dC
-              sm.red[buf][warp][t][(vi >> 1) * N + 2 * nl + (vi & 1)] = w[v];
+        for (int t = 0; t < kHalf; ++t) {
+          const Operands o = nx;
+          if (t + 1 < kHalf) load_db(first + t + 1, nx);
+          advance(o, h[t], h[t + 1], e[t]);
+        }
+        load_cy(first + kHalf - 1, nx);
+#pragma unroll
+        for (int t2 = kHalf - 2; t2 >= 0; t2 -= 2) {
+          float s[8];  // {s1, s1', s2, s2'} of tokens t2, t2 + 1
+#pragma unroll
+          for (int i = 1; i >= 0; --i) {
+            const int t = t2 + i;
+            const Operands o = nx;
+            if (t > 0) {
+              load_db(first + t - 1, nx);
+              load_cy(first + t - 1, nx);
+            }
+            f32x2 wb[2], wc[2];  // this pair's part of dB and dC of the four states
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const f32x2 dd = both(o.du.a, c), uu = both(o.du.b, c), yy = both(o.dy, c);
+              dh[c][0] = fma2(yy, o.c.a, dh[c][0]);
+              dh[c][1] = fma2(yy, o.c.b, dh[c][1]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                wb[j] = c ? fma2(dh[c][j], uu, wb[j]) : mul2(dh[c][j], uu);
+                wc[j] = c ? fma2(yy, h[t + 1][c][j], wc[j]) : mul2(yy, h[t + 1][c][j]);
+              }
+              const f32x2 s1 = fma2(dh[c][0], o.b.a, mul2(dh[c][1], o.b.b));
+              dh[c][0] = mul2(dh[c][0], e[t][c][0]);
+              dh[c][1] = mul2(dh[c][1], e[t][c][1]);
+              const f32x2 l0 = mul2(dh[c][0], h[t][c][0]), l1 = mul2(dh[c][1], h[t][c][1]);
+              const f32x2 s2 = fma2(l0, A1[c][0], mul2(l1, A1[c][1]));
+              dAt[c][0] = fma2(l0, dd, dAt[c][0]);
+              dAt[c][1] = fma2(l1, dd, dAt[c][1]);
+              s[4 * i + c] = lo2(s1) + hi2(s1);
+              s[4 * i + 2 + c] = lo2(s2) + hi2(s2);
+            }
+            float w[8] = {lo2(wb[0]), hi2(wb[0]), lo2(wb[1]), hi2(wb[1]), lo2(wc[0]), hi2(wc[0]), lo2(wc[1]), hi2(wc[1])};
+            using Chan = LaneSums<8, CL, ML>;  // over the warp's channel pairs
+            Chan::run(w, cl);
+            if (Chan::holds(cl)) {
+#pragma unroll
+              for (int v = 0; v < Chan::KEEP; ++v) {
+                const int vi = Chan::index(cl) + v;  // 0 .. 3: dB of states 4 nl ..; 4 .. 7: dC
+                sm.red[buf][warp][first + t][(vi >> 2) * N + 4 * nl + (vi & 3)] = w[v];
+              }
             }
           }
-          const f32x2 s1 = fma2(dh[0], b_t.a, mul2(dh[1], b_t.b));
-          dh[0] = mul2(dh[0], e[t][0]);
-          dh[1] = mul2(dh[1], e[t][1]);
-          const f32x2 l0 = mul2(dh[0], h[t][0]), l1 = mul2(dh[1], h[t][1]);
-          const f32x2 s2 = fma2(l0, A1[0], mul2(l1, A1[1]));
-          dAt[0] = fma2(l0, du_t.a, dAt[0]);
-          dAt[1] = fma2(l1, du_t.a, dAt[1]);
-          s[4 * i] = lo2(s1);
-          s[4 * i + 1] = hi2(s1);
-          s[4 * i + 2] = lo2(s2);
-          s[4 * i + 3] = hi2(s2);
-        }
-        using Chan = LaneSums<8, ML, 1>;  // over the states
-        Chan::run(s, nl);
-        if (Chan::holds(nl)) {
+          using Stat = LaneSums<8, ML, 1>;  // over the states
+          Stat::run(s, nl);
+          if (Stat::holds(nl)) {
 #pragma unroll
-          for (int v = 0; v < Chan::KEEP; ++v) {
-            const int vi = Chan::index(nl) + v;
-            sm.s[buf][(vi >> 1) & 1][(t2 + (vi >> 2)) * Smem::SR + 2 * pr + (vi & 1)] = s[v];
+            for (int v = 0; v < Stat::KEEP; ++v) {
+              const int vi = Stat::index(nl) + v;
+              sm.s[buf][(vi >> 1) & 1][(first + t2 + (vi >> 2)) * Smem::SR + 2 * pr + (vi & 1)] = s[v];
+            }
           }
         }
+      };
+      States mid;  // in front of the second half
+      {
+        States at, e;
+        Operands nx;
+        load_db(0, nx);
+#pragma unroll
+        for (int t = 0; t < kHalf; ++t) {
+          const Operands o = nx;
+          if (t + 1 < kHalf) load_db(t + 1, nx);
+          if (t == 0)
+            advance(o, h0, at, e);
+          else
+            advance(o, at, at, e);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) mid[c][j] = at[c][j];
       }
-      dA[0] = add2(dA[0], dAt[0]);
-      dA[1] = add2(dA[1], dAt[1]);
+      half(kHalf, mid);
+      half(0, h0);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) dA[c][j] = add2(dA[c][j], dAt[c][j]);
     }
     __syncthreads();
     if (tiles > 0) finish(tiles - 1);
     if (a.dS0 && q.first) {
-      float* o = a.dS0 + ((long long)q.seq * d.D + dch) * N + 2 * nl;
-      if (live0) *reinterpret_cast<float2*>(o) = make_float2(lo2(dh[0]), lo2(dh[1]));
-      if (live1) *reinterpret_cast<float2*>(o + N) = make_float2(hi2(dh[0]), hi2(dh[1]));
+      float* o = a.dS0 + ((long long)q.seq * d.D + dch) * N + 4 * nl;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (live[c])
+          *reinterpret_cast<float4*>(o + c * N) = make_float4(lo2(dh[c][0]), hi2(dh[c][0]), lo2(dh[c][1]), hi2(dh[c][1]));
     }
     __syncthreads();  // the next unit's first tile overwrites what finish read
   }
   // this row's sums over tokens: [N][D] of dA, [D] of dDskip, [D] of ddt_bias
   float* out = a.grads + (long long)blockIdx.y * (N + 2) * d.D;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if (live0) out[(long long)(2 * nl + j) * d.D + dch] = lo2(dA[j]);
-    if (live1) out[(long long)(2 * nl + j) * d.D + dch + 1] = hi2(dA[j]);
-  }
+  for (int c = 0; c < 2; ++c)
+    if (live[c])
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        out[(long long)(4 * nl + 2 * j) * d.D + dch + c] = lo2(dA[c][j]);
+        out[(long long)(4 * nl + 2 * j + 1) * d.D + dch + c] = hi2(dA[c][j]);
+      }
   // dDskip, ddt_bias: over the threads that held the same channels
   __syncthreads();
   float* cols = reinterpret_cast<float*>(smem_raw);  // [NT][8]
@@ -365,7 +426,7 @@ cudaError_t ssm_states(int N, F f) {
 
 }  // namespace
 
-int ssm_bwd_channels(int N) { return 2 * bwd_threads(N) / (N / 2); }
+int ssm_bwd_channels(int N) { return 2 * bwd_threads(N) / (N / 4); }
 
 int ssm_bwd_rows(const SsmDims& d) {
   const int cb = ssm_bwd_channels(d.N);
