@@ -5,21 +5,27 @@
 //   dB_t = sum_d dh_t D_t x_t,   dC_t = sum_d dy_t h_t,   ddt = dD_t softplus'(dt + dt_bias),   dS0 = a_0 dh_0.
 //
 // A block walks its units' tiles of 16 tokens from the last to the first.  The forward left the
-// state at the start of every tile, so the tile's 16 states and decays are formed again in registers
-// (a thread: two channels by two states) and then used in reverse.  Two channels share a register
-// pair for the packed fp32 instructions.  Sums: over n across the N / 2 lanes of a channel pair and over the
+// state at the start of every tile, so the tile's states and decays are formed again in registers and
+// then used in reverse.  Two states, or for the sums over channels two channels, share a register pair
+// for the packed fp32 instructions.  Sums: over n across the lanes of a channel pair and over the
 // channels of a warp, by exchanges that halve the values a lane keeps; over warps in shared memory;
 // over blocks by a second kernel from per-block partial rows, in order: results do not depend on timing.
-// Bound by instruction issue: about 20 per (token, channel, state) and thread, a third of them the
-// exchanges.
+// Bound by instruction issue and the return path of shared-memory loads together: B = 2, T = 4096,
+// D = 4096, N = 16, bf16: 510 us in this kernel (612 with two states per thread; 770 with the inputs'
+// loads in registers as well; 1020 with separate instructions).
 #include "gdr_ssm.cuh"
 
 namespace gdr {
 namespace {
 
-// Threads of a block: 32 channel pairs (for N = 64: 16) by the N / 4 lanes of each.
-constexpr int kHalf = kTile / 2;
-constexpr int bwd_threads(int N) { return N == 64 ? 256 : 8 * N; }
+// States per thread: two, or four.  With four what a token needs from shared memory serves eight states
+// of the two channels, and a tile's states and decays fit the registers in two halves, for a second
+// forward sweep over the first.  Both directions at B = 2, T = 4096, D = 2048, bf16, with two / four:
+//   N = 8: 351 / 541 us  (a channel pair's shared memory then serves too few threads)
+//   N = 16: 534 / 468 us
+//   N = 32: 946 / 1042 us, N = 64: 2010 / 1986 us  (more lanes to sum over; four spill 500 bytes)
+constexpr int bwd_states(int N) { return N == 16 ? 4 : 2; }
+constexpr int bwd_threads(int N) { return N == 4 ? 64 : N <= 16 ? 128 : 256; }
 
 struct SsmBwdArgs {
   const void *x, *dt, *Bm, *Cm, *dy;
@@ -33,14 +39,17 @@ struct SsmBwdArgs {
 // formed (or finished) beside it.
 template <typename IT, int N>
 struct BwdSmem {
-  static constexpr int NT = bwd_threads(N), ML = N / 4, CB = 2 * NT / ML, WARPS = NT / 32;
+  static constexpr int NT = bwd_threads(N), S = bwd_states(N), ML = N / S, CB = 2 * NT / ML, WARPS = NT / 32;
   static constexpr int QP = 4 * CB > NT ? 4 * CB / NT : 1;  // quads of channels of a tile per thread
-  // what a thread's own copies bring: its quads of x, dt, dy of the next tile, its states of the next two
-  Raw4<IT> raw[2][3][QP][NT];
-  float4 h[3][2][NT];
+  // what a thread's own copies bring: its quads of dt, dy of the next tile; of x, which the tile's end
+  // needs again, and its states, of three tiles
+  Raw4<IT> raw[2][2][QP][NT], x[3][QP][NT];
+  struct alignas(4 * S) Own {
+    float v[S];
+  } h[3][2][NT];
   Pair2 du[2][kTile][CB / 2];                      // {D, D'}, {D x, D' x'} of a channel pair
   f32x2 dy[2][kTile][CB / 2];
-  alignas(16) float x[2][kTile][CB], sig[2][kTile][CB];
+  alignas(16) float sig[2][kTile][CB];
   // sum_n dh B and sum_n l A; padded for the stores of a warp's lanes
   static constexpr int SR = CB + 8, SN = kTile * SR + 16;
   alignas(16) float s[2][2][SN];
@@ -51,35 +60,42 @@ struct BwdSmem {
 template <typename IT, int N>
 __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_kernel(SsmDims d, SsmBwdArgs a) {
   using Smem = BwdSmem<IT, N>;
-  constexpr int NT = Smem::NT, ML = Smem::ML, CB = Smem::CB, WARPS = Smem::WARPS, CL = 32 / ML;
+  constexpr int NT = Smem::NT, S = Smem::S, SP = S / 2, ML = Smem::ML, CB = Smem::CB, WARPS = Smem::WARPS, CL = 32 / ML;
+  constexpr int kHalf = S == 2 ? kTile : kTile / 2;  // tokens whose states are kept at a time
   constexpr int Q = CB / 4, QP = Smem::QP;  // quads of channels; of a tile per thread
   constexpr int BQ = (8 * N + NT - 1) / NT;                      // quads of B and C per thread
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   if (ssm_bad(d)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nl = tid % ML, cl = lane / ML, pr = tid / ML;  // states 4 nl .. 4 nl + 3 of channel pair pr
+  const int nl = tid % ML, cl = lane / ML, pr = tid / ML;  // states S nl .. S nl + S - 1 of channel pair pr
   const int blocks = (d.Dg + CB - 1) / CB, grp = blockIdx.x / blocks, blk = blockIdx.x - grp * blocks, c0 = blk * CB;
   const int nch = min(CB, d.Dg - c0);
   const long long dc0 = (long long)grp * d.Dg + c0;
   const bool live[2] = {2 * pr < nch, 2 * pr + 1 < nch};
   const long long dch = dc0 + 2 * pr;
   // [channel][pair of states]; a missing channel has A = 0 and loads zeros
-  using States = f32x2[2][2];
-  auto load_states = [&](const float* p, States& v) {  // p: [D][N]
+  using States = f32x2[2][SP];
+  using Own = typename Smem::Own;
+  auto unpack = [&](const Own(&o)[2], States& v) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const float4 f = live[c] ? *reinterpret_cast<const float4*>(p + (dch + c) * N + 4 * nl) : make_float4(0.f, 0.f, 0.f, 0.f);
-      v[c][0] = pack2(f.x, f.y);
-      v[c][1] = pack2(f.z, f.w);
-    }
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int j = 0; j < SP; ++j) v[c][j] = pack2(o[c].v[2 * j], o[c].v[2 * j + 1]);
+  };
+  auto load_states = [&](const float* p, States& v) {  // p: [D][N]
+    Own o[2] = {};
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (live[c]) o[c] = *reinterpret_cast<const Own*>(p + (dch + c) * N + S * nl);
+    unpack(o, v);
   };
   States A1, A2, dA = {};
   load_states(a.A, A1);
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < SP; ++j)
       A2[c][j] = pack2(fmaxf(lo2(A1[c][j]) * kLog2e, -kBig), fmaxf(hi2(A1[c][j]) * kLog2e, -kBig));
   float dDs[4] = {}, dbias[4] = {};
   const int qc = 4 * (tid % Q), qt = tid / Q, qn = qt < kTile ? nch - qc : 0;
@@ -107,18 +123,18 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
     auto whole = [&](int k) { return vec && nch == CB && (tiles - k) * kTile <= q.len; };
     auto fetch = [&](int k) {
       const int base = (tiles - 1 - k) * kTile;
-      const float* hs = a.h_saved + ((q.tile0 + tiles - 1 - k) * d.D + dch) * N + 4 * nl;
-      copy_async<16>(&sm.h[k % 3][0][tid], live[0] ? hs : a.h_saved, live[0] ? 16 : 0);
-      copy_async<16>(&sm.h[k % 3][1][tid], live[1] ? hs + N : a.h_saved, live[1] ? 16 : 0);
+      const float* hs = a.h_saved + ((q.tile0 + tiles - 1 - k) * d.D + dch) * N + S * nl;
+      copy_async<4 * S>(&sm.h[k % 3][0][tid], live[0] ? hs : a.h_saved, live[0] ? 4 * S : 0);
+      copy_async<4 * S>(&sm.h[k % 3][1][tid], live[1] ? hs + N : a.h_saved, live[1] ? 4 * S : 0);
       Raw4<IT>(*raw)[QP][NT] = sm.raw[k & 1];
       if (whole(k)) {
 #pragma unroll
         for (int i = 0; i < QP; ++i) {
           const long long t = base + qt + i * (NT / Q);
           if (qt < kTile) {
-            copy_async<sizeof(Raw4<IT>)>(&raw[0][i][tid], xq + t * d.ld_x, sizeof(Raw4<IT>));
-            copy_async<sizeof(Raw4<IT>)>(&raw[1][i][tid], dq + t * d.ld_dt, sizeof(Raw4<IT>));
-            copy_async<sizeof(Raw4<IT>)>(&raw[2][i][tid], yq + t * d.ld_dy, sizeof(Raw4<IT>));
+            copy_async<sizeof(Raw4<IT>)>(&sm.x[k % 3][i][tid], xq + t * d.ld_x, sizeof(Raw4<IT>));
+            copy_async<sizeof(Raw4<IT>)>(&raw[0][i][tid], dq + t * d.ld_dt, sizeof(Raw4<IT>));
+            copy_async<sizeof(Raw4<IT>)>(&raw[1][i][tid], yq + t * d.ld_dy, sizeof(Raw4<IT>));
           }
         }
       } else {
@@ -126,9 +142,9 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
         for (int i = 0; i < QP; ++i) {
           const long long t = base + qt + i * (NT / Q);
           const int n = t < q.len ? qn : 0;
-          raw[0][i][tid] = load_raw4(xq + t * d.ld_x, n, vec);
-          raw[1][i][tid] = load_raw4(dq + t * d.ld_dt, n, vec);
-          raw[2][i][tid] = load_raw4(yq + t * d.ld_dy, n, vec);
+          sm.x[k % 3][i][tid] = load_raw4(xq + t * d.ld_x, n, vec);
+          raw[0][i][tid] = load_raw4(dq + t * d.ld_dt, n, vec);
+          raw[1][i][tid] = load_raw4(yq + t * d.ld_dy, n, vec);
         }
       }
 #pragma unroll
@@ -148,9 +164,9 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
         const int tt = qt + i * (NT / Q);
         if (qt < kTile) {
           float xv[4], dv[4], yv[4], sg[4] = {1.f, 1.f, 1.f, 1.f};
-          sm.raw[buf][0][i][tid].get(xv);
-          sm.raw[buf][1][i][tid].get(dv);
-          sm.raw[buf][2][i][tid].get(yv);
+          sm.x[k % 3][i][tid].get(xv);
+          sm.raw[buf][0][i][tid].get(dv);
+          sm.raw[buf][1][i][tid].get(yv);
 #pragma unroll
           for (int c = 0; c < 4; c += 2) {
             f32x2 dl = add2(pack2(dv[c], dv[c + 1]), pack2(bias[c], bias[c + 1]));
@@ -164,7 +180,6 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
             sm.du[buf][tt][(qc + c) / 2] = Pair2{dl, mul2(dl, pack2(xv[c], xv[c + 1]))};
           }
           *reinterpret_cast<float4*>(&sm.dy[buf][tt][qc / 2]) = make_float4(yv[0], yv[1], yv[2], yv[3]);
-          *reinterpret_cast<float4*>(&sm.x[buf][tt][qc]) = make_float4(xv[0], xv[1], xv[2], xv[3]);
           *reinterpret_cast<float4*>(&sm.sig[buf][tt][qc]) = make_float4(sg[0], sg[1], sg[2], sg[3]);
         }
       }
@@ -187,12 +202,13 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
         if (qt < kTile && t < q.len) {
           const float4 s1 = *reinterpret_cast<const float4*>(&sm.s[buf][0][tt * Smem::SR + qc]);
           const float4 s2 = *reinterpret_cast<const float4*>(&sm.s[buf][1][tt * Smem::SR + qc]);
-          const float4 x4 = *reinterpret_cast<const float4*>(&sm.x[buf][tt][qc]);
           const float4 g4 = *reinterpret_cast<const float4*>(&sm.sig[buf][tt][qc]);
           const float4 y4 = *reinterpret_cast<const float4*>(&sm.dy[buf][tt][qc / 2]);
           const f32x2 d0 = sm.du[buf][tt][qc / 2].a, d1 = sm.du[buf][tt][qc / 2 + 1].a;
           const float s1v[4] = {s1.x, s1.y, s1.z, s1.w}, s2v[4] = {s2.x, s2.y, s2.z, s2.w};
-          const float xv[4] = {x4.x, x4.y, x4.z, x4.w}, gv[4] = {g4.x, g4.y, g4.z, g4.w}, yv[4] = {y4.x, y4.y, y4.z, y4.w};
+          float xv[4];
+          sm.x[k % 3][i][tid].get(xv);
+          const float gv[4] = {g4.x, g4.y, g4.z, g4.w}, yv[4] = {y4.x, y4.y, y4.z, y4.w};
           const float dl[4] = {lo2(d0), hi2(d0), lo2(d1), hi2(d1)};
           float ox[4], og[4];
 #pragma unroll
@@ -234,22 +250,24 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
       if (k + 1 < tiles) form(k + 1);
       if (k + 2 < tiles) fetch(k + 2);
       States h0;  // in front of the tile
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float4 f = sm.h[k % 3][c][tid];
-        h0[c][0] = pack2(f.x, f.y);
-        h0[c][1] = pack2(f.z, f.w);
+      {
+        const Own o[2] = {sm.h[k % 3][0][tid], sm.h[k % 3][1][tid]};
+        unpack(o, h0);
       }
+      struct alignas(8 * SP) Some {
+        f32x2 v[SP];
+      };
       struct Operands {
-        Pair2 du, b, c;
+        Pair2 du;
+        Some b, c;
         f32x2 dy;
       };
       auto load_db = [&](int t, Operands& o) {
         o.du = sm.du[buf][t][pr];
-        o.b = *reinterpret_cast<const Pair2*>(&sm.B[buf][t][4 * nl]);
+        o.b = *reinterpret_cast<const Some*>(&sm.B[buf][t][S * nl]);
       };
       auto load_cy = [&](int t, Operands& o) {
-        o.c = *reinterpret_cast<const Pair2*>(&sm.C[buf][t][4 * nl]);
+        o.c = *reinterpret_cast<const Some*>(&sm.C[buf][t][S * nl]);
         o.dy = sm.dy[buf][t][pr];
       };
       auto both = [](f32x2 v, int c) { return c ? pack2(hi2(v), hi2(v)) : pack2(lo2(v), lo2(v)); };
@@ -258,20 +276,21 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const f32x2 dd = both(o.du.a, c), uu = both(o.du.b, c);
-          e[c][0] = ex2_2(mul2(dd, A2[c][0]));
-          e[c][1] = ex2_2(mul2(dd, A2[c][1]));
-          to[c][0] = fma2(e[c][0], from[c][0], mul2(uu, o.b.a));
-          to[c][1] = fma2(e[c][1], from[c][1], mul2(uu, o.b.b));
+#pragma unroll
+          for (int j = 0; j < SP; ++j) {
+            e[c][j] = ex2_2(mul2(dd, A2[c][j]));
+            to[c][j] = fma2(e[c][j], from[c][j], mul2(uu, o.b.v[j]));
+          }
         }
       };
       States dAt = {};  // a tile's part first: the long sum then has 1/16 of the terms
-      // half a tile: its states and decays in order, then its gradients in reverse
+      // kHalf tokens: their states and decays in order, then their gradients in reverse
       auto half = [&](int first, const States& from) {
         States h[kHalf + 1], e[kHalf];
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) h[0][c][j] = from[c][j];
+          for (int j = 0; j < SP; ++j) h[0][c][j] = from[c][j];
         Operands nx;  // a token's operands are loaded a token ahead
         load_db(first, nx);
 #pragma unroll
@@ -292,35 +311,40 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
               load_db(first + t - 1, nx);
               load_cy(first + t - 1, nx);
             }
-            f32x2 wb[2], wc[2];  // this pair's part of dB and dC of the four states
+            f32x2 wb[SP], wc[SP];  // this pair's part of dB and dC of the states
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const f32x2 dd = both(o.du.a, c), uu = both(o.du.b, c), yy = both(o.dy, c);
-              dh[c][0] = fma2(yy, o.c.a, dh[c][0]);
-              dh[c][1] = fma2(yy, o.c.b, dh[c][1]);
+              f32x2 s1, s2;
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
+              for (int j = 0; j < SP; ++j) {
+                dh[c][j] = fma2(yy, o.c.v[j], dh[c][j]);
                 wb[j] = c ? fma2(dh[c][j], uu, wb[j]) : mul2(dh[c][j], uu);
                 wc[j] = c ? fma2(yy, h[t + 1][c][j], wc[j]) : mul2(yy, h[t + 1][c][j]);
+                s1 = j ? fma2(dh[c][j], o.b.v[j], s1) : mul2(dh[c][j], o.b.v[j]);
+                dh[c][j] = mul2(dh[c][j], e[t][c][j]);
+                const f32x2 l = mul2(dh[c][j], h[t][c][j]);
+                s2 = j ? fma2(l, A1[c][j], s2) : mul2(l, A1[c][j]);
+                dAt[c][j] = fma2(l, dd, dAt[c][j]);
               }
-              const f32x2 s1 = fma2(dh[c][0], o.b.a, mul2(dh[c][1], o.b.b));
-              dh[c][0] = mul2(dh[c][0], e[t][c][0]);
-              dh[c][1] = mul2(dh[c][1], e[t][c][1]);
-              const f32x2 l0 = mul2(dh[c][0], h[t][c][0]), l1 = mul2(dh[c][1], h[t][c][1]);
-              const f32x2 s2 = fma2(l0, A1[c][0], mul2(l1, A1[c][1]));
-              dAt[c][0] = fma2(l0, dd, dAt[c][0]);
-              dAt[c][1] = fma2(l1, dd, dAt[c][1]);
               s[4 * i + c] = lo2(s1) + hi2(s1);
               s[4 * i + 2 + c] = lo2(s2) + hi2(s2);
             }
-            float w[8] = {lo2(wb[0]), hi2(wb[0]), lo2(wb[1]), hi2(wb[1]), lo2(wc[0]), hi2(wc[0]), lo2(wc[1]), hi2(wc[1])};
-            using Chan = LaneSums<8, CL, ML>;  // over the warp's channel pairs
+            float w[2 * S];
+#pragma unroll
+            for (int j = 0; j < SP; ++j) {
+              w[2 * j] = lo2(wb[j]);
+              w[2 * j + 1] = hi2(wb[j]);
+              w[S + 2 * j] = lo2(wc[j]);
+              w[S + 2 * j + 1] = hi2(wc[j]);
+            }
+            using Chan = LaneSums<2 * S, CL, ML>;  // over the warp's channel pairs
             Chan::run(w, cl);
             if (Chan::holds(cl)) {
 #pragma unroll
               for (int v = 0; v < Chan::KEEP; ++v) {
-                const int vi = Chan::index(cl) + v;  // 0 .. 3: dB of states 4 nl ..; 4 .. 7: dC
-                sm.red[buf][warp][first + t][(vi >> 2) * N + 4 * nl + (vi & 3)] = w[v];
+                const int vi = Chan::index(cl) + v;  // dB of states S nl .., then dC
+                sm.red[buf][warp][first + t][(vi / S) * N + S * nl + vi % S] = w[v];
               }
             }
           }
@@ -335,40 +359,43 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
           }
         }
       };
-      States mid;  // in front of the second half
-      {
-        States at, e;
+      if constexpr (kHalf < kTile) {
+        States at[2], e;  // the state in front of the second half, turn about
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int j = 0; j < SP; ++j) at[0][c][j] = h0[c][j];
         Operands nx;
         load_db(0, nx);
 #pragma unroll
         for (int t = 0; t < kHalf; ++t) {
           const Operands o = nx;
           if (t + 1 < kHalf) load_db(t + 1, nx);
-          if (t == 0)
-            advance(o, h0, at, e);
-          else
-            advance(o, at, at, e);
+          advance(o, at[t & 1], at[(t + 1) & 1], e);
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) mid[c][j] = at[c][j];
+        half(kHalf, at[kHalf & 1]);
       }
-      half(kHalf, mid);
       half(0, h0);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) dA[c][j] = add2(dA[c][j], dAt[c][j]);
+        for (int j = 0; j < SP; ++j) dA[c][j] = add2(dA[c][j], dAt[c][j]);
     }
     __syncthreads();
     if (tiles > 0) finish(tiles - 1);
     if (a.dS0 && q.first) {
-      float* o = a.dS0 + ((long long)q.seq * d.D + dch) * N + 4 * nl;
+      float* o = a.dS0 + ((long long)q.seq * d.D + dch) * N + S * nl;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
-        if (live[c])
-          *reinterpret_cast<float4*>(o + c * N) = make_float4(lo2(dh[c][0]), hi2(dh[c][0]), lo2(dh[c][1]), hi2(dh[c][1]));
+        if (live[c]) {
+          Own v;
+#pragma unroll
+          for (int j = 0; j < SP; ++j) {
+            v.v[2 * j] = lo2(dh[c][j]);
+            v.v[2 * j + 1] = hi2(dh[c][j]);
+          }
+          *reinterpret_cast<Own*>(o + c * N) = v;
+        }
     }
     __syncthreads();  // the next unit's first tile overwrites what finish read
   }
@@ -378,9 +405,9 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
   for (int c = 0; c < 2; ++c)
     if (live[c])
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        out[(long long)(4 * nl + 2 * j) * d.D + dch + c] = lo2(dA[c][j]);
-        out[(long long)(4 * nl + 2 * j + 1) * d.D + dch + c] = hi2(dA[c][j]);
+      for (int j = 0; j < SP; ++j) {
+        out[(long long)(S * nl + 2 * j) * d.D + dch + c] = lo2(dA[c][j]);
+        out[(long long)(S * nl + 2 * j + 1) * d.D + dch + c] = hi2(dA[c][j]);
       }
   // dDskip, ddt_bias: over the threads that held the same channels
   __syncthreads();
@@ -426,7 +453,7 @@ cudaError_t ssm_states(int N, F f) {
 
 }  // namespace
 
-int ssm_bwd_channels(int N) { return 2 * bwd_threads(N) / (N / 4); }
+int ssm_bwd_channels(int N) { return 2 * bwd_threads(N) / (N / bwd_states(N)); }
 
 int ssm_bwd_rows(const SsmDims& d) {
   const int cb = ssm_bwd_channels(d.N);
