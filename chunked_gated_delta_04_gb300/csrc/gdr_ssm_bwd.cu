@@ -360,7 +360,8 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
         }
       };
       if constexpr (kHalf < kTile) {
-        States at[2], e;  // the state in front of the second half, turn about
+        static_assert(kHalf % 2 == 0, "the state in front of the second half ends in at[0]");
+        States at[2], e;  // turn about
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -373,9 +374,18 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
           if (t + 1 < kHalf) load_db(t + 1, nx);
           advance(o, at[t & 1], at[(t + 1) & 1], e);
         }
-        half(kHalf, at[kHalf & 1]);
+        // one copy of the code for both halves: it fills the instruction cache as it is
+#pragma unroll 1
+        for (int first = kHalf; first >= 0; first -= kHalf) {
+          half(first, at[0]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < SP; ++j) at[0][c][j] = h0[c][j];
+        }
+      } else {
+        half(0, h0);
       }
-      half(0, h0);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
