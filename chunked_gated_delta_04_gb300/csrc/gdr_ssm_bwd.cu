@@ -11,7 +11,7 @@
 // channels of a warp, by exchanges that halve the values a lane keeps; over warps in shared memory;
 // over blocks by a second kernel from per-block partial rows, in order: results do not depend on timing.
 // Bound by instruction issue and the return path of shared-memory loads together: B = 2, T = 4096,
-// D = 4096, N = 16, bf16: 510 us in this kernel (612 with two states per thread; 770 with the inputs'
+// D = 4096, N = 16, bf16: 479 us in this kernel (612 with two states per thread; 770 with the inputs'
 // loads in registers as well; 1020 with separate instructions).
 #include "gdr_ssm.cuh"
 
@@ -22,9 +22,8 @@ namespace {
 // of the two channels, and a tile's states and decays fit the registers in two halves, for a second
 // forward sweep over the first.  Both directions at B = 2, T = 4096, D = 2048, bf16, with two / four:
 //   N = 8: 351 / 541 us  (a channel pair's shared memory then serves too few threads)
-//   N = 16: 534 / 468 us
-//   N = 32: 946 / 1042 us, N = 64: 2010 / 1986 us  (more lanes to sum over; four spill 500 bytes)
-constexpr int bwd_states(int N) { return N == 16 ? 4 : 2; }
+//   N = 16: 534 / 456 us, N = 32: 945 / 841 us, N = 64: 2008 / 1686 us
+constexpr int bwd_states(int N) { return N >= 16 ? 4 : 2; }
 constexpr int bwd_threads(int N) { return N == 4 ? 64 : N <= 16 ? 128 : 256; }
 
 struct SsmBwdArgs {
@@ -374,7 +373,7 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
           if (t + 1 < kHalf) load_db(t + 1, nx);
           advance(o, at[t & 1], at[(t + 1) & 1], e);
         }
-        // one copy of the code for both halves: it fills the instruction cache as it is
+        // one copy of the code for both halves (two overflow the instruction cache: 506 us for 479)
 #pragma unroll 1
         for (int first = kHalf; first >= 0; first -= kHalf) {
           half(first, at[0]);
