@@ -82,13 +82,14 @@ long long token_stride(const Tensor& t, int inner) {
   int64_t ld = 0, span = 0;  // innermost leading dimension's stride; what the next one's has to be
   for (int64_t k = n - inner - 1; k >= 0; --k) {
     if (t.size(k) == 1) continue;
+    if (t.stride(k) < width) return -1;  // rows that overlap: a broadcast dimension's stride is 0
     if (ld == 0)
       ld = t.stride(k);
     else if (t.stride(k) != span)
       return -1;
     span = t.stride(k) * t.size(k);
   }
-  return ld != 0 && ld < width ? -1 : ld;
+  return ld;
 }
 long long strided(const char* name, const Tensor& t, int inner) {
   const long long ld = token_stride(t, inner);

@@ -505,3 +505,24 @@ def test_nothing_to_do(B, T):
     r, y = gdr.norm_forward(x, b, x, b, x, b)
     g = gdr.norm_backward(x, b, x, b, r, b, x, x)
     assert r.shape == y.shape == x.shape and not g[3].any() and not g[4].any() and not g[5].any()
+
+
+@pytest.mark.parametrize("B", [1, 3])
+def test_gradients_broadcast_over_tokens(B):
+    """The gradient of a mean over tokens comes as one row repeated (token stride 0): as if it were written out."""
+    r = gen(31)
+    T, C, N = 37, 24, 8
+    x, w, dt, z = r(B, T, C).cuda(), r(C, 4).cuda(), r(B, T, C, mul=0.3).cuda(), r(B, T, C).cuda()
+    A, Bm, Cm, wt = -torch.exp(r(C, N)).cuda(), r(B, T, 1, N).cuda(), r(B, T, 1, N).cuda(), r(C).cuda()
+    row = r(B, C).cuda()
+
+    def grads(f, shape_of_dy, *leaves):
+        ls = [t.clone().requires_grad_() for t in leaves]
+        return torch.autograd.grad(f(*ls), ls, shape_of_dy)
+
+    for f, leaves in ((lambda a, b: gdr.causal_conv(a, b)[0], (x, w)),
+                      (lambda a, b, c, d, e: gdr.selective_scan(a, b, c, d, e)[0], (x, dt, A, Bm, Cm)),
+                      (lambda a, b, c: gdr.block_norm(a, b, c)[0], (x, wt, z))):
+        dy = row[:, None].expand(B, T, C)
+        for a, b in zip(grads(f, dy, *leaves), grads(f, dy.contiguous(), *leaves)):
+            assert torch.equal(a, b)

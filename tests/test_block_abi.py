@@ -196,3 +196,18 @@ def test_token_strides():
     for bad in (base.transpose(0, 1), base[:, :4, 8:24], base[:, :, ::2]):
         with pytest.raises(ValueError):
             _ld("x", bad, 1)
+
+
+def test_token_strides_of_broadcast_rows():
+    """A row repeated over tokens or over the batch (stride 0) is no evenly spaced batch of rows."""
+    from chunked_gated_delta_04_gb300.block import _ld, _rows_ok
+
+    for t, inner in ((torch.zeros(1, 1, 16).expand(1, 5, 16), 1), (torch.zeros(2, 1, 16).expand(2, 5, 16), 1),
+                     (torch.zeros(1, 5, 16).expand(2, 5, 16), 1), (torch.zeros(1, 1, 1).expand(2, 5, 16), 1),
+                     (torch.zeros(2, 1, 2, 8).expand(2, 5, 2, 8), 2), (torch.zeros(1, 3, 16).expand(1, 3, 16)[:, :, :8], 1)):
+        if 0 in t.stride():
+            with pytest.raises(ValueError):
+                _ld("x", t, inner)
+            assert _rows_ok(t, inner).is_contiguous()
+        else:
+            assert _ld("x", t, inner) == 16
