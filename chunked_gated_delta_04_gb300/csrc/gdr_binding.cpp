@@ -14,6 +14,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <climits>
 #include <initializer_list>
 
 #include "../../include/gdr_block.h"
@@ -53,6 +54,12 @@ gdr_dtype type_code(at::ScalarType t) {
   if (t == at::kBFloat16) return GDR_DTYPE_BF16;
   TORCH_CHECK_VALUE(t == at::kFloat, "dtype ", t, ": float32 or bfloat16");
   return GDR_DTYPE_F32;
+}
+
+// A size as the library takes it: one that does not fit must not arrive as another.
+int size32(const char* name, int64_t v) {
+  TORCH_CHECK_VALUE(v <= INT_MAX, name, ": a size of ", v, " does not fit 32 bits");
+  return (int)v;
 }
 
 // An activation of the call: on the GPU, of a shape and type.
@@ -99,11 +106,11 @@ long long strided(const char* name, const Tensor& t, int inner) {
 }
 
 int sequences(const Tensor& cu, int64_t B) {
-  if (!cu.defined()) return (int)B;
+  if (!cu.defined()) return size32("x", B);
   TORCH_CHECK_VALUE(cu.is_cuda() && cu.scalar_type() == at::kInt && cu.dim() == 1 && cu.numel() >= 2 && cu.is_contiguous(),
                     "cu_seqlens: expected a contiguous CUDA int32 vector of at least 2 entries");
   TORCH_CHECK_VALUE(B == 1, "cu_seqlens needs a batch of 1 (the packed tokens)");
-  return (int)cu.numel() - 1;
+  return size32("cu_seqlens", cu.numel()) - 1;
 }
 
 void check_slots(const Tensor& slots, const Tensor& state, int64_t B) {
@@ -154,15 +161,15 @@ gdr_conv_problem conv_problem(const Tensor& x, const Tensor& w, const Tensor& b,
   const auto type = x.scalar_type();
   gdr_conv_problem p = {};
   p.dtype = type_code(type);
+  p.B = size32("x", B);
+  p.T = size32("x", T);
+  p.C = size32("x", C);
+  p.W = size32("weight", W);
   act("x", x, {B, T, C}, type);
   full("weight", w, {C, W});
   full("bias", b, {C});
   p.num_seqs = sequences(cu, B);
   full("initial_state", state, {p.num_seqs, W - 1, C}, type);
-  p.B = (int)B;
-  p.T = (int)T;
-  p.C = (int)C;
-  p.W = (int)W;
   p.cu_seqlens = (const int32_t*)ptr(cu);
   p.silu = (int)silu;
   p.ld_x = strided("x", x, 1);
@@ -219,18 +226,18 @@ PyObject* conv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto type = x.scalar_type();
   gdr_conv_problem p = {};
   p.dtype = type_code(type);
+  p.B = p.num_seqs = size32("x", B);
+  p.T = 1;
+  p.C = size32("x", C);
+  p.W = size32("weight", W);
+  p.num_slots = size32("state", state.size(0));
   act("x", x, {B, C}, type);
   full("weight", w, {C, W});
   full("bias", b, {C});
   full("state", state, {state.size(0), W - 1, C}, type);
   check_slots(slots, state, B);
-  p.B = p.num_seqs = (int)B;
-  p.T = 1;
-  p.C = (int)C;
-  p.W = (int)W;
   p.silu = (int)integer(a[5]);
   p.ld_x = strided("x", x, 1);
-  p.num_slots = (int)state.size(0);
   const Tensor y = fresh({B, C}, x);
   return answer(lib.gdr_conv_step(&p, ptr(x), (const float*)ptr(w), (const float*)ptr(b), ptr(state),
                                   (const int32_t*)ptr(slots), ptr(y), stream_of(x)),
@@ -250,6 +257,11 @@ gdr_ssm_problem ssm_problem(const SsmTensors& t, int lead, const Tensor& cu, lon
   const auto type = t.x.scalar_type();
   gdr_ssm_problem p = {};
   p.dtype = type_code(type);
+  p.B = size32("x", B);
+  p.T = size32("x", T);
+  p.D = size32("x", D);
+  p.N = size32("Bm", N);
+  p.G = size32("Bm", G);
   const std::array<int64_t, 3> row2 = {B, T, D};
   const std::array<int64_t, 4> bc2 = {B, T, G, N};
   const std::array<int64_t, 2> row1 = {B, D};
@@ -262,11 +274,6 @@ gdr_ssm_problem ssm_problem(const SsmTensors& t, int lead, const Tensor& cu, lon
   full("A", t.A, {D, N});
   full("D", t.D, {D});
   full("dt_bias", t.bias, {D});
-  p.B = (int)B;
-  p.T = (int)T;
-  p.D = (int)D;
-  p.N = (int)N;
-  p.G = (int)G;
   p.num_seqs = sequences(cu, B);
   p.cu_seqlens = (const int32_t*)ptr(cu);
   p.dt_softplus = (int)softplus;
@@ -340,7 +347,7 @@ PyObject* ssm_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(state.dim() == 3, "state: expected [num_slots, D, N], got ", state.sizes());
   full("state", state, {state.size(0), p.D, p.N});
   check_slots(slots, state, p.B);
-  p.num_slots = (int)state.size(0);
+  p.num_slots = size32("state", state.size(0));
   const Tensor y = fresh({p.B, p.D}, t.x);
   return answer(lib.gdr_ssm_step(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(t.A), ptr(t.Bm), ptr(t.Cm), (const float*)ptr(t.D),
                                  (const float*)ptr(t.bias), (float*)ptr(state), (const int32_t*)ptr(slots), ptr(y),
@@ -358,12 +365,12 @@ gdr_norm_problem norm_problem(const Tensor& x, const Tensor& post, const Tensor&
   gdr_norm_problem p = {};
   p.dtype = type_code(type);
   p.res_dtype = type_code(stream_type);
+  p.D = size32("x", D);
   act("x", x, x.sizes(), type);
   if (gate.defined()) act("gate", gate, x.sizes(), type);
   full("post_weight", post, {D});
   full("scale", scale, {D});
   full("pre_weight", pre, {D});
-  p.D = (int)D;
   p.eps = (float)eps;
   p.heads = 1;
   p.tokens = x.numel() / D;
@@ -371,7 +378,7 @@ gdr_norm_problem norm_problem(const Tensor& x, const Tensor& post, const Tensor&
   p.ld_x = token_stride(x, 1);
   p.ld_gate = gate.defined() ? token_stride(gate, 1) : 0;
   if ((p.ld_x < 0 || p.ld_gate < 0) && x.dim() > 2) {
-    p.heads = (int)x.size(-2);
+    p.heads = size32("x", x.size(-2));
     p.tokens = p.heads ? x.numel() / D / p.heads : 0;
     p.ld_x = strided("x", x, 2);
     p.ld_gate = gate.defined() ? strided("gate", gate, 2) : 0;
@@ -441,6 +448,13 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   gdr_problem p = {};
   p.dtype = type_code(type);
   p.layout = (gdr_state_layout)integer(a[6]);
+  p.B = p.num_seqs = size32("q", B);
+  p.T = 1;
+  p.Hk = size32("q", Hk);
+  p.Hv = size32("v", Hv);
+  p.DK = size32("q", DK);
+  p.DV = size32("v", DV);
+  const int num_slots = size32("state", state.size(0));
   full("q", q, {B, Hk, DK}, type);
   full("k", k, {B, Hk, DK}, type);
   full("v", v, {B, Hv, DV}, type);
@@ -449,16 +463,10 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool kv = p.layout == GDR_STATE_KV;
   full("state", state, {state.size(0), Hv, kv ? DK : DV, kv ? DV : DK});
   check_slots(slots, state, B);
-  p.B = p.num_seqs = (int)B;
-  p.T = 1;
-  p.Hk = (int)Hk;
-  p.Hv = (int)Hv;
-  p.DK = (int)DK;
-  p.DV = (int)DV;
   p.scale = (float)number(a[7]);
   p.prologue = (unsigned)integer(a[9]);
   const Tensor o = fresh({B, Hv, DV}, v);
-  return answer(lib.gdr_step(&p, ptr(q), ptr(k), ptr(v), (const float*)ptr(g), ptr(beta), (float*)ptr(state), (int)state.size(0),
+  return answer(lib.gdr_step(&p, ptr(q), ptr(k), ptr(v), (const float*)ptr(g), ptr(beta), (float*)ptr(state), num_slots,
                              (const int32_t*)ptr(slots), ptr(o), stream_of(q)),
                 o);
   END_HANDLE_TH_ERRORS

@@ -211,3 +211,21 @@ def test_token_strides_of_broadcast_rows():
             assert _rows_ok(t, inner).is_contiguous()
         else:
             assert _ld("x", t, inner) == 16
+
+
+def test_sizes_beyond_32_bits():
+    """A size that an int does not hold is refused, not cut to its low bits (the tensors here are one element)."""
+    def big(*shape, dtype=torch.float32):
+        return torch.zeros((1,) * len(shape), dtype=dtype).expand(shape)
+
+    n = (1 << 32) + 5
+    with pytest.raises(ValueError, match="does not fit 32 bits"):
+        gdr.conv_forward(big(1, n, 8), torch.zeros(8, 4))
+    with pytest.raises(ValueError, match="does not fit 32 bits"):
+        gdr.conv_step(big(2, 8), big(n, 3, 8), torch.zeros(8, 4))
+    with pytest.raises(ValueError, match="does not fit 32 bits"):
+        gdr.ssm_forward(big(1, n, 8), big(1, n, 8), torch.zeros(8, 4), big(1, n, 1, 4), big(1, n, 1, 4))
+    with pytest.raises(ValueError, match="does not fit 32 bits"):
+        gdr.norm_forward(big(2, n), big(n))
+    with pytest.raises(ValueError, match="does not fit 32 bits"):
+        gdr.step(big(1, 1, 16), big(1, 1, 16), big(1, 1, 16), big(1, 1), big(1, 1), big(n, 1, 16, 16))
