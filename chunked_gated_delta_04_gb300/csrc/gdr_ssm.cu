@@ -77,8 +77,7 @@ __global__ void __launch_bounds__(fwd_threads(NL))
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)  // finite, so that D = 0 past the end gives exp(0) = 1 also for A = -infinity
-      A2[c][j] = pack2(fmaxf(lo2(A2[c][j]) * kLog2e, -kBig), fmaxf(hi2(A2[c][j]) * kLog2e, -kBig));
+    for (int j = 0; j < 2; ++j) A2[c][j] = pack2(decay_rate(lo2(A2[c][j])), decay_rate(hi2(A2[c][j])));
   // staging: quad of channels qc of token qt (+ NT / Q tokens per further quad)
   const int qc = 4 * (tid % Q), qt = tid / Q, qn = qt < kTile ? nch - qc : 0;
   float bias[4] = {}, skip[4] = {};
@@ -287,7 +286,7 @@ __global__ void __launch_bounds__(256) ssm_join_kernel(SsmDims d, const float* _
   if (seq >= d.num_seqs) return;
   const long long u0 = d.cu ? d.unit_off[seq] : seq * d.seq_units;
   const int count = d.cu ? d.unit_off[seq + 1] - (int)u0 : d.seq_units;
-  const float a2 = fmaxf(A[dn] * kLog2e, -kBig);
+  const float a2 = decay_rate(A[dn]);
   const long long ch = dn / d.N;
   float cur = edge ? edge[seq * DN + dn] : 0.f;
   for (int k = 0; k < count; k += kAtOnce) {
@@ -419,8 +418,7 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmDims d, int B, int num
   }
   const float4 a = in ? *reinterpret_cast<const float4*>(A + (long long)ch * N + 4 * ln) : make_float4(0.f, 0.f, 0.f, 0.f);
   const float bias = in && dt_bias ? dt_bias[ch] : 0.f, skip = in && Dskip ? Dskip[ch] : 0.f;
-  const float a2[4] = {fmaxf(a.x * kLog2e, -kBig), fmaxf(a.y * kLog2e, -kBig), fmaxf(a.z * kLog2e, -kBig),
-                       fmaxf(a.w * kLog2e, -kBig)};
+  const float a2[4] = {decay_rate(a.x), decay_rate(a.y), decay_rate(a.z), decay_rate(a.w)};
   const int g = in ? ch / d.Dg : 0;
 #pragma unroll
   for (int r = 0; r < R; ++r) {

@@ -13,7 +13,12 @@
 namespace gdr {
 
 constexpr int kTile = 16;
-constexpr float kBig = 3.4e38f;
+// A log2(e), finite where A is -infinity, so that D = 0 past a sequence's end gives exp(0) = 1 there
+// too; a NaN stays one.
+__device__ __forceinline__ float decay_rate(float a) {
+  const float r = a * kLog2e;
+  return r < -3.4e38f ? -3.4e38f : r;
+}
 
 struct SsmDims {
   int D, N, G, Dg, T, num_seqs, softplus;

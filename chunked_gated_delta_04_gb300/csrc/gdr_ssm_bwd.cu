@@ -94,8 +94,7 @@ __global__ void __launch_bounds__(bwd_threads(N), 256 / bwd_threads(N)) ssm_bwd_
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int j = 0; j < SP; ++j)
-      A2[c][j] = pack2(fmaxf(lo2(A1[c][j]) * kLog2e, -kBig), fmaxf(hi2(A1[c][j]) * kLog2e, -kBig));
+    for (int j = 0; j < SP; ++j) A2[c][j] = pack2(decay_rate(lo2(A1[c][j])), decay_rate(hi2(A1[c][j])));
   float dDs[4] = {}, dbias[4] = {};
   const int qc = 4 * (tid % Q), qt = tid / Q, qn = qt < kTile ? nch - qc : 0;
   float bias[4] = {}, skip[4] = {};

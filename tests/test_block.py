@@ -237,6 +237,23 @@ def test_ssm_extremes():
     check(dict(y=y, S_T=S_T), ssm_ref(d, [40]))
 
 
+@pytest.mark.parametrize("what", ["A", "dt", "x", "Bm", "S0"])
+def test_ssm_nan_reaches_what_depends_on_it(what):
+    """A NaN in an input makes the outputs NaN that depend on it, and no others."""
+    d = ssm_inputs(F32, 8, 4, 1, [40], True)
+    at = {"A": (3, 2), "dt": (0, 30, 3), "x": (0, 30, 3), "Bm": (0, 30, 0, 1), "S0": (0, 3, 1)}[what]
+    d[what][at] = float("nan")
+    y, S_T, _ = gdr.ssm_forward(d["x"], d["dt"], d["A"], d["Bm"], d["Cm"], d["D"], d["dt_bias"], d["S0"])
+    t0 = 30 if what in ("dt", "x", "Bm") else 0
+    bad = torch.zeros(40, 8, dtype=torch.bool)
+    bad[t0:, slice(None) if what == "Bm" else 3] = True
+    assert torch.equal(y[0].isnan().cpu(), bad)
+    assert torch.equal(S_T[0].isnan().any(1).cpu(), bad[-1])
+    pool = d["S0"].clone()
+    ys = gdr.ssm_step(d["x"][:, 30], d["dt"][:, 30], d["A"], d["Bm"][:, 30], d["Cm"][:, 30], pool, d["D"], d["dt_bias"])
+    assert torch.equal(ys[0].isnan().cpu(), bad[30])
+
+
 @pytest.mark.parametrize("dtype,D,N,G", [(F32, 33, 4, 1), (BF, 64, 16, 2), (BF, 24, 64, 1), (F32, 130, 8, 1)])
 def test_ssm_step(dtype, D, N, G):
     d = ssm_inputs(dtype, D, N, G, [7], False)
