@@ -4,7 +4,7 @@ convolution, the selective state space scan, the block norms and the single-toke
 The functions here check shapes, types and strides, allocate outputs and workspace and make the call
 (in ``csrc/gdr_binding.cpp``), and raise: ``ValueError`` for what they find themselves, ``GDRError`` for
 a status.  Everything runs on the current stream, or on ``stream`` if one is given: outputs and
-workspace are then allocated on that stream, and the caller orders the inputs before it.
+workspace are then allocated on that stream, and the caller orders the inputs before it and keeps them until it is done.
 
     conv_forward, conv_backward, conv_step, causal_conv        (autograd)
     ssm_forward, ssm_backward, ssm_step, selective_scan        (autograd)
@@ -282,6 +282,8 @@ class _NormFunction(torch.autograd.Function):
         x, post_weight, gate, scale, r, pre_weight = ctx.saved_tensors
         if pre_weight is not None and dy is None:
             dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+        if pre_weight is not None and r is None:  # a plain norm's backward takes x as the r it was applied to
+            x = x.contiguous()
         if pre_weight is None and dr is None:
             dr = torch.zeros(x.shape, dtype=x.dtype if r is None else r.dtype, device=x.device)
         dx, dgate, dres, dpost, dscale, dpre = norm_backward(

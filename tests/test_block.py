@@ -543,3 +543,15 @@ def test_gradients_broadcast_over_tokens(B):
         dy = row[:, None].expand(B, T, C)
         for a, b in zip(grads(f, dy, *leaves), grads(f, dy.contiguous(), *leaves)):
             assert torch.equal(a, b)
+
+
+def test_plain_norm_of_a_slice_has_a_gradient():
+    r = gen(33)
+    big, w, dy = r(7, 48).cuda(), r(16).cuda(), r(7, 16).cuda()
+
+    def grads(x):
+        x, v = x.detach().requires_grad_(), w.clone().requires_grad_()
+        return torch.autograd.grad(gdr.block_norm(x, pre_weight=v)[1], (x, v), dy)
+
+    for a, b in zip(grads(big[:, 16:32]), grads(big[:, 16:32].contiguous())):
+        assert torch.equal(a, b)
