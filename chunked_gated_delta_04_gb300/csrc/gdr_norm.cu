@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(NormDims d, F
   };
   auto load = [&](long long row, Row& o) {
     const int D = row < d.rows ? d.D : 0;  // a missing row is zeros and is not stored
-    const long long tok = row / d.heads, at = (row - tok * d.heads) * d.D;
+    const long long tok = token_of(d, row), at = (row - tok * d.heads) * d.D;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       o.x[k] = load_raw8<TPR, SIDE>((const IT*)a.x + tok * d.ld_x + at, k, i0, D, d.vec);
@@ -135,6 +135,10 @@ gdr_status resolve_norm(const gdr_norm_problem* p, NormDims* d) {
   d->D = p->D;
   d->ld_x = p->ld_x ? p->ld_x : w;
   d->ld_gate = p->ld_gate ? p->ld_gate : w;
+  if (d->ld_x == w && d->ld_gate == w) {  // heads without a gap are rows like any others
+    d->heads = 1;
+    d->ld_x = d->ld_gate = p->D;
+  }
   d->eps = p->eps;
   d->vec = 0;
   return GDR_OK;

@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
   };
   auto load = [&](long long row, Row& o) {
     const int D = row < d.rows ? d.D : 0;  // a missing row is zeros and is not stored
-    const long long tok = row / d.heads, at = (row - tok * d.heads) * d.D;
+    const long long tok = token_of(d, row), at = (row - tok * d.heads) * d.D;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (need_x) o.x[k] = load_raw8<TPR, SIDE>((const IT*)a.x + tok * d.ld_x + at, k, i0, D, d.vec);
