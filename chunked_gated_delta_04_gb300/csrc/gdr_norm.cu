@@ -18,9 +18,15 @@ struct FwdPtrs {
   void *r, *y;
 };
 
+// Blocks per SM to fit the registers to (0: the compiler's choice).  Rows of 512 threads with everything
+// take 72 registers unasked, which leaves one block per SM: 8192 x 4096, bf16 with an fp32 stream, 108 us; with 64
+// registers and two blocks 80 us.  Wider rows would spill; narrower ones are better off unasked (8192 x
+// 2048, add: 22.4 us against 23.6).
+constexpr int fwd_min_blocks(int TPR, int K) { return TPR == 512 && K == 1 ? 2 : 0; }
+
 // A block walks rows and has the next ones' loads in flight while it works on the present ones.
 template <typename IT, typename RT, int TPR, int K, int PARTS, bool SIDE>
-__global__ void __launch_bounds__(norm_block(TPR)) norm_fwd_kernel(NormDims d, FwdPtrs a) {
+__global__ void __launch_bounds__(norm_block(TPR), fwd_min_blocks(TPR, K)) norm_fwd_kernel(NormDims d, FwdPtrs a) {
   constexpr int kRows = norm_rows(TPR);
   __shared__ float red[TPR > 32 ? 2 * TPR / 32 : 1];
   int flip = 0;
