@@ -5,6 +5,20 @@
 
 namespace gdr {
 
+// Shared memory in which a thread's part of the next row waits, or 0.  Rows of one chunk per thread
+// are loaded a row ahead into registers; of two chunks there is no room for that: gated rows and those of a
+// residual add have the next row's copies under way here (4096 x 8192 bf16, backward: gated 101 -> 77 us, add 96 -> 75,
+// 2048 x 8192 add in fp32 84 -> 79).  With everything the sums and weights of both norms already fill the
+// registers and the shared memory's port, and it would cost (192 -> 230 us).
+template <typename IT, typename RT, int TPR, int K, int PARTS, bool SIDE>
+constexpr size_t norm_stage_bytes() {
+  constexpr size_t chunk = (size_t)TPR * K, in = sizeof(Raw8<IT>), res = sizeof(Raw8<RT>);
+  constexpr bool x = PARTS & (kNormPost | kNormGate | kNormScale), z = PARTS & kNormGate;
+  constexpr bool pre = PARTS & kNormPre;
+  constexpr size_t bytes = chunk * ((x ? in : 0) + (z ? in : 0) + (pre ? in + res : 0) + res);
+  return TPR > 32 && K == 2 && !SIDE && PARTS >= 0 && !(x && pre) ? bytes : 0;
+}
+
 // Rows of more than a warp: the weights stay in shared memory (3 x D floats), since a row's work is
 // a chain of two block sums and each read of a weight from the L2 would lengthen it (8192 x 4096
 // with everything, fp32 stream: 193 us with global reads, 136 us with these).
@@ -12,6 +26,7 @@ template <typename IT, typename RT, int TPR, int K, int PARTS, bool SIDE>
 __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, NormBwdPtrs a) {
   constexpr int kBlock = norm_block(TPR), kRows = norm_rows(TPR);
   constexpr bool kAhead = K == 1;  // two rows in registers; wider ones would spill
+  constexpr bool kStage = norm_stage_bytes<IT, RT, TPR, K, PARTS, SIDE>() > 0;
   __shared__ float red[TPR > 32 ? 8 * TPR / 32 : 1];  // two buffers of 3 sums, two of 1
   __shared__ float cols[kRows > 1 ? kBlock * 8 : 1];
   int flip = 0, flip1 = 0;
@@ -67,13 +82,45 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
       if (gate) o.z[k] = load_raw8<TPR, SIDE>((const IT*)a.gate + tok * d.ld_gate + at, k, i0, D, d.vec);
     }
   };
+  // The same through shared memory: 16-byte pieces, each thread's own, in the order of load().  start: the
+  // copies; else from there to o.
+  auto staged = [&](long long row, Row& o, auto start) {
+    uint4* slot = reinterpret_cast<uint4*>(weights + 3 * Dp) + i0;
+    const long long tok = row / d.heads, at = (row - tok * d.heads) * d.D;
+    auto move = [&](const auto* p, auto& raw, int k) {
+      constexpr int kPieces = sizeof(raw) / 16;
+      const int c = channel<TPR, SIDE>(k, i0, 0);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i, slot += TPR)
+        if constexpr (decltype(start)::value)
+          copy_async<16>(slot, c < d.D ? reinterpret_cast<const uint4*>(p + c) + i : reinterpret_cast<const uint4*>(p), c < d.D ? 16 : 0);
+        else
+          reinterpret_cast<uint4*>(&raw)[i] = *slot;
+    };
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (need_x) move((const IT*)a.x + tok * d.ld_x + at, o.x[k], k);
+      if (pre) {
+        move((const RT*)a.r + row * d.D, o.r[k], k);
+        move((const IT*)a.dy + row * d.D, o.dy[k], k);
+      }
+      if (has_dr) move((const RT*)a.dr + row * d.D, o.dr[k], k);
+      if (gate) move((const IT*)a.gate + tok * d.ld_gate + at, o.z[k], k);
+    }
+  };
   const long long step = (long long)gridDim.x * kRows;
   long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
   Row cur;
   if (kAhead) load(row, cur);
+  if (kStage && row < d.rows) staged(row, cur, std::true_type{});
   for (long long base = (long long)blockIdx.x * kRows; base < d.rows; base += step, row += step) {
     Row next;
-    if (!kAhead) load(row, cur);
+    if (kStage) {
+      copy_async_wait();
+      staged(row, cur, std::false_type{});
+    } else if (!kAhead) {
+      load(row, cur);
+    }
     if (kAhead && base + step < d.rows) load(row + step, next);
     const int D = row < d.rows ? d.D : 0;
     float du[K][8], t[8], v[8], w[8];
@@ -97,6 +144,7 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_bwd_kernel(NormDims d, N
       }
     }
     if (post || pre) row_sums<TPR, 3>(s, red, flip);
+    if (kStage && base + step < d.rows) staged(row + step, cur, std::true_type{});  // behind the sums' barrier: the slots are read
     const float rx = post ? rsqrtf(s[0] * inv + d.eps) : 1.f;
     const float rr = rsqrtf(s[1] * inv + d.eps), m1 = s[2] * inv * rr;  // m1: mean(t rh)
     float q[1] = {0.f};
@@ -197,8 +245,10 @@ cudaError_t norm_bwd_launch(const NormDims& d, const NormBwdPtrs& a, int parts, 
     return norm_parts(parts, [&](auto pt) {
       return norm_side<TPR>(d.vec, [&](auto side) {
         constexpr auto kernel = norm_bwd_kernel<IT, RT, TPR, K, decltype(pt)::value, decltype(side)::value>;
-        constexpr size_t widest = TPR > 32 ? 3 * sizeof(float) * 8 * TPR * K : 0;  // for the shape's widest row
-        const size_t smem = TPR > 32 ? 3 * sizeof(float) * (size_t)((d.D + 7) & ~7) : 0;
+        constexpr size_t stage = norm_stage_bytes<IT, RT, TPR, K, decltype(pt)::value, decltype(side)::value>();
+        constexpr size_t widest = TPR > 32 ? 3 * sizeof(float) * 8 * TPR * K + stage : 0;  // for the shape's widest row
+        const size_t smem = TPR > 32 ? 3 * sizeof(float) * (size_t)((d.D + 7) & ~7) + stage : 0;
+        static_assert(widest + 1024 <= 227 * 1024, "shared memory of a block");
         if (smem > 0) {
           const cudaError_t e = set_smem_once((const void*)kernel, widest);
           if (e != cudaSuccess) return e;

@@ -331,6 +331,17 @@ def test_norm_many_rows(rows):
         norm_check(norm_run(d), d)
 
 
+@pytest.mark.parametrize("types", [(F32, F32), (BF, BF), (BF, F32)])
+@pytest.mark.parametrize("mode", ["full", "add", "gated", "scale"])
+def test_norm_wide_rows_in_turn(types, mode):
+    """Rows of a block each, more of them than blocks: the next row is under way while one is worked on."""
+    if types == (BF, F32) and not MODES[mode][3]:
+        pytest.skip("no residual")
+    for D in (4104, 8192):
+        d = norm_inputs(mode, *types, (333, D))
+        norm_check(norm_run(d), d)
+
+
 def test_norm_rows_of_heads_in_a_wider_tensor():
     B, T, H, D = 2, 5, 3, 64
     d = norm_inputs("gated", BF, BF, (B, T, H, D))
