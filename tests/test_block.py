@@ -566,3 +566,62 @@ def test_plain_norm_of_a_slice_has_a_gradient():
 
     for a, b in zip(grads(big[:, 16:32]), grads(big[:, 16:32].contiguous())):
         assert torch.equal(a, b)
+
+
+def test_packed_tokens_beyond_32_bit_offsets():
+    """The last sequence of a packed batch whose elements lie past 2^31: as the sequence alone."""
+    r = gen(41)
+    C, N, lens = 2048, 4, [1 << 20, 37]
+    T, n = sum(lens), lens[1]
+
+    def tail(*shape, mul=1.0):
+        t = torch.zeros(1, T, *shape, dtype=BF, device="cuda")
+        t[:, -n:] = r(1, n, *shape, dtype=BF, mul=mul).cuda()
+        return t
+
+    cu = cu_of(lens).cuda()
+    x, dy, dt, Bm, Cm = tail(C), tail(C), tail(C, mul=0.5), tail(1, N), tail(1, N)
+    w, A, b = r(C, 4).cuda(), -torch.exp(r(C, N)).cuda(), r(C).cuda()
+
+    def last(t):
+        return t[:, -n:].contiguous()
+
+    y, _ = gdr.conv_forward(x, w, b, None, cu)
+    dx = gdr.conv_backward(x, w, b, dy, None, None, cu)[0]
+    assert torch.equal(last(y), gdr.conv_forward(last(x), w, b)[0])
+    assert torch.equal(last(dx), gdr.conv_backward(last(x), w, b, last(dy))[0])
+    del y, dx
+    y, S, saved = gdr.ssm_forward(x, dt, A, Bm, Cm, b, None, None, cu)
+    g = gdr.ssm_backward(x, dt, A, Bm, Cm, saved, dy, b, None, None, cu)
+    y1, S1, saved1 = gdr.ssm_forward(last(x), last(dt), A, last(Bm), last(Cm), b)
+    g1 = gdr.ssm_backward(last(x), last(dt), A, last(Bm), last(Cm), saved1, last(dy), b)
+    assert torch.equal(last(y), y1) and torch.equal(S[1:], S1)
+    for i in (0, 1, 3, 4):
+        assert torch.equal(last(g[i]), g1[i]), i
+    del y, S, saved, g
+    out = gdr.norm_forward(x, b, dy)[0]
+    assert torch.equal(last(out), gdr.norm_forward(last(x), b, last(dy))[0])
+    d, d1 = gdr.norm_backward(x, b, dy, dr=dt), gdr.norm_backward(last(x), b, last(dy), dr=last(dt))
+    assert torch.equal(last(d[0]), d1[0]) and torch.equal(last(d[1]), d1[1])
+
+
+def test_pools_beyond_32_bit_offsets():
+    """A slot whose state lies past 2^31 elements of the pool: as in a pool of one."""
+    r = gen(42)
+    slot = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def both(state, call):  # state: [1, ...]; the call's outputs and the states after it
+        at = (1 << 31) // state[0].numel() + 1
+        pool = torch.empty(at + 1, *state.shape[1:], dtype=state.dtype, device="cuda")
+        pool[at] = state[0]
+        one = state.clone()
+        assert torch.equal(call(pool, slot + at), call(one, slot))
+        assert torch.equal(pool[at], one[0])
+
+    x, w = r(1, 2048, dtype=BF).cuda(), r(2048, 4).cuda()
+    both(r(1, 3, 2048, dtype=BF).cuda(), lambda p, s: gdr.conv_step(x, p, w, None, s))
+    A, bc = -torch.exp(r(2048, 16)).cuda(), r(1, 1, 16, dtype=BF).cuda()
+    both(r(1, 2048, 16).cuda(), lambda p, s: gdr.ssm_step(x, x, A, bc, bc, p, None, None, s))
+    q, g, beta = r(1, 2, 128, dtype=BF).cuda(), -r(1, 2).abs().cuda(), torch.sigmoid(r(1, 2, dtype=BF)).cuda()
+    for layout in ("KV", "VK"):
+        both(r(1, 2, 128, 128).cuda(), lambda p, s: gdr.step(q, q, q, g, beta, p, layout, None, s, gdr.GDR_PROLOGUE_QK_L2NORM))
