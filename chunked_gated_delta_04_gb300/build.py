@@ -98,7 +98,7 @@ def build_binding(force: bool = False) -> str:
             if f.read() == stamp and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
                 return BINDING
     tmp = BINDING + f".tmp{os.getpid()}"
-    r = subprocess.run(["g++"] + flags + [BINDING_SRC, "-o", tmp, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"],
+    r = subprocess.run(["g++"] + flags + [BINDING_SRC, "-o", tmp, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")

@@ -2,14 +2,14 @@
 // and strides, allocation of outputs and workspace, and the call on the current stream.
 //
 // A decoding step's kernel runs 2 to 10 us; marshalled in Python a call took 11 to 15 us of host time
-// on the GPU's host (attributes of eight tensors, the allocator, the foreign call), here 4 to 5.  The
+// on the GPU's host (attributes of eight tensors, the allocator, the foreign call), here 3 to 5.  The
 // library's entry points are bound by address, so this module does not link against it and follows
 // the library that the package has open.  Errors: ValueError for what is found here, the status
 // number for what the library refuses (the package raises GDRError from it).
 #include <Python.h>
 
 #include <ATen/core/TensorBody.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -125,10 +125,14 @@ void check_slots(const Tensor& slots, const Tensor& state, int64_t B) {
 
 gdr_stream_t stream_of(const Tensor& t) { return (gdr_stream_t)c10::cuda::getCurrentCUDAStream(t.get_device()).stream(); }
 
-Tensor fresh(IntArrayRef shape, const Tensor& like) { return at::empty(shape, like.options()); }
-Tensor fresh_f32(IntArrayRef shape, const Tensor& like) { return at::empty(shape, like.options().dtype(at::kFloat)); }
+// Uninitialised, on the current stream; without the dispatcher, which takes as long as the allocation.
+Tensor fresh_of(IntArrayRef shape, at::ScalarType type, const Tensor& like) {
+  return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
+}
+Tensor fresh(IntArrayRef shape, const Tensor& like) { return fresh_of(shape, like.scalar_type(), like); }
+Tensor fresh_f32(IntArrayRef shape, const Tensor& like) { return fresh_of(shape, at::kFloat, like); }
 Tensor workspace(size_t bytes, const Tensor& like) {  // torch's blocks are 512-byte aligned
-  return bytes ? at::empty({(int64_t)bytes}, like.options().dtype(at::kByte)) : Tensor();
+  return bytes ? fresh_of({(int64_t)bytes}, at::kByte, like) : Tensor();
 }
 
 PyObject* answer(gdr_status st, const Tensor& t) { return st == GDR_OK ? THPVariable_Wrap(t) : PyLong_FromLong(st); }
