@@ -21,6 +21,8 @@ import sys
 
 import torch
 
+from ._autograd import first_order, link
+
 _c = ctypes
 _P, _I, _LL, _SZ, _F = _c.c_void_p, _c.c_int, _c.c_longlong, _c.c_size_t, _c.c_float
 
@@ -166,6 +168,7 @@ class _ConvFunction(torch.autograd.Function):
         return conv_forward(x, weight, bias, initial_state, cu_seqlens, activation, output_final_state=True)
 
     @staticmethod
+    @first_order("causal_conv")
     def backward(ctx, dy, dlast):
         x, weight, bias, state, cu = ctx.saved_tensors
         dy = torch.zeros_like(x) if dy is None else _rows_ok(dy, 1)
@@ -220,20 +223,21 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, slots=None, dt_softp
 
 class _SSMFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus):
+    def forward(ctx, x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus, S0_link):
         y, S_T, saved = ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus)
-        ctx.save_for_backward(x, dt, A, Bm, Cm, D, dt_bias, saved, cu_seqlens)
+        ctx.save_for_backward(x, dt, A, Bm, Cm, D, dt_bias, saved, cu_seqlens, S0_link)
         ctx.dt_softplus, ctx.has_S0 = dt_softplus, S0 is not None
         ctx.set_materialize_grads(False)
         return y, S_T
 
     @staticmethod
+    @first_order("selective_scan")
     def backward(ctx, dy, dS_T):
-        x, dt, A, Bm, Cm, D, dt_bias, saved, cu = ctx.saved_tensors
+        x, dt, A, Bm, Cm, D, dt_bias, saved, cu, _ = ctx.saved_tensors
         dy = torch.zeros_like(x) if dy is None else _rows_ok(dy, 1)
         grads = ssm_backward(x, dt, A, Bm, Cm, saved, dy, D, dt_bias, None if dS_T is None else dS_T.contiguous(), cu,
                              ctx.dt_softplus, want_dS0=ctx.has_S0)
-        return (*grads, None, None)
+        return (*grads, None, None, None)
 
 
 def selective_scan(x, dt, A, Bm, Cm, D=None, dt_bias=None, initial_state=None, cu_seqlens=None, dt_softplus=True):
@@ -242,7 +246,8 @@ def selective_scan(x, dt, A, Bm, Cm, D=None, dt_bias=None, initial_state=None, c
     def f(t):
         return None if t is None else t.float()
 
-    return _SSMFunction.apply(x, dt, f(A), Bm, Cm, f(D), f(dt_bias), initial_state, cu_seqlens, dt_softplus)
+    return _SSMFunction.apply(x, dt, f(A), Bm, Cm, f(D), f(dt_bias), initial_state, cu_seqlens, dt_softplus,
+                              link(initial_state))
 
 
 # ---------------------------------------------------------------------------------- block norms
@@ -278,6 +283,7 @@ class _NormFunction(torch.autograd.Function):
         return r, y
 
     @staticmethod
+    @first_order("block_norm")
     def backward(ctx, dr, dy):
         x, post_weight, gate, scale, r, pre_weight = ctx.saved_tensors
         if pre_weight is not None and dy is None:
