@@ -27,6 +27,7 @@ from typing import Optional
 import torch
 
 from . import block as _block
+from ._autograd import first_order as _first_order, link as _link
 from .block import (  # noqa: F401 - the operators around the gated delta rule
     BLOCK_EXPORTS, block_norm, causal_conv, conv_backward, conv_forward, conv_step, gdr_conv_problem,
     gdr_norm_problem, gdr_ssm_problem, norm_backward, norm_forward, selective_scan, ssm_backward, ssm_forward,
@@ -396,22 +397,23 @@ def backward(q, k, v, g, beta, h_saved, dO, dS_T=None, cu_seqlens=None, layout="
 
 class _GDRFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, g, beta, S0, cu_seqlens, layout, scale, h_dtype, prologue, save_wy, cp_fwd, cp_bwd):
+    def forward(ctx, q, k, v, g, beta, S0, cu_seqlens, layout, scale, h_dtype, prologue, save_wy, cp_fwd, cp_bwd, S0_link):
         o, S_T, h_saved = forward(q, k, v, g, beta, S0, cu_seqlens, layout, scale, h_dtype=h_dtype,
                                   prologue=prologue, save_wy=save_wy, cp=cp_fwd)
-        ctx.save_for_backward(q, k, v, g, beta, h_saved, cu_seqlens)
+        ctx.save_for_backward(q, k, v, g, beta, h_saved, cu_seqlens, S0_link)
         ctx.layout, ctx.scale, ctx.has_S0, ctx.prologue = layout, scale, S0 is not None, prologue
         ctx.save_wy, ctx.cp_bwd = save_wy, cp_bwd
         return o, S_T
 
     @staticmethod
+    @_first_order("chunk_gated_delta_rule")
     def backward(ctx, do, dS_T):
-        q, k, v, g, beta, h_saved, cu_seqlens = ctx.saved_tensors
+        q, k, v, g, beta, h_saved, cu_seqlens, _ = ctx.saved_tensors
         dq, dk, dv, dg, dbeta, dS0 = backward(q, k, v, g, beta, h_saved, do.contiguous(),
                                               None if dS_T is None else dS_T.contiguous(), cu_seqlens,
                                               ctx.layout, ctx.scale, want_dS0=ctx.has_S0, prologue=ctx.prologue,
                                               save_wy=ctx.save_wy, cp=ctx.cp_bwd)
-        return dq, dk, dv, dg, dbeta, dS0, None, None, None, None, None, None, None, None
+        return dq, dk, dv, dg, dbeta, dS0, None, None, None, None, None, None, None, None, None
 
 
 def chunk_gated_delta_rule(q, k, v, g, beta, initial_state=None, cu_seqlens=None, layout="KV", scale=None,
@@ -424,4 +426,4 @@ def chunk_gated_delta_rule(q, k, v, g, beta, initial_state=None, cu_seqlens=None
     cp_bwd: context-parallel segments per sequence of each direction (1: off), for few long
     sequences whose (sequence, v-head) chains would leave most SMs idle."""
     return _GDRFunction.apply(q, k, v, g, beta, initial_state, cu_seqlens, layout, scale, h_dtype, prologue,
-                              save_wy, cp_fwd, cp_bwd)
+                              save_wy, cp_fwd, cp_bwd, _link(initial_state))

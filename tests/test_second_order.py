@@ -88,3 +88,46 @@ def test_second_derivatives_are_refused_on_the_gpu(name, loss):
     assert torch.equal(g, first)
     with pytest.raises(RuntimeError, match=f"{name} has no second derivative"):
         torch.autograd.grad(g.sum(), x)
+
+
+def delta_inputs(B, T, H, D, **kw):
+    gen = torch.Generator().manual_seed(3)
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=gen, dtype=kw["dtype"]).to(kw["device"])
+
+    q, k, v = rand(B, T, H, D), torch.nn.functional.normalize(rand(B, T, H, D), dim=-1), rand(B, T, H, D)
+    return q, k, v, -rand(B, T, H).abs(), torch.sigmoid(rand(B, T, H)), rand(B, H, D, D)
+
+
+@pytest.mark.parametrize("loss", ["product", "sum"])
+def test_second_derivatives_of_the_delta_rule_are_refused(monkeypatch, loss):
+    q, k, v, g, beta, S0 = delta_inputs(2, 5, 1, 3, dtype=F64, device="cpu")
+    monkeypatch.setattr(gdr, "forward", lambda q, k, v, g, beta, S0, *a, **kw: (v ** 3, S0 + 1, v ** 2))
+    monkeypatch.setattr(gdr, "backward", lambda q, k, v, g, beta, saved, do, dS, *a, **kw:
+                        (*[torch.zeros_like(t) for t in (q, k)], 3 * do * saved, torch.zeros_like(g), torch.zeros_like(beta), dS))
+    x, S0 = v.requires_grad_(), S0.requires_grad_()
+    run = losses(lambda x: gdr.chunk_gated_delta_rule(q, k, x, g, beta, S0)[0], x)[loss]
+    grad, = torch.autograd.grad(run(), x, create_graph=True)
+    assert torch.allclose(grad, torch.autograd.grad(losses(cube, x)[loss](), x)[0], rtol=1e-14)
+    for of in (x, S0):  # the state counts too
+        with pytest.raises(RuntimeError, match="chunk_gated_delta_rule has no second derivative"):
+            torch.autograd.grad(grad.sum(), of, retain_graph=True)
+    state = S0 * 1
+    total = gdr.chunk_gated_delta_rule(q, k, x, g, beta, state)[0].sum()
+    state.zero_()  # its owner may change it: it is not kept
+    assert torch.allclose(torch.autograd.grad(total, x)[0], 3 * x.detach() ** 2, rtol=1e-14)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("loss", ["product", "sum"])
+def test_second_derivatives_of_the_delta_rule_are_refused_on_the_gpu(loss):
+    q, k, v, g, beta, S0 = delta_inputs(1, 20, 2, 16, dtype=torch.float32, device="cuda")
+    x, S0 = v.requires_grad_(), S0.requires_grad_()
+    run = losses(lambda x: gdr.chunk_gated_delta_rule(q, k, x, g, beta, S0)[0], x)[loss]
+    first, = torch.autograd.grad(run(), x)
+    grad, = torch.autograd.grad(run(), x, create_graph=True)
+    assert torch.equal(grad, first)
+    for of in (x, S0):
+        with pytest.raises(RuntimeError, match="chunk_gated_delta_rule has no second derivative"):
+            torch.autograd.grad(grad.sum(), of, retain_graph=True)
