@@ -3,8 +3,9 @@ convolution, the selective state space scan, the block norms and the single-toke
 
 The functions here check shapes, types and strides, allocate outputs and workspace and make the call
 (in ``csrc/gdr_binding.cpp``), and raise: ``ValueError`` for what they find themselves, ``GDRError`` for
-a status.  Everything runs on the current stream, or on ``stream`` if one is given: outputs and
-workspace are then allocated on that stream, and the caller orders the inputs before it and keeps them until it is done.
+a status.  A call's tensors lie on one device, whichever is current, and the call runs there.  Everything runs on
+its current stream, or on ``stream`` if one is given: outputs and workspace are then allocated on that stream, and the
+caller orders the inputs before it and keeps them until it is done.
 
     conv_forward, conv_backward, conv_step, causal_conv        (autograd)
     ssm_forward, ssm_backward, ssm_step, selective_scan        (autograd)

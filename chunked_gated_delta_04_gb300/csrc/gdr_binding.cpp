@@ -10,6 +10,7 @@
 
 #include <ATen/core/TensorBody.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -23,6 +24,7 @@ namespace {
 
 using at::IntArrayRef;
 using at::Tensor;
+using c10::cuda::CUDAGuard;
 
 #define GDR_ENTRIES(X)                                                                                              \
   X(gdr_conv_fwd) X(gdr_conv_bwd) X(gdr_conv_step) X(gdr_conv_fwd_workspace_bytes) X(gdr_conv_bwd_workspace_bytes) \
@@ -62,18 +64,27 @@ int size32(const char* name, int64_t v) {
   return (int)v;
 }
 
+// A call's tensors lie on one device, that of its first activation: the kernels run there.  (The entry
+// points make it current for the call: the default stream of every device has the same handle, which
+// the library would take for the current device's.)
+void on_device(const char* name, const Tensor& t, at::Device dev) {
+  TORCH_CHECK_VALUE(t.device() == dev, name, ": on ", t.device(), ", the call's first tensor on ", dev);
+}
+
 // An activation of the call: on the GPU, of a shape and type.
-void act(const char* name, const Tensor& t, IntArrayRef shape, at::ScalarType type) {
+void act(const char* name, const Tensor& t, IntArrayRef shape, at::ScalarType type, at::Device dev) {
   TORCH_CHECK_VALUE(t.is_cuda() && t.scalar_type() == type && t.sizes() == shape, name, ": expected a CUDA ", type,
                     " tensor of shape ", shape, ", got ", t.scalar_type(), " ", t.sizes(), " on ", t.device());
+  on_device(name, t, dev);
 }
 
 // A contiguous tensor of a shape and type, or none.
-void full(const char* name, const Tensor& t, IntArrayRef shape, at::ScalarType type = at::kFloat) {
+void full(const char* name, const Tensor& t, IntArrayRef shape, at::Device dev, at::ScalarType type = at::kFloat) {
   if (!t.defined()) return;
   TORCH_CHECK_VALUE(t.is_cuda() && t.scalar_type() == type && t.sizes() == shape && t.is_contiguous(), name,
                     ": expected a contiguous CUDA ", type, " tensor of shape ", shape, ", got ", t.scalar_type(), " ",
                     t.sizes(), ", strides ", t.strides(), ", on ", t.device());
+  on_device(name, t, dev);
 }
 
 // Token stride of a [..., inner dimensions] activation (0: contiguous), -1 if its rows are not
@@ -105,19 +116,21 @@ long long strided(const char* name, const Tensor& t, int inner) {
   return ld;
 }
 
-int sequences(const Tensor& cu, int64_t B) {
+int sequences(const Tensor& cu, int64_t B, at::Device dev) {
   if (!cu.defined()) return size32("x", B);
   TORCH_CHECK_VALUE(cu.is_cuda() && cu.scalar_type() == at::kInt && cu.dim() == 1 && cu.numel() >= 2 && cu.is_contiguous(),
                     "cu_seqlens: expected a contiguous CUDA int32 vector of at least 2 entries");
+  on_device("cu_seqlens", cu, dev);
   TORCH_CHECK_VALUE(B == 1, "cu_seqlens needs a batch of 1 (the packed tokens)");
   return size32("cu_seqlens", cu.numel()) - 1;
 }
 
-void check_slots(const Tensor& slots, const Tensor& state, int64_t B) {
+void check_slots(const Tensor& slots, const Tensor& state, int64_t B, at::Device dev) {
   if (slots.defined()) {
     TORCH_CHECK_VALUE(slots.is_cuda() && slots.scalar_type() == at::kInt && slots.is_contiguous() && slots.dim() == 1 &&
                           slots.size(0) == B,
                       "slots: expected a contiguous CUDA int32 vector of ", B, " entries");
+    on_device("slots", slots, dev);
   } else {
     TORCH_CHECK_VALUE(state.size(0) >= B, "state: ", state.size(0), " states for ", B, " rows");
   }
@@ -163,22 +176,23 @@ gdr_conv_problem conv_problem(const Tensor& x, const Tensor& w, const Tensor& b,
   TORCH_CHECK_VALUE(x.dim() == 3, "x: expected [B, T, C], got ", x.sizes());
   const int64_t B = x.size(0), T = x.size(1), C = x.size(2), W = w.size(-1);
   const auto type = x.scalar_type();
+  const at::Device dev = x.device();
   gdr_conv_problem p = {};
   p.dtype = type_code(type);
   p.B = size32("x", B);
   p.T = size32("x", T);
   p.C = size32("x", C);
   p.W = size32("weight", W);
-  act("x", x, {B, T, C}, type);
-  full("weight", w, {C, W});
-  full("bias", b, {C});
-  p.num_seqs = sequences(cu, B);
-  full("initial_state", state, {p.num_seqs, W - 1, C}, type);
+  act("x", x, {B, T, C}, type, dev);
+  full("weight", w, {C, W}, dev);
+  full("bias", b, {C}, dev);
+  p.num_seqs = sequences(cu, B, dev);
+  full("initial_state", state, {p.num_seqs, W - 1, C}, dev, type);
   p.cu_seqlens = (const int32_t*)ptr(cu);
   p.silu = (int)silu;
   p.ld_x = strided("x", x, 1);
   if (dy.defined()) {
-    act("dy", dy, {B, T, C}, type);
+    act("dy", dy, {B, T, C}, type, dev);
     p.ld_dy = strided("dy", dy, 1);
   }
   return p;
@@ -191,6 +205,7 @@ PyObject* conv_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor &x = required(a[0], "x"), &w = required(a[1], "weight"), &b = tensor(a[2], "bias"),
                &state = tensor(a[3], "initial_state"), &cu = tensor(a[4], "cu_seqlens");
   const gdr_conv_problem p = conv_problem(x, w, b, state, cu, integer(a[5]), kNone);
+  const CUDAGuard current(x.device());
   const Tensor y = fresh(x.sizes(), x), last = integer(a[6]) ? fresh({p.num_seqs, p.W - 1, p.C}, x) : Tensor();
   const size_t bytes = cu.defined() ? lib.gdr_conv_fwd_workspace_bytes(&p) : 0;
   const Tensor ws = workspace(bytes, x);
@@ -207,7 +222,8 @@ PyObject* conv_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor &x = required(a[0], "x"), &w = required(a[1], "weight"), &b = tensor(a[2], "bias"), &dy = required(a[3], "dy"),
                &state = tensor(a[4], "initial_state"), &dlast = tensor(a[5], "dfinal_state"), &cu = tensor(a[6], "cu_seqlens");
   const gdr_conv_problem p = conv_problem(x, w, b, state, cu, integer(a[7]), dy);
-  full("dfinal_state", dlast, {p.num_seqs, p.W - 1, p.C}, x.scalar_type());
+  full("dfinal_state", dlast, {p.num_seqs, p.W - 1, p.C}, x.device(), x.scalar_type());
+  const CUDAGuard current(x.device());
   const Tensor dx = fresh(x.sizes(), x), dw = fresh(w.sizes(), w), db = b.defined() ? fresh(b.sizes(), b) : Tensor(),
                dstate = state.defined() ? fresh(state.sizes(), state) : Tensor();
   const size_t bytes = lib.gdr_conv_bwd_workspace_bytes(&p);
@@ -228,6 +244,7 @@ PyObject* conv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
                     " and ", state.sizes());
   const int64_t B = x.size(0), C = x.size(1), W = w.size(-1);
   const auto type = x.scalar_type();
+  const at::Device dev = x.device();
   gdr_conv_problem p = {};
   p.dtype = type_code(type);
   p.B = p.num_seqs = size32("x", B);
@@ -235,13 +252,14 @@ PyObject* conv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p.C = size32("x", C);
   p.W = size32("weight", W);
   p.num_slots = size32("state", state.size(0));
-  act("x", x, {B, C}, type);
-  full("weight", w, {C, W});
-  full("bias", b, {C});
-  full("state", state, {state.size(0), W - 1, C}, type);
-  check_slots(slots, state, B);
+  act("x", x, {B, C}, type, dev);
+  full("weight", w, {C, W}, dev);
+  full("bias", b, {C}, dev);
+  full("state", state, {state.size(0), W - 1, C}, dev, type);
+  check_slots(slots, state, B, dev);
   p.silu = (int)integer(a[5]);
   p.ld_x = strided("x", x, 1);
+  const CUDAGuard current(dev);
   const Tensor y = fresh({B, C}, x);
   return answer(lib.gdr_conv_step(&p, ptr(x), (const float*)ptr(w), (const float*)ptr(b), ptr(state),
                                   (const int32_t*)ptr(slots), ptr(y), stream_of(x)),
@@ -259,6 +277,7 @@ gdr_ssm_problem ssm_problem(const SsmTensors& t, int lead, const Tensor& cu, lon
                     lead == 2 ? "B, T" : "B", ", G, N], got ", t.x.sizes(), " and ", t.Bm.sizes());
   const int64_t B = t.x.size(0), T = lead == 2 ? t.x.size(1) : 1, D = t.x.size(-1), G = t.Bm.size(-2), N = t.Bm.size(-1);
   const auto type = t.x.scalar_type();
+  const at::Device dev = t.x.device();
   gdr_ssm_problem p = {};
   p.dtype = type_code(type);
   p.B = size32("x", B);
@@ -271,14 +290,14 @@ gdr_ssm_problem ssm_problem(const SsmTensors& t, int lead, const Tensor& cu, lon
   const std::array<int64_t, 2> row1 = {B, D};
   const std::array<int64_t, 3> bc1 = {B, G, N};
   const IntArrayRef row = lead == 2 ? IntArrayRef(row2) : IntArrayRef(row1), bc = lead == 2 ? IntArrayRef(bc2) : IntArrayRef(bc1);
-  act("x", t.x, row, type);
-  act("dt", t.dt, row, type);
-  act("Bm", t.Bm, bc, type);
-  act("Cm", t.Cm, bc, type);
-  full("A", t.A, {D, N});
-  full("D", t.D, {D});
-  full("dt_bias", t.bias, {D});
-  p.num_seqs = sequences(cu, B);
+  act("x", t.x, row, type, dev);
+  act("dt", t.dt, row, type, dev);
+  act("Bm", t.Bm, bc, type, dev);
+  act("Cm", t.Cm, bc, type, dev);
+  full("A", t.A, {D, N}, dev);
+  full("D", t.D, {D}, dev);
+  full("dt_bias", t.bias, {D}, dev);
+  p.num_seqs = sequences(cu, B, dev);
   p.cu_seqlens = (const int32_t*)ptr(cu);
   p.dt_softplus = (int)softplus;
   p.ld_x = strided("x", t.x, 1);
@@ -286,7 +305,7 @@ gdr_ssm_problem ssm_problem(const SsmTensors& t, int lead, const Tensor& cu, lon
   p.ld_b = strided("Bm", t.Bm, 2);
   p.ld_c = strided("Cm", t.Cm, 2);
   if (dy.defined()) {
-    act("dy", dy, row, type);
+    act("dy", dy, row, type, dev);
     p.ld_dy = strided("dy", dy, 1);
   }
   return p;
@@ -300,7 +319,8 @@ PyObject* ssm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      required(a[4], "Cm"), tensor(a[5], "D"), tensor(a[6], "dt_bias")};
   const Tensor &S0 = tensor(a[7], "S0"), &cu = tensor(a[8], "cu_seqlens");
   const gdr_ssm_problem p = ssm_problem(t, 2, cu, integer(a[9]), kNone);
-  full("S0", S0, {p.num_seqs, p.D, p.N});
+  full("S0", S0, {p.num_seqs, p.D, p.N}, t.x.device());
+  const CUDAGuard current(t.x.device());
   const Tensor y = fresh(t.x.sizes(), t.x), S_T = integer(a[10]) ? fresh_f32({p.num_seqs, p.D, p.N}, t.x) : Tensor(),
                saved = integer(a[11]) ? fresh_f32({(int64_t)(lib.gdr_ssm_saved_bytes(&p) / 4)}, t.x) : Tensor();
   const size_t bytes = lib.gdr_ssm_fwd_workspace_bytes(&p);
@@ -321,11 +341,13 @@ PyObject* ssm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor &saved = tensor(a[5], "h_saved"), &dy = required(a[6], "dy"), &dS_T = tensor(a[9], "dS_T"),
                &cu = tensor(a[10], "cu_seqlens");
   const gdr_ssm_problem p = ssm_problem(t, 2, cu, integer(a[11]), dy);
-  full("dS_T", dS_T, {p.num_seqs, p.D, p.N});
+  full("dS_T", dS_T, {p.num_seqs, p.D, p.N}, t.x.device());
   const int64_t need = (int64_t)(lib.gdr_ssm_saved_bytes(&p) / 4);
   TORCH_CHECK_VALUE(saved.defined() && saved.is_cuda() && saved.scalar_type() == at::kFloat && saved.is_contiguous() &&
                         saved.numel() >= need,
                     "h_saved: expected the ", need, " floats that ssm_forward kept (save=True)");
+  on_device("h_saved", saved, t.x.device());
+  const CUDAGuard current(t.x.device());
   const Tensor dx = fresh(t.x.sizes(), t.x), ddt = fresh(t.x.sizes(), t.x), dB = fresh(t.Bm.sizes(), t.x),
                dC = fresh(t.Bm.sizes(), t.x), dA = fresh(t.A.sizes(), t.A),
                dD = t.D.defined() ? fresh(t.D.sizes(), t.D) : Tensor(), db = t.bias.defined() ? fresh(t.bias.sizes(), t.bias) : Tensor(),
@@ -349,9 +371,11 @@ PyObject* ssm_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor &state = required(a[5], "state"), &slots = tensor(a[8], "slots");
   gdr_ssm_problem p = ssm_problem(t, 1, kNone, integer(a[9]), kNone);
   TORCH_CHECK_VALUE(state.dim() == 3, "state: expected [num_slots, D, N], got ", state.sizes());
-  full("state", state, {state.size(0), p.D, p.N});
-  check_slots(slots, state, p.B);
+  const at::Device dev = t.x.device();
+  full("state", state, {state.size(0), p.D, p.N}, dev);
+  check_slots(slots, state, p.B, dev);
   p.num_slots = size32("state", state.size(0));
+  const CUDAGuard current(dev);
   const Tensor y = fresh({p.B, p.D}, t.x);
   return answer(lib.gdr_ssm_step(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(t.A), ptr(t.Bm), ptr(t.Cm), (const float*)ptr(t.D),
                                  (const float*)ptr(t.bias), (float*)ptr(state), (const int32_t*)ptr(slots), ptr(y),
@@ -366,15 +390,16 @@ gdr_norm_problem norm_problem(const Tensor& x, const Tensor& post, const Tensor&
   TORCH_CHECK_VALUE(x.dim() >= 1 && x.size(-1) > 0, "x: expected [..., D], got ", x.sizes());
   const int64_t D = x.size(-1);
   const auto type = x.scalar_type();
+  const at::Device dev = x.device();
   gdr_norm_problem p = {};
   p.dtype = type_code(type);
   p.res_dtype = type_code(stream_type);
   p.D = size32("x", D);
-  act("x", x, x.sizes(), type);
-  if (gate.defined()) act("gate", gate, x.sizes(), type);
-  full("post_weight", post, {D});
-  full("scale", scale, {D});
-  full("pre_weight", pre, {D});
+  act("x", x, x.sizes(), type, dev);
+  if (gate.defined()) act("gate", gate, x.sizes(), type, dev);
+  full("post_weight", post, {D}, dev);
+  full("scale", scale, {D}, dev);
+  full("pre_weight", pre, {D}, dev);
   p.eps = (float)eps;
   p.heads = 1;
   p.tokens = x.numel() / D;
@@ -401,7 +426,8 @@ PyObject* norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                &scale = tensor(a[3], "scale"), &res = tensor(a[4], "residual"), &pre = tensor(a[5], "pre_weight");
   const auto type = res.defined() ? res.scalar_type() : x.scalar_type();
   const gdr_norm_problem p = norm_problem(x, post, gate, scale, pre, type, number(a[6]));
-  full("residual", res, x.sizes(), type);
+  full("residual", res, x.sizes(), x.device(), type);
+  const CUDAGuard current(x.device());
   const Tensor r = res.defined() ? fresh(x.sizes(), res) : pre.defined() ? Tensor() : fresh(x.sizes(), x),
                y = pre.defined() ? fresh(x.sizes(), x) : Tensor();
   return answer(lib.gdr_norm_fwd(&p, ptr(x), (const float*)ptr(post), ptr(gate), (const float*)ptr(scale), ptr(res),
@@ -420,10 +446,12 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const bool has_residual = r.defined();
   const auto type = has_residual ? r.scalar_type() : x.scalar_type();
   const gdr_norm_problem p = norm_problem(x, post, gate, scale, pre, type, number(a[8]));
-  full("r", r, x.sizes(), type);
-  full("dr", dr, x.sizes(), type);
-  full("dy", dy, x.sizes(), x.scalar_type());
+  const at::Device dev = x.device();
+  full("r", r, x.sizes(), dev, type);
+  full("dr", dr, x.sizes(), dev, type);
+  full("dy", dy, x.sizes(), dev, x.scalar_type());
   TORCH_CHECK_VALUE(has_residual || !pre.defined() || x.is_contiguous(), "x: a plain norm's backward needs a contiguous x");
+  const CUDAGuard current(dev);
   const Tensor dx = fresh(x.sizes(), x), dgate = gate.defined() ? fresh(x.sizes(), x) : Tensor(),
                dres = has_residual ? fresh(x.sizes(), r) : Tensor(), dpost = post.defined() ? fresh(post.sizes(), post) : Tensor(),
                dscale = scale.defined() ? fresh(scale.sizes(), scale) : Tensor(),
@@ -448,6 +476,7 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(q.dim() == 3 && v.dim() == 3 && state.dim() == 4, "expected q [B, Hk, DK], v [B, Hv, DV] and a state of four dimensions, got ",
                     q.sizes(), ", ", v.sizes(), " and ", state.sizes());
   const auto type = q.scalar_type();
+  const at::Device dev = q.device();
   const int64_t B = q.size(0), Hk = q.size(1), DK = q.size(2), Hv = v.size(1), DV = v.size(2);
   gdr_problem p = {};
   p.dtype = type_code(type);
@@ -459,16 +488,17 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p.DK = size32("q", DK);
   p.DV = size32("v", DV);
   const int num_slots = size32("state", state.size(0));
-  full("q", q, {B, Hk, DK}, type);
-  full("k", k, {B, Hk, DK}, type);
-  full("v", v, {B, Hv, DV}, type);
-  full("g", g, {B, Hv});
-  full("beta", beta, {B, Hv}, type);
+  full("q", q, {B, Hk, DK}, dev, type);
+  full("k", k, {B, Hk, DK}, dev, type);
+  full("v", v, {B, Hv, DV}, dev, type);
+  full("g", g, {B, Hv}, dev);
+  full("beta", beta, {B, Hv}, dev, type);
   const bool kv = p.layout == GDR_STATE_KV;
-  full("state", state, {state.size(0), Hv, kv ? DK : DV, kv ? DV : DK});
-  check_slots(slots, state, B);
+  full("state", state, {state.size(0), Hv, kv ? DK : DV, kv ? DV : DK}, dev);
+  check_slots(slots, state, B, dev);
   p.scale = (float)number(a[7]);
   p.prologue = (unsigned)integer(a[9]);
+  const CUDAGuard current(dev);
   const Tensor o = fresh({B, Hv, DV}, v);
   return answer(lib.gdr_step(&p, ptr(q), ptr(k), ptr(v), (const float*)ptr(g), ptr(beta), (float*)ptr(state), num_slots,
                              (const int32_t*)ptr(slots), ptr(o), stream_of(q)),
