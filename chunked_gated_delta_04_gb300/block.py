@@ -103,9 +103,15 @@ def _done(result, where):
     return result
 
 
-def _on(stream):
-    """The context in which a call on a stream of its own allocates and launches."""
-    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+def _on(stream, x):
+    """The context in which a call with tensor x on a stream of its own allocates and launches; a handle (int) is one
+    of x's device."""
+    device = x.device if isinstance(x, torch.Tensor) and x.is_cuda else None  # else the call says what x is
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device)
+    elif device is not None and stream.device != device:
+        raise ValueError(f"stream: of {stream.device}, the call's first tensor on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _ld(name, t, inner):
@@ -134,7 +140,7 @@ def conv_forward(x, weight, bias=None, initial_state=None, cu_seqlens=None, acti
     [C, W] and bias [C] fp32, initial_state [num_seqs, W - 1, C] (oldest row first).  Returns
     (y, final state or None)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return conv_forward(x, weight, bias, initial_state, cu_seqlens, activation, output_final_state)
     return _done(_binding().conv_forward(x, weight, bias, initial_state, cu_seqlens, _silu(activation), output_final_state),
                  "gdr_conv_fwd")
@@ -144,7 +150,7 @@ def conv_backward(x, weight, bias, dy, initial_state=None, dfinal_state=None, cu
                   stream=None):
     """Gradients of conv_forward: (dx, dweight, dbias or None, dinitial_state or None)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return conv_backward(x, weight, bias, dy, initial_state, dfinal_state, cu_seqlens, activation)
     return _done(_binding().conv_backward(x, weight, bias, dy, initial_state, dfinal_state, cu_seqlens, _silu(activation)),
                  "gdr_conv_bwd")
@@ -155,7 +161,7 @@ def conv_step(x, state, weight, bias=None, slots=None, activation="silu", stream
     row's slot (int32 [B]; None: row i at slot i).  Returns y [B, C]; a row whose slot is outside the
     pool is skipped and returns zeros."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return conv_step(x, state, weight, bias, slots, activation)
     return _done(_binding().conv_step(x, state, weight, bias, slots, _silu(activation)), "gdr_conv_step")
 
@@ -197,7 +203,7 @@ def ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, cu_seqlens=None
     [D] fp32, S0 [num_seqs, D, N] fp32.  Returns (y, S_T or None, h_saved or None); save keeps the
     states that ssm_backward needs."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus, output_final_state, save)
     return _done(_binding().ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, bool(dt_softplus), output_final_state,
                                         save), "gdr_ssm_fwd")
@@ -207,7 +213,7 @@ def ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D=None, dt_bias=None, dS_T=None,
                  want_dS0=True, stream=None):
     """Gradients of ssm_forward: (dx, ddt, dA, dBm, dCm, dD or None, ddt_bias or None, dS0 or None)."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D, dt_bias, dS_T, cu_seqlens, dt_softplus, want_dS0)
     return _done(_binding().ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D, dt_bias, dS_T, cu_seqlens, bool(dt_softplus),
                                          want_dS0), "gdr_ssm_bwd")
@@ -217,7 +223,7 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, slots=None, dt_softp
     """One token per row: x, dt [B, D], Bm, Cm [B, G, N]; state, a pool [num_slots, D, N] fp32, is
     updated in place at each row's slot (see conv_step).  Returns y [B, D]."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return ssm_step(x, dt, A, Bm, Cm, state, D, dt_bias, slots, dt_softplus)
     return _done(_binding().ssm_step(x, dt, A, Bm, Cm, state, D, dt_bias, slots, bool(dt_softplus)), "gdr_ssm_step")
 
@@ -258,7 +264,7 @@ def norm_forward(x, post_weight=None, gate=None, scale=None, residual=None, pre_
     without one; r is None for a plain norm in front of a block (pre_weight alone), y is None without
     pre_weight."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return norm_forward(x, post_weight, gate, scale, residual, pre_weight, eps)
     return _done(_binding().norm_forward(x, post_weight, gate, scale, residual, pre_weight, eps), "gdr_norm_fwd")
 
@@ -269,7 +275,7 @@ def norm_backward(x, post_weight=None, gate=None, scale=None, r=None, pre_weight
     dscale, dpre_weight), None where the forward had no such tensor.  r: the forward's r where it had a
     residual, else None."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, x):
             return norm_backward(x, post_weight, gate, scale, r, pre_weight, dr, dy, eps)
     return _done(_binding().norm_backward(x, post_weight, gate, scale, r, pre_weight, dr, dy, eps), "gdr_norm_bwd")
 
@@ -318,7 +324,7 @@ def step(q, k, v, g, beta, state, layout="KV", scale=None, slots=None, prologue=
     is updated in place at each row's slot (see conv_step).  prologue: GDR_PROLOGUE_* bits, as in
     forward (the mapped q, k and beta stay in fp32 here).  Returns o [B, Hv, DV]."""
     if stream is not None:
-        with _on(stream):
+        with _on(stream, q):
             return step(q, k, v, g, beta, state, layout, scale, slots, prologue)
     if layout not in _LAYOUT:
         raise ValueError(f"layout {layout!r}: 'KV' or 'VK'")

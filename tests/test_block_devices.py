@@ -1,5 +1,8 @@
 """A call's tensors lie on one device.  Tensors of another one are made without a GPU as fake tensors, which have
 shapes and devices and no memory: the refusal has to come before anything is allocated or launched."""
+import contextlib
+import types
+
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
@@ -35,3 +38,25 @@ def test_a_tensor_on_another_device_is_refused(call, name):
         args = {n: torch.empty(shape, dtype=dtype, device="cuda:1" if n == name else "cuda:0") for n, (shape, dtype) in CALLS[call].items()}
         with pytest.raises(ValueError, match=f"^{name}: on cuda:1, the call's first tensor on cuda:0"):
             getattr(gdr, call)(**args)
+
+
+@pytest.mark.parametrize("call", list(CALLS))
+def test_a_stream_is_one_of_the_tensors_device(monkeypatch, call):
+    """A handle is taken as a stream of the tensors' device, not of the current one; another device's stream is
+    refused: the call would run on a stream that nobody named."""
+    made = []
+
+    def external(handle, device=None):
+        made.append((handle, device))
+        return types.SimpleNamespace(device=device)
+
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    wrong = list(CALLS[call])[1]  # so that the call ends before it allocates
+    with FakeTensorMode():
+        args = {n: torch.empty(shape, dtype=dtype, device="cpu" if n == wrong else "cuda:1") for n, (shape, dtype) in CALLS[call].items()}
+        with pytest.raises(ValueError, match=wrong):
+            getattr(gdr, call)(**args, stream=1 << 20)
+        assert made == [(1 << 20, torch.device("cuda:1"))]
+        with pytest.raises(ValueError, match="stream: of cuda:0, the call's first tensor on cuda:1"):
+            getattr(gdr, call)(**args, stream=types.SimpleNamespace(device=torch.device("cuda:0")))
