@@ -29,9 +29,9 @@ import torch
 from . import block as _block
 from ._autograd import first_order as _first_order, link as _link
 from .block import (  # noqa: F401 - the operators around the gated delta rule
-    BLOCK_EXPORTS, block_norm, causal_conv, conv_backward, conv_forward, conv_step, gdr_conv_problem,
+    BLOCK_EXPORTS, block_norm, causal_conv, conv_backward, conv_forward, conv_step, conv_workspace, gdr_conv_problem,
     gdr_norm_problem, gdr_ssm_problem, norm_backward, norm_forward, selective_scan, ssm_backward, ssm_forward,
-    ssm_step, step)
+    ssm_step, ssm_workspace, step)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdr.so")

@@ -7,8 +7,16 @@ a status.  A call's tensors lie on one device, whichever is current, and the cal
 its current stream, or on ``stream`` if one is given: outputs and workspace are then allocated on that stream, and the
 caller orders the inputs before it and keeps them until it is done.
 
-    conv_forward, conv_backward, conv_step, causal_conv        (autograd)
-    ssm_forward, ssm_backward, ssm_step, selective_scan        (autograd)
+Packed batches (``cu_seqlens``): what cu_seqlens holds is checked on the device.  A malformed one (not 0 .. T in
+non-decreasing steps) computes nothing, the outputs are then uninitialised, and the workspace's status says so.  To be
+able to ask, hand a workspace in and ask after the call:
+
+    ws = conv_workspace(x, weight, cu_seqlens)
+    y, last = conv_forward(x, weight, cu_seqlens=cu_seqlens, workspace=ws)
+    status, flags = gdr_workspace_status(ws)   # synchronises; GDR_ERR_INVALID_ARG
+
+    conv_forward, conv_backward, conv_step, causal_conv        (autograd), conv_workspace
+    ssm_forward, ssm_backward, ssm_step, selective_scan        (autograd), ssm_workspace
     norm_forward, norm_backward, block_norm                    (autograd)
     step                                                       the gated delta rule, one token
 """
@@ -135,25 +143,43 @@ def _silu(activation):
 
 
 def conv_forward(x, weight, bias=None, initial_state=None, cu_seqlens=None, activation="silu", output_final_state=False,
-                 stream=None):
+                 stream=None, workspace=None):
     """Short causal depthwise convolution: x [B, T, C] (may be a slice of a wider tensor), weight
     [C, W] and bias [C] fp32, initial_state [num_seqs, W - 1, C] (oldest row first).  Returns
-    (y, final state or None)."""
+    (y, final state or None).  workspace: of conv_workspace, for its status."""
     if stream is not None:
         with _on(stream, x):
-            return conv_forward(x, weight, bias, initial_state, cu_seqlens, activation, output_final_state)
-    return _done(_binding().conv_forward(x, weight, bias, initial_state, cu_seqlens, _silu(activation), output_final_state),
-                 "gdr_conv_fwd")
+            return conv_forward(x, weight, bias, initial_state, cu_seqlens, activation, output_final_state,
+                                workspace=workspace)
+    return _done(_binding().conv_forward(x, weight, bias, initial_state, cu_seqlens, _silu(activation), output_final_state,
+                                         workspace), "gdr_conv_fwd")
 
 
 def conv_backward(x, weight, bias, dy, initial_state=None, dfinal_state=None, cu_seqlens=None, activation="silu",
-                  stream=None):
+                  stream=None, workspace=None):
     """Gradients of conv_forward: (dx, dweight, dbias or None, dinitial_state or None)."""
     if stream is not None:
         with _on(stream, x):
-            return conv_backward(x, weight, bias, dy, initial_state, dfinal_state, cu_seqlens, activation)
-    return _done(_binding().conv_backward(x, weight, bias, dy, initial_state, dfinal_state, cu_seqlens, _silu(activation)),
-                 "gdr_conv_bwd")
+            return conv_backward(x, weight, bias, dy, initial_state, dfinal_state, cu_seqlens, activation,
+                                 workspace=workspace)
+    return _done(_binding().conv_backward(x, weight, bias, dy, initial_state, dfinal_state, cu_seqlens, _silu(activation),
+                                          workspace), "gdr_conv_bwd")
+
+
+def conv_workspace(x, weight, cu_seqlens=None, backward=False):
+    """A workspace for conv_forward (or conv_backward) of these tensors, its status word clear."""
+    B, T, C = x.shape
+    cu = cu_seqlens
+    p = gdr_conv_problem(B, T, C, weight.shape[-1], B if cu is None else cu.numel() - 1, None if cu is None else cu.data_ptr(),
+                         _gdr._dtype_code(x.dtype))
+    return _workspace("conv", p, backward, x.device)
+
+
+def _workspace(op, p, backward, device):
+    nbytes = getattr(_gdr._lib_handle(), f"gdr_{op}_{'bwd' if backward else 'fwd'}_workspace_bytes")(_c.byref(p))
+    ws = _gdr.alloc_workspace(nbytes, device)
+    ws[:256].zero_()  # the status is a packed call's; of another it stays clear
+    return ws
 
 
 def conv_step(x, state, weight, bias=None, slots=None, activation="silu", stream=None):
@@ -168,11 +194,11 @@ def conv_step(x, state, weight, bias=None, slots=None, activation="silu", stream
 
 class _ConvFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, initial_state, cu_seqlens, activation):
+    def forward(ctx, x, weight, bias, initial_state, cu_seqlens, activation, workspace):
         ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
         ctx.activation = activation
         ctx.set_materialize_grads(False)
-        return conv_forward(x, weight, bias, initial_state, cu_seqlens, activation, output_final_state=True)
+        return conv_forward(x, weight, bias, initial_state, cu_seqlens, activation, output_final_state=True, workspace=workspace)
 
     @staticmethod
     @first_order("causal_conv")
@@ -181,7 +207,7 @@ class _ConvFunction(torch.autograd.Function):
         dy = torch.zeros_like(x) if dy is None else _rows_ok(dy, 1)
         dx, dw, db, dstate = conv_backward(x, weight, bias, dy, state, None if dlast is None else dlast.contiguous(), cu,
                                            ctx.activation)
-        return dx, dw, db, dstate, None, None
+        return dx, dw, db, dstate, None, None, None
 
 
 def _rows_ok(t, inner):
@@ -189,34 +215,45 @@ def _rows_ok(t, inner):
     return t if _binding().stride(t, inner) >= 0 else t.contiguous()
 
 
-def causal_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, activation="silu"):
+def causal_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, activation="silu", workspace=None):
     """Autograd entry point of the short causal convolution: (y, final state).  weight and bias may
-    be of any float type (they are used in fp32)."""
+    be of any float type (they are used in fp32).  workspace: the forward's, as conv_forward."""
     return _ConvFunction.apply(x, weight.float(), None if bias is None else bias.float(), initial_state, cu_seqlens,
-                               activation)
+                               activation, workspace)
 
 
 # ------------------------------------------------------------------------------- selective scan
 def ssm_forward(x, dt, A, Bm, Cm, D=None, dt_bias=None, S0=None, cu_seqlens=None, dt_softplus=True,
-                output_final_state=True, save=True, stream=None):
+                output_final_state=True, save=True, stream=None, workspace=None):
     """Selective state space scan: x, dt [B, T, D], A [D, N] fp32, Bm, Cm [B, T, G, N], D and dt_bias
     [D] fp32, S0 [num_seqs, D, N] fp32.  Returns (y, S_T or None, h_saved or None); save keeps the
-    states that ssm_backward needs."""
+    states that ssm_backward needs.  workspace: of ssm_workspace, for its status."""
     if stream is not None:
         with _on(stream, x):
-            return ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus, output_final_state, save)
+            return ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus, output_final_state, save,
+                               workspace=workspace)
     return _done(_binding().ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, bool(dt_softplus), output_final_state,
-                                        save), "gdr_ssm_fwd")
+                                        save, workspace), "gdr_ssm_fwd")
 
 
 def ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D=None, dt_bias=None, dS_T=None, cu_seqlens=None, dt_softplus=True,
-                 want_dS0=True, stream=None):
+                 want_dS0=True, stream=None, workspace=None):
     """Gradients of ssm_forward: (dx, ddt, dA, dBm, dCm, dD or None, ddt_bias or None, dS0 or None)."""
     if stream is not None:
         with _on(stream, x):
-            return ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D, dt_bias, dS_T, cu_seqlens, dt_softplus, want_dS0)
+            return ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D, dt_bias, dS_T, cu_seqlens, dt_softplus, want_dS0,
+                                workspace=workspace)
     return _done(_binding().ssm_backward(x, dt, A, Bm, Cm, h_saved, dy, D, dt_bias, dS_T, cu_seqlens, bool(dt_softplus),
-                                         want_dS0), "gdr_ssm_bwd")
+                                         want_dS0, workspace), "gdr_ssm_bwd")
+
+
+def ssm_workspace(x, Bm, cu_seqlens=None, backward=False):
+    """A workspace for ssm_forward (or ssm_backward) of these tensors, its status word clear."""
+    B, T, D = x.shape
+    cu = cu_seqlens
+    p = gdr_ssm_problem(B, T, D, Bm.shape[-1], Bm.shape[-2], B if cu is None else cu.numel() - 1,
+                        None if cu is None else cu.data_ptr(), _gdr._dtype_code(x.dtype))
+    return _workspace("ssm", p, backward, x.device)
 
 
 def ssm_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, slots=None, dt_softplus=True, stream=None):
@@ -230,8 +267,8 @@ def ssm_step(x, dt, A, Bm, Cm, state, D=None, dt_bias=None, slots=None, dt_softp
 
 class _SSMFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus, S0_link):
-        y, S_T, saved = ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus)
+    def forward(ctx, x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus, S0_link, workspace):
+        y, S_T, saved = ssm_forward(x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus, workspace=workspace)
         ctx.save_for_backward(x, dt, A, Bm, Cm, D, dt_bias, saved, cu_seqlens, S0_link)
         ctx.dt_softplus, ctx.has_S0 = dt_softplus, S0 is not None
         ctx.set_materialize_grads(False)
@@ -244,17 +281,18 @@ class _SSMFunction(torch.autograd.Function):
         dy = torch.zeros_like(x) if dy is None else _rows_ok(dy, 1)
         grads = ssm_backward(x, dt, A, Bm, Cm, saved, dy, D, dt_bias, None if dS_T is None else dS_T.contiguous(), cu,
                              ctx.dt_softplus, want_dS0=ctx.has_S0)
-        return (*grads, None, None, None)
+        return (*grads, None, None, None, None)
 
 
-def selective_scan(x, dt, A, Bm, Cm, D=None, dt_bias=None, initial_state=None, cu_seqlens=None, dt_softplus=True):
+def selective_scan(x, dt, A, Bm, Cm, D=None, dt_bias=None, initial_state=None, cu_seqlens=None, dt_softplus=True,
+                   workspace=None):
     """Autograd entry point of the selective scan: (y, final state).  A, D and dt_bias may be of any
-    float type (they are used in fp32)."""
+    float type (they are used in fp32).  workspace: the forward's, as ssm_forward."""
     def f(t):
         return None if t is None else t.float()
 
     return _SSMFunction.apply(x, dt, f(A), Bm, Cm, f(D), f(dt_bias), initial_state, cu_seqlens, dt_softplus,
-                              link(initial_state))
+                              link(initial_state), workspace)
 
 
 # ---------------------------------------------------------------------------------- block norms

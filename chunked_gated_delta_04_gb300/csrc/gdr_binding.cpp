@@ -144,9 +144,22 @@ Tensor fresh_of(IntArrayRef shape, at::ScalarType type, const Tensor& like) {
 }
 Tensor fresh(IntArrayRef shape, const Tensor& like) { return fresh_of(shape, like.scalar_type(), like); }
 Tensor fresh_f32(IntArrayRef shape, const Tensor& like) { return fresh_of(shape, at::kFloat, like); }
-Tensor workspace(size_t bytes, const Tensor& like) {  // torch's blocks are 512-byte aligned
-  return bytes ? fresh_of({(int64_t)bytes}, at::kByte, like) : Tensor();
-}
+// The caller's workspace, whose status it can ask for, or one of the bytes that the call needs (torch's
+// blocks are 512-byte aligned).  What the caller's holds too little of, the library refuses.
+struct Workspace {
+  Tensor t;
+  size_t bytes;
+  Workspace(size_t need, const Tensor& like) : bytes(need) {
+    if (need) t = fresh_of({(int64_t)need}, at::kByte, like);
+  }
+  Workspace(const Tensor& given, size_t need, const Tensor& like) : Workspace(given.defined() ? 0 : need, like) {
+    if (!given.defined()) return;
+    TORCH_CHECK_VALUE(given.is_cuda() && given.is_contiguous(), "workspace: expected a contiguous CUDA tensor");
+    on_device("workspace", given, like.device());
+    t = given;
+    bytes = given.nbytes();
+  }
+};
 
 PyObject* answer(gdr_status st, const Tensor& t) { return st == GDR_OK ? THPVariable_Wrap(t) : PyLong_FromLong(st); }
 PyObject* answer(gdr_status st, std::initializer_list<Tensor> ts) {
@@ -198,38 +211,38 @@ gdr_conv_problem conv_problem(const Tensor& x, const Tensor& w, const Tensor& b,
   return p;
 }
 
-// x, weight, bias, initial_state, cu_seqlens, silu, output_final_state
+// x, weight, bias, initial_state, cu_seqlens, silu, output_final_state, workspace
 PyObject* conv_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 7);
+  arguments(n, 8);
   const Tensor &x = required(a[0], "x"), &w = required(a[1], "weight"), &b = tensor(a[2], "bias"),
-               &state = tensor(a[3], "initial_state"), &cu = tensor(a[4], "cu_seqlens");
+               &state = tensor(a[3], "initial_state"), &cu = tensor(a[4], "cu_seqlens"), &given = tensor(a[7], "workspace");
   const gdr_conv_problem p = conv_problem(x, w, b, state, cu, integer(a[5]), kNone);
   const CUDAGuard current(x.device());
   const Tensor y = fresh(x.sizes(), x), last = integer(a[6]) ? fresh({p.num_seqs, p.W - 1, p.C}, x) : Tensor();
-  const size_t bytes = cu.defined() ? lib.gdr_conv_fwd_workspace_bytes(&p) : 0;
-  const Tensor ws = workspace(bytes, x);
+  const Workspace ws(given, cu.defined() ? lib.gdr_conv_fwd_workspace_bytes(&p) : 0, x);
   return answer(lib.gdr_conv_fwd(&p, ptr(x), (const float*)ptr(w), (const float*)ptr(b), ptr(state), ptr(y), ptr(last),
-                                 ptr(ws), bytes, stream_of(x)),
+                                 ptr(ws.t), ws.bytes, stream_of(x)),
                 {y, last});
   END_HANDLE_TH_ERRORS
 }
 
-// x, weight, bias, dy, initial_state, dfinal_state, cu_seqlens, silu
+// x, weight, bias, dy, initial_state, dfinal_state, cu_seqlens, silu, workspace
 PyObject* conv_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 8);
+  arguments(n, 9);
   const Tensor &x = required(a[0], "x"), &w = required(a[1], "weight"), &b = tensor(a[2], "bias"), &dy = required(a[3], "dy"),
-               &state = tensor(a[4], "initial_state"), &dlast = tensor(a[5], "dfinal_state"), &cu = tensor(a[6], "cu_seqlens");
+               &state = tensor(a[4], "initial_state"), &dlast = tensor(a[5], "dfinal_state"), &cu = tensor(a[6], "cu_seqlens"),
+               &given = tensor(a[8], "workspace");
   const gdr_conv_problem p = conv_problem(x, w, b, state, cu, integer(a[7]), dy);
   full("dfinal_state", dlast, {p.num_seqs, p.W - 1, p.C}, x.device(), x.scalar_type());
   const CUDAGuard current(x.device());
   const Tensor dx = fresh(x.sizes(), x), dw = fresh(w.sizes(), w), db = b.defined() ? fresh(b.sizes(), b) : Tensor(),
                dstate = state.defined() ? fresh(state.sizes(), state) : Tensor();
-  const size_t bytes = lib.gdr_conv_bwd_workspace_bytes(&p);
-  const Tensor ws = workspace(bytes, x);
+  const Workspace ws(given, lib.gdr_conv_bwd_workspace_bytes(&p), x);
   return answer(lib.gdr_conv_bwd(&p, ptr(x), (const float*)ptr(w), (const float*)ptr(b), ptr(state), ptr(dy), ptr(dlast),
-                                 ptr(dx), (float*)ptr(dw), (float*)ptr(db), ptr(dstate), ptr(ws), bytes, stream_of(x)),
+                                 ptr(dx), (float*)ptr(dw), (float*)ptr(db), ptr(dstate), ptr(ws.t), ws.bytes,
+                                 stream_of(x)),
                 {dx, dw, db, dstate});
   END_HANDLE_TH_ERRORS
 }
@@ -311,35 +324,34 @@ gdr_ssm_problem ssm_problem(const SsmTensors& t, int lead, const Tensor& cu, lon
   return p;
 }
 
-// x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus, output_final_state, save
+// x, dt, A, Bm, Cm, D, dt_bias, S0, cu_seqlens, dt_softplus, output_final_state, save, workspace
 PyObject* ssm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 12);
+  arguments(n, 13);
   const SsmTensors t{required(a[0], "x"), required(a[1], "dt"), required(a[2], "A"), required(a[3], "Bm"),
                      required(a[4], "Cm"), tensor(a[5], "D"), tensor(a[6], "dt_bias")};
-  const Tensor &S0 = tensor(a[7], "S0"), &cu = tensor(a[8], "cu_seqlens");
+  const Tensor &S0 = tensor(a[7], "S0"), &cu = tensor(a[8], "cu_seqlens"), &given = tensor(a[12], "workspace");
   const gdr_ssm_problem p = ssm_problem(t, 2, cu, integer(a[9]), kNone);
   full("S0", S0, {p.num_seqs, p.D, p.N}, t.x.device());
   const CUDAGuard current(t.x.device());
   const Tensor y = fresh(t.x.sizes(), t.x), S_T = integer(a[10]) ? fresh_f32({p.num_seqs, p.D, p.N}, t.x) : Tensor(),
                saved = integer(a[11]) ? fresh_f32({(int64_t)(lib.gdr_ssm_saved_bytes(&p) / 4)}, t.x) : Tensor();
-  const size_t bytes = lib.gdr_ssm_fwd_workspace_bytes(&p);
-  const Tensor ws = workspace(bytes, t.x);
+  const Workspace ws(given, lib.gdr_ssm_fwd_workspace_bytes(&p), t.x);
   return answer(lib.gdr_ssm_fwd(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(t.A), ptr(t.Bm), ptr(t.Cm), (const float*)ptr(t.D),
                                 (const float*)ptr(t.bias), (const float*)ptr(S0), ptr(y), (float*)ptr(S_T), (float*)ptr(saved),
-                                ptr(ws), bytes, stream_of(t.x)),
+                                ptr(ws.t), ws.bytes, stream_of(t.x)),
                 {y, S_T, saved});
   END_HANDLE_TH_ERRORS
 }
 
-// x, dt, A, Bm, Cm, h_saved, dy, D, dt_bias, dS_T, cu_seqlens, dt_softplus, want_dS0
+// x, dt, A, Bm, Cm, h_saved, dy, D, dt_bias, dS_T, cu_seqlens, dt_softplus, want_dS0, workspace
 PyObject* ssm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 13);
+  arguments(n, 14);
   const SsmTensors t{required(a[0], "x"), required(a[1], "dt"), required(a[2], "A"), required(a[3], "Bm"),
                      required(a[4], "Cm"), tensor(a[7], "D"), tensor(a[8], "dt_bias")};
   const Tensor &saved = tensor(a[5], "h_saved"), &dy = required(a[6], "dy"), &dS_T = tensor(a[9], "dS_T"),
-               &cu = tensor(a[10], "cu_seqlens");
+               &cu = tensor(a[10], "cu_seqlens"), &given = tensor(a[13], "workspace");
   const gdr_ssm_problem p = ssm_problem(t, 2, cu, integer(a[11]), dy);
   full("dS_T", dS_T, {p.num_seqs, p.D, p.N}, t.x.device());
   const int64_t need = (int64_t)(lib.gdr_ssm_saved_bytes(&p) / 4);
@@ -352,12 +364,11 @@ PyObject* ssm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                dC = fresh(t.Bm.sizes(), t.x), dA = fresh(t.A.sizes(), t.A),
                dD = t.D.defined() ? fresh(t.D.sizes(), t.D) : Tensor(), db = t.bias.defined() ? fresh(t.bias.sizes(), t.bias) : Tensor(),
                dS0 = integer(a[12]) ? fresh_f32({p.num_seqs, p.D, p.N}, t.x) : Tensor();
-  const size_t bytes = lib.gdr_ssm_bwd_workspace_bytes(&p);
-  const Tensor ws = workspace(bytes, t.x);
+  const Workspace ws(given, lib.gdr_ssm_bwd_workspace_bytes(&p), t.x);
   return answer(lib.gdr_ssm_bwd(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(t.A), ptr(t.Bm), ptr(t.Cm), (const float*)ptr(t.D),
                                 (const float*)ptr(t.bias), (const float*)ptr(saved), ptr(dy), (const float*)ptr(dS_T), ptr(dx),
                                 ptr(ddt), (float*)ptr(dA), ptr(dB), ptr(dC), (float*)ptr(dD), (float*)ptr(db), (float*)ptr(dS0),
-                                ptr(ws), bytes, stream_of(t.x)),
+                                ptr(ws.t), ws.bytes, stream_of(t.x)),
                 {dx, ddt, dA, dB, dC, dD, db, dS0});
   END_HANDLE_TH_ERRORS
 }
@@ -456,12 +467,11 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                dres = has_residual ? fresh(x.sizes(), r) : Tensor(), dpost = post.defined() ? fresh(post.sizes(), post) : Tensor(),
                dscale = scale.defined() ? fresh(scale.sizes(), scale) : Tensor(),
                dpre = pre.defined() ? fresh(pre.sizes(), pre) : Tensor();
-  const size_t bytes = lib.gdr_norm_bwd_workspace_bytes(&p);
-  const Tensor ws = workspace(bytes, x);
+  const Workspace ws(lib.gdr_norm_bwd_workspace_bytes(&p), x);
   const void* normed = has_residual ? ptr(r) : pre.defined() ? ptr(x) : nullptr;  // what w_pre was applied to
   return answer(lib.gdr_norm_bwd(&p, ptr(x), (const float*)ptr(post), ptr(gate), (const float*)ptr(scale), normed,
                                  (const float*)ptr(pre), has_residual, ptr(dr), ptr(dy), ptr(dx), ptr(dgate), ptr(dres),
-                                 (float*)ptr(dpost), (float*)ptr(dscale), (float*)ptr(dpre), ptr(ws), bytes, stream_of(x)),
+                                 (float*)ptr(dpost), (float*)ptr(dscale), (float*)ptr(dpre), ptr(ws.t), ws.bytes, stream_of(x)),
                 {dx, dgate, dres, dpost, dscale, dpre});
   END_HANDLE_TH_ERRORS
 }

@@ -21,7 +21,7 @@ def cubes(monkeypatch):
     monkeypatch.setattr(block, "conv_forward", lambda x, w, b, st, *a, **k: (x ** 3, x[:, -3:].clone()))
     monkeypatch.setattr(block, "conv_backward",
                         lambda x, w, b, dy, st, *a: (3 * dy * x ** 2, torch.zeros_like(w), None, None if st is None else torch.zeros_like(st)))
-    monkeypatch.setattr(block, "ssm_forward", lambda x, dt, A, B, C, D, bias, S0, *a: (x ** 3, S0 + 1 if S0 is not None else A + 1, x ** 2))
+    monkeypatch.setattr(block, "ssm_forward", lambda x, dt, A, B, C, D, bias, S0, *a, **k: (x ** 3, S0 + 1 if S0 is not None else A + 1, x ** 2))
     monkeypatch.setattr(block, "ssm_backward", lambda x, dt, A, B, C, saved, dy, D, bias, dS, *a, want_dS0:
                         (3 * dy * saved, *[torch.zeros_like(t) for t in (dt, A, B, C)], None, None, torch.zeros_like(dS) if want_dS0 else None))
     monkeypatch.setattr(block, "norm_forward", lambda x, post, gate, scale, res, pre, eps: (x ** 3 + (0 if res is None else res), None))
