@@ -87,6 +87,10 @@ void full(const char* name, const Tensor& t, IntArrayRef shape, at::Device dev, 
   on_device(name, t, dev);
 }
 
+// A parameter or state that the library reads by 16 bytes: itself, or a copy where it is a view that
+// begins between them (a parameter in a flat buffer).
+Tensor by_16(const Tensor& t) { return ((uintptr_t)ptr(t) & 15u) == 0 ? t : t.detach().clone(); }
+
 // Token stride of a [..., inner dimensions] activation (0: contiguous), -1 if its rows are not
 // contiguous and evenly spaced.
 long long token_stride(const Tensor& t, int inner) {
@@ -336,9 +340,10 @@ PyObject* ssm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const CUDAGuard current(t.x.device());
   const Tensor y = fresh(t.x.sizes(), t.x), S_T = integer(a[10]) ? fresh_f32({p.num_seqs, p.D, p.N}, t.x) : Tensor(),
                saved = integer(a[11]) ? fresh_f32({(int64_t)(lib.gdr_ssm_saved_bytes(&p) / 4)}, t.x) : Tensor();
+  const Tensor A = by_16(t.A), start = by_16(S0);
   const Workspace ws(given, lib.gdr_ssm_fwd_workspace_bytes(&p), t.x);
-  return answer(lib.gdr_ssm_fwd(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(t.A), ptr(t.Bm), ptr(t.Cm), (const float*)ptr(t.D),
-                                (const float*)ptr(t.bias), (const float*)ptr(S0), ptr(y), (float*)ptr(S_T), (float*)ptr(saved),
+  return answer(lib.gdr_ssm_fwd(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(A), ptr(t.Bm), ptr(t.Cm), (const float*)ptr(t.D),
+                                (const float*)ptr(t.bias), (const float*)ptr(start), ptr(y), (float*)ptr(S_T), (float*)ptr(saved),
                                 ptr(ws.t), ws.bytes, stream_of(t.x)),
                 {y, S_T, saved});
   END_HANDLE_TH_ERRORS
@@ -364,9 +369,10 @@ PyObject* ssm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                dC = fresh(t.Bm.sizes(), t.x), dA = fresh(t.A.sizes(), t.A),
                dD = t.D.defined() ? fresh(t.D.sizes(), t.D) : Tensor(), db = t.bias.defined() ? fresh(t.bias.sizes(), t.bias) : Tensor(),
                dS0 = integer(a[12]) ? fresh_f32({p.num_seqs, p.D, p.N}, t.x) : Tensor();
+  const Tensor A = by_16(t.A), end = by_16(dS_T), states = by_16(saved);
   const Workspace ws(given, lib.gdr_ssm_bwd_workspace_bytes(&p), t.x);
-  return answer(lib.gdr_ssm_bwd(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(t.A), ptr(t.Bm), ptr(t.Cm), (const float*)ptr(t.D),
-                                (const float*)ptr(t.bias), (const float*)ptr(saved), ptr(dy), (const float*)ptr(dS_T), ptr(dx),
+  return answer(lib.gdr_ssm_bwd(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(A), ptr(t.Bm), ptr(t.Cm), (const float*)ptr(t.D),
+                                (const float*)ptr(t.bias), (const float*)ptr(states), ptr(dy), (const float*)ptr(end), ptr(dx),
                                 ptr(ddt), (float*)ptr(dA), ptr(dB), ptr(dC), (float*)ptr(dD), (float*)ptr(db), (float*)ptr(dS0),
                                 ptr(ws.t), ws.bytes, stream_of(t.x)),
                 {dx, ddt, dA, dB, dC, dD, db, dS0});
@@ -387,8 +393,8 @@ PyObject* ssm_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   check_slots(slots, state, p.B, dev);
   p.num_slots = size32("state", state.size(0));
   const CUDAGuard current(dev);
-  const Tensor y = fresh({p.B, p.D}, t.x);
-  return answer(lib.gdr_ssm_step(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(t.A), ptr(t.Bm), ptr(t.Cm), (const float*)ptr(t.D),
+  const Tensor A = by_16(t.A), y = fresh({p.B, p.D}, t.x);
+  return answer(lib.gdr_ssm_step(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(A), ptr(t.Bm), ptr(t.Cm), (const float*)ptr(t.D),
                                  (const float*)ptr(t.bias), (float*)ptr(state), (const int32_t*)ptr(slots), ptr(y),
                                  stream_of(t.x)),
                 y);

@@ -13,8 +13,10 @@
  *    have the problem's dtype (F32 or BF16); arithmetic and every sum run in float32.
  *  - Activations that come in may be row-strided: ld_* is the distance between tokens in
  *    elements, at least the row's width; 0 means contiguous.  What goes out is contiguous.
- *    Base pointers need their element's alignment only; 16-byte aligned pointers and strides
- *    take the vector path.
+ *    Base pointers need their element's alignment only, and 16-byte aligned pointers and strides
+ *    take the vector path, but for the fp32 tensors of states, which are read and written by
+ *    16 bytes and refused (GDR_ERR_ALIGNMENT) unless they are aligned to 16: A, S0, S_T, dS_T,
+ *    dS0, h_saved and the pools of gdr_ssm_step and gdr_step.  Workspaces: 256 bytes, as in gdr.h.
  *  - Variable length: as in gdr.h (B = 1, cu_seqlens on the device).  A malformed cu_seqlens is
  *    found on the device: nothing is computed and gdr_workspace_status reports it.
  *  - A step reads and writes its states in place in a pool of num_slots states; slots (device,
