@@ -90,9 +90,9 @@ __device__ __forceinline__ void load_taps(const float* w, const float* bias, lon
 }
 
 // V neighbouring elements as they come from memory, converted where they are used, so that a load is
-// not waited for before that.
+// not waited for before that.  Aligned to its size: in shared memory it is the target of one asynchronous copy.
 template <typename IT, int V>
-struct Raw {
+struct alignas(V * sizeof(IT)) Raw {
   uint32_t w[V * sizeof(IT) / 4];
   __device__ __forceinline__ void load(const IT* p) {
     if constexpr (sizeof(w) == 8) {
@@ -143,6 +143,7 @@ __device__ __forceinline__ void store_row(IT* p, const f32x2 (&v)[kPairs<V>]) {
 template <typename IT, int V, int NS, int DEEP, typename F>
 __device__ __forceinline__ void walk_rows(const IT* const (&src)[NS], const long long (&ld)[NS], int n, Raw<IT, V>* slots,
                                           F row) {
+  static_assert(alignof(Raw<IT, V>) == sizeof(Raw<IT, V>), "a slot takes one copy of its size");
   const IT* p[NS];
 #pragma unroll
   for (int s = 0; s < NS; ++s) p[s] = src[s];
