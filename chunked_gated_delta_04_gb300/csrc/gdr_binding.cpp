@@ -175,6 +175,13 @@ PyObject* answer(gdr_status st, std::initializer_list<Tensor> ts) {
   return tuple;
 }
 
+// After a call that changed t in place: its version tells autograd, which may have saved it.  (Tensors of
+// inference mode have none.)
+gdr_status changed(const Tensor& t, gdr_status st) {
+  if (st == GDR_OK && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  return st;
+}
+
 long integer(PyObject* o) {
   const long v = PyLong_AsLong(o);
   if (v == -1 && PyErr_Occurred()) throw python_error();
@@ -278,8 +285,8 @@ PyObject* conv_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p.ld_x = strided("x", x, 1);
   const CUDAGuard current(dev);
   const Tensor y = fresh({B, C}, x);
-  return answer(lib.gdr_conv_step(&p, ptr(x), (const float*)ptr(w), (const float*)ptr(b), ptr(state),
-                                  (const int32_t*)ptr(slots), ptr(y), stream_of(x)),
+  return answer(changed(state, lib.gdr_conv_step(&p, ptr(x), (const float*)ptr(w), (const float*)ptr(b), ptr(state),
+                                                 (const int32_t*)ptr(slots), ptr(y), stream_of(x))),
                 y);
   END_HANDLE_TH_ERRORS
 }
@@ -394,9 +401,9 @@ PyObject* ssm_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p.num_slots = size32("state", state.size(0));
   const CUDAGuard current(dev);
   const Tensor A = by_16(t.A), y = fresh({p.B, p.D}, t.x);
-  return answer(lib.gdr_ssm_step(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(A), ptr(t.Bm), ptr(t.Cm), (const float*)ptr(t.D),
-                                 (const float*)ptr(t.bias), (float*)ptr(state), (const int32_t*)ptr(slots), ptr(y),
-                                 stream_of(t.x)),
+  return answer(changed(state, lib.gdr_ssm_step(&p, ptr(t.x), ptr(t.dt), (const float*)ptr(A), ptr(t.Bm), ptr(t.Cm),
+                                                (const float*)ptr(t.D), (const float*)ptr(t.bias), (float*)ptr(state),
+                                                (const int32_t*)ptr(slots), ptr(y), stream_of(t.x))),
                 y);
   END_HANDLE_TH_ERRORS
 }
@@ -516,8 +523,8 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p.prologue = (unsigned)integer(a[9]);
   const CUDAGuard current(dev);
   const Tensor o = fresh({B, Hv, DV}, v);
-  return answer(lib.gdr_step(&p, ptr(q), ptr(k), ptr(v), (const float*)ptr(g), ptr(beta), (float*)ptr(state), num_slots,
-                             (const int32_t*)ptr(slots), ptr(o), stream_of(q)),
+  return answer(changed(state, lib.gdr_step(&p, ptr(q), ptr(k), ptr(v), (const float*)ptr(g), ptr(beta), (float*)ptr(state),
+                                            num_slots, (const int32_t*)ptr(slots), ptr(o), stream_of(q))),
                 o);
   END_HANDLE_TH_ERRORS
 }
