@@ -10,41 +10,8 @@ namespace gdr {
 
 constexpr int kSmCount = 152;  // SMs of a GB300: grids are sized against it
 
-// V elements of one row in fp32: vector accesses for V = 4 and 8, scalar for V = 1.  p is aligned to
+// Stores of V elements of one row from fp32: vector accesses for V = 4 and 8, scalar for V = 1.  p is aligned to
 // the access (at most 16 bytes).
-template <int V>
-__device__ __forceinline__ void load_v(const float* p, float (&v)[V]) {
-  if constexpr (V == 1) {
-    v[0] = p[0];
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(p + i);
-      v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
-    }
-  }
-}
-template <int V>
-__device__ __forceinline__ void load_v(const __nv_bfloat16* p, float (&v)[V]) {
-  if constexpr (V == 1) {
-    v[0] = __bfloat162float(p[0]);
-  } else if constexpr (V == 4) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    v[0] = __uint_as_float(x.x << 16); v[1] = __uint_as_float(x.x & 0xffff0000u);
-    v[2] = __uint_as_float(x.y << 16); v[3] = __uint_as_float(x.y & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; i += 8) {
-      const uint4 x = *reinterpret_cast<const uint4*>(p + i);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {  // a bf16 is the upper half of the float of the same value
-        v[i + 2 * j] = __uint_as_float(w[j] << 16);
-        v[i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
-    }
-  }
-}
 template <int V>
 __device__ __forceinline__ void store_v(float* p, const float (&v)[V]) {
   if constexpr (V == 1) {
