@@ -309,12 +309,14 @@ def norm_forward(x, post_weight=None, gate=None, scale=None, residual=None, pre_
 
 def norm_backward(x, post_weight=None, gate=None, scale=None, r=None, pre_weight=None, dr=None, dy=None, eps=1e-6,
                   stream=None):
-    """Gradients of norm_forward from dr and dy (either may be None): (dx, dgate, dresidual, dpost_weight,
-    dscale, dpre_weight), None where the forward had no such tensor.  r: the forward's r where it had a
-    residual, else None."""
+    """Gradients of norm_forward from dr and dy, the gradients of the outputs that it had (of two, either may be
+    None): (dx, dgate, dresidual, dpost_weight, dscale, dpre_weight), None where the forward had no such tensor.
+    r: the forward's r where it had a residual, else None."""
     if stream is not None:
         with _on(stream, x):
             return norm_backward(x, post_weight, gate, scale, r, pre_weight, dr, dy, eps)
+    if dy is None and dr is not None and pre_weight is not None and r is not None:  # the library wants it with pre_weight
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
     return _done(_binding().norm_backward(x, post_weight, gate, scale, r, pre_weight, dr, dy, eps), "gdr_norm_bwd")
 
 

@@ -131,7 +131,7 @@ gdr_status gdr_norm_fwd(const gdr_norm_problem* p, const void* x, const float* w
 size_t gdr_norm_bwd_workspace_bytes(const gdr_norm_problem* p);
 
 /* r: the forward's r (required with w_pre; without a residual the forward's x).  dr (nullable: zero)
- * and dy (w_pre only) are the gradients of r and y; at least one is given.  has_residual says whether
+ * and dy (with w_pre, and only then) are the gradients of r and y; at least one is given.  has_residual says whether
  * the forward had one.  dresidual (nullable) is written when it had; dw_post, dgate, dscale, dw_pre
  * are required where the forward had their tensors. */
 gdr_status gdr_norm_bwd(const gdr_norm_problem* p, const void* x, const float* w_post, const void* gate,

@@ -149,3 +149,16 @@ def test_norm_outputs(mode):
     there((r, y), (has["res"] or not has["pre"], has["pre"]))
     there(gdr.norm_backward(d["x"], d["post"], d["z"], d["scale"], r if has["res"] else None, d["pre"], d["dr"], d["dy"]),
           (1, has["z"], has["res"], has["post"], has["scale"], has["pre"]))
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (BF, F32)])
+def test_norm_backward_of_one_output(types):
+    """Of two outputs either gradient may be absent: as one of zeros."""
+    d = norm_inputs("full", *types, (5, 48))
+    r, _ = gdr.norm_forward(d["x"], d["post"], d["z"], d["scale"], d["res"], d["pre"])
+
+    def grads(dr, dy):
+        return gdr.norm_backward(d["x"], d["post"], d["z"], d["scale"], r, d["pre"], dr, dy)
+
+    for a, b in ((grads(d["dr"], None), grads(d["dr"], torch.zeros_like(d["dy"]))), (grads(None, d["dy"]), grads(torch.zeros_like(d["dr"]), d["dy"]))):
+        assert all(torch.equal(s, t) for s, t in zip(a, b))
