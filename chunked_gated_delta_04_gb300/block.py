@@ -361,8 +361,8 @@ _LAYOUT = {"KV": 0, "VK": 1}
 def step(q, k, v, g, beta, state, layout="KV", scale=None, slots=None, prologue=0, stream=None):
     """The gated delta rule for one token per row: q, k [B, Hk, DK], v [B, Hv, DV], g [B, Hv] fp32,
     beta [B, Hv]; state, a pool [num_slots, Hv, DK, DV] ("KV") or [num_slots, Hv, DV, DK] ("VK") fp32,
-    is updated in place at each row's slot (see conv_step).  prologue: GDR_PROLOGUE_* bits, as in
-    forward (the mapped q, k and beta stay in fp32 here).  Returns o [B, Hv, DV]."""
+    is updated in place at each row's slot (see conv_step).  scale: None (or not above 0) is 1 / sqrt(DK).  prologue:
+    GDR_PROLOGUE_* bits, as in forward (the mapped q, k and beta stay in fp32 here).  Returns o [B, Hv, DV]."""
     if stream is not None:
         with _on(stream, q):
             return step(q, k, v, g, beta, state, layout, scale, slots, prologue)

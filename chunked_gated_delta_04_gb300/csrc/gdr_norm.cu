@@ -21,8 +21,10 @@ struct FwdPtrs {
 
 // Blocks per SM to fit the registers to (0: the compiler's choice).  Rows of 512 threads with everything
 // take 72 registers unasked, which leaves one block per SM: 8192 x 4096, bf16 with an fp32 stream, 108 us; with 64
-// registers and two blocks 80 us.  Wider rows would spill; narrower ones are better off unasked (8192 x
-// 2048, add: 22.4 us against 23.6).
+// registers and two blocks 80 us.  In fp32, where the cap was not measured against none, it costs 44 to 56
+// bytes of spills in the general kernel and with everything.  Wider rows spill without a cap (above 8192 channels 36 to
+// 280 bytes in bf16, up to 3.7 KB in fp32: 2048 x 16384, everything, fp32 267 us, where the bytes are 100); narrower ones
+// are better off unasked (8192 x 2048, add: 22.4 us against 23.6).
 constexpr int fwd_min_blocks(int TPR, int K) { return TPR == 512 && K == 1 ? 2 : 0; }
 
 // A block walks rows and has the next ones' loads in flight while it works on the present ones.

@@ -20,13 +20,16 @@ struct NormDims {
 
 // The token of a row.  Rows that lie evenly apart (heads 1, to which the host brings what it can) take no
 // division: with a 64-bit one per row, for eight channels a thread, gated 131072 x 128 took 61 us for both directions, now 58.6.
+// (The staged rows of the backward, which have a block each, still take one.)
 __device__ __forceinline__ long long token_of(const NormDims& d, long long row) {
   if (d.heads == 1) return row;
   return row < (1ll << 31) ? (long long)((uint32_t)row / (uint32_t)d.heads) : row / d.heads;
 }
 
-// Which tensors a call has.  The kernels are built for the combinations that models use, where
-// what is absent costs no registers, and once for any other (kNormAny: asked at run time).
+// Which tensors a call has.  The kernels are built for three combinations (norm_parts), where what is absent
+// costs no registers, and once for any other (kNormAny: asked at run time).  A norm alone in front of a block, and one behind
+// a scaled residual add, are among the others: 8192 x 4096, bf16, backward 78 us (bytes: 30) and 113 (60), where the
+// residual add's own kernel takes 84 (50).
 enum NormParts { kNormPost = 1, kNormGate = 2, kNormScale = 4, kNormPre = 8, kNormRes = 16, kNormAny = -1 };
 
 // Eight neighbouring channels as they come from memory, converted where they are used, so that a

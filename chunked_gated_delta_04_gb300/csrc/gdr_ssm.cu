@@ -502,7 +502,9 @@ gdr_status resolve_ssm(const gdr_ssm_problem* p, bool step, SsmDims* d) {
   // sequences into segments costs the first pass (0.7 of the full one).  So segments pay below about
   // one block per SM (B = 2, T = 4096, D = 4096, N = 16, 128 blocks: 285 us against 328), and where a
   // packed batch's longest sequence, which the host does not know, may be twice the average, below
-  // two.  They are made of at least 64 tokens, enough for six blocks per SM.
+  // two.  They are made of at least 64 tokens, enough for six blocks per SM.  The rule takes a packed batch's
+  // sequences for about equally long: one that outweighs the others is not cut where their number is large (D = 1024, N =
+  // 16, bf16, 30000 tokens and 19 times 100: forward 2254 us, backward 5403; 20 times 1595: 225 and 719).
   const long long blocks = fwd_blocks(*d), whole = (d->T + kTile - 1) / kTile * (long long)kTile;
   d->Lseg = (int)(whole < kTile ? kTile : whole);
   if (!step && d->total > 0 && blocks * d->num_seqs < (d->cu ? 2 : 1) * kSmCount) {

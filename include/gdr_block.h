@@ -22,7 +22,7 @@
  *  - A step reads and writes its states in place in a pool of num_slots states; slots (device,
  *    int32 [B], NULL: row i uses state i) names each row's.  A row whose slot is negative or not
  *    below num_slots is skipped and its output set to zero.  Two rows of one call must not name
- *    the same slot.
+ *    the same slot.  Rows of a call: at most 65535 (gdr_step), 262140 (the others).
  *  - Results are bitwise reproducible: no floating-point atomics.
  */
 #ifndef GDR_BLOCK_H_
