@@ -15,7 +15,9 @@ High-level helpers: ``forward`` / ``backward`` allocate outputs and workspace wi
 torch; ``chunk_gated_delta_rule`` is the autograd entry point.
 
 The operators that stand around it in a model (short causal convolution, selective
-scan, block norms, single-token step) are in ``block`` and re-exported here.
+scan, block norms, single-token step) are in ``block``, the attention mixer that stands
+beside it (rotary positions, attention, its step over a paged cache) in ``attn``;
+both are re-exported here.
 """
 from __future__ import annotations
 
@@ -32,6 +34,10 @@ from .block import (  # noqa: F401 - the operators around the gated delta rule
     BLOCK_EXPORTS, block_norm, causal_conv, conv_backward, conv_forward, conv_step, conv_workspace, gdr_conv_problem,
     gdr_norm_problem, gdr_ssm_problem, norm_backward, norm_forward, selective_scan, ssm_backward, ssm_forward,
     ssm_step, ssm_workspace, step)
+from .attn import (  # noqa: F401 - the attention mixer beside it
+    ATTN_EXPORTS, attention, attn_backward, attn_forward, attn_step, attn_workspace, cache_write, cache_write_workspace,
+    gdr_attn_problem, gdr_cache_problem, gdr_rope_problem, rope, rope_backward, rope_forward, rope_frequencies,
+    rope_workspace)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdr.so")
@@ -70,7 +76,7 @@ EXPORTS = ["gdr_max_chunks", "gdr_saved_states_bytes", "gdr_fwd_workspace_bytes"
            "gdr_fwd", "gdr_bwd", "gdr_workspace_status", "gdr_status_string", "gdr_path",
            "gdr_debug_set_stage_events", "gdr_debug_stage_count", "gdr_debug_stage_name",
            "gdr_debug_launch_count", "gdr_debug_last_cuda_error", "gdr_debug_cuda_error_string", "gdr_fwd_noalloc", "gdr_noalloc_status", "gdr_debug_tc_gemm", "gdr_debug_timeout_selftest", "gdr_debug_cp_segment", "gdr_debug_cp_segments",
-           *BLOCK_EXPORTS]
+           *BLOCK_EXPORTS, *ATTN_EXPORTS]
 
 
 def _open(path: str):

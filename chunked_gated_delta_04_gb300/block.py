@@ -80,6 +80,16 @@ def declare(lib, gdr_problem) -> None:
         fn.restype = result
     lib.gdr_step.argtypes = [_c.POINTER(gdr_problem)] + [_P] * 6 + [_I] + [_P] * 3
     lib.gdr_step.restype = _I
+    for name, (problem, args, result) in _attn().SIGNATURES.items():
+        fn = getattr(lib, name)
+        fn.argtypes = [_c.POINTER(problem)] + args
+        fn.restype = result
+
+
+def _attn():
+    from . import attn  # which imports this module
+
+    return attn
 
 
 _gdr = sys.modules[__package__]  # the package itself, which imports this module
@@ -99,7 +109,7 @@ def _binding():
             spec = importlib.util.spec_from_loader("gdr_binding", loader)
             _module = importlib.util.module_from_spec(spec)
             loader.exec_module(_module)
-        _module.bind({n: _c.cast(getattr(lib, n), _c.c_void_p).value for n in BLOCK_EXPORTS})
+        _module.bind({n: _c.cast(getattr(lib, n), _c.c_void_p).value for n in BLOCK_EXPORTS + _attn().ATTN_EXPORTS})
         _bound = lib
     return _module
 

@@ -1,5 +1,5 @@
 """Build libgdr.so in-tree: every csrc/*.cu compiled for sm_103a only, in parallel, then linked; and
-gdr_binding.so, the torch binding of the block operators (csrc/gdr_binding.cpp, g++).
+gdr_binding.so, the torch binding of the block and attention operators (csrc/gdr_binding.cpp, g++).
 
     python -m chunked_gated_delta_04_gb300.build [--force] [--delay]
 
@@ -44,7 +44,7 @@ def _sources():
 
 def _deps():
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))) + [
-        os.path.join(INCLUDE, "gdr.h"), os.path.join(INCLUDE, "gdr_block.h")]
+        os.path.join(INCLUDE, name) for name in ("gdr.h", "gdr_block.h", "gdr_attn.h")]
 
 
 def _target(delay: bool):
@@ -92,7 +92,7 @@ def build_binding(force: bool = False) -> str:
 
     flags = _binding_flags()
     stamp, stamp_path = " ".join([torch.__version__] + flags), BINDING + ".flags"
-    deps = [BINDING_SRC, os.path.join(INCLUDE, "gdr.h"), os.path.join(INCLUDE, "gdr_block.h")]
+    deps = [BINDING_SRC] + [os.path.join(INCLUDE, name) for name in ("gdr.h", "gdr_block.h", "gdr_attn.h")]
     if not force and os.path.exists(BINDING) and os.path.exists(stamp_path):
         with open(stamp_path) as f:
             if f.read() == stamp and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):

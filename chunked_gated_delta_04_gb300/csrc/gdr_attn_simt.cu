@@ -1,0 +1,333 @@
+// gdr_attn_simt.cu -- attention in fp32 on the CUDA cores (include/gdr_attn.h): fp32 problems, whose
+// accuracy the tensor cores' bf16 and tf32 products do not give, and bf16 ones that are not aligned for TMA.
+//
+//   forward     per 64 queries of a head, over the visible keys 64 at a time: S = scale Q K^T, running row
+//               maximum m and sum l, O <- O e^(m_old - m) + e^(S - m) V;  o = O / l, lse = m + log l
+//   backward    P = e^(S - lse), dS = P (dO V^T - delta):
+//               per 64 keys of a key head, over its query heads and the queries that see them: dV += P^T dO,
+//               dK += scale dS^T Q;  per 64 queries: dQ += scale dS K
+// A block is 16 x 16 threads; a thread holds 4 x 4 of S (rows ty + 16 r, columns tx + 16 c) and 4 rows by D / 16
+// features of an accumulator.  Bound by the FMA pipes and the shared-memory reads that feed them: 16 products for
+// every two 16-byte reads.
+#include "gdr_attn.cuh"
+
+namespace gdr {
+namespace {
+
+constexpr int kT = kSimtTile;
+constexpr int kThreads = 256;
+constexpr int kPS = kT + 4;  // row stride of a tile of P in floats
+
+// rows [r0, r0 + 64) of a head's [tokens, D] activations to shared memory [64][DP + 4] as fp32, zeros outside.
+template <typename IT, int DP>
+__device__ __forceinline__ void load_tile(float* dst, const IT* src, long long ld, int r0, int rows, int D) {
+  constexpr int S = DP + 4;
+  for (int e = threadIdx.x; e < kT * DP; e += kThreads) {
+    const int r = e / DP, c = e % DP;
+    dst[r * S + c] = r0 + r < rows && c < D ? to_f32(src[(long long)(r0 + r) * ld + c]) : 0.f;
+  }
+}
+
+// acc[r][c] += A[ty + 16 r] . B[tx + 16 c] over the DP features.
+template <int DP>
+__device__ __forceinline__ void dot_tile(const float* A, const float* B, int tx, int ty, float (&acc)[4][4]) {
+  constexpr int S = DP + 4;
+#pragma unroll 4
+  for (int k = 0; k < DP; k += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4*>(A + (ty + 16 * r) * S + k);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * S + k);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        acc[r][c] = fmaf(a[r].x, b[c].x, fmaf(a[r].y, b[c].y, fmaf(a[r].z, b[c].z, fmaf(a[r].w, b[c].w, acc[r][c]))));
+  }
+}
+
+// out[r][.] += sum_j M[ty + 16 r][j] X[j][features 4 tx + 64 w ..]: M [64][kPS], X [64][DP + 4].
+template <int DP>
+__device__ __forceinline__ void row_product(const float* M, const float* X, int tx, int ty, float (&out)[4][DP / 16]) {
+  constexpr int S = DP + 4;
+#pragma unroll 2
+  for (int j = 0; j < kT; j += 4) {
+    float4 p[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) p[r] = *reinterpret_cast<const float4*>(M + (ty + 16 * r) * kPS + j);
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+      for (int w = 0; w < DP / 64; ++w) {
+        const float4 x = *reinterpret_cast<const float4*>(X + (j + jj) * S + 4 * tx + 64 * w);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float pr = jj == 0 ? p[r].x : jj == 1 ? p[r].y : jj == 2 ? p[r].z : p[r].w;
+          out[r][4 * w] = fmaf(pr, x.x, out[r][4 * w]);
+          out[r][4 * w + 1] = fmaf(pr, x.y, out[r][4 * w + 1]);
+          out[r][4 * w + 2] = fmaf(pr, x.z, out[r][4 * w + 2]);
+          out[r][4 * w + 3] = fmaf(pr, x.w, out[r][4 * w + 3]);
+        }
+      }
+  }
+}
+
+// out[r][.] += sum_i M[i][4 ty + r] X[i][features 4 tx + 64 w ..].
+template <int DP>
+__device__ __forceinline__ void column_product(const float* M, const float* X, int tx, int ty, float (&out)[4][DP / 16]) {
+  constexpr int S = DP + 4;
+#pragma unroll 4
+  for (int i = 0; i < kT; ++i) {
+    const float4 p = *reinterpret_cast<const float4*>(M + i * kPS + 4 * ty);
+#pragma unroll
+    for (int w = 0; w < DP / 64; ++w) {
+      const float4 x = *reinterpret_cast<const float4*>(X + i * S + 4 * tx + 64 * w);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float pr = r == 0 ? p.x : r == 1 ? p.y : r == 2 ? p.z : p.w;
+        out[r][4 * w] = fmaf(pr, x.x, out[r][4 * w]);
+        out[r][4 * w + 1] = fmaf(pr, x.y, out[r][4 * w + 1]);
+        out[r][4 * w + 2] = fmaf(pr, x.z, out[r][4 * w + 2]);
+        out[r][4 * w + 3] = fmaf(pr, x.w, out[r][4 * w + 3]);
+      }
+    }
+  }
+}
+
+// An accumulator's row: features 4 tx + 64 w .. of it, times f.
+template <typename IT, int DP>
+__device__ __forceinline__ void store_row(IT* dst, const float (&v)[DP / 16], float f, int tx, int D) {
+#pragma unroll
+  for (int w = 0; w < DP / 64; ++w)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = 4 * tx + 64 * w + e;
+      if (c < D) dst[c] = from_f32<IT>(v[4 * w + e] * f);
+    }
+}
+
+template <int DP>
+constexpr size_t tile_bytes() { return sizeof(float) * kT * (DP + 4); }
+
+template <typename IT, int DP>
+__global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnDims d, AttnTiles t, AttnFwdArgs a) {
+  extern __shared__ float smem[];
+  float *Q = smem, *KV = Q + kT * (DP + 4), *P = KV + kT * (DP + 4);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *a.status = 0;  // of a packed batch: the tile table's kernel
+  int seq, h, tile;
+  if (!attn_tile(d, t, d.Hq, blockIdx.x, &seq, &h, &tile)) return;
+  const AttnSpan s = attn_span(d, seq);
+  const int i0 = tile * kT, off = s.m - s.n, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  if (i0 >= s.n) return;
+  const IT* q = (const IT*)a.q + s.q0 * d.ld_q + (long long)h * d.D;
+  const IT* k = (const IT*)a.k + s.k0 * d.ld_k + (long long)(h / d.G) * d.D;
+  const IT* v = (const IT*)a.v + s.k0 * d.ld_v + (long long)(h / d.G) * d.D;
+  load_tile<IT, DP>(Q, q, d.ld_q, i0, s.n, d.D);
+  float O[4][DP / 16] = {}, m[4], l[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = 0.f;
+  int lo, hi;
+  attn_keys(d, s, i0, min(s.n, i0 + kT), &lo, &hi);
+  const float c = d.scale * kLog2e;
+  for (int j0 = lo / kT * kT; j0 < hi; j0 += kT) {
+    __syncthreads();  // the values of the keys before are used up
+    load_tile<IT, DP>(KV, k, d.ld_k, j0, s.m, d.D);
+    __syncthreads();
+    float S[4][4] = {};
+    dot_tile<DP>(Q, KV, tx, ty, S);
+    __syncthreads();
+    load_tile<IT, DP>(KV, v, d.ld_v, j0, s.m, d.D);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = i0 + ty + 16 * r;
+      float top = m[r];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + tx + 16 * e;
+        S[r][e] = j < s.m && attn_sees(d, off, i, j) ? S[r][e] : -INFINITY;
+        // a NaN goes into the maximum, and from there into the row
+        top = S[r][e] > top || S[r][e] != S[r][e] ? S[r][e] : top;
+      }
+#pragma unroll
+      for (int x = 1; x < 16; x <<= 1) {
+        const float other = __shfl_xor_sync(0xffffffffu, top, x);
+        top = other > top || other != other ? other : top;
+      }
+      const float base = top == -INFINITY ? 0.f : top * c;  // a row that has seen nothing yet: e^(-inf - 0) = 0
+      const float f = ex2f(fmaf(m[r], c, -base));
+      m[r] = top;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p = ex2f(fmaf(S[r][e], c, -base));
+        sum += p;
+        P[(ty + 16 * r) * kPS + tx + 16 * e] = p;
+      }
+#pragma unroll
+      for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      l[r] = fmaf(l[r], f, sum);
+#pragma unroll
+      for (int e = 0; e < DP / 16; ++e) O[r][e] *= f;
+    }
+    __syncthreads();
+    row_product<DP>(P, KV, tx, ty, O);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = i0 + ty + 16 * r;
+    if (i >= s.n) continue;
+    store_row<IT, DP>((IT*)a.o + (s.q0 + i) * (long long)d.Hq * d.D + (long long)h * d.D, O[r], m[r] == -INFINITY ? 0.f : 1.f / l[r], tx, d.D);
+    if (tx == 0)
+      a.lse[s.lse0 + (long long)h * d.Tq + i] = m[r] == -INFINITY ? -INFINITY : fmaf(m[r], d.scale, logf(l[r]));
+  }
+}
+
+// P and dS of a tile: rows i0 .., columns j0 .. of a sequence.
+template <int DP>
+__device__ __forceinline__ void grad_tile(const AttnDims& d, const AttnSpan& s, int i0, int j0, const float* Q, const float* K,
+                                          const float* dO, const float* V, const float* lse, const float* delta, int tx, int ty,
+                                          float (&p)[4][4], float (&ds)[4][4]) {
+  const int off = s.m - s.n;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[r][e] = ds[r][e] = 0.f;
+  dot_tile<DP>(Q, K, tx, ty, p);
+  dot_tile<DP>(dO, V, tx, ty, ds);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = i0 + ty + 16 * r;
+    const float ls = i < s.n ? lse[i] : 0.f, dl = i < s.n ? delta[i] : 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + tx + 16 * e;
+      const bool on = i < s.n && j < s.m && attn_sees(d, off, i, j);
+      p[r][e] = on ? ex2f(kLog2e * fmaf(p[r][e], d.scale, -ls)) : 0.f;
+      ds[r][e] = on ? p[r][e] * (ds[r][e] - dl) : 0.f;
+    }
+  }
+}
+
+__device__ __forceinline__ void put_tile(float* dst, const float (&v)[4][4], int tx, int ty) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dst[(ty + 16 * r) * kPS + tx + 16 * e] = v[r][e];
+}
+
+template <typename IT, int DP>
+__global__ void __launch_bounds__(kThreads) attn_dkdv_simt_kernel(AttnDims d, AttnTiles t, AttnBwdArgs a) {
+  extern __shared__ float smem[];
+  constexpr int N = kT * (DP + 4);
+  float *K = smem, *V = K + N, *Q = V + N, *dO = Q + N, *M = dO + N;
+  int seq, h, tile;
+  if (!attn_tile(d, t, d.Hk, blockIdx.x, &seq, &h, &tile)) return;
+  const AttnSpan s = attn_span(d, seq);
+  const int j0 = tile * kT, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  if (j0 >= s.m) return;
+  load_tile<IT, DP>(K, (const IT*)a.k + s.k0 * d.ld_k + (long long)h * d.D, d.ld_k, j0, s.m, d.D);
+  load_tile<IT, DP>(V, (const IT*)a.v + s.k0 * d.ld_v + (long long)h * d.D, d.ld_v, j0, s.m, d.D);
+  float dK[4][DP / 16] = {}, dV[4][DP / 16] = {};
+  int lo, hi;
+  attn_queries(d, s, j0, min(s.m, j0 + kT), &lo, &hi);
+  for (int g = 0; g < d.G; ++g) {
+    const int hq = h * d.G + g;
+    const long long stat = s.lse0 + (long long)hq * d.Tq;
+    for (int i0 = lo / kT * kT; i0 < hi; i0 += kT) {
+      __syncthreads();
+      load_tile<IT, DP>(Q, (const IT*)a.q + s.q0 * d.ld_q + (long long)hq * d.D, d.ld_q, i0, s.n, d.D);
+      load_tile<IT, DP>(dO, (const IT*)a.dout + s.q0 * d.ld_do + (long long)hq * d.D, d.ld_do, i0, s.n, d.D);
+      __syncthreads();
+      float p[4][4], ds[4][4];
+      grad_tile<DP>(d, s, i0, j0, Q, K, dO, V, a.lse + stat, a.delta + stat, tx, ty, p, ds);
+      put_tile(M, p, tx, ty);
+      __syncthreads();
+      column_product<DP>(M, dO, tx, ty, dV);
+      __syncthreads();
+      put_tile(M, ds, tx, ty);
+      __syncthreads();
+      column_product<DP>(M, Q, tx, ty, dK);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int j = j0 + 4 * ty + r;
+    if (j >= s.m) continue;
+    const long long at = (s.k0 + j) * (long long)d.Hk * d.D + (long long)h * d.D;
+    store_row<IT, DP>((IT*)a.dk + at, dK[r], d.scale, tx, d.D);
+    store_row<IT, DP>((IT*)a.dv + at, dV[r], 1.f, tx, d.D);
+  }
+}
+
+template <typename IT, int DP>
+__global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(AttnDims d, AttnTiles t, AttnBwdArgs a) {
+  extern __shared__ float smem[];
+  constexpr int N = kT * (DP + 4);
+  float *Q = smem, *dO = Q + N, *K = dO + N, *V = K + N, *M = V + N;
+  int seq, h, tile;
+  if (!attn_tile(d, t, d.Hq, blockIdx.x, &seq, &h, &tile)) return;
+  const AttnSpan s = attn_span(d, seq);
+  const int i0 = tile * kT, hk = h / d.G, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  if (i0 >= s.n) return;
+  const long long stat = s.lse0 + (long long)h * d.Tq;
+  load_tile<IT, DP>(Q, (const IT*)a.q + s.q0 * d.ld_q + (long long)h * d.D, d.ld_q, i0, s.n, d.D);
+  load_tile<IT, DP>(dO, (const IT*)a.dout + s.q0 * d.ld_do + (long long)h * d.D, d.ld_do, i0, s.n, d.D);
+  float dQ[4][DP / 16] = {};
+  int lo, hi;
+  attn_keys(d, s, i0, min(s.n, i0 + kT), &lo, &hi);
+  for (int j0 = lo / kT * kT; j0 < hi; j0 += kT) {
+    __syncthreads();
+    load_tile<IT, DP>(K, (const IT*)a.k + s.k0 * d.ld_k + (long long)hk * d.D, d.ld_k, j0, s.m, d.D);
+    load_tile<IT, DP>(V, (const IT*)a.v + s.k0 * d.ld_v + (long long)hk * d.D, d.ld_v, j0, s.m, d.D);
+    __syncthreads();
+    float p[4][4], ds[4][4];
+    grad_tile<DP>(d, s, i0, j0, Q, K, dO, V, a.lse + stat, a.delta + stat, tx, ty, p, ds);
+    put_tile(M, ds, tx, ty);
+    __syncthreads();
+    row_product<DP>(M, K, tx, ty, dQ);
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = i0 + ty + 16 * r;
+    if (i < s.n) store_row<IT, DP>((IT*)a.dq + (s.q0 + i) * (long long)d.Hq * d.D + (long long)h * d.D, dQ[r], d.scale, tx, d.D);
+  }
+}
+
+template <typename F, typename A>
+cudaError_t go(F kernel, long long grid, size_t smem, const AttnDims& d, const AttnTiles& t, const A& a, cudaStream_t s, const char* stage) {
+  if (grid == 0) return cudaSuccess;
+  cudaError_t e = set_smem_once((const void*)kernel, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)grid, kThreads, smem, s>>>(d, t, a);
+  stage_mark(s, stage);
+  return cudaGetLastError();
+}
+
+template <typename IT, int DP>
+cudaError_t fwd(const AttnDims& d, const AttnTiles& t, const AttnFwdArgs& a, cudaStream_t s) {
+  return go(attn_fwd_simt_kernel<IT, DP>, attn_tile_count(d, false, kT) * d.Hq, 2 * tile_bytes<DP>() + sizeof(float) * kT * kPS, d, t, a,
+            s, "attn_fwd");
+}
+template <typename IT, int DP>
+cudaError_t bwd(const AttnDims& d, const AttnTiles& tq, const AttnTiles& tk, const AttnBwdArgs& a, cudaStream_t s) {
+  constexpr size_t smem = 4 * tile_bytes<DP>() + sizeof(float) * kT * kPS;
+  const cudaError_t e = go(attn_dkdv_simt_kernel<IT, DP>, attn_tile_count(d, true, kT) * d.Hk, smem, d, tk, a, s, "attn_dkdv");
+  if (e != cudaSuccess) return e;
+  return go(attn_dq_simt_kernel<IT, DP>, attn_tile_count(d, false, kT) * d.Hq, smem, d, tq, a, s, "attn_dq");
+}
+
+}  // namespace
+
+cudaError_t launch_attn_fwd_simt(const AttnDims& d, const AttnTiles& t, bool bf16, const AttnFwdArgs& a, cudaStream_t s) {
+  if (bf16) return d.D > 64 ? fwd<__nv_bfloat16, 128>(d, t, a, s) : fwd<__nv_bfloat16, 64>(d, t, a, s);
+  return d.D > 64 ? fwd<float, 128>(d, t, a, s) : fwd<float, 64>(d, t, a, s);
+}
+
+cudaError_t launch_attn_bwd_simt(const AttnDims& d, const AttnTiles& tq, const AttnTiles& tk, bool bf16, const AttnBwdArgs& a,
+                                 cudaStream_t s) {
+  if (bf16) return d.D > 64 ? bwd<__nv_bfloat16, 128>(d, tq, tk, a, s) : bwd<__nv_bfloat16, 64>(d, tq, tk, a, s);
+  return d.D > 64 ? bwd<float, 128>(d, tq, tk, a, s) : bwd<float, 64>(d, tq, tk, a, s);
+}
+
+}  // namespace gdr

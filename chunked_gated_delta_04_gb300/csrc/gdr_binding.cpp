@@ -1,4 +1,4 @@
-// gdr_binding.cpp -- the torch side of the operators of include/gdr_block.h: checks of shapes, types
+// gdr_binding.cpp -- the torch side of the operators of include/gdr_block.h and gdr_attn.h: checks of shapes, types
 // and strides, allocation of outputs and workspace, and the call on the current stream.
 //
 // A decoding step's kernel runs 2 to 10 us; marshalled in Python a call took 11 to 15 us of host time
@@ -18,6 +18,7 @@
 #include <climits>
 #include <initializer_list>
 
+#include "../../include/gdr_attn.h"
 #include "../../include/gdr_block.h"
 
 namespace {
@@ -28,7 +29,9 @@ using at::Tensor;
 #define GDR_ENTRIES(X)                                                                                              \
   X(gdr_conv_fwd) X(gdr_conv_bwd) X(gdr_conv_step) X(gdr_conv_fwd_workspace_bytes) X(gdr_conv_bwd_workspace_bytes) \
   X(gdr_ssm_fwd) X(gdr_ssm_bwd) X(gdr_ssm_step) X(gdr_ssm_saved_bytes) X(gdr_ssm_fwd_workspace_bytes)              \
-  X(gdr_ssm_bwd_workspace_bytes) X(gdr_norm_fwd) X(gdr_norm_bwd) X(gdr_norm_bwd_workspace_bytes) X(gdr_step)
+  X(gdr_ssm_bwd_workspace_bytes) X(gdr_norm_fwd) X(gdr_norm_bwd) X(gdr_norm_bwd_workspace_bytes) X(gdr_step) X(gdr_rope) X(gdr_rope_workspace_bytes)              \
+  X(gdr_attn_fwd) X(gdr_attn_bwd) X(gdr_attn_fwd_workspace_bytes) X(gdr_attn_bwd_workspace_bytes) X(gdr_attn_step)        \
+  X(gdr_attn_step_workspace_bytes) X(gdr_cache_write) X(gdr_cache_write_workspace_bytes)
 
 struct Library {
 #define GDR_FIELD(name) decltype(&::name) name;
@@ -127,13 +130,13 @@ long long strided(const char* name, const Tensor& t, int inner) {
   return ld;
 }
 
-int sequences(const Tensor& cu, int64_t B, at::Device dev) {
+int sequences(const Tensor& cu, int64_t B, at::Device dev, const char* name = "cu_seqlens") {
   if (!cu.defined()) return size32("x", B);
   TORCH_CHECK_VALUE(cu.is_cuda() && cu.scalar_type() == at::kInt && cu.dim() == 1 && cu.numel() >= 2 && cu.is_contiguous(),
-                    "cu_seqlens: expected a contiguous CUDA int32 vector of at least 2 entries");
-  on_device("cu_seqlens", cu, dev);
-  TORCH_CHECK_VALUE(B == 1, "cu_seqlens needs a batch of 1 (the packed tokens)");
-  return size32("cu_seqlens", cu.numel()) - 1;
+                    name, ": expected a contiguous CUDA int32 vector of at least 2 entries");
+  on_device(name, cu, dev);
+  TORCH_CHECK_VALUE(B == 1, name, " needs a batch of 1 (the packed tokens)");
+  return size32(name, cu.numel()) - 1;
 }
 
 void check_slots(const Tensor& slots, const Tensor& state, int64_t B, at::Device dev) {
@@ -536,6 +539,215 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ----------------------------------------------------------------------------- rotary positions
+// q, k (or None), freqs, positions, cu_seqlens, interleaved, inverse, scale, workspace
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 9);
+  const Tensor &q = required(a[0], "q"), &k = tensor(a[1], "k"), &freqs = required(a[2], "freqs"), &positions = tensor(a[3], "positions"),
+               &cu = tensor(a[4], "cu_seqlens"), &given = tensor(a[8], "workspace");
+  TORCH_CHECK_VALUE(q.dim() == 4 || q.dim() == 3, "q: expected [B, T, H, D] or [B, H, D], got ", q.sizes());
+  const bool rows = q.dim() == 3;
+  TORCH_CHECK_VALUE(!rows || positions.defined(), "positions: single tokens [B, H, D] need them");
+  const int64_t B = q.size(0), T = rows ? 1 : q.size(1), D = q.size(-1);
+  const auto type = q.scalar_type();
+  const at::Device dev = q.device();
+  gdr_rope_problem p = {};
+  p.dtype = type_code(type);
+  p.B = size32("q", B);
+  p.T = size32("q", T);
+  p.Hq = size32("q", q.size(-2));
+  p.D = size32("q", D);
+  act("q", q, q.sizes(), type, dev);
+  p.ld_q = strided("q", q, 2);
+  if (k.defined()) {
+    TORCH_CHECK_VALUE(k.dim() == q.dim(), "k: expected ", q.dim(), " dimensions, got ", k.sizes());
+    p.Hk = size32("k", k.size(-2));
+    if (rows)
+      act("k", k, {B, k.size(-2), D}, type, dev);
+    else
+      act("k", k, {B, T, k.size(-2), D}, type, dev);
+    p.ld_k = strided("k", k, 2);
+  }
+  TORCH_CHECK_VALUE(freqs.dim() == 1, "freqs: expected a vector, got ", freqs.sizes());
+  full("freqs", freqs, freqs.sizes(), dev, at::kDouble);
+  p.R = size32("freqs", 2 * freqs.size(0));
+  if (rows)
+    full("positions", positions, {B}, dev, at::kInt);
+  else
+    full("positions", positions, {B, T}, dev, at::kInt);
+  p.num_seqs = sequences(cu, B, dev);
+  p.cu_seqlens = positions.defined() ? nullptr : (const int32_t*)ptr(cu);
+  if (positions.defined()) p.num_seqs = p.B;
+  p.interleaved = (int)integer(a[5]);
+  p.inverse = (int)integer(a[6]);
+  p.scale = (float)number(a[7]);
+  const OnDevice current(dev);
+  const Tensor q_out = fresh(q.sizes(), q), k_out = k.defined() ? fresh(k.sizes(), k) : Tensor();
+  const Workspace ws(given, p.cu_seqlens ? lib.gdr_rope_workspace_bytes(&p) : 0, q);
+  return answer(lib.gdr_rope(&p, ptr(q), ptr(k), (const double*)ptr(freqs), (const int32_t*)ptr(positions), ptr(q_out), ptr(k_out),
+                             ptr(ws.t), ws.bytes, stream_of(q)),
+                {q_out, k_out});
+  END_HANDLE_TH_ERRORS
+}
+
+// ------------------------------------------------------------------------------------ attention
+gdr_attn_problem attn_problem(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& cu, const Tensor& cu_k, long causal,
+                              long window, double scale, const Tensor& dout) {
+  TORCH_CHECK_VALUE(q.dim() == 4 && k.dim() == 4, "expected q [B, Tq, Hq, D] and k, v [B, Tk, Hk, D], got ", q.sizes(), " and ", k.sizes());
+  const int64_t B = q.size(0), D = q.size(3);
+  const auto type = q.scalar_type();
+  const at::Device dev = q.device();
+  gdr_attn_problem p = {};
+  p.dtype = type_code(type);
+  p.B = size32("q", B);
+  p.Tq = size32("q", q.size(1));
+  p.Tk = size32("k", k.size(1));
+  p.Hq = size32("q", q.size(2));
+  p.Hk = size32("k", k.size(2));
+  p.D = size32("q", D);
+  act("q", q, q.sizes(), type, dev);
+  act("k", k, {B, k.size(1), k.size(2), D}, type, dev);
+  act("v", v, k.sizes(), type, dev);
+  p.ld_q = strided("q", q, 2);
+  p.ld_k = strided("k", k, 2);
+  p.ld_v = strided("v", v, 2);
+  if (dout.defined()) {
+    act("do", dout, q.sizes(), type, dev);
+    p.ld_do = strided("do", dout, 2);
+  }
+  p.num_seqs = sequences(cu, B, dev);
+  TORCH_CHECK_VALUE(cu.defined() || !cu_k.defined(), "cu_seqlens_k needs cu_seqlens");
+  const Tensor& keys = cu_k.defined() ? cu_k : cu;
+  if (cu_k.defined())
+    TORCH_CHECK_VALUE(sequences(cu_k, B, dev, "cu_seqlens_k") == p.num_seqs, "cu_seqlens_k: expected ", p.num_seqs + 1, " entries, got ", cu_k.numel());
+  p.cu_q = (const int32_t*)ptr(cu);
+  p.cu_k = (const int32_t*)ptr(keys);
+  p.causal = (int)causal;
+  TORCH_CHECK_VALUE(window >= 0, "window: ", window, " is negative");
+  p.window = window > INT_MAX ? 0 : (int)window;  // wider than any sequence: none
+  p.scale = (float)scale;
+  return p;
+}
+
+// q, k, v, cu_seqlens, cu_seqlens_k, causal, window, scale, workspace
+PyObject* attn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 9);
+  const Tensor &q = required(a[0], "q"), &k = required(a[1], "k"), &v = required(a[2], "v"), &cu = tensor(a[3], "cu_seqlens"),
+               &cu_k = tensor(a[4], "cu_seqlens_k"), &given = tensor(a[8], "workspace");
+  const gdr_attn_problem p = attn_problem(q, k, v, cu, cu_k, integer(a[5]), integer(a[6]), number(a[7]), kNone);
+  const OnDevice current(q.device());
+  const Tensor o = fresh(q.sizes(), q), lse = fresh_f32({p.B, p.Hq, p.Tq}, q);
+  const Workspace ws(given, lib.gdr_attn_fwd_workspace_bytes(&p), q);
+  return answer(lib.gdr_attn_fwd(&p, ptr(q), ptr(k), ptr(v), ptr(o), (float*)ptr(lse), ptr(ws.t), ws.bytes, stream_of(q)), {o, lse});
+  END_HANDLE_TH_ERRORS
+}
+
+// q, k, v, o, lse, do, cu_seqlens, cu_seqlens_k, causal, window, scale, workspace
+PyObject* attn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 12);
+  const Tensor &q = required(a[0], "q"), &k = required(a[1], "k"), &v = required(a[2], "v"), &o = required(a[3], "o"),
+               &lse = required(a[4], "lse"), &dout = required(a[5], "do"), &cu = tensor(a[6], "cu_seqlens"),
+               &cu_k = tensor(a[7], "cu_seqlens_k"), &given = tensor(a[11], "workspace");
+  const gdr_attn_problem p = attn_problem(q, k, v, cu, cu_k, integer(a[8]), integer(a[9]), number(a[10]), dout);
+  full("o", o, q.sizes(), q.device(), q.scalar_type());
+  full("lse", lse, {p.B, p.Hq, p.Tq}, q.device());
+  const OnDevice current(q.device());
+  const Tensor dq = fresh(q.sizes(), q), dk = fresh(k.sizes(), k), dv = fresh(v.sizes(), v);
+  const Workspace ws(given, lib.gdr_attn_bwd_workspace_bytes(&p), q);
+  return answer(lib.gdr_attn_bwd(&p, ptr(q), ptr(k), ptr(v), ptr(o), (const float*)ptr(lse), ptr(dout), ptr(dq), ptr(dk), ptr(dv),
+                                 ptr(ws.t), ws.bytes, stream_of(q)),
+                {dq, dk, dv});
+  END_HANDLE_TH_ERRORS
+}
+
+// The caches and the block table of B rows of heads [Hk, D].
+void cache_pages(gdr_cache_problem* p, const Tensor& k_cache, const Tensor& v_cache, const Tensor& table, int64_t B, int64_t Hk, int64_t D,
+                 at::ScalarType type, at::Device dev) {
+  TORCH_CHECK_VALUE(k_cache.dim() == 4 && table.dim() == 2, "expected k_cache [num_pages, page_size, Hk, D] and block_table [B, max_pages], got ",
+                    k_cache.sizes(), " and ", table.sizes());
+  full("k_cache", k_cache, {k_cache.size(0), k_cache.size(1), Hk, D}, dev, type);
+  full("v_cache", v_cache, k_cache.sizes(), dev, type);
+  full("block_table", table, {B, table.size(1)}, dev, at::kInt);
+  p->num_pages = size32("k_cache", k_cache.size(0));
+  p->page_size = size32("k_cache", k_cache.size(1));
+  p->max_pages = size32("block_table", table.size(1));
+}
+gdr_status both_changed(const Tensor& k_cache, const Tensor& v_cache, gdr_status st) { return changed(v_cache, changed(k_cache, st)); }
+
+// q, k, v, k_cache, v_cache, block_table, lengths, window, scale
+PyObject* attn_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 9);
+  const Tensor &q = required(a[0], "q"), &k = required(a[1], "k"), &v = required(a[2], "v"), &kc = required(a[3], "k_cache"),
+               &vc = required(a[4], "v_cache"), &table = required(a[5], "block_table"), &lengths = required(a[6], "lengths");
+  TORCH_CHECK_VALUE(q.dim() == 3 && k.dim() == 3, "expected q [B, Hq, D] and k, v [B, Hk, D], got ", q.sizes(), " and ", k.sizes());
+  const int64_t B = q.size(0), Hk = k.size(1), D = q.size(2);
+  const auto type = q.scalar_type();
+  const at::Device dev = q.device();
+  gdr_cache_problem p = {};
+  p.dtype = type_code(type);
+  p.B = size32("q", B);
+  p.T = 1;
+  p.Hq = size32("q", q.size(1));
+  p.Hk = size32("k", Hk);
+  p.D = size32("q", D);
+  act("q", q, q.sizes(), type, dev);
+  act("k", k, {B, Hk, D}, type, dev);
+  act("v", v, {B, Hk, D}, type, dev);
+  p.ld_q = strided("q", q, 2);
+  p.ld_k = strided("k", k, 2);
+  p.ld_v = strided("v", v, 2);
+  cache_pages(&p, kc, vc, table, B, Hk, D, type, dev);
+  full("lengths", lengths, {B}, dev, at::kInt);
+  const long window = integer(a[7]);
+  TORCH_CHECK_VALUE(window >= 0, "window: ", window, " is negative");
+  p.window = window > INT_MAX ? 0 : (int)window;
+  p.scale = (float)number(a[8]);
+  const OnDevice current(dev);
+  const Tensor o = fresh(q.sizes(), q);
+  const Workspace ws(lib.gdr_attn_step_workspace_bytes(&p), q);
+  return answer(both_changed(kc, vc, lib.gdr_attn_step(&p, ptr(q), ptr(k), ptr(v), ptr(kc), ptr(vc), (const int32_t*)ptr(table),
+                                                       (const int32_t*)ptr(lengths), ptr(o), ptr(ws.t), ws.bytes, stream_of(q))),
+                o);
+  END_HANDLE_TH_ERRORS
+}
+
+// k, v, k_cache, v_cache, block_table, starts, cu_seqlens, workspace
+PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 8);
+  const Tensor &k = required(a[0], "k"), &v = required(a[1], "v"), &kc = required(a[2], "k_cache"), &vc = required(a[3], "v_cache"),
+               &table = required(a[4], "block_table"), &starts = tensor(a[5], "starts"), &cu = tensor(a[6], "cu_seqlens"),
+               &given = tensor(a[7], "workspace");
+  TORCH_CHECK_VALUE(k.dim() == 4, "k: expected [B, T, Hk, D], got ", k.sizes());
+  const int64_t Hk = k.size(2), D = k.size(3);
+  const auto type = k.scalar_type();
+  const at::Device dev = k.device();
+  gdr_cache_problem p = {};
+  p.dtype = type_code(type);
+  p.T = size32("k", k.size(1));
+  p.Hk = size32("k", Hk);
+  p.D = size32("k", D);
+  act("k", k, k.sizes(), type, dev);
+  act("v", v, k.sizes(), type, dev);
+  p.ld_k = strided("k", k, 2);
+  p.ld_v = strided("v", v, 2);
+  p.B = sequences(cu, k.size(0), dev);
+  p.cu_seqlens = (const int32_t*)ptr(cu);
+  cache_pages(&p, kc, vc, table, p.B, Hk, D, type, dev);
+  full("starts", starts, {p.B}, dev, at::kInt);
+  const OnDevice current(dev);
+  const Workspace ws(given, lib.gdr_cache_write_workspace_bytes(&p), k);
+  const gdr_status st = both_changed(kc, vc, lib.gdr_cache_write(&p, ptr(k), ptr(v), ptr(kc), ptr(vc), (const int32_t*)ptr(table),
+                                                                 (const int32_t*)ptr(starts), ptr(ws.t), ws.bytes, stream_of(k)));
+  if (st != GDR_OK) return PyLong_FromLong(st);
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 // tensor, inner dimensions: token_stride
 PyObject* stride(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -566,7 +778,8 @@ PyObject* bind(PyObject*, PyObject* table) {
 #define GDR_METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {GDR_METHOD(conv_forward), GDR_METHOD(conv_backward), GDR_METHOD(conv_step), GDR_METHOD(ssm_forward),
                          GDR_METHOD(ssm_backward), GDR_METHOD(ssm_step), GDR_METHOD(norm_forward), GDR_METHOD(norm_backward),
-                         GDR_METHOD(step), GDR_METHOD(stride), {"bind", bind, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
+                         GDR_METHOD(step), GDR_METHOD(rope), GDR_METHOD(attn_forward), GDR_METHOD(attn_backward), GDR_METHOD(attn_step),
+                         GDR_METHOD(cache_write), GDR_METHOD(stride), {"bind", bind, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef definition = {PyModuleDef_HEAD_INIT, "gdr_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
