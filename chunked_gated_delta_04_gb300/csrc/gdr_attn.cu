@@ -204,7 +204,8 @@ gdr_status gdr_attn_fwd(const gdr_attn_problem* p, const void* q, const void* k,
   uint32_t* status = (uint32_t*)at;
   int2* table = (int2*)(at + 256);
   const bool bf16 = p->dtype == GDR_DTYPE_BF16;
-  const int size = kSimtTile;
+  const bool tc = bf16 && queries && keys && tma_rows(q, d.ld_q) && tma_rows(k, d.ld_k) && tma_rows(v, d.ld_v) && vec_ok(o);
+  const int size = tc ? attn_fwd_tc_tile(d) : kSimtTile;
   if (d.cu_q) {
     const TableSpec t{table, attn_tile_count(d, false, size), size, 0};
     const cudaError_t e = launch_tiles(d, t, nullptr, status, s);
@@ -212,7 +213,8 @@ gdr_status gdr_attn_fwd(const gdr_attn_problem* p, const void* q, const void* k,
   }
   if (!queries) return GDR_OK;
   const AttnFwdArgs a{q, k, v, o, lse, status};
-  return status_of(launch_attn_fwd_simt(d, tiles_of(d, table, false, size), bf16, a, s));
+  const AttnTiles t = tiles_of(d, table, false, size);
+  return status_of(tc ? launch_attn_fwd_tc(d, t, size, a, s) : launch_attn_fwd_simt(d, t, bf16, a, s));
 }
 
 gdr_status gdr_attn_bwd(const gdr_attn_problem* p, const void* q, const void* k, const void* v, const void* o,

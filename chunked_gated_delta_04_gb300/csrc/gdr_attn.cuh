@@ -106,4 +106,10 @@ cudaError_t launch_attn_fwd_simt(const AttnDims& d, const AttnTiles& t, bool bf1
 cudaError_t launch_attn_bwd_simt(const AttnDims& d, const AttnTiles& tq, const AttnTiles& tk, bool bf16, const AttnBwdArgs& a,
                                  cudaStream_t s);
 
+// Tensor-core kernels (bf16): q, k, v, dout aligned for TMA, the outputs for 16-byte stores.
+constexpr int kTcBlock = 128;  // rows of an MMA tile: queries, keys
+// Queries of a block's work: two tiles side by side, or one where that leaves SMs without work.
+int attn_fwd_tc_tile(const AttnDims& d);
+cudaError_t launch_attn_fwd_tc(const AttnDims& d, const AttnTiles& t, int tile, const AttnFwdArgs& a, cudaStream_t s);
+
 }  // namespace gdr

@@ -1,0 +1,384 @@
+// gdr_attn_tc.cu -- attention forward on the tensor cores (include/gdr_attn.h), bf16, D up to 128.
+//
+//   S = Q K^T,   P = e^{scale S - scale m},   O += P V,   o = O / l,   lse = scale m + log l
+//
+// per query with m the running maximum of its scores and l the running sum of e^..  A block takes NT tiles of 128 queries of a
+// head (two, so that the tensor core works on one while the other's scores are exponentiated) through the visible keys, 128 at
+// a time, and goes on to its next item (persistent, one block per SM).  Roles:
+//   warp 4 NT + 1  loads Q, then K and V tiles by TMA into a ring of slots
+//   warp 4 NT      issues the MMAs: S_t = Q_t K_j^T (both operands in shared memory), O_t += P_t V_j (P_t from TMEM)
+//   warps 4 t ..   the softmax of tile t, a thread per query: S from TMEM to registers, P as bf16 to TMEM over S
+// In TMEM: S_t (128 columns, P_t in its first 64) and O_t (DP columns).  Issue order per key block: O_0, next S_0, O_1, next S_1, so that
+// each tile's softmax runs beside the other tile's two products; MMAs of a block are executed in order, which makes
+// S's place free for the next scores once P V is issued.
+// The maximum that P is formed against (m) follows the true one only when that has grown by more than 2^8: then O and
+// l are rescaled; else P is up to 2^8, which bf16 holds as exactly as 1.
+#include <algorithm>
+
+#include "gdr_attn_tc.cuh"
+
+namespace gdr {
+namespace {
+
+using namespace tcx;
+
+template <int DP, int NT>
+struct FwdShape {
+  static constexpr int kThreads = NT * 128 + (NT == 2 ? 128 : 64);  // registers move between whole warpgroups
+  static constexpr uint32_t kTile = attn_tile_bytes<DP>();
+  static constexpr int kSlots = DP == 128 ? 4 : 6;  // of the ring of K and V tiles
+  static constexpr size_t kSmem = 1024 + (size_t)(NT + kSlots) * kTile;
+  static constexpr uint32_t kTmem = NT == 2 ? 512 : 256;
+  static constexpr uint32_t kO = NT * 128;  // first column of O_0
+};
+
+struct FwdMaps {
+  CUtensorMap q, k, v;
+};
+
+// An item: a head's queries i0 .. of a sequence, and the key blocks [lo, hi) of each tile (none: both 0) and of all.
+template <int NT>
+struct FwdItem {
+  AttnSpan s;
+  int h, i0, lo[NT], hi[NT], first, last;
+};
+
+template <int NT>
+__device__ __forceinline__ bool fwd_item(const AttnDims& d, const AttnTiles& t, unsigned x, FwdItem<NT>* w) {
+  int seq, tile;
+  if (!attn_tile(d, t, d.Hq, x, &seq, &w->h, &tile)) return false;
+  w->s = attn_span(d, seq);
+  w->i0 = tile * NT * kTcBlock;
+  w->first = 1 << 30;
+  w->last = 0;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int a = w->i0 + i * kTcBlock;
+    int lo = 0, hi = 0;
+    if (a < w->s.n) attn_keys(d, w->s, a, min(w->s.n, a + kTcBlock), &lo, &hi);
+    const bool any = lo < hi;
+    w->lo[i] = any ? lo / kTcBlock : 0;
+    w->hi[i] = any ? (hi + kTcBlock - 1) / kTcBlock : 0;
+    if (any) {
+      w->first = min(w->first, w->lo[i]);
+      w->last = max(w->last, w->hi[i]);
+    }
+  }
+  return true;
+}
+
+template <int DP, int NT>
+__global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
+    attn_fwd_tc_kernel(const __grid_constant__ FwdMaps maps, AttnDims d, AttnTiles tiles, unsigned items, AttnFwdArgs a) {
+  using Shape = FwdShape<DP, NT>;
+  constexpr int ST = Shape::kSlots;
+  extern __shared__ unsigned char raw[];
+  __shared__ uint64_t q_full[NT], q_empty[NT], kv_full[ST], kv_empty[ST], s_full[NT], p_ready[NT], o_done[NT], tail_full, drain;
+  __shared__ uint32_t tmem_slot;
+  unsigned char* const sq = align1024(raw);
+  unsigned char* const skv = sq + NT * Shape::kTile;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* const status = a.status;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *status = 0;  // of a packed batch: the tile table's kernel
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NT; ++i) {
+      tc::mbar_init(&q_full[i], 1);
+      tc::mbar_init(&q_empty[i], 1);
+      tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&p_ready[i], 4);
+      tc::mbar_init(&o_done[i], 1);
+    }
+    for (int i = 0; i < ST; ++i) {
+      tc::mbar_init(&kv_full[i], 1);
+      tc::mbar_init(&kv_empty[i], 1);
+    }
+    tc::mbar_init(&tail_full, 1);
+    tc::mbar_init(&drain, 1);
+    tc::fence_barrier_init();
+  }
+  if (warp == 4 * NT) tc::tmem_alloc<Shape::kTmem>(&tmem_slot);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  // Registers: three warpgroups are launched with 168 a thread; 2 x 216 + 72 is the same sum.
+  // (Each count stands in its role's own branch: the compiler allots the code behind it by it.)
+  if (warp >= 4 * NT) {
+    if constexpr (NT == 2) regs_less<72>();
+    if (warp == 4 * NT + 1) {
+    // ------------------------------------------------------------------------------- loads
+    AttnRing<ST> ring;
+    uint32_t q_parity = 0, tail_parity = 0;
+    bool ok = true;
+    auto load_kv = [&](const CUtensorMap* map, const FwdItem<NT>& w, int j, bool value) {
+      ok = ok && attn_warp_wait(&kv_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutFwd);
+      if (!ok) return;
+      unsigned char* const dst = skv + ring.slot * Shape::kTile;
+      const int rows = w.s.m - j * kTcBlock;  // of the sequence in this tile
+      // The values behind a sequence's end: a warp clears them before the tile counts as loaded.
+      uint64_t* const bar = value && rows < kTcBlock ? &tail_full : &kv_full[ring.slot];
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(bar, Shape::kTile);
+        attn_load_tile<DP>(dst, map, bar, w.h / d.G, w.s.k0 + (long long)j * kTcBlock);
+      }
+      if (bar == &tail_full) {
+        ok = attn_warp_wait(&tail_full, tail_parity, status, kDevErrTimeoutFwd);
+        tail_parity ^= 1u;
+        if (!ok) return;
+        attn_clear_rows<DP>(dst, rows);
+        if (lane == 0) tc::mbar_arrive(&kv_full[ring.slot]);
+      }
+      ring.next();
+    };
+    FwdItem<NT> w;
+    for (unsigned turn = 0; ok; ++turn) {
+      const long long x = attn_item(turn, items);
+      if (x < 0) break;
+      if (!fwd_item<NT>(d, tiles, (unsigned)x, &w)) continue;
+      for (int j = w.first; j < w.last && ok; ++j) {
+        if (j == w.first) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            if (i == 1) load_kv(&maps.k, w, j, false);
+            if (w.hi[i] == 0) continue;
+            ok = ok && attn_warp_wait(&q_empty[i], (q_parity >> i & 1u) ^ 1u, status, kDevErrTimeoutFwd);
+            if (ok && lane == 0) {
+              tc::mbar_arrive_expect_tx(&q_full[i], Shape::kTile);
+              attn_load_tile<DP>(sq + i * Shape::kTile, &maps.q, &q_full[i], w.h, w.s.q0 + w.i0 + i * kTcBlock);
+            }
+            q_parity ^= 1u << i;
+          }
+          if (NT == 1) load_kv(&maps.k, w, j, false);
+        } else {
+          load_kv(&maps.k, w, j, false);
+        }
+        load_kv(&maps.v, w, j, true);
+      }
+    }
+    // after a wait that ran out, the copies under way end before the block does
+    if (!ok)
+      for (int i = 0; i < ST; ++i) {
+        tc::mbar_wait(&kv_full[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutFwd);
+        ring.next();
+      }
+    } else if (warp == 4 * NT) {
+    // -------------------------------------------------------------------------------- MMAs
+    if (lane == 0) {
+      AttnRing<ST> ring;
+      uint32_t q_parity = 0, p_parity = 0;
+      const uint32_t q_at = tc::smem_u32(sq), kv_at = tc::smem_u32(skv);
+      bool ok = true;
+      FwdItem<NT> w;
+      for (unsigned turn = 0; ok; ++turn) {
+        const long long x = attn_item(turn, items);
+        if (x < 0) break;
+        if (!fwd_item<NT>(d, tiles, (unsigned)x, &w)) continue;
+        auto scores = [&](int i, int slot, int j) {  // S_i of key block j
+          attn_scores<DP>(tmem + i * 128, q_at + i * Shape::kTile, kv_at + slot * Shape::kTile);
+          tc::mma_commit(&s_full[i]);
+          if (j + 1 == w.hi[i]) tc::mma_commit(&q_empty[i]);
+        };
+        if (w.first < w.last) {
+          ok = tc::mbar_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            if (w.hi[i] == 0) continue;
+            ok = ok && tc::mbar_wait(&q_full[i], q_parity >> i & 1u, status, kDevErrTimeoutFwd);
+            q_parity ^= 1u << i;
+            tc::tc_fence_after();
+            if (ok && w.lo[i] == w.first) scores(i, ring.slot, w.first);
+          }
+          tc::mma_commit(&kv_empty[ring.slot]);
+          ring.next();
+        }
+        for (int j = w.first; j < w.last && ok; ++j) {
+          const int v_slot = ring.slot;
+          ok = tc::mbar_wait(&kv_full[v_slot], ring.parity, status, kDevErrTimeoutFwd);
+          ring.next();
+          bool k_here = false;
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            if (!ok) break;
+            if (j >= w.lo[i] && j < w.hi[i]) {
+              ok = tc::mbar_wait(&p_ready[i], p_parity >> i & 1u, status, kDevErrTimeoutFwd);
+              p_parity ^= 1u << i;
+              if (!ok) break;
+              tc::tc_fence_after();
+              attn_product<DP>(tmem + Shape::kO + i * DP, tmem + i * 128, kv_at + v_slot * Shape::kTile, j > w.lo[i]);
+              tc::mma_commit(&o_done[i]);
+            }
+            if (j + 1 >= w.lo[i] && j + 1 < w.hi[i]) {
+              if (!k_here) {
+                ok = tc::mbar_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
+                if (!ok) break;
+                k_here = true;
+              }
+              tc::tc_fence_after();
+              scores(i, ring.slot, j + 1);
+            }
+          }
+          if (!ok) break;
+          tc::mma_commit(&kv_empty[v_slot]);
+          if (j + 1 < w.last) {
+            tc::mma_commit(&kv_empty[ring.slot]);
+            ring.next();
+          }
+        }
+      }
+      if (!ok) {  // the products under way end before their memory is given back
+        tc::mma_commit(&drain);
+        tc::mbar_wait(&drain, 0, status, kDevErrTimeoutFwd);
+      }
+    }
+    __syncwarp();
+    }
+  } else {
+    if constexpr (NT == 2) regs_more<216>();
+    // ----------------------------------------------------------------------------- softmax
+    const int t = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t s_col = tc::tmem_lane_addr(tmem, warp, t * 128), o_col = tc::tmem_lane_addr(tmem, warp, Shape::kO + t * DP);
+    const float c = d.scale * kLog2e;
+    uint32_t parity = 0;  // of s_full; of o_done it is that of the block before
+    FwdItem<NT> w;
+    bool ok = true;
+    for (unsigned turn = 0; ok; ++turn) {
+      const long long x = attn_item(turn, items);
+      if (x < 0) break;
+      if (!fwd_item<NT>(d, tiles, (unsigned)x, &w)) continue;
+      const int i = w.i0 + t * kTcBlock + row, off = w.s.m - w.s.n;
+      int lo = w.lo[0], hi = w.hi[0];
+      if (NT == 2 && t == 1) lo = w.lo[NT - 1], hi = w.hi[NT - 1];
+      // the keys [from, to) that this query sees
+      const int from = d.window ? max(0, i + off - d.window + 1) : 0, to = d.causal ? min(w.s.m, i + off + 1) : w.s.m;
+      // blocks [clear, full) are seen whole by all of the tile's queries
+      const int i_first = w.i0 + t * kTcBlock, i_last = i_first + kTcBlock - 1;
+      const int whole_to = (d.causal ? min(w.s.m, i_first + off + 1) : w.s.m), whole_from = d.window ? i_last + off - d.window + 1 : 0;
+      float m = -INFINITY, l = 0.f;
+      for (int j = lo; j < hi; ++j) {
+        ok = attn_warp_wait(&s_full[t], parity, status, kDevErrTimeoutFwd);
+        if (!ok) break;
+        tc::tc_fence_after();
+        float s[128];
+#pragma unroll
+        for (int e = 0; e < 128; e += 32) tc::tmem_ld32(s_col + e, s + e);
+        tc::tmem_wait_ld();
+        const int j0 = j * kTcBlock;
+        if (j0 + kTcBlock > whole_to || j0 < whole_from) {
+          const int a0 = from - j0, a1 = to - j0;
+#pragma unroll
+          for (int e = 0; e < 128; ++e) s[e] = e >= a0 && e < a1 ? s[e] : -INFINITY;
+        }
+        float top = m;
+#pragma unroll
+        for (int e = 0; e < 128; e += 2) top = fmaxf(top, fmaxf(s[e], s[e + 1]));
+        if (j == lo) {
+          m = top;
+        } else {
+          const bool grown = (top - m) * c > 8.f;
+          if (__any_sync(0xffffffffu, grown)) {
+            const float f = grown ? ex2f((m - top) * c) : 1.f;  // of nothing seen before: 0
+            if (grown) m = top;
+            l *= f;
+            ok = attn_warp_wait(&o_done[t], parity ^ 1u, status, kDevErrTimeoutFwd);
+            if (!ok) break;
+            tc::tc_fence_after();
+#pragma unroll
+            for (int e = 0; e < DP; e += 16) {
+              float o[16];
+              uint32_t r[16];
+              tc::tmem_ld16(o_col + e, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 16; ++y) r[y] = __float_as_uint(o[y] * f);
+              tc::tmem_st16(o_col + e, r);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : m * c;
+        float sum[4] = {};
+#pragma unroll
+        for (int e = 0; e < 128; e += 64) {
+          uint32_t r[32];
+#pragma unroll
+          for (int y = 0; y < 32; ++y) {
+            const float p0 = ex2f(fmaf(s[e + 2 * y], c, -base)), p1 = ex2f(fmaf(s[e + 2 * y + 1], c, -base));
+            sum[(2 * y) & 3] += p0;
+            sum[(2 * y + 1) & 3] += p1;
+            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+            r[y] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          tc::tmem_st32(s_col + e / 2, r);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        GDR_DELAY(40);
+        if (lane == 0) tc::mbar_arrive(&p_ready[t]);
+        parity ^= 1u;
+      }
+      if (!ok) break;
+      const bool mine = i < w.s.n;
+      __nv_bfloat16* const out = (__nv_bfloat16*)a.o + ((w.s.q0 + i) * d.Hq + w.h) * (long long)d.D;
+      if (lo < hi) {
+        ok = attn_warp_wait(&o_done[t], parity ^ 1u, status, kDevErrTimeoutFwd);
+        if (!ok) break;
+        tc::tc_fence_after();
+      }
+      const float f = m == -INFINITY ? 0.f : 1.f / l;
+#pragma unroll
+      for (int e = 0; e < DP; e += 32) {
+        float o[32];
+        if (lo < hi) {
+          tc::tmem_ld32(o_col + e, o);
+          tc::tmem_wait_ld();
+        }
+        if (mine) {
+#pragma unroll
+          for (int y = 0; y < 32; y += 8) {
+            float v[8];
+#pragma unroll
+            for (int z = 0; z < 8; ++z) v[z] = m == -INFINITY ? 0.f : o[y + z] * f;
+            if (e + y < d.D) store_v<8>(out + e + y, v);
+          }
+        }
+      }
+      if (mine) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = m == -INFINITY ? -INFINITY : fmaf(m, d.scale, logf(l));
+      tc::tc_fence_before();  // O is read before this item's successor's first product into it, which the next arrival allows
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 4 * NT) tc::tmem_dealloc(tmem, Shape::kTmem);
+}
+
+template <int DP, int NT>
+cudaError_t fwd(const AttnDims& d, const AttnTiles& t, const AttnFwdArgs& a, cudaStream_t s) {
+  using Shape = FwdShape<DP, NT>;
+  FwdMaps maps;
+  const long long rows_q = (long long)d.B * d.Tq, rows_k = (long long)d.B * d.Tk;
+  if (!attn_map(&maps.q, a.q, d.D, d.Hq, rows_q, d.ld_q) || !attn_map(&maps.k, a.k, d.D, d.Hk, rows_k, d.ld_k) ||
+      !attn_map(&maps.v, a.v, d.D, d.Hk, rows_k, d.ld_v))
+    return cudaErrorInvalidValue;
+  const auto kernel = attn_fwd_tc_kernel<DP, NT>;
+  cudaError_t e = set_smem_once((const void*)kernel, Shape::kSmem);
+  if (e != cudaSuccess) return e;
+  const long long items = attn_tile_count(d, false, NT * kTcBlock) * d.Hq;
+  kernel<<<(unsigned)std::min<long long>(items, kSmCount), Shape::kThreads, Shape::kSmem, s>>>(maps, d, t, (unsigned)items, a);
+  stage_mark(s, "attn_fwd");
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int attn_fwd_tc_tile(const AttnDims& d) {
+  return attn_tile_count(d, false, 2 * kTcBlock) * d.Hq >= kSmCount ? 2 * kTcBlock : kTcBlock;
+}
+
+cudaError_t launch_attn_fwd_tc(const AttnDims& d, const AttnTiles& t, int tile, const AttnFwdArgs& a, cudaStream_t s) {
+  if (tile == 2 * kTcBlock) return d.D > 64 ? fwd<128, 2>(d, t, a, s) : fwd<64, 2>(d, t, a, s);
+  return d.D > 64 ? fwd<128, 1>(d, t, a, s) : fwd<64, 1>(d, t, a, s);
+}
+
+}  // namespace gdr

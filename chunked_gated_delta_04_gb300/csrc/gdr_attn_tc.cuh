@@ -1,0 +1,104 @@
+// gdr_attn_tc.cuh -- what the tensor-core kernels of attention share: tensor maps, rings of tiles in shared memory, the
+// tiles that end inside a sequence's last block.
+#pragma once
+
+#include "gdr_attn.cuh"
+#include "tc_common.cuh"
+
+namespace gdr {
+
+// Rows [r0, r0 + 128) of one head of a [tokens, H, D] tensor as DP / 64 slabs of 64 features (128-byte rows, swizzled); features
+// from D on and rows behind the last token arrive as zeros.
+template <int DP>
+constexpr uint32_t attn_tile_bytes() { return (uint32_t)(DP / 64) * kTcBlock * 128; }
+
+template <int DP>
+__device__ __forceinline__ void attn_load_tile(unsigned char* dst, const CUtensorMap* map, uint64_t* bar, int head, long long row) {
+#pragma unroll
+  for (int s = 0; s < DP / 64; ++s) tc::tma_load_3d(dst + s * kTcBlock * 128, map, bar, 64 * s, head, (int)row);
+}
+
+// Rows [from, 128) of a tile become zeros (a warp): they belong to another sequence, and what is in them must not reach
+// this one's sums, where it would be multiplied by zero.
+template <int DP>
+__device__ __forceinline__ void attn_clear_rows(unsigned char* tile, int from) {
+  const int lane = threadIdx.x & 31;
+  for (int s = 0; s < DP / 64; ++s)
+    for (int e = from * 8 + lane; e < kTcBlock * 8; e += 32)
+      *reinterpret_cast<uint4*>(tile + s * kTcBlock * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+  tc::fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// A tile of 128 rows in shared memory as an operand: the low word of its matrix descriptor, whose high word is the same for all.
+// K-major (rows are M or N): a K step of 16 features is 32 bytes on, a slab of 64 features the next one.  MN-major (rows are K):
+// a step of 16 rows is 2 KB on.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart, 128-byte swizzle
+constexpr uint32_t kSlabBytes = kTcBlock * 128;
+__device__ __forceinline__ uint32_t desc_kmajor(uint32_t saddr) { return saddr >> 4 | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mnmajor(uint32_t saddr) { return saddr >> 4 | (kSlabBytes >> 4) << 16; }
+__device__ __forceinline__ constexpr uint32_t kmajor_step(int kk) { return (uint32_t)(kk >> 2) * (kSlabBytes >> 4) + (uint32_t)(kk & 3) * 2u; }
+__device__ __forceinline__ constexpr uint32_t mnmajor_step(int kk) { return (uint32_t)kk * 128u; }
+
+// D = A B^T over DP features, A and B K-major tiles.
+template <int DP>
+__device__ __forceinline__ void attn_scores(uint32_t d_tmem, uint32_t a, uint32_t b) {
+  constexpr uint32_t id = tc::idesc_bf16(kTcBlock, kTcBlock, 0, 0);
+  a = desc_kmajor(a);
+  b = desc_kmajor(b);
+#pragma unroll
+  for (int kk = 0; kk < DP / 16; ++kk)
+    tc::mma_bf16(d_tmem, (uint64_t)kDescHi << 32 | (a + kmajor_step(kk)), (uint64_t)kDescHi << 32 | (b + kmajor_step(kk)), id, kk > 0);
+}
+// D (+)= A B: A [128 x 128] in TMEM as bf16 (64 columns), B a tile of 128 rows by DP features.
+template <int DP>
+__device__ __forceinline__ void attn_product(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate) {
+  constexpr uint32_t id = tc::idesc_bf16(kTcBlock, DP, 0, 1);
+  b = desc_mnmajor(b);
+#pragma unroll
+  for (int kk = 0; kk < kTcBlock / 16; ++kk)
+    tc::mma_bf16_ts(d_tmem, a_tmem + 8u * kk, (uint64_t)kDescHi << 32 | (b + mnmajor_step(kk)), id, accumulate || kk > 0);
+}
+
+// mbar_wait by a whole warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool attn_warp_wait(uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t bit) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status, bit));
+}
+
+// Registers per thread from here on, for a warpgroup: what one gives up another may take.
+template <int N>
+__device__ __forceinline__ void regs_less() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A place in a ring of N slots: slot and parity of its use.
+template <int N>
+struct AttnRing {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// Tensor map of a [rows, H, D] bf16 tensor with token stride ld, for attn_load_tile.
+inline bool attn_map(CUtensorMap* m, const void* base, int D, int H, long long rows, long long ld) {
+  return get_encoder() && map_3d_rows(m, base, (uint64_t)D, (uint64_t)H, (uint64_t)rows, (uint64_t)ld, kTcBlock);
+}
+
+// Work item `turn` of a block: items lie by falling work, and the rounds of the grid take them forth and back, so that a block
+// that had the largest of one round gets the smallest of the next.  -1: none is left.
+__device__ __forceinline__ long long attn_item(unsigned turn, unsigned items) {
+  const long long first = (long long)turn * gridDim.x;
+  const long long x = first + (turn & 1u ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  return x < items ? x : -1;
+}
+
+}  // namespace gdr

@@ -71,6 +71,17 @@ bool map_3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t heads, uin
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3D map over a [rows][heads][cols] bf16 tensor whose rows are ld elements apart, box = 64 columns x 1 head x box_rows rows.
+bool map_3d_rows(CUtensorMap* m, const void* base, uint64_t cols, uint64_t heads, uint64_t rows, uint64_t ld, uint32_t box_rows) {
+  cuuint64_t dims[3] = {cols, heads, rows};
+  cuuint64_t strides[2] = {cols * 2, ld * 2};
+  cuuint32_t box[3] = {64, 1, box_rows};
+  cuuint32_t es[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 2D map over a [rows][cols] matrix of `dt` (element size esz) with a box of
 // box_cols x box_rows, 128-byte swizzle (box_cols * esz must be 128).
 bool map_2d_box(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint32_t esz, uint64_t cols,
