@@ -239,7 +239,9 @@ gdr_status gdr_attn_bwd(const gdr_attn_problem* p, const void* q, const void* k,
   int2* table_k = (int2*)(at + 256 + table_bytes(d, false));
   float* delta = (float*)(at + 256 + table_bytes(d, false) + table_bytes(d, true));
   const bool bf16 = p->dtype == GDR_DTYPE_BF16;
-  const int size_q = kSimtTile, size_k = kSimtTile;
+  const bool tc = bf16 && queries && keys && tma_rows(q, d.ld_q) && tma_rows(k, d.ld_k) && tma_rows(v, d.ld_v) && tma_rows(dout, d.ld_do) &&
+                  vec_ok(dq) && vec_ok(dk) && vec_ok(dv);
+  const int size_q = tc ? kTcBlock : kSimtTile, size_k = size_q;
   cudaError_t e = cudaSuccess;
   if (d.cu_q) {
     const TableSpec tq{table_q, attn_tile_count(d, false, size_q), size_q, 0}, tk{table_k, attn_tile_count(d, true, size_k), size_k, 1};
@@ -261,7 +263,8 @@ gdr_status gdr_attn_bwd(const gdr_attn_problem* p, const void* q, const void* k,
     if (e != cudaSuccess) return status_of(e);
   }
   const AttnBwdArgs a{q, k, v, dout, lse, delta, dq, dk, dv, status};
-  return status_of(launch_attn_bwd_simt(d, tiles_of(d, table_q, false, size_q), tiles_of(d, table_k, true, size_k), bf16, a, s));
+  const AttnTiles tq = tiles_of(d, table_q, false, size_q), tk = tiles_of(d, table_k, true, size_k);
+  return status_of(tc ? launch_attn_bwd_tc(d, tq, tk, a, s) : launch_attn_bwd_simt(d, tq, tk, bf16, a, s));
 }
 
 }  // extern "C"

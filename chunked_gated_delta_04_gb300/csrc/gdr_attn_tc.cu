@@ -326,24 +326,8 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
         if (!ok) break;
         tc::tc_fence_after();
       }
-      const float f = m == -INFINITY ? 0.f : 1.f / l;
-#pragma unroll
-      for (int e = 0; e < DP; e += 32) {
-        float o[32];
-        if (lo < hi) {
-          tc::tmem_ld32(o_col + e, o);
-          tc::tmem_wait_ld();
-        }
-        if (mine) {
-#pragma unroll
-          for (int y = 0; y < 32; y += 8) {
-            float v[8];
-#pragma unroll
-            for (int z = 0; z < 8; ++z) v[z] = m == -INFINITY ? 0.f : o[y + z] * f;
-            if (e + y < d.D) store_v<8>(out + e + y, v);
-          }
-        }
-      }
+      // a query that has seen nothing has l = 0 and O = 0 or, where a product has not begun, none
+      attn_store_row<DP>(o_col, out, d.D, m == -INFINITY ? 0.f : 1.f / l, lo < hi, mine);
       if (mine) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = m == -INFINITY ? -INFINITY : fmaf(m, d.scale, logf(l));
       tc::tc_fence_before();  // O is read before this item's successor's first product into it, which the next arrival allows
     }

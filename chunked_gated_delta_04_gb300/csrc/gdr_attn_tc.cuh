@@ -50,14 +50,15 @@ __device__ __forceinline__ void attn_scores(uint32_t d_tmem, uint32_t a, uint32_
   for (int kk = 0; kk < DP / 16; ++kk)
     tc::mma_bf16(d_tmem, (uint64_t)kDescHi << 32 | (a + kmajor_step(kk)), (uint64_t)kDescHi << 32 | (b + kmajor_step(kk)), id, kk > 0);
 }
-// D (+)= A B: A [128 x 128] in TMEM as bf16 (64 columns), B a tile of 128 rows by DP features.
-template <int DP>
+// D (+)= A B: A [128 x 128] in TMEM as bf16 (32 columns for its first 64 columns, those of the others begin at column Second),
+// B a tile of 128 rows by DP features.
+template <int DP, uint32_t Second = 32>
 __device__ __forceinline__ void attn_product(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate) {
   constexpr uint32_t id = tc::idesc_bf16(kTcBlock, DP, 0, 1);
   b = desc_mnmajor(b);
 #pragma unroll
   for (int kk = 0; kk < kTcBlock / 16; ++kk)
-    tc::mma_bf16_ts(d_tmem, a_tmem + 8u * kk, (uint64_t)kDescHi << 32 | (b + mnmajor_step(kk)), id, accumulate || kk > 0);
+    tc::mma_bf16_ts(d_tmem, a_tmem + (kk < 4 ? 8u * kk : Second + 8u * (kk - 4)), (uint64_t)kDescHi << 32 | (b + mnmajor_step(kk)), id, accumulate || kk > 0);
 }
 
 // mbar_wait by a whole warp, with one answer for all of its lanes.
@@ -73,6 +74,40 @@ __device__ __forceinline__ void regs_less() {
 template <int N>
 __device__ __forceinline__ void regs_more() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// 32 columns of this thread's TMEM lane: 64 values as bf16, the even ones in the lower halves.
+__device__ __forceinline__ void attn_put64(uint32_t taddr, const float* v) {
+  uint32_t r[32];
+#pragma unroll
+  for (int y = 0; y < 32; ++y) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * y], v[2 * y + 1]);
+    r[y] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  tc::tmem_st32(taddr, r);
+}
+
+// A row of an accumulator, DP columns of this thread's TMEM lane from taddr on, times f to out as bf16 (D features; with `any`
+// false or f zero the row is zero, whatever the accumulator holds; nothing is written unless `mine`).
+template <int DP>
+__device__ __forceinline__ void attn_store_row(uint32_t taddr, __nv_bfloat16* out, int D, float f, bool any, bool mine) {
+#pragma unroll
+  for (int e = 0; e < DP; e += 32) {
+    float o[32];
+    if (any) {
+      tc::tmem_ld32(taddr + e, o);
+      tc::tmem_wait_ld();
+    }
+    if (mine) {
+#pragma unroll
+      for (int y = 0; y < 32; y += 8) {
+        float v[8];
+#pragma unroll
+        for (int z = 0; z < 8; ++z) v[z] = any && f != 0.f ? o[y + z] * f : 0.f;
+        if (e + y < D) store_v<8>(out + e + y, v);
+      }
+    }
+  }
 }
 
 // A place in a ring of N slots: slot and parity of its use.

@@ -1,0 +1,595 @@
+// gdr_attn_tc_bwd.cu -- attention backward on the tensor cores (include/gdr_attn.h), bf16, D up to 128.
+//
+//   P = e^{scale Q K^T - lse},   dS = P (dO V^T - delta),   dV = P^T dO,   dK = scale dS^T Q,   dQ = scale dS K
+//
+// Two kernels, each of which forms P and dS anew: one takes 128 keys through the queries that see them (dK, dV), one 128 queries
+// through the keys that they see (dQ).  That is seven products per pair of tiles where one kernel would do with five, but the sums stay
+// in TMEM: no pass over dQ in memory for every key tile, and no atomics, whose order would change results.
+// Both are persistent, one block per SM, with the same roles: a warp for the TMA copies, a thread that issues the MMAs, two
+// warpgroups for the arithmetic on P and dS; thread = row of the tile in TMEM, the warpgroups take 64 columns each.
+//   keys:    S^T = K Q^T and dP^T = V dO^T have the keys as rows, so that P^T and dS^T, written over them as bf16, are the
+//            products' operands from TMEM.  TMEM: S^T, dP^T 128 columns each, dV, dK: all 512.  Issue order: dV, next S^T, dK, next
+//            dP^T; P is formed beside dK and dP^T, dS beside dV and the next S^T.  A spare warp brings lse and delta.
+//   queries: S = Q K^T and dP = dO V^T free their columns as soon as they are in registers; dS has two places of its own.
+#include <algorithm>
+
+#include "gdr_attn_tc.cuh"
+
+namespace gdr {
+namespace {
+
+using namespace tcx;
+
+constexpr int kThreads = 384;  // 8 warps of arithmetic, MMAs, copies, statistics, one idle
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kStatWarp = 10;
+constexpr int kRing = 4;
+
+struct BwdMaps {
+  CUtensorMap q, k, v, dout;
+};
+
+template <int DP>
+constexpr size_t bwd_smem() { return 1024 + (size_t)(2 + kRing) * attn_tile_bytes<DP>(); }
+
+// ------------------------------------------------------------------------------------ dK, dV
+struct KeyItem {
+  AttnSpan s;
+  int h, j0, lo, hi;  // key head, first key, query tiles [lo, hi)
+};
+__device__ __forceinline__ bool key_item(const AttnDims& d, const AttnTiles& t, unsigned x, KeyItem* w) {
+  int seq, tile;
+  if (!attn_tile(d, t, d.Hk, x, &seq, &w->h, &tile)) return false;
+  w->s = attn_span(d, seq);
+  w->j0 = tile * kTcBlock;
+  int lo = 0, hi = 0;
+  if (w->j0 < w->s.m) attn_queries(d, w->s, w->j0, min(w->s.m, w->j0 + kTcBlock), &lo, &hi);
+  w->lo = lo < hi ? lo / kTcBlock : 0;
+  w->hi = lo < hi ? (hi + kTcBlock - 1) / kTcBlock : 0;
+  return true;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dkdv_tc_kernel(const __grid_constant__ BwdMaps maps, AttnDims d, AttnTiles tiles, unsigned items, AttnBwdArgs a) {
+  constexpr uint32_t kTile = attn_tile_bytes<DP>();
+  constexpr uint32_t kS = 0, kdP = 128, kdV = 256, kdK = 256 + DP;
+  extern __shared__ unsigned char raw[];
+  __shared__ uint64_t kv_full[2], kv_empty[2], ring_full[kRing], ring_empty[kRing], s_full, dp_full, p_ready, ds_ready, done, tail_full, drain;
+  __shared__ uint64_t stat_full[2], stat_empty[2];
+  __shared__ __align__(16) float stat[2][2][kTcBlock];  // lse log2(e), delta of a query tile
+  __shared__ uint32_t tmem_slot;
+  unsigned char* const kv = align1024(raw);  // K, V
+  unsigned char* const ring_at = kv + 2 * kTile;  // Q, dO, Q, dO
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* const status = a.status;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&kv_full[i], 1);
+      tc::mbar_init(&kv_empty[i], 1);
+      tc::mbar_init(&stat_full[i], 1);
+      tc::mbar_init(&stat_empty[i], 8);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(&ring_full[i], 1);
+      tc::mbar_init(&ring_empty[i], 1);
+    }
+    tc::mbar_init(&s_full, 1);
+    tc::mbar_init(&dp_full, 1);
+    tc::mbar_init(&p_ready, 8);
+    tc::mbar_init(&ds_ready, 8);
+    tc::mbar_init(&done, 1);
+    tc::mbar_init(&tail_full, 1);
+    tc::mbar_init(&drain, 1);
+    tc::fence_barrier_init();
+  }
+  if (warp == kMmaWarp) tc::tmem_alloc<512>(&tmem_slot);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  KeyItem w;
+  bool ok = true;
+
+  if (warp == kLoadWarp) {
+    AttnRing<kRing> ring;
+    uint32_t kv_parity = 0, tail_parity = 0;
+    // a tile of Q or dO; the rows behind a sequence's end become zeros before it counts as loaded
+    auto load = [&](const CUtensorMap* map, int hq, int i) {
+      ok = ok && attn_warp_wait(&ring_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
+      if (!ok) return;
+      unsigned char* const dst = ring_at + ring.slot * kTile;
+      const int rows = w.s.n - i * kTcBlock;
+      uint64_t* const bar = rows < kTcBlock ? &tail_full : &ring_full[ring.slot];
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(bar, kTile);
+        attn_load_tile<DP>(dst, map, bar, hq, w.s.q0 + (long long)i * kTcBlock);
+      }
+      if (bar == &tail_full) {
+        ok = attn_warp_wait(&tail_full, tail_parity, status, kDevErrTimeoutBwd);
+        tail_parity ^= 1u;
+        if (!ok) return;
+        attn_clear_rows<DP>(dst, rows);
+        if (lane == 0) tc::mbar_arrive(&ring_full[ring.slot]);
+      }
+      ring.next();
+    };
+    for (unsigned turn = 0; ok; ++turn) {
+      const long long x = attn_item(turn, items);
+      if (x < 0) break;
+      if (!key_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
+      auto load_kv = [&](int which, const CUtensorMap* map) {
+        ok = ok && attn_warp_wait(&kv_empty[which], kv_parity ^ 1u, status, kDevErrTimeoutBwd);
+        if (ok && lane == 0) {
+          tc::mbar_arrive_expect_tx(&kv_full[which], kTile);
+          attn_load_tile<DP>(kv + which * kTile, map, &kv_full[which], w.h, w.s.k0 + w.j0);
+        }
+      };
+      load_kv(0, &maps.k);
+      load(&maps.q, w.h * d.G, w.lo);
+      load_kv(1, &maps.v);
+      kv_parity ^= 1u;
+      for (int g = 0; g < d.G && ok; ++g)
+        for (int i = w.lo; i < w.hi && ok; ++i) {
+          if (g > 0 || i > w.lo) load(&maps.q, w.h * d.G + g, i);
+          load(&maps.dout, w.h * d.G + g, i);
+        }
+    }
+    if (!ok)  // after a wait that ran out, the copies under way end before the block does
+      for (int i = 0; i < kRing; ++i) {
+        tc::mbar_wait(&ring_full[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
+        ring.next();
+      }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      AttnRing<kRing> ring;  // of the next Q; its dO is one further
+      uint32_t kv_parity = 0, parity = 0;
+      const uint32_t k_at = tc::smem_u32(kv), v_at = k_at + kTile, r_at = tc::smem_u32(ring_at);
+      auto wait = [&](uint64_t* bar, uint32_t p) {
+        ok = ok && tc::mbar_wait(bar, p, status, kDevErrTimeoutBwd);
+        tc::tc_fence_after();
+        return ok;
+      };
+      for (unsigned turn = 0; ok; ++turn) {
+        const long long x = attn_item(turn, items);
+        if (x < 0) break;
+        if (!key_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
+        const int steps = (w.hi - w.lo) * d.G;
+        wait(&kv_full[0], kv_parity);
+        if (wait(&ring_full[ring.slot], ring.parity)) {
+          attn_scores<DP>(tmem + kS, k_at, r_at + ring.slot * kTile);
+          tc::mma_commit(&s_full);
+          if (steps == 1) tc::mma_commit(&kv_empty[0]);
+        }
+        wait(&kv_full[1], kv_parity);
+        if (wait(&ring_full[ring.slot + 1], ring.parity)) {
+          attn_scores<DP>(tmem + kdP, v_at, r_at + (ring.slot + 1) * kTile);
+          tc::mma_commit(&dp_full);
+          if (steps == 1) tc::mma_commit(&kv_empty[1]);
+        }
+        kv_parity ^= 1u;
+        for (int it = 0; it < steps && ok; ++it) {
+          const int q_slot = ring.slot;
+          const bool more = it + 1 < steps;
+          ring.next();
+          ring.next();
+          if (!wait(&p_ready, parity)) break;
+          attn_product<DP, 64>(tmem + kdV, tmem + kS, r_at + (q_slot + 1) * kTile, it > 0);
+          tc::mma_commit(&ring_empty[q_slot + 1]);
+          if (more) {
+            if (!wait(&ring_full[ring.slot], ring.parity)) break;
+            attn_scores<DP>(tmem + kS, k_at, r_at + ring.slot * kTile);
+            tc::mma_commit(&s_full);
+            if (it + 2 == steps) tc::mma_commit(&kv_empty[0]);
+          }
+          if (!wait(&ds_ready, parity)) break;
+          attn_product<DP, 64>(tmem + kdK, tmem + kdP, r_at + q_slot * kTile, it > 0);
+          tc::mma_commit(&ring_empty[q_slot]);
+          if (more) {
+            if (!wait(&ring_full[ring.slot + 1], ring.parity)) break;
+            attn_scores<DP>(tmem + kdP, v_at, r_at + (ring.slot + 1) * kTile);
+            tc::mma_commit(&dp_full);
+            if (it + 2 == steps) tc::mma_commit(&kv_empty[1]);
+          } else {
+            tc::mma_commit(&done);
+          }
+          parity ^= 1u;
+        }
+      }
+      if (!ok) {  // the products under way end before their memory is given back
+        tc::mma_commit(&drain);
+        tc::mbar_wait(&drain, 0, status, kDevErrTimeoutBwd);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kStatWarp) {
+    AttnRing<2> ring;
+    for (unsigned turn = 0; ok; ++turn) {
+      const long long x = attn_item(turn, items);
+      if (x < 0) break;
+      if (!key_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
+      for (int g = 0; g < d.G && ok; ++g) {
+        const long long at = w.s.lse0 + (long long)(w.h * d.G + g) * d.Tq;
+        for (int i = w.lo; i < w.hi; ++i) {
+          float ls[4], dl[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = i * kTcBlock + 32 * e + lane;
+            const bool on = r < w.s.n;
+            ls[e] = on ? a.lse[at + r] * kLog2e : INFINITY;
+            dl[e] = on ? a.delta[at + r] : 0.f;
+            if (ls[e] == -INFINITY) ls[e] = INFINITY;  // a query that sees nothing: e^-infinity
+          }
+          ok = attn_warp_wait(&stat_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
+          if (!ok) break;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            stat[ring.slot][0][32 * e + lane] = ls[e];
+            stat[ring.slot][1][32 * e + lane] = dl[e];
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&stat_full[ring.slot]);
+          ring.next();
+        }
+      }
+    }
+  } else if (warp < 8) {
+    const int half = warp >> 2, row = threadIdx.x & 127, col = 64 * half;
+    const uint32_t s_col = tc::tmem_lane_addr(tmem, warp, kS + col), dp_col = tc::tmem_lane_addr(tmem, warp, kdP + col);
+    const float c = d.scale * kLog2e;
+    uint32_t parity = 0, done_parity = 0;
+    AttnRing<2> ring;
+    for (unsigned turn = 0; ok; ++turn) {
+      const long long x = attn_item(turn, items);
+      if (x < 0) break;
+      if (!key_item(d, tiles, (unsigned)x, &w)) continue;
+      const int j = w.j0 + row, off = w.s.m - w.s.n;
+      // the queries [from, to) that see this key; tiles [.., ..) in which every query sees every key of the tile
+      const int from = d.causal ? j - off : 0;
+      const long long to = d.window ? (long long)j - off + d.window : w.s.n;
+      const int j_last = w.j0 + kTcBlock - 1;
+      const int whole_from = d.causal ? j_last - off : 0;
+      const long long whole_to = d.window ? (long long)w.j0 - off + d.window : (1ll << 40);
+      for (int g = 0; g < d.G && ok; ++g)
+        for (int i = w.lo; i < w.hi; ++i) {
+          ok = attn_warp_wait(&stat_full[ring.slot], ring.parity, status, kDevErrTimeoutBwd);
+          ok = ok && attn_warp_wait(&s_full, parity, status, kDevErrTimeoutBwd);
+          if (!ok) break;
+          tc::tc_fence_after();
+          const int i0 = i * kTcBlock;
+          float p[64], dp[64];
+          tc::tmem_ld32(s_col, p);
+          tc::tmem_ld32(s_col + 32, p + 32);
+          tc::tmem_wait_ld();
+          const float* ls = stat[ring.slot][0] + col;
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(ls + e);
+            p[e] = ex2f(fmaf(p[e], c, -l4.x));
+            p[e + 1] = ex2f(fmaf(p[e + 1], c, -l4.y));
+            p[e + 2] = ex2f(fmaf(p[e + 2], c, -l4.z));
+            p[e + 3] = ex2f(fmaf(p[e + 3], c, -l4.w));
+          }
+          if (i0 < whole_from || i0 + kTcBlock > whole_to) {
+            const int a0 = from - i0 - col;
+            const int a1 = (int)min(to - i0 - col, 1ll << 20);
+#pragma unroll
+            for (int e = 0; e < 64; ++e) p[e] = e >= a0 && e < a1 ? p[e] : 0.f;
+          }
+          attn_put64(s_col, p);
+          tc::tmem_wait_st();
+          tc::tc_fence_before();
+          __syncwarp();
+          GDR_DELAY(41);
+          if (lane == 0) tc::mbar_arrive(&p_ready);
+          ok = attn_warp_wait(&dp_full, parity, status, kDevErrTimeoutBwd);
+          if (!ok) break;
+          tc::tc_fence_after();
+          tc::tmem_ld32(dp_col, dp);
+          tc::tmem_ld32(dp_col + 32, dp + 32);
+          tc::tmem_wait_ld();
+          const float* dl = stat[ring.slot][1] + col;
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            const float4 d4 = *reinterpret_cast<const float4*>(dl + e);
+            dp[e] = p[e] * (dp[e] - d4.x);
+            dp[e + 1] = p[e + 1] * (dp[e + 1] - d4.y);
+            dp[e + 2] = p[e + 2] * (dp[e + 2] - d4.z);
+            dp[e + 3] = p[e + 3] * (dp[e + 3] - d4.w);
+          }
+          attn_put64(dp_col, dp);
+          tc::tmem_wait_st();
+          tc::tc_fence_before();
+          __syncwarp();
+          GDR_DELAY(42);
+          if (lane == 0) {
+            tc::mbar_arrive(&ds_ready);
+            tc::mbar_arrive(&stat_empty[ring.slot]);
+          }
+          parity ^= 1u;
+          ring.next();
+        }
+      if (!ok) break;
+      const bool any = w.lo < w.hi;
+      if (any) {
+        ok = attn_warp_wait(&done, done_parity, status, kDevErrTimeoutBwd);
+        done_parity ^= 1u;
+        if (!ok) break;
+        tc::tc_fence_after();
+      }
+      // the first warpgroup stores dV, the second dK
+      __nv_bfloat16* const out = (__nv_bfloat16*)(half ? a.dk : a.dv) + ((w.s.k0 + j) * d.Hk + w.h) * (long long)d.D;
+      attn_store_row<DP>(tc::tmem_lane_addr(tmem, warp, half ? kdK : kdV), out, d.D, half ? d.scale : 1.f, any, j < w.s.m);
+      tc::tc_fence_before();  // read before the next item's first product into them, which the next arrival allows
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------------------- dQ
+struct QueryItem {
+  AttnSpan s;
+  int h, i0, lo, hi;  // query head, first query, key tiles [lo, hi)
+};
+__device__ __forceinline__ bool query_item(const AttnDims& d, const AttnTiles& t, unsigned x, QueryItem* w) {
+  int seq, tile;
+  if (!attn_tile(d, t, d.Hq, x, &seq, &w->h, &tile)) return false;
+  w->s = attn_span(d, seq);
+  w->i0 = tile * kTcBlock;
+  int lo = 0, hi = 0;
+  if (w->i0 < w->s.n) attn_keys(d, w->s, w->i0, min(w->s.n, w->i0 + kTcBlock), &lo, &hi);
+  w->lo = lo < hi ? lo / kTcBlock : 0;
+  w->hi = lo < hi ? (hi + kTcBlock - 1) / kTcBlock : 0;
+  return true;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dq_tc_kernel(const __grid_constant__ BwdMaps maps, AttnDims d, AttnTiles tiles, unsigned items, AttnBwdArgs a) {
+  constexpr uint32_t kTile = attn_tile_bytes<DP>();
+  constexpr uint32_t kS = 0, kdP = 128, kdQ = 256, kdS = 384;  // dS: two places of 64 columns
+  extern __shared__ unsigned char raw[];
+  __shared__ uint64_t q_full[2], q_empty[2], ring_full[kRing], ring_empty[kRing], s_full, dp_full, s_free, dp_free, ds_ready, done, tail_full, drain;
+  __shared__ uint32_t tmem_slot;
+  unsigned char* const qd = align1024(raw);  // Q, dO
+  unsigned char* const ring_at = qd + 2 * kTile;  // K, V, K, V
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* const status = a.status;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&q_full[i], 1);
+      tc::mbar_init(&q_empty[i], 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(&ring_full[i], 1);
+      tc::mbar_init(&ring_empty[i], 1);
+    }
+    tc::mbar_init(&s_full, 1);
+    tc::mbar_init(&dp_full, 1);
+    tc::mbar_init(&s_free, 8);
+    tc::mbar_init(&dp_free, 8);
+    tc::mbar_init(&ds_ready, 8);
+    tc::mbar_init(&done, 1);
+    tc::mbar_init(&tail_full, 1);
+    tc::mbar_init(&drain, 1);
+    tc::fence_barrier_init();
+  }
+  if (warp == kMmaWarp) tc::tmem_alloc<512>(&tmem_slot);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  QueryItem w;
+  bool ok = true;
+
+  if (warp == kLoadWarp) {
+    AttnRing<kRing> ring;
+    uint32_t q_parity = 0, tail_parity = 0;
+    // a tile of K or V; the keys behind a sequence's end become zeros before it counts as loaded (values are not summed here)
+    auto load = [&](const CUtensorMap* map, int j, bool key) {
+      ok = ok && attn_warp_wait(&ring_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
+      if (!ok) return;
+      unsigned char* const dst = ring_at + ring.slot * kTile;
+      const int rows = w.s.m - j * kTcBlock;
+      uint64_t* const bar = key && rows < kTcBlock ? &tail_full : &ring_full[ring.slot];
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(bar, kTile);
+        attn_load_tile<DP>(dst, map, bar, w.h / d.G, w.s.k0 + (long long)j * kTcBlock);
+      }
+      if (bar == &tail_full) {
+        ok = attn_warp_wait(&tail_full, tail_parity, status, kDevErrTimeoutBwd);
+        tail_parity ^= 1u;
+        if (!ok) return;
+        attn_clear_rows<DP>(dst, rows);
+        if (lane == 0) tc::mbar_arrive(&ring_full[ring.slot]);
+      }
+      ring.next();
+    };
+    for (unsigned turn = 0; ok; ++turn) {
+      const long long x = attn_item(turn, items);
+      if (x < 0) break;
+      if (!query_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
+      auto load_q = [&](int which, const CUtensorMap* map) {
+        ok = ok && attn_warp_wait(&q_empty[which], q_parity ^ 1u, status, kDevErrTimeoutBwd);
+        if (ok && lane == 0) {
+          tc::mbar_arrive_expect_tx(&q_full[which], kTile);
+          attn_load_tile<DP>(qd + which * kTile, map, &q_full[which], w.h, w.s.q0 + w.i0);
+        }
+      };
+      load_q(0, &maps.q);
+      load(&maps.k, w.lo, true);
+      load_q(1, &maps.dout);
+      q_parity ^= 1u;
+      load(&maps.v, w.lo, false);
+      for (int j = w.lo + 1; j < w.hi && ok; ++j) {
+        load(&maps.k, j, true);
+        load(&maps.v, j, false);
+      }
+    }
+    if (!ok)  // after a wait that ran out, the copies under way end before the block does
+      for (int i = 0; i < kRing; ++i) {
+        tc::mbar_wait(&ring_full[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
+        ring.next();
+      }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      AttnRing<kRing> ring;  // of the next K; its V is one further
+      uint32_t q_parity = 0, free_parity = 1, parity = 0;  // s_free, dp_free: of the tile before
+      uint32_t place = 0;
+      const uint32_t q_at = tc::smem_u32(qd), do_at = q_at + kTile, r_at = tc::smem_u32(ring_at);
+      auto wait = [&](uint64_t* bar, uint32_t p) {
+        ok = ok && tc::mbar_wait(bar, p, status, kDevErrTimeoutBwd);
+        tc::tc_fence_after();
+        return ok;
+      };
+      for (unsigned turn = 0; ok; ++turn) {
+        const long long x = attn_item(turn, items);
+        if (x < 0) break;
+        if (!query_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
+        const int steps = w.hi - w.lo;
+        auto scores = [&](int it) {  // S and dP of a step
+          if (it == 0) wait(&q_full[0], q_parity);
+          wait(&ring_full[ring.slot], ring.parity);
+          if (!wait(&s_free, free_parity)) return;
+          attn_scores<DP>(tmem + kS, q_at, r_at + ring.slot * kTile);
+          tc::mma_commit(&s_full);
+          if (it + 1 == steps) tc::mma_commit(&q_empty[0]);
+          if (it == 0) wait(&q_full[1], q_parity);
+          wait(&ring_full[ring.slot + 1], ring.parity);
+          if (!wait(&dp_free, free_parity)) return;
+          attn_scores<DP>(tmem + kdP, do_at, r_at + (ring.slot + 1) * kTile);
+          tc::mma_commit(&dp_full);
+          tc::mma_commit(&ring_empty[ring.slot + 1]);
+          if (it + 1 == steps) tc::mma_commit(&q_empty[1]);
+          free_parity ^= 1u;
+          ring.next();
+          ring.next();
+        };
+        int k_slot = ring.slot;
+        scores(0);
+        q_parity ^= 1u;
+        for (int it = 0; it < steps && ok; ++it) {
+          const int next_slot = ring.slot;
+          if (it + 1 < steps) scores(it + 1);
+          if (!wait(&ds_ready, parity)) break;
+          attn_product<DP>(tmem + kdQ, tmem + kdS + 64 * place, r_at + k_slot * kTile, it > 0);
+          tc::mma_commit(&ring_empty[k_slot]);
+          if (it + 1 == steps) tc::mma_commit(&done);
+          k_slot = next_slot;
+          parity ^= 1u;
+          place ^= 1u;
+        }
+      }
+      if (!ok) {  // the products under way end before their memory is given back
+        tc::mma_commit(&drain);
+        tc::mbar_wait(&drain, 0, status, kDevErrTimeoutBwd);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    const int half = warp >> 2, row = threadIdx.x & 127, col = 64 * half;
+    const uint32_t s_col = tc::tmem_lane_addr(tmem, warp, kS + col), dp_col = tc::tmem_lane_addr(tmem, warp, kdP + col);
+    const uint32_t ds_col = tc::tmem_lane_addr(tmem, warp, kdS + 32 * half);
+    const float c = d.scale * kLog2e;
+    uint32_t parity = 0, done_parity = 0, place = 0;
+    for (unsigned turn = 0; ok; ++turn) {
+      const long long x = attn_item(turn, items);
+      if (x < 0) break;
+      if (!query_item(d, tiles, (unsigned)x, &w)) continue;
+      const int i = w.i0 + row, off = w.s.m - w.s.n;
+      const bool mine = i < w.s.n;
+      const long long at = w.s.lse0 + (long long)w.h * d.Tq + i;
+      float ls = mine ? a.lse[at] * kLog2e : INFINITY;
+      if (ls == -INFINITY) ls = INFINITY;  // a query that sees nothing: e^-infinity
+      const float dl = mine ? a.delta[at] : 0.f;
+      const int from = d.window ? max(0, i + off - d.window + 1) : 0, to = d.causal ? min(w.s.m, i + off + 1) : w.s.m;
+      const int i_last = w.i0 + kTcBlock - 1;
+      const int whole_to = d.causal ? min(w.s.m, w.i0 + off + 1) : w.s.m, whole_from = d.window ? i_last + off - d.window + 1 : 0;
+      for (int j = w.lo; j < w.hi; ++j) {
+        ok = attn_warp_wait(&s_full, parity, status, kDevErrTimeoutBwd);
+        if (!ok) break;
+        tc::tc_fence_after();
+        float p[64], dp[64];
+        tc::tmem_ld32(s_col, p);
+        tc::tmem_ld32(s_col + 32, p + 32);
+        tc::tmem_wait_ld();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&s_free);
+#pragma unroll
+        for (int e = 0; e < 64; ++e) p[e] = ex2f(fmaf(p[e], c, -ls));
+        const int j0 = j * kTcBlock;
+        const bool partial = j0 + kTcBlock > whole_to || j0 < whole_from;
+        ok = attn_warp_wait(&dp_full, parity, status, kDevErrTimeoutBwd);
+        if (!ok) break;
+        tc::tc_fence_after();
+        tc::tmem_ld32(dp_col, dp);
+        tc::tmem_ld32(dp_col + 32, dp + 32);
+        tc::tmem_wait_ld();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&dp_free);
+#pragma unroll
+        for (int e = 0; e < 64; ++e) dp[e] = p[e] * (dp[e] - dl);
+        if (partial) {
+          const int a0 = from - j0 - col, a1 = to - j0 - col;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) dp[e] = e >= a0 && e < a1 ? dp[e] : 0.f;
+        }
+        attn_put64(ds_col + 64 * place, dp);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        GDR_DELAY(43);
+        if (lane == 0) tc::mbar_arrive(&ds_ready);
+        parity ^= 1u;
+        place ^= 1u;
+      }
+      if (!ok) break;
+      const bool any = w.lo < w.hi;
+      if (any) {
+        ok = attn_warp_wait(&done, done_parity, status, kDevErrTimeoutBwd);
+        done_parity ^= 1u;
+        if (!ok) break;
+        tc::tc_fence_after();
+      }
+      // each warpgroup stores half of the features
+      __nv_bfloat16* const out = (__nv_bfloat16*)a.dq + ((w.s.q0 + i) * d.Hq + w.h) * (long long)d.D + half * (DP / 2);
+      attn_store_row<DP / 2>(tc::tmem_lane_addr(tmem, warp, kdQ + half * (DP / 2)), out, d.D - half * (DP / 2), d.scale, any, mine);
+      tc::tc_fence_before();  // read before the next item's first product into it, which the next arrival allows
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int DP>
+cudaError_t bwd(const AttnDims& d, const AttnTiles& tq, const AttnTiles& tk, const AttnBwdArgs& a, cudaStream_t s) {
+  BwdMaps maps;
+  const long long rows_q = (long long)d.B * d.Tq, rows_k = (long long)d.B * d.Tk;
+  if (!attn_map(&maps.q, a.q, d.D, d.Hq, rows_q, d.ld_q) || !attn_map(&maps.k, a.k, d.D, d.Hk, rows_k, d.ld_k) ||
+      !attn_map(&maps.v, a.v, d.D, d.Hk, rows_k, d.ld_v) || !attn_map(&maps.dout, a.dout, d.D, d.Hq, rows_q, d.ld_do))
+    return cudaErrorInvalidValue;
+  constexpr size_t smem = bwd_smem<DP>();
+  cudaError_t e = set_smem_once((const void*)attn_dkdv_tc_kernel<DP>, smem);
+  if (e == cudaSuccess) e = set_smem_once((const void*)attn_dq_tc_kernel<DP>, smem);
+  if (e != cudaSuccess) return e;
+  const long long keys = attn_tile_count(d, true, kTcBlock) * d.Hk, queries = attn_tile_count(d, false, kTcBlock) * d.Hq;
+  attn_dkdv_tc_kernel<DP><<<(unsigned)std::min<long long>(keys, kSmCount), kThreads, smem, s>>>(maps, d, tk, (unsigned)keys, a);
+  stage_mark(s, "attn_dkdv");
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  attn_dq_tc_kernel<DP><<<(unsigned)std::min<long long>(queries, kSmCount), kThreads, smem, s>>>(maps, d, tq, (unsigned)queries, a);
+  stage_mark(s, "attn_dq");
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_bwd_tc(const AttnDims& d, const AttnTiles& tq, const AttnTiles& tk, const AttnBwdArgs& a, cudaStream_t s) {
+  return d.D > 64 ? bwd<128>(d, tq, tk, a, s) : bwd<64>(d, tq, tk, a, s);
+}
+
+}  // namespace gdr
