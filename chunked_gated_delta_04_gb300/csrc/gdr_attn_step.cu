@@ -366,32 +366,43 @@ __global__ void __launch_bounds__(kThreads) attn_step_kernel(StepDims d, const I
   if (blockIdx.x >= blocks) return;
   const long long start = total * blockIdx.x / blocks, end = total * (blockIdx.x + 1) / blocks;
 
-  // the copies of the tile at `from` into a stage; true: a page outside the pool
-  auto load = [&](const Cursor<KT>& from, int stage) {
-    constexpr int TPR = DP / N, RP = kThreads / TPR;  // threads of a row, rows at a time
-    IT* const ks = stages + (size_t)stage * 2 * KT * S;
+  constexpr int TPR = DP / N, RP = kThreads / TPR, PASS = KT / RP;  // threads of a row, rows at a time, rows of a thread
+  const int c_of = tid % TPR * N, r_of = tid / TPR;
+  // The pages of the thread's rows of a tile: -1 for a position that is not seen, -2 for a page outside the pool.
+  auto pages_of = [&](const Cursor<KT>& from, int (&pages)[PASS]) {
+    const int p0 = (from.row.tile0 + from.tile) * KT, first = p0 / d.page_size, rest = p0 - first * d.page_size;
+    const int32_t* at = table + (long long)from.b * d.max_pages + first;
+#pragma unroll
+    for (int i = 0; i < PASS; ++i) {
+      const int r = r_of + RP * i, x = rest + r;
+      const bool seen = p0 + r >= from.row.lo && p0 + r <= from.row.len;
+      pages[i] = seen ? at[d.page_size >= KT ? (int)(x >= d.page_size) : x / d.page_size] : -1;
+      if (seen && (pages[i] < 0 || pages[i] >= d.num_pages)) pages[i] = -2;
+    }
+  };
+  // The copies of the tile at `from` into a stage; true: a page outside the pool.
+  auto load = [&](const Cursor<KT>& from, const int (&pages)[PASS], int stage) {
+    IT* const ks = stages + (size_t)stage * 2 * KT * S + r_of * S + c_of;
     IT* const vs = ks + KT * S;
-    const int c = tid % TPR * N, h = from.unit / d.HB;
-    const int p0 = (from.row.tile0 + from.tile) * KT;
-    const int32_t* pages = table + (long long)from.b * d.max_pages;
+    const int h = from.unit / d.HB, p0 = (from.row.tile0 + from.tile) * KT, rest = p0 % d.page_size;
+    const int last = from.row.len - p0;  // the new token's row, if it is one of the tile's
+    const bool wide = c_of < d.D;
     bool bad = false;
 #pragma unroll
-    for (int i = 0; i < KT / RP; ++i) {
-      const int r = tid / TPR + RP * i, p = p0 + r;
-      IT *kd = ks + r * S + c, *vd = vs + r * S + c;
-      const bool seen = p >= from.row.lo && p <= from.row.len;
-      long long at = 0;
-      bool ok = seen;
-      if (seen) {
-        const int pi = p / d.page_size, page = pages[pi];
-        ok = page >= 0 && page < d.num_pages;
-        bad |= !ok;
-        if (ok) at = (((long long)page * d.page_size + (p - pi * d.page_size)) * d.Hk + h) * d.D + c;
+    for (int i = 0; i < PASS; ++i) {
+      const int r = r_of + RP * i, x = rest + r;
+      const int place = d.page_size >= KT ? (x >= d.page_size ? x - d.page_size : x) : x % d.page_size;
+      const bool ok = pages[i] >= 0 && wide;
+      bad |= pages[i] == -2;
+      const long long at = ok ? (((long long)pages[i] * d.page_size + place) * d.Hk + h) * d.D + c_of : 0;
+      if (r != last) {
+        copy_async_l2(ks + RP * i * S, k_cache + at, ok ? 16 : 0);
+        copy_async_l2(vs + RP * i * S, v_cache + at, ok ? 16 : 0);
+        continue;
       }
-      if (c >= d.D) ok = false;
-      if (p == from.row.len && c < d.D) {  // the new token
-        uint4 kn, vn;
-        const IT *kf = k + (long long)from.b * d.ld_k + (long long)h * d.D + c, *vf = v + (long long)from.b * d.ld_v + (long long)h * d.D + c;
+      uint4 kn = make_uint4(0, 0, 0, 0), vn = kn;
+      if (wide) {
+        const IT *kf = k + (long long)from.b * d.ld_k + (long long)h * d.D + c_of, *vf = v + (long long)from.b * d.ld_v + (long long)h * d.D + c_of;
         if (d.vec) {
           kn = *reinterpret_cast<const uint4*>(kf);
           vn = *reinterpret_cast<const uint4*>(vf);
@@ -402,15 +413,12 @@ __global__ void __launch_bounds__(kThreads) attn_step_kernel(StepDims d, const I
           kn = *reinterpret_cast<const uint4*>(a);
           vn = *reinterpret_cast<const uint4*>(b);
         }
-        *reinterpret_cast<uint4*>(kd) = kn;
-        *reinterpret_cast<uint4*>(vd) = vn;
-        if (ok && from.unit % d.HB == 0) {  // one unit of a key head writes
-          *reinterpret_cast<uint4*>(k_cache + at) = kn;
-          *reinterpret_cast<uint4*>(v_cache + at) = vn;
-        }
-      } else {
-        copy_async_l2(kd, k_cache + at, ok ? 16 : 0);
-        copy_async_l2(vd, v_cache + at, ok ? 16 : 0);
+      }
+      *reinterpret_cast<uint4*>(ks + RP * i * S) = kn;
+      *reinterpret_cast<uint4*>(vs + RP * i * S) = vn;
+      if (ok && from.unit % d.HB == 0) {  // one unit of a key head writes
+        *reinterpret_cast<uint4*>(k_cache + at) = kn;
+        *reinterpret_cast<uint4*>(v_cache + at) = vn;
       }
     }
     return bad;
@@ -421,14 +429,21 @@ __global__ void __launch_bounds__(kThreads) attn_step_kernel(StepDims d, const I
   ahead = here;
   uint32_t bad_stages = 0;
   long long loaded = start;
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) {
+  int pages[PASS];  // of the tile whose copies are next: read a tile ahead of them
+  pages_of(ahead, pages);
+  auto load_next = [&](int into) {
+    bad_stages &= ~(1u << into);
     if (loaded < end) {
-      bad_stages |= (uint32_t)load(ahead, i) << i;
-      if (++loaded < end) ahead.next(d, lengths, units);
+      bad_stages |= (uint32_t)load(ahead, pages, into) << into;
+      if (++loaded < end) {
+        ahead.next(d, lengths, units);
+        pages_of(ahead, pages);
+      }
     }
     copy_async_commit();
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) load_next(i);
   Engine e;
   const float c = d.scale * kLog2e;
   int stage = 0, first_tile = here.tile, heads = 0;
@@ -450,15 +465,7 @@ __global__ void __launch_bounds__(kThreads) attn_step_kernel(StepDims d, const I
     }
     copy_async_wait_group<kStages - 2>();
     __syncthreads();
-    {
-      const int into = (stage + kStages - 1) % kStages;
-      bad_stages &= ~(1u << into);
-      if (loaded < end) {
-        bad_stages |= (uint32_t)load(ahead, into) << into;
-        if (++loaded < end) ahead.next(d, lengths, units);
-      }
-      copy_async_commit();
-    }
+    load_next((stage + kStages - 1) % kStages);
     const IT* ks = stages + (size_t)stage * 2 * KT * S;
     e.tile(ks, ks + KT * S, (here.row.tile0 + here.tile) * KT, here.row, c, heads);
     bad |= bad_stages >> stage & 1;

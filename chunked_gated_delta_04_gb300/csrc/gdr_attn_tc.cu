@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
     uint32_t q_parity = 0, tail_parity = 0;
     bool ok = true;
     auto load_kv = [&](const CUtensorMap* map, const FwdItem<NT>& w, int j, bool value) {
+      GDR_DELAY(49);
       ok = ok && attn_warp_wait(&kv_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutFwd);
       if (!ok) return;
       unsigned char* const dst = skv + ring.slot * Shape::kTile;
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
           for (int i = 0; i < NT; ++i) {
             if (!ok) break;
             if (j >= w.lo[i] && j < w.hi[i]) {
+              GDR_DELAY(48);
               ok = tc::mbar_wait(&p_ready[i], p_parity >> i & 1u, status, kDevErrTimeoutFwd);
               p_parity ^= 1u << i;
               if (!ok) break;

@@ -22,14 +22,95 @@ using namespace tcx;
 
 constexpr int kThreads = 384;  // 8 warps of arithmetic, MMAs, copies, statistics, one idle
 constexpr int kMmaWarp = 8, kLoadWarp = 9, kStatWarp = 10;
-constexpr int kRing = 4;
+// Two tiles that stay, and rings of the ones that pass: three slots for what the last product of a step reads (Q, or K), two for
+// what an earlier one does (dO, or V).
+constexpr int kA = 3, kB = 2;
 
 struct BwdMaps {
   CUtensorMap q, k, v, dout;
 };
 
+// Behind the tiles in shared memory.
+struct BwdShared {
+  float stat[2][2][kTcBlock];  // lse log2(e), delta of a query tile
+  uint64_t keep_full[2], keep_empty[2], a_full[kA], a_empty[kA], b_full[kB], b_empty[kB], stat_full[2], stat_empty[2];
+  uint64_t s_full, dp_full, s_free, dp_free, p_ready, ds_ready[2], done, tail_full, drain;
+  uint32_t tmem_slot;
+};
 template <int DP>
-constexpr size_t bwd_smem() { return 1024 + (size_t)(2 + kRing) * attn_tile_bytes<DP>(); }
+constexpr size_t bwd_smem() { return (size_t)(2 + kA + kB) * attn_tile_bytes<DP>() + sizeof(BwdShared); }
+static_assert(bwd_smem<128>() <= 227 * 1024, "shared memory of a block");
+
+// The tiles need 1024-byte alignment; the kernels have no other shared memory.
+extern __shared__ __align__(1024) unsigned char bwd_raw[];
+
+__device__ __forceinline__ void bwd_barriers(BwdShared& b) {
+  for (int i = 0; i < 2; ++i) {
+    tc::mbar_init(&b.keep_full[i], 1);
+    tc::mbar_init(&b.keep_empty[i], 1);
+    tc::mbar_init(&b.stat_full[i], 1);
+    tc::mbar_init(&b.stat_empty[i], 8);
+    tc::mbar_init(&b.ds_ready[i], 8);
+  }
+  for (int i = 0; i < kA; ++i) {
+    tc::mbar_init(&b.a_full[i], 1);
+    tc::mbar_init(&b.a_empty[i], 1);
+  }
+  for (int i = 0; i < kB; ++i) {
+    tc::mbar_init(&b.b_full[i], 1);
+    tc::mbar_init(&b.b_empty[i], 1);
+  }
+  tc::mbar_init(&b.s_full, 1);
+  tc::mbar_init(&b.dp_full, 1);
+  tc::mbar_init(&b.s_free, 8);
+  tc::mbar_init(&b.dp_free, 8);
+  tc::mbar_init(&b.p_ready, 8);
+  tc::mbar_init(&b.done, 1);
+  tc::mbar_init(&b.tail_full, 1);
+  tc::mbar_init(&b.drain, 1);
+  tc::fence_barrier_init();
+}
+
+// The loading warp's side of a ring.
+template <int DP, int N>
+struct BwdLoader {
+  BwdShared& b;
+  unsigned char* at;
+  uint64_t *full, *empty;
+  uint32_t* status;
+  AttnRing<N> ring;
+
+  // The rows [r0, r0 + 128) of a head; `rows` of them are the sequence's, and with `clear` the others become zeros before the
+  // tile counts as loaded.
+  __device__ __forceinline__ bool load(const CUtensorMap* map, int head, long long r0, int rows, bool clear, uint32_t& tail_parity) {
+    GDR_DELAY(47);
+    if (!attn_warp_wait(&empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd)) return false;
+    unsigned char* const dst = at + ring.slot * attn_tile_bytes<DP>();
+    const bool tail = clear && rows < kTcBlock;
+    uint64_t* const bar = tail ? &b.tail_full : &full[ring.slot];
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+      tc::mbar_arrive_expect_tx(bar, attn_tile_bytes<DP>());
+      attn_load_tile<DP>(dst, map, bar, head, r0);
+    }
+    if (tail) {
+      const bool ok = attn_warp_wait(&b.tail_full, tail_parity, status, kDevErrTimeoutBwd);
+      tail_parity ^= 1u;
+      if (!ok) return false;
+      attn_clear_rows<DP>(dst, rows);
+      if (lane == 0) tc::mbar_arrive(&full[ring.slot]);
+    }
+    ring.next();
+    return true;
+  }
+  // After a wait that ran out, the copies under way end before the block does.
+  __device__ __forceinline__ void drain() {
+    for (int i = 0; i < N; ++i) {
+      tc::mbar_wait(&full[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
+      ring.next();
+    }
+  }
+};
 
 // ------------------------------------------------------------------------------------ dK, dV
 struct KeyItem {
@@ -53,97 +134,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_dkdv_tc_kernel(const __grid_constant__ BwdMaps maps, AttnDims d, AttnTiles tiles, unsigned items, AttnBwdArgs a) {
   constexpr uint32_t kTile = attn_tile_bytes<DP>();
   constexpr uint32_t kS = 0, kdP = 128, kdV = 256, kdK = 256 + DP;
-  extern __shared__ unsigned char raw[];
-  __shared__ uint64_t kv_full[2], kv_empty[2], ring_full[kRing], ring_empty[kRing], s_full, dp_full, p_ready, ds_ready, done, tail_full, drain;
-  __shared__ uint64_t stat_full[2], stat_empty[2];
-  __shared__ __align__(16) float stat[2][2][kTcBlock];  // lse log2(e), delta of a query tile
-  __shared__ uint32_t tmem_slot;
-  unsigned char* const kv = align1024(raw);  // K, V
-  unsigned char* const ring_at = kv + 2 * kTile;  // Q, dO, Q, dO
+  unsigned char* const keep = bwd_raw;  // K, V
+  unsigned char* const a_at = keep + 2 * kTile;
+  unsigned char* const b_at = a_at + kA * kTile;
+  BwdShared& b = *reinterpret_cast<BwdShared*>(b_at + kB * kTile);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* const status = a.status;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&kv_full[i], 1);
-      tc::mbar_init(&kv_empty[i], 1);
-      tc::mbar_init(&stat_full[i], 1);
-      tc::mbar_init(&stat_empty[i], 8);
-    }
-    for (int i = 0; i < kRing; ++i) {
-      tc::mbar_init(&ring_full[i], 1);
-      tc::mbar_init(&ring_empty[i], 1);
-    }
-    tc::mbar_init(&s_full, 1);
-    tc::mbar_init(&dp_full, 1);
-    tc::mbar_init(&p_ready, 8);
-    tc::mbar_init(&ds_ready, 8);
-    tc::mbar_init(&done, 1);
-    tc::mbar_init(&tail_full, 1);
-    tc::mbar_init(&drain, 1);
-    tc::fence_barrier_init();
-  }
-  if (warp == kMmaWarp) tc::tmem_alloc<512>(&tmem_slot);
+  if (threadIdx.x == 0) bwd_barriers(b);
+  if (warp == kMmaWarp) tc::tmem_alloc<512>(&b.tmem_slot);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = b.tmem_slot;
   KeyItem w;
   bool ok = true;
 
   if (warp == kLoadWarp) {
-    AttnRing<kRing> ring;
+    BwdLoader<DP, kA> qs{b, a_at, b.a_full, b.a_empty, status};
+    BwdLoader<DP, kB> dos{b, b_at, b.b_full, b.b_empty, status};
     uint32_t kv_parity = 0, tail_parity = 0;
-    // a tile of Q or dO; the rows behind a sequence's end become zeros before it counts as loaded
-    auto load = [&](const CUtensorMap* map, int hq, int i) {
-      ok = ok && attn_warp_wait(&ring_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
-      if (!ok) return;
-      unsigned char* const dst = ring_at + ring.slot * kTile;
-      const int rows = w.s.n - i * kTcBlock;
-      uint64_t* const bar = rows < kTcBlock ? &tail_full : &ring_full[ring.slot];
-      if (lane == 0) {
-        tc::mbar_arrive_expect_tx(bar, kTile);
-        attn_load_tile<DP>(dst, map, bar, hq, w.s.q0 + (long long)i * kTcBlock);
-      }
-      if (bar == &tail_full) {
-        ok = attn_warp_wait(&tail_full, tail_parity, status, kDevErrTimeoutBwd);
-        tail_parity ^= 1u;
-        if (!ok) return;
-        attn_clear_rows<DP>(dst, rows);
-        if (lane == 0) tc::mbar_arrive(&ring_full[ring.slot]);
-      }
-      ring.next();
-    };
     for (unsigned turn = 0; ok; ++turn) {
       const long long x = attn_item(turn, items);
       if (x < 0) break;
       if (!key_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
       auto load_kv = [&](int which, const CUtensorMap* map) {
-        ok = ok && attn_warp_wait(&kv_empty[which], kv_parity ^ 1u, status, kDevErrTimeoutBwd);
+        ok = ok && attn_warp_wait(&b.keep_empty[which], kv_parity ^ 1u, status, kDevErrTimeoutBwd);
         if (ok && lane == 0) {
-          tc::mbar_arrive_expect_tx(&kv_full[which], kTile);
-          attn_load_tile<DP>(kv + which * kTile, map, &kv_full[which], w.h, w.s.k0 + w.j0);
+          tc::mbar_arrive_expect_tx(&b.keep_full[which], kTile);
+          attn_load_tile<DP>(keep + which * kTile, map, &b.keep_full[which], w.h, w.s.k0 + w.j0);
         }
       };
       load_kv(0, &maps.k);
-      load(&maps.q, w.h * d.G, w.lo);
-      load_kv(1, &maps.v);
-      kv_parity ^= 1u;
       for (int g = 0; g < d.G && ok; ++g)
         for (int i = w.lo; i < w.hi && ok; ++i) {
-          if (g > 0 || i > w.lo) load(&maps.q, w.h * d.G + g, i);
-          load(&maps.dout, w.h * d.G + g, i);
+          const long long r0 = w.s.q0 + (long long)i * kTcBlock;
+          const int rows = w.s.n - i * kTcBlock;
+          ok = qs.load(&maps.q, w.h * d.G + g, r0, rows, true, tail_parity);
+          if (g == 0 && i == w.lo) load_kv(1, &maps.v);
+          ok = ok && dos.load(&maps.dout, w.h * d.G + g, r0, rows, true, tail_parity);
         }
+      kv_parity ^= 1u;
     }
-    if (!ok)  // after a wait that ran out, the copies under way end before the block does
-      for (int i = 0; i < kRing; ++i) {
-        tc::mbar_wait(&ring_full[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
-        ring.next();
-      }
+    if (!ok) {
+      qs.drain();
+      dos.drain();
+    }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
-      AttnRing<kRing> ring;  // of the next Q; its dO is one further
+      AttnRing<kA> qs;
+      AttnRing<kB> dos;
       uint32_t kv_parity = 0, parity = 0;
-      const uint32_t k_at = tc::smem_u32(kv), v_at = k_at + kTile, r_at = tc::smem_u32(ring_at);
+      const uint32_t k_at = tc::smem_u32(keep), v_at = k_at + kTile, q_at = tc::smem_u32(a_at), do_at = tc::smem_u32(b_at);
       auto wait = [&](uint64_t* bar, uint32_t p) {
         ok = ok && tc::mbar_wait(bar, p, status, kDevErrTimeoutBwd);
         tc::tc_fence_after();
@@ -154,50 +195,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (x < 0) break;
         if (!key_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
         const int steps = (w.hi - w.lo) * d.G;
-        wait(&kv_full[0], kv_parity);
-        if (wait(&ring_full[ring.slot], ring.parity)) {
-          attn_scores<DP>(tmem + kS, k_at, r_at + ring.slot * kTile);
-          tc::mma_commit(&s_full);
-          if (steps == 1) tc::mma_commit(&kv_empty[0]);
-        }
-        wait(&kv_full[1], kv_parity);
-        if (wait(&ring_full[ring.slot + 1], ring.parity)) {
-          attn_scores<DP>(tmem + kdP, v_at, r_at + (ring.slot + 1) * kTile);
-          tc::mma_commit(&dp_full);
-          if (steps == 1) tc::mma_commit(&kv_empty[1]);
-        }
+        auto scores = [&](bool last) {  // S^T of the next step
+          if (!wait(&b.a_full[qs.slot], qs.parity)) return;
+          attn_scores<DP>(tmem + kS, k_at, q_at + qs.slot * kTile);
+          tc::mma_commit(&b.s_full);
+          if (last) tc::mma_commit(&b.keep_empty[0]);
+        };
+        auto dscores = [&](bool last) {  // dP^T of the next step
+          if (!wait(&b.b_full[dos.slot], dos.parity)) return;
+          attn_scores<DP>(tmem + kdP, v_at, do_at + dos.slot * kTile);
+          tc::mma_commit(&b.dp_full);
+          if (last) tc::mma_commit(&b.keep_empty[1]);
+        };
+        if (wait(&b.keep_full[0], kv_parity)) scores(steps == 1);
+        if (wait(&b.keep_full[1], kv_parity)) dscores(steps == 1);
         kv_parity ^= 1u;
         for (int it = 0; it < steps && ok; ++it) {
-          const int q_slot = ring.slot;
-          const bool more = it + 1 < steps;
-          ring.next();
-          ring.next();
-          if (!wait(&p_ready, parity)) break;
-          attn_product<DP, 64>(tmem + kdV, tmem + kS, r_at + (q_slot + 1) * kTile, it > 0);
-          tc::mma_commit(&ring_empty[q_slot + 1]);
-          if (more) {
-            if (!wait(&ring_full[ring.slot], ring.parity)) break;
-            attn_scores<DP>(tmem + kS, k_at, r_at + ring.slot * kTile);
-            tc::mma_commit(&s_full);
-            if (it + 2 == steps) tc::mma_commit(&kv_empty[0]);
-          }
-          if (!wait(&ds_ready, parity)) break;
-          attn_product<DP, 64>(tmem + kdK, tmem + kdP, r_at + q_slot * kTile, it > 0);
-          tc::mma_commit(&ring_empty[q_slot]);
-          if (more) {
-            if (!wait(&ring_full[ring.slot + 1], ring.parity)) break;
-            attn_scores<DP>(tmem + kdP, v_at, r_at + (ring.slot + 1) * kTile);
-            tc::mma_commit(&dp_full);
-            if (it + 2 == steps) tc::mma_commit(&kv_empty[1]);
-          } else {
-            tc::mma_commit(&done);
-          }
+          const int q_slot = qs.slot, do_slot = dos.slot;
+          const bool more = it + 1 < steps, last = it + 2 == steps;
+          qs.next();
+          dos.next();
+          GDR_DELAY(45);
+          if (!wait(&b.p_ready, parity)) break;
+          attn_product<DP, 64>(tmem + kdV, tmem + kS, do_at + do_slot * kTile, it > 0);
+          tc::mma_commit(&b.b_empty[do_slot]);
+          if (more) scores(last);
+          GDR_DELAY(46);
+          if (!wait(&b.ds_ready[0], parity)) break;
+          attn_product<DP, 64>(tmem + kdK, tmem + kdP, q_at + q_slot * kTile, it > 0);
+          tc::mma_commit(&b.a_empty[q_slot]);
+          if (more)
+            dscores(last);
+          else
+            tc::mma_commit(&b.done);
           parity ^= 1u;
         }
       }
       if (!ok) {  // the products under way end before their memory is given back
-        tc::mma_commit(&drain);
-        tc::mbar_wait(&drain, 0, status, kDevErrTimeoutBwd);
+        tc::mma_commit(&b.drain);
+        tc::mbar_wait(&b.drain, 0, status, kDevErrTimeoutBwd);
       }
     }
     __syncwarp();
@@ -219,15 +255,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             dl[e] = on ? a.delta[at + r] : 0.f;
             if (ls[e] == -INFINITY) ls[e] = INFINITY;  // a query that sees nothing: e^-infinity
           }
-          ok = attn_warp_wait(&stat_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
+          ok = attn_warp_wait(&b.stat_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
           if (!ok) break;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            stat[ring.slot][0][32 * e + lane] = ls[e];
-            stat[ring.slot][1][32 * e + lane] = dl[e];
+            b.stat[ring.slot][0][32 * e + lane] = ls[e];
+            b.stat[ring.slot][1][32 * e + lane] = dl[e];
           }
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&stat_full[ring.slot]);
+          if (lane == 0) tc::mbar_arrive(&b.stat_full[ring.slot]);
           ring.next();
         }
       }
@@ -251,8 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long whole_to = d.window ? (long long)w.j0 - off + d.window : (1ll << 40);
       for (int g = 0; g < d.G && ok; ++g)
         for (int i = w.lo; i < w.hi; ++i) {
-          ok = attn_warp_wait(&stat_full[ring.slot], ring.parity, status, kDevErrTimeoutBwd);
-          ok = ok && attn_warp_wait(&s_full, parity, status, kDevErrTimeoutBwd);
+          ok = attn_warp_wait(&b.stat_full[ring.slot], ring.parity, status, kDevErrTimeoutBwd);
+          ok = ok && attn_warp_wait(&b.s_full, parity, status, kDevErrTimeoutBwd);
           if (!ok) break;
           tc::tc_fence_after();
           const int i0 = i * kTcBlock;
@@ -260,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_ld32(s_col, p);
           tc::tmem_ld32(s_col + 32, p + 32);
           tc::tmem_wait_ld();
-          const float* ls = stat[ring.slot][0] + col;
+          const float* ls = b.stat[ring.slot][0] + col;
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
             const float4 l4 = *reinterpret_cast<const float4*>(ls + e);
@@ -280,14 +316,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tc_fence_before();
           __syncwarp();
           GDR_DELAY(41);
-          if (lane == 0) tc::mbar_arrive(&p_ready);
-          ok = attn_warp_wait(&dp_full, parity, status, kDevErrTimeoutBwd);
+          if (lane == 0) tc::mbar_arrive(&b.p_ready);
+          ok = attn_warp_wait(&b.dp_full, parity, status, kDevErrTimeoutBwd);
           if (!ok) break;
           tc::tc_fence_after();
           tc::tmem_ld32(dp_col, dp);
           tc::tmem_ld32(dp_col + 32, dp + 32);
           tc::tmem_wait_ld();
-          const float* dl = stat[ring.slot][1] + col;
+          const float* dl = b.stat[ring.slot][1] + col;
 #pragma unroll
           for (int e = 0; e < 64; e += 4) {
             const float4 d4 = *reinterpret_cast<const float4*>(dl + e);
@@ -302,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           GDR_DELAY(42);
           if (lane == 0) {
-            tc::mbar_arrive(&ds_ready);
-            tc::mbar_arrive(&stat_empty[ring.slot]);
+            tc::mbar_arrive(&b.ds_ready[0]);
+            tc::mbar_arrive(&b.stat_empty[ring.slot]);
           }
           parity ^= 1u;
           ring.next();
@@ -311,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const bool any = w.lo < w.hi;
       if (any) {
-        ok = attn_warp_wait(&done, done_parity, status, kDevErrTimeoutBwd);
+        ok = attn_warp_wait(&b.done, done_parity, status, kDevErrTimeoutBwd);
         done_parity ^= 1u;
         if (!ok) break;
         tc::tc_fence_after();
@@ -349,95 +385,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_dq_tc_kernel(const __grid_constant__ BwdMaps maps, AttnDims d, AttnTiles tiles, unsigned items, AttnBwdArgs a) {
   constexpr uint32_t kTile = attn_tile_bytes<DP>();
   constexpr uint32_t kS = 0, kdP = 128, kdQ = 256, kdS = 384;  // dS: two places of 64 columns
-  extern __shared__ unsigned char raw[];
-  __shared__ uint64_t q_full[2], q_empty[2], ring_full[kRing], ring_empty[kRing], s_full, dp_full, s_free, dp_free, ds_ready, done, tail_full, drain;
-  __shared__ uint32_t tmem_slot;
-  unsigned char* const qd = align1024(raw);  // Q, dO
-  unsigned char* const ring_at = qd + 2 * kTile;  // K, V, K, V
+  unsigned char* const keep = bwd_raw;  // Q, dO
+  unsigned char* const a_at = keep + 2 * kTile;
+  unsigned char* const b_at = a_at + kA * kTile;
+  BwdShared& b = *reinterpret_cast<BwdShared*>(b_at + kB * kTile);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* const status = a.status;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&q_full[i], 1);
-      tc::mbar_init(&q_empty[i], 1);
-    }
-    for (int i = 0; i < kRing; ++i) {
-      tc::mbar_init(&ring_full[i], 1);
-      tc::mbar_init(&ring_empty[i], 1);
-    }
-    tc::mbar_init(&s_full, 1);
-    tc::mbar_init(&dp_full, 1);
-    tc::mbar_init(&s_free, 8);
-    tc::mbar_init(&dp_free, 8);
-    tc::mbar_init(&ds_ready, 8);
-    tc::mbar_init(&done, 1);
-    tc::mbar_init(&tail_full, 1);
-    tc::mbar_init(&drain, 1);
-    tc::fence_barrier_init();
-  }
-  if (warp == kMmaWarp) tc::tmem_alloc<512>(&tmem_slot);
+  if (threadIdx.x == 0) bwd_barriers(b);
+  if (warp == kMmaWarp) tc::tmem_alloc<512>(&b.tmem_slot);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = b.tmem_slot;
   QueryItem w;
   bool ok = true;
 
   if (warp == kLoadWarp) {
-    AttnRing<kRing> ring;
+    BwdLoader<DP, kA> ks{b, a_at, b.a_full, b.a_empty, status};
+    BwdLoader<DP, kB> vs{b, b_at, b.b_full, b.b_empty, status};
     uint32_t q_parity = 0, tail_parity = 0;
-    // a tile of K or V; the keys behind a sequence's end become zeros before it counts as loaded (values are not summed here)
-    auto load = [&](const CUtensorMap* map, int j, bool key) {
-      ok = ok && attn_warp_wait(&ring_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
-      if (!ok) return;
-      unsigned char* const dst = ring_at + ring.slot * kTile;
-      const int rows = w.s.m - j * kTcBlock;
-      uint64_t* const bar = key && rows < kTcBlock ? &tail_full : &ring_full[ring.slot];
-      if (lane == 0) {
-        tc::mbar_arrive_expect_tx(bar, kTile);
-        attn_load_tile<DP>(dst, map, bar, w.h / d.G, w.s.k0 + (long long)j * kTcBlock);
-      }
-      if (bar == &tail_full) {
-        ok = attn_warp_wait(&tail_full, tail_parity, status, kDevErrTimeoutBwd);
-        tail_parity ^= 1u;
-        if (!ok) return;
-        attn_clear_rows<DP>(dst, rows);
-        if (lane == 0) tc::mbar_arrive(&ring_full[ring.slot]);
-      }
-      ring.next();
-    };
     for (unsigned turn = 0; ok; ++turn) {
       const long long x = attn_item(turn, items);
       if (x < 0) break;
       if (!query_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
       auto load_q = [&](int which, const CUtensorMap* map) {
-        ok = ok && attn_warp_wait(&q_empty[which], q_parity ^ 1u, status, kDevErrTimeoutBwd);
+        ok = ok && attn_warp_wait(&b.keep_empty[which], q_parity ^ 1u, status, kDevErrTimeoutBwd);
         if (ok && lane == 0) {
-          tc::mbar_arrive_expect_tx(&q_full[which], kTile);
-          attn_load_tile<DP>(qd + which * kTile, map, &q_full[which], w.h, w.s.q0 + w.i0);
+          tc::mbar_arrive_expect_tx(&b.keep_full[which], kTile);
+          attn_load_tile<DP>(keep + which * kTile, map, &b.keep_full[which], w.h, w.s.q0 + w.i0);
         }
       };
       load_q(0, &maps.q);
-      load(&maps.k, w.lo, true);
-      load_q(1, &maps.dout);
+      for (int j = w.lo; j < w.hi && ok; ++j) {
+        const long long r0 = w.s.k0 + (long long)j * kTcBlock;
+        const int rows = w.s.m - j * kTcBlock;
+        ok = ks.load(&maps.k, w.h / d.G, r0, rows, true, tail_parity);
+        if (j == w.lo) load_q(1, &maps.dout);
+        ok = ok && vs.load(&maps.v, w.h / d.G, r0, rows, false, tail_parity);  // values are not summed here
+      }
       q_parity ^= 1u;
-      load(&maps.v, w.lo, false);
-      for (int j = w.lo + 1; j < w.hi && ok; ++j) {
-        load(&maps.k, j, true);
-        load(&maps.v, j, false);
-      }
     }
-    if (!ok)  // after a wait that ran out, the copies under way end before the block does
-      for (int i = 0; i < kRing; ++i) {
-        tc::mbar_wait(&ring_full[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
-        ring.next();
-      }
+    if (!ok) {
+      ks.drain();
+      vs.drain();
+    }
   } else if (warp == kMmaWarp) {
     if (lane == 0) {
-      AttnRing<kRing> ring;  // of the next K; its V is one further
-      uint32_t q_parity = 0, free_parity = 1, parity = 0;  // s_free, dp_free: of the tile before
-      uint32_t place = 0;
-      const uint32_t q_at = tc::smem_u32(qd), do_at = q_at + kTile, r_at = tc::smem_u32(ring_at);
+      AttnRing<kA> ks;
+      AttnRing<kB> vs;
+      AttnRing<2> place;  // of dS
+      uint32_t q_parity = 0, free_parity = 1;  // s_free, dp_free: of the step before
+      const uint32_t q_at = tc::smem_u32(keep), do_at = q_at + kTile, k_at = tc::smem_u32(a_at), v_at = tc::smem_u32(b_at);
       auto wait = [&](uint64_t* bar, uint32_t p) {
         ok = ok && tc::mbar_wait(bar, p, status, kDevErrTimeoutBwd);
         tc::tc_fence_after();
@@ -449,41 +447,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!query_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
         const int steps = w.hi - w.lo;
         auto scores = [&](int it) {  // S and dP of a step
-          if (it == 0) wait(&q_full[0], q_parity);
-          wait(&ring_full[ring.slot], ring.parity);
-          if (!wait(&s_free, free_parity)) return;
-          attn_scores<DP>(tmem + kS, q_at, r_at + ring.slot * kTile);
-          tc::mma_commit(&s_full);
-          if (it + 1 == steps) tc::mma_commit(&q_empty[0]);
-          if (it == 0) wait(&q_full[1], q_parity);
-          wait(&ring_full[ring.slot + 1], ring.parity);
-          if (!wait(&dp_free, free_parity)) return;
-          attn_scores<DP>(tmem + kdP, do_at, r_at + (ring.slot + 1) * kTile);
-          tc::mma_commit(&dp_full);
-          tc::mma_commit(&ring_empty[ring.slot + 1]);
-          if (it + 1 == steps) tc::mma_commit(&q_empty[1]);
+          if (it == 0) wait(&b.keep_full[0], q_parity);
+          wait(&b.a_full[ks.slot], ks.parity);
+          if (!wait(&b.s_free, free_parity)) return;
+          attn_scores<DP>(tmem + kS, q_at, k_at + ks.slot * kTile);
+          tc::mma_commit(&b.s_full);
+          if (it + 1 == steps) tc::mma_commit(&b.keep_empty[0]);
+          if (it == 0) wait(&b.keep_full[1], q_parity);
+          wait(&b.b_full[vs.slot], vs.parity);
+          if (!wait(&b.dp_free, free_parity)) return;
+          attn_scores<DP>(tmem + kdP, do_at, v_at + vs.slot * kTile);
+          tc::mma_commit(&b.dp_full);
+          tc::mma_commit(&b.b_empty[vs.slot]);
+          if (it + 1 == steps) tc::mma_commit(&b.keep_empty[1]);
           free_parity ^= 1u;
-          ring.next();
-          ring.next();
+          ks.next();
+          vs.next();
         };
-        int k_slot = ring.slot;
+        int k_slot = ks.slot;
         scores(0);
         q_parity ^= 1u;
         for (int it = 0; it < steps && ok; ++it) {
-          const int next_slot = ring.slot;
+          const int next_slot = ks.slot;
           if (it + 1 < steps) scores(it + 1);
-          if (!wait(&ds_ready, parity)) break;
-          attn_product<DP>(tmem + kdQ, tmem + kdS + 64 * place, r_at + k_slot * kTile, it > 0);
-          tc::mma_commit(&ring_empty[k_slot]);
-          if (it + 1 == steps) tc::mma_commit(&done);
+          // (a barrier for each place: the step after this one may be through before this wait begins)
+          GDR_DELAY(44);
+          if (!wait(&b.ds_ready[place.slot], place.parity)) break;
+          attn_product<DP>(tmem + kdQ, tmem + kdS + 64 * place.slot, k_at + k_slot * kTile, it > 0);
+          tc::mma_commit(&b.a_empty[k_slot]);
+          if (it + 1 == steps) tc::mma_commit(&b.done);
           k_slot = next_slot;
-          parity ^= 1u;
-          place ^= 1u;
+          place.next();
         }
       }
       if (!ok) {  // the products under way end before their memory is given back
-        tc::mma_commit(&drain);
-        tc::mbar_wait(&drain, 0, status, kDevErrTimeoutBwd);
+        tc::mma_commit(&b.drain);
+        tc::mbar_wait(&b.drain, 0, status, kDevErrTimeoutBwd);
       }
     }
     __syncwarp();
@@ -507,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i_last = w.i0 + kTcBlock - 1;
       const int whole_to = d.causal ? min(w.s.m, w.i0 + off + 1) : w.s.m, whole_from = d.window ? i_last + off - d.window + 1 : 0;
       for (int j = w.lo; j < w.hi; ++j) {
-        ok = attn_warp_wait(&s_full, parity, status, kDevErrTimeoutBwd);
+        ok = attn_warp_wait(&b.s_full, parity, status, kDevErrTimeoutBwd);
         if (!ok) break;
         tc::tc_fence_after();
         float p[64], dp[64];
@@ -516,12 +515,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_wait_ld();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&s_free);
+        if (lane == 0) tc::mbar_arrive(&b.s_free);
 #pragma unroll
         for (int e = 0; e < 64; ++e) p[e] = ex2f(fmaf(p[e], c, -ls));
         const int j0 = j * kTcBlock;
         const bool partial = j0 + kTcBlock > whole_to || j0 < whole_from;
-        ok = attn_warp_wait(&dp_full, parity, status, kDevErrTimeoutBwd);
+        ok = attn_warp_wait(&b.dp_full, parity, status, kDevErrTimeoutBwd);
         if (!ok) break;
         tc::tc_fence_after();
         tc::tmem_ld32(dp_col, dp);
@@ -529,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_wait_ld();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&dp_free);
+        if (lane == 0) tc::mbar_arrive(&b.dp_free);
 #pragma unroll
         for (int e = 0; e < 64; ++e) dp[e] = p[e] * (dp[e] - dl);
         if (partial) {
@@ -542,14 +541,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_before();
         __syncwarp();
         GDR_DELAY(43);
-        if (lane == 0) tc::mbar_arrive(&ds_ready);
+        if (lane == 0) tc::mbar_arrive(&b.ds_ready[place]);
         parity ^= 1u;
         place ^= 1u;
       }
       if (!ok) break;
       const bool any = w.lo < w.hi;
       if (any) {
-        ok = attn_warp_wait(&done, done_parity, status, kDevErrTimeoutBwd);
+        ok = attn_warp_wait(&b.done, done_parity, status, kDevErrTimeoutBwd);
         done_parity ^= 1u;
         if (!ok) break;
         tc::tc_fence_after();
