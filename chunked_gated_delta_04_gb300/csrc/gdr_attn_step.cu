@@ -2,24 +2,29 @@
 // (include/gdr_attn.h).
 //
 // The step reads the visible part of the cache once and is bound by that.  The work is the list of all tiles of 64
-// (bf16) or 32 (fp32) positions of all rows and key heads, one behind the other; a launch of two blocks per SM cuts the list into
-// equal parts, so that one long sequence, many short ones and any mixture of them load every SM alike.  Which rows have
-// how many tiles is on the device only (lengths): every block sums them up itself.  A block takes its tiles in order, with the
-// copies of the next two under way (cp.async; a step's rows are 256-byte pieces, wherever their page lies), and keeps
-// the running maximum m, sum l and O of a (row, key head), for up to 16 query heads that share it:
+// (bf16) or 32 (fp32) positions of all rows and key heads, one behind the other, each (row, key head) with one more place for what
+// beginning and ending it costs; a launch of two blocks per SM cuts the list into equal parts, so that one long sequence, many short ones and any mixture of them load every SM alike.  Which rows have
+// how many tiles is on the device only (lengths): every block sums them up itself.  A block takes its tiles in order.  One warp
+// has TMA bring them into a ring of three stages (128 KB per SM under way): boxes of as many positions of a page as a power of two
+// divides its size by, at most a tile.  Four warps keep the running maximum m, sum l and O of a (row, key head), for up to 16
+// query heads that share it:
 //   bf16: mma.m16n8k16, query heads as the rows, so that P's accumulator is the next product's operand; a warp takes 16 of a
 //         tile's positions.  The products are small beside the copies (16 rows of 16 positions of 128 features: 32 instructions).
 //   fp32: on the FMA pipes, 4 lanes per position for S, 4 features per lane for O.
 // A (row, key head) that lies within one block is finished there; of the others each block leaves its part (m, l, O), and a
-// second launch adds them in order.  The new token's key and value go from the call's inputs to shared memory and the cache.
+// second launch adds them in order.  Short rows change every tile: whatever a unit needs (its queries, its new token) comes
+// through the ring with its tiles, and its warps' parts are added in the stage that its last tile had.  The new token's key and value go from the call's inputs to shared memory and the cache;
+// what a page holds outside a row's visible positions is replaced by zeros there.
 #include <cmath>
+#include <cstring>
 
 #include "gdr_attn.cuh"
+#include "tc_primitives.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 128;  // that compute; a warp more copies
 constexpr int kWarps = kThreads / 32;
 constexpr int kStages = 3;
 constexpr int kHeads = 16;  // query heads of a unit
@@ -31,14 +36,29 @@ struct StepDims {
   float scale;
   long long ld_q, ld_k, ld_v;
   int vec;  // q, k, v by 16 bytes
+  int box;  // positions of a copy
 };
 
-// Positions that a tile covers, and the tile of a row's first visible position.
+struct StepMaps {
+  CUtensorMap k, v;
+};
+
+// A stage: K then V, each in slabs of 128 bytes of every position's features, 16-byte chunks swizzled by the position.
+template <typename IT> constexpr int slab_features() { return 128 / (int)sizeof(IT); }
+
+// Positions that a tile covers.
 template <typename IT> constexpr int tile_keys() { return sizeof(IT) == 2 ? 64 : 32; }
+template <typename IT> constexpr int slab_bytes() { return tile_keys<IT>() * 128; }
+// Byte offset of 16-byte chunk `c` of position `r` in a K or V tile.
+template <typename IT>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return (uint32_t)((c >> 3) * slab_bytes<IT>() + r * 128 + (((c ^ r) & 7) << 4));
+}
 
 // The visible positions lo .. len of a row and its tiles; false: the row is skipped.
 struct Row {
   int len, lo, tile0, tiles;
+  __device__ __forceinline__ int places() const { return tiles ? tiles + 1 : 0; }  // in the list, of each unit
 };
 template <int KT>
 __device__ __forceinline__ Row row_of(const StepDims& d, const int32_t* lengths, int b) {
@@ -51,29 +71,31 @@ __device__ __forceinline__ Row row_of(const StepDims& d, const int32_t* lengths,
   return r;
 }
 
-// Tiles of the rows before thread t's rows (B cut into kThreads runs), and of all: prefix[kThreads + 1] in shared memory.
+// Places of one unit of the rows before thread t's rows (B cut into kThreads runs), and of all: prefix[kThreads + 1] in shared memory.
 template <int KT>
 __device__ __forceinline__ void sum_rows(const StepDims& d, const int32_t* lengths, long long* prefix) {
   const int tid = threadIdx.x, run = (d.B + kThreads - 1) / kThreads;
+  const bool on = tid < kThreads;
   long long sum = 0;
-  for (int b = tid * run; b < min(d.B, (tid + 1) * run); ++b) sum += row_of<KT>(d, lengths, b).tiles;
+  if (on)
+    for (int b = tid * run; b < min(d.B, (tid + 1) * run); ++b) sum += row_of<KT>(d, lengths, b).places();
   long long v = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, v, o);
     if ((tid & 31) >= o) v += y;
   }
-  prefix[tid + 1] = v;  // within the warp
+  if (on) prefix[tid + 1] = v;  // within the warp
   if (tid == 0) prefix[0] = 0;
   __syncthreads();
   long long before = 0;
-  for (int w = 0; w < (tid >> 5); ++w) before += prefix[32 * (w + 1)];
+  for (int w = 0; w < (tid >> 5) && on; ++w) before += prefix[32 * (w + 1)];
   __syncthreads();
-  prefix[tid + 1] = v + before;
+  if (on) prefix[tid + 1] = v + before;
   __syncthreads();
 }
 
-// Where a position of the flat list of tiles lies: row, unit of the row (key head and block of query heads), tile of the unit.
+// A place in the list: row, unit of the row (key head and block of query heads), tile of the unit (-1: the place in front of it).
 template <int KT>
 struct Cursor {
   int b, unit, tile;
@@ -87,21 +109,29 @@ struct Cursor {
     long long rest = at - prefix[lo] * units;
     b = lo * ((d.B + kThreads - 1) / kThreads);
     row = row_of<KT>(d, lengths, b);
-    while (rest >= (long long)row.tiles * units) {
-      rest -= (long long)row.tiles * units;
+    while (rest >= (long long)row.places() * units) {
+      rest -= (long long)row.places() * units;
       row = row_of<KT>(d, lengths, ++b);
     }
-    unit = (int)(rest / row.tiles);
-    tile = (int)(rest % row.tiles);
+    unit = (int)(rest / row.places());
+    tile = (int)(rest % row.places()) - 1;
   }
-  // The next tile, of which there is one.
-  __device__ __forceinline__ void next(const StepDims& d, const int32_t* lengths, int units) {
-    if (++tile < row.tiles) return;
+  // The next tile, if there is one before place `end`; `at` is the place it is at.
+  __device__ __forceinline__ bool next(const StepDims& d, const int32_t* lengths, int units, long long* at, long long end) {
+    const bool within = tile + 1 < row.tiles;
+    *at += within ? 1 : 2;
+    if (*at >= end) return false;
+    if (within) {
+      ++tile;
+      return true;
+    }
     tile = 0;
-    if (++unit < units) return;
-    unit = 0;
-    do row = row_of<KT>(d, lengths, ++b);
-    while (row.tiles == 0);
+    if (++unit == units) {
+      unit = 0;
+      do row = row_of<KT>(d, lengths, ++b);
+      while (row.tiles == 0);
+    }
+    return true;
   }
 };
 
@@ -121,35 +151,38 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 16 bytes, or zeros (`bytes` 0, nothing is read), past the L1: a cache is read once.
-__device__ __forceinline__ void copy_async_l2(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+// A box of a cache: features f .., one head, positions place .. of a page.
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, uint64_t* bar, int f, int h, int place, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(f), "r"(h), "r"(place), "r"(page), "r"(smem_addr(bar))
+      : "memory");
 }
 
 // The larger, or a NaN where there is one: it has to reach the row's result.
 __device__ __forceinline__ float max_nan(float a, float b) { return b > a || b != b ? b : a; }
 
+// A bounded wait by a whole warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, uint32_t* status) {
+  return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, status, kDevErrTimeoutFwd));
+}
+
 // Running softmax of a warp's part of the tiles, products on the tensor cores.
 template <int DP>
 struct EngineBf16 {
-  static constexpr int kRows = kHeads;  // of the accumulator in shared memory
+  static constexpr int kBlocks = 2;     // per SM
   uint32_t qa[DP / 16][4];
   float O[DP / 8][4], m[2], l[2];  // heads lane / 4 and lane / 4 + 8; m in units of S
 
-  __device__ __forceinline__ void begin(const __nv_bfloat16* q, int heads, const StepDims& d) {
+  __device__ __forceinline__ void begin(const __nv_bfloat16* q, int heads, int D) {  // q: shared memory [heads][D]
     const int lane = threadIdx.x & 31, g = lane >> 2, c = 2 * (lane & 3);
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = g + 8 * (i & 1), f = 16 * kk + c + 8 * (i >> 1);
-        uint32_t w = 0;
-        if (r < heads && f < d.D) {  // D is even
-          const __nv_bfloat16* at = q + (long long)r * d.D + f;
-          const __nv_bfloat162 two = __halves2bfloat162(at[0], at[1]);
-          w = *reinterpret_cast<const uint32_t*>(&two);
-        }
-        qa[kk][i] = w;
+        qa[kk][i] = r < heads && f < D ? *reinterpret_cast<const uint32_t*>(q + r * D + f) : 0u;
       }
 #pragma unroll
     for (int n = 0; n < DP / 8; ++n)
@@ -159,19 +192,24 @@ struct EngineBf16 {
     l[0] = l[1] = 0.f;
   }
 
-  // The warp's 16 positions of a tile whose first position is p0: K and V rows of DP + 8 elements.
-  __device__ __forceinline__ void tile(const __nv_bfloat16* K, const __nv_bfloat16* V, int p0, const Row& row, float c, int) {
-    constexpr int S = DP + 8;
+  // The warp's 16 positions of a tile whose first position is p0.
+  __device__ __forceinline__ void tile(const unsigned char* K, const unsigned char* V, int p0, const Row& row, float c) {
+    using IT = __nv_bfloat16;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const uint32_t ka = smem_addr(K) + 2 * ((16 * w + (lane & 7) + 8 * (lane >> 4)) * S + 8 * (lane >> 3 & 1));
-    float s[2][4] = {};
+    const uint32_t ka = smem_addr(K);
+    const int kr = 16 * w + (lane & 7) + 8 * (lane >> 4);
+    float s[2][4] = {}, s2[2][4] = {};  // even and odd steps: two chains of products at a time are too few
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
       uint32_t b[4];
-      ldmatrix4(b, ka + 32 * kk);
-      mma16816(s[0], qa[kk], b[0], b[1]);
-      mma16816(s[1], qa[kk], b[2], b[3]);
+      ldmatrix4(b, ka + chunk_at<IT>(kr, 2 * kk + (lane >> 3 & 1)));
+      mma16816(kk & 1 ? s2[0] : s[0], qa[kk], b[0], b[1]);
+      mma16816(kk & 1 ? s2[1] : s[1], qa[kk], b[2], b[3]);
     }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] += s2[n][i];
     const int at = p0 + 16 * w + 2 * (lane & 3);
     float top[2] = {m[0], m[1]};
 #pragma unroll
@@ -197,17 +235,19 @@ struct EngineBf16 {
         pa[2 * n + r] = pack_bf16(p0_, p1_);
       }
       l[r] = fmaf(l[r], f, sum);
+      if (__any_sync(0xffffffffu, f != 1.f))
 #pragma unroll
-      for (int n = 0; n < DP / 8; ++n) {
-        O[n][2 * r] *= f;
-        O[n][2 * r + 1] *= f;
-      }
+        for (int n = 0; n < DP / 8; ++n) {
+          O[n][2 * r] *= f;
+          O[n][2 * r + 1] *= f;
+        }
     }
-    const uint32_t va = smem_addr(V) + 2 * ((16 * w + (lane & 15)) * S + 8 * (lane >> 4));
+    const uint32_t va = smem_addr(V);
+    const int vr = 16 * w + (lane & 15);
 #pragma unroll
     for (int n = 0; n < DP / 16; ++n) {
       uint32_t b[4];
-      ldmatrix4t(b, va + 32 * n);
+      ldmatrix4t(b, va + chunk_at<IT>(vr, 2 * n + (lane >> 4)));
       mma16816(O[2 * n], pa, b[0], b[1]);
       mma16816(O[2 * n + 1], pa, b[2], b[3]);
     }
@@ -225,22 +265,18 @@ struct EngineBf16 {
       }
     }
   }
-  // acc[head][feature] = (first ? 0 : acc) + O f(head).
+  // acc[head][feature] = O f(head) of the heads.
   template <typename F>
-  __device__ __forceinline__ void add(float* acc, bool first, int, F f) {
+  __device__ __forceinline__ void put(float* acc, int heads, F f) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int head = (lane >> 2) + 8 * r;
+      if (head >= heads) continue;
       const float by = f(head);
 #pragma unroll
-      for (int n = 0; n < DP / 8; ++n) {
-        float2* at = reinterpret_cast<float2*>(acc + head * DP + 8 * n + 2 * (lane & 3));
-        float2 v = first ? make_float2(0.f, 0.f) : *at;
-        v.x = fmaf(O[n][2 * r], by, v.x);
-        v.y = fmaf(O[n][2 * r + 1], by, v.y);
-        *at = v;
-      }
+      for (int n = 0; n < DP / 8; ++n)
+        *reinterpret_cast<float2*>(acc + head * DP + 8 * n + 2 * (lane & 3)) = make_float2(O[n][2 * r] * by, O[n][2 * r + 1] * by);
     }
   }
 };
@@ -248,13 +284,16 @@ struct EngineBf16 {
 // The same in fp32; NH: query heads that it is built for (at least the unit's).
 template <int DP, int NH>
 struct EngineF32 {
-  static constexpr int kRows = NH;
+  static constexpr int kBlocks = NH == kHeads ? 1 : 2;
   static constexpr int F = DP / 32;  // features of O per lane: F lane ..
-  const float* q;                    // shared memory [NH][DP], zeros behind the heads and features
+  const float* q;                    // shared memory [heads][D]
+  int heads, D;
   float O[NH][F], m[NH], l[NH];
 
-  __device__ __forceinline__ void begin(const float* from, int, const StepDims&) {
+  __device__ __forceinline__ void begin(const float* from, int heads_, int D_) {
     q = from;
+    heads = heads_;
+    D = D_;
 #pragma unroll
     for (int r = 0; r < NH; ++r) {
 #pragma unroll
@@ -263,20 +302,20 @@ struct EngineF32 {
       l[r] = 0.f;
     }
   }
-  // The warp's 8 positions of a tile: K and V rows of DP + 4 elements.
-  __device__ __forceinline__ void tile(const float* K, const float* V, int p0, const Row& row, float c, int) {
-    constexpr int S = DP + 4;
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const float* kr = K + (8 * w + (lane >> 2)) * S;
+  // The warp's 8 positions of a tile.
+  __device__ __forceinline__ void tile(const unsigned char* K, const unsigned char* V, int p0, const Row& row, float c) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, kr = 8 * w + (lane >> 2);
     float s[NH];
 #pragma unroll
     for (int r = 0; r < NH; ++r) s[r] = 0.f;
 #pragma unroll
     for (int k = 0; k < DP; k += 16) {
-      const float4 a = *reinterpret_cast<const float4*>(kr + k + 4 * (lane & 3));
+      if (k >= D) break;
+      const float4 a = *reinterpret_cast<const float4*>(K + chunk_at<float>(kr, k / 4 + (lane & 3)));
 #pragma unroll
       for (int r = 0; r < NH; ++r) {
-        const float4 b = *reinterpret_cast<const float4*>(q + r * DP + k + 4 * (lane & 3));
+        // (heads behind the unit's last are the last one's copies, whose results are not used)
+        const float4 b = *reinterpret_cast<const float4*>(q + min(r, heads - 1) * D + k + 4 * (lane & 3));
         s[r] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, s[r]))));
       }
     }
@@ -301,7 +340,8 @@ struct EngineF32 {
     for (int j = 0; j < 8; ++j) {
       float v[F];
 #pragma unroll
-      for (int i = 0; i < F; ++i) v[i] = V[(8 * w + j) * S + F * lane + i];
+      for (int i = 0; i < F; ++i)
+        v[i] = reinterpret_cast<const float*>(V + chunk_at<float>(8 * w + j, F * lane / 4))[F * lane % 4 + i];
 #pragma unroll
       for (int r = 0; r < NH; ++r) {
         const float pj = __shfl_sync(0xffffffffu, s[r], 4 * j);
@@ -322,233 +362,294 @@ struct EngineF32 {
     }
   }
   template <typename Fn>
-  __device__ __forceinline__ void add(float* acc, bool first, int, Fn f) {
+  __device__ __forceinline__ void put(float* acc, int, Fn f) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int r = 0; r < NH; ++r) {
+      if (r >= heads) break;
       const float by = f(r);
 #pragma unroll
-      for (int i = 0; i < F; ++i) {
-        float* at = acc + r * DP + F * lane + i;
-        *at = fmaf(O[r][i], by, first ? 0.f : *at);
-      }
+      for (int i = 0; i < F; ++i) acc[r * DP + F * lane + i] = O[r][i] * by;
     }
   }
 };
 
 template <typename IT, int DP>
-constexpr int row_elements() { return DP + 16 / (int)sizeof(IT); }
+constexpr size_t stage_bytes() { return 2 * sizeof(IT) * tile_keys<IT>() * DP; }
+// Beside a stage: the queries of the unit that begins with its tile, and the new token of the one that ends with it.
 template <typename IT, int DP>
-constexpr size_t stage_bytes() { return 2 * sizeof(IT) * tile_keys<IT>() * row_elements<IT, DP>(); }
-template <typename IT, int DP>  // the stages, the accumulator, fp32: the queries
+constexpr size_t side_bytes(int rows) { return sizeof(IT) * DP * (rows + 2); }
+template <typename IT, int DP>  // room to align, then the stages and what is beside them; fp32: the queries of the unit in work
 constexpr size_t step_smem(int rows) {
-  return kStages * stage_bytes<IT, DP>() + sizeof(float) * rows * DP * (sizeof(IT) == 4 ? 2 : 1);
+  return 1024 + kStages * (stage_bytes<IT, DP>() + side_bytes<IT, DP>(rows)) + (sizeof(IT) == 4 ? sizeof(IT) * DP * rows : 0);
 }
 // A part: O [kHeads][DP], m [kHeads], l [kHeads] (l < 0: the row needs a page outside the pool).
 template <int DP>
 constexpr int part_floats() { return kHeads * (DP + 2); }
 
 template <typename IT, int DP, typename Engine>
-__global__ void __launch_bounds__(kThreads) attn_step_kernel(StepDims d, const IT* __restrict__ q, const IT* __restrict__ k,
-                                                             const IT* __restrict__ v, IT* __restrict__ k_cache, IT* __restrict__ v_cache,
-                                                             const int32_t* __restrict__ table, const int32_t* __restrict__ lengths,
-                                                             IT* __restrict__ o, float* __restrict__ parts) {
-  constexpr int KT = tile_keys<IT>(), S = row_elements<IT, DP>(), N = 16 / (int)sizeof(IT);
-  extern __shared__ __align__(16) unsigned char smem[];
+__global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
+    attn_step_kernel(const __grid_constant__ StepMaps maps, StepDims d, const IT* __restrict__ q, const IT* __restrict__ k,
+                     const IT* __restrict__ v, IT* __restrict__ k_cache, IT* __restrict__ v_cache, const int32_t* __restrict__ table,
+                     const int32_t* __restrict__ lengths, IT* __restrict__ o, int2* __restrict__ spans, float* __restrict__ parts,
+                     uint32_t* __restrict__ status) {
+  constexpr int KT = tile_keys<IT>(), N = 16 / (int)sizeof(IT), kSlabs = DP / slab_features<IT>();
+  constexpr uint32_t kTileBytes = stage_bytes<IT, DP>() / 2;
+  extern __shared__ unsigned char raw[];
   __shared__ long long prefix[kThreads + 1];
-  __shared__ float ms[kWarps][kHeads], ls[kWarps][kHeads];
-  IT* const stages = reinterpret_cast<IT*>(smem);
-  float* const acc = reinterpret_cast<float*>(smem + kStages * stage_bytes<IT, DP>());
-  const int tid = threadIdx.x, warp = tid >> 5, units = d.Hk * d.HB;
-  sum_rows<KT>(d, lengths, prefix);
+  __shared__ float ms[2][kWarps][kHeads], ls[2][kWarps][kHeads];
+  __shared__ uint64_t full[kStages], empty[kStages];
+  __shared__ int stage_bad[kStages], stage_page[kStages];  // the page that the new token goes to, or -1
+  unsigned char* const stages = (unsigned char*)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, units = d.Hk * d.HB, rows = min(d.G, kHeads);
+  // new key, new value, queries
+  auto side = [&](int stage) { return reinterpret_cast<IT*>(stages + kStages * stage_bytes<IT, DP>() + stage * side_bytes<IT, DP>(rows)); };
+  asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up, and waits
+  if (blockIdx.x == 0 && tid == 0) *status = 0;  // (a wait that runs out sets it two seconds later)
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], kWarps);
+    }
+    tc::fence_barrier_init();
+  }
+  sum_rows<KT>(d, lengths, prefix);  // its barriers order what is above, too
   const long long total = prefix[kThreads] * units;
-  const long long blocks = min((long long)gridDim.x, total);  // that have a tile
+  // no more blocks than places: of the blocks between those that have a unit's first and last tile, each has some of its tiles
+  const long long blocks = min((long long)gridDim.x, total);
   if (blockIdx.x >= blocks) return;
   const long long start = total * blockIdx.x / blocks, end = total * (blockIdx.x + 1) / blocks;
+  Cursor<KT> here;
+  here.seek(d, lengths, prefix, units, start);
+  long long at = start;
+  if (here.tile < 0 && !here.next(d, lengths, units, &at, end)) return;
+  long long count = 0;  // tiles so far
+  int stage = 0;
+  uint32_t parity = 0;
 
-  constexpr int TPR = DP / N, RP = kThreads / TPR, PASS = KT / RP;  // threads of a row, rows at a time, rows of a thread
-  const int c_of = tid % TPR * N, r_of = tid / TPR;
-  // The pages of the thread's rows of a tile: -1 for a position that is not seen, -2 for a page outside the pool.
-  auto pages_of = [&](const Cursor<KT>& from, int (&pages)[PASS]) {
-    const int p0 = (from.row.tile0 + from.tile) * KT, first = p0 / d.page_size, rest = p0 - first * d.page_size;
-    const int32_t* at = table + (long long)from.b * d.max_pages + first;
+  if (warp == kWarps) {
+    // -------------------------------------------------------------------------------- copies
+    constexpr int R = KT / 32;  // boxes of a lane at most
+    const int boxes = KT / d.box;
+    const uint32_t bytes = (uint32_t)d.box * 128;
+    // the pages of the lane's boxes of a tile: -1 for positions that are not seen or only written, -2 for a page outside the pool
+    auto pages_of = [&](int (&pages)[R]) {
+      const int p0 = (here.row.tile0 + here.tile) * KT, first = p0 / d.page_size, rest = p0 - first * d.page_size;
+      const int32_t* at = table + (long long)here.b * d.max_pages + first;
 #pragma unroll
-    for (int i = 0; i < PASS; ++i) {
-      const int r = r_of + RP * i, x = rest + r;
-      const bool seen = p0 + r >= from.row.lo && p0 + r <= from.row.len;
-      pages[i] = seen ? at[d.page_size >= KT ? (int)(x >= d.page_size) : x / d.page_size] : -1;
-      if (seen && (pages[i] < 0 || pages[i] >= d.num_pages)) pages[i] = -2;
-    }
-  };
-  // The copies of the tile at `from` into a stage; true: a page outside the pool.
-  auto load = [&](const Cursor<KT>& from, const int (&pages)[PASS], int stage) {
-    IT* const ks = stages + (size_t)stage * 2 * KT * S + r_of * S + c_of;
-    IT* const vs = ks + KT * S;
-    const int h = from.unit / d.HB, p0 = (from.row.tile0 + from.tile) * KT, rest = p0 % d.page_size;
-    const int last = from.row.len - p0;  // the new token's row, if it is one of the tile's
-    const bool wide = c_of < d.D;
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < PASS; ++i) {
-      const int r = r_of + RP * i, x = rest + r;
-      const int place = d.page_size >= KT ? (x >= d.page_size ? x - d.page_size : x) : x % d.page_size;
-      const bool ok = pages[i] >= 0 && wide;
-      bad |= pages[i] == -2;
-      const long long at = ok ? (((long long)pages[i] * d.page_size + place) * d.Hk + h) * d.D + c_of : 0;
-      if (r != last) {
-        copy_async_l2(ks + RP * i * S, k_cache + at, ok ? 16 : 0);
-        copy_async_l2(vs + RP * i * S, v_cache + at, ok ? 16 : 0);
-        continue;
+      for (int i = 0; i < R; ++i) {
+        const int x = lane + 32 * i, r = x * d.box, y = rest + r;
+        pages[i] = -1;
+        if (x >= boxes || p0 + r + d.box <= here.row.lo || p0 + r > here.row.len) continue;
+        const int page = at[d.page_size >= KT ? (int)(y >= d.page_size) : y / d.page_size];
+        pages[i] = page < 0 || page >= d.num_pages ? -2 : p0 + r == here.row.len ? -1 : page;
       }
-      uint4 kn = make_uint4(0, 0, 0, 0), vn = kn;
-      if (wide) {
-        const IT *kf = k + (long long)from.b * d.ld_k + (long long)h * d.D + c_of, *vf = v + (long long)from.b * d.ld_v + (long long)h * d.D + c_of;
-        if (d.vec) {
-          kn = *reinterpret_cast<const uint4*>(kf);
-          vn = *reinterpret_cast<const uint4*>(vf);
-        } else {
-          alignas(16) IT a[N], b[N];
+    };
+    auto new_page = [&]() {  // of a unit's last tile, one unit of a key head
+      if (here.tile + 1 < here.row.tiles || here.unit % d.HB != 0) return -1;
+      const int page = table[(long long)here.b * d.max_pages + here.row.len / d.page_size];
+      return page >= 0 && page < d.num_pages ? page : -1;
+    };
+    int pages[R];
+    pages_of(pages);
+    int into = new_page();
+    for (bool more = true; more; ++count) {
+      const int h = here.unit / d.HB, hb = here.unit % d.HB, b = here.b, rest = (here.row.tile0 + here.tile) * KT % d.page_size;
+      const bool begins = count == 0 || here.tile == 0, ends = here.tile + 1 == here.row.tiles;
+      int from[R], place[R];
+      bool bad = false;
+      int copies = 0;
 #pragma unroll
-          for (int e = 0; e < N; ++e) a[e] = kf[e], b[e] = vf[e];
-          kn = *reinterpret_cast<const uint4*>(a);
-          vn = *reinterpret_cast<const uint4*>(b);
+      for (int i = 0; i < R; ++i) {
+        const int y = rest + (lane + 32 * i) * d.box;
+        place[i] = d.page_size >= KT ? (y >= d.page_size ? y - d.page_size : y) : y % d.page_size;
+        from[i] = pages[i];
+        bad |= pages[i] == -2;
+        copies += __popc(__ballot_sync(0xffffffffu, pages[i] >= 0));
+      }
+      bad = __any_sync(0xffffffffu, bad);
+      const int page = into;
+      more = here.next(d, lengths, units, &at, end);
+      if (more) {  // the next tile's pages are on their way while this one's copies are issued
+        pages_of(pages);
+        into = new_page();
+      }
+      if (!attn_wait(&empty[stage], parity ^ 1u, status)) break;
+      unsigned char* const ks = stages + (size_t)stage * stage_bytes<IT, DP>();
+      IT* const beside = side(stage);
+      const int heads = min(kHeads, d.G - hb * kHeads);
+      const IT* const qf = q + (long long)b * d.ld_q + (long long)(h * d.G + hb * kHeads) * d.D;
+      const IT *const kf = k + (long long)b * d.ld_k + (long long)h * d.D, *const vf = v + (long long)b * d.ld_v + (long long)h * d.D;
+      const uint32_t row_bytes = (uint32_t)d.D * sizeof(IT);
+      uint32_t extra = 0;
+      if (d.vec) {
+        extra = (begins ? heads * row_bytes : 0u) + (ends ? 2 * row_bytes : 0u);
+      } else {  // not aligned for bulk copies
+        if (begins)
+          for (int i = lane; i < heads * d.D; i += 32) beside[2 * DP + i] = qf[i];
+        if (ends)
+          for (int i = lane; i < d.D; i += 32) beside[i] = kf[i], beside[DP + i] = vf[i];
+        __syncwarp();
+      }
+      if (lane == 0) {
+        stage_bad[stage] = bad;
+        stage_page[stage] = page;
+        tc::mbar_arrive_expect_tx(&full[stage], 2 * kSlabs * bytes * copies + extra);
+        if (d.vec && begins) tc::bulk_load(beside + 2 * DP, qf, heads * row_bytes, &full[stage]);
+        if (d.vec && ends) {
+          tc::bulk_load(beside, kf, row_bytes, &full[stage]);
+          tc::bulk_load(beside + DP, vf, row_bytes, &full[stage]);
         }
       }
-      *reinterpret_cast<uint4*>(ks + RP * i * S) = kn;
-      *reinterpret_cast<uint4*>(vs + RP * i * S) = vn;
-      if (ok && from.unit % d.HB == 0) {  // one unit of a key head writes
-        *reinterpret_cast<uint4*>(k_cache + at) = kn;
-        *reinterpret_cast<uint4*>(v_cache + at) = vn;
-      }
-    }
-    return bad;
-  };
-
-  Cursor<KT> here, ahead;
-  here.seek(d, lengths, prefix, units, start);
-  ahead = here;
-  uint32_t bad_stages = 0;
-  long long loaded = start;
-  int pages[PASS];  // of the tile whose copies are next: read a tile ahead of them
-  pages_of(ahead, pages);
-  auto load_next = [&](int into) {
-    bad_stages &= ~(1u << into);
-    if (loaded < end) {
-      bad_stages |= (uint32_t)load(ahead, pages, into) << into;
-      if (++loaded < end) {
-        ahead.next(d, lengths, units);
-        pages_of(ahead, pages);
-      }
-    }
-    copy_async_commit();
-  };
+      __syncwarp();
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) load_next(i);
+      for (int i = 0; i < R; ++i)
+        if (from[i] >= 0) {
+          unsigned char* const to = ks + (lane + 32 * i) * bytes;
+#pragma unroll
+          for (int sl = 0; sl < kSlabs; ++sl) {
+            load_box(to + sl * slab_bytes<IT>(), &maps.k, &full[stage], sl * slab_features<IT>(), h, place[i], from[i]);
+            load_box(to + kTileBytes + sl * slab_bytes<IT>(), &maps.v, &full[stage], sl * slab_features<IT>(), h, place[i], from[i]);
+          }
+        }
+      if (++stage == kStages) {
+        stage = 0;
+        parity ^= 1u;
+      }
+    }
+    // every copy is waited for by the warps that compute; should one of their waits have run out, here
+    for (int i = 0; i < kStages; ++i) {
+      if (count > i) attn_wait(&full[i], (uint32_t)((count - 1 - i) / kStages) & 1u, status);
+    }
+    return;
+  }
+
   Engine e;
   const float c = d.scale * kLog2e;
-  int stage = 0, first_tile = here.tile, heads = 0;
-  bool fresh = true, bad = false;
-  for (long long at = start; at < end; ++at) {
+  int first_tile = here.tile, heads = 0, ended = 0;  // ended: units, or parts of one, so far
+  // Where a wait has run out the block goes on without waiting, so that no warp is left at a barrier; its results are lost.
+  bool fresh = true, bad = false, ok = true;
+  for (bool more = true; more;) {
+    ok = ok && attn_wait(&full[stage], parity, status);
+    unsigned char* const ks = stages + (size_t)stage * stage_bytes<IT, DP>();
+    unsigned char* const vs = ks + kTileBytes;
+    const IT* const beside = side(stage);
     if (fresh) {
-      const int hb = here.unit % d.HB, h0 = here.unit / d.HB * d.G + hb * kHeads;
-      heads = min(kHeads, d.G - hb * kHeads);
-      const IT* from = q + (long long)here.b * d.ld_q + (long long)h0 * d.D;
-      if constexpr (sizeof(IT) == 4) {
-        float* qs = acc + Engine::kRows * DP;
-        for (int i = tid; i < Engine::kRows * DP; i += kThreads) qs[i] = i / DP < heads && i % DP < d.D ? from[(long long)(i / DP) * d.D + i % DP] : 0.f;
-        e.begin(qs, heads, d);  // the barrier below orders it
+      heads = min(kHeads, d.G - here.unit % d.HB * kHeads);
+      if constexpr (sizeof(IT) == 4) {  // read all through the unit, while the stage goes on to others
+        IT* const qs = side(kStages);
+        for (int i = tid; i < heads * d.D; i += kThreads) qs[i] = beside[2 * DP + i];
+        tc::named_sync(1, kThreads);
+        e.begin(qs, heads, d.D);
       } else {
-        e.begin(from, heads, d);
+        e.begin(beside + 2 * DP, heads, d.D);
       }
       first_tile = here.tile;
       fresh = bad = false;
     }
-    copy_async_wait_group<kStages - 2>();
-    __syncthreads();
-    load_next((stage + kStages - 1) % kStages);
-    const IT* ks = stages + (size_t)stage * 2 * KT * S;
-    e.tile(ks, ks + KT * S, (here.row.tile0 + here.tile) * KT, here.row, c, heads);
-    bad |= bad_stages >> stage & 1;
-    stage = (stage + 1) % kStages;
-    if (here.tile + 1 < here.row.tiles && at + 1 < end) {
-      ++here.tile;
-      continue;
-    }
-    // the end of a (row, unit), or of the block's part of it
-    e.stats(ms[warp], ls[warp], heads);
-    bad = __syncthreads_or(bad);
-    auto top_of = [&](int r) { return max_nan(max_nan(ms[0][r], ms[1][r]), max_nan(ms[2][r], ms[3][r])); };
-    auto share = [&](int w, int r) {  // of warp w's part in the whole
-      const float top = top_of(r), base = top == -INFINITY ? 0.f : top * c;
-      return ex2f(fmaf(ms[w][r], c, -base));
-    };
-    for (int w = 0; w < kWarps; ++w) {
-      if (warp == w) e.add(acc, w == 0, heads, [&](int r) { return r < heads ? share(w, r) : 0.f; });
-      __syncthreads();
-    }
-    const bool whole = first_tile == 0 && here.tile + 1 == here.row.tiles;
-    float* const part = parts + ((long long)blockIdx.x * 2 + (at - (here.tile - first_tile) > start ? 1 : 0)) * part_floats<DP>();
-    for (int i = tid; i < heads * DP; i += kThreads) {
-      const int r = i / DP, f = i % DP;
-      if (whole) {
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum = fmaf(ls[w][r], share(w, r), sum);
-        const int h = here.unit / d.HB * d.G + here.unit % d.HB * kHeads + r;
-        if (f < d.D) o[((long long)here.b * d.Hq + h) * d.D + f] = from_f32<IT>(bad ? 0.f : acc[i] / sum);
-      } else {
-        part[i] = acc[i];
-        if (f == 0) {
-          float sum = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) sum = fmaf(ls[w][r], share(w, r), sum);
-          part[kHeads * DP + r] = top_of(r);
-          part[kHeads * (DP + 1) + r] = bad ? -1.f : sum;
+    const int p0 = (here.row.tile0 + here.tile) * KT;
+    const bool edge = p0 < here.row.lo || p0 + KT > here.row.len;
+    if (edge) {  // of the warp's own positions: values that are not seen become zeros, the new token comes to its place
+      constexpr int W = KT / kWarps, C = DP / N;
+      for (int x = lane; x < W * C; x += 32) {
+        const int r = W * warp + x / C, p = p0 + r;
+        if (p < here.row.lo || p > here.row.len) *reinterpret_cast<uint4*>(vs + chunk_at<IT>(r, x % C)) = make_uint4(0, 0, 0, 0);
+      }
+      const int r = here.row.len - p0;
+      if (r / W == warp && r < KT && lane < C) {
+        const bool on = lane * N < d.D;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const uint4 kn = on ? reinterpret_cast<const uint4*>(beside)[lane] : zero, vn = on ? reinterpret_cast<const uint4*>(beside + DP)[lane] : zero;
+        *reinterpret_cast<uint4*>(ks + chunk_at<IT>(r, lane)) = kn;
+        *reinterpret_cast<uint4*>(vs + chunk_at<IT>(r, lane)) = vn;
+        if (stage_page[stage] >= 0 && on) {
+          const long long to = (((long long)stage_page[stage] * d.page_size + here.row.len % d.page_size) * d.Hk + here.unit / d.HB) * d.D + lane * N;
+          *reinterpret_cast<uint4*>(k_cache + to) = kn;
+          *reinterpret_cast<uint4*>(v_cache + to) = vn;
         }
       }
+      __syncwarp();
     }
-    fresh = true;
-    if (at + 1 < end) {
-      here.next(d, lengths, units);
-      __syncthreads();  // acc, ms and ls are used again
+    e.tile(ks, vs, p0, here.row, c);
+    bad |= stage_bad[stage] != 0;
+    Cursor<KT> then = here;
+    more = then.next(d, lengths, units, &at, end);
+    const bool last = here.tile + 1 == here.row.tiles || !more;  // of a (row, unit), or of the block's part of it
+    if (last) {
+      float(&m_of)[kWarps][kHeads] = ms[ended & 1], (&l_of)[kWarps][kHeads] = ls[ended & 1];  // (a warp that is one unit on writes to the others)
+      e.stats(m_of[warp], l_of[warp], heads);
+      tc::named_sync(1, kThreads);  // from here on no warp reads the tile: its stage takes the warps' parts
+      float* const acc = reinterpret_cast<float*>(ks);
+      auto top_of = [&](int r) { return max_nan(max_nan(m_of[0][r], m_of[1][r]), max_nan(m_of[2][r], m_of[3][r])); };
+      auto share = [&](int w, int r) {  // of warp w's part in the whole
+        const float top = top_of(r), base = top == -INFINITY ? 0.f : top * c;
+        return ex2f(fmaf(m_of[w][r], c, -base));
+      };
+      e.put(acc + warp * kHeads * DP, heads, [&](int r) { return share(warp, r); });
+      tc::named_sync(1, kThreads);
+      const bool whole = first_tile == 0 && here.tile + 1 == here.row.tiles;
+      const int slot = ended++ > 0 ? 1 : 0;
+      float* const part = parts + ((long long)blockIdx.x * 2 + slot) * part_floats<DP>();
+      if (tid == 0) {  // which blocks have the unit's parts
+        int2* const span = spans + (long long)here.b * units + here.unit;
+        if (first_tile == 0) span->x = whole ? -1 : (int)blockIdx.x * 2 + slot;
+        if (here.tile + 1 == here.row.tiles) span->y = (int)blockIdx.x;
+      }
+      for (int r = warp; r < heads; r += kWarps) {  // a warp per head, DP / 32 features per lane
+        float l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) l = fmaf(l_of[w][r], share(w, r), l);
+        const float by = 1.f / l;
+        const int h = here.unit / d.HB * d.G + here.unit % d.HB * kHeads + r;
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) {
+          const int f = 32 * i + lane;
+          float sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) sum += acc[(w * kHeads + r) * DP + f];
+          if (!whole)
+            part[r * DP + f] = sum;
+          else if (f < d.D)
+            o[((long long)here.b * d.Hq + h) * d.D + f] = from_f32<IT>(bad ? 0.f : sum * by);
+        }
+        if (!whole && lane == 0) {
+          part[kHeads * DP + r] = top_of(r);
+          part[kHeads * (DP + 1) + r] = bad ? -1.f : l;
+        }
+      }
+      fresh = true;
     }
+    if (edge || last) tc::fence_proxy_async_smem();  // a later round's copies come to the same places
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&empty[stage]);
+    if (++stage == kStages) {
+      stage = 0;
+      parity ^= 1u;
+    }
+    here = then;
   }
-  copy_async_wait();
 }
 
 // The rows' results that several blocks have parts of, and zeros for the rows that were skipped.  A block per query head of a row.
 template <typename IT, int DP>
-__global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, int launched, const int32_t* __restrict__ lengths, IT* __restrict__ o,
-                                                             const float* __restrict__ parts) {
-  constexpr int KT = tile_keys<IT>();
-  __shared__ long long prefix[kThreads + 1];
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, const int32_t* __restrict__ lengths, IT* __restrict__ o,
+                                                             const int2* __restrict__ spans, const float* __restrict__ parts) {
   __shared__ float red[kWarps][2];
-  __shared__ float weight[kThreads];
-  const int tid = threadIdx.x, b = (int)(blockIdx.x / (unsigned)d.Hq), h = (int)(blockIdx.x % (unsigned)d.Hq), units = d.Hk * d.HB;
-  const Row row = row_of<KT>(d, lengths, b);
+  __shared__ float total_of[kWarps][DP];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = (int)(blockIdx.x / (unsigned)d.Hq), h = (int)(blockIdx.x % (unsigned)d.Hq);
+  const int r = h % d.G % kHeads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the step's launch, which this one may overtake
+  const int2 span = spans[((long long)b * d.Hk + h / d.G) * d.HB + h % d.G / kHeads];  // (not written for a row that was skipped)
+  const Row row = row_of<tile_keys<IT>()>(d, lengths, b);
   IT* out = o + ((long long)b * d.Hq + h) * d.D;
   if (row.tiles == 0) {
     if (tid < d.D) out[tid] = from_f32<IT>(0.f);
     return;
   }
-  sum_rows<KT>(d, lengths, prefix);
-  const long long total = prefix[kThreads] * units;
-  const int run = (d.B + kThreads - 1) / kThreads;
-  const long long blocks = min((long long)launched, total);
-  long long before = prefix[b / run];
-  for (int x = b / run * run; x < b; ++x) before += row_of<KT>(d, lengths, x).tiles;
-  const int unit = h / d.G * d.HB + h % d.G / kHeads, r = h % d.G % kHeads;
-  const long long a = before * units + (long long)unit * row.tiles, z = a + row.tiles - 1;
-  auto start_of = [&](long long x) { return total * x / blocks; };
-  auto block_of = [&](long long at) {
-    long long x = at * blocks / total;
-    while (start_of(x + 1) <= at) ++x;
-    while (start_of(x) > at) --x;
-    return (int)x;
-  };
-  const int c0 = block_of(a), c1 = block_of(z);
-  if (c0 == c1) return;
-  auto part_of = [&](int x) { return parts + ((long long)x * 2 + (a > start_of(x) ? 1 : 0)) * part_floats<DP>(); };
+  if (span.x < 0) return;
+  // the first block's part is its second where another unit's came before it; the later blocks begin within this unit
+  const int c0 = span.x >> 1, c1 = span.y;
+  auto part_of = [&](int x) { return parts + ((long long)x * 2 + (x == c0 ? span.x & 1 : 0)) * part_floats<DP>(); };
   const float c = d.scale * kLog2e;
   // the largest maximum, and whether a part is bad
   float top = -INFINITY, bad = 0.f;
@@ -572,21 +673,44 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, int lau
     top = max_nan(top, red[w][0]);
     bad = fmaxf(bad, red[w][1]);
   }
+  __syncthreads();  // red is used again
   const float base = top == -INFINITY ? 0.f : top * c;
-  float sum = 0.f, l = 0.f;
-  for (int x0 = c0; x0 <= c1; x0 += kThreads) {  // in order, a hundred parts at a time
-    __syncthreads();
-    const int n = min(kThreads, c1 - x0 + 1);
-    if (tid < n) weight[tid] = ex2f(fmaf(part_of(x0 + tid)[kHeads * DP + r], c, -base));
-    __syncthreads();
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float* p = part_of(x0 + i);
-      l = fmaf(p[kHeads * (DP + 1) + r], weight[i], l);
-      if (tid < DP) sum = fmaf(p[r * DP + tid], weight[i], sum);
+  // a warp takes every fourth part, a lane DP / 32 features, eight parts' loads under way; then the warps' sums in order
+  constexpr int F = DP / 32;
+  float sum[F] = {}, l = 0.f;
+  for (int x0 = c0 + warp; x0 <= c1; x0 += 8 * kWarps) {
+    float v[8][F], pm[8], pl[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int x = x0 + i * kWarps;
+      const float* p = part_of(min(x, c1));
+      pm[i] = x <= c1 ? p[kHeads * DP + r] : -INFINITY;
+      pl[i] = p[kHeads * (DP + 1) + r];
+#pragma unroll
+      for (int f = 0; f < F; ++f) v[i][f] = p[r * DP + F * lane + f];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (x0 + i * kWarps > c1) break;
+      const float weight = ex2f(fmaf(pm[i], c, -base));
+      l = fmaf(pl[i], weight, l);
+#pragma unroll
+      for (int f = 0; f < F; ++f) sum[f] = fmaf(v[i][f], weight, sum[f]);
     }
   }
-  if (tid < d.D) out[tid] = from_f32<IT>(bad > 0.f ? 0.f : sum / l);
+#pragma unroll
+  for (int f = 0; f < F; ++f) total_of[warp][F * lane + f] = sum[f];
+  if (lane == 0) red[warp][0] = l;
+  __syncthreads();
+  if (tid < d.D) {
+    float a0 = 0.f, l0 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      a0 += total_of[w][tid];
+      l0 += red[w][0];
+    }
+    out[tid] = from_f32<IT>(bad > 0.f ? 0.f : a0 / l0);
+  }
 }
 
 // ------------------------------------------------------------------------------ prompts to pages
@@ -646,6 +770,7 @@ gdr_status check_cache(const gdr_cache_problem* p, bool step) {
   // positions of a row are 32-bit numbers, as lengths are
   if ((long long)p->max_pages * p->page_size >= most || wk >= most) return GDR_ERR_UNSUPPORTED;
   if (step && (long long)p->B * p->Hq >= most) return GDR_ERR_UNSUPPORTED;
+  if (wk * p->page_size * (long long)dtype_bytes(p->dtype) >= 1ll << 40) return GDR_ERR_UNSUPPORTED;  // a page, as a stride of TMA
   if (!step && (p->cu_seqlens ? (long long)p->T : (long long)p->B * p->T) >= most) return GDR_ERR_UNSUPPORTED;
   return GDR_OK;
 }
@@ -653,7 +778,7 @@ gdr_status check_cache(const gdr_cache_problem* p, bool step) {
 struct StepShape {
   StepDims d;
   int blocks;
-  size_t bytes;
+  size_t spans, bytes;  // bytes: the status word, the spans, the parts
 };
 StepShape step_shape(const gdr_cache_problem* p) {
   StepShape s;
@@ -661,27 +786,50 @@ StepShape step_shape(const gdr_cache_problem* p) {
   const int G = p->Hq / p->Hk, KT = p->dtype == GDR_DTYPE_BF16 ? tile_keys<__nv_bfloat16>() : tile_keys<float>();
   s.d = StepDims{p->B, p->Hq, p->Hk, p->D, G, (G + kHeads - 1) / kHeads, p->num_pages, p->page_size, p->max_pages, p->window,
                  p->scale > 0.f ? p->scale : (float)(1.0 / sqrt((double)p->D)), p->ld_q ? p->ld_q : wq, p->ld_k ? p->ld_k : wk,
-                 p->ld_v ? p->ld_v : wk, 0};
+                 p->ld_v ? p->ld_v : wk, 0, 1};
+  while (s.d.box < KT && p->page_size % (2 * s.d.box) == 0) s.d.box *= 2;
   const long long most = ((long long)p->max_pages * p->page_size + KT - 1) / KT;  // tiles of a row at most
   const double tiles = (double)p->B * p->Hk * s.d.HB * (double)most;
   s.blocks = tiles < 2 * kSmCount ? (int)tiles : 2 * kSmCount;
   if (s.blocks < 1) s.blocks = 1;
-  s.bytes = block_align(sizeof(float) * 2 * (size_t)s.blocks * (p->D > 64 ? part_floats<128>() : part_floats<64>()));
+  s.spans = block_align(sizeof(int2) * (size_t)p->B * p->Hk * s.d.HB);
+  s.bytes = 256 + s.spans + block_align(sizeof(float) * 2 * (size_t)s.blocks * (p->D > 64 ? part_floats<128>() : part_floats<64>()));
   return s;
 }
 
 template <typename IT, int DP, typename Engine>
 cudaError_t step(const StepShape& sh, const void* q, const void* k, const void* v, void* kc, void* vc, const int32_t* table,
-                 const int32_t* lengths, void* o, float* parts, cudaStream_t s) {
+                 const int32_t* lengths, void* o, void* workspace, cudaStream_t s) {
+  uint32_t* const status = (uint32_t*)workspace;
+  int2* const spans = (int2*)((char*)workspace + 256);
+  float* const parts = (float*)((char*)workspace + 256 + sh.spans);
   const auto kernel = attn_step_kernel<IT, DP, Engine>;
-  constexpr size_t smem = step_smem<IT, DP>(Engine::kRows);
-  cudaError_t e = set_smem_once((const void*)kernel, smem);
+  const size_t smem = step_smem<IT, DP>(sh.d.G < kHeads ? sh.d.G : kHeads);
+  cudaError_t e = set_smem_once((const void*)kernel, step_smem<IT, DP>(kHeads));
   if (e != cudaSuccess) return e;
-  kernel<<<sh.blocks, kThreads, smem, s>>>(sh.d, (const IT*)q, (const IT*)k, (const IT*)v, (IT*)kc, (IT*)vc, table, lengths, (IT*)o, parts);
+  StepMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (sh.d.num_pages > 0) {  // without pages no copy is issued
+    const bool bf16 = sizeof(IT) == 2;
+    const uint64_t dims[4] = {(uint64_t)sh.d.D, (uint64_t)sh.d.Hk, (uint64_t)sh.d.page_size, (uint64_t)sh.d.num_pages};
+    const uint32_t box[4] = {(uint32_t)slab_features<IT>(), 1, (uint32_t)sh.d.box, 1};
+    if (!get_encoder() || !map_4d(&maps.k, kc, bf16, dims, box) || !map_4d(&maps.v, vc, bf16, dims, box)) return cudaErrorInvalidValue;
+  }
+  kernel<<<sh.blocks, kThreads + 32, smem, s>>>(maps, sh.d, (const IT*)q, (const IT*)k, (const IT*)v, (IT*)kc, (IT*)vc, table, lengths, (IT*)o, spans, parts, status);
   stage_mark(s, "attn_step");
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attn_join_kernel<IT, DP><<<(unsigned)(sh.d.B * sh.d.Hq), kThreads, 0, s>>>(sh.d, sh.blocks, lengths, (IT*)o, parts);
+  cudaLaunchAttribute early = {};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3((unsigned)(sh.d.B * sh.d.Hq));
+  config.blockDim = dim3(kThreads);
+  config.stream = s;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  e = cudaLaunchKernelEx(&config, attn_join_kernel<IT, DP>, sh.d, lengths, (IT*)o, (const int2*)spans, (const float*)parts);
+  if (e != cudaSuccess) return e;
   stage_mark(s, "attn_join");
   return cudaGetLastError();
 }
@@ -712,13 +860,12 @@ gdr_status gdr_attn_step(const gdr_cache_problem* p, const void* q, const void* 
   StepShape sh = step_shape(p);
   if (!workspace || workspace_bytes < sh.bytes) return GDR_ERR_WORKSPACE;
   if ((uintptr_t)workspace & 255u) return GDR_ERR_ALIGNMENT;
-  sh.d.vec = vec_ok(k) && vec_ok(v) && sh.d.ld_k * el % 16 == 0 && sh.d.ld_v * el % 16 == 0;
+  sh.d.vec = vec_ok(q) && vec_ok(k) && vec_ok(v) && sh.d.ld_q * el % 16 == 0 && sh.d.ld_k * el % 16 == 0 && sh.d.ld_v * el % 16 == 0;
   cudaStream_t s = (cudaStream_t)stream;
   stage_begin(s);
-  float* parts = (float*)workspace;
   auto run = [&](auto it, auto dp, auto engine) {
     return status_of(step<decltype(it), decltype(dp)::value, typename decltype(engine)::type>(sh, q, k, v, k_cache, v_cache, block_table, lengths,
-                                                                                              o, parts, s));
+                                                                                              o, workspace, s));
   };
   using W = std::integral_constant<int, 128>;
   using N = std::integral_constant<int, 64>;

@@ -194,6 +194,7 @@ bool tc_available();
 bool get_encoder();
 bool map_3d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t heads, uint64_t rows);
 bool map_3d_rows(CUtensorMap* m, const void* base, uint64_t cols, uint64_t heads, uint64_t rows, uint64_t ld, uint32_t box_rows);
+bool map_4d(CUtensorMap* m, const void* base, bool bf16, const uint64_t (&n)[4], const uint32_t (&b)[4]);
 bool map_2d(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows);
 bool map_2d_box(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint32_t esz, uint64_t cols,
                 uint64_t rows, uint32_t box_cols, uint32_t box_rows);

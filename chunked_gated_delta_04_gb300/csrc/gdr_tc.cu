@@ -82,6 +82,18 @@ bool map_3d_rows(CUtensorMap* m, const void* base, uint64_t cols, uint64_t heads
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 4D map over a contiguous tensor of these dimensions (innermost first) with such a box, 128-byte swizzle.
+bool map_4d(CUtensorMap* m, const void* base, bool bf16, const uint64_t (&n)[4], const uint32_t (&b)[4]) {
+  const cuuint64_t el = bf16 ? 2 : 4;
+  cuuint64_t dims[4] = {n[0], n[1], n[2], n[3]};
+  cuuint64_t strides[3] = {n[0] * el, n[0] * n[1] * el, n[0] * n[1] * n[2] * el};
+  cuuint32_t box[4] = {b[0], b[1], b[2], b[3]};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return g_encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(base), dims, strides,
+                  box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 2D map over a [rows][cols] matrix of `dt` (element size esz) with a box of
 // box_cols x box_rows, 128-byte swizzle (box_cols * esz must be 128).
 bool map_2d_box(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint32_t esz, uint64_t cols,
