@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
   __shared__ uint32_t tmem_slot;
   unsigned char* const sq = align1024(raw);
   unsigned char* const skv = sq + NT * Shape::kTile;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = attn_warp(), lane = threadIdx.x & 31;
   uint32_t* const status = a.status;
   if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *status = 0;  // of a packed batch: the tile table's kernel
   if (threadIdx.x == 0) {
@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
       }
     } else if (warp == 4 * NT) {
     // -------------------------------------------------------------------------------- MMAs
-    if (lane == 0) {
+    {
+      const uint32_t leader = attn_leader();
       AttnRing<ST> ring;
       uint32_t q_parity = 0, p_parity = 0;
       const uint32_t q_at = tc::smem_u32(sq), kv_at = tc::smem_u32(skv);
@@ -176,26 +177,26 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
         if (x < 0) break;
         if (!fwd_item<NT>(d, tiles, (unsigned)x, &w)) continue;
         auto scores = [&](int i, int slot, int j) {  // S_i of key block j
-          attn_scores<DP>(tmem + i * 128, q_at + i * Shape::kTile, kv_at + slot * Shape::kTile);
-          tc::mma_commit(&s_full[i]);
-          if (j + 1 == w.hi[i]) tc::mma_commit(&q_empty[i]);
+          attn_scores<DP>(tmem + i * 128, q_at + i * Shape::kTile, kv_at + slot * Shape::kTile, leader);
+          attn_commit(&s_full[i], leader);
+          if (j + 1 == w.hi[i]) attn_commit(&q_empty[i], leader);
         };
         if (w.first < w.last) {
-          ok = tc::mbar_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
+          ok = attn_warp_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             if (w.hi[i] == 0) continue;
-            ok = ok && tc::mbar_wait(&q_full[i], q_parity >> i & 1u, status, kDevErrTimeoutFwd);
+            ok = ok && attn_warp_wait(&q_full[i], q_parity >> i & 1u, status, kDevErrTimeoutFwd);
             q_parity ^= 1u << i;
             tc::tc_fence_after();
             if (ok && w.lo[i] == w.first) scores(i, ring.slot, w.first);
           }
-          tc::mma_commit(&kv_empty[ring.slot]);
+          attn_commit(&kv_empty[ring.slot], leader);
           ring.next();
         }
         for (int j = w.first; j < w.last && ok; ++j) {
           const int v_slot = ring.slot;
-          ok = tc::mbar_wait(&kv_full[v_slot], ring.parity, status, kDevErrTimeoutFwd);
+          ok = attn_warp_wait(&kv_full[v_slot], ring.parity, status, kDevErrTimeoutFwd);
           ring.next();
           bool k_here = false;
 #pragma unroll
@@ -203,16 +204,16 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
             if (!ok) break;
             if (j >= w.lo[i] && j < w.hi[i]) {
               GDR_DELAY(48);
-              ok = tc::mbar_wait(&p_ready[i], p_parity >> i & 1u, status, kDevErrTimeoutFwd);
+              ok = attn_warp_wait(&p_ready[i], p_parity >> i & 1u, status, kDevErrTimeoutFwd);
               p_parity ^= 1u << i;
               if (!ok) break;
               tc::tc_fence_after();
-              attn_product<DP>(tmem + Shape::kO + i * DP, tmem + i * 128, kv_at + v_slot * Shape::kTile, j > w.lo[i]);
-              tc::mma_commit(&o_done[i]);
+              attn_product<DP>(tmem + Shape::kO + i * DP, tmem + i * 128, kv_at + v_slot * Shape::kTile, j > w.lo[i], leader);
+              attn_commit(&o_done[i], leader);
             }
             if (j + 1 >= w.lo[i] && j + 1 < w.hi[i]) {
               if (!k_here) {
-                ok = tc::mbar_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
+                ok = attn_warp_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
                 if (!ok) break;
                 k_here = true;
               }
@@ -221,16 +222,16 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
             }
           }
           if (!ok) break;
-          tc::mma_commit(&kv_empty[v_slot]);
+          attn_commit(&kv_empty[v_slot], leader);
           if (j + 1 < w.last) {
-            tc::mma_commit(&kv_empty[ring.slot]);
+            attn_commit(&kv_empty[ring.slot], leader);
             ring.next();
           }
         }
       }
       if (!ok) {  // the products under way end before their memory is given back
-        tc::mma_commit(&drain);
-        tc::mbar_wait(&drain, 0, status, kDevErrTimeoutFwd);
+        attn_commit(&drain, leader);
+        attn_warp_wait(&drain, 0, status, kDevErrTimeoutFwd);
       }
     }
     __syncwarp();

@@ -40,25 +40,55 @@ __device__ __forceinline__ uint32_t desc_mnmajor(uint32_t saddr) { return saddr 
 __device__ __forceinline__ constexpr uint32_t kmajor_step(int kk) { return (uint32_t)(kk >> 2) * (kSlabBytes >> 4) + (uint32_t)(kk & 3) * 2u; }
 __device__ __forceinline__ constexpr uint32_t mnmajor_step(int kk) { return (uint32_t)kk * 128u; }
 
+// The MMAs are issued by one lane, but the whole warp runs the code around them, with a warp index that is the same for all lanes by
+// construction (attn_warp): addresses and descriptors then stay in uniform registers, where the instruction wants them.  In a
+// branch of one lane each MMA first moved its operands there one by one, which took 90 cycles an MMA of 64.
+__device__ __forceinline__ int attn_warp() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+__device__ __forceinline__ uint32_t attn_leader() {  // 1 in one lane of the warp
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void attn_commit(uint64_t* bar, uint32_t leader) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(tc::smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+
 // D = A B^T over DP features, A and B K-major tiles.
 template <int DP>
-__device__ __forceinline__ void attn_scores(uint32_t d_tmem, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void attn_scores(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t leader) {
   constexpr uint32_t id = tc::idesc_bf16(kTcBlock, kTcBlock, 0, 0);
   a = desc_kmajor(a);
   b = desc_kmajor(b);
 #pragma unroll
   for (int kk = 0; kk < DP / 16; ++kk)
-    tc::mma_bf16(d_tmem, (uint64_t)kDescHi << 32 | (a + kmajor_step(kk)), (uint64_t)kDescHi << 32 | (b + kmajor_step(kk)), id, kk > 0);
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a + kmajor_step(kk)), "r"(b + kmajor_step(kk)), "r"(kDescHi), "r"(id), "r"(kk > 0 ? 1u : 0u), "r"(leader)
+        : "memory");
 }
 // D (+)= A B: A [128 x 128] in TMEM as bf16 (32 columns for its first 64 columns, those of the others begin at column Second),
 // B a tile of 128 rows by DP features.
 template <int DP, uint32_t Second = 32>
-__device__ __forceinline__ void attn_product(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate) {
+__device__ __forceinline__ void attn_product(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate, uint32_t leader) {
   constexpr uint32_t id = tc::idesc_bf16(kTcBlock, DP, 0, 1);
   b = desc_mnmajor(b);
 #pragma unroll
   for (int kk = 0; kk < kTcBlock / 16; ++kk)
-    tc::mma_bf16_ts(d_tmem, a_tmem + (kk < 4 ? 8u * kk : Second + 8u * (kk - 4)), (uint64_t)kDescHi << 32 | (b + mnmajor_step(kk)), id, accumulate || kk > 0);
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+        "mov.b64 y, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem + (kk < 4 ? 8u * kk : Second + 8u * (kk - 4))), "r"(b + mnmajor_step(kk)), "r"(kDescHi), "r"(id),
+        "r"(accumulate || kk > 0 ? 1u : 0u), "r"(leader)
+        : "memory");
 }
 
 // mbar_wait by a whole warp, with one answer for all of its lanes.

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* const a_at = keep + 2 * kTile;
   unsigned char* const b_at = a_at + kA * kTile;
   BwdShared& b = *reinterpret_cast<BwdShared*>(b_at + kB * kTile);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = attn_warp(), lane = threadIdx.x & 31;
   uint32_t* const status = a.status;
   if (threadIdx.x == 0) bwd_barriers(b);
   if (warp == kMmaWarp) tc::tmem_alloc<512>(&b.tmem_slot);
@@ -180,13 +180,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       dos.drain();
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
+    {
+      const uint32_t leader = attn_leader();
       AttnRing<kA> qs;
       AttnRing<kB> dos;
       uint32_t kv_parity = 0, parity = 0;
       const uint32_t k_at = tc::smem_u32(keep), v_at = k_at + kTile, q_at = tc::smem_u32(a_at), do_at = tc::smem_u32(b_at);
       auto wait = [&](uint64_t* bar, uint32_t p) {
-        ok = ok && tc::mbar_wait(bar, p, status, kDevErrTimeoutBwd);
+        ok = ok && attn_warp_wait(bar, p, status, kDevErrTimeoutBwd);
         tc::tc_fence_after();
         return ok;
       };
@@ -197,15 +198,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int steps = (w.hi - w.lo) * d.G;
         auto scores = [&](bool last) {  // S^T of the next step
           if (!wait(&b.a_full[qs.slot], qs.parity)) return;
-          attn_scores<DP>(tmem + kS, k_at, q_at + qs.slot * kTile);
-          tc::mma_commit(&b.s_full);
-          if (last) tc::mma_commit(&b.keep_empty[0]);
+          attn_scores<DP>(tmem + kS, k_at, q_at + qs.slot * kTile, leader);
+          attn_commit(&b.s_full, leader);
+          if (last) attn_commit(&b.keep_empty[0], leader);
         };
         auto dscores = [&](bool last) {  // dP^T of the next step
           if (!wait(&b.b_full[dos.slot], dos.parity)) return;
-          attn_scores<DP>(tmem + kdP, v_at, do_at + dos.slot * kTile);
-          tc::mma_commit(&b.dp_full);
-          if (last) tc::mma_commit(&b.keep_empty[1]);
+          attn_scores<DP>(tmem + kdP, v_at, do_at + dos.slot * kTile, leader);
+          attn_commit(&b.dp_full, leader);
+          if (last) attn_commit(&b.keep_empty[1], leader);
         };
         if (wait(&b.keep_full[0], kv_parity)) scores(steps == 1);
         if (wait(&b.keep_full[1], kv_parity)) dscores(steps == 1);
@@ -217,23 +218,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           dos.next();
           GDR_DELAY(45);
           if (!wait(&b.p_ready, parity)) break;
-          attn_product<DP, 64>(tmem + kdV, tmem + kS, do_at + do_slot * kTile, it > 0);
-          tc::mma_commit(&b.b_empty[do_slot]);
+          attn_product<DP, 64>(tmem + kdV, tmem + kS, do_at + do_slot * kTile, it > 0, leader);
+          attn_commit(&b.b_empty[do_slot], leader);
           if (more) scores(last);
           GDR_DELAY(46);
           if (!wait(&b.ds_ready[0], parity)) break;
-          attn_product<DP, 64>(tmem + kdK, tmem + kdP, q_at + q_slot * kTile, it > 0);
-          tc::mma_commit(&b.a_empty[q_slot]);
+          attn_product<DP, 64>(tmem + kdK, tmem + kdP, q_at + q_slot * kTile, it > 0, leader);
+          attn_commit(&b.a_empty[q_slot], leader);
           if (more)
             dscores(last);
           else
-            tc::mma_commit(&b.done);
+            attn_commit(&b.done, leader);
           parity ^= 1u;
         }
       }
       if (!ok) {  // the products under way end before their memory is given back
-        tc::mma_commit(&b.drain);
-        tc::mbar_wait(&b.drain, 0, status, kDevErrTimeoutBwd);
+        attn_commit(&b.drain, leader);
+        attn_warp_wait(&b.drain, 0, status, kDevErrTimeoutBwd);
       }
     }
     __syncwarp();
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* const a_at = keep + 2 * kTile;
   unsigned char* const b_at = a_at + kA * kTile;
   BwdShared& b = *reinterpret_cast<BwdShared*>(b_at + kB * kTile);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = attn_warp(), lane = threadIdx.x & 31;
   uint32_t* const status = a.status;
   if (threadIdx.x == 0) bwd_barriers(b);
   if (warp == kMmaWarp) tc::tmem_alloc<512>(&b.tmem_slot);
@@ -430,14 +431,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       vs.drain();
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
+    {
+      const uint32_t leader = attn_leader();
       AttnRing<kA> ks;
       AttnRing<kB> vs;
       AttnRing<2> place;  // of dS
       uint32_t q_parity = 0, free_parity = 1;  // s_free, dp_free: of the step before
       const uint32_t q_at = tc::smem_u32(keep), do_at = q_at + kTile, k_at = tc::smem_u32(a_at), v_at = tc::smem_u32(b_at);
       auto wait = [&](uint64_t* bar, uint32_t p) {
-        ok = ok && tc::mbar_wait(bar, p, status, kDevErrTimeoutBwd);
+        ok = ok && attn_warp_wait(bar, p, status, kDevErrTimeoutBwd);
         tc::tc_fence_after();
         return ok;
       };
@@ -450,16 +452,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (it == 0) wait(&b.keep_full[0], q_parity);
           wait(&b.a_full[ks.slot], ks.parity);
           if (!wait(&b.s_free, free_parity)) return;
-          attn_scores<DP>(tmem + kS, q_at, k_at + ks.slot * kTile);
-          tc::mma_commit(&b.s_full);
-          if (it + 1 == steps) tc::mma_commit(&b.keep_empty[0]);
+          attn_scores<DP>(tmem + kS, q_at, k_at + ks.slot * kTile, leader);
+          attn_commit(&b.s_full, leader);
+          if (it + 1 == steps) attn_commit(&b.keep_empty[0], leader);
           if (it == 0) wait(&b.keep_full[1], q_parity);
           wait(&b.b_full[vs.slot], vs.parity);
           if (!wait(&b.dp_free, free_parity)) return;
-          attn_scores<DP>(tmem + kdP, do_at, v_at + vs.slot * kTile);
-          tc::mma_commit(&b.dp_full);
-          tc::mma_commit(&b.b_empty[vs.slot]);
-          if (it + 1 == steps) tc::mma_commit(&b.keep_empty[1]);
+          attn_scores<DP>(tmem + kdP, do_at, v_at + vs.slot * kTile, leader);
+          attn_commit(&b.dp_full, leader);
+          attn_commit(&b.b_empty[vs.slot], leader);
+          if (it + 1 == steps) attn_commit(&b.keep_empty[1], leader);
           free_parity ^= 1u;
           ks.next();
           vs.next();
@@ -473,16 +475,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (a barrier for each place: the step after this one may be through before this wait begins)
           GDR_DELAY(44);
           if (!wait(&b.ds_ready[place.slot], place.parity)) break;
-          attn_product<DP>(tmem + kdQ, tmem + kdS + 64 * place.slot, k_at + k_slot * kTile, it > 0);
-          tc::mma_commit(&b.a_empty[k_slot]);
-          if (it + 1 == steps) tc::mma_commit(&b.done);
+          attn_product<DP>(tmem + kdQ, tmem + kdS + 64 * place.slot, k_at + k_slot * kTile, it > 0, leader);
+          attn_commit(&b.a_empty[k_slot], leader);
+          if (it + 1 == steps) attn_commit(&b.done, leader);
           k_slot = next_slot;
           place.next();
         }
       }
       if (!ok) {  // the products under way end before their memory is given back
-        tc::mma_commit(&b.drain);
-        tc::mbar_wait(&b.drain, 0, status, kDevErrTimeoutBwd);
+        attn_commit(&b.drain, leader);
+        attn_warp_wait(&b.drain, 0, status, kDevErrTimeoutBwd);
       }
     }
     __syncwarp();
