@@ -272,9 +272,12 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 128; ++e) s[e] = e >= a0 && e < a1 ? s[e] : -INFINITY;
         }
-        float top = m;
+        float tops[4] = {m, m, m, m};  // four chains: one alone is 64 steps long
 #pragma unroll
-        for (int e = 0; e < 128; e += 2) top = fmaxf(top, fmaxf(s[e], s[e + 1]));
+        for (int e = 0; e < 128; e += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) tops[y] = fmaxf(tops[y], fmaxf(s[e + 2 * y], s[e + 2 * y + 1]));
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         if (j == lo) {
           m = top;
         } else {
@@ -299,21 +302,22 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
           }
         }
         const float base = m == -INFINITY ? 0.f : m * c;
-        float sum[4] = {};
+        const f32x2 c2 = pack2(c, c), base2 = pack2(-base, -base);
+        f32x2 sum[4] = {0, 0, 0, 0};  // pairs of zeros
 #pragma unroll
         for (int e = 0; e < 128; e += 64) {
           uint32_t r[32];
 #pragma unroll
           for (int y = 0; y < 32; ++y) {
-            const float p0 = ex2f(fmaf(s[e + 2 * y], c, -base)), p1 = ex2f(fmaf(s[e + 2 * y + 1], c, -base));
-            sum[(2 * y) & 3] += p0;
-            sum[(2 * y + 1) & 3] += p1;
-            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+            const f32x2 p2 = ex2_2(fma2(pack2(s[e + 2 * y], s[e + 2 * y + 1]), c2, base2));
+            sum[y & 3] = add2(sum[y & 3], p2);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(lo2(p2), hi2(p2));
             r[y] = *reinterpret_cast<const uint32_t*>(&b);
           }
           tc::tmem_st32(s_col + e / 2, r);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const f32x2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += lo2(both) + hi2(both);
         tc::tmem_wait_st();
         tc::tc_fence_before();
         __syncwarp();
