@@ -27,56 +27,64 @@ __device__ __forceinline__ int tile_work(const AttnDims& d, const AttnSpan& s, c
   return max(0, hi - lo);
 }
 
-__global__ void __launch_bounds__(1024) attn_tiles_kernel(AttnDims d, TableSpec t0, TableSpec t1, uint32_t* status) {
-  __shared__ int bin[kBins], bad, start, shift;
-  __shared__ int warp_sum_s[32];
+constexpr int kSeqsHere = 1024;  // sequences whose bounds fit in shared memory
+
+__global__ void __launch_bounds__(kBins) attn_tiles_kernel(AttnDims d, TableSpec t0, TableSpec t1, uint32_t* status) {
+  __shared__ int bin[kBins], warp_sums[kBins / 32];
+  __shared__ int32_t cu_q[kSeqsHere + 1], cu_k[kSeqsHere + 1];
   const TableSpec t = blockIdx.x == 0 ? t0 : t1;
-  const int tid = threadIdx.x;
-  if (tid == 0) {
-    bad = d.cu_q[0] != 0 || d.cu_q[d.num_seqs] != d.Tq || d.cu_k[0] != 0 || d.cu_k[d.num_seqs] != d.Tk;
-    start = 0;
-    const int most = t.keys ? d.Tq : d.Tk;  // of a tile's work
-    shift = 0;
-    while ((most >> shift) >= kBins) ++shift;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool here = d.num_seqs <= kSeqsHere;  // else they are read where they lie
+  bool bad = false;
+  for (int n = tid; n < d.num_seqs; n += kBins) {
+    const int q0 = d.cu_q[n], q1 = d.cu_q[n + 1], k0 = d.cu_k[n], k1 = d.cu_k[n + 1];
+    bad |= q0 > q1 || k0 > k1 || (n == 0 && (q0 != 0 || k0 != 0)) || (n == d.num_seqs - 1 && (q1 != d.Tq || k1 != d.Tk));
+    if (here) {
+      cu_q[n] = q0, cu_q[n + 1] = q1;  // (neighbours write the same)
+      cu_k[n] = k0, cu_k[n + 1] = k1;
+    }
   }
   bin[tid] = 0;
-  __syncthreads();
-  for (int n = tid; n < d.num_seqs; n += 1024)
-    if (d.cu_q[n] > d.cu_q[n + 1] || d.cu_k[n] > d.cu_k[n + 1]) bad = 1;
-  __syncthreads();
+  bad = __syncthreads_or(bad);
   if (tid == 0 && blockIdx.x == 0) *status = bad ? kDevErrBadCuSeqlens : 0u;
   int used = 0;
   if (!bad) {
+    AttnDims own = d;
+    if (here) own.cu_q = cu_q, own.cu_k = cu_k;
+    const int most = t.keys ? d.Tq : d.Tk, shift = max(0, 32 - __clz(most) - 10);  // of a tile's work; to a bin
     // a warp per sequence, a lane per tile: count the tiles of each amount of work ...
-    for (int pass = 0; pass < 2; ++pass) {
-      for (int n = tid >> 5; n < d.num_seqs; n += 32) {
-        const AttnSpan s = attn_span(d, n);
+    auto each = [&](auto f) {
+      for (int n = warp; n < d.num_seqs; n += kBins / 32) {
+        const AttnSpan s = attn_span(own, n);
         const int tiles = ((t.keys ? s.m : s.n) + t.size - 1) / t.size;
-        for (int i = tid & 31; i < tiles; i += 32) {
-          const int b = kBins - 1 - min(kBins - 1, tile_work(d, s, t, i) >> shift);
-          const int at = atomicAdd(&bin[b], 1);
-          if (pass == 1) t.table[at] = make_int2(n, i);  // order within a bin varies, results do not
-        }
+        for (int i = lane; i < tiles; i += 32) f(n, i, &bin[kBins - 1 - min(kBins - 1, tile_work(own, s, t, i) >> shift)]);
       }
-      __syncthreads();
-      if (pass == 0) {  // ... then the bins' starts, and every tile to its place
-        int v = bin[tid], sum = v;
+    };
+    each([&](int, int, int* b) { atomicAdd(b, 1); });
+    __syncthreads();
+    // ... then the bins' starts, and every tile to its place (the order within a bin varies, results do not)
+    const int v = bin[tid];
+    int sum = v;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, sum, o);
-          if ((tid & 31) >= o) sum += y;
-        }
-        if ((tid & 31) == 31) warp_sum_s[tid >> 5] = sum;
-        __syncthreads();
-        for (int w = 0; w < (tid >> 5); ++w) sum += warp_sum_s[w];
-        bin[tid] = sum - v;
-        if (tid == 1023) start = sum;
-        __syncthreads();
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
     }
-    used = start;
+    if (lane == 31) warp_sums[warp] = sum;
+    __syncthreads();
+    int all = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, all, o);
+      if (lane >= o) all += y;
+    }
+    used = __shfl_sync(0xffffffffu, all, 31);
+    const int before = __shfl_sync(0xffffffffu, all, max(0, warp - 1));
+    bin[tid] = sum - v + (warp ? before : 0);
+    __syncthreads();
+    each([&](int n, int i, int* b) { t.table[atomicAdd(b, 1)] = make_int2(n, i); });
   }
-  for (long long i = used + tid; i < t.slots; i += 1024) t.table[i] = make_int2(-1, 0);
+  for (long long i = used + tid; i < t.slots; i += kBins) t.table[i] = make_int2(-1, 0);
 }
 
 // ------------------------------------------------------------------------------------- delta
@@ -164,7 +172,7 @@ AttnTiles tiles_of(const AttnDims& d, const int2* table, bool keys, int size) {
 }
 
 cudaError_t launch_tiles(const AttnDims& d, const TableSpec& a, const TableSpec* b, uint32_t* status, cudaStream_t s) {
-  attn_tiles_kernel<<<b ? 2 : 1, 1024, 0, s>>>(d, a, b ? *b : a, status);
+  attn_tiles_kernel<<<b ? 2 : 1, kBins, 0, s>>>(d, a, b ? *b : a, status);
   stage_mark(s, "attn_tiles");
   return cudaGetLastError();
 }

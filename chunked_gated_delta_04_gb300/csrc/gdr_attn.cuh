@@ -108,7 +108,7 @@ cudaError_t launch_attn_bwd_simt(const AttnDims& d, const AttnTiles& tq, const A
 
 // Tensor-core kernels (bf16): q, k, v, dout aligned for TMA, the outputs for 16-byte stores.
 constexpr int kTcBlock = 128;  // rows of an MMA tile: queries, keys
-// Queries of a block's work: two tiles side by side, or one where that leaves SMs without work.
+// Queries of a block's work: two tiles side by side, or one (its keys in two lanes) where that leaves SMs without work.
 int attn_fwd_tc_tile(const AttnDims& d);
 cudaError_t launch_attn_fwd_tc(const AttnDims& d, const AttnTiles& t, int tile, const AttnFwdArgs& a, cudaStream_t s);
 cudaError_t launch_attn_bwd_tc(const AttnDims& d, const AttnTiles& tq, const AttnTiles& tk, const AttnBwdArgs& a, cudaStream_t s);

@@ -714,7 +714,9 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, const i
 }
 
 // ------------------------------------------------------------------------------ prompts to pages
-// A copy, bound by memory: 16 bytes of one token and head per thread, k and v one after the other.
+// A copy, bound by memory.  A thread takes kPieces times 16 bytes of one token, of k and of v: what it looks up (sequence, place,
+// page) serves all of them, and their loads are under way together.
+constexpr int kPieces = 2;
 struct WriteDims {
   int B, T, Hk, D, num_pages, page_size, max_pages;
   const int32_t* cu;
@@ -734,24 +736,32 @@ __global__ void __launch_bounds__(256) cache_write_kernel(WriteDims d, const IT*
     if (blockIdx.x == 0 && threadIdx.x == 0) *status = bad ? kDevErrBadCuSeqlens : 0u;
     if (bad) return;
   }
-  const int wide = d.Hk * d.D / V;
-  const long long x = (long long)blockIdx.x * 256 + threadIdx.x, token = x / wide;
+  const int wide = d.Hk * d.D / V, part = (wide + kPieces - 1) / kPieces;  // pieces of a token, of them a thread's distance
+  const long long x = (long long)blockIdx.x * 256 + threadIdx.x, token = x / part;
   if (token >= d.tokens) return;
-  const int c = (int)(x - token * wide) * V;
+  const int c = (int)(x - token * part);
+  using Piece = std::conditional_t<V == 1, IT, uint4>;
+  Piece a[kPieces], b[kPieces];
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int e = c + i * part;
+    if (e >= wide) break;
+    a[i] = __ldcs(reinterpret_cast<const Piece*>(k + token * d.ld_k) + e);
+    b[i] = __ldcs(reinterpret_cast<const Piece*>(v + token * d.ld_v) + e);
+  }
   const int n = d.cu ? seq_of(d.cu, d.B, token) : (int)(token / d.T);
   const long long t = d.cu ? token - d.cu[n] : token - (long long)n * d.T;
   const long long pos = t + (starts ? starts[n] : 0);
   if (pos < 0 || pos >= (long long)d.max_pages * d.page_size) return;
-  const int pi = (int)(pos / d.page_size), page = table[(long long)n * d.max_pages + pi];
+  const int pi = (int)pos / d.page_size, page = table[(long long)n * d.max_pages + pi];
   if (page < 0 || page >= d.num_pages) return;
-  const long long to = ((long long)page * d.page_size + (pos - (long long)pi * d.page_size)) * d.Hk * d.D + c;
-  if constexpr (V == 1) {
-    k_cache[to] = k[token * d.ld_k + c];
-    v_cache[to] = v[token * d.ld_v + c];
-  } else {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(k + token * d.ld_k + c)), b = __ldcs(reinterpret_cast<const uint4*>(v + token * d.ld_v + c));
-    *reinterpret_cast<uint4*>(k_cache + to) = a;
-    *reinterpret_cast<uint4*>(v_cache + to) = b;
+  const long long to = ((long long)page * d.page_size + ((int)pos - pi * d.page_size)) * d.Hk * d.D;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int e = c + i * part;
+    if (e >= wide) break;
+    reinterpret_cast<Piece*>(k_cache + to)[e] = a[i];
+    reinterpret_cast<Piece*>(v_cache + to)[e] = b[i];
   }
 }
 
@@ -895,7 +905,7 @@ gdr_status gdr_cache_write(const gdr_cache_problem* p, const void* k, const void
                     p->ld_v ? p->ld_v : wk};
   const int n16 = (int)(16 / el);
   const bool vec = vec_ok(k) && vec_ok(v) && d.ld_k % n16 == 0 && d.ld_v % n16 == 0;
-  const long long threads = tokens * (wk / (vec ? n16 : 1));
+  const long long threads = tokens * ((wk / (vec ? n16 : 1) + kPieces - 1) / kPieces);
   const long long grid = threads == 0 ? (p->cu_seqlens ? 1 : 0) : (threads + 255) / 256;
   if (grid == 0) return GDR_OK;
   if (grid >= (1ll << 31)) return GDR_ERR_UNSUPPORTED;

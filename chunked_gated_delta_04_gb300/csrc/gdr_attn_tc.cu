@@ -2,17 +2,21 @@
 //
 //   S = Q K^T,   P = e^{scale S - scale m},   O += P V,   o = O / l,   lse = scale m + log l
 //
-// per query with m the running maximum of its scores and l the running sum of e^..  A block takes NT tiles of 128 queries of a
-// head (two, so that the tensor core works on one while the other's scores are exponentiated) through the visible keys, 128 at
-// a time, and goes on to its next item (persistent, one block per SM).  Roles:
-//   warp 4 NT + 1  loads Q, then K and V tiles by TMA into a ring of slots
-//   warp 4 NT      issues the MMAs: S_t = Q_t K_j^T (both operands in shared memory), O_t += P_t V_j (P_t from TMEM)
-//   warps 4 t ..   the softmax of tile t, a thread per query: S from TMEM to registers, P as bf16 to TMEM over S
-// In TMEM: S_t (128 columns, P_t in its first 64) and O_t (DP columns).  Issue order per key block: O_0, next S_0, O_1, next S_1, so that
-// each tile's softmax runs beside the other tile's two products; MMAs of a block are executed in order, which makes
+// per query with m the running maximum of its scores and l the running sum of e^..  A block takes two lanes of work through the
+// visible keys, 128 at a time, so that the tensor core works on one while the other's scores are exponentiated, and goes on to its
+// next item (persistent, one block per SM).  The lanes are two tiles of 128 queries of a head, or, where that leaves SMs without
+// work (Split), the even and the odd key blocks of one tile, which are joined at the end.  Roles:
+//   warp 9     loads Q, then K and V tiles by TMA into a ring of slots
+//   warp 8     issues the MMAs: S_t = Q_t K_j^T (both operands in shared memory), O_t += P_t V_j (P_t from TMEM)
+//   warps 4 t  the softmax of lane t, a thread per query: S from TMEM to registers, P as bf16 to TMEM over S
+// In TMEM: S_t (128 columns, P_t in its first 64) and O_t (DP columns).  Issue order: O_0, next S_0, O_1, next S_1, so that
+// each lane's softmax runs beside the other lane's two products; MMAs of a block are executed in order, which makes
 // S's place free for the next scores once P V is issued.
 // The maximum that P is formed against (m) follows the true one only when that has grown by more than 2^8: then O and
 // l are rescaled; else P is up to 2^8, which bf16 holds as exactly as 1.
+// B = 1, T = 8192, 32 heads on 8 of 128, causal: 334 us, 1.65 PFLOP/s of the formula's operations, 85 % of what cuBLAS reaches; a pair
+// of tiles takes 2630 cycles, its products alone 2048: what is left is the wait of each lane's products for its softmax (1370
+// cycles, 780 of them exponentials and sums).  Split: three parts of 515 queries, 8 heads of 64, a window of 1024: 14.3 us, 16.4 with one lane.
 #include <algorithm>
 
 #include "gdr_attn_tc.cuh"
@@ -22,13 +26,14 @@ namespace {
 
 using namespace tcx;
 
-template <int DP, int NT>
+constexpr int NT = 2;  // lanes of work
+template <int DP, bool Split>
 struct FwdShape {
-  static constexpr int kThreads = NT * 128 + (NT == 2 ? 128 : 64);  // registers move between whole warpgroups
+  static constexpr int kThreads = 384;  // registers move between whole warpgroups
   static constexpr uint32_t kTile = attn_tile_bytes<DP>();
+  static constexpr int kQ = Split ? 1 : 2;          // tiles of queries
   static constexpr int kSlots = DP == 128 ? 4 : 6;  // of the ring of K and V tiles
-  static constexpr size_t kSmem = 1024 + (size_t)(NT + kSlots) * kTile;
-  static constexpr uint32_t kTmem = NT == 2 ? 512 : 256;
+  static constexpr size_t kSmem = 1024 + (size_t)(kQ + kSlots) * kTile;
   static constexpr uint32_t kO = NT * 128;  // first column of O_0
 };
 
@@ -37,25 +42,24 @@ struct FwdMaps {
 };
 
 // An item: a head's queries i0 .. of a sequence, and the key blocks [lo, hi) of each tile (none: both 0) and of all.
-template <int NT>
 struct FwdItem {
   AttnSpan s;
   int h, i0, lo[NT], hi[NT], first, last;
 };
 
-template <int NT>
-__device__ __forceinline__ bool fwd_item(const AttnDims& d, const AttnTiles& t, unsigned x, FwdItem<NT>* w) {
+template <int Q>
+__device__ __forceinline__ bool fwd_item(const AttnDims& d, const AttnTiles& t, unsigned x, FwdItem* w) {
   int seq, tile;
   if (!attn_tile(d, t, d.Hq, x, &seq, &w->h, &tile)) return false;
   w->s = attn_span(d, seq);
-  w->i0 = tile * NT * kTcBlock;
+  w->i0 = tile * Q * kTcBlock;
   w->first = 1 << 30;
   w->last = 0;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int a = w->i0 + i * kTcBlock;
     int lo = 0, hi = 0;
-    if (a < w->s.n) attn_keys(d, w->s, a, min(w->s.n, a + kTcBlock), &lo, &hi);
+    if (i < Q && a < w->s.n) attn_keys(d, w->s, a, min(w->s.n, a + kTcBlock), &lo, &hi);
     const bool any = lo < hi;
     w->lo[i] = any ? lo / kTcBlock : 0;
     w->hi[i] = any ? (hi + kTcBlock - 1) / kTcBlock : 0;
@@ -67,16 +71,17 @@ __device__ __forceinline__ bool fwd_item(const AttnDims& d, const AttnTiles& t, 
   return true;
 }
 
-template <int DP, int NT>
-__global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
+template <int DP, bool Split>
+__global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
     attn_fwd_tc_kernel(const __grid_constant__ FwdMaps maps, AttnDims d, AttnTiles tiles, unsigned items, AttnFwdArgs a) {
-  using Shape = FwdShape<DP, NT>;
-  constexpr int ST = Shape::kSlots;
+  using Shape = FwdShape<DP, Split>;
+  constexpr int ST = Shape::kSlots, Q = Shape::kQ;
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t q_full[NT], q_empty[NT], kv_full[ST], kv_empty[ST], s_full[NT], p_ready[NT], o_done[NT], tail_full, drain;
   __shared__ uint32_t tmem_slot;
+  __shared__ float joint[Split ? 2 : 1][2][NT][kTcBlock];  // Split: maxima and sums of an item's two lanes, of the next item's
   unsigned char* const sq = align1024(raw);
-  unsigned char* const skv = sq + NT * Shape::kTile;
+  unsigned char* const skv = sq + Q * Shape::kTile;
   const int warp = attn_warp(), lane = threadIdx.x & 31;
   uint32_t* const status = a.status;
   if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *status = 0;  // of a packed batch: the tile table's kernel
@@ -96,7 +101,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
     tc::mbar_init(&drain, 1);
     tc::fence_barrier_init();
   }
-  if (warp == 4 * NT) tc::tmem_alloc<Shape::kTmem>(&tmem_slot);
+  if (warp == 4 * NT) tc::tmem_alloc<512>(&tmem_slot);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -105,13 +110,13 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
   // Registers: three warpgroups are launched with 168 a thread; 2 x 216 + 72 is the same sum.
   // (Each count stands in its role's own branch: the compiler allots the code behind it by it.)
   if (warp >= 4 * NT) {
-    if constexpr (NT == 2) regs_less<72>();
+    regs_less<72>();
     if (warp == 4 * NT + 1) {
     // ------------------------------------------------------------------------------- loads
     AttnRing<ST> ring;
     uint32_t q_parity = 0, tail_parity = 0;
     bool ok = true;
-    auto load_kv = [&](const CUtensorMap* map, const FwdItem<NT>& w, int j, bool value) {
+    auto load_kv = [&](const CUtensorMap* map, const FwdItem& w, int j, bool value) {
       GDR_DELAY(49);
       ok = ok && attn_warp_wait(&kv_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutFwd);
       if (!ok) return;
@@ -132,29 +137,34 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
       }
       ring.next();
     };
-    FwdItem<NT> w;
+    FwdItem w;
     for (unsigned turn = 0; ok; ++turn) {
       const long long x = attn_item(turn, items);
       if (x < 0) break;
-      if (!fwd_item<NT>(d, tiles, (unsigned)x, &w)) continue;
-      for (int j = w.first; j < w.last && ok; ++j) {
-        if (j == w.first) {
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            if (i == 1) load_kv(&maps.k, w, j, false);
-            if (w.hi[i] == 0) continue;
-            ok = ok && attn_warp_wait(&q_empty[i], (q_parity >> i & 1u) ^ 1u, status, kDevErrTimeoutFwd);
-            if (ok && lane == 0) {
-              tc::mbar_arrive_expect_tx(&q_full[i], Shape::kTile);
-              attn_load_tile<DP>(sq + i * Shape::kTile, &maps.q, &q_full[i], w.h, w.s.q0 + w.i0 + i * kTcBlock);
-            }
-            q_parity ^= 1u << i;
-          }
-          if (NT == 1) load_kv(&maps.k, w, j, false);
-        } else {
-          load_kv(&maps.k, w, j, false);
+      if (!fwd_item<Q>(d, tiles, (unsigned)x, &w)) continue;
+      auto load_q = [&](int i) {
+        ok = ok && attn_warp_wait(&q_empty[i], (q_parity >> i & 1u) ^ 1u, status, kDevErrTimeoutFwd);
+        if (ok && lane == 0) {
+          tc::mbar_arrive_expect_tx(&q_full[i], Shape::kTile);
+          attn_load_tile<DP>(sq + i * Shape::kTile, &maps.q, &q_full[i], w.h, w.s.q0 + w.i0 + i * kTcBlock);
         }
-        load_kv(&maps.v, w, j, true);
+        q_parity ^= 1u << i;
+      };
+      if (w.first >= w.last) continue;
+      if (w.hi[0]) load_q(0);
+      load_kv(&maps.k, w, w.first, false);
+      if (Q == 2 && w.hi[1]) load_q(1);
+      if constexpr (Split) {  // the order in which they are used: two blocks of scores are ahead of the values
+        if (w.first + 1 < w.last) load_kv(&maps.k, w, w.first + 1, false);
+        for (int j = w.first; j < w.last && ok; ++j) {
+          load_kv(&maps.v, w, j, true);
+          if (j + 2 < w.last) load_kv(&maps.k, w, j + 2, false);
+        }
+      } else {
+        for (int j = w.first; j < w.last && ok; ++j) {
+          if (j > w.first) load_kv(&maps.k, w, j, false);
+          load_kv(&maps.v, w, j, true);
+        }
       }
     }
     // after a wait that ran out, the copies under way end before the block does
@@ -171,16 +181,47 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
       uint32_t q_parity = 0, p_parity = 0;
       const uint32_t q_at = tc::smem_u32(sq), kv_at = tc::smem_u32(skv);
       bool ok = true;
-      FwdItem<NT> w;
+      FwdItem w;
       for (unsigned turn = 0; ok; ++turn) {
         const long long x = attn_item(turn, items);
         if (x < 0) break;
-        if (!fwd_item<NT>(d, tiles, (unsigned)x, &w)) continue;
+        if (!fwd_item<Q>(d, tiles, (unsigned)x, &w)) continue;
         auto scores = [&](int i, int slot, int j) {  // S_i of key block j
-          attn_scores<DP>(tmem + i * 128, q_at + i * Shape::kTile, kv_at + slot * Shape::kTile, leader);
+          const int q = Split ? 0 : i;
+          attn_scores<DP>(tmem + i * 128, q_at + q * Shape::kTile, kv_at + slot * Shape::kTile, leader);
           attn_commit(&s_full[i], leader);
-          if (j + 1 == w.hi[i]) attn_commit(&q_empty[i], leader);
+          if (j + 1 == w.hi[q]) attn_commit(&q_empty[q], leader);
         };
+        if constexpr (Split) {
+          if (w.first >= w.last) continue;
+          auto next_scores = [&](int j) {
+            ok = ok && attn_warp_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
+            if (!ok) return;
+            tc::tc_fence_after();
+            scores((j - w.first) & 1, ring.slot, j);
+            attn_commit(&kv_empty[ring.slot], leader);
+            ring.next();
+          };
+          ok = attn_warp_wait(&q_full[0], q_parity & 1u, status, kDevErrTimeoutFwd);
+          q_parity ^= 1u;
+          next_scores(w.first);
+          if (w.first + 1 < w.last) next_scores(w.first + 1);
+          for (int j = w.first; j < w.last && ok; ++j) {
+            const int i = (j - w.first) & 1;
+            ok = attn_warp_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
+            GDR_DELAY(48);
+            ok = ok && attn_warp_wait(&p_ready[i], p_parity >> i & 1u, status, kDevErrTimeoutFwd);
+            p_parity ^= 1u << i;
+            if (!ok) break;
+            tc::tc_fence_after();
+            attn_product<DP>(tmem + Shape::kO + i * DP, tmem + i * 128, kv_at + ring.slot * Shape::kTile, j > w.first + 1, leader);
+            attn_commit(&o_done[i], leader);
+            attn_commit(&kv_empty[ring.slot], leader);
+            ring.next();
+            if (j + 2 < w.last) next_scores(j + 2);
+          }
+          continue;
+        }
         if (w.first < w.last) {
           ok = attn_warp_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
 #pragma unroll
@@ -237,28 +278,30 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
     __syncwarp();
     }
   } else {
-    if constexpr (NT == 2) regs_more<216>();
+    regs_more<216>();
     // ----------------------------------------------------------------------------- softmax
     const int t = warp >> 2, row = threadIdx.x & 127;
     const uint32_t s_col = tc::tmem_lane_addr(tmem, warp, t * 128), o_col = tc::tmem_lane_addr(tmem, warp, Shape::kO + t * DP);
     const float c = d.scale * kLog2e;
     uint32_t parity = 0;  // of s_full; of o_done it is that of the block before
-    FwdItem<NT> w;
+    FwdItem w;
     bool ok = true;
-    for (unsigned turn = 0; ok; ++turn) {
+    // (Split: where a wait has run out a warpgroup goes on without waiting, so that the other is not left at their barriers.)
+    for (unsigned turn = 0; Split || ok; ++turn) {
       const long long x = attn_item(turn, items);
       if (x < 0) break;
-      if (!fwd_item<NT>(d, tiles, (unsigned)x, &w)) continue;
-      const int i = w.i0 + t * kTcBlock + row, off = w.s.m - w.s.n;
-      int lo = w.lo[0], hi = w.hi[0];
-      if (NT == 2 && t == 1) lo = w.lo[NT - 1], hi = w.hi[NT - 1];
+      if (!fwd_item<Q>(d, tiles, (unsigned)x, &w)) continue;
+      const int first_row = w.i0 + (Split ? 0 : t * kTcBlock), i = first_row + row, off = w.s.m - w.s.n;
+      int lo = w.lo[0], hi = w.hi[0];  // Split: every second of them, from lo + t on
+      if (!Split && t == 1) lo = w.lo[1], hi = w.hi[1];
+      const int begin = Split ? lo + t : lo;
       // the keys [from, to) that this query sees
       const int from = d.window ? max(0, i + off - d.window + 1) : 0, to = d.causal ? min(w.s.m, i + off + 1) : w.s.m;
       // blocks [clear, full) are seen whole by all of the tile's queries
-      const int i_first = w.i0 + t * kTcBlock, i_last = i_first + kTcBlock - 1;
+      const int i_first = first_row, i_last = i_first + kTcBlock - 1;
       const int whole_to = (d.causal ? min(w.s.m, i_first + off + 1) : w.s.m), whole_from = d.window ? i_last + off - d.window + 1 : 0;
       float m = -INFINITY, l = 0.f;
-      for (int j = lo; j < hi; ++j) {
+      for (int j = begin; j < hi && ok; j += Split ? 2 : 1) {
         ok = attn_warp_wait(&s_full[t], parity, status, kDevErrTimeoutFwd);
         if (!ok) break;
         tc::tc_fence_after();
@@ -278,7 +321,7 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
 #pragma unroll
           for (int y = 0; y < 4; ++y) tops[y] = fmaxf(tops[y], fmaxf(s[e + 2 * y], s[e + 2 * y + 1]));
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-        if (j == lo) {
+        if (j == begin) {
           m = top;
         } else {
           const bool grown = (top - m) * c > 8.f;
@@ -325,37 +368,56 @@ __global__ void __launch_bounds__(FwdShape<DP, NT>::kThreads, 1)
         if (lane == 0) tc::mbar_arrive(&p_ready[t]);
         parity ^= 1u;
       }
-      if (!ok) break;
+      if (!Split && !ok) break;
       const bool mine = i < w.s.n;
       __nv_bfloat16* const out = (__nv_bfloat16*)a.o + ((w.s.q0 + i) * d.Hq + w.h) * (long long)d.D;
-      if (lo < hi) {
-        ok = attn_warp_wait(&o_done[t], parity ^ 1u, status, kDevErrTimeoutFwd);
-        if (!ok) break;
+      if (begin < hi) {
+        ok = ok && attn_warp_wait(&o_done[t], parity ^ 1u, status, kDevErrTimeoutFwd);
+        if (!Split && !ok) break;
         tc::tc_fence_after();
       }
-      // a query that has seen nothing has l = 0 and O = 0 or, where a product has not begun, none
-      attn_store_row<DP>(o_col, out, d.D, m == -INFINITY ? 0.f : 1.f / l, lo < hi, mine);
-      if (mine) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = m == -INFINITY ? -INFINITY : fmaf(m, d.scale, logf(l));
+      if constexpr (Split) {  // every thread joins its query's two lanes for half of the features
+        float(&of)[2][NT][kTcBlock] = joint[turn & 1];
+        of[0][t][row] = m;
+        of[1][t][row] = l;
+        tc::tc_fence_before();
+        tc::named_sync(1, 2 * kTcBlock);
+        tc::tc_fence_after();
+        const float m0 = of[0][0][row], m1 = of[0][1][row], top = fmaxf(m0, m1);
+        const float f0 = m0 == -INFINITY ? 0.f : ex2f((m0 - top) * c), f1 = m1 == -INFINITY ? 0.f : ex2f((m1 - top) * c);
+        const float sum = fmaf(of[1][0][row], f0, of[1][1][row] * f1);
+        const float by = top == -INFINITY ? 0.f : 1.f / sum;
+        const int f = t * (DP / 2);
+        attn_store_row<DP / 2>(tc::tmem_lane_addr(tmem, warp, Shape::kO + f), tc::tmem_lane_addr(tmem, warp, Shape::kO + DP + f), out + f, d.D - f,
+                               f0 * by, f1 * by, lo < hi, lo + 1 < hi, mine);
+        if (mine && t == 0) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = top == -INFINITY ? -INFINITY : fmaf(top, d.scale, logf(sum));
+        tc::tc_fence_before();
+        tc::named_sync(1, 2 * kTcBlock);  // both lanes' O are read before either is begun anew
+      } else {
+        // a query that has seen nothing has l = 0 and O = 0 or, where a product has not begun, none
+        attn_store_row<DP>(o_col, out, d.D, m == -INFINITY ? 0.f : 1.f / l, lo < hi, mine);
+        if (mine) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = m == -INFINITY ? -INFINITY : fmaf(m, d.scale, logf(l));
+      }
       tc::tc_fence_before();  // O is read before this item's successor's first product into it, which the next arrival allows
     }
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == 4 * NT) tc::tmem_dealloc(tmem, Shape::kTmem);
+  if (warp == 4 * NT) tc::tmem_dealloc(tmem, 512);
 }
 
-template <int DP, int NT>
+template <int DP, bool Split>
 cudaError_t fwd(const AttnDims& d, const AttnTiles& t, const AttnFwdArgs& a, cudaStream_t s) {
-  using Shape = FwdShape<DP, NT>;
+  using Shape = FwdShape<DP, Split>;
   FwdMaps maps;
   const long long rows_q = (long long)d.B * d.Tq, rows_k = (long long)d.B * d.Tk;
   if (!attn_map(&maps.q, a.q, d.D, d.Hq, rows_q, d.ld_q) || !attn_map(&maps.k, a.k, d.D, d.Hk, rows_k, d.ld_k) ||
       !attn_map(&maps.v, a.v, d.D, d.Hk, rows_k, d.ld_v))
     return cudaErrorInvalidValue;
-  const auto kernel = attn_fwd_tc_kernel<DP, NT>;
+  const auto kernel = attn_fwd_tc_kernel<DP, Split>;
   cudaError_t e = set_smem_once((const void*)kernel, Shape::kSmem);
   if (e != cudaSuccess) return e;
-  const long long items = attn_tile_count(d, false, NT * kTcBlock) * d.Hq;
+  const long long items = attn_tile_count(d, false, Shape::kQ * kTcBlock) * d.Hq;
   kernel<<<(unsigned)std::min<long long>(items, kSmCount), Shape::kThreads, Shape::kSmem, s>>>(maps, d, t, (unsigned)items, a);
   stage_mark(s, "attn_fwd");
   return cudaGetLastError();
@@ -368,8 +430,8 @@ int attn_fwd_tc_tile(const AttnDims& d) {
 }
 
 cudaError_t launch_attn_fwd_tc(const AttnDims& d, const AttnTiles& t, int tile, const AttnFwdArgs& a, cudaStream_t s) {
-  if (tile == 2 * kTcBlock) return d.D > 64 ? fwd<128, 2>(d, t, a, s) : fwd<64, 2>(d, t, a, s);
-  return d.D > 64 ? fwd<128, 1>(d, t, a, s) : fwd<64, 1>(d, t, a, s);
+  if (tile == 2 * kTcBlock) return d.D > 64 ? fwd<128, false>(d, t, a, s) : fwd<64, false>(d, t, a, s);
+  return d.D > 64 ? fwd<128, true>(d, t, a, s) : fwd<64, true>(d, t, a, s);
 }
 
 }  // namespace gdr

@@ -140,6 +140,28 @@ __device__ __forceinline__ void attn_store_row(uint32_t taddr, __nv_bfloat16* ou
   }
 }
 
+// The same of the sum of two accumulators' rows, times f0 and f1, where there are any.
+template <int DP>
+__device__ __forceinline__ void attn_store_row(uint32_t taddr0, uint32_t taddr1, __nv_bfloat16* out, int D, float f0, float f1, bool any0,
+                                               bool any1, bool mine) {
+#pragma unroll
+  for (int e = 0; e < DP; e += 32) {
+    float o0[32], o1[32];
+    if (any0) tc::tmem_ld32(taddr0 + e, o0);
+    if (any1) tc::tmem_ld32(taddr1 + e, o1);
+    tc::tmem_wait_ld();
+    if (mine) {
+#pragma unroll
+      for (int y = 0; y < 32; y += 8) {
+        float v[8];
+#pragma unroll
+        for (int z = 0; z < 8; ++z) v[z] = (any0 && f0 != 0.f ? o0[y + z] * f0 : 0.f) + (any1 && f1 != 0.f ? o1[y + z] * f1 : 0.f);
+        if (e + y < D) store_v<8>(out + e + y, v);
+      }
+    }
+  }
+}
+
 // A place in a ring of N slots: slot and parity of its use.
 template <int N>
 struct AttnRing {
