@@ -1,11 +1,11 @@
 """A small hybrid language model over the framework's operators, trained and then served.
 
 Every layer is  stream -> norm -> mixer -> residual scale -> stream; mixers alternate between the
-gated delta rule and the selective scan.  A mixer passes its inputs through the short causal
-convolution and its output through a gated norm.  The residual add of a layer and the norm in front
-of the next one are one call (block_norm), on an fp32 stream.
+gated delta rule and the selective scan, and with --attention N every N-th is attention with rotary
+positions.  A recurrent mixer passes its inputs through the short causal convolution and its output through a gated
+norm.  The residual add of a layer and the norm in front of the next one are one call (block_norm), on an fp32 stream.
 
-    python examples/hybrid_block.py [--steps 100] [--dtype bfloat16]
+    python examples/hybrid_block.py [--steps 100] [--dtype bfloat16] [--attention 4]
 
 trains on a synthetic task (every token's successor under a fixed permutation), then answers prompts token by
 token from the states that the prompt left in the pools, and compares the logits with those of the
@@ -115,13 +115,58 @@ class ScanMixer(nn.Module):
         return self.out(y)
 
 
+class AttentionMixer(nn.Module):
+    """q, k, v of one projection, half of every head turned by its position, two query heads for each key head.  Served, a slot's
+    keys and values lie in pages of a pool, which are its own."""
+
+    def __init__(self, dim, heads, width, page=16, room=128):
+        super().__init__()
+        self.Hq, self.Hk, self.D = 2 * heads, heads, width
+        self.page, self.pages = page, -(-room // page)  # of a slot
+        self.sizes = [self.Hq, heads, heads]
+        self.proj = nn.Linear(dim, sum(self.sizes) * width, bias=False)
+        self.out = nn.Linear(self.Hq * width, dim, bias=False)
+        self.register_buffer("freqs", gdr.rope_frequencies(width // 2, device="cpu")[0])
+
+    def state(self, slots, dtype):
+        pool = [torch.zeros(slots * self.pages, self.page, self.Hk, self.D, device="cuda", dtype=dtype) for _ in range(2)]
+        table = torch.randperm(slots * self.pages, generator=torch.Generator().manual_seed(3)).view(slots, self.pages)
+        return [*pool, table.to(torch.int32).cuda(), torch.zeros(slots, dtype=torch.int32, device="cuda")]
+
+    def split(self, x):
+        return self.proj(x).unflatten(-1, (-1, self.D)).split(self.sizes, -2)  # slices, used where they lie
+
+    def forward(self, x, pool=None, slots=None):
+        q, k, v = self.split(x)
+        q, k = gdr.rope(q, k, self.freqs)
+        if pool is not None:
+            k_cache, v_cache, table, lengths = pool
+            gdr.cache_write(k, v, k_cache, v_cache, table[slots.long()])
+            lengths[slots.long()] = x.shape[1]
+        return self.out(gdr.attention(q, k, v).flatten(-2))
+
+    def step(self, x, pool, slots):
+        k_cache, v_cache, table, lengths = pool
+        at = lengths[slots.long()]
+        q, k, v = self.split(x)
+        q, k = gdr.rope_forward(q, k, self.freqs, positions=at)
+        o = gdr.attn_step(q, k, v, k_cache, v_cache, table[slots.long()], at)
+        lengths[slots.long()] = at + 1
+        return self.out(o.flatten(-2))
+
+
 class HybridModel(nn.Module):
-    def __init__(self, vocab=64, dim=128, layers=4, heads=2, width=64, dtype=torch.bfloat16):
+    def __init__(self, vocab=64, dim=128, layers=4, heads=2, width=64, dtype=torch.bfloat16, attention=0):
         super().__init__()
         self.dtype = dtype
         self.embed = nn.Embedding(vocab, dim)
-        self.mixers = nn.ModuleList(DeltaMixer(dim, heads, width) if i % 2 == 0 else ScanMixer(dim, heads * width)
-                                    for i in range(layers))
+
+        def mixer(i):
+            if attention and (i + 1) % attention == 0:
+                return AttentionMixer(dim, heads, width)
+            return DeltaMixer(dim, heads, width) if i % 2 == 0 else ScanMixer(dim, heads * width)
+
+        self.mixers = nn.ModuleList(mixer(i) for i in range(layers))
         self.norms = nn.ParameterList(param(dim, value=1.0) for _ in range(layers + 1))
         self.scales = nn.ParameterList(param(dim, value=0.5) for _ in range(layers))
         self.head = nn.Linear(dim, vocab, bias=False)
@@ -205,10 +250,11 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--steps", type=int, default=100)
     ap.add_argument("--dtype", choices=["bfloat16", "float32"], default="bfloat16")
+    ap.add_argument("--attention", type=int, default=0, help="every N-th layer is attention (0: none)")
     a = ap.parse_args()
     torch.manual_seed(0)
     vocab = 64
-    model = HybridModel(vocab, dtype=getattr(torch, a.dtype)).cuda()
+    model = HybridModel(vocab, dtype=getattr(torch, a.dtype), attention=a.attention).cuda()
     losses = train(model, a.steps, vocab)
     print(f"loss {losses[0]:.3f} -> {losses[-1]:.3f} in {a.steps} steps")
     seq, diff = serve(model, vocab)
