@@ -406,6 +406,10 @@ __global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
   auto side = [&](int stage) { return reinterpret_cast<IT*>(stages + kStages * stage_bytes<IT, DP>() + stage * side_bytes<IT, DP>(rows)); };
   asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up, and waits
   if (blockIdx.x == 0 && tid == 0) *status = 0;  // (a wait that runs out sets it two seconds later)
+  if (tid == kThreads) {
+    tc::tma_prefetch_desc(&maps.k);
+    tc::tma_prefetch_desc(&maps.v);
+  }
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       tc::mbar_init(&full[i], 1);

@@ -102,6 +102,11 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
     tc::fence_barrier_init();
   }
   if (warp == 4 * NT) tc::tmem_alloc<512>(&tmem_slot);
+  if (warp == 4 * NT + 1 && lane == 0) {
+    tc::tma_prefetch_desc(&maps.q);
+    tc::tma_prefetch_desc(&maps.k);
+    tc::tma_prefetch_desc(&maps.v);
+  }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();

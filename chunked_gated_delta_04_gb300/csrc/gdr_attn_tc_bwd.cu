@@ -142,6 +142,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* const status = a.status;
   if (threadIdx.x == 0) bwd_barriers(b);
   if (warp == kMmaWarp) tc::tmem_alloc<512>(&b.tmem_slot);
+  if (warp == kLoadWarp && lane == 0) {
+    tc::tma_prefetch_desc(&maps.q);
+    tc::tma_prefetch_desc(&maps.k);
+    tc::tma_prefetch_desc(&maps.v);
+    tc::tma_prefetch_desc(&maps.dout);
+  }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -394,6 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* const status = a.status;
   if (threadIdx.x == 0) bwd_barriers(b);
   if (warp == kMmaWarp) tc::tmem_alloc<512>(&b.tmem_slot);
+  if (warp == kLoadWarp && lane == 0) {
+    tc::tma_prefetch_desc(&maps.q);
+    tc::tma_prefetch_desc(&maps.k);
+    tc::tma_prefetch_desc(&maps.v);
+    tc::tma_prefetch_desc(&maps.dout);
+  }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
