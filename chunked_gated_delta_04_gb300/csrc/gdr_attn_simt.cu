@@ -8,7 +8,7 @@
 //               dK += scale dS^T Q;  per 64 queries: dQ += scale dS K
 // A block is 16 x 16 threads; a thread holds 4 x 4 of S (rows ty + 16 r, columns tx + 16 c) and 4 rows by D / 16
 // features of an accumulator.  Bound by the FMA pipes and the shared-memory reads that feed them: 16 products for
-// every two 16-byte reads.  Where there are too few tiles to fill the SMs, the blocks of a cluster share a tile: each takes every
+// every two 16-byte reads; the next tiles are copied asynchronously beside them.  Where there are too few tiles to fill the SMs, the blocks of a cluster share a tile: each takes every
 // n-th step of its loop, and each sums the parts of some of the rows from the others' shared memory, in the order of their ranks
 // (1903 tokens in four sequences, 4 heads on 2, D = 64: forward 115 -> 56 us, dK and dV 393 -> 89, dQ 143 -> 66).
 #include "gdr_attn.cuh"
@@ -21,15 +21,16 @@ constexpr int kT = kSimtTile;
 constexpr int kThreads = 256;
 constexpr int kPS = kT + 4;  // row stride of a tile of P in floats
 
-// rows [r0, r0 + 64) of a head's [tokens, D] activations to shared memory [64][DP + 4] as fp32, zeros outside.
+// rows [r0, r0 + 64) of a head's [tokens, D] activations to shared memory [64][DP + 4] as fp32, zeros outside; there after
+// copy_async_wait and a barrier (copies that pass no registers, where type and alignment allow them).
 template <typename IT, int DP>
 __device__ __forceinline__ void load_tile(float* dst, const IT* src, long long ld, int r0, int rows, int D) {
   constexpr int S = DP + 4;
   if (sizeof(IT) == 4 && ((uintptr_t)src & 15) == 0 && ld % 4 == 0) {
     for (int e = threadIdx.x; e < kT * (DP / 4); e += kThreads) {
       const int r = e / (DP / 4), c = e % (DP / 4) * 4;
-      const float4 v = r0 + r < rows && c < D ? *reinterpret_cast<const float4*>(src + (long long)(r0 + r) * ld + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-      *reinterpret_cast<float4*>(dst + r * S + c) = v;
+      const bool on = r0 + r < rows && c < D;
+      copy_async<16>(dst + r * S + c, on ? src + (long long)(r0 + r) * ld + c : src, on ? 16 : 0);
     }
     return;
   }
@@ -159,7 +160,7 @@ constexpr size_t tile_bytes() { return sizeof(float) * kT * (DP + 4); }
 template <typename IT, int DP>
 __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnDims d, AttnTiles t, AttnFwdArgs a) {
   extern __shared__ float smem[];
-  float *Q = smem, *KV = Q + kT * (DP + 4), *P = KV + kT * (DP + 4);
+  float *Q = smem, *K = Q + kT * (DP + 4), *V = K + kT * (DP + 4), *P = V + kT * (DP + 4);
   if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *a.status = 0;  // of a packed batch: the tile table's kernel
   int seq, h, tile;
   const int n = cluster_size(), rank = n > 1 ? (int)tc::cluster_ctarank() : 0;
@@ -177,14 +178,14 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnDims d, Att
   int lo, hi;
   attn_keys(d, s, i0, min(s.n, i0 + kT), &lo, &hi);
   const float c = d.scale * kLog2e;
-  for (int j0 = (lo / kT + rank) * kT; j0 < hi; j0 += kT * n) {
-    __syncthreads();  // the values of the keys before are used up
-    load_tile<IT, DP>(KV, k, d.ld_k, j0, s.m, d.D);
-    __syncthreads();
+  const int begin = (lo / kT + rank) * kT;
+  if (begin < hi) load_tile<IT, DP>(K, k, d.ld_k, begin, s.m, d.D);
+  for (int j0 = begin; j0 < hi; j0 += kT * n) {
+    copy_async_wait();
+    __syncthreads();  // the keys are here, and the values and P of the step before used up
+    load_tile<IT, DP>(V, v, d.ld_v, j0, s.m, d.D);
     float S[4][4] = {};
-    dot_tile<DP>(Q, KV, tx, ty, S);
-    __syncthreads();
-    load_tile<IT, DP>(KV, v, d.ld_v, j0, s.m, d.D);
+    dot_tile<DP>(Q, K, tx, ty, S);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = i0 + ty + 16 * r;
@@ -217,12 +218,14 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnDims d, Att
 #pragma unroll
       for (int e = 0; e < DP / 16; ++e) O[r][e] *= f;
     }
+    copy_async_wait();
     __syncthreads();
-    row_product<DP>(P, KV, tx, ty, O);
+    if (j0 + kT * n < hi) load_tile<IT, DP>(K, k, d.ld_k, j0 + kT * n, s.m, d.D);
+    row_product<DP>(P, V, tx, ty, O);
   }
   if (n > 1) {  // every block's O, maxima and sums; then the rows of its share from all of them
     __syncthreads();
-    put_rows<DP, false>(KV, O, tx, ty);
+    put_rows<DP, false>(K, O, tx, ty);
     if (tx == 0)
 #pragma unroll
       for (int r = 0; r < 4; ++r) P[ty + 16 * r] = m[r], P[kT + ty + 16 * r] = l[r];
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnDims d, Att
         if (y >= n) break;
         const float f = ex2f(fmaf(mx[y], c, -base));
         sum = fmaf(load_peer(P + kT + r, y), f, sum);
-        o = fmaf(load_peer(KV + r * (DP + 4) + x, y), f, o);
+        o = fmaf(load_peer(K + r * (DP + 4) + x, y), f, o);
       }
       ((IT*)a.o)[(s.q0 + i) * (long long)d.Hq * d.D + (long long)h * d.D + x] = from_f32<IT>(top == -INFINITY ? 0.f : o / sum);
       if (x == 0) a.lse[s.lse0 + (long long)h * d.Tq + i] = top == -INFINITY ? -INFINITY : fmaf(top, d.scale, logf(sum));
@@ -299,7 +302,7 @@ template <typename IT, int DP>
 __global__ void __launch_bounds__(kThreads) attn_dkdv_simt_kernel(AttnDims d, AttnTiles t, AttnBwdArgs a) {
   extern __shared__ float smem[];
   constexpr int N = kT * (DP + 4);
-  float *K = smem, *V = K + N, *Q = V + N, *dO = Q + N, *M = dO + N;
+  float *K = smem, *V = K + N, *Q = V + N, *dO = Q + N, *Qn = dO + N, *M = Qn + N;  // Qn: the next step's
   int seq, h, tile;
   const int n = cluster_size(), rank = n > 1 ? (int)tc::cluster_ctarank() : 0;
   if (!attn_tile(d, t, d.Hk, blockIdx.x / n, &seq, &h, &tile)) return;
@@ -311,29 +314,45 @@ __global__ void __launch_bounds__(kThreads) attn_dkdv_simt_kernel(AttnDims d, At
   float dK[4][DP / 16] = {}, dV[4][DP / 16] = {};
   int lo, hi;
   attn_queries(d, s, j0, min(s.m, j0 + kT), &lo, &hi);
-  int step = 0;
-  for (int g = 0; g < d.G; ++g) {
-    const int hq = h * d.G + g;
+  const int first = lo / kT, length = lo < hi ? (hi + kT - 1) / kT - first : 0, steps = length * d.G;
+  // queries and gradients of a step: query head and first query
+  auto at_step = [&](int st, int* hq, int* i0) {
+    *hq = h * d.G + st / length;
+    *i0 = (first + st % length) * kT;
+  };
+  auto load = [&](float* dst, const void* from, long long ld, int st) {
+    int hq, i0;
+    at_step(st, &hq, &i0);
+    load_tile<IT, DP>(dst, (const IT*)from + s.q0 * ld + (long long)hq * d.D, ld, i0, s.n, d.D);
+  };
+  if (rank < steps) {
+    load(Q, a.q, d.ld_q, rank);
+    load(dO, a.dout, d.ld_do, rank);
+  }
+  for (int st = rank; st < steps; st += n) {
+    int hq, i0;
+    at_step(st, &hq, &i0);
     const long long stat = s.lse0 + (long long)hq * d.Tq;
-    for (int i0 = lo / kT * kT; i0 < hi; i0 += kT) {
-      if (step++ % n != rank) continue;
-      __syncthreads();
-      load_tile<IT, DP>(Q, (const IT*)a.q + s.q0 * d.ld_q + (long long)hq * d.D, d.ld_q, i0, s.n, d.D);
-      load_tile<IT, DP>(dO, (const IT*)a.dout + s.q0 * d.ld_do + (long long)hq * d.D, d.ld_do, i0, s.n, d.D);
-      __syncthreads();
-      float p[4][4], ds[4][4];
-      grad_tile<DP>(d, s, i0, j0, Q, K, dO, V, a.lse + stat, a.delta + stat, tx, ty, p, ds);
-      put_tile(M, p, tx, ty);
-      __syncthreads();
-      column_product<DP>(M, dO, tx, ty, dV);
-      __syncthreads();
-      put_tile(M, ds, tx, ty);
-      __syncthreads();
-      column_product<DP>(M, Q, tx, ty, dK);
-    }
+    copy_async_wait();
+    __syncthreads();
+    if (st + n < steps) load(Qn, a.q, d.ld_q, st + n);
+    float p[4][4], ds[4][4];
+    grad_tile<DP>(d, s, i0, j0, Q, K, dO, V, a.lse + stat, a.delta + stat, tx, ty, p, ds);
+    put_tile(M, p, tx, ty);
+    __syncthreads();
+    column_product<DP>(M, dO, tx, ty, dV);
+    __syncthreads();
+    if (st + n < steps) load(dO, a.dout, d.ld_do, st + n);
+    put_tile(M, ds, tx, ty);
+    __syncthreads();
+    column_product<DP>(M, Q, tx, ty, dK);
+    float* const t = Q;
+    Q = Qn;
+    Qn = t;
   }
   if (n > 1) {
     __syncthreads();
+    Q = smem + 2 * N;  // the same place in every block, whichever it had last
     put_rows<DP, true>(Q, dK, tx, ty);
     put_rows<DP, true>(dO, dV, tx, ty);
     tc::cluster_sync();
@@ -357,7 +376,7 @@ template <typename IT, int DP>
 __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(AttnDims d, AttnTiles t, AttnBwdArgs a) {
   extern __shared__ float smem[];
   constexpr int N = kT * (DP + 4);
-  float *Q = smem, *dO = Q + N, *K = dO + N, *V = K + N, *M = V + N;
+  float *Q = smem, *dO = Q + N, *K = dO + N, *V = K + N, *Kn = V + N, *M = Kn + N;  // Kn: the next step's
   int seq, h, tile;
   const int n = cluster_size(), rank = n > 1 ? (int)tc::cluster_ctarank() : 0;
   if (!attn_tile(d, t, d.Hq, blockIdx.x / n, &seq, &h, &tile)) return;
@@ -370,19 +389,31 @@ __global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(AttnDims d, Attn
   float dQ[4][DP / 16] = {};
   int lo, hi;
   attn_keys(d, s, i0, min(s.n, i0 + kT), &lo, &hi);
-  for (int j0 = (lo / kT + rank) * kT; j0 < hi; j0 += kT * n) {
+  const IT* const k = (const IT*)a.k + s.k0 * d.ld_k + (long long)hk * d.D;
+  const IT* const v = (const IT*)a.v + s.k0 * d.ld_v + (long long)hk * d.D;
+  const int begin = (lo / kT + rank) * kT;
+  if (begin < hi) {
+    load_tile<IT, DP>(K, k, d.ld_k, begin, s.m, d.D);
+    load_tile<IT, DP>(V, v, d.ld_v, begin, s.m, d.D);
+  }
+  for (int j0 = begin; j0 < hi; j0 += kT * n) {
+    const bool more = j0 + kT * n < hi;
+    copy_async_wait();
     __syncthreads();
-    load_tile<IT, DP>(K, (const IT*)a.k + s.k0 * d.ld_k + (long long)hk * d.D, d.ld_k, j0, s.m, d.D);
-    load_tile<IT, DP>(V, (const IT*)a.v + s.k0 * d.ld_v + (long long)hk * d.D, d.ld_v, j0, s.m, d.D);
-    __syncthreads();
+    if (more) load_tile<IT, DP>(Kn, k, d.ld_k, j0 + kT * n, s.m, d.D);
     float p[4][4], ds[4][4];
     grad_tile<DP>(d, s, i0, j0, Q, K, dO, V, a.lse + stat, a.delta + stat, tx, ty, p, ds);
     put_tile(M, ds, tx, ty);
     __syncthreads();
+    if (more) load_tile<IT, DP>(V, v, d.ld_v, j0 + kT * n, s.m, d.D);
     row_product<DP>(M, K, tx, ty, dQ);
+    float* const t = K;
+    K = Kn;
+    Kn = t;
   }
   if (n > 1) {
     __syncthreads();
+    K = smem + 2 * N;  // the same place in every block, whichever it had last
     put_rows<DP, false>(K, dQ, tx, ty);
     tc::cluster_sync();
     const long long at = (s.q0 + i0) * (long long)d.Hq * d.D + (long long)h * d.D;
@@ -426,12 +457,12 @@ cudaError_t go(F kernel, long long items, size_t smem, int resident, long long s
 
 template <typename IT, int DP>
 cudaError_t fwd(const AttnDims& d, const AttnTiles& t, const AttnFwdArgs& a, cudaStream_t s) {
-  return go(attn_fwd_simt_kernel<IT, DP>, attn_tile_count(d, false, kT) * d.Hq, 2 * tile_bytes<DP>() + sizeof(float) * kT * kPS, 2,
+  return go(attn_fwd_simt_kernel<IT, DP>, attn_tile_count(d, false, kT) * d.Hq, 3 * tile_bytes<DP>() + sizeof(float) * kT * kPS, DP == 64 ? 2 : 1,
             (d.Tk + kT - 1) / kT, d, t, a, s, "attn_fwd");
 }
 template <typename IT, int DP>
 cudaError_t bwd(const AttnDims& d, const AttnTiles& tq, const AttnTiles& tk, const AttnBwdArgs& a, cudaStream_t s) {
-  constexpr size_t smem = 4 * tile_bytes<DP>() + sizeof(float) * kT * kPS;
+  constexpr size_t smem = 5 * tile_bytes<DP>() + sizeof(float) * kT * kPS;
   constexpr int resident = DP == 64 ? 2 : 1;
   const cudaError_t e = go(attn_dkdv_simt_kernel<IT, DP>, attn_tile_count(d, true, kT) * d.Hk, smem, resident,
                            (long long)((d.Tq + kT - 1) / kT) * d.G, d, tk, a, s, "attn_dkdv");

@@ -5,7 +5,8 @@
 // per query with m the running maximum of its scores and l the running sum of e^..  A block takes two lanes of work through the
 // visible keys, 128 at a time, so that the tensor core works on one while the other's scores are exponentiated, and goes on to its
 // next item (persistent, one block per SM).  The lanes are two tiles of 128 queries of a head, or, where that leaves SMs without
-// work (Split), the even and the odd key blocks of one tile, which are joined at the end.  Roles:
+// work (Split), the even and the odd key blocks of one tile, which are joined at the end; where even these tiles are less than half
+// of the SMs, the blocks of a cluster take two of its lanes each, and are joined through shared memory.  Roles:
 //   warp 9     loads Q, then K and V tiles by TMA into a ring of slots
 //   warp 8     issues the MMAs: S_t = Q_t K_j^T (both operands in shared memory), O_t += P_t V_j (P_t from TMEM)
 //   warps 4 t  the softmax of lane t, a thread per query: S from TMEM to registers, P as bf16 to TMEM over S
@@ -71,7 +72,8 @@ __device__ __forceinline__ bool fwd_item(const AttnDims& d, const AttnTiles& t, 
   return true;
 }
 
-template <int DP, bool Split>
+// Split, and Share: the blocks of a cluster on one tile.
+template <int DP, bool Split, bool Share>
 __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
     attn_fwd_tc_kernel(const __grid_constant__ FwdMaps maps, AttnDims d, AttnTiles tiles, unsigned items, AttnFwdArgs a) {
   using Shape = FwdShape<DP, Split>;
@@ -80,6 +82,11 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
   __shared__ uint64_t q_full[NT], q_empty[NT], kv_full[ST], kv_empty[ST], s_full[NT], p_ready[NT], o_done[NT], tail_full, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ float joint[Split ? 2 : 1][2][NT][kTcBlock];  // Split: maxima and sums of an item's two lanes, of the next item's
+  const int n = Share ? attn_cluster_size() : 1, rank = Share ? (int)tc::cluster_ctarank() : 0;
+  // Split: the block's key blocks of an item are the first + own(i)-th ones, lane i & 1
+  auto own = [&](int i) { return (i >> 1) * 2 * n + 2 * rank + (i & 1); };
+  auto own_count = [&](int all) { return all <= 0 ? 0 : all / (2 * n) * 2 + max(0, min(2, all % (2 * n) - 2 * rank)); };
+  float* const part = reinterpret_cast<float*>(align1024(raw));  // shared items: the block's O, once its tiles are used up
   unsigned char* const sq = align1024(raw);
   unsigned char* const skv = sq + Q * Shape::kTile;
   const int warp = attn_warp(), lane = threadIdx.x & 31;
@@ -144,7 +151,7 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
     };
     FwdItem w;
     for (unsigned turn = 0; ok; ++turn) {
-      const long long x = attn_item(turn, items);
+      const long long x = attn_item(turn, items, n);
       if (x < 0) break;
       if (!fwd_item<Q>(d, tiles, (unsigned)x, &w)) continue;
       auto load_q = [&](int i) {
@@ -156,16 +163,20 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
         q_parity ^= 1u << i;
       };
       if (w.first >= w.last) continue;
-      if (w.hi[0]) load_q(0);
-      load_kv(&maps.k, w, w.first, false);
-      if (Q == 2 && w.hi[1]) load_q(1);
       if constexpr (Split) {  // the order in which they are used: two blocks of scores are ahead of the values
-        if (w.first + 1 < w.last) load_kv(&maps.k, w, w.first + 1, false);
-        for (int j = w.first; j < w.last && ok; ++j) {
-          load_kv(&maps.v, w, j, true);
-          if (j + 2 < w.last) load_kv(&maps.k, w, j + 2, false);
+        const int count = own_count(w.last - w.first);
+        if (count == 0) continue;
+        load_q(0);
+        load_kv(&maps.k, w, w.first + own(0), false);
+        if (count > 1) load_kv(&maps.k, w, w.first + own(1), false);
+        for (int i = 0; i < count && ok; ++i) {
+          load_kv(&maps.v, w, w.first + own(i), true);
+          if (i + 2 < count) load_kv(&maps.k, w, w.first + own(i + 2), false);
         }
       } else {
+        if (w.hi[0]) load_q(0);
+        load_kv(&maps.k, w, w.first, false);
+        if (w.hi[1]) load_q(1);
         for (int j = w.first; j < w.last && ok; ++j) {
           if (j > w.first) load_kv(&maps.k, w, j, false);
           load_kv(&maps.v, w, j, true);
@@ -188,42 +199,44 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
       bool ok = true;
       FwdItem w;
       for (unsigned turn = 0; ok; ++turn) {
-        const long long x = attn_item(turn, items);
+        const long long x = attn_item(turn, items, n);
         if (x < 0) break;
         if (!fwd_item<Q>(d, tiles, (unsigned)x, &w)) continue;
         auto scores = [&](int i, int slot, int j) {  // S_i of key block j
-          const int q = Split ? 0 : i;
-          attn_scores<DP>(tmem + i * 128, q_at + q * Shape::kTile, kv_at + slot * Shape::kTile, leader);
+          attn_scores<DP>(tmem + i * 128, q_at + i * Shape::kTile, kv_at + slot * Shape::kTile, leader);
           attn_commit(&s_full[i], leader);
-          if (j + 1 == w.hi[q]) attn_commit(&q_empty[q], leader);
+          if (j + 1 == w.hi[i]) attn_commit(&q_empty[i], leader);
         };
         if constexpr (Split) {
-          if (w.first >= w.last) continue;
-          auto next_scores = [&](int j) {
+          const int count = w.first < w.last ? own_count(w.last - w.first) : 0;
+          if (count == 0) continue;
+          auto next_scores = [&](int i) {
             ok = ok && attn_warp_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
             if (!ok) return;
             tc::tc_fence_after();
-            scores((j - w.first) & 1, ring.slot, j);
+            attn_scores<DP>(tmem + (i & 1) * 128, q_at, kv_at + ring.slot * Shape::kTile, leader);
+            attn_commit(&s_full[i & 1], leader);
+            if (i + 1 == count) attn_commit(&q_empty[0], leader);
             attn_commit(&kv_empty[ring.slot], leader);
             ring.next();
           };
           ok = attn_warp_wait(&q_full[0], q_parity & 1u, status, kDevErrTimeoutFwd);
           q_parity ^= 1u;
-          next_scores(w.first);
-          if (w.first + 1 < w.last) next_scores(w.first + 1);
-          for (int j = w.first; j < w.last && ok; ++j) {
-            const int i = (j - w.first) & 1;
+          next_scores(0);
+          if (count > 1) next_scores(1);
+          for (int j = 0; j < count && ok; ++j) {
+            const int i = j & 1;
             ok = attn_warp_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
             GDR_DELAY(48);
             ok = ok && attn_warp_wait(&p_ready[i], p_parity >> i & 1u, status, kDevErrTimeoutFwd);
             p_parity ^= 1u << i;
             if (!ok) break;
             tc::tc_fence_after();
-            attn_product<DP>(tmem + Shape::kO + i * DP, tmem + i * 128, kv_at + ring.slot * Shape::kTile, j > w.first + 1, leader);
+            attn_product<DP>(tmem + Shape::kO + i * DP, tmem + i * 128, kv_at + ring.slot * Shape::kTile, j > 1, leader);
             attn_commit(&o_done[i], leader);
             attn_commit(&kv_empty[ring.slot], leader);
             ring.next();
-            if (j + 2 < w.last) next_scores(j + 2);
+            if (j + 2 < count) next_scores(j + 2);
           }
           continue;
         }
@@ -293,20 +306,20 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
     bool ok = true;
     // (Split: where a wait has run out a warpgroup goes on without waiting, so that the other is not left at their barriers.)
     for (unsigned turn = 0; Split || ok; ++turn) {
-      const long long x = attn_item(turn, items);
+      const long long x = attn_item(turn, items, n);
       if (x < 0) break;
       if (!fwd_item<Q>(d, tiles, (unsigned)x, &w)) continue;
       const int first_row = w.i0 + (Split ? 0 : t * kTcBlock), i = first_row + row, off = w.s.m - w.s.n;
-      int lo = w.lo[0], hi = w.hi[0];  // Split: every second of them, from lo + t on
+      int lo = w.lo[0], hi = w.hi[0];  // Split: the lane's of them, from begin on
       if (!Split && t == 1) lo = w.lo[1], hi = w.hi[1];
-      const int begin = Split ? lo + t : lo;
+      const int begin = Split ? lo + 2 * rank + t : lo;
       // the keys [from, to) that this query sees
       const int from = d.window ? max(0, i + off - d.window + 1) : 0, to = d.causal ? min(w.s.m, i + off + 1) : w.s.m;
       // blocks [clear, full) are seen whole by all of the tile's queries
       const int i_first = first_row, i_last = i_first + kTcBlock - 1;
       const int whole_to = (d.causal ? min(w.s.m, i_first + off + 1) : w.s.m), whole_from = d.window ? i_last + off - d.window + 1 : 0;
       float m = -INFINITY, l = 0.f;
-      for (int j = begin; j < hi && ok; j += Split ? 2 : 1) {
+      for (int j = begin; j < hi && ok; j += Split ? 2 * n : 1) {
         ok = attn_warp_wait(&s_full[t], parity, status, kDevErrTimeoutFwd);
         if (!ok) break;
         tc::tc_fence_after();
@@ -391,10 +404,19 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
         const float m0 = of[0][0][row], m1 = of[0][1][row], top = fmaxf(m0, m1);
         const float f0 = m0 == -INFINITY ? 0.f : ex2f((m0 - top) * c), f1 = m1 == -INFINITY ? 0.f : ex2f((m1 - top) * c);
         const float sum = fmaf(of[1][0][row], f0, of[1][1][row] * f1);
-        const float by = top == -INFINITY ? 0.f : 1.f / sum;
         const int f = t * (DP / 2);
-        attn_store_row<DP / 2>(tc::tmem_lane_addr(tmem, warp, Shape::kO + f), tc::tmem_lane_addr(tmem, warp, Shape::kO + DP + f), out + f, d.D - f,
-                               f0 * by, f1 * by, lo < hi, lo + 1 < hi, mine);
+        const uint32_t o0 = tc::tmem_lane_addr(tmem, warp, Shape::kO + f), o1 = tc::tmem_lane_addr(tmem, warp, Shape::kO + DP + f);
+        const bool any0 = lo + 2 * rank < hi, any1 = lo + 2 * rank + 1 < hi;
+        if constexpr (Share) {
+          put_part<DP, DP / 2>(part, row, f, o0, o1, f0, f1, any0, any1);
+          if (t == 0) {  // to the second set, which one item leaves unused
+            joint[Split][0][0][row] = top;
+            joint[Split][1][0][row] = sum;
+          }
+          continue;
+        }
+        const float by = top == -INFINITY ? 0.f : 1.f / sum;
+        attn_store_row<DP / 2>(o0, o1, out + f, d.D - f, f0 * by, f1 * by, any0, any1, mine);
         if (mine && t == 0) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = top == -INFINITY ? -INFINITY : fmaf(top, d.scale, logf(sum));
         tc::tc_fence_before();
         tc::named_sync(1, 2 * kTcBlock);  // both lanes' O are read before either is begun anew
@@ -405,6 +427,35 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
       }
       tc::tc_fence_before();  // O is read before this item's successor's first product into it, which the next arrival allows
     }
+  }
+  if constexpr (Share) {  // the cluster's one item: every block has its share of the queries
+    __syncwarp();
+    tc::cluster_sync();
+    FwdItem w;
+    const long long x = attn_item(0, items, n);
+    if (warp < 4 * NT && x >= 0 && fwd_item<Q>(d, tiles, (unsigned)x, &w)) {
+      const int r0 = kTcBlock * rank / n, r1 = min(kTcBlock * (rank + 1) / n, w.s.n - w.i0);
+      const float c = d.scale * kLog2e;
+      for (int e = threadIdx.x; e < (r1 - r0) * (DP / 4); e += 2 * kTcBlock) {
+        const int r = r0 + e / (DP / 4), piece = e % (DP / 4), i = w.i0 + r;
+        float top = -INFINITY, sum = 0.f;
+        for (int y = 0; y < n; ++y) top = fmaxf(top, load_peer(&joint[Split][0][0][r], y));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int y = 0; y < n; ++y) {
+          const float m = load_peer(&joint[Split][0][0][r], y), f = m == -INFINITY ? 0.f : ex2f((m - top) * c);
+          const float4 v = load_peer4(part + part_at<DP>(r, piece), y);
+          sum = fmaf(load_peer(&joint[Split][1][0][r], y), f, sum);
+          o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+        }
+        const float by = top == -INFINITY ? 0.f : 1.f / sum;
+        if (4 * piece < d.D)
+          store4((__nv_bfloat16*)a.o + ((w.s.q0 + i) * d.Hq + w.h) * (long long)d.D + 4 * piece,
+                 top == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
+        if (piece == 0) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = top == -INFINITY ? -INFINITY : fmaf(top, d.scale, logf(sum));
+      }
+    }
+    __syncwarp();
+    tc::cluster_sync();  // no block ends while others read it
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -419,11 +470,13 @@ cudaError_t fwd(const AttnDims& d, const AttnTiles& t, const AttnFwdArgs& a, cud
   if (!attn_map(&maps.q, a.q, d.D, d.Hq, rows_q, d.ld_q) || !attn_map(&maps.k, a.k, d.D, d.Hk, rows_k, d.ld_k) ||
       !attn_map(&maps.v, a.v, d.D, d.Hk, rows_k, d.ld_v))
     return cudaErrorInvalidValue;
-  const auto kernel = attn_fwd_tc_kernel<DP, Split>;
+  const long long items = attn_tile_count(d, false, Shape::kQ * kTcBlock) * d.Hq;
+  const int n = Split ? attn_sharers(items, (d.Tk + 2 * kTcBlock - 1) / (2 * kTcBlock)) : 1;
+  const auto kernel = n > 1 ? attn_fwd_tc_kernel<DP, Split, Split> : attn_fwd_tc_kernel<DP, Split, false>;
   cudaError_t e = set_smem_once((const void*)kernel, Shape::kSmem);
   if (e != cudaSuccess) return e;
-  const long long items = attn_tile_count(d, false, Shape::kQ * kTcBlock) * d.Hq;
-  kernel<<<(unsigned)std::min<long long>(items, kSmCount), Shape::kThreads, Shape::kSmem, s>>>(maps, d, t, (unsigned)items, a);
+  e = attn_launch(kernel, n > 1 ? items * n : std::min<long long>(items, kSmCount), Shape::kThreads, Shape::kSmem, n, s, maps, d, t, (unsigned)items, a);
+  if (e != cudaSuccess) return e;
   stage_mark(s, "attn_fwd");
   return cudaGetLastError();
 }

@@ -35,8 +35,9 @@ __device__ __forceinline__ void attn_clear_rows(unsigned char* tile, int from) {
 // a step of 16 rows is 2 KB on.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8-row groups 1024 bytes apart, 128-byte swizzle
 constexpr uint32_t kSlabBytes = kTcBlock * 128;
-__device__ __forceinline__ uint32_t desc_kmajor(uint32_t saddr) { return saddr >> 4 | 1u << 16; }
-__device__ __forceinline__ uint32_t desc_mnmajor(uint32_t saddr) { return saddr >> 4 | (kSlabBytes >> 4) << 16; }
+// (In a cluster an address in shared memory has the block's rank above its low 18 bits.)
+__device__ __forceinline__ uint32_t desc_kmajor(uint32_t saddr) { return (saddr >> 4 & 0x3FFFu) | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mnmajor(uint32_t saddr) { return (saddr >> 4 & 0x3FFFu) | (kSlabBytes >> 4) << 16; }
 __device__ __forceinline__ constexpr uint32_t kmajor_step(int kk) { return (uint32_t)(kk >> 2) * (kSlabBytes >> 4) + (uint32_t)(kk & 3) * 2u; }
 __device__ __forceinline__ constexpr uint32_t mnmajor_step(int kk) { return (uint32_t)kk * 128u; }
 
@@ -182,10 +183,109 @@ inline bool attn_map(CUtensorMap* m, const void* base, int D, int H, long long r
 
 // Work item `turn` of a block: items lie by falling work, and the rounds of the grid take them forth and back, so that a block
 // that had the largest of one round gets the smallest of the next.  -1: none is left.
-__device__ __forceinline__ long long attn_item(unsigned turn, unsigned items) {
-  const long long first = (long long)turn * gridDim.x;
-  const long long x = first + (turn & 1u ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+// Where there are fewer items than SMs, the blocks of a cluster share one (blocks: n of them); it is their only one.
+__device__ __forceinline__ long long attn_item(unsigned turn, unsigned items, unsigned n = 1) {
+  const unsigned block = blockIdx.x / n, grid = gridDim.x / n;
+  const long long first = (long long)turn * grid;
+  const long long x = first + (turn & 1u ? grid - 1 - block : block);
   return x < items ? x : -1;
+}
+
+// Blocks that share an item: as many as SMs allow, at most 8, and no more than an item has steps.
+inline int attn_sharers(long long items, long long steps) {
+  int n = 1;
+  while (n < 8 && items * 2 * n <= kSmCount && 2 * n <= steps) n *= 2;
+  return n;
+}
+__device__ __forceinline__ int attn_cluster_size() {
+  uint32_t n;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return (int)n;
+}
+template <typename F, typename... Args>
+inline cudaError_t attn_launch(F kernel, long long grid, int threads, size_t smem, int cluster, cudaStream_t s, Args... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3((unsigned)grid);
+  config.blockDim = dim3((unsigned)threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = s;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, args...);
+}
+
+// Columns [c0, c0 + N) of a row of this block's part [128][DP] in shared memory: 16-byte pieces, placed by the row so that rows do not
+// meet in a bank.
+template <int DP>
+__device__ __forceinline__ uint32_t part_at(int row, int piece) {
+  return (uint32_t)(row * DP + 4 * ((piece ^ row) & (DP / 4 - 1)));
+}
+template <int DP, int N>
+__device__ __forceinline__ void put_part(float* part, int row, int c0, uint32_t taddr, float f, bool any) {
+#pragma unroll
+  for (int e = 0; e < N; e += 16) {
+    float o[16];
+    if (any) {
+      tc::tmem_ld16(taddr + e, o);
+      tc::tmem_wait_ld();
+    }
+#pragma unroll
+    for (int y = 0; y < 16; y += 4)
+      *reinterpret_cast<float4*>(part + part_at<DP>(row, (c0 + e + y) / 4)) =
+          any && f != 0.f ? make_float4(o[y] * f, o[y + 1] * f, o[y + 2] * f, o[y + 3] * f) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+// The same of the sum of two accumulators' rows, times f0 and f1.
+template <int DP, int N>
+__device__ __forceinline__ void put_part(float* part, int row, int c0, uint32_t taddr0, uint32_t taddr1, float f0, float f1, bool any0, bool any1) {
+#pragma unroll
+  for (int e = 0; e < N; e += 16) {
+    float o[16], p[16];
+    if (any0) tc::tmem_ld16(taddr0 + e, o);
+    if (any1) tc::tmem_ld16(taddr1 + e, p);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int y = 0; y < 16; ++y) o[y] = (any0 && f0 != 0.f ? o[y] * f0 : 0.f) + (any1 && f1 != 0.f ? p[y] * f1 : 0.f);
+#pragma unroll
+    for (int y = 0; y < 16; y += 4)
+      *reinterpret_cast<float4*>(part + part_at<DP>(row, (c0 + e + y) / 4)) = make_float4(o[y], o[y + 1], o[y + 2], o[y + 3]);
+  }
+}
+// 16 bytes at the same place of another block's shared memory.
+__device__ __forceinline__ float4 load_peer4(const float* p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(tc::mapa(tc::smem_u32(p), (uint32_t)rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_peer(const float* p, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::mapa(tc::smem_u32(p), (uint32_t)rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const float x[4] = {v.x, v.y, v.z, v.w};
+  store_v<4>(p, x);
+}
+// This block's share of the rows, summed over the n blocks' parts in the order of their ranks, times f; by 256 threads.
+template <int DP>
+__device__ __forceinline__ void sum_parts(const float* part, int rank, int n, __nv_bfloat16* out, long long ld, int rows, int D, float f) {
+  const int r0 = kTcBlock * rank / n, r1 = min(rows, kTcBlock * (rank + 1) / n);
+  for (int e = threadIdx.x; e < (r1 - r0) * (DP / 4); e += 256) {
+    const int r = r0 + e / (DP / 4), q = e % (DP / 4);
+    if (4 * q >= D) continue;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < n; ++x) {
+      const float4 v = load_peer4(part + part_at<DP>(r, q), x);
+      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+    store4(out + (long long)r * ld + 4 * q, make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f));
+  }
 }
 
 }  // namespace gdr

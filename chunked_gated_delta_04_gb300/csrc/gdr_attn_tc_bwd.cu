@@ -11,6 +11,8 @@
 //            products' operands from TMEM.  TMEM: S^T, dP^T 128 columns each, dV, dK: all 512.  Issue order: dV, next S^T, dK, next
 //            dP^T; P is formed beside dK and dP^T, dS beside dV and the next S^T.  A spare warp brings lse and delta.
 //   queries: S = Q K^T and dP = dO V^T free their columns as soon as they are in registers; dS has two places of its own.
+// Where the tiles are less than half of the SMs (few key heads, short sequences), the blocks of a cluster share one (Share): each
+// takes every n-th step, and sums some of the rows from all blocks' shared memory, in the order of their ranks.
 #include <algorithm>
 
 #include "gdr_attn_tc.cuh"
@@ -129,7 +131,7 @@ __device__ __forceinline__ bool key_item(const AttnDims& d, const AttnTiles& t, 
   return true;
 }
 
-template <int DP>
+template <int DP, bool Share>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dkdv_tc_kernel(const __grid_constant__ BwdMaps maps, AttnDims d, AttnTiles tiles, unsigned items, AttnBwdArgs a) {
   constexpr uint32_t kTile = attn_tile_bytes<DP>();
@@ -152,6 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = b.tmem_slot;
+  const int n = Share ? attn_cluster_size() : 1, rank = Share ? (int)tc::cluster_ctarank() : 0;
+  float* const part = reinterpret_cast<float*>(bwd_raw);  // Share: the block's sums, once its tiles are used up
   KeyItem w;
   bool ok = true;
 
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     BwdLoader<DP, kB> dos{b, b_at, b.b_full, b.b_empty, status};
     uint32_t kv_parity = 0, tail_parity = 0;
     for (unsigned turn = 0; ok; ++turn) {
-      const long long x = attn_item(turn, items);
+      const long long x = attn_item(turn, items, n);
       if (x < 0) break;
       if (!key_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
       auto load_kv = [&](int which, const CUtensorMap* map) {
@@ -170,13 +174,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           attn_load_tile<DP>(keep + which * kTile, map, &b.keep_full[which], w.h, w.s.k0 + w.j0);
         }
       };
+      const int length = w.hi - w.lo, steps = length * d.G;
+      if (rank >= steps) continue;
       load_kv(0, &maps.k);
-      for (int g = 0; g < d.G && ok; ++g)
-        for (int i = w.lo; i < w.hi && ok; ++i) {
+      for (int st = rank; st < steps && ok; st += n) {
+          const int g = st / length, i = w.lo + st % length;
           const long long r0 = w.s.q0 + (long long)i * kTcBlock;
           const int rows = w.s.n - i * kTcBlock;
           ok = qs.load(&maps.q, w.h * d.G + g, r0, rows, true, tail_parity);
-          if (g == 0 && i == w.lo) load_kv(1, &maps.v);
+          if (st == rank) load_kv(1, &maps.v);
           ok = ok && dos.load(&maps.dout, w.h * d.G + g, r0, rows, true, tail_parity);
         }
       kv_parity ^= 1u;
@@ -198,10 +204,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
       };
       for (unsigned turn = 0; ok; ++turn) {
-        const long long x = attn_item(turn, items);
+        const long long x = attn_item(turn, items, n);
         if (x < 0) break;
         if (!key_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
-        const int steps = (w.hi - w.lo) * d.G;
+        const int steps = ((w.hi - w.lo) * d.G - rank + n - 1) / n;  // the block's
+        if (steps <= 0) continue;
         auto scores = [&](bool last) {  // S^T of the next step
           if (!wait(&b.a_full[qs.slot], qs.parity)) return;
           attn_scores<DP>(tmem + kS, k_at, q_at + qs.slot * kTile, leader);
@@ -247,12 +254,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kStatWarp) {
     AttnRing<2> ring;
     for (unsigned turn = 0; ok; ++turn) {
-      const long long x = attn_item(turn, items);
+      const long long x = attn_item(turn, items, n);
       if (x < 0) break;
       if (!key_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
-      for (int g = 0; g < d.G && ok; ++g) {
-        const long long at = w.s.lse0 + (long long)(w.h * d.G + g) * d.Tq;
-        for (int i = w.lo; i < w.hi; ++i) {
+      const int length = w.hi - w.lo, steps = length * d.G;
+      for (int st = rank; st < steps; st += n) {
+          const int g = st / length, i = w.lo + st % length;
+          const long long at = w.s.lse0 + (long long)(w.h * d.G + g) * d.Tq;
           float ls[4], dl[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -272,7 +280,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&b.stat_full[ring.slot]);
           ring.next();
-        }
       }
     }
   } else if (warp < 8) {
@@ -282,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t parity = 0, done_parity = 0;
     AttnRing<2> ring;
     for (unsigned turn = 0; ok; ++turn) {
-      const long long x = attn_item(turn, items);
+      const long long x = attn_item(turn, items, n);
       if (x < 0) break;
       if (!key_item(d, tiles, (unsigned)x, &w)) continue;
       const int j = w.j0 + row, off = w.s.m - w.s.n;
@@ -292,8 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j_last = w.j0 + kTcBlock - 1;
       const int whole_from = d.causal ? j_last - off : 0;
       const long long whole_to = d.window ? (long long)w.j0 - off + d.window : (1ll << 40);
-      for (int g = 0; g < d.G && ok; ++g)
-        for (int i = w.lo; i < w.hi; ++i) {
+      const int length = w.hi - w.lo, steps = length * d.G;
+      for (int st = rank; st < steps; st += n) {
+          const int i = w.lo + (d.G == 1 ? st : st % length);
           ok = attn_warp_wait(&b.stat_full[ring.slot], ring.parity, status, kDevErrTimeoutBwd);
           ok = ok && attn_warp_wait(&b.s_full, parity, status, kDevErrTimeoutBwd);
           if (!ok) break;
@@ -352,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ring.next();
         }
       if (!ok) break;
-      const bool any = w.lo < w.hi;
+      const bool any = rank < steps;
       if (any) {
         ok = attn_warp_wait(&b.done, done_parity, status, kDevErrTimeoutBwd);
         done_parity ^= 1u;
@@ -360,10 +368,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_after();
       }
       // the first warpgroup stores dV, the second dK
-      __nv_bfloat16* const out = (__nv_bfloat16*)(half ? a.dk : a.dv) + ((w.s.k0 + j) * d.Hk + w.h) * (long long)d.D;
-      attn_store_row<DP>(tc::tmem_lane_addr(tmem, warp, half ? kdK : kdV), out, d.D, half ? d.scale : 1.f, any, j < w.s.m);
+      const uint32_t from_t = tc::tmem_lane_addr(tmem, warp, half ? kdK : kdV);
+      if constexpr (Share) {
+        put_part<DP, DP>(part + half * kTcBlock * DP, row, 0, from_t, half ? d.scale : 1.f, any);
+      } else {
+        __nv_bfloat16* const out = (__nv_bfloat16*)(half ? a.dk : a.dv) + ((w.s.k0 + j) * d.Hk + w.h) * (long long)d.D;
+        attn_store_row<DP>(from_t, out, d.D, half ? d.scale : 1.f, any, j < w.s.m);
+      }
       tc::tc_fence_before();  // read before the next item's first product into them, which the next arrival allows
     }
+  }
+  if constexpr (Share) {
+    __syncwarp();
+    tc::cluster_sync();
+    const long long x = attn_item(0, items, n);
+    if (warp < 8 && x >= 0 && key_item(d, tiles, (unsigned)x, &w)) {
+      const long long at = ((w.s.k0 + w.j0) * d.Hk + w.h) * (long long)d.D, ld = (long long)d.Hk * d.D;
+      sum_parts<DP>(part, rank, n, (__nv_bfloat16*)a.dv + at, ld, w.s.m - w.j0, d.D, 1.f);
+      sum_parts<DP>(part + kTcBlock * DP, rank, n, (__nv_bfloat16*)a.dk + at, ld, w.s.m - w.j0, d.D, 1.f);
+    }
+    __syncwarp();
+    tc::cluster_sync();  // no block ends while others read it
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -387,7 +412,7 @@ __device__ __forceinline__ bool query_item(const AttnDims& d, const AttnTiles& t
   return true;
 }
 
-template <int DP>
+template <int DP, bool Share>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dq_tc_kernel(const __grid_constant__ BwdMaps maps, AttnDims d, AttnTiles tiles, unsigned items, AttnBwdArgs a) {
   constexpr uint32_t kTile = attn_tile_bytes<DP>();
@@ -410,6 +435,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = b.tmem_slot;
+  const int n = Share ? attn_cluster_size() : 1, rank = Share ? (int)tc::cluster_ctarank() : 0;
+  float* const part = reinterpret_cast<float*>(bwd_raw);  // Share: the block's sums, once its tiles are used up
   QueryItem w;
   bool ok = true;
 
@@ -418,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     BwdLoader<DP, kB> vs{b, b_at, b.b_full, b.b_empty, status};
     uint32_t q_parity = 0, tail_parity = 0;
     for (unsigned turn = 0; ok; ++turn) {
-      const long long x = attn_item(turn, items);
+      const long long x = attn_item(turn, items, n);
       if (x < 0) break;
       if (!query_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
       auto load_q = [&](int which, const CUtensorMap* map) {
@@ -428,12 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           attn_load_tile<DP>(keep + which * kTile, map, &b.keep_full[which], w.h, w.s.q0 + w.i0);
         }
       };
+      if (w.lo + rank >= w.hi) continue;
       load_q(0, &maps.q);
-      for (int j = w.lo; j < w.hi && ok; ++j) {
+      for (int j = w.lo + rank; j < w.hi && ok; j += n) {
         const long long r0 = w.s.k0 + (long long)j * kTcBlock;
         const int rows = w.s.m - j * kTcBlock;
         ok = ks.load(&maps.k, w.h / d.G, r0, rows, true, tail_parity);
-        if (j == w.lo) load_q(1, &maps.dout);
+        if (j == w.lo + rank) load_q(1, &maps.dout);
         ok = ok && vs.load(&maps.v, w.h / d.G, r0, rows, false, tail_parity);  // values are not summed here
       }
       q_parity ^= 1u;
@@ -456,10 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
       };
       for (unsigned turn = 0; ok; ++turn) {
-        const long long x = attn_item(turn, items);
+        const long long x = attn_item(turn, items, n);
         if (x < 0) break;
         if (!query_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
-        const int steps = w.hi - w.lo;
+        const int steps = (w.hi - w.lo - rank + n - 1) / n;  // the block's
+        if (steps <= 0) continue;
         auto scores = [&](int it) {  // S and dP of a step
           if (it == 0) wait(&b.keep_full[0], q_parity);
           wait(&b.a_full[ks.slot], ks.parity);
@@ -507,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = d.scale * kLog2e;
     uint32_t parity = 0, done_parity = 0, place = 0;
     for (unsigned turn = 0; ok; ++turn) {
-      const long long x = attn_item(turn, items);
+      const long long x = attn_item(turn, items, n);
       if (x < 0) break;
       if (!query_item(d, tiles, (unsigned)x, &w)) continue;
       const int i = w.i0 + row, off = w.s.m - w.s.n;
@@ -519,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int from = d.window ? max(0, i + off - d.window + 1) : 0, to = d.causal ? min(w.s.m, i + off + 1) : w.s.m;
       const int i_last = w.i0 + kTcBlock - 1;
       const int whole_to = d.causal ? min(w.s.m, w.i0 + off + 1) : w.s.m, whole_from = d.window ? i_last + off - d.window + 1 : 0;
-      for (int j = w.lo; j < w.hi; ++j) {
+      for (int j = w.lo + rank; j < w.hi; j += n) {
         ok = attn_warp_wait(&b.s_full, parity, status, kDevErrTimeoutBwd);
         if (!ok) break;
         tc::tc_fence_after();
@@ -560,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         place ^= 1u;
       }
       if (!ok) break;
-      const bool any = w.lo < w.hi;
+      const bool any = w.lo + rank < w.hi;
       if (any) {
         ok = attn_warp_wait(&b.done, done_parity, status, kDevErrTimeoutBwd);
         done_parity ^= 1u;
@@ -568,10 +597,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tc_fence_after();
       }
       // each warpgroup stores half of the features
-      __nv_bfloat16* const out = (__nv_bfloat16*)a.dq + ((w.s.q0 + i) * d.Hq + w.h) * (long long)d.D + half * (DP / 2);
-      attn_store_row<DP / 2>(tc::tmem_lane_addr(tmem, warp, kdQ + half * (DP / 2)), out, d.D - half * (DP / 2), d.scale, any, mine);
+      const uint32_t from_t = tc::tmem_lane_addr(tmem, warp, kdQ + half * (DP / 2));
+      if constexpr (Share) {
+        put_part<DP, DP / 2>(part, row, half * (DP / 2), from_t, d.scale, any);
+      } else {
+        __nv_bfloat16* const out = (__nv_bfloat16*)a.dq + ((w.s.q0 + i) * d.Hq + w.h) * (long long)d.D + half * (DP / 2);
+        attn_store_row<DP / 2>(from_t, out, d.D - half * (DP / 2), d.scale, any, mine);
+      }
       tc::tc_fence_before();  // read before the next item's first product into it, which the next arrival allows
     }
+  }
+  if constexpr (Share) {
+    __syncwarp();
+    tc::cluster_sync();
+    const long long x = attn_item(0, items, n);
+    if (warp < 8 && x >= 0 && query_item(d, tiles, (unsigned)x, &w)) {
+      const long long at = ((w.s.q0 + w.i0) * d.Hq + w.h) * (long long)d.D, ld = (long long)d.Hq * d.D;
+      sum_parts<DP>(part, rank, n, (__nv_bfloat16*)a.dq + at, ld, w.s.n - w.i0, d.D, 1.f);
+    }
+    __syncwarp();
+    tc::cluster_sync();  // no block ends while others read it
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -585,18 +630,22 @@ cudaError_t bwd(const AttnDims& d, const AttnTiles& tq, const AttnTiles& tk, con
   if (!attn_map(&maps.q, a.q, d.D, d.Hq, rows_q, d.ld_q) || !attn_map(&maps.k, a.k, d.D, d.Hk, rows_k, d.ld_k) ||
       !attn_map(&maps.v, a.v, d.D, d.Hk, rows_k, d.ld_v) || !attn_map(&maps.dout, a.dout, d.D, d.Hq, rows_q, d.ld_do))
     return cudaErrorInvalidValue;
-  constexpr size_t smem = bwd_smem<DP>();
-  cudaError_t e = set_smem_once((const void*)attn_dkdv_tc_kernel<DP>, smem);
-  if (e == cudaSuccess) e = set_smem_once((const void*)attn_dq_tc_kernel<DP>, smem);
+  auto go = [&](auto kernel, auto shared, long long items, long long steps, const AttnTiles& t, const char* stage) {
+    constexpr size_t smem = bwd_smem<DP>();
+    const int n = attn_sharers(items, steps);
+    cudaError_t e = set_smem_once(n > 1 ? (const void*)shared : (const void*)kernel, smem);
+    if (e != cudaSuccess) return e;
+    e = n > 1 ? attn_launch(shared, items * n, kThreads, smem, n, s, maps, d, t, (unsigned)items, a)
+              : attn_launch(kernel, std::min<long long>(items, kSmCount), kThreads, smem, 1, s, maps, d, t, (unsigned)items, a);
+    if (e != cudaSuccess) return e;
+    stage_mark(s, stage);
+    return cudaGetLastError();
+  };
+  const cudaError_t e = go(attn_dkdv_tc_kernel<DP, false>, attn_dkdv_tc_kernel<DP, true>, attn_tile_count(d, true, kTcBlock) * d.Hk,
+                           (long long)((d.Tq + kTcBlock - 1) / kTcBlock) * d.G, tk, "attn_dkdv");
   if (e != cudaSuccess) return e;
-  const long long keys = attn_tile_count(d, true, kTcBlock) * d.Hk, queries = attn_tile_count(d, false, kTcBlock) * d.Hq;
-  attn_dkdv_tc_kernel<DP><<<(unsigned)std::min<long long>(keys, kSmCount), kThreads, smem, s>>>(maps, d, tk, (unsigned)keys, a);
-  stage_mark(s, "attn_dkdv");
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  attn_dq_tc_kernel<DP><<<(unsigned)std::min<long long>(queries, kSmCount), kThreads, smem, s>>>(maps, d, tq, (unsigned)queries, a);
-  stage_mark(s, "attn_dq");
-  return cudaGetLastError();
+  return go(attn_dq_tc_kernel<DP, false>, attn_dq_tc_kernel<DP, true>, attn_tile_count(d, false, kTcBlock) * d.Hq,
+            (d.Tk + kTcBlock - 1) / kTcBlock, tq, "attn_dq");
 }
 
 }  // namespace

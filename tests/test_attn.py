@@ -173,6 +173,21 @@ def test_attention_heads(dtype, Hq, Hk):
     attn_case(dtype, [200], [200], Hq, Hk, 128, scale=0.3, packed=False)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("D,n,m,Hq,Hk,B", [(128, 150, 150, 20, 20, 4), (64, 260, 129, 32, 16, 3), (80, 129, 400, 24, 24, 2)])
+def test_attention_many_tiles(dtype, D, n, m, Hq, Hk, B):
+    """Tiles enough that no two blocks share one, and that blocks take several."""
+    attn_case(dtype, [n] * B, [m] * B, Hq, Hk, D, packed=False)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("n,m,Hq,Hk", [(1, 5000, 2, 1), (100, 3001, 1, 1), (2000, 2000, 3, 1), (640, 640, 16, 2), (129, 1500, 6, 2)])
+def test_attention_few_tiles(dtype, n, m, Hq, Hk):
+    """Few tiles of many steps, which blocks share."""
+    attn_case(dtype, [n], [m], Hq, Hk, 64, packed=False)
+    attn_case(dtype, [n], [m], Hq, Hk, 128, window=700, packed=False, train=n > 1)
+
+
 PACKED = [([130, 1, 0, 257, 64], None), ([100, 0, 33, 5], [300, 40, 0, 2]), ([0, 0], [5, 0]), ([20, 30, 300], [0, 0, 0]), ([128, 128, 1], None),
           ([3] * 40, [5] * 40)]
 
