@@ -10,7 +10,7 @@
 // features of an accumulator.  Bound by the FMA pipes and the shared-memory reads that feed them: 16 products for
 // every two 16-byte reads; the next tiles are copied asynchronously beside them.  Where there are too few tiles to fill the SMs, the blocks of a cluster share a tile: each takes every
 // n-th step of its loop, and each sums the parts of some of the rows from the others' shared memory, in the order of their ranks
-// (1903 tokens in four sequences, 4 heads on 2, D = 64: forward 115 -> 56 us, dK and dV 393 -> 89, dQ 143 -> 66).
+// (1903 tokens in four sequences, 4 heads on 2, D = 64: forward 115 -> 46 us, dK and dV 393 -> 77, dQ 143 -> 57, copies beside the products and packed sums included).
 #include "gdr_attn.cuh"
 #include "tc_primitives.cuh"
 
@@ -46,11 +46,29 @@ __device__ __forceinline__ int cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
   return (int)n;
 }
-// A float at the same place of another block's shared memory.
+// A float, or four, at the same place of another block's shared memory.
 __device__ __forceinline__ float load_peer(const float* p, int rank) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::mapa(tc::smem_u32(p), (uint32_t)rank)) : "memory");
   return v;
+}
+__device__ __forceinline__ float4 load_peer4(const float* p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(tc::mapa(tc::smem_u32(p), (uint32_t)rank))
+               : "memory");
+  return v;
+}
+// Four features of a row (all of them, or none: D is a multiple of 16), times f.
+template <typename IT>
+__device__ __forceinline__ void store4(IT* p, float4 v, float f) {
+  const float x[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
+  if ((uintptr_t)p % (4 * sizeof(IT)) == 0) {
+    store_v<4>(p, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = from_f32<IT>(x[i]);
+  }
 }
 // Rows 4 ty + r (Column) or ty + 16 r of an accumulator to a tile [64][DP + 4].
 template <int DP, bool Column>
@@ -65,33 +83,45 @@ __device__ __forceinline__ void put_rows(float* dst, const float (&v)[4][DP / 16
 // Rows of this block's share of a tile, summed over the cluster's blocks, times f to `out` (row `first` on at out, D features).
 template <typename IT, int DP>
 __device__ __forceinline__ void sum_rows(const float* tile, int rank, int n, IT* out, long long ld, int rows, int D, float f) {
-  const int r0 = kT * rank / n, r1 = kT * (rank + 1) / n;
-  for (int e = threadIdx.x; e < (r1 - r0) * DP; e += kThreads) {
-    const int r = r0 + e / DP, c = e % DP;
-    if (r >= rows || c >= D) continue;
-    float sum = 0.f;
-    for (int x = 0; x < n; ++x) sum += load_peer(tile + r * (DP + 4) + c, x);
-    out[(long long)r * ld + c] = from_f32<IT>(sum * f);
+  const int r0 = kT * rank / n, r1 = min(rows, kT * (rank + 1) / n);
+  for (int e = threadIdx.x; e < (r1 - r0) * (DP / 4); e += kThreads) {
+    const int r = r0 + e / (DP / 4), c = e % (DP / 4) * 4;
+    if (c >= D) continue;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < n; ++x) {
+      const float4 v = load_peer4(tile + r * (DP + 4) + c, x);
+      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+    }
+    store4(out + (long long)r * ld + c, sum, f);
   }
 }
 
-// acc[r][c] += A[ty + 16 r] . B[tx + 16 c] over the DP features.
+// acc[r][c] = A[ty + 16 r] . B[tx + 16 c] over the DP features; even and odd ones in the halves of a packed sum, which takes half the
+// instructions.
 template <int DP>
 __device__ __forceinline__ void dot_tile(const float* A, const float* B, int tx, int ty, float (&acc)[4][4]) {
   constexpr int S = DP + 4;
+  f32x2 sum[4][4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sum[r][c] = 0;  // a pair of zeros
 #pragma unroll 4
   for (int k = 0; k < DP; k += 4) {
-    float4 a[4], b[4];
+    ulonglong2 a[4], b[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4*>(A + (ty + 16 * r) * S + k);
+    for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const ulonglong2*>(A + (ty + 16 * r) * S + k);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const float4*>(B + (tx + 16 * c) * S + k);
+    for (int c = 0; c < 4; ++c) b[c] = *reinterpret_cast<const ulonglong2*>(B + (tx + 16 * c) * S + k);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        acc[r][c] = fmaf(a[r].x, b[c].x, fmaf(a[r].y, b[c].y, fmaf(a[r].z, b[c].z, fmaf(a[r].w, b[c].w, acc[r][c]))));
+      for (int c = 0; c < 4; ++c) sum[r][c] = fma2(a[r].y, b[c].y, fma2(a[r].x, b[c].x, sum[r][c]));
   }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[r][c] = lo2(sum[r][c]) + hi2(sum[r][c]);
 }
 
 // out[r][.] += sum_j M[ty + 16 r][j] X[j][features 4 tx + 64 w ..]: M [64][kPS], X [64][DP + 4].
@@ -157,8 +187,13 @@ __device__ __forceinline__ void store_row(IT* dst, const float (&v)[DP / 16], fl
 template <int DP>
 constexpr size_t tile_bytes() { return sizeof(float) * kT * (DP + 4); }
 
+// Whether some query of a tile does not see some key of it.
+__device__ __forceinline__ bool partial(const AttnDims& d, const AttnSpan& s, int off, int i0, int j0) {
+  return j0 + kT > s.m || (d.causal && j0 + kT - 1 > i0 + off) || (d.window && j0 <= i0 + kT - 1 + off - d.window);
+}
+
 template <typename IT, int DP>
-__global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnDims d, AttnTiles t, AttnFwdArgs a) {
+__global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_fwd_simt_kernel(AttnDims d, AttnTiles t, AttnFwdArgs a) {
   extern __shared__ float smem[];
   float *Q = smem, *K = Q + kT * (DP + 4), *V = K + kT * (DP + 4), *P = V + kT * (DP + 4);
   if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *a.status = 0;  // of a packed batch: the tile table's kernel
@@ -184,24 +219,22 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnDims d, Att
     copy_async_wait();
     __syncthreads();  // the keys are here, and the values and P of the step before used up
     load_tile<IT, DP>(V, v, d.ld_v, j0, s.m, d.D);
-    float S[4][4] = {};
+    float S[4][4];
     dot_tile<DP>(Q, K, tx, ty, S);
+    if (partial(d, s, off, i0, j0))
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + tx + 16 * e;
+          if (j >= s.m || !attn_sees(d, off, i0 + ty + 16 * r, j)) S[r][e] = -INFINITY;
+        }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int i = i0 + ty + 16 * r;
-      float top = m[r];
+      // (a NaN passes the maximum by and reaches the row through its own exponential)
+      float top = fmaxf(fmaxf(fmaxf(m[r], S[r][0]), fmaxf(S[r][1], S[r][2])), S[r][3]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = j0 + tx + 16 * e;
-        S[r][e] = j < s.m && attn_sees(d, off, i, j) ? S[r][e] : -INFINITY;
-        // a NaN goes into the maximum, and from there into the row
-        top = S[r][e] > top || S[r][e] != S[r][e] ? S[r][e] : top;
-      }
-#pragma unroll
-      for (int x = 1; x < 16; x <<= 1) {
-        const float other = __shfl_xor_sync(0xffffffffu, top, x);
-        top = other > top || other != other ? other : top;
-      }
+      for (int x = 1; x < 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
       const float base = top == -INFINITY ? 0.f : top * c;  // a row that has seen nothing yet: e^(-inf - 0) = 0
       const float f = ex2f(fmaf(m[r], c, -base));
       m[r] = top;
@@ -231,26 +264,23 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnDims d, Att
       for (int r = 0; r < 4; ++r) P[ty + 16 * r] = m[r], P[kT + ty + 16 * r] = l[r];
     tc::cluster_sync();
     const int r0 = kT * rank / n, r1 = kT * (rank + 1) / n;
-    for (int e = threadIdx.x; e < (r1 - r0) * DP; e += kThreads) {
-      const int r = r0 + e / DP, x = e % DP, i = i0 + r;
+    for (int e = threadIdx.x; e < (r1 - r0) * (DP / 4); e += kThreads) {
+      const int r = r0 + e / (DP / 4), x = e % (DP / 4) * 4, i = i0 + r;
       if (i >= s.n || x >= d.D) continue;
-      float mx[8], top = -INFINITY;
-#pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        mx[y] = y < n ? load_peer(P + r, y) : -INFINITY;
-        top = mx[y] > top || mx[y] != mx[y] ? mx[y] : top;
-      }
+      float top = -INFINITY, sum = 0.f;
+      for (int y = 0; y < n; ++y) top = fmaxf(top, load_peer(P + r, y));
       const float base = top == -INFINITY ? 0.f : top * c;
-      float sum = 0.f, o = 0.f;
-#pragma unroll
-      for (int y = 0; y < 8; ++y) {
-        if (y >= n) break;
-        const float f = ex2f(fmaf(mx[y], c, -base));
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int y = 0; y < n; ++y) {
+        const float f = ex2f(fmaf(load_peer(P + r, y), c, -base));
+        const float4 v = load_peer4(K + r * (DP + 4) + x, y);
         sum = fmaf(load_peer(P + kT + r, y), f, sum);
-        o = fmaf(load_peer(K + r * (DP + 4) + x, y), f, o);
+        o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
       }
-      ((IT*)a.o)[(s.q0 + i) * (long long)d.Hq * d.D + (long long)h * d.D + x] = from_f32<IT>(top == -INFINITY ? 0.f : o / sum);
-      if (x == 0) a.lse[s.lse0 + (long long)h * d.Tq + i] = top == -INFINITY ? -INFINITY : fmaf(top, d.scale, logf(sum));
+      const bool none = top == -INFINITY && sum == 0.f;
+      store4((IT*)a.o + (s.q0 + i) * (long long)d.Hq * d.D + (long long)h * d.D + x, none ? make_float4(0.f, 0.f, 0.f, 0.f) : o,
+             none ? 0.f : 1.f / sum);
+      if (x == 0) a.lse[s.lse0 + (long long)h * d.Tq + i] = none ? -INFINITY : fmaf(top, d.scale, logf(sum));
     }
     tc::cluster_sync();  // no block ends while others read it
     return;
@@ -259,9 +289,9 @@ __global__ void __launch_bounds__(kThreads) attn_fwd_simt_kernel(AttnDims d, Att
   for (int r = 0; r < 4; ++r) {
     const int i = i0 + ty + 16 * r;
     if (i >= s.n) continue;
-    store_row<IT, DP>((IT*)a.o + (s.q0 + i) * (long long)d.Hq * d.D + (long long)h * d.D, O[r], m[r] == -INFINITY ? 0.f : 1.f / l[r], tx, d.D);
+    store_row<IT, DP>((IT*)a.o + (s.q0 + i) * (long long)d.Hq * d.D + (long long)h * d.D, O[r], m[r] == -INFINITY && l[r] == 0.f ? 0.f : 1.f / l[r], tx, d.D);
     if (tx == 0)
-      a.lse[s.lse0 + (long long)h * d.Tq + i] = m[r] == -INFINITY ? -INFINITY : fmaf(m[r], d.scale, logf(l[r]));
+      a.lse[s.lse0 + (long long)h * d.Tq + i] = m[r] == -INFINITY && l[r] == 0.f ? -INFINITY : fmaf(m[r], d.scale, logf(l[r]));
   }
 }
 
@@ -271,23 +301,24 @@ __device__ __forceinline__ void grad_tile(const AttnDims& d, const AttnSpan& s, 
                                           const float* dO, const float* V, const float* lse, const float* delta, int tx, int ty,
                                           float (&p)[4][4], float (&ds)[4][4]) {
   const int off = s.m - s.n;
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) p[r][e] = ds[r][e] = 0.f;
   dot_tile<DP>(Q, K, tx, ty, p);
   dot_tile<DP>(dO, V, tx, ty, ds);
+  const bool cut = i0 + kT > s.n || partial(d, s, off, i0, j0);
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int i = i0 + ty + 16 * r;
     const float ls = i < s.n ? lse[i] : 0.f, dl = i < s.n ? delta[i] : 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int j = j0 + tx + 16 * e;
-      const bool on = i < s.n && j < s.m && attn_sees(d, off, i, j);
-      p[r][e] = on ? ex2f(kLog2e * fmaf(p[r][e], d.scale, -ls)) : 0.f;
-      ds[r][e] = on ? p[r][e] * (ds[r][e] - dl) : 0.f;
+      p[r][e] = ex2f(kLog2e * fmaf(p[r][e], d.scale, -ls));
+      ds[r][e] = p[r][e] * (ds[r][e] - dl);
     }
+    if (cut)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + tx + 16 * e;
+        if (i >= s.n || j >= s.m || !attn_sees(d, off, i, j)) p[r][e] = ds[r][e] = 0.f;
+      }
   }
 }
 
@@ -299,7 +330,7 @@ __device__ __forceinline__ void put_tile(float* dst, const float (&v)[4][4], int
 }
 
 template <typename IT, int DP>
-__global__ void __launch_bounds__(kThreads) attn_dkdv_simt_kernel(AttnDims d, AttnTiles t, AttnBwdArgs a) {
+__global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_dkdv_simt_kernel(AttnDims d, AttnTiles t, AttnBwdArgs a) {
   extern __shared__ float smem[];
   constexpr int N = kT * (DP + 4);
   float *K = smem, *V = K + N, *Q = V + N, *dO = Q + N, *Qn = dO + N, *M = Qn + N;  // Qn: the next step's
@@ -373,7 +404,7 @@ __global__ void __launch_bounds__(kThreads) attn_dkdv_simt_kernel(AttnDims d, At
 }
 
 template <typename IT, int DP>
-__global__ void __launch_bounds__(kThreads) attn_dq_simt_kernel(AttnDims d, AttnTiles t, AttnBwdArgs a) {
+__global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_dq_simt_kernel(AttnDims d, AttnTiles t, AttnBwdArgs a) {
   extern __shared__ float smem[];
   constexpr int N = kT * (DP + 4);
   float *Q = smem, *dO = Q + N, *K = dO + N, *V = K + N, *Kn = V + N, *M = Kn + N;  // Kn: the next step's
