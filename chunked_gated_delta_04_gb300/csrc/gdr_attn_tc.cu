@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
   using Shape = FwdShape<DP, Split>;
   constexpr int ST = Shape::kSlots, Q = Shape::kQ;
   extern __shared__ unsigned char raw[];
-  __shared__ uint64_t q_full[NT], q_empty[NT], kv_full[ST], kv_empty[ST], s_full[NT], p_ready[NT], o_done[NT], tail_full, drain;
+  __shared__ uint64_t q_full[NT], q_empty[NT], kv_full[ST], kv_empty[ST], s_full[NT], p_half[NT], p_ready[NT], o_done[NT], tail_full, drain;
   __shared__ uint32_t tmem_slot;
   __shared__ float joint[Split ? 2 : 1][2][NT][kTcBlock];  // Split: maxima and sums of an item's two lanes, of the next item's
   const int n = Share ? attn_cluster_size() : 1, rank = Share ? (int)tc::cluster_ctarank() : 0;
@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
       tc::mbar_init(&q_full[i], 1);
       tc::mbar_init(&q_empty[i], 1);
       tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&p_half[i], 4);
       tc::mbar_init(&p_ready[i], 4);
       tc::mbar_init(&o_done[i], 1);
     }
@@ -202,6 +203,19 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
         const long long x = attn_item(turn, items, n);
         if (x < 0) break;
         if (!fwd_item<Q>(d, tiles, (unsigned)x, &w)) continue;
+        auto value_product = [&](int i, int slot, bool more) {  // O_i (+)= P_i V, the first half of it once that half of P is there
+          const uint32_t o = tmem + Shape::kO + i * DP, p = tmem + i * 128, v = kv_at + slot * Shape::kTile, parity = p_parity >> i & 1u;
+          p_parity ^= 1u << i;
+          ok = ok && attn_warp_wait(&p_half[i], parity, status, kDevErrTimeoutFwd);
+          if (!ok) return false;
+          tc::tc_fence_after();
+          attn_product<DP, 32, 0, 4>(o, p, v, more, leader);
+          ok = attn_warp_wait(&p_ready[i], parity, status, kDevErrTimeoutFwd);
+          if (!ok) return false;
+          tc::tc_fence_after();
+          attn_product<DP, 32, 4, 8>(o, p, v, true, leader);
+          return true;
+        };
         auto scores = [&](int i, int slot, int j) {  // S_i of key block j
           attn_scores<DP>(tmem + i * 128, q_at + i * Shape::kTile, kv_at + slot * Shape::kTile, leader);
           attn_commit(&s_full[i], leader);
@@ -228,11 +242,7 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
             const int i = j & 1;
             ok = attn_warp_wait(&kv_full[ring.slot], ring.parity, status, kDevErrTimeoutFwd);
             GDR_DELAY(48);
-            ok = ok && attn_warp_wait(&p_ready[i], p_parity >> i & 1u, status, kDevErrTimeoutFwd);
-            p_parity ^= 1u << i;
-            if (!ok) break;
-            tc::tc_fence_after();
-            attn_product<DP>(tmem + Shape::kO + i * DP, tmem + i * 128, kv_at + ring.slot * Shape::kTile, j > 1, leader);
+            if (!value_product(i, ring.slot, j > 1)) break;
             attn_commit(&o_done[i], leader);
             attn_commit(&kv_empty[ring.slot], leader);
             ring.next();
@@ -263,11 +273,7 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
             if (!ok) break;
             if (j >= w.lo[i] && j < w.hi[i]) {
               GDR_DELAY(48);
-              ok = attn_warp_wait(&p_ready[i], p_parity >> i & 1u, status, kDevErrTimeoutFwd);
-              p_parity ^= 1u << i;
-              if (!ok) break;
-              tc::tc_fence_after();
-              attn_product<DP>(tmem + Shape::kO + i * DP, tmem + i * 128, kv_at + v_slot * Shape::kTile, j > w.lo[i], leader);
+              if (!value_product(i, v_slot, j > w.lo[i])) break;
               attn_commit(&o_done[i], leader);
             }
             if (j + 1 >= w.lo[i] && j + 1 < w.hi[i]) {
@@ -376,6 +382,12 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
             r[y] = *reinterpret_cast<const uint32_t*>(&b);
           }
           tc::tmem_st32(s_col + e / 2, r);
+          if (e == 0) {  // the product with the first half of the values may begin
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&p_half[t]);
+          }
         }
         const f32x2 both = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += lo2(both) + hi2(both);

@@ -75,13 +75,13 @@ __device__ __forceinline__ void attn_scores(uint32_t d_tmem, uint32_t a, uint32_
         : "memory");
 }
 // D (+)= A B: A [128 x 128] in TMEM as bf16 (32 columns for its first 64 columns, those of the others begin at column Second),
-// B a tile of 128 rows by DP features.
-template <int DP, uint32_t Second = 32>
+// B a tile of 128 rows by DP features; K steps From .. To of its 8.
+template <int DP, uint32_t Second = 32, int From = 0, int To = kTcBlock / 16>
 __device__ __forceinline__ void attn_product(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, bool accumulate, uint32_t leader) {
   constexpr uint32_t id = tc::idesc_bf16(kTcBlock, DP, 0, 1);
   b = desc_mnmajor(b);
 #pragma unroll
-  for (int kk = 0; kk < kTcBlock / 16; ++kk)
+  for (int kk = From; kk < To; ++kk)
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
         "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
