@@ -32,6 +32,7 @@ constexpr int kSeqsHere = 1024;  // sequences whose bounds fit in shared memory
 __global__ void __launch_bounds__(kBins) attn_tiles_kernel(AttnDims d, TableSpec t0, TableSpec t1, uint32_t* status) {
   __shared__ int bin[kBins], warp_sums[kBins / 32];
   __shared__ int32_t cu_q[kSeqsHere + 1], cu_k[kSeqsHere + 1];
+  launch_next();
   const TableSpec t = blockIdx.x == 0 ? t0 : t1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool here = d.num_seqs <= kSeqsHere;  // else they are read where they lie
@@ -93,6 +94,8 @@ __global__ void __launch_bounds__(kBins) attn_tiles_kernel(AttnDims d, TableSpec
 template <typename IT>
 __global__ void __launch_bounds__(256) attn_delta_kernel(AttnDims d, const IT* __restrict__ o, const IT* __restrict__ dout,
                                                          float* __restrict__ delta, uint32_t* status, bool vec) {
+  launch_wait();
+  launch_next();
   if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *status = 0;  // of a packed batch: the tile table's kernel
   constexpr int V = 16 / sizeof(IT);
   const int lane = threadIdx.x & 31;
@@ -259,10 +262,13 @@ gdr_status gdr_attn_bwd(const gdr_attn_problem* p, const void* q, const void* k,
   if (queries) {
     const long long rows = (long long)d.B * d.Tq * d.Hq;
     const bool vec = vec_ok(o) && vec_ok(dout) && d.ld_do * el % 16 == 0;
+    const bool behind = d.cu_q != nullptr;
     if (bf16)
-      attn_delta_kernel<<<(unsigned)((rows + 15) / 16), 256, 0, s>>>(d, (const __nv_bfloat16*)o, (const __nv_bfloat16*)dout, delta, status, vec);
+      e = attn_launch(attn_delta_kernel<__nv_bfloat16>, (rows + 15) / 16, 256, 0, 1, behind, s, d, (const __nv_bfloat16*)o,
+                      (const __nv_bfloat16*)dout, delta, status, vec);
     else
-      attn_delta_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(d, (const float*)o, (const float*)dout, delta, status, vec);
+      e = attn_launch(attn_delta_kernel<float>, (rows + 7) / 8, 256, 0, 1, behind, s, d, (const float*)o, (const float*)dout, delta, status, vec);
+    if (e != cudaSuccess) return status_of(e);
     stage_mark(s, "attn_delta");
     e = cudaGetLastError();
     if (e != cudaSuccess) return status_of(e);

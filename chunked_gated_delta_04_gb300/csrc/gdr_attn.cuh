@@ -100,6 +100,35 @@ struct AttnBwdArgs {
   uint32_t* status;
 };
 
+// A call's launches overlap: one that is `behind` another of the call may be set up while that one ends (its blocks get their memory and
+// barriers ready), and waits for its results with launch_wait before it touches anything of the call's.
+__device__ __forceinline__ void launch_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+template <typename F, typename... Args>
+inline cudaError_t attn_launch(F kernel, long long grid, int threads, size_t smem, int cluster, bool behind, cudaStream_t s, Args... args) {
+  cudaLaunchAttribute attr[2] = {};
+  int n = 0;
+  if (cluster > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = (unsigned)cluster;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (behind) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3((unsigned)grid);
+  config.blockDim = dim3((unsigned)threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = s;
+  config.attrs = attr;
+  config.numAttrs = (unsigned)n;
+  return cudaLaunchKernelEx(&config, kernel, args...);
+}
+
 // SIMT kernels: fp32, and bf16 whose pointers or strides the tensor-core path does not take.
 constexpr int kSimtTile = 64;  // queries and keys of a tile
 cudaError_t launch_attn_fwd_simt(const AttnDims& d, const AttnTiles& t, bool bf16, const AttnFwdArgs& a, cudaStream_t s);

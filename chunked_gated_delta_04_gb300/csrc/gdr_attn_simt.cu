@@ -196,6 +196,7 @@ template <typename IT, int DP>
 __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_fwd_simt_kernel(AttnDims d, AttnTiles t, AttnFwdArgs a) {
   extern __shared__ float smem[];
   float *Q = smem, *K = Q + kT * (DP + 4), *V = K + kT * (DP + 4), *P = V + kT * (DP + 4);
+  launch_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *a.status = 0;  // of a packed batch: the tile table's kernel
   int seq, h, tile;
   const int n = cluster_size(), rank = n > 1 ? (int)tc::cluster_ctarank() : 0;
@@ -334,6 +335,8 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_dkdv_simt_ker
   extern __shared__ float smem[];
   constexpr int N = kT * (DP + 4);
   float *K = smem, *V = K + N, *Q = V + N, *dO = Q + N, *Qn = dO + N, *M = Qn + N;  // Qn: the next step's
+  launch_wait();
+  launch_next();
   int seq, h, tile;
   const int n = cluster_size(), rank = n > 1 ? (int)tc::cluster_ctarank() : 0;
   if (!attn_tile(d, t, d.Hk, blockIdx.x / n, &seq, &h, &tile)) return;
@@ -408,6 +411,8 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_dq_simt_kerne
   extern __shared__ float smem[];
   constexpr int N = kT * (DP + 4);
   float *Q = smem, *dO = Q + N, *K = dO + N, *V = K + N, *Kn = V + N, *M = Kn + N;  // Kn: the next step's
+  launch_wait();
+  launch_next();
   int seq, h, tile;
   const int n = cluster_size(), rank = n > 1 ? (int)tc::cluster_ctarank() : 0;
   if (!attn_tile(d, t, d.Hq, blockIdx.x / n, &seq, &h, &tile)) return;
@@ -462,25 +467,14 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_dq_simt_kerne
 // resident: blocks that an SM holds; steps: of the longest tile's loop.  Blocks of a cluster: as many as it takes to give every SM its
 // blocks, at most 8, and no more than there are steps.
 template <typename F, typename A>
-cudaError_t go(F kernel, long long items, size_t smem, int resident, long long steps, const AttnDims& d, const AttnTiles& t, const A& a,
+cudaError_t go(F kernel, long long items, size_t smem, int resident, long long steps, bool behind, const AttnDims& d, const AttnTiles& t, const A& a,
                cudaStream_t s, const char* stage) {
   if (items == 0) return cudaSuccess;
   cudaError_t e = set_smem_once((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   int n = 1;
   while (n < 8 && items * n < (long long)resident * kSmCount && 2 * n <= steps) n *= 2;
-  cudaLaunchAttribute cluster = {};
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = (unsigned)n;
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  cudaLaunchConfig_t config = {};
-  config.gridDim = dim3((unsigned)(items * n));
-  config.blockDim = dim3(kThreads);
-  config.dynamicSmemBytes = smem;
-  config.stream = s;
-  config.attrs = &cluster;
-  config.numAttrs = 1;
-  e = cudaLaunchKernelEx(&config, kernel, d, t, a);
+  e = attn_launch(kernel, items * n, kThreads, smem, n, behind, s, d, t, a);
   if (e != cudaSuccess) return e;
   stage_mark(s, stage);
   return cudaGetLastError();
@@ -489,16 +483,17 @@ cudaError_t go(F kernel, long long items, size_t smem, int resident, long long s
 template <typename IT, int DP>
 cudaError_t fwd(const AttnDims& d, const AttnTiles& t, const AttnFwdArgs& a, cudaStream_t s) {
   return go(attn_fwd_simt_kernel<IT, DP>, attn_tile_count(d, false, kT) * d.Hq, 3 * tile_bytes<DP>() + sizeof(float) * kT * kPS, DP == 64 ? 2 : 1,
-            (d.Tk + kT - 1) / kT, d, t, a, s, "attn_fwd");
+            (d.Tk + kT - 1) / kT, d.cu_q != nullptr, d, t, a, s, "attn_fwd");
 }
 template <typename IT, int DP>
 cudaError_t bwd(const AttnDims& d, const AttnTiles& tq, const AttnTiles& tk, const AttnBwdArgs& a, cudaStream_t s) {
   constexpr size_t smem = 5 * tile_bytes<DP>() + sizeof(float) * kT * kPS;
   constexpr int resident = DP == 64 ? 2 : 1;
+  const bool behind = d.cu_q != nullptr || d.Tq > 0;  // the tables' launch, or delta's
   const cudaError_t e = go(attn_dkdv_simt_kernel<IT, DP>, attn_tile_count(d, true, kT) * d.Hk, smem, resident,
-                           (long long)((d.Tq + kT - 1) / kT) * d.G, d, tk, a, s, "attn_dkdv");
+                           (long long)((d.Tq + kT - 1) / kT) * d.G, behind, d, tk, a, s, "attn_dkdv");
   if (e != cudaSuccess) return e;
-  return go(attn_dq_simt_kernel<IT, DP>, attn_tile_count(d, false, kT) * d.Hq, smem, resident, (d.Tk + kT - 1) / kT, d, tq, a, s, "attn_dq");
+  return go(attn_dq_simt_kernel<IT, DP>, attn_tile_count(d, false, kT) * d.Hq, smem, resident, (d.Tk + kT - 1) / kT, true, d, tq, a, s, "attn_dq");
 }
 
 }  // namespace

@@ -782,7 +782,7 @@ gdr_status check_cache(const gdr_cache_problem* p, bool step) {
   if (p->D % 16 != 0 || p->D > 128) return GDR_ERR_UNSUPPORTED;
   const long long most = 1ll << 31;
   // positions of a row are 32-bit numbers, as lengths are
-  if ((long long)p->max_pages * p->page_size >= most || wk >= most) return GDR_ERR_UNSUPPORTED;
+  if ((long long)p->max_pages * p->page_size >= most - 256 || wk >= most) return GDR_ERR_UNSUPPORTED;  // (a tile's end fits, too)
   if (step && (long long)p->B * p->Hq >= most) return GDR_ERR_UNSUPPORTED;
   if (wk * p->page_size * (long long)dtype_bytes(p->dtype) >= 1ll << 40) return GDR_ERR_UNSUPPORTED;  // a page, as a stride of TMA
   if (!step && (p->cu_seqlens ? (long long)p->T : (long long)p->B * p->T) >= most) return GDR_ERR_UNSUPPORTED;

@@ -91,7 +91,6 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
   unsigned char* const skv = sq + Q * Shape::kTile;
   const int warp = attn_warp(), lane = threadIdx.x & 31;
   uint32_t* const status = a.status;
-  if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *status = 0;  // of a packed batch: the tile table's kernel
   if (threadIdx.x == 0) {
     for (int i = 0; i < NT; ++i) {
       tc::mbar_init(&q_full[i], 1);
@@ -119,6 +118,8 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  launch_wait();  // for a packed batch's tile table
+  if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *status = 0;  // of a packed batch: the tile table's kernel
 
   // Registers: three warpgroups are launched with 168 a thread; 2 x 216 + 72 is the same sum.
   // (Each count stands in its role's own branch: the compiler allots the code behind it by it.)
@@ -427,15 +428,18 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
           }
           continue;
         }
-        const float by = top == -INFINITY ? 0.f : 1.f / sum;
+        const bool none = top == -INFINITY && sum == 0.f;  // (scores that are all NaN leave the maximum at -infinity, too)
+        const float by = none ? 0.f : 1.f / sum;
         attn_store_row<DP / 2>(o0, o1, out + f, d.D - f, f0 * by, f1 * by, any0, any1, mine);
-        if (mine && t == 0) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = top == -INFINITY ? -INFINITY : fmaf(top, d.scale, logf(sum));
+        if (mine && t == 0) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = none ? -INFINITY : fmaf(top, d.scale, logf(sum));
         tc::tc_fence_before();
         tc::named_sync(1, 2 * kTcBlock);  // both lanes' O are read before either is begun anew
       } else {
-        // a query that has seen nothing has l = 0 and O = 0 or, where a product has not begun, none
-        attn_store_row<DP>(o_col, out, d.D, m == -INFINITY ? 0.f : 1.f / l, lo < hi, mine);
-        if (mine) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = m == -INFINITY ? -INFINITY : fmaf(m, d.scale, logf(l));
+        // a query that has seen nothing has l = 0 and O = 0 or, where a product has not begun, none (one whose scores are all NaN has
+        // the maximum of the first, and l = NaN)
+        const bool none = m == -INFINITY && l == 0.f;
+        attn_store_row<DP>(o_col, out, d.D, none ? 0.f : 1.f / l, lo < hi, mine);
+        if (mine) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = none ? -INFINITY : fmaf(m, d.scale, logf(l));
       }
       tc::tc_fence_before();  // O is read before this item's successor's first product into it, which the next arrival allows
     }
@@ -459,11 +463,12 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
           sum = fmaf(load_peer(&joint[Split][1][0][r], y), f, sum);
           o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
         }
-        const float by = top == -INFINITY ? 0.f : 1.f / sum;
+        const bool none = top == -INFINITY && sum == 0.f;
+        const float by = none ? 0.f : 1.f / sum;
         if (4 * piece < d.D)
           store4((__nv_bfloat16*)a.o + ((w.s.q0 + i) * d.Hq + w.h) * (long long)d.D + 4 * piece,
-                 top == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
-        if (piece == 0) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = top == -INFINITY ? -INFINITY : fmaf(top, d.scale, logf(sum));
+                 none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * by, o.y * by, o.z * by, o.w * by));
+        if (piece == 0) a.lse[w.s.lse0 + (long long)w.h * d.Tq + i] = none ? -INFINITY : fmaf(top, d.scale, logf(sum));
       }
     }
     __syncwarp();
@@ -487,7 +492,7 @@ cudaError_t fwd(const AttnDims& d, const AttnTiles& t, const AttnFwdArgs& a, cud
   const auto kernel = n > 1 ? attn_fwd_tc_kernel<DP, Split, Split> : attn_fwd_tc_kernel<DP, Split, false>;
   cudaError_t e = set_smem_once((const void*)kernel, Shape::kSmem);
   if (e != cudaSuccess) return e;
-  e = attn_launch(kernel, n > 1 ? items * n : std::min<long long>(items, kSmCount), Shape::kThreads, Shape::kSmem, n, s, maps, d, t, (unsigned)items, a);
+  e = attn_launch(kernel, n > 1 ? items * n : std::min<long long>(items, kSmCount), Shape::kThreads, Shape::kSmem, n, d.cu_q != nullptr, s, maps, d, t, (unsigned)items, a);
   if (e != cudaSuccess) return e;
   stage_mark(s, "attn_fwd");
   return cudaGetLastError();

@@ -202,22 +202,6 @@ __device__ __forceinline__ int attn_cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
   return (int)n;
 }
-template <typename F, typename... Args>
-inline cudaError_t attn_launch(F kernel, long long grid, int threads, size_t smem, int cluster, cudaStream_t s, Args... args) {
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t config = {};
-  config.gridDim = dim3((unsigned)grid);
-  config.blockDim = dim3((unsigned)threads);
-  config.dynamicSmemBytes = smem;
-  config.stream = s;
-  config.attrs = &attr;
-  config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, kernel, args...);
-}
-
 // Columns [c0, c0 + N) of a row of this block's part [128][DP] in shared memory: 16-byte pieces, placed by the row so that rows do not
 // meet in a bank.
 template <int DP>

@@ -88,7 +88,7 @@ gdr_status gdr_attn_bwd(const gdr_attn_problem* p, const void* q, const void* k,
  * k_cache, v_cache [num_pages, page_size, Hk, D]: pages of page_size positions.  block_table [B, max_pages]
  * int32 names each row's pages in order: position t of row b lies at place t % page_size of page
  * block_table[b][t / page_size].  Two rows of one call must not write to the same place.  Several rows
- * may read the same page. */
+ * may read the same page.  A table covers fewer than 2^31 - 256 positions. */
 typedef struct {
   int B;                     /* rows (gdr_attn_step), sequences (gdr_cache_write) */
   int T;                     /* gdr_cache_write: tokens of a sequence, or all tokens with cu_seqlens; step: 1 */

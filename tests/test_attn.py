@@ -228,12 +228,13 @@ def test_attention_is_reproducible(dtype):
 
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("packed", [False, True])
-def test_sequences_do_not_reach_one_another(dtype, packed):
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (80, 40)])  # tiles that blocks share, and tiles enough
+def test_sequences_do_not_reach_one_another(dtype, packed, Hq, Hk):
     """NaN and infinities in one sequence leave the others' results bit for bit what they are."""
     lens = [100, 60, 170] if packed else [100, 100, 100]
     r = gen(12)
     shape = (1, sum(lens)) if packed else (3, 100)
-    ts = [r(*shape, 4, 64, dtype=dtype), r(*shape, 2, 64, dtype=dtype), r(*shape, 2, 64, dtype=dtype), r(*shape, 4, 64, dtype=dtype)]
+    ts = [r(*shape, h, 64, dtype=dtype) for h in (Hq, Hk, Hk, Hq)]
     how = dict(cu_seqlens=cu_of(lens)) if packed else {}
 
     def run(q, k, v, do):
@@ -248,6 +249,34 @@ def test_sequences_do_not_reach_one_another(dtype, packed):
     for a, b in zip(run(*spoilt), sound):
         a, b = a.view(-1, *a.shape[2:]), b.view(-1, *b.shape[2:])
         assert torch.equal(a[:lens[0]], b[:lens[0]]) and torch.equal(a[lens[0] + lens[1]:], b[lens[0] + lens[1]:])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("H,T", [(2, 300), (40, 700)])
+def test_a_query_that_is_not_a_number(dtype, H, T):
+    """Its row is not a number, and the others are bit for bit what they were."""
+    r = gen(15)
+    q, k, v = (r(2, T, H, 64, dtype=dtype) for _ in range(3))
+    want, lse = gdr.attn_forward(q, k, v)
+    bad = q.clone()
+    bad[1, 150] = float("nan")
+    o, ls = gdr.attn_forward(bad, k, v)
+    assert o[1, 150].isnan().all() and ls[1, :, 150].isnan().all()
+    keep = torch.ones(2, T, dtype=torch.bool, device="cuda")
+    keep[1, 150] = False
+    assert torch.equal(o[keep], want[keep]) and torch.equal(ls.transpose(1, 2)[keep], lse.transpose(1, 2)[keep])
+    table, lengths = torch.zeros(2, 1, dtype=torch.int32, device="cuda"), torch.tensor([3, 5], dtype=torch.int32).cuda()
+    table[1] = 1
+    kc, vc = k[:, :16].contiguous(), v[:, :16].contiguous()
+    o = gdr.attn_step(bad[:, 150], k[:, 0], v[:, 0], kc, vc, table, lengths)
+    assert torch.isfinite(o[0]).all() and o[1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_many_sequences(dtype):
+    """More sequences than the tile tables' kernel keeps the bounds of."""
+    lens = [3] * 1200 + [200] + [0] * 100 + [1] * 50
+    attn_case(dtype, lens, lens, 2, 1, 64, same_cu=True)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
