@@ -16,6 +16,9 @@ names each row's pages in order:
     q, k = rope_forward(q, k, freqs, positions=lengths)                 # then token by token: q, k, v [B, H, D]
     o = attn_step(q, k, v, k_cache, v_cache, block_table, lengths)
     lengths += 1
+
+Captured into a CUDA graph, a backward pass needs leaves whose earlier eager graphs are gone: autograd adds a leaf's gradient on the
+stream that it was first used on while such a graph lives, and that stream is not part of the capture.
 """
 from __future__ import annotations
 
@@ -171,8 +174,8 @@ def rope(q, k, freqs, positions=None, cu_seqlens=None, interleaved=False, scale=
 
 # --------------------------------------------------------------------------------------- attention
 def _scale(scale):
-    if scale is not None and not scale > 0:
-        raise ValueError(f"scale {scale}: above 0, or None for 1 / sqrt(D)")
+    if scale is not None and not 2.0 ** -126 <= scale < 2.0 ** 128:  # (what rounds to 0 would mean the default)
+        raise ValueError(f"scale {scale}: above 0 and in the range of 32 bits, or None for 1 / sqrt(D)")
     return 0.0 if scale is None else scale
 
 
@@ -235,7 +238,8 @@ def attn_step(q, k, v, k_cache, v_cache, block_table, lengths, window=0, scale=N
     block_table int32 [B, max_pages], a row's pages in order; lengths int32 [B], the positions that a row's cache holds.  k and v are
     written at position lengths[b] of their row, and its query attends to positions 0 .. lengths[b] (with a window to the last
     `window` of them).  Returns o [B, Hq, D].  A row whose length is negative or fills its table is skipped and returns zeros;
-    so does a row that needs a page outside the pool.  lengths itself is the caller's to advance."""
+    one that needs a page outside the pool returns zeros, too (k and v are written if their own page is in the pool).  lengths itself
+    is the caller's to advance."""
     if stream is not None:
         with _on(stream, q):
             return attn_step(q, k, v, k_cache, v_cache, block_table, lengths, window, scale)

@@ -8,9 +8,11 @@
 //               dK += scale dS^T Q;  per 64 queries: dQ += scale dS K
 // A block is 16 x 16 threads; a thread holds 4 x 4 of S (rows ty + 16 r, columns tx + 16 c) and 4 rows by D / 16
 // features of an accumulator.  Bound by the FMA pipes and the shared-memory reads that feed them: 16 products for
-// every two 16-byte reads; the next tiles are copied asynchronously beside them.  Where there are too few tiles to fill the SMs, the blocks of a cluster share a tile: each takes every
-// n-th step of its loop, and each sums the parts of some of the rows from the others' shared memory, in the order of their ranks
-// (1903 tokens in four sequences, 4 heads on 2, D = 64: forward 115 -> 46 us, dK and dV 393 -> 77, dQ 143 -> 57, copies beside the products and packed sums included).
+// every two 16-byte reads; the next tiles are copied asynchronously beside them.  A third of the pipes' rate is reached: two blocks of eight
+// warps an SM, whose barriers and reads are not hidden.  Where there are too few tiles to fill the SMs, the blocks of a cluster share a
+// tile: each takes every n-th step of its loop, and each sums the parts of some of the rows from the others' shared memory, in the order
+// of their ranks (1903 tokens in four sequences, 4 heads on 2, D = 64: forward 115 -> 46 us, dK and dV 393 -> 77, dQ 143 -> 57, copies
+// beside the products and packed sums included).
 #include "gdr_attn.cuh"
 #include "tc_primitives.cuh"
 

@@ -13,6 +13,10 @@
 //   queries: S = Q K^T and dP = dO V^T free their columns as soon as they are in registers; dS has two places of its own.
 // Where the tiles are less than half of the SMs (few key heads, short sequences), the blocks of a cluster share one (Share): each
 // takes every n-th step, and sums some of the rows from all blocks' shared memory, in the order of their ranks.
+// Bound by the products.  B = 1, T = 8192, 32 heads on 8 of 128, causal: dK and dV 612 us, 1.80 PFLOP/s of the four products that are
+// issued, 93 % of cuBLAS's rate; dQ 493 us, 1.67 PFLOP/s of its three.  2 x 4096 tokens, 16 heads of 128: 181 and 146 us (from the first form's
+// 222 and 196), where beginnings and ends of items, about 5 us each, weigh more.  One key head for 8 query heads, T = 4096, 32 tiles of
+// keys shared by 4 blocks each: 137 us for all three launches.
 #include <algorithm>
 
 #include "gdr_attn_tc.cuh"
@@ -180,13 +184,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rank >= steps) continue;
       load_kv(0, &maps.k);
       for (int st = rank; st < steps && ok; st += n) {
-          const int g = st / length, i = w.lo + st % length;
-          const long long r0 = w.s.q0 + (long long)i * kTcBlock;
-          const int rows = w.s.n - i * kTcBlock;
-          ok = qs.load(&maps.q, w.h * d.G + g, r0, rows, true, tail_parity);
-          if (st == rank) load_kv(1, &maps.v);
-          ok = ok && dos.load(&maps.dout, w.h * d.G + g, r0, rows, true, tail_parity);
-        }
+        const int g = st / length, i = w.lo + st % length;
+        const long long r0 = w.s.q0 + (long long)i * kTcBlock;
+        const int rows = w.s.n - i * kTcBlock;
+        ok = qs.load(&maps.q, w.h * d.G + g, r0, rows, true, tail_parity);
+        if (st == rank) load_kv(1, &maps.v);
+        ok = ok && dos.load(&maps.dout, w.h * d.G + g, r0, rows, true, tail_parity);
+      }
       kv_parity ^= 1u;
     }
     if (!ok) {
@@ -261,27 +265,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!key_item(d, tiles, (unsigned)x, &w) || w.lo >= w.hi) continue;
       const int length = w.hi - w.lo, steps = length * d.G;
       for (int st = rank; st < steps; st += n) {
-          const int g = st / length, i = w.lo + st % length;
-          const long long at = w.s.lse0 + (long long)(w.h * d.G + g) * d.Tq;
-          float ls[4], dl[4];
+        const int g = st / length, i = w.lo + st % length;
+        const long long at = w.s.lse0 + (long long)(w.h * d.G + g) * d.Tq;
+        float ls[4], dl[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = i * kTcBlock + 32 * e + lane;
-            const bool on = r < w.s.n;
-            ls[e] = on ? a.lse[at + r] * kLog2e : INFINITY;
-            dl[e] = on ? a.delta[at + r] : 0.f;
-            if (ls[e] == -INFINITY) ls[e] = INFINITY;  // a query that sees nothing: e^-infinity
-          }
-          ok = attn_warp_wait(&b.stat_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
-          if (!ok) break;
+        for (int e = 0; e < 4; ++e) {
+          const int r = i * kTcBlock + 32 * e + lane;
+          const bool on = r < w.s.n;
+          ls[e] = on ? a.lse[at + r] * kLog2e : INFINITY;
+          dl[e] = on ? a.delta[at + r] : 0.f;
+          if (ls[e] == -INFINITY) ls[e] = INFINITY;  // a query that sees nothing: e^-infinity
+        }
+        ok = attn_warp_wait(&b.stat_empty[ring.slot], ring.parity ^ 1u, status, kDevErrTimeoutBwd);
+        if (!ok) break;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            b.stat[ring.slot][0][32 * e + lane] = ls[e];
-            b.stat[ring.slot][1][32 * e + lane] = dl[e];
-          }
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&b.stat_full[ring.slot]);
-          ring.next();
+        for (int e = 0; e < 4; ++e) {
+          b.stat[ring.slot][0][32 * e + lane] = ls[e];
+          b.stat[ring.slot][1][32 * e + lane] = dl[e];
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&b.stat_full[ring.slot]);
+        ring.next();
       }
     }
   } else if (warp < 8) {
@@ -303,64 +307,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long whole_to = d.window ? (long long)w.j0 - off + d.window : (1ll << 40);
       const int length = w.hi - w.lo, steps = length * d.G;
       for (int st = rank; st < steps; st += n) {
-          const int i = w.lo + (d.G == 1 ? st : st % length);
-          ok = attn_warp_wait(&b.stat_full[ring.slot], ring.parity, status, kDevErrTimeoutBwd);
-          ok = ok && attn_warp_wait(&b.s_full, parity, status, kDevErrTimeoutBwd);
-          if (!ok) break;
-          tc::tc_fence_after();
-          const int i0 = i * kTcBlock;
-          float p[64], dp[64];
-          tc::tmem_ld32(s_col, p);
-          tc::tmem_ld32(s_col + 32, p + 32);
-          tc::tmem_wait_ld();
-          const float* ls = b.stat[ring.slot][0] + col;
+        const int i = w.lo + (d.G == 1 ? st : st % length);
+        ok = attn_warp_wait(&b.stat_full[ring.slot], ring.parity, status, kDevErrTimeoutBwd);
+        ok = ok && attn_warp_wait(&b.s_full, parity, status, kDevErrTimeoutBwd);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const int i0 = i * kTcBlock;
+        float p[64], dp[64];
+        tc::tmem_ld32(s_col, p);
+        tc::tmem_ld32(s_col + 32, p + 32);
+        tc::tmem_wait_ld();
+        const float* ls = b.stat[ring.slot][0] + col;
 #pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(ls + e);
-            p[e] = ex2f(fmaf(p[e], c, -l4.x));
-            p[e + 1] = ex2f(fmaf(p[e + 1], c, -l4.y));
-            p[e + 2] = ex2f(fmaf(p[e + 2], c, -l4.z));
-            p[e + 3] = ex2f(fmaf(p[e + 3], c, -l4.w));
-          }
-          if (i0 < whole_from || i0 + kTcBlock > whole_to) {
-            const int a0 = from - i0 - col;
-            const int a1 = (int)min(to - i0 - col, 1ll << 20);
-#pragma unroll
-            for (int e = 0; e < 64; ++e) p[e] = e >= a0 && e < a1 ? p[e] : 0.f;
-          }
-          attn_put64(s_col, p);
-          tc::tmem_wait_st();
-          tc::tc_fence_before();
-          __syncwarp();
-          GDR_DELAY(41);
-          if (lane == 0) tc::mbar_arrive(&b.p_ready);
-          ok = attn_warp_wait(&b.dp_full, parity, status, kDevErrTimeoutBwd);
-          if (!ok) break;
-          tc::tc_fence_after();
-          tc::tmem_ld32(dp_col, dp);
-          tc::tmem_ld32(dp_col + 32, dp + 32);
-          tc::tmem_wait_ld();
-          const float* dl = b.stat[ring.slot][1] + col;
-#pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            const float4 d4 = *reinterpret_cast<const float4*>(dl + e);
-            dp[e] = p[e] * (dp[e] - d4.x);
-            dp[e + 1] = p[e + 1] * (dp[e + 1] - d4.y);
-            dp[e + 2] = p[e + 2] * (dp[e + 2] - d4.z);
-            dp[e + 3] = p[e + 3] * (dp[e + 3] - d4.w);
-          }
-          attn_put64(dp_col, dp);
-          tc::tmem_wait_st();
-          tc::tc_fence_before();
-          __syncwarp();
-          GDR_DELAY(42);
-          if (lane == 0) {
-            tc::mbar_arrive(&b.ds_ready[0]);
-            tc::mbar_arrive(&b.stat_empty[ring.slot]);
-          }
-          parity ^= 1u;
-          ring.next();
+        for (int e = 0; e < 64; e += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(ls + e);
+          p[e] = ex2f(fmaf(p[e], c, -l4.x));
+          p[e + 1] = ex2f(fmaf(p[e + 1], c, -l4.y));
+          p[e + 2] = ex2f(fmaf(p[e + 2], c, -l4.z));
+          p[e + 3] = ex2f(fmaf(p[e + 3], c, -l4.w));
         }
+        if (i0 < whole_from || i0 + kTcBlock > whole_to) {
+          const int a0 = from - i0 - col;
+          const int a1 = (int)min(to - i0 - col, 1ll << 20);
+#pragma unroll
+          for (int e = 0; e < 64; ++e) p[e] = e >= a0 && e < a1 ? p[e] : 0.f;
+        }
+        attn_put64(s_col, p);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        GDR_DELAY(41);
+        if (lane == 0) tc::mbar_arrive(&b.p_ready);
+        ok = attn_warp_wait(&b.dp_full, parity, status, kDevErrTimeoutBwd);
+        if (!ok) break;
+        tc::tc_fence_after();
+        tc::tmem_ld32(dp_col, dp);
+        tc::tmem_ld32(dp_col + 32, dp + 32);
+        tc::tmem_wait_ld();
+        const float* dl = b.stat[ring.slot][1] + col;
+#pragma unroll
+        for (int e = 0; e < 64; e += 4) {
+          const float4 d4 = *reinterpret_cast<const float4*>(dl + e);
+          dp[e] = p[e] * (dp[e] - d4.x);
+          dp[e + 1] = p[e + 1] * (dp[e + 1] - d4.y);
+          dp[e + 2] = p[e + 2] * (dp[e + 2] - d4.z);
+          dp[e + 3] = p[e + 3] * (dp[e + 3] - d4.w);
+        }
+        attn_put64(dp_col, dp);
+        tc::tmem_wait_st();
+        tc::tc_fence_before();
+        __syncwarp();
+        GDR_DELAY(42);
+        if (lane == 0) {
+          tc::mbar_arrive(&b.ds_ready[0]);
+          tc::mbar_arrive(&b.stat_empty[ring.slot]);
+        }
+        parity ^= 1u;
+        ring.next();
+      }
       if (!ok) break;
       const bool any = rank < steps;
       if (any) {

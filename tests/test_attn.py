@@ -544,6 +544,66 @@ def test_malformed_cu_seqlens_can_be_seen():
         assert gdr.gdr_workspace_status(ws) == want and bool(kc.any()) == well
 
 
+def test_a_call_without_queries_clears_the_status():
+    q = torch.ones(1, 10, 2, 64, device="cuda")
+    cu = torch.tensor([0, 5, 3, 10], dtype=torch.int32).cuda()
+    lse = torch.zeros(1, 2, 10, device="cuda")
+    for backward in (False, True):
+        ws = gdr.attn_workspace(q, q, cu, backward=backward)
+        if backward:
+            gdr.attn_backward(q, q, q, q, lse, q, cu_seqlens=cu, workspace=ws)
+        else:
+            gdr.attn_forward(q, q, q, cu_seqlens=cu, workspace=ws)
+        assert gdr.gdr_workspace_status(ws) == (gdr.GDR_ERR_INVALID_ARG, 1)
+        none = q[:, :0]
+        if backward:
+            gdr.attn_backward(none, q, q, none, lse[..., :0].contiguous(), none, workspace=ws)
+        else:
+            gdr.attn_forward(none, q, q, workspace=ws)
+        assert gdr.gdr_workspace_status(ws) == (gdr.GDR_OK, 0)
+
+
+def test_a_row_with_a_page_outside_the_pool_keeps_its_own_page():
+    """The row's result is zero; its token goes to its page where that is in the pool, and nowhere else."""
+    kc = torch.zeros(4, 16, 1, 64, device="cuda")
+    vc = kc.clone()
+    one = torch.ones(2, 1, 64, device="cuda")
+    table = torch.tensor([[9, 2], [1, -1]], dtype=torch.int32).cuda()
+    o = gdr.attn_step(one, one, one, kc, vc, table, torch.tensor([20, 20], dtype=torch.int32).cuda())
+    assert not o.any()
+    want = torch.zeros_like(kc)
+    want[2, 4] = 1
+    assert torch.equal(kc, want) and torch.equal(vc, want)
+
+
+def test_training_step_in_a_graph():
+    """Forward and backward through autograd, captured: replays on new inputs give what eager steps give."""
+    r = gen(33)
+    q, k, v, do = r(1, 300, 4, 64, dtype=BF), r(1, 300, 2, 64, dtype=BF), r(1, 300, 2, 64, dtype=BF), r(1, 300, 4, 64, dtype=BF)
+    freqs, _ = gdr.rope_frequencies(64)
+    cu = torch.tensor([0, 170, 300], dtype=torch.int32).cuda()
+
+    def grads(q, k, v):
+        q, k, v = (t.detach().requires_grad_() for t in (q, k, v))
+        q1, k1 = gdr.rope(q, k, freqs, cu_seqlens=cu)
+        o = gdr.attention(q1, k1, v, cu_seqlens=cu, window=100)
+        return [o.detach(), *torch.autograd.grad(o, (q, k, v), do)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        grads(q, k, v)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = grads(q, k, v)
+    for t in (q, k, v, do):
+        t.copy_(torch.randn(t.shape, generator=torch.Generator().manual_seed(7)).to(BF))
+    graph.replay()
+    got = [t.clone() for t in held]
+    assert all(torch.equal(a, b) for a, b in zip(got, grads(q, k, v)))
+
+
 def test_caches_have_versions():
     kc, vc = torch.ones(2, 16, 1, 64, device="cuda"), torch.ones(2, 16, 1, 64, device="cuda")
     was = kc._version, vc._version

@@ -224,6 +224,23 @@ def test_python_refusals():
             gdr.attn_forward(q.expand(2, 6, 4, 16), k.expand(2, 9, 2, 16).contiguous(), k.expand(2, 9, 2, 16).contiguous())
 
 
+@pytest.mark.parametrize("scale", [1e-50, 1e-40, -1.0, 1e39, INF])
+def test_scales_beyond_32_bits(scale):
+    """What rounds to 0 as a 32-bit number would otherwise be taken for the default."""
+    x = torch.zeros(2, 4, 2, 16)
+    with pytest.raises(ValueError, match="scale"):
+        gdr.attn_forward(x, x, x, scale=scale)
+    with pytest.raises(ValueError, match="scale"):
+        gdr.attn_step(x[0], x[0], x[0], x, x, x, x, scale=scale)
+
+
+def test_token_counts_at_the_limit(lib):
+    """The end of the last tile has to be a 32-bit number."""
+    for name in ("Tq", "Tk"):
+        assert lib.gdr_attn_fwd_workspace_bytes(R(att(B=1, num_seqs=1, **{name: (1 << 31) - 1000}))) == 0
+        assert lib.gdr_attn_fwd_workspace_bytes(R(att(B=1, num_seqs=1, Hq=1, Hk=1, **{name: (1 << 31) - 1025}))) == 256
+
+
 def test_sizes_beyond_32_bits():
     def big(*shape, dtype=F32):
         return torch.zeros((1,) * len(shape), dtype=dtype).expand(shape)
