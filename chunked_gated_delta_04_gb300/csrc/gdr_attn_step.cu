@@ -17,7 +17,8 @@
 // through the ring with its tiles, and its warps' parts are added in the stage that its last tile had.  The new token's key and value
 // go from the call's inputs to shared memory and the cache; what a page holds outside a row's visible positions is replaced by zeros there.
 // bf16, pages of 64: 64 rows of up to 8192 positions, 32 heads on 8 of 128: 122 us, 5.9 TB/s (437 us and more before what a unit needs came through
-// the ring); one row of 65536: 40 us, of which 6 are set-up and 5 the join, 4 TB/s between.  With 16-byte copies by all threads the
+// the ring); one row of 65536: 34 us, of which about 10 are set-up and the join (40 with eight parts' loads
+// a warp, begun behind the maxima).  With 16-byte copies by all threads the
 // latter took 84 us (1000 instructions a tile and warp), with a bulk copy for every position 96 (41 cycles a copy, one after the other).
 #include <cmath>
 #include <cstring>
@@ -638,8 +639,9 @@ __global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
   }
 }
 
-// The rows' results that several blocks have parts of, and zeros for the rows that were skipped.  A block per query head of a row.
-template <typename IT, int DP>
+// The rows' results that several blocks have parts of, and zeros for the rows that were skipped.  A block per query head of a row;
+// a warp has Ahead parts' loads under way, the first ones' while the largest maximum is looked for.  Bound by latency.
+template <typename IT, int DP, int Ahead>
 __global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, const int32_t* __restrict__ lengths, IT* __restrict__ o,
                                                              const int2* __restrict__ spans, const float* __restrict__ parts) {
   __shared__ float red[kWarps][2];
@@ -659,6 +661,22 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, const i
   const int c0 = span.x >> 1, c1 = span.y;
   auto part_of = [&](int x) { return parts + ((long long)x * 2 + (x == c0 ? span.x & 1 : 0)) * part_floats<DP>(); };
   const float c = d.scale * kLog2e;
+  // a warp takes every fourth part, a lane DP / 32 features
+  constexpr int F = DP / 32;
+  float v[Ahead][F], pm[Ahead], pl[Ahead];
+  auto load = [&](int x0) {
+#pragma unroll
+    for (int i = 0; i < Ahead; ++i) {
+      const int x = x0 + i * kWarps;
+      if (x > c1) break;
+      const float* p = part_of(x);
+      pm[i] = p[kHeads * DP + r];
+      pl[i] = p[kHeads * (DP + 1) + r];
+#pragma unroll
+      for (int f = 0; f < F; ++f) v[i][f] = p[r * DP + F * lane + f];
+    }
+  };
+  load(c0 + warp);
   // the largest maximum, and whether a part is bad
   float top = -INFINITY, bad = 0.f;
   for (int x = c0 + tid; x <= c1; x += kThreads) {
@@ -683,22 +701,11 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, const i
   }
   __syncthreads();  // red is used again
   const float base = top == -INFINITY ? 0.f : top * c;
-  // a warp takes every fourth part, a lane DP / 32 features, eight parts' loads under way; then the warps' sums in order
-  constexpr int F = DP / 32;
   float sum[F] = {}, l = 0.f;
-  for (int x0 = c0 + warp; x0 <= c1; x0 += 8 * kWarps) {
-    float v[8][F], pm[8], pl[8];
+  for (int x0 = c0 + warp; x0 <= c1; x0 += Ahead * kWarps) {
+    if (x0 > c0 + warp) load(x0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int x = x0 + i * kWarps;
-      const float* p = part_of(min(x, c1));
-      pm[i] = x <= c1 ? p[kHeads * DP + r] : -INFINITY;
-      pl[i] = p[kHeads * (DP + 1) + r];
-#pragma unroll
-      for (int f = 0; f < F; ++f) v[i][f] = p[r * DP + F * lane + f];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < Ahead; ++i) {
       if (x0 + i * kWarps > c1) break;
       const float weight = ex2f(fmaf(pm[i], c, -base));
       l = fmaf(pl[i], weight, l);
@@ -706,6 +713,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, const i
       for (int f = 0; f < F; ++f) sum[f] = fmaf(v[i][f], weight, sum[f]);
     }
   }
+  // then the warps' sums in order
 #pragma unroll
   for (int f = 0; f < F; ++f) total_of[warp][F * lane + f] = sum[f];
   if (lane == 0) red[warp][0] = l;
@@ -846,7 +854,9 @@ cudaError_t step(const StepShape& sh, const void* q, const void* k, const void* 
   config.stream = s;
   config.attrs = &early;
   config.numAttrs = 1;
-  e = cudaLaunchKernelEx(&config, attn_join_kernel<IT, DP>, sh.d, lengths, (IT*)o, (const int2*)spans, (const float*)parts);
+  // Where units are few each is in many parts: 20 loads a warp instead of 8, which keep more registers than many small joins can spare.
+  const auto join = (long long)sh.blocks >= 32ll * sh.d.B * sh.d.Hk * sh.d.HB ? attn_join_kernel<IT, DP, 20> : attn_join_kernel<IT, DP, 8>;
+  e = cudaLaunchKernelEx(&config, join, sh.d, lengths, (IT*)o, (const int2*)spans, (const float*)parts);
   if (e != cudaSuccess) return e;
   stage_mark(s, "attn_join");
   return cudaGetLastError();
