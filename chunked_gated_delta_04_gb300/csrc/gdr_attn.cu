@@ -33,6 +33,7 @@ constexpr int kSeqsHere = 1024;  // sequences whose bounds fit in shared memory
 __global__ void __launch_bounds__(kBins) attn_tiles_kernel(AttnDims d, TableSpec t0, TableSpec t1, uint32_t* status) {
   __shared__ int bin[kBins], warp_sums[kBins / 32];
   __shared__ int32_t cu_q[kSeqsHere + 1], cu_k[kSeqsHere + 1];
+  launch_wait();
   launch_next();
   const TableSpec t = blockIdx.x == 0 ? t0 : t1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -94,8 +95,7 @@ __global__ void __launch_bounds__(kBins) attn_tiles_kernel(AttnDims d, TableSpec
 // Bound by memory: o and do are read once.  2 x 4096 tokens, 16 heads of 128 in bf16, 67 MB: 20 us, set-up and waiting for the launch before
 // included; two or four rows per thread, for more loads under way, took 24 us and more.
 template <typename IT>
-__global__ void __launch_bounds__(256) attn_delta_kernel(AttnDims d, const IT* __restrict__ o, const IT* __restrict__ dout,
-                                                         float* __restrict__ delta, uint32_t* status, bool vec) {
+__global__ void __launch_bounds__(256) attn_delta_kernel(AttnDims d, const IT* o, const IT* dout, float* delta, uint32_t* status, bool vec) {
   launch_wait();
   launch_next();
   if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *status = 0;  // of a packed batch: the tile table's kernel
@@ -177,7 +177,8 @@ AttnTiles tiles_of(const AttnDims& d, const int2* table, bool keys, int size) {
 }
 
 cudaError_t launch_tiles(const AttnDims& d, const TableSpec& a, const TableSpec* b, uint32_t* status, cudaStream_t s) {
-  attn_tiles_kernel<<<b ? 2 : 1, kBins, 0, s>>>(d, a, b ? *b : a, status);
+  const cudaError_t e = attn_launch(attn_tiles_kernel, b ? 2 : 1, kBins, 0, 1, s, d, a, b ? *b : a, status);
+  if (e != cudaSuccess) return e;
   stage_mark(s, "attn_tiles");
   return cudaGetLastError();
 }
@@ -264,12 +265,11 @@ gdr_status gdr_attn_bwd(const gdr_attn_problem* p, const void* q, const void* k,
   if (queries) {
     const long long rows = (long long)d.B * d.Tq * d.Hq;
     const bool vec = vec_ok(o) && vec_ok(dout) && d.ld_do * el % 16 == 0;
-    const bool behind = d.cu_q != nullptr;
     if (bf16)
-      e = attn_launch(attn_delta_kernel<__nv_bfloat16>, (rows + 15) / 16, 256, 0, 1, behind, s, d, (const __nv_bfloat16*)o,
+      e = attn_launch(attn_delta_kernel<__nv_bfloat16>, (rows + 15) / 16, 256, 0, 1, s, d, (const __nv_bfloat16*)o,
                       (const __nv_bfloat16*)dout, delta, status, vec);
     else
-      e = attn_launch(attn_delta_kernel<float>, (rows + 7) / 8, 256, 0, 1, behind, s, d, (const float*)o, (const float*)dout, delta, status, vec);
+      e = attn_launch(attn_delta_kernel<float>, (rows + 7) / 8, 256, 0, 1, s, d, (const float*)o, (const float*)dout, delta, status, vec);
     if (e != cudaSuccess) return status_of(e);
     stage_mark(s, "attn_delta");
     e = cudaGetLastError();

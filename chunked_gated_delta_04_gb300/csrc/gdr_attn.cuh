@@ -100,12 +100,21 @@ struct AttnBwdArgs {
   uint32_t* status;
 };
 
-// A call's launches overlap: one that is `behind` another of the call may be set up while that one ends (its blocks get their memory and
-// barriers ready), and waits for its results with launch_wait before it touches anything of the call's.
+// Launches overlap: one may be set up while the one before it in the stream, of the same call or an earlier one, ends (its blocks get
+// their memory and barriers ready), and waits with launch_wait for that one's end before it touches anything but its parameters and its
+// own shared memory.  Every kernel here waits, in every block that does anything, so that its end is the end of all before it.
+// Operands are not read through __restrict__ pointers or __ldg: such loads may be moved in front of the wait, and take what they read as
+// unchanged from the kernel's beginning on.
 __device__ __forceinline__ void launch_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+// 16 bytes that are read once; stays behind launch_wait (volatile).
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 template <typename F, typename... Args>
-inline cudaError_t attn_launch(F kernel, long long grid, int threads, size_t smem, int cluster, bool behind, cudaStream_t s, Args... args) {
+inline cudaError_t attn_launch(F kernel, long long grid, int threads, size_t smem, int cluster, cudaStream_t s, Args... args) {
   cudaLaunchAttribute attr[2] = {};
   int n = 0;
   if (cluster > 1) {
@@ -114,11 +123,9 @@ inline cudaError_t attn_launch(F kernel, long long grid, int threads, size_t sme
     attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
     ++n;
   }
-  if (behind) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n].val.programmaticStreamSerializationAllowed = 1;
+  ++n;
   cudaLaunchConfig_t config = {};
   config.gridDim = dim3((unsigned)grid);
   config.blockDim = dim3((unsigned)threads);

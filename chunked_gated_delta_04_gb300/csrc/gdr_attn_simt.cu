@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_fwd_simt_kern
   extern __shared__ float smem[];
   float *Q = smem, *K = Q + kT * (DP + 4), *V = K + kT * (DP + 4), *P = V + kT * (DP + 4);
   launch_wait();
+  launch_next();
   if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *a.status = 0;  // of a packed batch: the tile table's kernel
   int seq, h, tile;
   const int n = cluster_size(), rank = n > 1 ? (int)tc::cluster_ctarank() : 0;
@@ -469,14 +470,14 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_dq_simt_kerne
 // resident: blocks that an SM holds; steps: of the longest tile's loop.  Blocks of a cluster: as many as it takes to give every SM its
 // blocks, at most 8, and no more than there are steps.
 template <typename F, typename A>
-cudaError_t go(F kernel, long long items, size_t smem, int resident, long long steps, bool behind, const AttnDims& d, const AttnTiles& t, const A& a,
+cudaError_t go(F kernel, long long items, size_t smem, int resident, long long steps, const AttnDims& d, const AttnTiles& t, const A& a,
                cudaStream_t s, const char* stage) {
   if (items == 0) return cudaSuccess;
   cudaError_t e = set_smem_once((const void*)kernel, smem);
   if (e != cudaSuccess) return e;
   int n = 1;
   while (n < 8 && items * n < (long long)resident * kSmCount && 2 * n <= steps) n *= 2;
-  e = attn_launch(kernel, items * n, kThreads, smem, n, behind, s, d, t, a);
+  e = attn_launch(kernel, items * n, kThreads, smem, n, s, d, t, a);
   if (e != cudaSuccess) return e;
   stage_mark(s, stage);
   return cudaGetLastError();
@@ -485,17 +486,16 @@ cudaError_t go(F kernel, long long items, size_t smem, int resident, long long s
 template <typename IT, int DP>
 cudaError_t fwd(const AttnDims& d, const AttnTiles& t, const AttnFwdArgs& a, cudaStream_t s) {
   return go(attn_fwd_simt_kernel<IT, DP>, attn_tile_count(d, false, kT) * d.Hq, 3 * tile_bytes<DP>() + sizeof(float) * kT * kPS, DP == 64 ? 2 : 1,
-            (d.Tk + kT - 1) / kT, d.cu_q != nullptr, d, t, a, s, "attn_fwd");
+            (d.Tk + kT - 1) / kT, d, t, a, s, "attn_fwd");
 }
 template <typename IT, int DP>
 cudaError_t bwd(const AttnDims& d, const AttnTiles& tq, const AttnTiles& tk, const AttnBwdArgs& a, cudaStream_t s) {
   constexpr size_t smem = 5 * tile_bytes<DP>() + sizeof(float) * kT * kPS;
   constexpr int resident = DP == 64 ? 2 : 1;
-  const bool behind = d.cu_q != nullptr || d.Tq > 0;  // the tables' launch, or delta's
   const cudaError_t e = go(attn_dkdv_simt_kernel<IT, DP>, attn_tile_count(d, true, kT) * d.Hk, smem, resident,
-                           (long long)((d.Tq + kT - 1) / kT) * d.G, behind, d, tk, a, s, "attn_dkdv");
+                           (long long)((d.Tq + kT - 1) / kT) * d.G, d, tk, a, s, "attn_dkdv");
   if (e != cudaSuccess) return e;
-  return go(attn_dq_simt_kernel<IT, DP>, attn_tile_count(d, false, kT) * d.Hq, smem, resident, (d.Tk + kT - 1) / kT, true, d, tq, a, s, "attn_dq");
+  return go(attn_dq_simt_kernel<IT, DP>, attn_tile_count(d, false, kT) * d.Hq, smem, resident, (d.Tk + kT - 1) / kT, d, tq, a, s, "attn_dq");
 }
 
 }  // namespace

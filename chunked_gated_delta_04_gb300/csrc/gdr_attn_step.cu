@@ -17,8 +17,8 @@
 // through the ring with its tiles, and its warps' parts are added in the stage that its last tile had.  The new token's key and value
 // go from the call's inputs to shared memory and the cache; what a page holds outside a row's visible positions is replaced by zeros there.
 // bf16, pages of 64: 64 rows of up to 8192 positions, 32 heads on 8 of 128: 122 us, 5.9 TB/s (437 us and more before what a unit needs came through
-// the ring); one row of 65536: 34 us, of which about 10 are set-up and the join (40 with eight parts' loads
-// a warp, begun behind the maxima).  With 16-byte copies by all threads the
+// the ring); one row of 65536: 32 us, of which about 8 are set-up and the join (with eight parts' loads a warp, begun behind the maxima, 6 us
+// more).  With 16-byte copies by all threads the
 // latter took 84 us (1000 instructions a tile and warp), with a bulk copy for every position 96 (41 cycles a copy, one after the other).
 #include <cmath>
 #include <cstring>
@@ -394,10 +394,10 @@ constexpr int part_floats() { return kHeads * (DP + 2); }
 
 template <typename IT, int DP, typename Engine>
 __global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
-    attn_step_kernel(const __grid_constant__ StepMaps maps, StepDims d, const IT* __restrict__ q, const IT* __restrict__ k,
-                     const IT* __restrict__ v, IT* __restrict__ k_cache, IT* __restrict__ v_cache, const int32_t* __restrict__ table,
-                     const int32_t* __restrict__ lengths, IT* __restrict__ o, int2* __restrict__ spans, float* __restrict__ parts,
-                     uint32_t* __restrict__ status) {
+    attn_step_kernel(const __grid_constant__ StepMaps maps, StepDims d, const IT* q, const IT* k,
+                     const IT* v, IT* k_cache, IT* v_cache, const int32_t* table,
+                     const int32_t* lengths, IT* o, int2* spans, float* parts,
+                     uint32_t* status) {
   constexpr int KT = tile_keys<IT>(), N = 16 / (int)sizeof(IT), kSlabs = DP / slab_features<IT>();
   constexpr uint32_t kTileBytes = stage_bytes<IT, DP>() / 2;
   extern __shared__ unsigned char raw[];
@@ -409,7 +409,8 @@ __global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, units = d.Hk * d.HB, rows = min(d.G, kHeads);
   // new key, new value, queries
   auto side = [&](int stage) { return reinterpret_cast<IT*>(stages + kStages * stage_bytes<IT, DP>() + stage * side_bytes<IT, DP>(rows)); };
-  asm volatile("griddepcontrol.launch_dependents;");  // the join may be set up, and waits
+  launch_wait();
+  launch_next();
   if (blockIdx.x == 0 && tid == 0) *status = 0;  // (a wait that runs out sets it two seconds later)
   if (tid == kThreads) {
     tc::tma_prefetch_desc(&maps.k);
@@ -642,13 +643,14 @@ __global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
 // The rows' results that several blocks have parts of, and zeros for the rows that were skipped.  A block per query head of a row;
 // a warp has Ahead parts' loads under way, the first ones' while the largest maximum is looked for.  Bound by latency.
 template <typename IT, int DP, int Ahead>
-__global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, const int32_t* __restrict__ lengths, IT* __restrict__ o,
-                                                             const int2* __restrict__ spans, const float* __restrict__ parts) {
+__global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, const int32_t* lengths, IT* o,
+                                                             const int2* spans, const float* parts) {
   __shared__ float red[kWarps][2];
   __shared__ float total_of[kWarps][DP];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = (int)(blockIdx.x / (unsigned)d.Hq), h = (int)(blockIdx.x % (unsigned)d.Hq);
   const int r = h % d.G % kHeads;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the step's launch, which this one may overtake
+  launch_wait();
+  launch_next();
   const int2 span = spans[((long long)b * d.Hk + h / d.G) * d.HB + h % d.G / kHeads];  // (not written for a row that was skipped)
   const Row row = row_of<tile_keys<IT>()>(d, lengths, b);
   IT* out = o + ((long long)b * d.Hq + h) * d.D;
@@ -731,7 +733,7 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, const i
 
 // ------------------------------------------------------------------------------ prompts to pages
 // A copy, bound by memory.  A thread takes kPieces times 16 bytes of one token, of k and of v: what it looks up (sequence, place,
-// page) serves all of them, and their loads are under way together.  Eight prompts, 234 MB read and written: 39 us, 6.0 TB/s (42 with one piece).
+// page) serves all of them, and their loads are under way together.  Eight prompts, 234 MB read and written: 37 us, 6.3 TB/s (3 us more with one piece).
 constexpr int kPieces = 2;
 struct WriteDims {
   int B, T, Hk, D, num_pages, page_size, max_pages;
@@ -740,10 +742,12 @@ struct WriteDims {
 };
 
 template <typename IT, int V>
-__global__ void __launch_bounds__(256) cache_write_kernel(WriteDims d, const IT* __restrict__ k, const IT* __restrict__ v,
-                                                          IT* __restrict__ k_cache, IT* __restrict__ v_cache,
-                                                          const int32_t* __restrict__ table, const int32_t* __restrict__ starts,
-                                                          uint32_t* __restrict__ status) {
+__global__ void __launch_bounds__(256) cache_write_kernel(WriteDims d, const IT* k, const IT* v,
+                                                          IT* k_cache, IT* v_cache,
+                                                          const int32_t* table, const int32_t* starts,
+                                                          uint32_t* status) {
+  launch_wait();
+  launch_next();
   if (d.cu) {
     bool bad = false;
     for (int n = threadIdx.x; n < d.B; n += 256) bad |= d.cu[n] > d.cu[n + 1];
@@ -762,8 +766,14 @@ __global__ void __launch_bounds__(256) cache_write_kernel(WriteDims d, const IT*
   for (int i = 0; i < kPieces; ++i) {
     const int e = c + i * part;
     if (e >= wide) break;
-    a[i] = __ldcs(reinterpret_cast<const Piece*>(k + token * d.ld_k) + e);
-    b[i] = __ldcs(reinterpret_cast<const Piece*>(v + token * d.ld_v) + e);
+    const Piece *ka = reinterpret_cast<const Piece*>(k + token * d.ld_k) + e, *va = reinterpret_cast<const Piece*>(v + token * d.ld_v) + e;
+    if constexpr (V == 1) {
+      a[i] = *ka;
+      b[i] = *va;
+    } else {
+      a[i] = load_once(ka);
+      b[i] = load_once(va);
+    }
   }
   const int n = d.cu ? seq_of(d.cu, d.B, token) : (int)(token / d.T);
   const long long t = d.cu ? token - d.cu[n] : token - (long long)n * d.T;
@@ -841,22 +851,15 @@ cudaError_t step(const StepShape& sh, const void* q, const void* k, const void* 
     const uint32_t box[4] = {(uint32_t)slab_features<IT>(), 1, (uint32_t)sh.d.box, 1};
     if (!get_encoder() || !map_4d(&maps.k, kc, bf16, dims, box) || !map_4d(&maps.v, vc, bf16, dims, box)) return cudaErrorInvalidValue;
   }
-  kernel<<<sh.blocks, kThreads + 32, smem, s>>>(maps, sh.d, (const IT*)q, (const IT*)k, (const IT*)v, (IT*)kc, (IT*)vc, table, lengths, (IT*)o, spans, parts, status);
+  e = attn_launch(kernel, sh.blocks, kThreads + 32, smem, 1, s, maps, sh.d, (const IT*)q, (const IT*)k, (const IT*)v, (IT*)kc, (IT*)vc, table,
+                  lengths, (IT*)o, spans, parts, status);
+  if (e != cudaSuccess) return e;
   stage_mark(s, "attn_step");
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute early = {};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t config = {};
-  config.gridDim = dim3((unsigned)(sh.d.B * sh.d.Hq));
-  config.blockDim = dim3(kThreads);
-  config.stream = s;
-  config.attrs = &early;
-  config.numAttrs = 1;
   // Where units are few each is in many parts: 20 loads a warp instead of 8, which keep more registers than many small joins can spare.
   const auto join = (long long)sh.blocks >= 32ll * sh.d.B * sh.d.Hk * sh.d.HB ? attn_join_kernel<IT, DP, 20> : attn_join_kernel<IT, DP, 8>;
-  e = cudaLaunchKernelEx(&config, join, sh.d, lengths, (IT*)o, (const int2*)spans, (const float*)parts);
+  e = attn_launch(join, (long long)sh.d.B * sh.d.Hq, kThreads, 0, 1, s, sh.d, lengths, (IT*)o, (const int2*)spans, (const float*)parts);
   if (e != cudaSuccess) return e;
   stage_mark(s, "attn_join");
   return cudaGetLastError();
@@ -931,8 +934,9 @@ gdr_status gdr_cache_write(const gdr_cache_problem* p, const void* k, const void
   stage_begin(s);
   auto go = [&](auto it, auto vv) {
     using IT = decltype(it);
-    cache_write_kernel<IT, decltype(vv)::value><<<(unsigned)grid, 256, 0, s>>>(d, (const IT*)k, (const IT*)v, (IT*)k_cache, (IT*)v_cache,
-                                                                               block_table, starts, (uint32_t*)workspace);
+    const cudaError_t e = attn_launch(cache_write_kernel<IT, decltype(vv)::value>, grid, 256, 0, 1, s, d, (const IT*)k, (const IT*)v,
+                                      (IT*)k_cache, (IT*)v_cache, block_table, starts, (uint32_t*)workspace);
+    if (e != cudaSuccess) return status_of(e);
     stage_mark(s, "cache_write");
     return status_of(cudaGetLastError());
   };

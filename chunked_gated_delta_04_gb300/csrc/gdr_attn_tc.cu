@@ -17,7 +17,7 @@
 // l are rescaled; else P is up to 2^8, which bf16 holds as exactly as 1.
 // B = 1, T = 8192, 32 heads on 8 of 128, causal: 331 us, 1.66 PFLOP/s of the formula's operations, 86 % of what cuBLAS reaches; a pair
 // of tiles takes 2630 cycles, its products alone 2048: what is left is the wait of each lane's products for its softmax (1370
-// cycles, 780 of them exponentials and sums).  Split: three parts of 515 queries, 8 heads of 64, a window of 1024: 14.3 us, 16.4 with one lane.
+// cycles, 780 of them exponentials and sums).  Split: three parts of 515 queries, 8 heads of 64, a window of 1024: 13.4 us, 2 more with one lane.
 #include <algorithm>
 
 #include "gdr_attn_tc.cuh"
@@ -118,7 +118,8 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  launch_wait();  // for a packed batch's tile table
+  launch_wait();
+  launch_next();
   if (blockIdx.x == 0 && threadIdx.x == 0 && !d.cu_q) *status = 0;  // of a packed batch: the tile table's kernel
 
   // Registers: three warpgroups are launched with 168 a thread; 2 x 216 + 72 is the same sum.
@@ -492,7 +493,7 @@ cudaError_t fwd(const AttnDims& d, const AttnTiles& t, const AttnFwdArgs& a, cud
   const auto kernel = n > 1 ? attn_fwd_tc_kernel<DP, Split, Split> : attn_fwd_tc_kernel<DP, Split, false>;
   cudaError_t e = set_smem_once((const void*)kernel, Shape::kSmem);
   if (e != cudaSuccess) return e;
-  e = attn_launch(kernel, n > 1 ? items * n : std::min<long long>(items, kSmCount), Shape::kThreads, Shape::kSmem, n, d.cu_q != nullptr, s, maps, d, t, (unsigned)items, a);
+  e = attn_launch(kernel, n > 1 ? items * n : std::min<long long>(items, kSmCount), Shape::kThreads, Shape::kSmem, n, s, maps, d, t, (unsigned)items, a);
   if (e != cudaSuccess) return e;
   stage_mark(s, "attn_fwd");
   return cudaGetLastError();

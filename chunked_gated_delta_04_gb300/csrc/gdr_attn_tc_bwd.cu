@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = b.tmem_slot;
-  launch_wait();  // for delta and a packed batch's tables
+  launch_wait();
   launch_next();
   const int n = Share ? attn_cluster_size() : 1, rank = Share ? (int)tc::cluster_ctarank() : 0;
   float* const part = reinterpret_cast<float*>(bwd_raw);  // Share: the block's sums, once its tiles are used up
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = b.tmem_slot;
-  launch_wait();  // for delta and a packed batch's tables
+  launch_wait();
   launch_next();
   const int n = Share ? attn_cluster_size() : 1, rank = Share ? (int)tc::cluster_ctarank() : 0;
   float* const part = reinterpret_cast<float*>(bwd_raw);  // Share: the block's sums, once its tiles are used up
@@ -643,8 +643,8 @@ cudaError_t bwd(const AttnDims& d, const AttnTiles& tq, const AttnTiles& tk, con
     const int n = attn_sharers(items, steps);
     cudaError_t e = set_smem_once(n > 1 ? (const void*)shared : (const void*)kernel, smem);
     if (e != cudaSuccess) return e;
-    e = n > 1 ? attn_launch(shared, items * n, kThreads, smem, n, true, s, maps, d, t, (unsigned)items, a)
-              : attn_launch(kernel, std::min<long long>(items, kSmCount), kThreads, smem, 1, true, s, maps, d, t, (unsigned)items, a);
+    e = n > 1 ? attn_launch(shared, items * n, kThreads, smem, n, s, maps, d, t, (unsigned)items, a)
+              : attn_launch(kernel, std::min<long long>(items, kSmCount), kThreads, smem, 1, s, maps, d, t, (unsigned)items, a);
     if (e != cudaSuccess) return e;
     stage_mark(s, stage);
     return cudaGetLastError();

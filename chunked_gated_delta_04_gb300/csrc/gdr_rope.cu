@@ -7,7 +7,7 @@
 // Bound by memory: every feature is read and written once.  A thread keeps the sines of its pairs in registers and takes
 // several heads of its token, so that they are worked out once for up to eight; the first two heads' loads are under way
 // meanwhile.  Features that are passed on have warps of their own.  B = 2, T = 4096, 16 + 16 heads of 128, 64 features turned, bf16, forward
-// and backward: 53 us, 5.0 TB/s (66 us with the loads behind the sines; 73 us with both kinds of threads in one warp and four heads' loads).
+// and backward: 51 us, 5.3 TB/s (66 us with the loads behind the sines; 73 us with both kinds of threads in one warp and four heads' loads).
 #include <cmath>
 
 #include "gdr_attn.cuh"
@@ -49,7 +49,7 @@ struct Raw {
   __device__ __forceinline__ void load(const IT* p) {
     if constexpr (V >= N) {
 #pragma unroll
-      for (int i = 0; i < V; i += N) *reinterpret_cast<uint4*>(x + i) = __ldg(reinterpret_cast<const uint4*>(p + i));
+      for (int i = 0; i < V; i += N) *reinterpret_cast<uint4*>(x + i) = *reinterpret_cast<const uint4*>(p + i);
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) x[i] = p[i];
@@ -68,9 +68,11 @@ __device__ __forceinline__ void put_v(IT* p, const float (&v)[V]) {
 
 // V pairs per thread; Pairs: neighbouring features, else halves apart.
 template <typename IT, int V, bool Neighbours>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeDims d, const IT* __restrict__ q, const IT* __restrict__ k,
-                                                        const double* __restrict__ freqs, const int32_t* __restrict__ positions,
-                                                        IT* __restrict__ q_out, IT* __restrict__ k_out, uint32_t* __restrict__ status) {
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeDims d, const IT* q, const IT* k,
+                                                        const double* freqs, const int32_t* positions,
+                                                        IT* q_out, IT* k_out, uint32_t* status) {
+  launch_wait();
+  launch_next();
   if (d.cu) {  // places come from cu_seqlens: every block looks through them, the first reports
     bool bad = false;
     for (int n = threadIdx.x; n < d.num_seqs; n += kThreads) bad |= d.cu[n] > d.cu[n + 1];
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeDims d, const IT* __
       } else {  // whole 16 bytes: V divides what is left
 #pragma unroll
         for (int i = 0; i < N; i += 16 / sizeof(IT))
-          if (i < n) *reinterpret_cast<uint4*>(to + at + i) = __ldg(reinterpret_cast<const uint4*>(from + at + i));
+          if (i < n) *reinterpret_cast<uint4*>(to + at + i) = *reinterpret_cast<const uint4*>(from + at + i);
       }
     }
     return;
@@ -239,8 +241,9 @@ gdr_status gdr_rope(const gdr_rope_problem* p, const void* q, const void* k, con
   if (grid >= (1ll << 31)) return GDR_ERR_UNSUPPORTED;
   auto go = [&](auto it, auto vv, auto nb) {
     using IT = decltype(it);
-    rope_kernel<IT, decltype(vv)::value, decltype(nb)::value><<<(unsigned)grid, kThreads, 0, s>>>(
-        d, (const IT*)q, (const IT*)k, freqs, positions, (IT*)q_out, (IT*)k_out, (uint32_t*)workspace);
+    const cudaError_t e = attn_launch(rope_kernel<IT, decltype(vv)::value, decltype(nb)::value>, grid, kThreads, 0, 1, s, d, (const IT*)q,
+                                      (const IT*)k, freqs, positions, (IT*)q_out, (IT*)k_out, (uint32_t*)workspace);
+    if (e != cudaSuccess) return e;
     stage_mark(s, "rope");
     return cudaGetLastError();
   };

@@ -576,6 +576,44 @@ def test_a_row_with_a_page_outside_the_pool_keeps_its_own_page():
     assert torch.equal(kc, want) and torch.equal(vc, want)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,heads,packed", [(40, 2, True), (700, 8, False), (1500, 2, True)])
+def test_calls_in_a_row_wait_for_each_other(dtype, T, heads, packed):
+    """Every call reads what the one before it wrote, its launches begin while that one ends, and memory goes round: the same bits as with
+    a synchronisation behind each call."""
+    r = gen(34)
+    q0, k0, v0 = (r(1, T, heads, 64, dtype=dtype) for _ in range(3))
+    freqs, _ = gdr.rope_frequencies(64)
+    cu = torch.tensor([0, T // 3, T], dtype=torch.int32).cuda() if packed else None
+    pages = (T + 15) // 16 + 2
+    table = torch.arange(2 * pages, dtype=torch.int32).view(2, pages).cuda()[:2 if packed else 1].contiguous()
+
+    def chain(after):
+        q, k, v, out = q0, k0, v0, []
+        kc, vc = torch.zeros(2 * pages, 16, heads, 64, dtype=dtype, device="cuda"), torch.zeros(2 * pages, 16, heads, 64, dtype=dtype, device="cuda")
+        lengths = torch.tensor([T // 3, T - T // 3] if packed else [T], dtype=torch.int32).cuda()
+        for _ in range(6):
+            q, k = after(gdr.rope_forward(q, k, freqs, cu_seqlens=cu))
+            o, lse = after(gdr.attn_forward(q, k, v, cu_seqlens=cu))
+            dq, dk, dv = after(gdr.attn_backward(q, k, v, o, lse, o, cu_seqlens=cu))
+            after(gdr.cache_write(k, v, kc, vc, table, cu_seqlens=cu))
+            x = o[0, :lengths.numel()]
+            for _ in range(3):
+                x = after(gdr.attn_step(x, k[0, :lengths.numel()], x, kc, vc, table, lengths))
+            out += [o, lse, dq, dk, dv, x, kc.clone(), vc.clone()]
+            q, k, v = q + dq, k + dk, o
+        return out
+
+    def synced(x):
+        torch.cuda.synchronize()
+        return x
+
+    want = chain(synced)
+    for _ in range(3):
+        got = chain(lambda x: x)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_training_step_in_a_graph():
     """Forward and backward through autograd, captured: replays on new inputs give what eager steps give."""
     r = gen(33)
