@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(kBins) attn_tiles_kernel(AttnDims d, TableSpec
 // ------------------------------------------------------------------------------------- delta
 // delta_i = do_i . o_i: what the sum of p dp over a row comes to, with the o that was stored.  A warp per row of D features.
 // Bound by memory: o and do are read once.  2 x 4096 tokens, 16 heads of 128 in bf16, 67 MB: 20 us, set-up and waiting for the launch before
-// included; two or four rows per thread, for more loads under way, took 24 us and more.
+// included (o has just been written, and is on its way from L2 to memory meanwhile).  Two or four rows per thread, blocks of 64, 128 or 1024
+// threads, a grid that stays and loads ahead, and divisions in 32 bits were no faster (20 to 42 us).
 template <typename IT>
 __global__ void __launch_bounds__(256) attn_delta_kernel(AttnDims d, const IT* o, const IT* dout, float* delta, uint32_t* status, bool vec) {
   launch_wait();
