@@ -544,6 +544,51 @@ def test_malformed_cu_seqlens_can_be_seen():
         assert gdr.gdr_workspace_status(ws) == want and bool(kc.any()) == well
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_tokens_beyond_32_bit_offsets(dtype):
+    """Token strides that take the last tokens behind 2^31 elements: the same bits as contiguous inputs."""
+    T, ld = 2200, 1 << 20
+    r = gen(35)
+    q, k, v, do = r(1, T, 4, 64, dtype=dtype), r(1, T, 2, 64, dtype=dtype), r(1, T, 2, 64, dtype=dtype), r(1, T, 4, 64, dtype=dtype)
+    wide = torch.empty(T * ld, dtype=dtype, device="cuda").view(1, T, ld)
+    at, views = 0, []
+    for t in (q, k, v, do):
+        n = t.shape[2] * 64
+        views.append(wide[..., at:at + n].unflatten(-1, (t.shape[2], 64)))
+        views[-1].copy_(t)
+        at += n
+    freqs, _ = gdr.rope_frequencies(64)
+    table = torch.arange((T + 15) // 16, dtype=torch.int32).view(1, -1).cuda()
+
+    def all_of(q, k, v, do):
+        kc, vc = (torch.zeros(table.shape[1], 16, 2, 64, dtype=dtype, device="cuda") for _ in range(2))
+        o, lse = gdr.attn_forward(q, k, v, window=500)
+        gdr.cache_write(k, v, kc, vc, table)
+        return [*gdr.rope_forward(q, k, freqs), o, lse, *gdr.attn_backward(q, k, v, o, lse, do, window=500), kc, vc]
+
+    assert all(torch.equal(a, b) for a, b in zip(all_of(*views), all_of(q, k, v, do)))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_caches_beyond_32_bit_offsets(dtype):
+    """Pages behind 2^31 elements of the pool: the same bits as with a small one."""
+    size, Hk, D, lens = 16, 2, 128, [70, 33]
+    r = gen(36)
+    few, first = 12, (1 << 31) // (size * Hk * D) + 3
+    k, v = r(2, 80, Hk, D, dtype=dtype), r(2, 80, Hk, D, dtype=dtype)
+    q, k1, v1 = r(2, 4, D, dtype=dtype), r(2, Hk, D, dtype=dtype), r(2, Hk, D, dtype=dtype)
+    table = torch.arange(few, dtype=torch.int32).view(2, -1).flip(1).contiguous().cuda()
+    lengths = torch.tensor(lens, dtype=torch.int32).cuda()
+
+    def all_of(pages, offset):
+        kc, vc = (torch.empty(pages, size, Hk, D, dtype=dtype, device="cuda") for _ in range(2))
+        kc[offset:].zero_(), vc[offset:].zero_()
+        gdr.cache_write(k, v, kc, vc, table + offset)
+        return gdr.attn_step(q, k1, v1, kc, vc, table + offset, lengths), kc[offset:].clone(), vc[offset:].clone()
+
+    assert all(torch.equal(a, b) for a, b in zip(all_of(first + few, first), all_of(few, 0)))
+
+
 def test_a_call_without_queries_clears_the_status():
     q = torch.ones(1, 10, 2, 64, device="cuda")
     cu = torch.tensor([0, 5, 3, 10], dtype=torch.int32).cuda()
