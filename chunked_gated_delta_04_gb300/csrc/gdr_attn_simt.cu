@@ -239,8 +239,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_fwd_simt_kern
       float top = fmaxf(fmaxf(fmaxf(m[r], S[r][0]), fmaxf(S[r][1], S[r][2])), S[r][3]);
 #pragma unroll
       for (int x = 1; x < 16; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float base = top == -INFINITY ? 0.f : top * c;  // a row that has seen nothing yet: e^(-inf - 0) = 0
-      const float f = ex2f(fmaf(m[r], c, -base));
+      const float base = attn_base(top, c), f = attn_rescale(m[r], c, base);
       m[r] = top;
       float sum = 0.f;
 #pragma unroll
@@ -273,10 +272,10 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_fwd_simt_kern
       if (i >= s.n || x >= d.D) continue;
       float top = -INFINITY, sum = 0.f;
       for (int y = 0; y < n; ++y) top = fmaxf(top, load_peer(P + r, y));
-      const float base = top == -INFINITY ? 0.f : top * c;
+      const float base = attn_base(top, c);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int y = 0; y < n; ++y) {
-        const float f = ex2f(fmaf(load_peer(P + r, y), c, -base));
+        const float f = attn_rescale(load_peer(P + r, y), c, base);
         const float4 v = load_peer4(K + r * (DP + 4) + x, y);
         sum = fmaf(load_peer(P + kT + r, y), f, sum);
         o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);

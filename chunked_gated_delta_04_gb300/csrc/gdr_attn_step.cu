@@ -230,7 +230,7 @@ struct EngineBf16 {
     for (int r = 0; r < 2; ++r) {
       top[r] = max_nan(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
       top[r] = max_nan(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      const float base = top[r] == -INFINITY ? 0.f : top[r] * c, f = ex2f(fmaf(m[r], c, -base));
+      const float base = attn_base(top[r], c), f = attn_rescale(m[r], c, base);
       m[r] = top[r];
       float sum = 0.f;
 #pragma unroll
@@ -334,7 +334,7 @@ struct EngineF32 {
       float top = max_nan(m[r], s[r]);
 #pragma unroll
       for (int x = 4; x < 32; x <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float base = top == -INFINITY ? 0.f : top * c, f = ex2f(fmaf(m[r], c, -base));
+      const float base = attn_base(top, c), f = attn_rescale(m[r], c, base);
       m[r] = top;
       s[r] = ex2f(fmaf(s[r], c, -base));
       l[r] = fmaf(l[r], f, s[r]);  // of the lane's positions
@@ -591,10 +591,7 @@ __global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
       tc::named_sync(1, kThreads);  // from here on no warp reads the tile: its stage takes the warps' parts
       float* const acc = reinterpret_cast<float*>(ks);
       auto top_of = [&](int r) { return max_nan(max_nan(m_of[0][r], m_of[1][r]), max_nan(m_of[2][r], m_of[3][r])); };
-      auto share = [&](int w, int r) {  // of warp w's part in the whole
-        const float top = top_of(r), base = top == -INFINITY ? 0.f : top * c;
-        return ex2f(fmaf(m_of[w][r], c, -base));
-      };
+      auto share = [&](int w, int r) { return attn_rescale(m_of[w][r], c, attn_base(top_of(r), c)); };  // of warp w's part in the whole
       e.put(acc + warp * kHeads * DP, heads, [&](int r) { return share(warp, r); });
       tc::named_sync(1, kThreads);
       const bool whole = first_tile == 0 && here.tile + 1 == here.row.tiles;
@@ -702,14 +699,14 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, const i
     bad = fmaxf(bad, red[w][1]);
   }
   __syncthreads();  // red is used again
-  const float base = top == -INFINITY ? 0.f : top * c;
+  const float base = attn_base(top, c);
   float sum[F] = {}, l = 0.f;
   for (int x0 = c0 + warp; x0 <= c1; x0 += Ahead * kWarps) {
     if (x0 > c0 + warp) load(x0);
 #pragma unroll
     for (int i = 0; i < Ahead; ++i) {
       if (x0 + i * kWarps > c1) break;
-      const float weight = ex2f(fmaf(pm[i], c, -base));
+      const float weight = attn_rescale(pm[i], c, base);
       l = fmaf(pl[i], weight, l);
 #pragma unroll
       for (int f = 0; f < F; ++f) sum[f] = fmaf(v[i][f], weight, sum[f]);
