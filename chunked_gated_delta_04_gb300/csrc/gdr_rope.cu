@@ -28,6 +28,7 @@ struct RopeDims {
   int rot_chunks, pass_chunks;  // of a head: threads that rotate, threads that pass features on
   int lanes;                    // threads that share a token's heads
   long long rotating;           // threads that rotate, of all tokens; the others' warps come behind them
+  int narrow;                   // both kinds' places fit 32 bits: 64-bit divisions cost as much as the rotation
 };
 
 // freq / (2 pi) mod 1 in units of 2^-64: the mantissa times 2^66 / (2 pi), shifted by the exponent.
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeDims d, const IT* q,
   const int chunks = rotates ? d.rot_chunks : d.pass_chunks;
   int c, lane;
   long long token;
-  if (d.rotating < (1ll << 31)) {  // (64-bit divisions would cost as much as the rotation)
+  if (d.narrow) {
     const uint32_t y = (uint32_t)x / (uint32_t)max(chunks, 1);
     c = (int)((uint32_t)x - y * (uint32_t)chunks);
     token = y / (uint32_t)d.lanes;
@@ -237,6 +238,8 @@ gdr_status gdr_rope(const gdr_rope_problem* p, const void* q, const void* k, con
   while (per > 1 && d.tokens * chunks * ((heads + per - 1) / per) < 2048ll * kSmCount) per /= 2;
   d.lanes = (heads + per - 1) / per;
   d.rotating = d.tokens * d.lanes * d.rot_chunks;
+  // the last block's threads behind the last place count, too
+  d.narrow = d.tokens * d.lanes * (d.rot_chunks > d.pass_chunks ? d.rot_chunks : d.pass_chunks) + kThreads < 1ll << 32;
   const long long grid = d.tokens == 0 ? (d.cu ? 1 : 0) : (d.tokens * chunks * d.lanes + kThreads - 1) / kThreads;
   if (grid == 0) return GDR_OK;
   if (grid >= (1ll << 31)) return GDR_ERR_UNSUPPORTED;
