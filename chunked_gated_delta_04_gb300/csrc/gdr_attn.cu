@@ -153,6 +153,7 @@ gdr_status resolve(const gdr_attn_problem* p, AttnDims* d) {
   d->num_seqs = p->num_seqs, d->cu_q = p->cu_q, d->cu_k = p->cu_k;
   d->causal = p->causal;
   d->window = p->window >= p->Tk ? 0 : p->window;  // a window as wide as the keys hides nothing
+  if (d->window && (long long)p->Tq + d->window >= tokens) return GDR_ERR_UNSUPPORTED;  // (where a window begins is such a number, too)
   d->scale = p->scale > 0.f ? p->scale : (float)(1.0 / sqrt((double)p->D));
   d->ld_q = p->ld_q ? p->ld_q : wq, d->ld_do = p->ld_do ? p->ld_do : wq;
   d->ld_k = p->ld_k ? p->ld_k : wk, d->ld_v = p->ld_v ? p->ld_v : wk;

@@ -60,7 +60,8 @@ gdr_status gdr_rope(const gdr_rope_problem* p, const void* q, const void* k, con
  *   s_ij = scale q_i . k_j,   p_i = softmax over the visible j,   o_i = sum_j p_ij v_j,   lse_i = log sum_j exp s_ij
  * Of a sequence with n queries and m keys, query i sees key j if  j <= i + m - n  (with causal set)
  * and  j > i + m - n - window  (with window > 0).  A query that sees none has o = 0 and lse = -infinity
- * and no part in the gradients. */
+ * and no part in the gradients.  Queries, keys, and queries plus a window that is narrower than the keys number fewer than
+ * 2^31 - 1024. */
 typedef struct {
   int B, Tq, Tk, Hq, Hk, D;
   int num_seqs;              /* fixed length: = B */
