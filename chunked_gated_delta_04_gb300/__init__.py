@@ -35,9 +35,9 @@ from .block import (  # noqa: F401 - the operators around the gated delta rule
     gdr_norm_problem, gdr_ssm_problem, norm_backward, norm_forward, selective_scan, ssm_backward, ssm_forward,
     ssm_step, ssm_workspace, step)
 from .attn import (  # noqa: F401 - the attention mixer beside it
-    ATTN_EXPORTS, attention, attn_backward, attn_forward, attn_step, attn_workspace, cache_write, cache_write_workspace,
-    gdr_attn_problem, gdr_cache_problem, gdr_rope_problem, rope, rope_backward, rope_forward, rope_frequencies,
-    rope_workspace)
+    ATTN_EXPORTS, attention, attn_backward, attn_forward, attn_step, attn_step_workspace, attn_workspace, cache_write,
+    cache_write_workspace, gdr_attn_problem, gdr_cache_problem, gdr_rope_problem, rope, rope_backward, rope_forward,
+    rope_frequencies, rope_workspace)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdr.so")

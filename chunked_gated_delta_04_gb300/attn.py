@@ -4,7 +4,7 @@ such a cache.  Checks, streams, workspaces, packed batches and errors as in ``bl
 
     rope_forward, rope_backward, rope_frequencies, rope        (autograd), rope_workspace
     attn_forward, attn_backward, attention                     (autograd), attn_workspace
-    attn_step                                                  one token per row over a paged cache
+    attn_step, attn_step_workspace                             one token per row over a paged cache
     cache_write, cache_write_workspace                         a prompt's keys and values into it
 
 Served, a sequence's keys and values lie in pages of a pool [num_pages, page_size, Hk, D]; block_table [B, max_pages]
@@ -233,17 +233,24 @@ def attention(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal=True, window=0
 
 
 # ----------------------------------------------------------------------------------- a paged cache
-def attn_step(q, k, v, k_cache, v_cache, block_table, lengths, window=0, scale=None, stream=None):
+def attn_step(q, k, v, k_cache, v_cache, block_table, lengths, window=0, scale=None, stream=None, workspace=None):
     """Attention of one token per row: q [B, Hq, D], k and v [B, Hk, D]; k_cache and v_cache [num_pages, page_size, Hk, D];
     block_table int32 [B, max_pages], a row's pages in order; lengths int32 [B], the positions that a row's cache holds.  k and v are
     written at position lengths[b] of their row, and its query attends to positions 0 .. lengths[b] (with a window to the last
     `window` of them).  Returns o [B, Hq, D].  A row whose length is negative or fills its table is skipped and returns zeros;
     one that needs a page outside the pool returns zeros, too (k and v are written if their own page is in the pool).  lengths itself
-    is the caller's to advance."""
+    is the caller's to advance.  workspace: of attn_step_workspace, for its status."""
     if stream is not None:
         with _on(stream, q):
-            return attn_step(q, k, v, k_cache, v_cache, block_table, lengths, window, scale)
-    return _done(_binding().attn_step(q, k, v, k_cache, v_cache, block_table, lengths, window, _scale(scale)), "gdr_attn_step")
+            return attn_step(q, k, v, k_cache, v_cache, block_table, lengths, window, scale, workspace=workspace)
+    return _done(_binding().attn_step(q, k, v, k_cache, v_cache, block_table, lengths, window, _scale(scale), workspace), "gdr_attn_step")
+
+
+def attn_step_workspace(q, k_cache, block_table):
+    """A workspace for attn_step of these tensors, its status word clear."""
+    p = gdr_cache_problem(q.shape[0], 1, q.shape[1], k_cache.shape[2], q.shape[2], k_cache.shape[0], k_cache.shape[1],
+                          block_table.shape[1], None, _gdr._dtype_code(q.dtype))
+    return _clear_workspace("gdr_attn_step_workspace_bytes", p, q.device)
 
 
 def cache_write(k, v, k_cache, v_cache, block_table, starts=None, cu_seqlens=None, stream=None, workspace=None):

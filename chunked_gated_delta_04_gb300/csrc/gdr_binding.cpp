@@ -677,12 +677,13 @@ void cache_pages(gdr_cache_problem* p, const Tensor& k_cache, const Tensor& v_ca
 }
 gdr_status both_changed(const Tensor& k_cache, const Tensor& v_cache, gdr_status st) { return changed(v_cache, changed(k_cache, st)); }
 
-// q, k, v, k_cache, v_cache, block_table, lengths, window, scale
+// q, k, v, k_cache, v_cache, block_table, lengths, window, scale, workspace
 PyObject* attn_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  arguments(n, 9);
+  arguments(n, 10);
   const Tensor &q = required(a[0], "q"), &k = required(a[1], "k"), &v = required(a[2], "v"), &kc = required(a[3], "k_cache"),
-               &vc = required(a[4], "v_cache"), &table = required(a[5], "block_table"), &lengths = required(a[6], "lengths");
+               &vc = required(a[4], "v_cache"), &table = required(a[5], "block_table"), &lengths = required(a[6], "lengths"),
+               &given = tensor(a[9], "workspace");
   TORCH_CHECK_VALUE(q.dim() == 3 && k.dim() == 3, "expected q [B, Hq, D] and k, v [B, Hk, D], got ", q.sizes(), " and ", k.sizes());
   const int64_t B = q.size(0), Hk = k.size(1), D = q.size(2);
   const auto type = q.scalar_type();
@@ -708,7 +709,7 @@ PyObject* attn_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   p.scale = (float)number(a[8]);
   const OnDevice current(dev);
   const Tensor o = fresh(q.sizes(), q);
-  const Workspace ws(lib.gdr_attn_step_workspace_bytes(&p), q);
+  const Workspace ws(given, lib.gdr_attn_step_workspace_bytes(&p), q);
   return answer(both_changed(kc, vc, lib.gdr_attn_step(&p, ptr(q), ptr(k), ptr(v), ptr(kc), ptr(vc), (const int32_t*)ptr(table),
                                                        (const int32_t*)ptr(lengths), ptr(o), ptr(ws.t), ws.bytes, stream_of(q))),
                 o);
