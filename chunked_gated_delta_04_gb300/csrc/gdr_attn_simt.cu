@@ -14,6 +14,7 @@
 // of their ranks (1903 tokens in four sequences, 4 heads on 2, D = 64: forward 115 -> 46 us, dK and dV 393 -> 77, dQ 143 -> 57, copies
 // beside the products and packed sums included).
 #include "gdr_attn.cuh"
+#include "gdr_instrument.cuh"
 #include "tc_primitives.cuh"
 
 namespace gdr {
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_fwd_simt_kern
   for (int j0 = begin; j0 < hi; j0 += kT * n) {
     copy_async_wait();
     __syncthreads();  // the keys are here, and the values and P of the step before used up
+    GDR_DELAY_WARP(63);
     load_tile<IT, DP>(V, v, d.ld_v, j0, s.m, d.D);
     float S[4][4];
     dot_tile<DP>(Q, K, tx, ty, S);
@@ -265,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_fwd_simt_kern
     if (tx == 0)
 #pragma unroll
       for (int r = 0; r < 4; ++r) P[ty + 16 * r] = m[r], P[kT + ty + 16 * r] = l[r];
+    GDR_DELAY_WARP(64);
     tc::cluster_sync();
     const int r0 = kT * rank / n, r1 = kT * (rank + 1) / n;
     for (int e = threadIdx.x; e < (r1 - r0) * (DP / 4); e += kThreads) {
@@ -371,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_dkdv_simt_ker
     const long long stat = s.lse0 + (long long)hq * d.Tq;
     copy_async_wait();
     __syncthreads();
+    GDR_DELAY_WARP(63);
     if (st + n < steps) load(Qn, a.q, d.ld_q, st + n);
     float p[4][4], ds[4][4];
     grad_tile<DP>(d, s, i0, j0, Q, K, dO, V, a.lse + stat, a.delta + stat, tx, ty, p, ds);
@@ -391,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_dkdv_simt_ker
     Q = smem + 2 * N;  // the same place in every block, whichever it had last
     put_rows<DP, true>(Q, dK, tx, ty);
     put_rows<DP, true>(dO, dV, tx, ty);
+    GDR_DELAY_WARP(64);
     tc::cluster_sync();
     const long long at = (s.k0 + j0) * (long long)d.Hk * d.D + (long long)h * d.D, ld = (long long)d.Hk * d.D;
     sum_rows<IT, DP>(Q, rank, n, (IT*)a.dk + at, ld, s.m - j0, d.D, d.scale);
@@ -438,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_dq_simt_kerne
     const bool more = j0 + kT * n < hi;
     copy_async_wait();
     __syncthreads();
+    GDR_DELAY_WARP(63);
     if (more) load_tile<IT, DP>(Kn, k, d.ld_k, j0 + kT * n, s.m, d.D);
     float p[4][4], ds[4][4];
     grad_tile<DP>(d, s, i0, j0, Q, K, dO, V, a.lse + stat, a.delta + stat, tx, ty, p, ds);
@@ -453,6 +459,7 @@ __global__ void __launch_bounds__(kThreads, DP == 64 ? 2 : 1) attn_dq_simt_kerne
     __syncthreads();
     K = smem + 2 * N;  // the same place in every block, whichever it had last
     put_rows<DP, false>(K, dQ, tx, ty);
+    GDR_DELAY_WARP(64);
     tc::cluster_sync();
     const long long at = (s.q0 + i0) * (long long)d.Hq * d.D + (long long)h * d.D;
     sum_rows<IT, DP>(K, rank, n, (IT*)a.dq + at, (long long)d.Hq * d.D, s.n - i0, d.D, d.scale);

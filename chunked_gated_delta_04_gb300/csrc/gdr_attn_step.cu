@@ -24,6 +24,7 @@
 #include <cstring>
 
 #include "gdr_attn.cuh"
+#include "gdr_instrument.cuh"
 #include "tc_primitives.cuh"
 
 namespace gdr {
@@ -485,6 +486,7 @@ __global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
         into = new_page();
       }
       if (!attn_wait(&empty[stage], parity ^ 1u, status)) break;
+      GDR_DELAY_WARP(50);
       unsigned char* const ks = stages + (size_t)stage * stage_bytes<IT, DP>();
       IT* const beside = side(stage);
       const int heads = min(kHeads, d.G - hb * kHeads);
@@ -541,6 +543,7 @@ __global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
   bool fresh = true, bad = false, ok = true;
   for (bool more = true; more;) {
     ok = ok && attn_wait(&full[stage], parity, status);
+    GDR_DELAY_WARP(51);
     unsigned char* const ks = stages + (size_t)stage * stage_bytes<IT, DP>();
     unsigned char* const vs = ks + kTileBytes;
     const IT* const beside = side(stage);
@@ -586,6 +589,7 @@ __global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
     more = then.next(d, lengths, units, &at, end);
     const bool last = here.tile + 1 == here.row.tiles || !more;  // of a (row, unit), or of the block's part of it
     if (last) {
+      GDR_DELAY_WARP(52);
       float(&m_of)[kWarps][kHeads] = ms[ended & 1], (&l_of)[kWarps][kHeads] = ls[ended & 1];  // (a warp that is one unit on writes to the others)
       e.stats(m_of[warp], l_of[warp], heads);
       tc::named_sync(1, kThreads);  // from here on no warp reads the tile: its stage takes the warps' parts
@@ -593,7 +597,9 @@ __global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
       auto top_of = [&](int r) { return max_nan(max_nan(m_of[0][r], m_of[1][r]), max_nan(m_of[2][r], m_of[3][r])); };
       auto share = [&](int w, int r) { return attn_rescale(m_of[w][r], c, attn_base(top_of(r), c)); };  // of warp w's part in the whole
       e.put(acc + warp * kHeads * DP, heads, [&](int r) { return share(warp, r); });
+      GDR_DELAY_WARP(53);
       tc::named_sync(1, kThreads);
+      GDR_DELAY_WARP(54);
       const bool whole = first_tile == 0 && here.tile + 1 == here.row.tiles;
       const int slot = ended++ > 0 ? 1 : 0;
       float* const part = parts + ((long long)blockIdx.x * 2 + slot) * part_floats<DP>();
@@ -628,6 +634,7 @@ __global__ void __launch_bounds__(kThreads + 32, Engine::kBlocks)
     }
     if (edge || last) tc::fence_proxy_async_smem();  // a later round's copies come to the same places
     __syncwarp();
+    GDR_DELAY_WARP(55);
     if (lane == 0) tc::mbar_arrive(&empty[stage]);
     if (++stage == kStages) {
       stage = 0;

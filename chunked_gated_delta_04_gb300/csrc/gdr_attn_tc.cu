@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
             tc::tmem_wait_st();
             tc::tc_fence_before();
             __syncwarp();
+            GDR_DELAY_WARP(56);
             if (lane == 0) tc::mbar_arrive(&p_half[t]);
           }
         }
@@ -410,6 +411,7 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
       }
       if constexpr (Split) {  // every thread joins its query's two lanes for half of the features
         float(&of)[2][NT][kTcBlock] = joint[turn & 1];
+        GDR_DELAY_WARP(60);
         of[0][t][row] = m;
         of[1][t][row] = l;
         tc::tc_fence_before();
@@ -447,6 +449,7 @@ __global__ void __launch_bounds__(FwdShape<DP, Split>::kThreads, 1)
   }
   if constexpr (Share) {  // the cluster's one item: every block has its share of the queries
     __syncwarp();
+    GDR_DELAY_WARP(61);
     tc::cluster_sync();
     FwdItem w;
     const long long x = attn_item(0, items, n);

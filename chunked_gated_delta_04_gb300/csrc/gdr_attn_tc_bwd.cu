@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           b.stat[ring.slot][1][32 * e + lane] = dl[e];
         }
         __syncwarp();
+        GDR_DELAY_WARP(57);
         if (lane == 0) tc::mbar_arrive(&b.stat_full[ring.slot]);
         ring.next();
       }
@@ -386,6 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if constexpr (Share) {
     __syncwarp();
+    GDR_DELAY_WARP(62);
     tc::cluster_sync();
     const long long x = attn_item(0, items, n);
     if (warp < 8 && x >= 0 && key_item(d, tiles, (unsigned)x, &w)) {
@@ -566,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_wait_ld();
         tc::tc_fence_before();
         __syncwarp();
+        GDR_DELAY_WARP(58);
         if (lane == 0) tc::mbar_arrive(&b.s_free);
 #pragma unroll
         for (int e = 0; e < 64; ++e) p[e] = ex2f(fmaf(p[e], c, -ls));
@@ -579,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::tmem_wait_ld();
         tc::tc_fence_before();
         __syncwarp();
+        GDR_DELAY_WARP(59);
         if (lane == 0) tc::mbar_arrive(&b.dp_free);
 #pragma unroll
         for (int e = 0; e < 64; ++e) dp[e] = p[e] * (dp[e] - dl);
@@ -617,6 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if constexpr (Share) {
     __syncwarp();
+    GDR_DELAY_WARP(62);
     tc::cluster_sync();
     const long long x = attn_item(0, items, n);
     if (warp < 8 && x >= 0 && query_item(d, tiles, (unsigned)x, &w)) {

@@ -9,7 +9,8 @@
 //                     of a cluster pair) sleep a short, bounded, pseudo-random time at a
 //                     hand-off point, so that it runs late against the roles it hands work
 //                     to.  Only timing changes: every result must stay bit for bit the same,
-//                     which the tests check against the normal build.
+//                     which the tests check against the normal build.  GDR_DELAY_WARP(site), by
+//                     all lanes of a warp, brings them together again behind the sleep.
 #pragma once
 
 #include <stdint.h>
@@ -27,7 +28,15 @@ __device__ __forceinline__ void debug_delay(uint32_t site) {
   if ((x & 3u) != 0u) __nanosleep(256u + (x >> 20) % 4096u);
 }
 #define GDR_DELAY(site) gdr::tcx::debug_delay(site)
+#define GDR_DELAY_WARP(site)     \
+  do {                           \
+    gdr::tcx::debug_delay(site); \
+    __syncwarp();                \
+  } while (0)
 #else
+#define GDR_DELAY_WARP(site) \
+  do {                       \
+  } while (0)
 #define GDR_DELAY(site) \
   do {                  \
   } while (0)
