@@ -17,6 +17,11 @@ names each row's pages in order:
     o = attn_step(q, k, v, k_cache, v_cache, block_table, lengths)
     lengths += 1
 
+bf16 tensors whose base and token strides are multiples of 16 bytes run on the tensor cores, others on the CUDA cores, at a fiftieth of the rate
+(whatever torch allocates, and slices of it along tokens and heads, are such multiples; a view that begins at an odd element is not).  Values
+are taken as finite within a sequence: a NaN or an infinity at a masked place may still reach queries that do not see it, through a
+product with a probability of zero.  It reaches no other sequence, and what a cache holds behind a row's end reaches nobody.
+
 Captured into a CUDA graph, a backward pass needs leaves whose earlier eager graphs are gone: autograd adds a leaf's gradient on the
 stream that it was first used on while such a graph lives, and that stream is not part of the capture.
 """
@@ -90,6 +95,8 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origina
       "ntk"     the base grown so that the slowest pair is factor times as slow and the fastest as it was
       "yarn"    pairs that turn beta_fast times or more over original_length stay, those that turn beta_slow times or less are
                 divided by factor, those between are mixed in proportion to their turns; scale 0.1 ln(factor) + 1
+                (a model that was tuned with a ramp over the pairs' indices between the two rounded bounds has other frequencies
+                between them: hand those to rope as they are)
     """
     if rotary_dim <= 0 or rotary_dim % 2:
         raise ValueError(f"rotary_dim {rotary_dim}: even and above 0")
@@ -182,7 +189,7 @@ def _scale(scale):
 def attn_forward(q, k, v, cu_seqlens=None, cu_seqlens_k=None, causal=True, window=0, scale=None, stream=None, workspace=None):
     """Softmax attention: q [B, Tq, Hq, D], k and v [B, Tk, Hk, D], Hq a multiple of Hk (query head h reads key head
     h // (Hq // Hk)).  Of n queries and m keys of a sequence, query i sees key j if j <= i + m - n (causal) and
-    j > i + m - n - window (window > 0).  Packed batches: cu_seqlens of the queries, cu_seqlens_k of the keys where they differ.
+    j > i + m - n - window (window > 0; fewer than 2^31 - 1024 queries and window together, unless it is as wide as the keys).  Packed batches: cu_seqlens of the queries, cu_seqlens_k of the keys where they differ.
     Returns (o [B, Tq, Hq, D], lse [B, Hq, Tq] fp32, the log of the sum of exponentials); a query that sees no key has o = 0 and
     lse = -infinity."""
     if stream is not None:
@@ -238,7 +245,8 @@ def attn_step(q, k, v, k_cache, v_cache, block_table, lengths, window=0, scale=N
     block_table int32 [B, max_pages], a row's pages in order; lengths int32 [B], the positions that a row's cache holds.  k and v are
     written at position lengths[b] of their row, and its query attends to positions 0 .. lengths[b] (with a window to the last
     `window` of them).  Returns o [B, Hq, D].  A row whose length is negative or fills its table is skipped and returns zeros;
-    one that needs a page outside the pool returns zeros, too (k and v are written if their own page is in the pool).  lengths itself
+    one that needs a page outside the pool returns zeros, too (k and v are written if their own page is in the pool).  Rows may read the
+    same pages, but no two may write to the same place: rows that fill a batch up have a length of -1.  lengths itself
     is the caller's to advance.  workspace: of attn_step_workspace, for its status."""
     if stream is not None:
         with _on(stream, q):
@@ -256,7 +264,7 @@ def attn_step_workspace(q, k_cache, block_table):
 def cache_write(k, v, k_cache, v_cache, block_table, starts=None, cu_seqlens=None, stream=None, workspace=None):
     """Writes k and v [B, T, Hk, D] (packed: [1, T, Hk, D]) into their sequences' pages from position starts[n] (int32 [B];
     None: 0) on; cache and block_table as attn_step, a row of the table per sequence.  Tokens whose position or page does not exist
-    are left out."""
+    are left out; no two may go to the same place."""
     if stream is not None:
         with _on(stream, k):
             return cache_write(k, v, k_cache, v_cache, block_table, starts, cu_seqlens, workspace=workspace)

@@ -10,7 +10,7 @@ namespace {
 // ------------------------------------------------------------------------------ tile tables
 // A packed batch's cu_seqlens are checked, and its tiles written by falling work (tiles of a long causal sequence differ by
 // its length; what starts last decides when the launch ends).  One block per table: keys or queries, tiles of `size`.  Bound by latency:
-// 9 us for 28080 tokens in eight sequences, of which the launch behind it hides its own set-up.
+// 9 us for 28580 tokens in eight sequences, of which the launch behind it hides its own set-up.
 struct TableSpec {
   int2* table;
   long long slots;

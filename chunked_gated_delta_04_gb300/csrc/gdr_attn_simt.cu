@@ -13,6 +13,8 @@
 // tile: each takes every n-th step of its loop, and each sums the parts of some of the rows from the others' shared memory, in the order
 // of their ranks (1903 tokens in four sequences, 4 heads on 2, D = 64: forward 115 -> 46 us, dK and dV 393 -> 77, dQ 143 -> 57, copies
 // beside the products and packed sums included).
+// T = 4096, causal: fp32, 8 heads of 64, forward 530 us, 32 TFLOP/s, backward 1630 us, 26; of 128, 930 and 3070 us, 37 and 28.  bf16 off 16 bytes,
+// 16 heads of 128: 2490 and 7460 us, with loads of single elements, where the tensor cores take 51 and 175 us.
 #include "gdr_attn.cuh"
 #include "gdr_instrument.cuh"
 #include "tc_primitives.cuh"

@@ -16,10 +16,11 @@
 // second launch adds them in order.  Short rows change every tile: whatever a unit needs (its queries, its new token) comes
 // through the ring with its tiles, and its warps' parts are added in the stage that its last tile had.  The new token's key and value
 // go from the call's inputs to shared memory and the cache; what a page holds outside a row's visible positions is replaced by zeros there.
-// bf16, pages of 64: 64 rows of up to 8192 positions, 32 heads on 8 of 128: 122 us, 5.9 TB/s (437 us and more before what a unit needs came through
-// the ring); one row of 65536: 32 us, of which about 8 are set-up and the join (with eight parts' loads a warp, begun behind the maxima, 6 us
-// more).  With 16-byte copies by all threads the
-// latter took 84 us (1000 instructions a tile and warp), with a bulk copy for every position 96 (41 cycles a copy, one after the other).
+// bf16, pages of 64: 64 rows of up to 8192 positions, 32 heads on 8 of 128: 117 to 121 us, 6.0 TB/s (437 us and more before what a unit needs
+// came through the ring); 40 heads on 8: 123.  fp32, 32 heads on 8: 247 us, 5.8 TB/s, but 40 on 8: 1242 us, 1.2 TB/s (above four query heads a
+// unit's arithmetic is that of sixteen, one block per SM, and binds).  One row of 65536: 31 us, of which about 8 are set-up and the join (with
+// eight parts' loads a warp, begun behind the maxima, 6 us more).  With 16-byte copies by all threads the latter took 84 us (1000 instructions a
+// tile and warp), with a bulk copy for every position 96 (41 cycles a copy, one after the other).
 #include <cmath>
 #include <cstring>
 
@@ -737,7 +738,8 @@ __global__ void __launch_bounds__(kThreads) attn_join_kernel(StepDims d, const i
 
 // ------------------------------------------------------------------------------ prompts to pages
 // A copy, bound by memory.  A thread takes kPieces times 16 bytes of one token, of k and of v: what it looks up (sequence, place,
-// page) serves all of them, and their loads are under way together.  Eight prompts, 234 MB read and written: 37 us, 6.3 TB/s (3 us more with one piece).
+// page) serves all of them, and their loads are under way together.  Eight prompts, 234 MB read and written: 37 us, 6.3 TB/s (3 us more with one piece);
+// element by element, where k or v is off 16 bytes, 93 us.
 constexpr int kPieces = 2;
 struct WriteDims {
   int B, T, Hk, D, num_pages, page_size, max_pages;

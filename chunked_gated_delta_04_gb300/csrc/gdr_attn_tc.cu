@@ -15,9 +15,9 @@
 // S's place free for the next scores once P V is issued.
 // The maximum that P is formed against (m) follows the true one only when that has grown by more than 2^8: then O and
 // l are rescaled; else P is up to 2^8, which bf16 holds as exactly as 1.
-// B = 1, T = 8192, 32 heads on 8 of 128, causal: 331 us, 1.66 PFLOP/s of the formula's operations, 86 % of what cuBLAS reaches; a pair
+// B = 1, T = 8192, 32 heads on 8 of 128, causal: 319 to 338 us, 1.63 to 1.72 PFLOP/s of the formula's operations, 84 to 89 % of cuBLAS's rate; a pair
 // of tiles takes 2630 cycles, its products alone 2048: what is left is the wait of each lane's products for its softmax (1370
-// cycles, 780 of them exponentials and sums).  Split: three parts of 515 queries, 8 heads of 64, a window of 1024: 13.4 us, 2 more with one lane.
+// cycles, 780 of them exponentials and sums).  Split: three parts of 515 queries, 8 heads of 64, a window of 1024: 12.4 to 13.4 us, 2 more with one lane.
 #include <algorithm>
 
 #include "gdr_attn_tc.cuh"

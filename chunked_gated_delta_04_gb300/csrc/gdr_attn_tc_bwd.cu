@@ -13,10 +13,10 @@
 //   queries: S = Q K^T and dP = dO V^T free their columns as soon as they are in registers; dS has two places of its own.
 // Where the tiles are less than half of the SMs (few key heads, short sequences), the blocks of a cluster share one (Share): each
 // takes every n-th step, and sums some of the rows from all blocks' shared memory, in the order of their ranks.
-// Bound by the products.  B = 1, T = 8192, 32 heads on 8 of 128, causal: dK and dV 612 us, 1.80 PFLOP/s of the four products that are
-// issued, 93 % of cuBLAS's rate; dQ 493 us, 1.67 PFLOP/s of its three.  2 x 4096 tokens, 16 heads of 128: 181 and 146 us (from the first form's
-// 222 and 196), where beginnings and ends of items, about 5 us each, weigh more.  One key head for 8 query heads, T = 4096, 32 tiles of
-// keys shared by 4 blocks each: 137 us for all three launches.
+// Bound by the products.  B = 1, T = 8192, 32 heads on 8 of 128, causal: dK and dV 612 to 627 us, 1.75 to 1.80 PFLOP/s of the four products that
+// are issued, 90 to 93 % of cuBLAS's rate; dQ 493 to 522 us, 1.58 to 1.67 PFLOP/s of its three.  2 x 4096 tokens, 16 heads of 128: 182 and 147 us
+// (from the first form's 222 and 196), where beginnings and ends of items, about 5 us each, weigh more.  One key head for 8 query heads,
+// T = 4096, 32 tiles of keys shared by 4 blocks each: 137 to 141 us for all three launches.
 #include <algorithm>
 
 #include "gdr_attn_tc.cuh"

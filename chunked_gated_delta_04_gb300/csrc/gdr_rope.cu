@@ -8,7 +8,8 @@
 // several heads of its token, so that they are worked out once for up to eight; the first two heads' loads are under way
 // meanwhile.  Features that are passed on have warps of their own.  B = 2, T = 4096, 16 + 16 heads of 128, 64 features turned, bf16, forward
 // and backward: 51 us, 5.3 TB/s (66 us with the loads behind the sines; 73 us with both kinds of threads in one warp and four heads' loads;
-// 57 and 65 us with the next one or two heads' loads in front of a head's stores, whose registers cost warps).
+// 57 and 65 us with the next one or two heads' loads in front of a head's stores, whose registers cost warps).  Element by element, where base
+// or strides are off 16 bytes, one way takes 53 us for 25, in fp32 67 for 45.
 #include <cmath>
 
 #include "gdr_attn.cuh"

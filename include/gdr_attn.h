@@ -108,7 +108,8 @@ size_t gdr_attn_step_workspace_bytes(const gdr_cache_problem* p);
  * before the call.  The row's k and v go to position lengths[b], then its query attends to positions
  * 0 .. lengths[b] (with a window, to the last `window` of them).  A row whose length is negative or
  * fills its table is skipped: its output is zero, nothing is written.  One that needs a page outside the
- * pool has an output of zero, too; its k and v are written if their own page is in the pool. */
+ * pool has an output of zero, too; its k and v are written if their own page is in the pool.  The workspace's
+ * status word says whether a wait ran out, after which o is not to be used. */
 gdr_status gdr_attn_step(const gdr_cache_problem* p, const void* q, const void* k, const void* v, void* k_cache,
                          void* v_cache, const int32_t* block_table, const int32_t* lengths, void* o, void* workspace,
                          size_t workspace_bytes, gdr_stream_t stream);
